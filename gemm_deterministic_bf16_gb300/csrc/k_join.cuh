@@ -1,0 +1,398 @@
+// k_join.cuh -- the norms before and after a block joined with its gate and
+// residual scale: kernels for one element type (each k_join_*.cu instantiates
+// one).
+//
+// Forward, for each token (a row of H features):
+//   n   = z / sqrt(mean(z^2) + eps) * w_post      (the norm after the block; n = z without w_post)
+//   out = x + scale * gate * n
+//   y   = out / sqrt(mean(out^2) + eps) * w_pre   (the next block's norm)
+// y is formed from the sum before it is rounded to the stored type, so each
+// output is rounded once.  Without z, out is x itself and only y is written.
+//
+// Backward, with a = 1 / sqrt(mean(r^2) + eps), b = 1 / sqrt(mean(z^2) + eps),
+// r the stored sum:
+//   dx = dr + a dy w_pre - r a^3 / H * sum(dy w_pre r)
+//   t  = scale * dx,  dgate = t n,  dn = t gate
+//   dz = b dn w_post - z b^3 / H * sum(dn w_post z)
+//   dw_pre = sum over tokens of dy r a,  dw_post = sum over tokens of dn z b
+// dgate is summed over what the gate is broadcast over (features, tokens or
+// both).  Sums over tokens: each block of threads adds the rows of its set
+// (rows s, s + sets, ...) in order, and a second kernel adds the sets in a
+// fixed order, so results do not depend on the run.
+#pragma once
+
+#include "block.h"
+#include "elt.cuh"
+
+namespace detffn {
+namespace join {
+
+// A thread's 8 V features of a row: with VEC unit i is features
+// 8 (i G + t) .. + 7 (16-byte accesses), else features (8 i + j) G + t.
+template <bool VEC>
+__device__ __forceinline__ int col(int i, int j, int G, int t) {
+  return VEC ? 8 * (i * G + t) + j : (8 * i + j) * G + t;
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void load(const void* base, long long off, int H, int i, int G, int t, float (&v)[8]) {
+  using E = typename Io<DT>::E;
+  const E* p = static_cast<const E*>(base) + off;
+  if (VEC) {
+    const int c = col<VEC>(i, 0, G, t);
+    if (c < H) {
+      Io<DT>::ld8(p + c, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = col<VEC>(i, j, G, t);
+      v[j] = c < H ? Io<DT>::ld(p + c) : 0.0f;
+    }
+  }
+}
+
+template <int DT, bool VEC>
+__device__ __forceinline__ void store(void* base, long long off, int H, int i, int G, int t, const float (&v)[8]) {
+  using E = typename Io<DT>::E;
+  E* p = static_cast<E*>(base) + off;
+  if (VEC) {
+    const int c = col<VEC>(i, 0, G, t);
+    if (c < H) Io<DT>::st8(p + c, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int c = col<VEC>(i, j, G, t);
+      if (c < H) Io<DT>::st(p + c, v[j]);
+    }
+  }
+}
+
+// A parameter vector, in the elements' type or in FP32.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_param(const void* base, int pdtype, long long off, int H, int i, int G, int t,
+                                           float (&v)[8]) {
+  if (DT == DETFFN_F32 || pdtype == DT) load<DT, VEC>(base, off, H, i, G, t, v);
+  else load<DETFFN_F32, VEC>(base, off, H, i, G, t, v);
+}
+
+template <int DT>
+__device__ __forceinline__ float param(const void* base, int pdtype, long long i) {
+  if (DT == DETFFN_F32 || pdtype == DT) return Io<DT>::ld(static_cast<const typename Io<DT>::E*>(base) + i);
+  return static_cast<const float*>(base)[i];
+}
+template <int DT>
+__device__ __forceinline__ void put_param(void* base, int pdtype, long long i, float v) {
+  if (DT == DETFFN_F32 || pdtype == DT) Io<DT>::st(static_cast<typename Io<DT>::E*>(base) + i, v);
+  else static_cast<float*>(base)[i] = v;
+}
+
+// The gate's values for unit i of token m.
+template <int DT, bool VEC>
+__device__ __forceinline__ void load_gate(const JoinArgs& a, long long m, int H, int i, int G, int t, float (&v)[8]) {
+  if (a.gate_cs) {
+    load_param<DT, VEC>(a.gate, a.pdtype, m * a.gate_rs, H, i, G, t, v);
+  } else {
+    const float g = param<DT>(a.gate, a.pdtype, m * a.gate_rs);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = g;
+  }
+}
+
+template <int DT, int V, bool VEC>
+__global__ void __launch_bounds__(512) k_fwd(const __grid_constant__ JoinArgs a) {
+  __shared__ float buf[2 * 32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int G = blockDim.x, t = threadIdx.x, H = a.H;
+  const float inv = 1.0f / (float)H;
+  int turn = 0;
+  for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
+    float r[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) load<DT, VEC>(a.x.p, m * a.x.ld, H, i, G, t, r[i]);
+    if (a.z.p) {
+      float n[V][8];
+#pragma unroll
+      for (int i = 0; i < V; ++i) load<DT, VEC>(a.z.p, m * a.z.ld, H, i, G, t, n[i]);
+      if (a.w_post) {
+        float s[1] = {0.0f};
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) s[0] = fmaf(n[i][j], n[i][j], s[0]);
+        block_sums<1>(s, buf, turn);
+        const float b = rsqrtf(s[0] * inv + a.eps);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          float w[8];
+          load_param<DT, VEC>(a.w_post, a.pdtype, 0, H, i, G, t, w);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) n[i][j] *= b * w[j];
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float g[8];
+        if (a.gate) {
+          load_gate<DT, VEC>(a, m, H, i, G, t, g);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) n[i][j] *= g[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] = fmaf(a.scale, n[i][j], r[i][j]);
+        store<DT, VEC>(const_cast<void*>(a.out.p), m * a.out.ld, H, i, G, t, r[i]);
+      }
+    }
+    if (a.w_pre) {
+      float s[1] = {0.0f};
+#pragma unroll
+      for (int i = 0; i < V; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[0] = fmaf(r[i][j], r[i][j], s[0]);
+      block_sums<1>(s, buf, turn);
+      const float q = rsqrtf(s[0] * inv + a.eps);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float w[8];
+        load_param<DT, VEC>(a.w_pre, a.pdtype, 0, H, i, G, t, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[i][j] *= q * w[j];
+        store<DT, VEC>(const_cast<void*>(a.y.p), m * a.y.ld, H, i, G, t, r[i]);
+      }
+    }
+  }
+}
+
+// Row set s = blockIdx.x: rows s, s + gridDim.x, ...
+template <int DT, int V, bool VEC>
+__global__ void __launch_bounds__(512) k_bwd(const __grid_constant__ JoinArgs a) {
+  __shared__ float buf[2 * 3 * 32], buf2[2 * 2 * 32];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int G = blockDim.x, t = threadIdx.x, H = a.H;
+  const float inv = 1.0f / (float)H;
+  int turn = 0, turn2 = 0;
+  const bool feature = a.dgate && a.gate_cs && !a.gate_rs, full = a.dgate && a.gate_cs && a.gate_rs;
+  const bool token = a.dgate && !a.gate_cs && a.gate_rs, scalar = a.dgate && !a.gate_cs && !a.gate_rs;
+  float wpre[V][8], wpost[V][8], wgate[V][8], whole = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) wpre[i][j] = wpost[i][j] = wgate[i][j] = 0.0f;
+  for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
+    float dx[V][8], z[V][8];
+    float s[3] = {0.0f, 0.0f, 0.0f};  // sum r^2, sum dy w_pre r, sum z^2
+    if (a.z.p) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        load<DT, VEC>(a.z.p, m * a.z.ld, H, i, G, t, z[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[2] = fmaf(z[i][j], z[i][j], s[2]);
+      }
+    }
+    if (a.w_pre) {
+      float r[V][8], dy[V][8];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float w[8];
+        load<DT, VEC>(a.r.p, m * a.r.ld, H, i, G, t, r[i]);
+        load<DT, VEC>(a.dy.p, m * a.dy.ld, H, i, G, t, dy[i]);
+        load_param<DT, VEC>(a.w_pre, a.pdtype, 0, H, i, G, t, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          s[0] = fmaf(r[i][j], r[i][j], s[0]);
+          s[1] = fmaf(dy[i][j] * w[j], r[i][j], s[1]);
+        }
+      }
+      block_sums<3>(s, buf, turn);
+      const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * (q * q * q);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        float w[8];
+        load_param<DT, VEC>(a.w_pre, a.pdtype, 0, H, i, G, t, w);
+        if (a.dr.p) {
+          load<DT, VEC>(a.dr.p, m * a.dr.ld, H, i, G, t, dx[i]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) dx[i][j] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float qd = q * dy[i][j];
+          dx[i][j] += fmaf(qd, w[j], -k * r[i][j]);
+          wpre[i][j] = fmaf(qd, r[i][j], wpre[i][j]);
+        }
+        store<DT, VEC>(const_cast<void*>(a.dx.p), m * a.dx.ld, H, i, G, t, dx[i]);
+      }
+    } else {
+      if (a.w_post) block_sums<3>(s, buf, turn);
+#pragma unroll
+      for (int i = 0; i < V; ++i) load<DT, VEC>(a.dr.p, m * a.dr.ld, H, i, G, t, dx[i]);
+    }
+    if (!a.dz.p) continue;
+    // dx becomes dn w_post, the gradient of the normalised z.
+    const float b = a.w_post ? rsqrtf(s[2] * inv + a.eps) : 1.0f;
+    float e[2] = {0.0f, 0.0f};  // sum dn w_post z, sum t n
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float w[8], g[8];
+      if (a.w_post) {
+        load_param<DT, VEC>(a.w_post, a.pdtype, 0, H, i, G, t, w);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
+      }
+      if (a.gate) {
+        load_gate<DT, VEC>(a, m, H, i, G, t, g);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+      }
+      float dg[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = a.scale * dx[i][j], zn = a.z.p ? z[i][j] * b : 0.0f;
+        dg[j] = d * (zn * w[j]);
+        const float dn = d * g[j];
+        wpost[i][j] = fmaf(dn, zn, wpost[i][j]);
+        dx[i][j] = dn * w[j];
+        if (a.z.p) e[0] = fmaf(dx[i][j], z[i][j], e[0]);
+        e[1] += dg[j];
+        wgate[i][j] += dg[j];
+      }
+      if (full) {
+        if (DT == DETFFN_F32 || a.pdtype == DT) store<DT, VEC>(a.dgate, m * H, H, i, G, t, dg);
+        else store<DETFFN_F32, VEC>(a.dgate, m * H, H, i, G, t, dg);
+      }
+    }
+    if (a.w_post || token || scalar) {
+      block_sums<2>(e, buf2, turn2);
+      if (token && t == 0) put_param<DT>(a.dgate, a.pdtype, m, e[1]);
+      whole += e[1];
+    }
+    const float k = a.w_post ? e[0] * inv * (b * b * b) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      if (a.w_post) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dx[i][j] = fmaf(b, dx[i][j], -k * z[i][j]);
+      }
+      store<DT, VEC>(const_cast<void*>(a.dz.p), m * a.dz.ld, H, i, G, t, dx[i]);
+    }
+  }
+  // This set's column sums.
+  float* p = a.part;
+  const long long sets = gridDim.x;
+#pragma unroll
+  for (int kind = 0; kind < 3; ++kind) {
+    if (kind == 0 ? !a.dw_post : kind == 1 ? !a.dw_pre : !feature) continue;
+    const float(&acc)[V][8] = kind == 0 ? wpost : kind == 1 ? wpre : wgate;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      store<DETFFN_F32, VEC>(p, (long long)blockIdx.x * H, H, i, G, t, acc[i]);
+    p += sets * H;
+  }
+  if (scalar && t == 0) p[blockIdx.x] = whole;
+}
+
+// out[c] = sum over sets of part[s][c]: eight threads per column take sets
+// q, q + 8, ... in order and their sums are added in order.
+template <int DT>
+__global__ void __launch_bounds__(256) k_sets(const float* __restrict__ part, int sets, long long n, void* out0,
+                                              void* out1, void* out2, long long per, int pdtype) {
+  __shared__ float s[8][33];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const long long c = blockIdx.x * 32ll + lane;
+  const float* p = part + blockIdx.y * per;
+  float v = 0.0f;
+  if (c < n)
+    for (int k = q; k < sets; k += 8) v += p[(long long)k * n + c];
+  s[q][lane] = v;
+  __syncthreads();
+  if (q == 0 && c < n) {
+#pragma unroll
+    for (int k = 1; k < 8; ++k) v += s[k][lane];
+    put_param<DT>(blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2, pdtype, c, v);
+  }
+}
+
+inline bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
+
+// Whether every row access of the call is whole 16-byte vectors.
+template <int DT>
+bool vectors(const JoinArgs& a) {
+  if (a.H % 8) return false;
+  const Rows* rows[] = {&a.x, &a.z, &a.out, &a.y, &a.r, &a.dr, &a.dy, &a.dx, &a.dz};
+  for (const Rows* r : rows)
+    if (r->p && (!on16(r->p) || (r->ld * Io<DT>::kBytes) % 16)) return false;
+  const int pb = a.pdtype == DETFFN_F32 ? 4 : 2;
+  if (!on16(a.w_post) || !on16(a.w_pre)) return false;
+  if (a.gate && a.gate_cs && (!on16(a.gate) || (a.gate_rs * pb) % 16 || !on16(a.dgate))) return false;
+  return true;
+}
+
+// Threads of a row and the 8-feature units of each: one unit a thread up to
+// 512 threads, then more units.
+inline int pick(int H, int* threads) {
+  const int units = (H + 7) / 8;
+  int v = 1;
+  while (v < 8 && (units + v - 1) / v > 512) v *= 2;
+  *threads = ((units + v - 1) / v + 31) / 32 * 32;
+  return v;
+}
+
+template <int DT>
+cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
+  int threads;
+  const int v = pick(a.H, &threads);
+  const bool vec = vectors<DT>(a);
+  const long long most = 152ll * 16;
+  const dim3 grid((unsigned)(a.M < most ? a.M : most));
+  auto go = [&](auto k) { return launch_dependent(k, grid, threads, 0, st, a); };
+  switch (v) {
+    case 1: return go(vec ? k_fwd<DT, 1, true> : k_fwd<DT, 1, false>);
+    case 2: return go(vec ? k_fwd<DT, 2, true> : k_fwd<DT, 2, false>);
+    case 4: return go(vec ? k_fwd<DT, 4, true> : k_fwd<DT, 4, false>);
+    default: return go(vec ? k_fwd<DT, 8, true> : k_fwd<DT, 8, false>);
+  }
+}
+
+template <int DT>
+cudaError_t backward(const JoinArgs& a, cudaStream_t st) {
+  int threads;
+  const int v = pick(a.H, &threads);
+  const bool vec = vectors<DT>(a);
+  const int sets = (int)(a.M < kJoinSets ? a.M : kJoinSets);
+  auto go = [&](auto k) { return launch_dependent(k, dim3(sets), threads, 0, st, a); };
+  cudaError_t e;
+  switch (v) {
+    case 1: e = go(vec ? k_bwd<DT, 1, true> : k_bwd<DT, 1, false>); break;
+    case 2: e = go(vec ? k_bwd<DT, 2, true> : k_bwd<DT, 2, false>); break;
+    case 4: e = go(vec ? k_bwd<DT, 4, true> : k_bwd<DT, 4, false>); break;
+    default: e = go(vec ? k_bwd<DT, 8, true> : k_bwd<DT, 8, false>); break;
+  }
+  if (e != cudaSuccess) return e;
+  void* out[3] = {};
+  int n = 0;
+  if (a.dw_post) out[n++] = a.dw_post;
+  if (a.dw_pre) out[n++] = a.dw_pre;
+  if (a.dgate && a.gate_cs && !a.gate_rs) out[n++] = a.dgate;
+  if (n) {
+    e = launch_dependent(k_sets<DT>, dim3((unsigned)((a.H + 31) / 32), n), 256, 0, st, (const float*)a.part, sets,
+                         (long long)a.H, out[0], out[1], out[2], (long long)sets * a.H, a.pdtype);
+    if (e != cudaSuccess) return e;
+  }
+  if (a.dgate && !a.gate_cs && !a.gate_rs)
+    e = launch_dependent(k_sets<DT>, dim3(1), 256, 0, st, (const float*)a.part + (long long)n * sets * a.H, sets, 1ll,
+                         a.dgate, (void*)nullptr, (void*)nullptr, 0ll, a.pdtype);
+  return e;
+}
+
+}  // namespace join
+}  // namespace detffn

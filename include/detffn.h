@@ -361,6 +361,97 @@ DETFFN_API detffn_status detffn_selfcheck_pieces(int max_levels, unsigned long l
 DETFFN_API detffn_status detffn_selfcheck_fused_schedule(unsigned long long *cases,
                                                          unsigned long long *failures);
 
+/* ------------------------------------------------------------------------
+ * Operators around the FFN: the norms before and after a block joined with
+ * its gate and residual scale, 8-bit checkpoints of gate and up, and a
+ * mixture-of-experts layer for a few tokens.  Unlike the tree contractions
+ * above these keep every sum in FP32 and round each output once; their
+ * results do not depend on the stream or the run either.  Calls without a
+ * handle run on the current device.
+ * ------------------------------------------------------------------------ */
+
+/* The residual join (forward).  For each token m < M, over H <= 32768
+ * features:
+ *   n   = z / sqrt(mean(z^2) + eps) * w_post     (n = z where w_post is NULL)
+ *   out = x + scale * gate * n                    (gate 1 where NULL)
+ *   y   = out / sqrt(mean(out^2) + eps) * w_pre   (skipped where w_pre is NULL)
+ * y is formed from the unrounded sum.  z NULL: the norm before a block alone,
+ * y from x (w_post, gate and out are then NULL).
+ * x, z, out, y are rows of `dtype` with row strides ldx, ... in elements
+ * (>= H where M > 1).  w_post, w_pre [H] and the gate are `param_dtype`: the
+ * rows' type or FP32.  The gate of token m and feature c is
+ * gate[m * gate_rs + c * gate_cs], gate_cs in {0, 1}: (0, 0) one number,
+ * (0, 1) one per feature, (s, 0) one per token, (s, 1) one per element.
+ * out may be exactly x (in place); no other output overlaps anything. */
+DETFFN_API detffn_status detffn_join_forward(const void* x, long long ldx, const void* z, long long ldz,
+                                             const void* w_post, const void* gate, long long gate_rs,
+                                             long long gate_cs, float scale, const void* w_pre, float eps, void* out,
+                                             long long ldo, void* y, long long ldy, long long M, long long H,
+                                             int dtype, int param_dtype, void* stream);
+
+/* Scratch bytes of detffn_join_backward. */
+DETFFN_API detffn_status detffn_join_workspace_size(long long M, long long H, size_t* bytes);
+
+/* The residual join's gradients.  r is the forward's out as it was stored
+ * (x where there was no z), dr and dy the gradients of out and y (either may
+ * be NULL: zero; dy goes with w_pre).
+ *   dx = dr + the norm's gradient of dy         (where w_pre; else dx is dr itself, pass NULL)
+ *   dz, dgate, dw_post, dw_pre as the formulas above give them
+ * dgate has the gate's own shape, contiguous ([1], [H], [M] or [M, H]); it,
+ * dw_post and dw_pre are `param_dtype`, written (not added to), and given
+ * exactly where the parameter is.  dz NULL: no block output (w_post, gate and
+ * z are NULL too).  z is read only with w_post or a gate.  dx may be exactly
+ * dr and dz exactly z.  Sums over tokens run in an order fixed by M alone. */
+DETFFN_API detffn_status detffn_join_backward(const void* r, long long ldr, const void* dr, long long lddr,
+                                              const void* dy, long long lddy, const void* z, long long ldz,
+                                              const void* w_post, const void* gate, long long gate_rs,
+                                              long long gate_cs, float scale, const void* w_pre, float eps, void* dx,
+                                              long long lddx, void* dz, long long lddz, void* dgate, void* dw_post,
+                                              void* dw_pre, long long M, long long H, int dtype, int param_dtype,
+                                              void* ws, size_t ws_bytes, void* stream);
+
+/* 8-bit activation checkpoints of gate and up [M, I] (contiguous, `dtype`):
+ * codes [M, I] signed bytes and scales [M, ceil(I / 64)] FP32, one scale per
+ * 64 consecutive features of a token (the last block of a row may be short).
+ *   scale = max|v| * (1 / 127),  code = rint(v / scale) in [-127, 127],  value = code * scale
+ * A block of zeros has scale 0; a block that holds an infinity or a NaN has
+ * scale NaN, and all its values read back as NaN. */
+DETFFN_API detffn_status detffn_ckpt8_pack(const void* gate, const void* up, void* gate_codes, void* gate_scales,
+                                           void* up_codes, void* up_scales, long long M, long long I, int dtype,
+                                           void* stream);
+
+/* The values of a checkpoint, rounded once to `dtype`. */
+DETFFN_API detffn_status detffn_ckpt8_unpack(const void* gate_codes, const void* gate_scales, const void* up_codes,
+                                             const void* up_scales, void* gate, void* up, long long M, long long I,
+                                             int dtype, void* stream);
+
+/* The SiLU stage of the backward pass from a checkpoint's values g and u:
+ *   a = g sigma(g),  dU = dh a,  dG = dh u sigma(g) (1 + g (1 - sigma(g))),  h = a u
+ * in FP32, each output rounded once to dh's `dtype`; h may be NULL. */
+DETFFN_API detffn_status detffn_ckpt8_silu_backward(const void* dh, const void* gate_codes, const void* gate_scales,
+                                                    const void* up_codes, const void* up_scales, void* dU, void* dG,
+                                                    void* h, long long M, long long I, int dtype, void* stream);
+
+/* A mixture-of-experts layer for T <= 64 tokens, E <= 512 experts of which
+ * each token takes top_k <= 16 (H, I <= 65536):
+ *   logits = x Wr^T; the top_k largest, in descending order, the lower index first among equals
+ *   w = exp(logit - max) / sum, the sum over the chosen (normalize 1) or over all experts (0)
+ *   out = sum over the chosen, in that order, of w * ((SiLU(x Wg[e]^T) * (x Wu[e]^T)) Wd[e]^T)
+ * x [T, H], Wr [E, H], Wg, Wu [E, I, H], Wd [E, H, I], out [T, H], contiguous,
+ * of `dtype`.  experts (int) and weights (FP32) [T, top_k] receive the
+ * routing where not NULL.  Sums are FP32; the hidden activation is rounded
+ * once to `dtype`.  A token's result does not depend on the other tokens of
+ * the call.  A NaN logit is taken first and makes the token's weights NaN.
+ * options->path: EXACT takes the CUDA-core kernels (any sizes and types).
+ * `ws` is of detffn_moe_workspace_size bytes, 256-byte aligned. */
+DETFFN_API detffn_status detffn_moe_workspace_size(long long T, long long E, int top_k, long long H, long long I,
+                                                   int dtype, size_t* bytes);
+DETFFN_API detffn_status detffn_moe_forward(detffn_handle h, const void* x, const void* Wr, const void* Wg,
+                                            const void* Wu, const void* Wd, void* out, int* experts, float* weights,
+                                            long long T, long long E, int top_k, int normalize, long long H,
+                                            long long I, int dtype, void* ws, size_t ws_bytes, void* stream,
+                                            const detffn_options* opts);
+
 /* Synchronises `stream`, then returns and clears the handle's device status
  * word (DETFFN_OK or DETFFN_ERR_TIMEOUT from a bounded wait).  The word is
  * sticky: once a wait has run out, every later streaming kernel launched

@@ -1,0 +1,196 @@
+"""The mixture-of-experts layer for a few tokens against its definition in 64
+bits.
+
+Tolerance, element by element: with e = 2^-24, u the unit roundoff of the
+stored type and sums of absolute values, a gate or up value is off by at most
+H e S_x (S_x = |x| |W|^T; the tensor cores' partial sums are covered by the
+factor 2 below), h by that through |SiLU'| <= 1.1 and up, plus u |h| of its
+rounding, and out by the weighted sum of those plus u |out|."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": (torch.bfloat16, 2.0 ** -8), "f16": (torch.float16, 2.0 ** -11), "f32": (torch.float32, 2.0 ** -24)}
+E24 = 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def G():
+    import gemm_deterministic_bf16_gb300 as G
+    from gemm_deterministic_bf16_gb300 import build
+    build.build()
+    assert G.detffn_get_status() == 0
+    return G
+
+
+def inputs(T, E, H, I, dt, seed, k=1):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda s, std=1.0: (torch.randn(s, generator=g, device="cuda") * std).to(DT[dt][0])  # noqa: E731
+    s = dict(x=n((T, H)), Wr=n((E, H), 0.5 / H ** 0.5), Wg=n((E, I, H), 1 / H ** 0.5), Wu=n((E, I, H), 1 / H ** 0.5),
+             Wd=n((E, H, I), 1 / I ** 0.5))
+    for _ in range(50):   # no token whose choice hangs on the last bits of an FP32 sum
+        top = (s["x"].double() @ s["Wr"].double().T).topk(min(k + 1, E), -1).values
+        near = (top[:, :-1] - top[:, 1:] < 2e-5).any(-1)
+        if not bool(near.any()):
+            break
+        s["x"] = torch.where(near[:, None], n((T, H)), s["x"])
+    return s
+
+
+def route64(x, Wr, k, normalize):
+    p = torch.softmax(x.double() @ Wr.double().T, -1)
+    top, ids = torch.sort(p, dim=-1, descending=True, stable=True)
+    w, ids = top[:, :k], ids[:, :k]
+    return (w / w.sum(-1, keepdim=True) if normalize else w), ids
+
+
+def moe64(s, ids, w, dt):
+    """out and the bound of its error, given the routing."""
+    x = s["x"].double()
+    out, bound = torch.zeros_like(x), torch.zeros_like(x)
+    H, I = s["Wg"].shape[2], s["Wg"].shape[1]
+    u = DT[dt][1]
+    for e in ids.unique().tolist():
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        wg, wu, wd = (s[n][e].double() for n in ("Wg", "Wu", "Wd"))
+        g, up = x[t] @ wg.T, x[t] @ wu.T
+        eg, eu = 2 * H * E24 * (x[t].abs() @ wg.abs().T), 2 * H * E24 * (x[t].abs() @ wu.abs().T)
+        a = g * torch.sigmoid(g)
+        h = a * up
+        eh = 1.1 * eg * up.abs() + (a.abs() + 1.1 * eg) * eu + (u + 16 * E24) * h.abs()
+        wt = w[t, j, None]
+        out[t] += wt * (h @ wd.T)
+        bound[t] += wt * (eh @ wd.abs().T + (2 * I + 40) * E24 * (h.abs() @ wd.abs().T))
+    return out, bound * (1 + u) + u * out.abs() + 1e-30
+
+
+def check(G, s, k, normalize, dt, **kw):
+    out, ids, w = G.detffn_moe_forward(s["x"], s["Wr"], s["Wg"], s["Wu"], s["Wd"], k, normalize=normalize, **kw)
+    assert G.detffn_get_status() == 0
+    wr, idr = route64(s["x"], s["Wr"], k, normalize)
+    assert torch.equal(ids.long(), idr)
+    assert bool(((w.double() - wr).abs() <= 2e-5 * wr + 1e-30).all())
+    ref, bound = moe64(s, idr, wr, dt)
+    bad = ~((out.double() - ref).abs() <= bound + 2e-5 * ref.abs())
+    assert not bool(bad.any()), float(((out.double() - ref).abs() / bound).max())
+    return out
+
+
+# Tokens, experts, top_k, H, I: one token to the most, one expert to many,
+# widths inside and across tiles, odd widths (the general kernels).
+CASES = [(1, 1, 1, 64, 64), (1, 8, 2, 256, 128), (1, 128, 8, 512, 192), (3, 4, 4, 136, 72), (16, 32, 4, 512, 256),
+         (17, 16, 3, 264, 200), (64, 8, 2, 256, 384), (64, 64, 6, 512, 128), (33, 512, 16, 128, 64), (5, 7, 5, 1032, 1416),
+         (64, 1, 1, 320, 72), (2, 3, 2, 8, 8), (1, 2, 1, 4096, 768), (40, 5, 2, 2048, 1024)]
+
+
+@pytest.mark.parametrize("normalize", [True, False])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T,E,k,H,I", CASES)
+def test_layer(G, T, E, k, H, I, dt, normalize):
+    check(G, inputs(T, E, H, I, dt, T + E + H, k), k, normalize, dt)
+
+
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 2, 1, 1, 1), (3, 5, 2, 33, 17), (9, 4, 3, 255, 129), (64, 6, 2, 100, 36)])
+@pytest.mark.parametrize("dt", list(DT))
+def test_odd_widths(G, T, E, k, H, I, dt):
+    check(G, inputs(T, E, H, I, dt, 7 * T + H, k), k, True, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+def test_the_general_kernels_by_option(G, dt):
+    check(G, inputs(9, 8, 256, 192, dt, 3, 2), 2, True, dt, path=G.PATH_EXACT)
+
+
+def test_ties_go_to_the_lowest_index(G):
+    """Small whole numbers: every logit is exact, and many are equal."""
+    T, E, k, H, I = 32, 48, 8, 64, 64
+    g = torch.Generator(device="cuda").manual_seed(5)
+    s = inputs(T, E, H, I, "bf16", 5)
+    s["x"] = torch.randint(-1, 2, (T, H), generator=g, device="cuda").bfloat16()
+    s["Wr"] = torch.randint(-1, 2, (E, H), generator=g, device="cuda").bfloat16()
+    s["Wr"][E // 2:] = s["Wr"][:E // 2]
+    s["x"][3] = 0                                     # all logits equal
+    out, ids, w = G.detffn_moe_forward(s["x"], s["Wr"], s["Wg"], s["Wu"], s["Wd"], k)
+    logits = (s["x"].double() @ s["Wr"].double().T)
+    ref = torch.sort(logits, dim=-1, descending=True, stable=True).indices[:, :k]
+    assert torch.equal(ids.long(), ref)
+    assert ids[3].tolist() == list(range(k)) and torch.equal(w[3], torch.full((k,), 1.0 / k, device="cuda"))
+
+
+def test_every_token_to_one_expert(G):
+    T, E, H, I = 64, 16, 256, 256
+    s = inputs(T, E, H, I, "bf16", 8)
+    s["Wr"].zero_()
+    s["Wr"][11] = s["x"].float().mean(0).bfloat16()
+    s["x"] = (s["x"] * 0.1 + s["Wr"][11] * 8)
+    out = check(G, s, 1, True, "bf16")
+    assert bool(out.any())
+
+
+@pytest.mark.parametrize("path", [0, 1])
+@pytest.mark.parametrize("T,E,k,H,I", [(64, 32, 4, 512, 320), (23, 8, 2, 1024, 192)])
+def test_a_token_does_not_depend_on_the_others(G, T, E, k, H, I, path):
+    s = inputs(T, E, H, I, "bf16", 13, k)
+    rest = (s["Wr"], s["Wg"], s["Wu"], s["Wd"], k)
+    full = G.detffn_moe_forward(s["x"], *rest, path=path)
+    again = G.detffn_moe_forward(s["x"], *rest, path=path)
+    assert all(torch.equal(a, b) for a, b in zip(full, again))
+    for rows in ([0], [T - 1], list(range(3, 12)), list(range(T))[::-1]):
+        part = G.detffn_moe_forward(s["x"][rows].contiguous(), *rest, path=path)
+        assert all(torch.equal(a[rows], b) for a, b in zip(full, part)), rows
+
+
+def test_a_token_that_is_not_finite_stays_alone(G):
+    s = inputs(12, 8, 256, 128, "bf16", 17, 2)
+    rest = (s["Wr"], s["Wg"], s["Wu"], s["Wd"], 2)
+    ref = G.detffn_moe_forward(s["x"], *rest)
+    x = s["x"].clone()
+    x[4, 9], x[7, 0] = float("nan"), float("inf")
+    out, ids, w = G.detffn_moe_forward(x, *rest)
+    ok = [i for i in range(12) if i not in (4, 7)]
+    assert all(torch.equal(a[ok], b[ok]) for a, b in zip((out, ids, w), ref))
+    assert bool(out[4].isnan().all()) and bool(out[7].isnan().all()) and bool(w[4].isnan().all())
+    assert bool((ids >= 0).all()) and bool((ids < 8).all())
+
+
+def test_empty_streams_and_workspace(G):
+    s = inputs(6, 8, 256, 192, "bf16", 19, 2)
+    rest = (s["Wr"], s["Wg"], s["Wu"], s["Wd"], 2)
+    assert G.detffn_moe_forward(s["x"][:0], *rest)[0].shape == (0, 256)
+    ref = G.detffn_moe_forward(s["x"], *rest)
+    ws = torch.full((G.detffn_moe_workspace_size(6, 8, 2, 256, 192),), 255, dtype=torch.uint8, device="cuda")
+    for _ in range(3):   # a workspace full of old values, used again and again
+        assert all(torch.equal(a, b) for a, b in zip(ref, G.detffn_moe_forward(s["x"], *rest, ws=ws)))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(4):
+        got = G.detffn_moe_forward(s["x"], *rest, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        assert all(torch.equal(a, b) for a, b in zip(ref, got))
+
+
+def test_refusals(G):
+    s = inputs(6, 8, 256, 192, "bf16", 23, 2)
+    rest = (s["Wr"], s["Wg"], s["Wu"], s["Wd"])
+    big = torch.zeros((65, 256), dtype=torch.bfloat16, device="cuda")
+    for x, k in ((big, 2), (s["x"], 9), (s["x"], 0), (s["x"], 17)):
+        with pytest.raises(G.DetFFNError) as e:
+            G.detffn_moe_forward(x, *rest, k)
+        assert e.value.status == 2
+    with pytest.raises(ValueError):
+        G.detffn_moe_forward(s["x"].float(), *rest, 2)
+    with pytest.raises(ValueError):
+        G.detffn_moe_forward(s["x"], s["Wr"][:4].contiguous(), *rest[1:], 2)
+    with pytest.raises(ValueError):
+        G.detffn_moe_forward(s["x"], s["Wr"], s["Wg"].transpose(1, 2), s["Wu"], s["Wd"], 2)
+    with pytest.raises(G.DetFFNError) as e:
+        G.detffn_moe_forward(s["x"], *rest, 2, out=s["x"])
+    assert e.value.status == 1
+    with pytest.raises(G.DetFFNError) as e:
+        G.detffn_moe_forward(s["x"], *rest, 2, ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 5
+    for bad in (dict(flags=2), dict(path=5), dict(spin_limit=-1)):
+        with pytest.raises(G.DetFFNError) as e:
+            G.detffn_moe_forward(s["x"], *rest, 2, **bad)
+        assert e.value.status == 1
