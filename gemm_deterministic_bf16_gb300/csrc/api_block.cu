@@ -324,7 +324,8 @@ detffn_status moe_sizes(long long T, long long E, long long k, long long H, long
 
 // Workspace layout; with experts and weights of their own where the caller
 // takes none.
-MoeArgs moe_plan(Arena& w, long long T, long long E, long long k, long long H, long long I, int dtype) {
+MoeArgs moe_plan(Arena& w, long long T, long long E, long long k, long long H, long long I, int dtype,
+                 MoeScratch* sc) {
   MoeArgs a;
   a.T = (int)T;
   a.E = (int)E;
@@ -338,7 +339,9 @@ MoeArgs moe_plan(Arena& w, long long T, long long E, long long k, long long H, l
   a.pos = w.take<int>(T * k);
   a.pair = w.take<int>(T * k);
   a.first = w.take<int>(E + 1);
-  a.h = w.take<char>(T * k * I * bytes_of(dtype));
+  a.h = w.take<char>(T * k * I * 4);
+  sc->counters = w.take<int>(E + (H + 127) / 128);
+  sc->y = w.take<float>(T * k * H);
   return a;
 }
 
@@ -351,7 +354,8 @@ detffn_status detffn_moe_workspace_size(long long T, long long E, int top_k, lon
   if (!bytes) return DETFFN_ERR_INVALID_ARG;
   TRY(moe_sizes(T, E, top_k, H, I, dtype));
   Arena w(nullptr);
-  moe_plan(w, T, E, top_k, H, I, dtype);
+  MoeScratch sc;
+  moe_plan(w, T, E, top_k, H, I, dtype, &sc);
   *bytes = (w.off + 255) & ~(size_t)255;
   return DETFFN_OK;
 }
@@ -383,7 +387,8 @@ detffn_status detffn_moe_forward(detffn_handle h, const void* x, const void* Wr,
   const int alias[] = {-1, -1, -1, -1};
   TRY(check_overlap(in, 5, outs, 4, alias));
   Arena w(ws);
-  MoeArgs a = moe_plan(w, T, E, top_k, H, I, dtype);
+  MoeScratch sc;
+  MoeArgs a = moe_plan(w, T, E, top_k, H, I, dtype, &sc);
   a.x = x;
   a.Wr = Wr;
   a.Wg = Wg;
@@ -393,10 +398,20 @@ detffn_status detffn_moe_forward(detffn_handle h, const void* x, const void* Wr,
   a.normalize = normalize;
   if (experts) a.experts = experts;
   if (weights) a.weights = weights;
+  const int path = opts ? opts->path : DETFFN_PATH_AUTO;
+  const bool tensor = path != DETFFN_PATH_EXACT && moe_tensor_covers(a);
+  if (path == DETFFN_PATH_TENSOR && !tensor) return DETFFN_ERR_UNSUPPORTED;
+  Waits wt;
+  wt.status = h->d_status;
+  if (opts) {
+    wt.spin = opts->spin_limit;
+    wt.stall = (opts->flags & DETFFN_FLAG_TEST_STALL) ? 1 : 0;
+  }
   int prev = 0;
   TRYCU(cudaGetDevice(&prev));
   if (prev != h->device) TRYCU(cudaSetDevice(h->device));
-  const cudaError_t e = launch_moe_general(a, (cudaStream_t)stream);
+  const cudaError_t e = tensor ? launch_moe_tensor(a, sc, wt, h->sm_count, (cudaStream_t)stream)
+                               : launch_moe_general(a, (cudaStream_t)stream);
   if (prev != h->device) cudaSetDevice(prev);
   return cu(e);
 }

@@ -4,13 +4,13 @@
 //   l[t, e] = x[t, :] . Wr[e, :]                       (router logits, FP32)
 //   the k largest of l[t, :] in descending order, the lowest index first among equals
 //   w[t, j] = exp(l_j - max) / sum                     (the sum over the k chosen, or over all E)
-//   h = SiLU(x Wg[e]^T) * (x Wu[e]^T),  y = h Wd[e]^T  (the expert, FP32 sums, h rounded once)
+//   h = SiLU(x Wg[e]^T) * (x Wu[e]^T),  y = h Wd[e]^T  (the expert; FP32 sums, h in FP32 here)
 //   out[t, :] = sum over j = 0 .. k-1 of w[t, j] y[t, j, :]
 //
 // Every sum runs in an order that the sizes H and I alone fix, so a token's
 // result does not depend on the other tokens of the call.
 #include "elt.cuh"
-#include "moe.h"
+#include "moe.cuh"
 
 namespace detffn {
 namespace {
@@ -24,81 +24,36 @@ __device__ __forceinline__ float warp_dot(const typename Io<DT>::E* a, const typ
   return warp_sum(s);
 }
 
-// Logits of expert blockIdx.x: one warp per token.
-template <int DT>
-__global__ void __launch_bounds__(256) k_logits(const __grid_constant__ MoeArgs a) {
+// Logits of expert blockIdx.x: one warp per token.  With VEC lane l takes
+// features 8 l .. 8 l + 7, 8 l + 256 .., ... (16-byte loads, several in flight).
+// Block 0 also clears the counters of the kernel that follows.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) k_logits(const __grid_constant__ MoeArgs a, int* counters, int n) {
   grid_dep_wait();
   grid_dep_launch();
   using E = typename Io<DT>::E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x;
+  if (e == 0)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
+  const E* w = static_cast<const E*>(a.Wr) + e * a.H;
   for (int t = warp; t < a.T; t += 8) {
-    const float l = warp_dot<DT>(static_cast<const E*>(a.x) + t * a.H, static_cast<const E*>(a.Wr) + e * a.H, a.H, lane);
-    if (lane == 0) a.logits[t * a.E + e] = l;
-  }
-}
-
-// Order of logits: larger first, a NaN before all (it then shows in the
-// weights), the lower index first among equals.
-__device__ __forceinline__ unsigned long long rank_key(float l, int e) {
-  const uint32_t b = __float_as_uint(l + 0.0f);  // -0 becomes +0
-  const uint32_t k = l != l ? 0xFFFFFFFFu : (b & 0x80000000u) ? ~b : b | 0x80000000u;
-  return ((unsigned long long)k << 32) | (uint32_t)~e;
-}
-
-// The choice of one token by one warp; E <= 512 logits, 16 a lane.
-__device__ void choose(const float* logits, int E, int k, bool normalize, int lane, int* experts, float* weights) {
-  constexpr int N = kMoeMaxExperts / 32;
-  float l[N];
-  unsigned used = 0;
-  float top = -INFINITY, all = 0.0f;
+    const E* x = static_cast<const E*>(a.x) + t * a.H;
+    float s;
+    if (VEC) {
+      s = 0.0f;
+#pragma unroll 4
+      for (long long c = 8 * lane; c < a.H; c += 256) {
+        float p[8], q[8];
+        Io<DT>::ld8(x + c, p);
+        Io<DT>::ld8(w + c, q);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const int e = lane + 32 * i;
-    l[i] = e < E ? logits[e] : -INFINITY;
-  }
-  float w = 0.0f, sum = 0.0f;
-  int mine = 0;
-  for (int j = 0; j < k; ++j) {
-    unsigned long long best = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int e = lane + 32 * i;
-      if (e < E && !(used >> i & 1)) {
-        const unsigned long long q = rank_key(l[i], e);
-        best = q > best ? q : best;
+        for (int j = 0; j < 8; ++j) s = fmaf(p[j], q[j], s);
       }
+      s = warp_sum(s);
+    } else {
+      s = warp_dot<DT>(x, w, a.H, lane);
     }
-#pragma unroll
-    for (int d = 16; d; d >>= 1) {
-      const unsigned long long o = __shfl_xor_sync(0xffffffffu, best, d);
-      best = o > best ? o : best;
-    }
-    const int e = (int)~(uint32_t)best;
-    float v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (e == lane + 32 * i) {
-        used |= 1u << i;
-        v = l[i];
-      }
-    v = __shfl_sync(0xffffffffu, v, e & 31);
-    if (j == 0) top = v;
-    const float x = expf(v - top);
-    sum += x;
-    if (lane == j) {
-      w = x;
-      mine = e;
-    }
-  }
-  if (!normalize) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (lane + 32 * i < E) all += expf(l[i] - top);
-    sum = warp_sum(all);
-  }
-  if (lane < k) {
-    experts[lane] = mine;
-    weights[lane] = w / sum;
+    if (lane == 0) a.logits[t * a.E + e] = s;
   }
 }
 
@@ -109,7 +64,8 @@ __global__ void __launch_bounds__(1024) k_select(const __grid_constant__ MoeArgs
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = a.T * a.k;
   for (int t = warp; t < a.T; t += blockDim.x / 32)
-    choose(a.logits + (long long)t * a.E, a.E, a.k, a.normalize, lane, a.experts + t * a.k, a.weights + t * a.k);
+    moe_choose<kMoeMaxExperts / 32>(a.logits + (long long)t * a.E, a.E, a.k, a.normalize, lane, a.experts + t * a.k,
+                                    a.weights + t * a.k);
   __syncthreads();
   for (int p = threadIdx.x; p < P; p += blockDim.x) ids[p] = a.experts[p];
   __syncthreads();
@@ -148,7 +104,7 @@ __global__ void __launch_bounds__(256) k_gateup(const __grid_constant__ MoeArgs 
   for (int p = p0; p < p1; ++p) {
     const E* x = static_cast<const E*>(a.x) + (a.pair[p] / a.k) * a.H;
     const float g = warp_dot<DT>(x, wg, a.H, lane), u = warp_dot<DT>(x, wu, a.H, lane);
-    if (lane == 0) Io<DT>::st(static_cast<E*>(a.h) + p * a.I + i, g / (1.0f + expf(-g)) * u);
+    if (lane == 0) static_cast<float*>(a.h)[p * a.I + i] = g / (1.0f + expf(-g)) * u;
   }
 }
 
@@ -165,14 +121,23 @@ __global__ void __launch_bounds__(256) k_down(const __grid_constant__ MoeArgs a)
   for (int j = 0; j < a.k; ++j) {
     const int q = t * a.k + j;
     const E* w = static_cast<const E*>(a.Wd) + (a.experts[q] * a.H + r) * a.I;
-    s = fmaf(a.weights[q], warp_dot<DT>(static_cast<const E*>(a.h) + a.pos[q] * a.I, w, a.I, lane), s);
+    const float* hp = static_cast<const float*>(a.h) + a.pos[q] * a.I;
+    float y = 0.0f;
+    for (long long i = lane; i < a.I; i += 32) y = fmaf(Io<DT>::ld(w + i), hp[i], y);
+    s = fmaf(a.weights[q], warp_sum(y), s);
   }
   if (lane == 0) Io<DT>::st(static_cast<E*>(a.out) + t * a.H + r, s);
 }
 
 template <int DT>
+cudaError_t logits(const MoeArgs& a, int* counters, int n, cudaStream_t st) {
+  const bool vec = a.H % 8 == 0 && (((uintptr_t)a.x | (uintptr_t)a.Wr) & 15u) == 0;
+  return launch_dependent(vec ? k_logits<DT, true> : k_logits<DT, false>, dim3(a.E), 256, 0, st, a, counters, n);
+}
+
+template <int DT>
 cudaError_t general(const MoeArgs& a, cudaStream_t st) {
-  cudaError_t e = launch_dependent(k_logits<DT>, dim3(a.E), 256, 0, st, a);
+  cudaError_t e = launch_moe_logits(a, nullptr, 0, st);
   if (e == cudaSuccess) e = launch_dependent(k_select, dim3(1), 1024, 0, st, a);
   if (e == cudaSuccess) e = launch_dependent(k_gateup<DT>, dim3((unsigned)((a.I + 7) / 8), a.E), 256, 0, st, a);
   if (e == cudaSuccess) e = launch_dependent(k_down<DT>, dim3((unsigned)((a.H + 7) / 8), a.T), 256, 0, st, a);
@@ -180,6 +145,11 @@ cudaError_t general(const MoeArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
+
+cudaError_t launch_moe_logits(const MoeArgs& a, int* counters, int n, cudaStream_t st) {
+  return a.dtype == DETFFN_F32 ? logits<DETFFN_F32>(a, counters, n, st)
+         : a.dtype == DETFFN_F16 ? logits<DETFFN_F16>(a, counters, n, st) : logits<DETFFN_BF16>(a, counters, n, st);
+}
 
 cudaError_t launch_moe_general(const MoeArgs& a, cudaStream_t st) {
   return a.dtype == DETFFN_F32 ? general<DETFFN_F32>(a, st)

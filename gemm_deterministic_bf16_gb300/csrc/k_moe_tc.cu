@@ -1,0 +1,546 @@
+// k_moe_tc.cu -- the mixture-of-experts layer for a few tokens on the tensor
+// cores, BF16 and FP16 (the formulas are those of k_moe.cu).
+//
+// One persistent launch, one CTA per SM, after the router's logits.  Every
+// CTA works the routing out for itself from the logits (one warp per token),
+// so that nothing is handed over through memory, then takes units in turn:
+//   gate/up: 64 rows of Wg[e] over the same 64 rows of Wu[e] (the MMA's 128
+//     rows) times the expert's tokens, K = H; h for those 64 features
+//   down:    128 rows of Wd[e] times the expert's rows of h, K = I; partial
+//     outputs y of the pairs
+// All gate/up units come before all down units, experts in ascending order.
+// A down unit waits (bounded) until its expert's gate/up units are counted,
+// with its first weight tiles already on their way; the CTA that finishes
+// the last expert of a 128-feature tile of the output adds the pairs of each
+// token there, in the order of its choices.
+//
+// The work is the weights' bytes: each active expert's are read once, by TMA
+// boxes of 64 rows x 64 K (128-byte swizzle) into a ring of stages of 128 K,
+// and the tokens' rows by row gathers (x) or row boxes (h: the pairs of an
+// expert are neighbours).  h goes to the down projection as two terms, its
+// rounding to the stored type and the rounding of what that left (16 bits of
+// BF16, 22 of FP16), both multiplied into the same accumulator: with one term
+// the rounding of h alone doubles the variance of out's error (1.41 times the
+// error of one rounding, measured), and the second costs only tensor time,
+// which is idle here.  A row's sum over K is one accumulation in FP32 in
+// tensor memory, whatever the other columns are, so a token's result does not
+// depend on the other tokens.
+#include <mutex>
+
+#include "elt.cuh"
+#include "moe.cuh"
+#include "ptx.cuh"
+#include "tc.h"
+
+namespace detffn {
+namespace {
+
+// Instruction descriptor, kind::f16: FP32 accumulator, BF16 or FP16 operands,
+// both K-major, M x N tile.
+__device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N) {
+  return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+constexpr int kThreads = 256;     // warp 0 loads, warp 1 issues MMAs, warps 4-7 form the outputs
+constexpr int kEpi0 = 4;          // first epilogue warp (its TMEM lane quarter is warp % 4)
+constexpr int KS = 128;           // K positions of a stage
+constexpr int kBoxBytes = 64 * 128;              // 64 rows x 64 K
+constexpr int kWeightBytes = 4 * kBoxBytes;      // 128 rows x 128 K
+constexpr int kMaxStages = 8;
+constexpr int kSmemMax = 227 * 1024;
+constexpr int kXch = 64 * 16 * 4;                // up values of one 16-column chunk
+
+struct Bars {
+  uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], fin;
+  uint32_t tmem;
+  int abort, go;
+  int active;   // experts with tokens
+  int most;     // most tokens of one expert
+};
+
+struct Args {
+  MoeArgs m;
+  int NB;            // most token columns of a unit (T rounded up to 16)
+  int ring;          // bytes for stages
+  int ta, tb;        // gate/up units and down units of an expert
+  int* ready;        // [E] gate/up units done
+  int* tickets;      // [tb] down units done
+  float* y;          // [T * k][H]
+  int* status;
+  long long spin;
+  int stall;
+};
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, long long limit, volatile int* abort_flag,
+                                              int* status) {
+  for (long long i = 0; i < limit; ++i) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((i & 1023) == 1023 && *abort_flag) return false;
+  }
+  *abort_flag = 1;
+  if (status) atomicExch(status, (int)DETFFN_ERR_TIMEOUT);
+  return false;
+}
+
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* tmap, int x, int y, int z, uint64_t* bar,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+      "%4}], [%5], %6;" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
+      : "memory");
+}
+// Four rows y0 .. y3 of a map whose box is one row high, to four consecutive
+// rows of shared memory; rows past the tensor's end read zeros.
+__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, int y0, int y1, int y2, int y3,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
+      "%5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_u32(bar))
+      : "memory");
+}
+__device__ __forceinline__ int ld_acquire(const int* p) {
+  int v;
+  asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The routing tables in shared memory.
+struct Tables {
+  int* first;       // [E + 1] first pair of each expert
+  int* act;         // [E] active experts, ascending
+  float* w;         // [P] weights by pair (token * k + slot)
+  uint16_t* id;     // [P] expert by pair
+  uint16_t* pos;    // [P] place of a pair in expert order
+  uint16_t* tok;    // [P] token at each place
+};
+__host__ __device__ inline int tables_bytes(int E, int P) { return ((E + 1 + E + P) * 4 + 3 * P * 2 + 15) & ~15; }
+__device__ __forceinline__ Tables tables_at(unsigned char* p, int E, int P) {
+  Tables t;
+  t.first = reinterpret_cast<int*>(p);
+  t.act = t.first + E + 1;
+  t.w = reinterpret_cast<float*>(t.act + E);
+  t.id = reinterpret_cast<uint16_t*>(t.w + P);
+  t.pos = t.id + P;
+  t.tok = t.pos + P;
+  return t;
+}
+
+struct Unit {
+  bool down;
+  int a, tile, e, p0, n;   // active index, tile of the expert, expert, first pair, pairs
+};
+__device__ __forceinline__ Unit unit_at(long long u, const Args& g, const Tables& t, int active) {
+  Unit r;
+  const long long na = (long long)active * g.ta;
+  r.down = u >= na;
+  const long long v = r.down ? u - na : u;
+  const int per = r.down ? g.tb : g.ta;
+  r.a = (int)(v / per);
+  r.tile = (int)(v - (long long)r.a * per);
+  r.e = t.act[r.a];
+  r.p0 = t.first[r.e];
+  r.n = t.first[r.e + 1] - r.p0;
+  return r;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_moe(const __grid_constant__ CUtensorMap mWg, const __grid_constant__ CUtensorMap mWu,
+          const __grid_constant__ CUtensorMap mWd, const __grid_constant__ CUtensorMap mX,
+          const __grid_constant__ CUtensorMap mH, const __grid_constant__ Args g) {
+  using El = typename Io<DT>::E;
+  extern __shared__ unsigned char raw[];
+  unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  const MoeArgs& m = g.m;
+  const int P = m.T * m.k;
+  Bars* bars = reinterpret_cast<Bars*>(smem + g.ring);
+  float* xch = reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(bars) + ((sizeof(Bars) + 127) & ~127));
+  const Tables t = tables_at(reinterpret_cast<unsigned char*>(xch) + kXch, m.E, P);
+  volatile int* abort_flag = &bars->abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long limit = g.spin > 0 ? g.spin : kDefaultSpin;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kMaxStages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->accf[b], 1);
+      mbar_init(&bars->acce[b], 4);
+    }
+    mbar_init(&bars->fin, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&mWg);
+    prefetch_tmap(&mWu);
+    prefetch_tmap(&mWd);
+    prefetch_tmap(&mX);
+    prefetch_tmap(&mH);
+  }
+  const uint32_t tcols = 2 * g.NB <= 32 ? 32 : 2 * g.NB <= 64 ? 64 : 128;  // two accumulators of NB columns
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem, tcols);
+    tmem_relinquish();
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+
+  // ---------------- the routing ----------------
+  for (int e = threadIdx.x; e < m.E; e += kThreads) t.act[e] = 0;
+  for (int q = warp; q < m.T; q += kThreads / 32) {
+    if (m.E <= 128) moe_choose<4>(m.logits + (long long)q * m.E, m.E, m.k, m.normalize, lane, t.id + q * m.k, t.w + q * m.k);
+    else moe_choose<16>(m.logits + (long long)q * m.E, m.E, m.k, m.normalize, lane, t.id + q * m.k, t.w + q * m.k);
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < P; p += kThreads) atomicAdd(&t.act[t.id[p]], 1);  // (counts, for now)
+  __syncthreads();
+  if (warp == 0) {
+    // Exclusive sums of the counts and the list of active experts, 32 at a time.
+    int at = 0, na = 0, most = 0;
+    for (int e0 = 0; e0 < m.E; e0 += 32) {
+      const int e = e0 + lane, c = e < m.E ? t.act[e] : 0;
+      int s = c;
+      most = max(most, c);
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, s, d);
+        if (lane >= d) s += v;
+      }
+      if (e < m.E) t.first[e] = at + s - c;
+      at += __shfl_sync(0xffffffffu, s, 31);
+      const unsigned on = __ballot_sync(0xffffffffu, c > 0);
+      if (c > 0) t.act[na + __popc(on & ((1u << lane) - 1u))] = e;  // na + .. <= e: counts not yet read stay whole
+      na += __popc(on);
+      __syncwarp();
+    }
+    most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
+    if (lane == 0) {
+      t.first[m.E] = at;
+      bars->active = na;
+      bars->most = most;
+    }
+  }
+  __syncthreads();
+  for (int p = threadIdx.x; p < P; p += kThreads) {
+    const int e = t.id[p];
+    int at = t.first[e];
+    for (int q = 0; q < p; ++q) at += t.id[q] == e;
+    t.pos[p] = (uint16_t)at;
+    t.tok[at] = (uint16_t)(p / m.k);
+    if (blockIdx.x == 0) {
+      m.experts[p] = e;
+      m.weights[p] = t.w[p];
+    }
+  }
+  tc_fence_before();
+  // (One decision for the CTA: a timeout recorded earlier stops it here.)
+  if (threadIdx.x == 0) bars->go = g.status == nullptr || *(volatile int*)g.status == 0;
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem;
+  const int active = bars->active;
+  // Stages: the weights, then four token tiles of NB rows (a half of K each:
+  // x or the first terms of h, then the second terms), NB as this call's
+  // largest expert needs it.
+  const int NB = (bars->most + 15) / 16 * 16, stage_bytes = kWeightBytes + 4 * NB * 128;
+  const int NS = min(kMaxStages, g.ring / stage_bytes);
+  const long long units = bars->go ? (long long)active * (g.ta + g.tb) : 0;
+  const int ka = (int)((m.H + KS - 1) / KS), kb = (int)((m.I + KS - 1) / KS);
+
+  if (warp == 0) {
+    // ---------------- loads ----------------
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
+    Ring rs;
+    long long issued = 0;  // stages whose weights went out
+    bool ok = true;
+    auto stage = [&](int s) { return smem + (size_t)s * stage_bytes; };
+    for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
+      const Unit q = unit_at(u, g, t, active);
+      const int nk = q.down ? kb : ka, quads = (q.n + 3) / 4, rows16 = (q.n + 15) / 16;
+      const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * rows16 * 2048u : 2u * quads * 512u);
+      // Lane j gathers tokens 4 j .. 4 j + 3 of the expert (rows past its last: zeros).
+      int y[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[i] = !q.down && 4 * lane + i < q.n ? t.tok[q.p0 + 4 * lane + i] : m.T;
+      auto weights = [&](int ks, Ring r) -> bool {
+        const bool wok = wait_or_abort(&bars->empty[r.slot], r.phase ^ 1u, limit, abort_flag, g.status);
+        if (!__all_sync(0xffffffffu, wok)) return false;
+        if (g.stall) return true;
+        if (lane == 0) {
+          unsigned char* d = stage(r.slot);
+          uint64_t* bar = &bars->full[r.slot];
+          mbar_arrive_expect_tx(bar, bytes);
+          if (q.down) {
+            for (int i = 0; i < 4; ++i)  // box i: K half i / 2, rows 64 (i % 2)
+              tma_load_3d_hint(d + i * kBoxBytes, &mWd, ks * KS + (i >> 1) * 64, q.tile * 128 + (i & 1) * 64, q.e, bar, pol);
+          } else {
+            for (int i = 0; i < 2; ++i) {
+              tma_load_3d_hint(d + 2 * i * kBoxBytes, &mWg, ks * KS + i * 64, q.tile * 64, q.e, bar, pol);
+              tma_load_3d_hint(d + (2 * i + 1) * kBoxBytes, &mWu, ks * KS + i * 64, q.tile * 64, q.e, bar, pol);
+            }
+          }
+        }
+        __syncwarp();
+        return true;
+      };
+      auto tokens = [&](int ks, Ring r) {
+        if (g.stall) return;
+        unsigned char* d = stage(r.slot) + kWeightBytes;
+        uint64_t* bar = &bars->full[r.slot];
+        if (q.down) {
+          if (lane < 4 * rows16) {
+            const int half = lane & 1, term = lane >> 1 & 1, b = lane >> 2;
+            tma_load_2d(d + (2 * term + half) * NB * 128 + b * 2048, &mH, ks * KS + half * 64, term * P + q.p0 + b * 16, bar);
+          }
+        } else if (lane < quads) {
+          tma_gather4(d + lane * 512, &mX, ks * KS, y[0], y[1], y[2], y[3], bar);
+          tma_gather4(d + NB * 128 + lane * 512, &mX, ks * KS + 64, y[0], y[1], y[2], y[3], bar);
+        }
+        __syncwarp();
+      };
+      // A down unit's first weight tiles go out before the wait for h.
+      int ahead = 0;
+      Ring w = rs;
+      if (q.down) {
+        for (; ahead < nk && ahead < NS && ok; ++ahead, w.next(NS)) {
+          ok = weights(ahead, w);
+          if (!ok) break;
+          ++issued;
+        }
+        bool rok = ok;
+        if (ok && lane == 0) {
+          long long i = 0;
+          for (; i < limit; ++i) {
+            if (ld_acquire(g.ready + q.e) >= g.ta) break;
+            if ((i & 255) == 255 && *abort_flag) {
+              i = limit;
+              break;
+            }
+            __nanosleep(32);
+          }
+          if (i >= limit) {
+            rok = false;
+            *abort_flag = 1;
+            if (g.status) atomicExch(g.status, (int)DETFFN_ERR_TIMEOUT);
+          } else {
+            fence_proxy_async_global();  // the TMA loads below read what generic stores wrote
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, (int)rok, 0) != 0;
+        // (Also after a stop: stages with their weights out get their tokens, so that each completes.)
+        for (int ks = 0; ks < ahead; ++ks, rs.next(NS)) tokens(ks, rs);
+      }
+      for (int ks = ahead; ks < nk && ok; ++ks, rs.next(NS)) {
+        ok = weights(ks, rs);
+        if (!ok) break;
+        ++issued;
+        tokens(ks, rs);
+      }
+    }
+    // Drain: every stage that was filled has landed (long bound).
+    if (!g.stall && lane == 0) {
+      Ring r;
+      for (long long i = 0; i < issued; ++i, r.next(NS))
+        if (i + NS >= issued) mbar_wait(&bars->full[r.slot], r.phase, kDefaultSpin, nullptr);
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issue ----------------
+    Ring rs, rb;
+    bool ok = true;
+    for (long long u = blockIdx.x; u < units && ok; u += gridDim.x, rb.next(2)) {
+      const Unit q = unit_at(u, g, t, active);
+      const int nk = q.down ? kb : ka;
+      const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, (q.n + 15) / 16 * 16);
+      bool wok = wait_or_abort(&bars->acce[rb.slot], rb.phase ^ 1u, limit, abort_flag, g.status);
+      ok = __all_sync(0xffffffffu, wok) != 0;
+      for (int ks = 0; ks < nk && ok; ++ks, rs.next(NS)) {
+        wok = wait_or_abort(&bars->full[rs.slot], rs.phase, limit, abort_flag, g.status);
+        if (!__all_sync(0xffffffffu, wok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        unsigned char* d = smem + (size_t)rs.slot * stage_bytes;
+        if (elect_one()) {
+          for (int i = 0; i < (q.down ? 4 : 2); ++i) {
+            const uint64_t da = smem_desc_sw128(d + (i & 1) * 2 * kBoxBytes);
+            const uint64_t db = smem_desc_sw128(d + kWeightBytes + i * NB * 128);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_bf16(tmem + (uint32_t)(rb.slot * NB), da + 2u * kk, db + 2u * kk, idesc,
+                          ks > 0 || i > 0 || kk > 0 ? 1u : 0u);
+          }
+          tc_commit(&bars->empty[rs.slot]);
+          if (ks == nk - 1) tc_commit(&bars->accf[rb.slot]);
+        }
+        __syncwarp();
+      }
+    }
+    if (elect_one()) tc_commit(&bars->fin);
+    __syncwarp();
+    if (lane == 0) mbar_wait(&bars->fin, 0, kDefaultSpin, nullptr);
+  } else if (warp >= kEpi0) {
+    // ---------------- outputs ----------------
+    const int quarter = warp & 3, row = quarter * 32 + lane, et = threadIdx.x - kEpi0 * 32;
+    Ring rb;
+    for (long long u = blockIdx.x; u < units; u += gridDim.x, rb.next(2)) {
+      const Unit q = unit_at(u, g, t, active);
+      const bool aok = wait_or_abort(&bars->accf[rb.slot], rb.phase, limit, abort_flag, g.status);
+      // One decision for the four warps.
+      epi_sync();
+      if (et == 0) bars->go = 1;
+      epi_sync();
+      if (!aok) bars->go = 0;
+      epi_sync();
+      if (!bars->go) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * NB);
+      for (int c0 = 0; c0 < q.n; c0 += 16) {
+        uint32_t v[16];
+        tmem_ld16(taddr + (uint32_t)c0, v);
+        tmem_wait_ld();
+        if (q.down) {
+          const long long r = q.tile * 128ll + row;
+          if (r < m.H) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c0 + i < q.n) g.y[(long long)(q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]);
+          }
+        } else {
+          if (row >= 64) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) xch[i * 64 + row - 64] = __uint_as_float(v[i]);
+          }
+          epi_sync();
+          const long long r = q.tile * 64ll + row;
+          if (row < 64 && r < m.I) {
+            El* h = static_cast<El*>(m.h) + r;
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (c0 + i < q.n) {
+                const float gt = __uint_as_float(v[i]), hv = __fdividef(gt, 1.0f + __expf(-gt)) * xch[i * 64 + row];
+                El* at = h + (long long)(q.p0 + c0 + i) * m.I;
+                Io<DT>::st(at, hv);
+                const float left = hv - Io<DT>::ld(at);
+                // (Beyond the stored type's range the first term is an infinity and stays one.)
+                Io<DT>::st(at + P * m.I, fabsf(left) <= 3.4e38f ? left : 0.0f);
+              }
+          }
+          epi_sync();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->acce[rb.slot]);
+      if (q.down) {
+        epi_sync();
+        if (et == 0) {
+          __threadfence();
+          bars->go = atomicAdd(g.tickets + q.tile, 1) == active - 1 ? 2 : 1;
+        }
+        epi_sync();
+        if (bars->go == 2) {
+          // Every expert's part of this tile is in y: out of each token, its
+          // choices in order; a warp takes every fourth token, a lane four features.
+          __threadfence();
+          const long long r = q.tile * 128ll + 4 * lane;
+          if (r < m.H) {
+            for (int tk = quarter; tk < m.T; tk += 4) {
+              float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+              for (int j = 0; j < m.k; ++j) {
+                const int p = tk * m.k + j;
+                const float w = t.w[p];
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(g.y + (long long)t.pos[p] * m.H + r));
+                s.x = fmaf(w, v.x, s.x);
+                s.y = fmaf(w, v.y, s.y);
+                s.z = fmaf(w, v.z, s.z);
+                s.w = fmaf(w, v.w, s.w);
+              }
+              El* o = static_cast<El*>(m.out) + tk * m.H + r;
+              Io<DT>::st(o, s.x);
+              Io<DT>::st(o + 1, s.y);
+              Io<DT>::st(o + 2, s.z);
+              Io<DT>::st(o + 3, s.w);
+            }
+          }
+        }
+        epi_sync();
+      } else {
+        // h of this tile is written: count it.
+        fence_proxy_async_global();
+        epi_sync();
+        if (et == 0) {
+          __threadfence();
+          atomicAdd(g.ready + q.e, 1);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, tcols);
+  }
+}
+
+template <int DT>
+cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int sm_count, cudaStream_t st) {
+  static std::once_flag once;
+  static cudaError_t setup = cudaSuccess;
+  std::call_once(once, [] {
+    setup = cudaFuncSetAttribute(k_moe<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+  });
+  if (setup != cudaSuccess) return setup;
+  const bool f16 = DT == DETFFN_F16;
+  CUtensorMap mWg, mWu, mWd, mX, mH;
+  const long long dg[3] = {m.H, m.I, m.E}, dd[3] = {m.I, m.H, m.E}, dx[2] = {m.H, m.T}, dh[2] = {m.I, 2ll * m.T * m.k};
+  const int bw[3] = {64, 64, 1}, bx[2] = {64, 1}, bh[2] = {64, 16};
+  if (!tc_make_map_nd(&mWg, f16, m.Wg, 3, dg, bw) || !tc_make_map_nd(&mWu, f16, m.Wu, 3, dg, bw) ||
+      !tc_make_map_nd(&mWd, f16, m.Wd, 3, dd, bw) || !tc_make_map_nd(&mX, f16, m.x, 2, dx, bx) ||
+      !tc_make_map_nd(&mH, f16, m.h, 2, dh, bh))
+    return cudaErrorInvalidValue;
+  Args g{};
+  g.m = m;
+  g.NB = (m.T + 15) / 16 * 16;
+  const int stage = kWeightBytes + 4 * g.NB * 128;  // the largest
+  const int rest = 1024 + (int)((sizeof(Bars) + 127) & ~127) + kXch + tables_bytes(m.E, m.T * m.k);
+  g.ring = (kSmemMax - rest) & ~1023;
+  if (g.ring < 2 * stage) return cudaErrorInvalidConfiguration;
+  g.ta = (int)((m.I + 63) / 64);
+  g.tb = (int)((m.H + 127) / 128);
+  g.ready = sc.counters;
+  g.tickets = sc.counters + m.E;
+  g.y = sc.y;
+  g.status = wt.status;
+  g.spin = wt.spin;
+  g.stall = wt.stall;
+  cudaError_t e = launch_moe_logits(m, sc.counters, m.E + g.tb, st);
+  if (e != cudaSuccess) return e;
+  const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * (g.ta + g.tb);
+  const int grid = (int)(most < sm_count ? most : sm_count);
+  return launch_dependent(k_moe<DT>, dim3(grid), kThreads, kSmemMax, st, mWg, mWu, mWd, mX, mH, g);
+}
+
+}  // namespace
+
+bool moe_tensor_covers(const MoeArgs& m) {
+  const void* p[] = {m.x, m.Wg, m.Wu, m.Wd, m.h};
+  for (const void* q : p)
+    if ((uintptr_t)q & 15u) return false;
+  return m.dtype != DETFFN_F32 && m.H % 8 == 0 && m.I % 8 == 0;
+}
+
+cudaError_t launch_moe_tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int sm_count, cudaStream_t st) {
+  return m.dtype == DETFFN_F16 ? tensor<DETFFN_F16>(m, sc, wt, sm_count, st)
+                               : tensor<DETFFN_BF16>(m, sc, wt, sm_count, st);
+}
+
+}  // namespace detffn

@@ -751,6 +751,22 @@ EncodeTiledFn encode_fn() {
 
 }  // namespace
 
+bool tc_make_map_nd(CUtensorMap* m, bool f16, const void* base, int nd, const long long* dim, const int* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc || nd < 2 || nd > 3) return false;
+  cuuint64_t dims[3], strides[2];
+  cuuint32_t bx[3];
+  const cuuint32_t es[3] = {1, 1, 1};
+  for (int i = 0; i < nd; ++i) {
+    dims[i] = (cuuint64_t)dim[i];
+    bx[i] = (cuuint32_t)box[i];
+    if (i + 1 < nd) strides[i] = i ? strides[i - 1] * dims[i] : dims[i] * 2;
+  }
+  return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, nd, const_cast<void*>(base),
+             dims, strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc_make_map(CUtensorMap* m, const uint16_t* base, long long rows, long long K, long long ld, int box_rows) {
   EncodeTiledFn enc = encode_fn();
   if (!enc) return false;

@@ -20,11 +20,27 @@ struct MoeArgs {
   float* weights = nullptr;
   // Workspace: logits [T][E]; pos [T][k], the place of a token's slot among
   // the pairs ordered by expert; pair [T * k], the token * k + slot at each
-  // place; first [E + 1], each expert's first place; h [T * k][I].
+  // place; first [E + 1], each expert's first place; h, FP32
+  // [T * k][I] or two terms [2][T * k][I] of the stored type.
   float* logits = nullptr;
   int *pos = nullptr, *pair = nullptr, *first = nullptr;
   void* h = nullptr;
 };
+
+// Workspace of the tensor kernel alone: counters [E + ceil(H / 128)] and the
+// pairs' outputs y [T * k][H] in FP32.
+struct MoeScratch {
+  int* counters = nullptr;
+  float* y = nullptr;
+};
+
+// Router logits; block 0 clears n counters.
+cudaError_t launch_moe_logits(const MoeArgs& a, int* counters, int n, cudaStream_t st);
+
+// Tensor-core kernels (BF16 and FP16, widths multiples of 8, 16-byte-aligned
+// tensors).
+bool moe_tensor_covers(const MoeArgs& a);
+cudaError_t launch_moe_tensor(const MoeArgs& a, const MoeScratch& sc, const Waits& wt, int sm_count, cudaStream_t st);
 
 // CUDA-core kernels for any sizes (FP32, FP16 or BF16).
 cudaError_t launch_moe_general(const MoeArgs& a, cudaStream_t st);

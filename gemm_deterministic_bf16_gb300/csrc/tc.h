@@ -59,6 +59,10 @@ cudaError_t launch_tc_gemm(const uint16_t* A, long long lda, const uint16_t* B, 
 // swizzle, boxes of 64 (K) x box_rows.
 bool tc_make_map(CUtensorMap* m, const uint16_t* base, long long rows, long long K, long long ld, int box_rows);
 
+// A tensor map over a contiguous array of nd = 2 or 3 axes (innermost first;
+// BF16 or FP16, rows a multiple of 16 bytes), 128-byte swizzle.
+bool tc_make_map_nd(CUtensorMap* m, bool f16, const void* base, int nd, const long long* dim, const int* box);
+
 // ---------------------------------------------------------------------------
 // Few-token contractions (k_tcs.cu): out[r * ldo + c] = T_K(X[r, :], W[c, :])
 // for r < R <= 32 tokens and c < C weight rows, the weights streamed once with

@@ -439,8 +439,8 @@ DETFFN_API detffn_status detffn_ckpt8_silu_backward(const void* dh, const void* 
  *   out = sum over the chosen, in that order, of w * ((SiLU(x Wg[e]^T) * (x Wu[e]^T)) Wd[e]^T)
  * x [T, H], Wr [E, H], Wg, Wu [E, I, H], Wd [E, H, I], out [T, H], contiguous,
  * of `dtype`.  experts (int) and weights (FP32) [T, top_k] receive the
- * routing where not NULL.  Sums are FP32; the hidden activation is rounded
- * once to `dtype`.  A token's result does not depend on the other tokens of
+ * routing where not NULL.  Sums are FP32, the hidden activation keeps at least
+ * 16 significant bits, and out is rounded once.  A token's result does not depend on the other tokens of
  * the call.  A NaN logit is taken first and makes the token's weights NaN.
  * options->path: EXACT takes the CUDA-core kernels (any sizes and types).
  * `ws` is of detffn_moe_workspace_size bytes, 256-byte aligned. */
