@@ -299,28 +299,34 @@ __global__ void __launch_bounds__(512) k_bwd(const __grid_constant__ JoinArgs a)
   if (scalar && t == 0) p[blockIdx.x] = whole;
 }
 
-// out[c] = sum over sets of part[s][c]: eight threads per column take sets
-// q, q + 8, ... in order and their sums are added in order.
+constexpr int kSetReads = 10;
+static_assert(kJoinSets <= 32 * kSetReads, "a thread of k_sets reads at most kSetReads sets");
+
+// out[c] = sum over sets of part[s][c]: Q = blockDim / 32 threads per column
+// take sets q, q + Q, ... in order and their sums are added in order.
 template <int DT>
-__global__ void __launch_bounds__(256) k_sets(const float* __restrict__ part, int sets, long long n, void* out0,
+__global__ void __launch_bounds__(1024) k_sets(const float* __restrict__ part, int sets, long long n, void* out0,
                                               void* out1, void* out2, long long per, int pdtype) {
-  __shared__ float s[8][33];
+  __shared__ float s[32][33];
   grid_dep_wait();
   grid_dep_launch();
-  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, Q = blockDim.x >> 5;
   const long long c = blockIdx.x * 32ll + lane;
-  const float* p = part + blockIdx.y * per;
+  const float* p = part + blockIdx.y * per + c;
   float v = 0.0f;
-  if (c < n)
-    for (int k = q; k < sets; k += 8) v += p[(long long)k * n + c];
+  if (c < n) {
+#pragma unroll
+    for (int k = 0; k < kSetReads; ++k)   // (all reads under way before the first addition)
+      if (q + k * Q < sets) v += __ldcg(p + (long long)(q + k * Q) * n);
+  }
   s[q][lane] = v;
   __syncthreads();
   if (q == 0 && c < n) {
-#pragma unroll
-    for (int k = 1; k < 8; ++k) v += s[k][lane];
+    for (int k = 1; k < Q; ++k) v += s[k][lane];
     put_param<DT>(blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2, pdtype, c, v);
   }
 }
+inline int sets_threads(int sets) { return sets <= 8 * kSetReads ? 256 : sets <= 16 * kSetReads ? 512 : 1024; }
 
 inline bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -345,53 +351,6 @@ inline int pick(int H, int* threads) {
   while (v < 8 && (units + v - 1) / v > 512) v *= 2;
   *threads = ((units + v - 1) / v + 31) / 32 * 32;
   return v;
-}
-
-template <int DT>
-cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
-  int threads;
-  const int v = pick(a.H, &threads);
-  const bool vec = vectors<DT>(a);
-  const long long most = 152ll * 16;
-  const dim3 grid((unsigned)(a.M < most ? a.M : most));
-  auto go = [&](auto k) { return launch_dependent(k, grid, threads, 0, st, a); };
-  switch (v) {
-    case 1: return go(vec ? k_fwd<DT, 1, true> : k_fwd<DT, 1, false>);
-    case 2: return go(vec ? k_fwd<DT, 2, true> : k_fwd<DT, 2, false>);
-    case 4: return go(vec ? k_fwd<DT, 4, true> : k_fwd<DT, 4, false>);
-    default: return go(vec ? k_fwd<DT, 8, true> : k_fwd<DT, 8, false>);
-  }
-}
-
-template <int DT>
-cudaError_t backward(const JoinArgs& a, cudaStream_t st) {
-  int threads;
-  const int v = pick(a.H, &threads);
-  const bool vec = vectors<DT>(a);
-  const int sets = (int)(a.M < kJoinSets ? a.M : kJoinSets);
-  auto go = [&](auto k) { return launch_dependent(k, dim3(sets), threads, 0, st, a); };
-  cudaError_t e;
-  switch (v) {
-    case 1: e = go(vec ? k_bwd<DT, 1, true> : k_bwd<DT, 1, false>); break;
-    case 2: e = go(vec ? k_bwd<DT, 2, true> : k_bwd<DT, 2, false>); break;
-    case 4: e = go(vec ? k_bwd<DT, 4, true> : k_bwd<DT, 4, false>); break;
-    default: e = go(vec ? k_bwd<DT, 8, true> : k_bwd<DT, 8, false>); break;
-  }
-  if (e != cudaSuccess) return e;
-  void* out[3] = {};
-  int n = 0;
-  if (a.dw_post) out[n++] = a.dw_post;
-  if (a.dw_pre) out[n++] = a.dw_pre;
-  if (a.dgate && a.gate_cs && !a.gate_rs) out[n++] = a.dgate;
-  if (n) {
-    e = launch_dependent(k_sets<DT>, dim3((unsigned)((a.H + 31) / 32), n), 256, 0, st, (const float*)a.part, sets,
-                         (long long)a.H, out[0], out[1], out[2], (long long)sets * a.H, a.pdtype);
-    if (e != cudaSuccess) return e;
-  }
-  if (a.dgate && !a.gate_cs && !a.gate_rs)
-    e = launch_dependent(k_sets<DT>, dim3(1), 256, 0, st, (const float*)a.part + (long long)n * sets * a.H, sets, 1ll,
-                         a.dgate, (void*)nullptr, (void*)nullptr, 0ll, a.pdtype);
-  return e;
 }
 
 }  // namespace join
