@@ -340,7 +340,7 @@ MoeArgs moe_plan(Arena& w, long long T, long long E, long long k, long long H, l
   a.pair = w.take<int>(T * k);
   a.first = w.take<int>(E + 1);
   a.h = w.take<char>(T * k * I * 4);
-  sc->counters = w.take<int>(E + (H + 127) / 128);
+  sc->counters = w.take<int>(1 + E + (H + 127) / 128);
   sc->y = w.take<float>(T * k * H);
   return a;
 }

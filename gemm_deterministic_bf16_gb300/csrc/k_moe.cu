@@ -24,10 +24,68 @@ __device__ __forceinline__ float warp_dot(const typename Io<DT>::E* a, const typ
   return warp_sum(s);
 }
 
-// Logits of expert blockIdx.x: one warp per token.  With VEC lane l takes
-// features 8 l .. 8 l + 7, 8 l + 256 .., ... (16-byte loads, several in flight).
+// Router logits of four tokens and four experts by one block: each of eight
+// warps takes an eighth of H (in 16-byte vectors; a token's sum is split by H
+// alone), the sixteen sums of a warp meet in sixteen exchanges instead of
+// eighty, and sixteen threads add the warps' parts in order.  What bounds it
+// is the latency of its loads, so all of a warp's are independent.
 // Block 0 also clears the counters of the kernel that follows.
-template <int DT, bool VEC>
+template <int DT>
+__global__ void __launch_bounds__(256) k_logits_tile(const __grid_constant__ MoeArgs a, int* counters, int n) {
+  __shared__ float part[8][16];
+  grid_dep_wait();
+  grid_dep_launch();
+  using E = typename Io<DT>::E;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e0 = blockIdx.x * 4, t0 = blockIdx.y * 4;
+  if (blockIdx.x == 0 && blockIdx.y == 0)
+    for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
+  const int vecs = (int)(a.H / 8), per = (vecs + 7) / 8, lo = warp * per, hi = min(vecs, lo + per);
+  const E* x = static_cast<const E*>(a.x) + t0 * a.H;
+  const E* w = static_cast<const E*>(a.Wr) + e0 * a.H;
+  const int nt = min(4, a.T - t0), ne = min(4, a.E - e0);
+  float v[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+#pragma unroll 2
+  for (int c = lo + lane; c < hi; c += 32) {
+    float p[4][8], q[4][8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      // (past the last token or expert: the last one's, and its sum is not stored)
+      Io<DT>::ld8(x + min(i, nt - 1) * a.H + 8 * c, p[i]);
+      Io<DT>::ld8(w + min(i, ne - 1) * a.H + 8 * c, q[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i] = fmaf(p[i >> 2][j], q[i & 3][j], v[i]);
+  }
+  // Lane l keeps the half of the values that bit 0, 1, 2, 3 of l names in turn:
+  // it ends with value l & 15 (bits reversed), then both halves of the warp add.
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int half = 8 >> b;
+    const bool up = lane >> b & 1;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half];
+      v[i] = (up ? v[i + half] : v[i]) + __shfl_xor_sync(0xffffffffu, send, 1 << b);
+    }
+  }
+  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
+  if (lane < 16) part[warp][((lane & 1) << 3) | ((lane & 2) << 1) | ((lane & 4) >> 1) | ((lane & 8) >> 3)] = v[0];
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    const int t = threadIdx.x >> 2, e = threadIdx.x & 3;
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += part[i][threadIdx.x];
+    if (t < nt && e < ne) a.logits[(long long)(t0 + t) * a.E + e0 + e] = s;
+  }
+}
+
+// The same for any H and alignment: expert blockIdx.x, one warp per token.
+template <int DT>
 __global__ void __launch_bounds__(256) k_logits(const __grid_constant__ MoeArgs a, int* counters, int n) {
   grid_dep_wait();
   grid_dep_launch();
@@ -35,24 +93,8 @@ __global__ void __launch_bounds__(256) k_logits(const __grid_constant__ MoeArgs 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.x;
   if (e == 0)
     for (int i = threadIdx.x; i < n; i += blockDim.x) counters[i] = 0;
-  const E* w = static_cast<const E*>(a.Wr) + e * a.H;
   for (int t = warp; t < a.T; t += 8) {
-    const E* x = static_cast<const E*>(a.x) + t * a.H;
-    float s;
-    if (VEC) {
-      s = 0.0f;
-#pragma unroll 4
-      for (long long c = 8 * lane; c < a.H; c += 256) {
-        float p[8], q[8];
-        Io<DT>::ld8(x + c, p);
-        Io<DT>::ld8(w + c, q);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s = fmaf(p[j], q[j], s);
-      }
-      s = warp_sum(s);
-    } else {
-      s = warp_dot<DT>(x, w, a.H, lane);
-    }
+    const float s = warp_dot<DT>(static_cast<const E*>(a.x) + t * a.H, static_cast<const E*>(a.Wr) + e * a.H, a.H, lane);
     if (lane == 0) a.logits[t * a.E + e] = s;
   }
 }
@@ -63,9 +105,13 @@ __global__ void __launch_bounds__(1024) k_select(const __grid_constant__ MoeArgs
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = a.T * a.k;
-  for (int t = warp; t < a.T; t += blockDim.x / 32)
-    moe_choose<kMoeMaxExperts / 32>(a.logits + (long long)t * a.E, a.E, a.k, a.normalize, lane, a.experts + t * a.k,
-                                    a.weights + t * a.k);
+  for (int t = warp; t < a.T; t += blockDim.x / 32) {
+    const MoeChoice c = moe_choose<kMoeMaxExperts / 32>(a.logits + (long long)t * a.E, a.E, a.k, a.normalize, lane);
+    if (lane < a.k) {
+      a.experts[t * a.k + lane] = c.expert;
+      a.weights[t * a.k + lane] = c.weight;
+    }
+  }
   __syncthreads();
   for (int p = threadIdx.x; p < P; p += blockDim.x) ids[p] = a.experts[p];
   __syncthreads();
@@ -132,7 +178,8 @@ __global__ void __launch_bounds__(256) k_down(const __grid_constant__ MoeArgs a)
 template <int DT>
 cudaError_t logits(const MoeArgs& a, int* counters, int n, cudaStream_t st) {
   const bool vec = a.H % 8 == 0 && (((uintptr_t)a.x | (uintptr_t)a.Wr) & 15u) == 0;
-  return launch_dependent(vec ? k_logits<DT, true> : k_logits<DT, false>, dim3(a.E), 256, 0, st, a, counters, n);
+  if (vec) return launch_dependent(k_logits_tile<DT>, dim3((a.E + 3) / 4, (a.T + 3) / 4), 256, 0, st, a, counters, n);
+  return launch_dependent(k_logits<DT>, dim3(a.E), 256, 0, st, a, counters, n);
 }
 
 template <int DT>

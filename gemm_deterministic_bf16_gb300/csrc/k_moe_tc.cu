@@ -10,7 +10,9 @@
 //     outputs y of the pairs
 // All gate/up units come before all down units, experts in ascending order.
 // A down unit waits (bounded) until its expert's gate/up units are counted,
-// with its first weight tiles already on their way; the CTA that finishes
+// with its first weight tiles already on their way.  Those units were claimed
+// earlier, by CTAs that are running and wait for nothing themselves, so the
+// wait ends whatever else holds the other SMs; the CTA that finishes
 // the last expert of a 128-feature tile of the output adds the pairs of each
 // token there, in the order of its choices.
 //
@@ -48,12 +50,14 @@ constexpr int kBoxBytes = 64 * 128;              // 64 rows x 64 K
 constexpr int kWeightBytes = 4 * kBoxBytes;      // 128 rows x 128 K
 constexpr int kMaxStages = 8;
 constexpr int kSmemMax = 227 * 1024;
+constexpr int kUnits = 4;                        // units a CTA has claimed and not finished, at most
 constexpr int kXch = 64 * 16 * 4;                // up values of one 16-column chunk
 
 struct Bars {
-  uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], fin;
+  uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], ufull[kUnits], uempty[kUnits], fin;
   uint32_t tmem;
   int abort, go;
+  int unit[kUnits];  // claimed units; past the last: no more
   int active;   // experts with tokens
   int most;     // most tokens of one expert
 };
@@ -63,6 +67,7 @@ struct Args {
   int NB;            // most token columns of a unit (T rounded up to 16)
   int ring;          // bytes for stages
   int ta, tb;        // gate/up units and down units of an expert
+  int* claim;        // units claimed by all CTAs
   int* ready;        // [E] gate/up units done
   int* tickets;      // [tb] down units done
   float* y;          // [T * k][H]
@@ -107,20 +112,37 @@ __device__ __forceinline__ int ld_acquire(const int* p) {
 }
 __device__ __forceinline__ void fence_proxy_async_global() { asm volatile("fence.proxy.async.global;" ::: "memory"); }
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The same barrier; whether `ok` held in all 128 threads.
+__device__ __forceinline__ bool epi_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
 
-// The routing tables in shared memory.
+// The routing tables in shared memory.  A token takes an expert once, so an
+// expert's tokens are a mask of 64 bits, and a pair's place among the pairs
+// ordered by expert and token is the expert's first plus a count of bits.
 struct Tables {
+  uint32_t* mask;   // [E][2] tokens of each expert
   int* first;       // [E + 1] first pair of each expert
   int* act;         // [E] active experts, ascending
   float* w;         // [P] weights by pair (token * k + slot)
   uint16_t* id;     // [P] expert by pair
-  uint16_t* pos;    // [P] place of a pair in expert order
+  uint16_t* pos;    // [P] place of a pair
   uint16_t* tok;    // [P] token at each place
 };
-__host__ __device__ inline int tables_bytes(int E, int P) { return ((E + 1 + E + P) * 4 + 3 * P * 2 + 15) & ~15; }
+__host__ __device__ inline int tables_bytes(int E, int P) { return ((2 * E + E + 1 + E + P) * 4 + 3 * P * 2 + 15) & ~15; }
 __device__ __forceinline__ Tables tables_at(unsigned char* p, int E, int P) {
   Tables t;
-  t.first = reinterpret_cast<int*>(p);
+  t.mask = reinterpret_cast<uint32_t*>(p);
+  t.first = reinterpret_cast<int*>(t.mask + 2 * E);
   t.act = t.first + E + 1;
   t.w = reinterpret_cast<float*>(t.act + E);
   t.id = reinterpret_cast<uint16_t*>(t.w + P);
@@ -133,14 +155,14 @@ struct Unit {
   bool down;
   int a, tile, e, p0, n;   // active index, tile of the expert, expert, first pair, pairs
 };
-__device__ __forceinline__ Unit unit_at(long long u, const Args& g, const Tables& t, int active) {
+__device__ __forceinline__ Unit unit_at(int u, const Args& g, const Tables& t, int active) {
   Unit r;
-  const long long na = (long long)active * g.ta;
+  const int na = active * g.ta;
   r.down = u >= na;
-  const long long v = r.down ? u - na : u;
+  const int v = r.down ? u - na : u;
   const int per = r.down ? g.tb : g.ta;
-  r.a = (int)(v / per);
-  r.tile = (int)(v - (long long)r.a * per);
+  r.a = v / per;
+  r.tile = v - r.a * per;
   r.e = t.act[r.a];
   r.p0 = t.first[r.e];
   r.n = t.first[r.e + 1] - r.p0;
@@ -173,6 +195,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->accf[b], 1);
       mbar_init(&bars->acce[b], 4);
     }
+    for (int q = 0; q < kUnits; ++q) {
+      mbar_init(&bars->ufull[q], 1);
+      mbar_init(&bars->uempty[q], 5);   // the MMA warp and four epilogue warps
+    }
     mbar_init(&bars->fin, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -182,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&mX);
     prefetch_tmap(&mH);
   }
-  const uint32_t tcols = 2 * g.NB <= 32 ? 32 : 2 * g.NB <= 64 ? 64 : 128;  // two accumulators of NB columns
+  const uint32_t tcols = g.NB <= 16 ? 64 : g.NB <= 32 ? 128 : 256;  // two accumulators of 2 NB columns
   if (warp == 1) {
     tmem_alloc(&bars->tmem, tcols);
     tmem_relinquish();
@@ -190,20 +216,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
 
+  // The first claim, under way during the routing.
+  int claimed = 0;
+  if (threadIdx.x == 0) claimed = atomicAdd(g.claim, 1);
+
   // ---------------- the routing ----------------
-  for (int e = threadIdx.x; e < m.E; e += kThreads) t.act[e] = 0;
-  for (int q = warp; q < m.T; q += kThreads / 32) {
-    if (m.E <= 128) moe_choose<4>(m.logits + (long long)q * m.E, m.E, m.k, m.normalize, lane, t.id + q * m.k, t.w + q * m.k);
-    else moe_choose<16>(m.logits + (long long)q * m.E, m.E, m.k, m.normalize, lane, t.id + q * m.k, t.w + q * m.k);
-  }
+  for (int e = threadIdx.x; e < 2 * m.E; e += kThreads) t.mask[e] = 0;
   __syncthreads();
-  for (int p = threadIdx.x; p < P; p += kThreads) atomicAdd(&t.act[t.id[p]], 1);  // (counts, for now)
+  for (int q = warp; q < m.T; q += kThreads / 32) {
+    const float* l = m.logits + (long long)q * m.E;
+    const MoeChoice c = m.E <= 128 ? moe_choose<4>(l, m.E, m.k, m.normalize, lane)
+                                   : moe_choose<kMoeMaxExperts / 32>(l, m.E, m.k, m.normalize, lane);
+    if (lane < m.k) {
+      const int p = q * m.k + lane;
+      t.id[p] = (uint16_t)c.expert;
+      t.w[p] = c.weight;
+      atomicOr(&t.mask[2 * c.expert + (q >> 5)], 1u << (q & 31));
+      if (blockIdx.x == 0) {
+        m.experts[p] = c.expert;
+        m.weights[p] = c.weight;
+      }
+    }
+  }
   __syncthreads();
   if (warp == 0) {
     // Exclusive sums of the counts and the list of active experts, 32 at a time.
     int at = 0, na = 0, most = 0;
     for (int e0 = 0; e0 < m.E; e0 += 32) {
-      const int e = e0 + lane, c = e < m.E ? t.act[e] : 0;
+      const int e = e0 + lane, c = e < m.E ? __popc(t.mask[2 * e]) + __popc(t.mask[2 * e + 1]) : 0;
       int s = c;
       most = max(most, c);
 #pragma unroll
@@ -214,9 +254,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (e < m.E) t.first[e] = at + s - c;
       at += __shfl_sync(0xffffffffu, s, 31);
       const unsigned on = __ballot_sync(0xffffffffu, c > 0);
-      if (c > 0) t.act[na + __popc(on & ((1u << lane) - 1u))] = e;  // na + .. <= e: counts not yet read stay whole
+      if (c > 0) t.act[na + __popc(on & ((1u << lane) - 1u))] = e;
       na += __popc(on);
-      __syncwarp();
     }
     most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
     if (lane == 0) {
@@ -227,15 +266,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   __syncthreads();
   for (int p = threadIdx.x; p < P; p += kThreads) {
-    const int e = t.id[p];
-    int at = t.first[e];
-    for (int q = 0; q < p; ++q) at += t.id[q] == e;
+    const int e = t.id[p], q = p / m.k;
+    const uint64_t mask = ((uint64_t)t.mask[2 * e + 1] << 32) | t.mask[2 * e];
+    const int at = t.first[e] + __popcll(mask & ((1ull << q) - 1ull));
     t.pos[p] = (uint16_t)at;
-    t.tok[at] = (uint16_t)(p / m.k);
-    if (blockIdx.x == 0) {
-      m.experts[p] = e;
-      m.weights[p] = t.w[p];
-    }
+    t.tok[at] = (uint16_t)q;
   }
   tc_fence_before();
   // (One decision for the CTA: a timeout recorded earlier stops it here.)
@@ -244,23 +279,34 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   const int active = bars->active;
-  // Stages: the weights, then four token tiles of NB rows (a half of K each:
-  // x or the first terms of h, then the second terms), NB as this call's
+  // Stages: the weights, then for each half of K a token tile of up to 2 NB
+  // rows (x; or the first terms of h and then the second), NB as this call's
   // largest expert needs it.
   const int NB = (bars->most + 15) / 16 * 16, stage_bytes = kWeightBytes + 4 * NB * 128;
   const int NS = min(kMaxStages, g.ring / stage_bytes);
-  const long long units = bars->go ? (long long)active * (g.ta + g.tb) : 0;
+  const int units = bars->go ? active * (g.ta + g.tb) : 0;
   const int ka = (int)((m.H + KS - 1) / KS), kb = (int)((m.I + KS - 1) / KS);
 
   if (warp == 0) {
     // ---------------- loads ----------------
     uint64_t pol;
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(pol));
-    Ring rs;
+    Ring rs, ru;
     long long issued = 0;  // stages whose weights went out
     bool ok = true;
     auto stage = [&](int s) { return smem + (size_t)s * stage_bytes; };
-    for (long long u = blockIdx.x; u < units && ok; u += gridDim.x) {
+    int u = __shfl_sync(0xffffffffu, claimed, 0);
+    while (true) {
+      // Hand the claimed unit (or the end) to the other warps.
+      if (!__all_sync(0xffffffffu, wait_or_abort(&bars->uempty[ru.slot], ru.phase ^ 1u, limit, abort_flag, g.status))) break;
+      if (lane == 0) {
+        bars->unit[ru.slot] = u;
+        mbar_arrive(&bars->ufull[ru.slot]);
+      }
+      __syncwarp();
+      ru.next(kUnits);
+      if (u >= units) break;
+      if (lane == 0) claimed = atomicAdd(g.claim, 1);  // the next, under way during this one
       const Unit q = unit_at(u, g, t, active);
       const int nk = q.down ? kb : ka, quads = (q.n + 3) / 4, rows16 = (q.n + 15) / 16;
       const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * rows16 * 2048u : 2u * quads * 512u);
@@ -295,12 +341,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* bar = &bars->full[r.slot];
         if (q.down) {
           if (lane < 4 * rows16) {
+            // (the second terms' rows follow the first terms' of this unit)
             const int half = lane & 1, term = lane >> 1 & 1, b = lane >> 2;
-            tma_load_2d(d + (2 * term + half) * NB * 128 + b * 2048, &mH, ks * KS + half * 64, term * P + q.p0 + b * 16, bar);
+            tma_load_2d(d + half * 2 * NB * 128 + (term * rows16 + b) * 2048, &mH, ks * KS + half * 64,
+                        term * P + q.p0 + b * 16, bar);
           }
         } else if (lane < quads) {
           tma_gather4(d + lane * 512, &mX, ks * KS, y[0], y[1], y[2], y[3], bar);
-          tma_gather4(d + NB * 128 + lane * 512, &mX, ks * KS + 64, y[0], y[1], y[2], y[3], bar);
+          tma_gather4(d + 2 * NB * 128 + lane * 512, &mX, ks * KS + 64, y[0], y[1], y[2], y[3], bar);
         }
         __syncwarp();
       };
@@ -342,6 +390,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++issued;
         tokens(ks, rs);
       }
+      if (!ok) break;
+      u = __shfl_sync(0xffffffffu, claimed, 0);
     }
     // Drain: every stage that was filled has landed (long bound).
     if (!g.stall && lane == 0) {
@@ -351,13 +401,21 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     // ---------------- MMA issue ----------------
-    Ring rs, rb;
+    Ring rs, rb, ru;
     bool ok = true;
-    for (long long u = blockIdx.x; u < units && ok; u += gridDim.x, rb.next(2)) {
+    while (true) {
+      bool wok = wait_or_abort(&bars->ufull[ru.slot], ru.phase, limit, abort_flag, g.status);
+      if (!__all_sync(0xffffffffu, wok)) break;
+      const int u = bars->unit[ru.slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->uempty[ru.slot]);
+      ru.next(kUnits);
+      if (u >= units) break;
       const Unit q = unit_at(u, g, t, active);
-      const int nk = q.down ? kb : ka;
-      const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, (q.n + 15) / 16 * 16);
-      bool wok = wait_or_abort(&bars->acce[rb.slot], rb.phase ^ 1u, limit, abort_flag, g.status);
+      const int nk = q.down ? kb : ka, cols = (q.n + 15) / 16 * 16;
+      const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, q.down ? 2 * cols : cols);
+      const uint32_t acc = tmem + (uint32_t)(rb.slot * 2 * g.NB);
+      wok = wait_or_abort(&bars->acce[rb.slot], rb.phase ^ 1u, limit, abort_flag, g.status);
       ok = __all_sync(0xffffffffu, wok) != 0;
       for (int ks = 0; ks < nk && ok; ++ks, rs.next(NS)) {
         wok = wait_or_abort(&bars->full[rs.slot], rs.phase, limit, abort_flag, g.status);
@@ -368,19 +426,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         unsigned char* d = smem + (size_t)rs.slot * stage_bytes;
         if (elect_one()) {
-          for (int i = 0; i < (q.down ? 4 : 2); ++i) {
-            const uint64_t da = smem_desc_sw128(d + (i & 1) * 2 * kBoxBytes);
-            const uint64_t db = smem_desc_sw128(d + kWeightBytes + i * NB * 128);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const uint64_t da = smem_desc_sw128(d + half * 2 * kBoxBytes);
+            const uint64_t db = smem_desc_sw128(d + kWeightBytes + half * 2 * NB * 128);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_bf16(tmem + (uint32_t)(rb.slot * NB), da + 2u * kk, db + 2u * kk, idesc,
-                          ks > 0 || i > 0 || kk > 0 ? 1u : 0u);
+              tc_mma_bf16(acc, da + 2u * kk, db + 2u * kk, idesc, ks > 0 || half > 0 || kk > 0 ? 1u : 0u);
           }
           tc_commit(&bars->empty[rs.slot]);
           if (ks == nk - 1) tc_commit(&bars->accf[rb.slot]);
         }
         __syncwarp();
       }
+      if (!ok) break;
+      rb.next(2);
     }
     if (elect_one()) tc_commit(&bars->fin);
     __syncwarp();
@@ -388,24 +448,30 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= kEpi0) {
     // ---------------- outputs ----------------
     const int quarter = warp & 3, row = quarter * 32 + lane, et = threadIdx.x - kEpi0 * 32;
-    Ring rb;
-    for (long long u = blockIdx.x; u < units; u += gridDim.x, rb.next(2)) {
-      const Unit q = unit_at(u, g, t, active);
-      const bool aok = wait_or_abort(&bars->accf[rb.slot], rb.phase, limit, abort_flag, g.status);
-      // One decision for the four warps.
-      epi_sync();
-      if (et == 0) bars->go = 1;
-      epi_sync();
-      if (!aok) bars->go = 0;
-      epi_sync();
-      if (!bars->go) break;
+    Ring rb, ru;
+    for (;; rb.next(2)) {
+      // The next unit, and its sums.
+      bool aok = wait_or_abort(&bars->ufull[ru.slot], ru.phase, limit, abort_flag, g.status);
+      const int u = aok ? bars->unit[ru.slot] : 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars->uempty[ru.slot]);
+      ru.next(kUnits);
+      const Unit q = unit_at(aok && u < units ? u : 0, g, t, active);
+      if (aok && u < units) aok = wait_or_abort(&bars->accf[rb.slot], rb.phase, limit, abort_flag, g.status);
+      // One decision for the four warps: with a barrier each below, none may
+      // leave alone.
+      if (!epi_all(aok) || u >= units) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * NB);
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * 2 * g.NB);
       for (int c0 = 0; c0 < q.n; c0 += 16) {
         uint32_t v[16];
         tmem_ld16(taddr + (uint32_t)c0, v);
-        tmem_wait_ld();
         if (q.down) {
+          uint32_t v2[16];   // the second terms' part
+          tmem_ld16(taddr + (uint32_t)((q.n + 15) / 16 * 16 + c0), v2);
+          tmem_wait_ld();
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(v2[i]));
           const long long r = q.tile * 128ll + row;
           if (r < m.H) {
 #pragma unroll
@@ -413,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (c0 + i < q.n) g.y[(long long)(q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]);
           }
         } else {
+          tmem_wait_ld();
           if (row >= 64) {
 #pragma unroll
             for (int i = 0; i < 16; ++i) xch[i * 64 + row - 64] = __uint_as_float(v[i]);
@@ -476,8 +543,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_global();
         epi_sync();
         if (et == 0) {
-          __threadfence();
-          atomicAdd(g.ready + q.e, 1);
+          asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(g.ready + q.e) : "memory");
         }
       }
     }
@@ -516,13 +582,14 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   if (g.ring < 2 * stage) return cudaErrorInvalidConfiguration;
   g.ta = (int)((m.I + 63) / 64);
   g.tb = (int)((m.H + 127) / 128);
-  g.ready = sc.counters;
-  g.tickets = sc.counters + m.E;
+  g.claim = sc.counters;
+  g.ready = sc.counters + 1;
+  g.tickets = g.ready + m.E;
   g.y = sc.y;
   g.status = wt.status;
   g.spin = wt.spin;
   g.stall = wt.stall;
-  cudaError_t e = launch_moe_logits(m, sc.counters, m.E + g.tb, st);
+  cudaError_t e = launch_moe_logits(m, sc.counters, 1 + m.E + g.tb, st);
   if (e != cudaSuccess) return e;
   const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * (g.ta + g.tb);
   const int grid = (int)(most < sm_count ? most : sm_count);

@@ -27,7 +27,7 @@ struct MoeArgs {
   void* h = nullptr;
 };
 
-// Workspace of the tensor kernel alone: counters [E + ceil(H / 128)] and the
+// Workspace of the tensor kernel alone: counters [1 + E + ceil(H / 128)] and the
 // pairs' outputs y [T * k][H] in FP32.
 struct MoeScratch {
   int* counters = nullptr;
