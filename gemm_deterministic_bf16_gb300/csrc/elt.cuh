@@ -42,6 +42,7 @@ template <> struct Io<DETFFN_F16> {
   static constexpr int kBytes = 2;
   __device__ static float ld(const E* p) { return __half2float(__ushort_as_half(*p)); }
   __device__ static void st(E* p, float v) { *p = __half_as_ushort(__float2half_rn(v)); }
+  __device__ static float round(float v) { return __half2float(__float2half_rn(v)); }
   __device__ static float2 two(uint32_t w) {
     return __half22float2(*reinterpret_cast<const __half2*>(&w));
   }
@@ -62,6 +63,7 @@ template <> struct Io<DETFFN_BF16> {
   static constexpr int kBytes = 2;
   __device__ static float ld(const E* p) { return bf2f(*p); }
   __device__ static void st(E* p, float v) { *p = f2bf(v); }
+  __device__ static float round(float v) { return bf2f(f2bf(v)); }
   __device__ static float2 two(uint32_t w) {
     return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   }

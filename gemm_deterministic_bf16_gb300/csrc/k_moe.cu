@@ -102,15 +102,22 @@ __global__ void __launch_bounds__(256) k_logits(const __grid_constant__ MoeArgs 
 // The choices of all tokens and the pairs ordered by expert, by one block.
 __global__ void __launch_bounds__(1024) k_select(const __grid_constant__ MoeArgs a) {
   __shared__ int ids[kMoeMaxTokens * kMoeMaxTopK], count[kMoeMaxExperts + 1];
+  __shared__ float chosen[kMoeMaxTokens * kMoeMaxTopK];
   grid_dep_wait();
   grid_dep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = a.T * a.k;
   for (int t = warp; t < a.T; t += blockDim.x / 32) {
-    const MoeChoice c = moe_choose<kMoeMaxExperts / 32>(a.logits + (long long)t * a.E, a.E, a.k, a.normalize, lane);
+    const float* l = a.logits + (long long)t * a.E;
+    uint32_t key[kMoeMaxExperts / 32];
+    moe_keys<kMoeMaxExperts / 32>(a.logits, a.T, a.E, t, lane, key);
+    const MoeChoice c = moe_choose<kMoeMaxExperts / 32>(key, a.k, lane);
     if (lane < a.k) {
       a.experts[t * a.k + lane] = c.expert;
-      a.weights[t * a.k + lane] = c.weight;
+      chosen[t * a.k + lane] = c.logit;
     }
+    __syncwarp();
+    const float all = a.normalize ? -1.0f : moe_sum(l, a.E, chosen[t * a.k], lane);
+    if (lane < a.k) a.weights[t * a.k + lane] = moe_weight(chosen + t * a.k, a.k, lane, all);
   }
   __syncthreads();
   for (int p = threadIdx.x; p < P; p += blockDim.x) ids[p] = a.experts[p];

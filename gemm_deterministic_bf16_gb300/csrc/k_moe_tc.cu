@@ -43,7 +43,8 @@ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-constexpr int kThreads = 256;     // warp 0 loads, warp 1 issues MMAs, warps 4-7 form the outputs
+constexpr int kThreads = 512;     // all work out the routing; then warp 0 loads, warp 1 issues MMAs, warp 2
+                                  // forms the routing weights, warps 4-7 the outputs
 constexpr int kEpi0 = 4;          // first epilogue warp (its TMEM lane quarter is warp % 4)
 constexpr int KS = 128;           // K positions of a stage
 constexpr int kBoxBytes = 64 * 128;              // 64 rows x 64 K
@@ -51,10 +52,10 @@ constexpr int kWeightBytes = 4 * kBoxBytes;      // 128 rows x 128 K
 constexpr int kMaxStages = 8;
 constexpr int kSmemMax = 227 * 1024;
 constexpr int kUnits = 4;                        // units a CTA has claimed and not finished, at most
-constexpr int kXch = 64 * 16 * 4;                // up values of one 16-column chunk
+constexpr int kXch = 128 * 8 * 4;                // gate and up values of eight tokens
 
 struct Bars {
-  uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], ufull[kUnits], uempty[kUnits], fin;
+  uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], ufull[kUnits], uempty[kUnits], weights, fin;
   uint32_t tmem;
   int abort, go;
   int unit[kUnits];  // claimed units; past the last: no more
@@ -64,7 +65,7 @@ struct Bars {
 
 struct Args {
   MoeArgs m;
-  int NB;            // most token columns of a unit (T rounded up to 16)
+  int cols;          // most columns of a unit's sums: twice T rounded up to 8
   int ring;          // bytes for stages
   int ta, tb;        // gate/up units and down units of an expert
   int* claim;        // units claimed by all CTAs
@@ -133,18 +134,22 @@ struct Tables {
   uint32_t* mask;   // [E][2] tokens of each expert
   int* first;       // [E + 1] first pair of each expert
   int* act;         // [E] active experts, ascending
-  float* w;         // [P] weights by pair (token * k + slot)
+  float* l;         // [P] chosen logits by pair (token * k + slot)
+  float* w;         // [P] weights by pair
   uint16_t* id;     // [P] expert by pair
   uint16_t* pos;    // [P] place of a pair
   uint16_t* tok;    // [P] token at each place
 };
-__host__ __device__ inline int tables_bytes(int E, int P) { return ((2 * E + E + 1 + E + P) * 4 + 3 * P * 2 + 15) & ~15; }
+__host__ __device__ inline int tables_bytes(int E, int P) {
+  return ((4 * E + 1 + 2 * P) * 4 + 3 * P * 2 + 15) & ~15;
+}
 __device__ __forceinline__ Tables tables_at(unsigned char* p, int E, int P) {
   Tables t;
   t.mask = reinterpret_cast<uint32_t*>(p);
   t.first = reinterpret_cast<int*>(t.mask + 2 * E);
   t.act = t.first + E + 1;
-  t.w = reinterpret_cast<float*>(t.act + E);
+  t.l = reinterpret_cast<float*>(t.act + E);
+  t.w = t.l + P;
   t.id = reinterpret_cast<uint16_t*>(t.w + P);
   t.pos = t.id + P;
   t.tok = t.pos + P;
@@ -199,6 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->ufull[q], 1);
       mbar_init(&bars->uempty[q], 5);   // the MMA warp and four epilogue warps
     }
+    mbar_init(&bars->weights, 1);
     mbar_init(&bars->fin, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -208,57 +214,122 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&mX);
     prefetch_tmap(&mH);
   }
-  const uint32_t tcols = g.NB <= 16 ? 64 : g.NB <= 32 ? 128 : 256;  // two accumulators of 2 NB columns
+  const uint32_t tcols = g.cols <= 16 ? 32 : g.cols <= 32 ? 64 : g.cols <= 64 ? 128 : 256;  // two units' sums
   if (warp == 1) {
     tmem_alloc(&bars->tmem, tcols);
     tmem_relinquish();
   }
+  for (int e = threadIdx.x; e < 2 * m.E; e += kThreads) t.mask[e] = 0;
   grid_dep_wait();
   grid_dep_launch();
 
-  // The first claim, under way during the routing.
-  int claimed = 0;
-  if (threadIdx.x == 0) claimed = atomicAdd(g.claim, 1);
+  // The first claim, and whether a timeout recorded earlier stops this launch:
+  // under way during the routing.
+  int claimed = 0, stopped = 0;
+  if (threadIdx.x == 0) {
+    claimed = atomicAdd(g.claim, 1);
+    if (g.status) stopped = *(volatile int*)g.status;
+  }
 
   // ---------------- the routing ----------------
-  for (int e = threadIdx.x; e < 2 * m.E; e += kThreads) t.mask[e] = 0;
-  __syncthreads();
-  for (int q = warp; q < m.T; q += kThreads / 32) {
-    const float* l = m.logits + (long long)q * m.E;
-    const MoeChoice c = m.E <= 128 ? moe_choose<4>(l, m.E, m.k, m.normalize, lane)
-                                   : moe_choose<kMoeMaxExperts / 32>(l, m.E, m.k, m.normalize, lane);
-    if (lane < m.k) {
-      const int p = q * m.k + lane;
-      t.id[p] = (uint16_t)c.expert;
-      t.w[p] = c.weight;
-      atomicOr(&t.mask[2 * c.expert + (q >> 5)], 1u << (q & 31));
-      if (blockIdx.x == 0) {
-        m.experts[p] = c.expert;
-        m.weights[p] = c.weight;
+  if (m.E <= 128 && m.T * m.E * m.E <= 1 << 17) {
+    // Small: every logit's rank among its token's by comparing it with them
+    // all (one token of 128 experts: 0.3 us against 1.6 of k rounds of a warp;
+    // 64 of 64: 2 against 5), through the memory of the stages.
+    uint32_t* key = reinterpret_cast<uint32_t*>(smem);
+    const int ld = (m.E + 3) & ~3;   // (past the last expert: 0, below every key)
+    if (ld == m.E) {   // whole rows of 16 bytes
+      for (int i = threadIdx.x; i < m.T * ld / 4; i += kThreads) {
+        const float4 l = __ldcg(reinterpret_cast<const float4*>(m.logits) + i);
+        reinterpret_cast<uint4*>(key)[i] = make_uint4(moe_key(l.x), moe_key(l.y), moe_key(l.z), moe_key(l.w));
+      }
+    } else {
+#pragma unroll 4
+      for (int i = threadIdx.x; i < m.T * ld; i += kThreads) {
+        const int q = i / ld, e = i - q * ld;
+        key[i] = e < m.E ? moe_key(__ldcg(m.logits + (long long)q * m.E + e)) : 0u;
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < m.T * ld; i += kThreads) {
+      const int q = i / ld, e = i - q * ld;
+      const uint32_t mine = key[i];
+      if (mine == 0u) continue;
+      int rank = 0;
+      for (int f = 0; f < ld; f += 4) {
+        // A larger key comes first, and an equal one of a lower expert.
+        const uint4 o = *reinterpret_cast<const uint4*>(key + q * ld + f);
+        rank += (o.x + (f < e ? 1u : 0u) > mine) + (o.y + (f + 1 < e ? 1u : 0u) > mine) +
+                (o.z + (f + 2 < e ? 1u : 0u) > mine) + (o.w + (f + 3 < e ? 1u : 0u) > mine);
+      }
+      if (rank < m.k) {
+        t.id[q * m.k + rank] = (uint16_t)e;
+        t.l[q * m.k + rank] = moe_logit(mine);
+      }
+    }
+  } else {
+    // Rounds, one warp to a token; up to 128 experts the logits of a warp's four
+    // tokens are read at once.
+    for (int q0 = warp; q0 < m.T; q0 += 4 * (kThreads / 32)) {
+      if (m.E <= 128) {
+        uint32_t key[4][4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) moe_keys<4>(m.logits, m.T, m.E, q0 + b * (kThreads / 32), lane, key[b]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+          const int q = q0 + b * (kThreads / 32);
+          if (q >= m.T) break;
+          const MoeChoice c = moe_choose<4>(key[b], m.k, lane);
+          if (lane < m.k) {
+            t.id[q * m.k + lane] = (uint16_t)c.expert;
+            t.l[q * m.k + lane] = c.logit;
+          }
+        }
+      } else {
+        for (int q = q0; q < m.T && q < q0 + 4 * (kThreads / 32); q += kThreads / 32) {
+          uint32_t key[kMoeMaxExperts / 32];
+          moe_keys<kMoeMaxExperts / 32>(m.logits, m.T, m.E, q, lane, key);
+          const MoeChoice c = moe_choose<kMoeMaxExperts / 32>(key, m.k, lane);
+          if (lane < m.k) {
+            t.id[q * m.k + lane] = (uint16_t)c.expert;
+            t.l[q * m.k + lane] = c.logit;
+          }
+        }
       }
     }
   }
   __syncthreads();
+  for (int p = threadIdx.x; p < P; p += kThreads) {
+    const int q = p / m.k, e = t.id[p];
+    atomicOr(&t.mask[2 * e + (q >> 5)], 1u << (q & 31));
+  }
+  __syncthreads();
   if (warp == 0) {
-    // Exclusive sums of the counts and the list of active experts, 32 at a time.
-    int at = 0, na = 0, most = 0;
-    for (int e0 = 0; e0 < m.E; e0 += 32) {
-      const int e = e0 + lane, c = e < m.E ? __popc(t.mask[2 * e]) + __popc(t.mask[2 * e + 1]) : 0;
-      int s = c;
-      most = max(most, c);
+    // Exclusive sums of the counts and the list of active experts: a lane
+    // takes a run of experts.
+    const int per = (m.E + 31) / 32, e0 = lane * per, e1 = min(m.E, e0 + per);
+    int c = 0, on = 0, most = 0;
+    for (int e = e0; e < e1; ++e) {
+      const int n = __popc(t.mask[2 * e]) + __popc(t.mask[2 * e + 1]);
+      c += n;
+      on += n > 0;
+      most = max(most, n);
+    }
+    int s = c | on << 16;   // (at most 1024 pairs, 512 experts)
 #pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int v = __shfl_up_sync(0xffffffffu, s, d);
-        if (lane >= d) s += v;
-      }
-      if (e < m.E) t.first[e] = at + s - c;
-      at += __shfl_sync(0xffffffffu, s, 31);
-      const unsigned on = __ballot_sync(0xffffffffu, c > 0);
-      if (c > 0) t.act[na + __popc(on & ((1u << lane) - 1u))] = e;
-      na += __popc(on);
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += v;
+    }
+    int at = (s & 0xFFFF) - c, na = (s >> 16) - on;
+    for (int e = e0; e < e1; ++e) {
+      const int n = __popc(t.mask[2 * e]) + __popc(t.mask[2 * e + 1]);
+      t.first[e] = at;
+      at += n;
+      if (n > 0) t.act[na++] = e;
     }
     most = (int)__reduce_max_sync(0xffffffffu, (unsigned)most);
-    if (lane == 0) {
+    if (lane == 31) {
       t.first[m.E] = at;
       bars->active = na;
       bars->most = most;
@@ -272,17 +343,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     t.pos[p] = (uint16_t)at;
     t.tok[at] = (uint16_t)q;
   }
+  fence_proxy_async_smem();  // (the stages' memory held keys until here)
   tc_fence_before();
-  // (One decision for the CTA: a timeout recorded earlier stops it here.)
-  if (threadIdx.x == 0) bars->go = g.status == nullptr || *(volatile int*)g.status == 0;
+  if (threadIdx.x == 0) bars->go = stopped == 0;
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   const int active = bars->active;
-  // Stages: the weights, then for each half of K a token tile of up to 2 NB
-  // rows (x; or the first terms of h and then the second), NB as this call's
-  // largest expert needs it.
-  const int NB = (bars->most + 15) / 16 * 16, stage_bytes = kWeightBytes + 4 * NB * 128;
+  // Stages: the weights, then for each half of K a token tile of NB rows (x; or
+  // the first terms of h and then the second, each in whole eights), as this
+  // call's largest expert needs it: with up to eight tokens an expert, six
+  // stages fit.
+  const int NB = 2 * ((bars->most + 7) / 8 * 8), stage_bytes = kWeightBytes + 2 * NB * 128;
   const int NS = min(kMaxStages, g.ring / stage_bytes);
   const int units = bars->go ? active * (g.ta + g.tb) : 0;
   const int ka = (int)((m.H + KS - 1) / KS), kb = (int)((m.I + KS - 1) / KS);
@@ -306,10 +378,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       ru.next(kUnits);
       if (u >= units) break;
-      if (lane == 0) claimed = atomicAdd(g.claim, 1);  // the next, under way during this one
       const Unit q = unit_at(u, g, t, active);
-      const int nk = q.down ? kb : ka, quads = (q.n + 3) / 4, rows16 = (q.n + 15) / 16;
-      const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * rows16 * 2048u : 2u * quads * 512u);
+      const int nk = q.down ? kb : ka, quads = (q.n + 3) / 4, eights = (q.n + 7) / 8;
+      const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * eights * 1024u : 2u * quads * 512u);
       // Lane j gathers tokens 4 j .. 4 j + 3 of the expert (rows past its last: zeros).
       int y[4];
 #pragma unroll
@@ -340,15 +411,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* d = stage(r.slot) + kWeightBytes;
         uint64_t* bar = &bars->full[r.slot];
         if (q.down) {
-          if (lane < 4 * rows16) {
+          if (lane < 4 * eights) {
             // (the second terms' rows follow the first terms' of this unit)
             const int half = lane & 1, term = lane >> 1 & 1, b = lane >> 2;
-            tma_load_2d(d + half * 2 * NB * 128 + (term * rows16 + b) * 2048, &mH, ks * KS + half * 64,
-                        term * P + q.p0 + b * 16, bar);
+            tma_load_2d(d + half * NB * 128 + (term * eights + b) * 1024, &mH, ks * KS + half * 64,
+                        term * P + q.p0 + b * 8, bar);
           }
         } else if (lane < quads) {
           tma_gather4(d + lane * 512, &mX, ks * KS, y[0], y[1], y[2], y[3], bar);
-          tma_gather4(d + 2 * NB * 128 + lane * 512, &mX, ks * KS + 64, y[0], y[1], y[2], y[3], bar);
+          tma_gather4(d + NB * 128 + lane * 512, &mX, ks * KS + 64, y[0], y[1], y[2], y[3], bar);
         }
         __syncwarp();
       };
@@ -381,10 +452,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         ok = __shfl_sync(0xffffffffu, (int)rok, 0) != 0;
+        if (ahead == nk && lane == 0) claimed = atomicAdd(g.claim, 1);
         // (Also after a stop: stages with their weights out get their tokens, so that each completes.)
         for (int ks = 0; ks < ahead; ++ks, rs.next(NS)) tokens(ks, rs);
       }
       for (int ks = ahead; ks < nk && ok; ++ks, rs.next(NS)) {
+        // The next unit is claimed with this one's last loads: earlier, a CTA
+        // that waits for h would hold a second unit that an idle one could take.
+        if (ks == nk - 1 && lane == 0) claimed = atomicAdd(g.claim, 1);
         ok = weights(ks, rs);
         if (!ok) break;
         ++issued;
@@ -412,9 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       ru.next(kUnits);
       if (u >= units) break;
       const Unit q = unit_at(u, g, t, active);
-      const int nk = q.down ? kb : ka, cols = (q.n + 15) / 16 * 16;
-      const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, q.down ? 2 * cols : cols);
-      const uint32_t acc = tmem + (uint32_t)(rb.slot * 2 * g.NB);
+      const int nk = q.down ? kb : ka;
+      const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, q.down ? (q.n + 7) / 8 * 16 : (q.n + 15) / 16 * 16);
+      const uint32_t acc = tmem + (uint32_t)(rb.slot * g.cols);
       wok = wait_or_abort(&bars->acce[rb.slot], rb.phase ^ 1u, limit, abort_flag, g.status);
       ok = __all_sync(0xffffffffu, wok) != 0;
       for (int ks = 0; ks < nk && ok; ++ks, rs.next(NS)) {
@@ -429,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const uint64_t da = smem_desc_sw128(d + half * 2 * kBoxBytes);
-            const uint64_t db = smem_desc_sw128(d + kWeightBytes + half * 2 * NB * 128);
+            const uint64_t db = smem_desc_sw128(d + kWeightBytes + half * NB * 128);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
               tc_mma_bf16(acc, da + 2u * kk, db + 2u * kk, idesc, ks > 0 || half > 0 || kk > 0 ? 1u : 0u);
@@ -445,7 +520,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) tc_commit(&bars->fin);
     __syncwarp();
     if (lane == 0) mbar_wait(&bars->fin, 0, kDefaultSpin, nullptr);
-  } else if (warp >= kEpi0) {
+  } else if (warp == 2) {
+    // ---------------- routing weights, wanted only at the end ----------------
+    for (int q = 0; q < m.T; ++q) {
+      const float all = m.normalize ? -1.0f : moe_sum(m.logits + (long long)q * m.E, m.E, t.l[q * m.k], lane);
+      const int p = q * m.k + lane;
+      if (lane < m.k) {
+        const float w = moe_weight(t.l + q * m.k, m.k, lane, all);
+        t.w[p] = w;
+        if (blockIdx.x == 0) {
+          m.experts[p] = t.id[p];
+          m.weights[p] = w;
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->weights);
+  } else if (warp >= kEpi0 && warp < kEpi0 + 4) {
     // ---------------- outputs ----------------
     const int quarter = warp & 3, row = quarter * 32 + lane, et = threadIdx.x - kEpi0 * 32;
     Ring rb, ru;
@@ -462,42 +553,39 @@ __global__ void __launch_bounds__(kThreads, 1)
       // leave alone.
       if (!epi_all(aok) || u >= units) break;
       tc_fence_after();
-      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * 2 * g.NB);
-      for (int c0 = 0; c0 < q.n; c0 += 16) {
-        uint32_t v[16];
-        tmem_ld16(taddr + (uint32_t)c0, v);
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * g.cols);
+      for (int c0 = 0; c0 < q.n; c0 += 8) {
+        uint32_t v[8];
+        tmem_ld8(taddr + (uint32_t)c0, v);
         if (q.down) {
-          uint32_t v2[16];   // the second terms' part
-          tmem_ld16(taddr + (uint32_t)((q.n + 15) / 16 * 16 + c0), v2);
+          uint32_t v2[8];   // the second terms' part
+          tmem_ld8(taddr + (uint32_t)((q.n + 7) / 8 * 8 + c0), v2);
           tmem_wait_ld();
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __float_as_uint(__uint_as_float(v[i]) + __uint_as_float(v2[i]));
           const long long r = q.tile * 128ll + row;
           if (r < m.H) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c0 + i < q.n) g.y[(long long)(q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]);
+            for (int i = 0; i < 8; ++i)
+              if (c0 + i < q.n)
+                g.y[(long long)(q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]) + __uint_as_float(v2[i]);
           }
         } else {
+          // Gate rows are lanes 0..63 and up rows 64..127 of tensor memory: they
+          // meet in shared memory, and all threads take (feature, token) pairs.
           tmem_wait_ld();
-          if (row >= 64) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) xch[i * 64 + row - 64] = __uint_as_float(v[i]);
-          }
+          for (int i = 0; i < 8; ++i) xch[i * 128 + row] = __uint_as_float(v[i]);
           epi_sync();
-          const long long r = q.tile * 64ll + row;
-          if (row < 64 && r < m.I) {
-            El* h = static_cast<El*>(m.h) + r;
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              if (c0 + i < q.n) {
-                const float gt = __uint_as_float(v[i]), hv = __fdividef(gt, 1.0f + __expf(-gt)) * xch[i * 64 + row];
-                El* at = h + (long long)(q.p0 + c0 + i) * m.I;
-                Io<DT>::st(at, hv);
-                const float left = hv - Io<DT>::ld(at);
-                // (Beyond the stored type's range the first term is an infinity and stays one.)
-                Io<DT>::st(at + P * m.I, fabsf(left) <= 3.4e38f ? left : 0.0f);
-              }
+          const long long r = q.tile * 64ll + (et & 63);
+          if (r < m.I) {
+#pragma unroll 1
+            for (int i = et >> 6; i < 8 && c0 + i < q.n; i += 2) {
+              const float gt = xch[i * 128 + (et & 63)], hv = __fdividef(gt, 1.0f + __expf(-gt)) * xch[i * 128 + 64 + (et & 63)];
+              El* at = static_cast<El*>(m.h) + (long long)(q.p0 + c0 + i) * m.I + r;
+              Io<DT>::st(at, hv);
+              const float left = hv - Io<DT>::round(hv);
+              // (Beyond the stored type's range the first term is an infinity and stays one.)
+              Io<DT>::st(at + P * m.I, fabsf(left) <= 3.4e38f ? left : 0.0f);
+            }
           }
           epi_sync();
         }
@@ -512,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           bars->go = atomicAdd(g.tickets + q.tile, 1) == active - 1 ? 2 : 1;
         }
         epi_sync();
-        if (bars->go == 2) {
+        // (The routing weights are this CTA's own work of long ago.)
+        if (bars->go == 2 && epi_all(wait_or_abort(&bars->weights, 0, limit, abort_flag, g.status))) {
           // Every expert's part of this tile is in y: out of each token, its
           // choices in order; a warp takes every fourth token, a lane four features.
           __threadfence();
@@ -529,11 +618,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                 s.z = fmaf(w, v.z, s.z);
                 s.w = fmaf(w, v.w, s.w);
               }
-              El* o = static_cast<El*>(m.out) + tk * m.H + r;
-              Io<DT>::st(o, s.x);
-              Io<DT>::st(o + 1, s.y);
-              Io<DT>::st(o + 2, s.z);
-              Io<DT>::st(o + 3, s.w);
+              *reinterpret_cast<uint2*>(static_cast<El*>(m.out) + tk * m.H + r) =
+                  make_uint2(Io<DT>::pair(s.x, s.y), Io<DT>::pair(s.z, s.w));
             }
           }
         }
@@ -568,15 +654,15 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   const bool f16 = DT == DETFFN_F16;
   CUtensorMap mWg, mWu, mWd, mX, mH;
   const long long dg[3] = {m.H, m.I, m.E}, dd[3] = {m.I, m.H, m.E}, dx[2] = {m.H, m.T}, dh[2] = {m.I, 2ll * m.T * m.k};
-  const int bw[3] = {64, 64, 1}, bx[2] = {64, 1}, bh[2] = {64, 16};
+  const int bw[3] = {64, 64, 1}, bx[2] = {64, 1}, bh[2] = {64, 8};
   if (!tc_make_map_nd(&mWg, f16, m.Wg, 3, dg, bw) || !tc_make_map_nd(&mWu, f16, m.Wu, 3, dg, bw) ||
       !tc_make_map_nd(&mWd, f16, m.Wd, 3, dd, bw) || !tc_make_map_nd(&mX, f16, m.x, 2, dx, bx) ||
       !tc_make_map_nd(&mH, f16, m.h, 2, dh, bh))
     return cudaErrorInvalidValue;
   Args g{};
   g.m = m;
-  g.NB = (m.T + 15) / 16 * 16;
-  const int stage = kWeightBytes + 4 * g.NB * 128;  // the largest
+  g.cols = 2 * ((m.T + 7) / 8 * 8);
+  const int stage = kWeightBytes + 2 * g.cols * 128;  // the largest
   const int rest = 1024 + (int)((sizeof(Bars) + 127) & ~127) + kXch + tables_bytes(m.E, m.T * m.k);
   g.ring = (kSmemMax - rest) & ~1023;
   if (g.ring < 2 * stage) return cudaErrorInvalidConfiguration;
@@ -599,7 +685,7 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
 }  // namespace
 
 bool moe_tensor_covers(const MoeArgs& m) {
-  const void* p[] = {m.x, m.Wg, m.Wu, m.Wd, m.h};
+  const void* p[] = {m.x, m.Wg, m.Wu, m.Wd, m.h, m.out};
   for (const void* q : p)
     if ((uintptr_t)q & 15u) return false;
   return m.dtype != DETFFN_F32 && m.H % 8 == 0 && m.I % 8 == 0;
