@@ -10,13 +10,31 @@ OK, INVALID, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE = range(6)
 A = [1 << 30, 2 << 30, 3 << 30, 4 << 30, 5 << 30, 6 << 30, 7 << 30, 8 << 30, 9 << 30, 10 << 30]
 
 
+_vp, _ll, _int, _f, _sz = ctypes.c_void_p, ctypes.c_longlong, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+_ARGS = {
+    "detffn_join_forward": [_vp, _ll, _vp, _ll, _vp, _vp, _ll, _ll, _f, _vp, _f, _vp, _ll, _vp, _ll, _ll, _ll, _int,
+                            _int, _vp],
+    "detffn_join_workspace_size": [_ll, _ll, ctypes.POINTER(_sz)],
+    "detffn_join_backward": [_vp, _ll, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _ll, _ll, _f, _vp, _f, _vp, _ll, _vp,
+                             _ll, _vp, _vp, _vp, _ll, _ll, _int, _int, _vp, _sz, _vp],
+    "detffn_ckpt8_pack": [_vp] * 6 + [_ll, _ll, _int, _vp],
+    "detffn_ckpt8_unpack": [_vp] * 6 + [_ll, _ll, _int, _vp],
+    "detffn_ckpt8_silu_backward": [_vp] * 8 + [_ll, _ll, _int, _vp],
+    "detffn_moe_workspace_size": [_ll, _ll, _int, _ll, _ll, _int, ctypes.POINTER(_sz)],
+    "detffn_moe_forward": [_vp] * 9 + [_ll, _ll, _int, _int, _ll, _ll, _int, _vp, _sz, _vp,
+                                       _vp],
+}
+
+
 @pytest.fixture(scope="module")
 def call():
-    from gemm_deterministic_bf16_gb300 import block, build
+    from gemm_deterministic_bf16_gb300 import build, detffn
     build.build()
 
     def go(name, *args):
-        return block._fn(name)(*args)
+        f = getattr(detffn.lib(), name)
+        f.argtypes = _ARGS[name]
+        return f(*args)
     return go
 
 
