@@ -341,7 +341,9 @@ MoeArgs moe_plan(Arena& w, long long T, long long E, long long k, long long H, l
   a.first = w.take<int>(E + 1);
   a.h = w.take<char>(T * k * I * 4);
   sc->counters = w.take<int>(1 + E + (H + 127) / 128);
-  sc->y = w.take<float>(T * k * H);
+  int parts = 1, stages = 0;
+  moe_parts(H, I, &parts, &stages);
+  sc->y = w.take<float>(parts * T * k * H);
   return a;
 }
 

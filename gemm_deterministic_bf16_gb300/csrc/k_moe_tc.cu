@@ -6,15 +6,22 @@
 // so that nothing is handed over through memory, then takes units in turn:
 //   gate/up: 64 rows of Wg[e] over the same 64 rows of Wu[e] (the MMA's 128
 //     rows) times the expert's tokens, K = H; h for those 64 features
-//   down:    128 rows of Wd[e] times the expert's rows of h, K = I; partial
-//     outputs y of the pairs
+//   down:    128 rows of Wd[e] times the expert's rows of h, K = I or a part of
+//     it; partial outputs y of the pairs
 // All gate/up units come before all down units, experts in ascending order.
 // A down unit waits (bounded) until its expert's gate/up units are counted,
 // with its first weight tiles already on their way.  Those units were claimed
 // earlier, by CTAs that are running and wait for nothing themselves, so the
-// wait ends whatever else holds the other SMs; the CTA that finishes
-// the last expert of a 128-feature tile of the output adds the pairs of each
-// token there, in the order of its choices.
+// wait ends whatever else holds the other SMs.  At the end all CTAs add the
+// pairs of each token, in the order of its choices, as the 128-feature tiles of
+// the output are counted complete (left to the CTA that counts a tile last,
+// that alone took 18 us for 64 tokens of 64 experts).
+//
+// The down projection's K is cut where H gives few tiles (into as many parts
+// as make 16 units of an expert, of two stages or more): one CTA alone is slow
+// to stream a whole row tile, as its ring holds six stages.  Four tokens of 6
+// experts, H = 616, I = 1376: 20.2 us whole, TODO us in parts.  The cut depends
+// on H and I alone, and the parts are added in order.
 //
 // The work is the weights' bytes: each active expert's are read once, by TMA
 // boxes of 64 rows x 64 K (128-byte swizzle) into a ring of stages of 128 K,
@@ -43,9 +50,10 @@ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-constexpr int kThreads = 512;     // all work out the routing; then warp 0 loads, warp 1 issues MMAs, warp 2
-                                  // forms the routing weights, warps 4-7 the outputs
+constexpr int kThreads = 512;     // all work out the routing; then warp 0 loads, warp 1 issues MMAs, warps
+                                  // 4-7 read the sums, 8-15 form the routing weights, and 4-15 out
 constexpr int kEpi0 = 4;          // first epilogue warp (its TMEM lane quarter is warp % 4)
+constexpr int kHelpers = kThreads / 32 - kEpi0 - 4;  // warps that form the routing weights
 constexpr int KS = 128;           // K positions of a stage
 constexpr int kBoxBytes = 64 * 128;              // 64 rows x 64 K
 constexpr int kWeightBytes = 4 * kBoxBytes;      // 128 rows x 128 K
@@ -55,7 +63,7 @@ constexpr int kUnits = 4;                        // units a CTA has claimed and 
 constexpr int kXch = 128 * 8 * 4;                // gate and up values of eight tokens
 
 struct Bars {
-  uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], ufull[kUnits], uempty[kUnits], weights, fin;
+  uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], ufull[kUnits], uempty[kUnits], weights, done, fin;
   uint32_t tmem;
   int abort, go;
   int unit[kUnits];  // claimed units; past the last: no more
@@ -67,11 +75,12 @@ struct Args {
   MoeArgs m;
   int cols;          // most columns of a unit's sums: twice T rounded up to 8
   int ring;          // bytes for stages
-  int ta, tb;        // gate/up units and down units of an expert
+  int ta, tb;        // gate/up tiles and down tiles of an expert
+  int parts, kpart;  // parts of a down tile's K, stages of a part
   int* claim;        // units claimed by all CTAs
   int* ready;        // [E] gate/up units done
   int* tickets;      // [tb] down units done
-  float* y;          // [T * k][H]
+  float* y;          // [parts][T * k][H]
   int* status;
   long long spin;
   int stall;
@@ -158,16 +167,21 @@ __device__ __forceinline__ Tables tables_at(unsigned char* p, int E, int P) {
 
 struct Unit {
   bool down;
-  int a, tile, e, p0, n;   // active index, tile of the expert, expert, first pair, pairs
+  int a, tile, part, e, p0, n;   // active index, tile of the expert, part of K, expert, first pair, pairs
 };
 __device__ __forceinline__ Unit unit_at(int u, const Args& g, const Tables& t, int active) {
   Unit r;
   const int na = active * g.ta;
   r.down = u >= na;
   const int v = r.down ? u - na : u;
-  const int per = r.down ? g.tb : g.ta;
+  const int per = r.down ? g.tb * g.parts : g.ta;
   r.a = v / per;
   r.tile = v - r.a * per;
+  r.part = 0;
+  if (r.down) {
+    r.part = r.tile / g.tb;
+    r.tile -= r.part * g.tb;
+  }
   r.e = t.act[r.a];
   r.p0 = t.first[r.e];
   r.n = t.first[r.e + 1] - r.p0;
@@ -204,7 +218,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bars->ufull[q], 1);
       mbar_init(&bars->uempty[q], 5);   // the MMA warp and four epilogue warps
     }
-    mbar_init(&bars->weights, 1);
+    mbar_init(&bars->weights, kHelpers);
+    mbar_init(&bars->done, 1);
     mbar_init(&bars->fin, 1);
     bars->abort = 0;
     fence_mbar_init();
@@ -356,7 +371,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   // stages fit.
   const int NB = 2 * ((bars->most + 7) / 8 * 8), stage_bytes = kWeightBytes + 2 * NB * 128;
   const int NS = min(kMaxStages, g.ring / stage_bytes);
-  const int units = bars->go ? active * (g.ta + g.tb) : 0;
+  const int units = bars->go ? active * (g.ta + g.tb * g.parts) : 0;
   const int ka = (int)((m.H + KS - 1) / KS), kb = (int)((m.I + KS - 1) / KS);
 
   if (warp == 0) {
@@ -379,7 +394,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ru.next(kUnits);
       if (u >= units) break;
       const Unit q = unit_at(u, g, t, active);
-      const int nk = q.down ? kb : ka, quads = (q.n + 3) / 4, eights = (q.n + 7) / 8;
+      const int k0 = q.part * g.kpart, nk = q.down ? min(g.kpart, kb - k0) : ka, quads = (q.n + 3) / 4, eights = (q.n + 7) / 8;
       const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * eights * 1024u : 2u * quads * 512u);
       // Lane j gathers tokens 4 j .. 4 j + 3 of the expert (rows past its last: zeros).
       int y[4];
@@ -395,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_arrive_expect_tx(bar, bytes);
           if (q.down) {
             for (int i = 0; i < 4; ++i)  // box i: K half i / 2, rows 64 (i % 2)
-              tma_load_3d_hint(d + i * kBoxBytes, &mWd, ks * KS + (i >> 1) * 64, q.tile * 128 + (i & 1) * 64, q.e, bar, pol);
+              tma_load_3d_hint(d + i * kBoxBytes, &mWd, (k0 + ks) * KS + (i >> 1) * 64, q.tile * 128 + (i & 1) * 64, q.e, bar, pol);
           } else {
             for (int i = 0; i < 2; ++i) {
               tma_load_3d_hint(d + 2 * i * kBoxBytes, &mWg, ks * KS + i * 64, q.tile * 64, q.e, bar, pol);
@@ -414,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < 4 * eights) {
             // (the second terms' rows follow the first terms' of this unit)
             const int half = lane & 1, term = lane >> 1 & 1, b = lane >> 2;
-            tma_load_2d(d + half * NB * 128 + (term * eights + b) * 1024, &mH, ks * KS + half * 64,
+            tma_load_2d(d + half * NB * 128 + (term * eights + b) * 1024, &mH, (k0 + ks) * KS + half * 64,
                         term * P + q.p0 + b * 8, bar);
           }
         } else if (lane < quads) {
@@ -487,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ru.next(kUnits);
       if (u >= units) break;
       const Unit q = unit_at(u, g, t, active);
-      const int nk = q.down ? kb : ka;
+      const int nk = q.down ? min(g.kpart, kb - q.part * g.kpart) : ka;
       const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, q.down ? (q.n + 7) / 8 * 16 : (q.n + 15) / 16 * 16);
       const uint32_t acc = tmem + (uint32_t)(rb.slot * g.cols);
       wok = wait_or_abort(&bars->acce[rb.slot], rb.phase ^ 1u, limit, abort_flag, g.status);
@@ -520,9 +535,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (elect_one()) tc_commit(&bars->fin);
     __syncwarp();
     if (lane == 0) mbar_wait(&bars->fin, 0, kDefaultSpin, nullptr);
-  } else if (warp == 2) {
+  } else if (warp >= kEpi0 + 4) {
     // ---------------- routing weights, wanted only at the end ----------------
-    for (int q = 0; q < m.T; ++q) {
+    for (int q = warp - kEpi0 - 4; q < m.T; q += kHelpers) {
       const float all = m.normalize ? -1.0f : moe_sum(m.logits + (long long)q * m.E, m.E, t.l[q * m.k], lane);
       const int p = q * m.k + lane;
       if (lane < m.k) {
@@ -566,7 +581,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (c0 + i < q.n)
-                g.y[(long long)(q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]) + __uint_as_float(v2[i]);
+                g.y[((long long)q.part * P + q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]) + __uint_as_float(v2[i]);
           }
         } else {
           // Gate rows are lanes 0..63 and up rows 64..127 of tensor memory: they
@@ -594,36 +609,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->acce[rb.slot]);
       if (q.down) {
+        // This unit's part of y is written: count it.
         epi_sync();
-        if (et == 0) {
-          __threadfence();
-          bars->go = atomicAdd(g.tickets + q.tile, 1) == active - 1 ? 2 : 1;
-        }
-        epi_sync();
-        // (The routing weights are this CTA's own work of long ago.)
-        if (bars->go == 2 && epi_all(wait_or_abort(&bars->weights, 0, limit, abort_flag, g.status))) {
-          // Every expert's part of this tile is in y: out of each token, its
-          // choices in order; a warp takes every fourth token, a lane four features.
-          __threadfence();
-          const long long r = q.tile * 128ll + 4 * lane;
-          if (r < m.H) {
-            for (int tk = quarter; tk < m.T; tk += 4) {
-              float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-              for (int j = 0; j < m.k; ++j) {
-                const int p = tk * m.k + j;
-                const float w = t.w[p];
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(g.y + (long long)t.pos[p] * m.H + r));
-                s.x = fmaf(w, v.x, s.x);
-                s.y = fmaf(w, v.y, s.y);
-                s.z = fmaf(w, v.z, s.z);
-                s.w = fmaf(w, v.w, s.w);
-              }
-              *reinterpret_cast<uint2*>(static_cast<El*>(m.out) + tk * m.H + r) =
-                  make_uint2(Io<DT>::pair(s.x, s.y), Io<DT>::pair(s.z, s.w));
-            }
-          }
-        }
-        epi_sync();
+        if (et == 0) asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(g.tickets + q.tile) : "memory");
       } else {
         // h of this tile is written: count it.
         fence_proxy_async_global();
@@ -632,6 +620,74 @@ __global__ void __launch_bounds__(kThreads, 1)
           asm volatile("red.release.gpu.global.add.s32 [%0], 1;" ::"l"(g.ready + q.e) : "memory");
         }
       }
+    }
+    epi_sync();
+    if (et == 0) mbar_arrive(&bars->done);
+  }
+
+  // ---------------- the pairs of each token added ----------------
+  // A warp takes 128 features of one token, a lane four of them: the parts of
+  // a choice in order, then its weight times their sum.  The reads of sixteen
+  // parts go through shared memory (the stages are done with), so that they are
+  // all under way in a loop of few instructions: unrolled for registers the
+  // same code, run once and cold, took 3 us more.
+  if (warp >= kEpi0 && units > 0) {
+    bool ok = wait_or_abort(&bars->done, 0, limit, abort_flag, g.status) &&
+              wait_or_abort(&bars->weights, 0, limit, abort_flag, g.status);
+    ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+    constexpr int kWarps = kThreads / 32 - kEpi0;
+    const int terms = m.k * g.parts;
+    float4* mine = reinterpret_cast<float4*>(smem + (warp - kEpi0) * 16 * 512) + lane;
+    for (int c = (warp - kEpi0) * gridDim.x + blockIdx.x; ok && c < g.tb * m.T; c += gridDim.x * kWarps) {
+      const int tk = c / g.tb, tile = c - tk * g.tb;
+      // Every expert's parts of this tile have to be in y.
+      if (lane == 0) {
+        long long i = 0;
+        while (ld_acquire(g.tickets + tile) < active * g.parts && i < limit) {
+          if ((++i & 255) == 0 && *abort_flag) i = limit;
+          __nanosleep(32);
+        }
+        if (i >= limit) {
+          *abort_flag = 1;
+          if (g.status) atomicExch(g.status, (int)DETFFN_ERR_TIMEOUT);
+          ok = false;
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+      __syncwarp();   // (lane 0's acquire comes before the reads of all)
+      const long long r = tile * 128ll + 4 * lane;
+      if (!ok || r >= m.H) continue;
+      const float* y = g.y + r;
+      float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), one = s;
+      int j = tk * m.k, part = 0;      // of the next read
+      int ja = j, parta = 0;           // of the next addition
+      for (int i0 = 0; i0 < terms; i0 += 16) {
+        const int n = min(16, terms - i0);
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(mine + i * 32)),
+                       "l"(y + ((long long)part * P + t.pos[j]) * m.H)
+                       : "memory");
+          if (++part == g.parts) {
+            part = 0;
+            ++j;
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+          const float4 v = mine[i * 32];
+          one = parta == 0 ? v : make_float4(one.x + v.x, one.y + v.y, one.z + v.z, one.w + v.w);
+          if (++parta == g.parts) {
+            const float w = t.w[ja];
+            s = make_float4(fmaf(w, one.x, s.x), fmaf(w, one.y, s.y), fmaf(w, one.z, s.z), fmaf(w, one.w, s.w));
+            parta = 0;
+            ++ja;
+          }
+        }
+      }
+      *reinterpret_cast<uint2*>(static_cast<El*>(m.out) + tk * m.H + r) =
+          make_uint2(Io<DT>::pair(s.x, s.y), Io<DT>::pair(s.z, s.w));
     }
   }
 
@@ -668,6 +724,7 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   if (g.ring < 2 * stage) return cudaErrorInvalidConfiguration;
   g.ta = (int)((m.I + 63) / 64);
   g.tb = (int)((m.H + 127) / 128);
+  moe_parts(m.H, m.I, &g.parts, &g.kpart);
   g.claim = sc.counters;
   g.ready = sc.counters + 1;
   g.tickets = g.ready + m.E;
@@ -677,12 +734,21 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   g.stall = wt.stall;
   cudaError_t e = launch_moe_logits(m, sc.counters, 1 + m.E + g.tb, st);
   if (e != cudaSuccess) return e;
-  const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * (g.ta + g.tb);
+  const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * (g.ta + g.tb * g.parts);
   const int grid = (int)(most < sm_count ? most : sm_count);
   return launch_dependent(k_moe<DT>, dim3(grid), kThreads, kSmemMax, st, mWg, mWu, mWd, mX, mH, g);
 }
 
 }  // namespace
+
+void moe_parts(long long H, long long I, int* parts, int* stages) {
+  const int tiles = (int)((H + 127) / 128), kb = (int)((I + KS - 1) / KS);
+  const int want = tiles < 16 ? 16 / tiles : 1;
+  int per = (kb + want - 1) / want;
+  if (per < 2) per = 2;
+  *stages = per;
+  *parts = (kb + per - 1) / per;
+}
 
 bool moe_tensor_covers(const MoeArgs& m) {
   const void* p[] = {m.x, m.Wg, m.Wu, m.Wd, m.h, m.out};

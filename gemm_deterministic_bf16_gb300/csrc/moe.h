@@ -28,7 +28,7 @@ struct MoeArgs {
 };
 
 // Workspace of the tensor kernel alone: counters [1 + E + ceil(H / 128)] and the
-// pairs' outputs y [T * k][H] in FP32.
+// pairs' outputs y [parts][T * k][H] in FP32.
 struct MoeScratch {
   int* counters = nullptr;
   float* y = nullptr;
@@ -36,6 +36,9 @@ struct MoeScratch {
 
 // Router logits; block 0 clears n counters.
 cudaError_t launch_moe_logits(const MoeArgs& a, int* counters, int n, cudaStream_t st);
+
+// The parts a down projection's K is summed in, and the 128-wide stages of a part.
+void moe_parts(long long H, long long I, int* parts, int* stages);
 
 // Tensor-core kernels (BF16 and FP16, widths multiples of 8, 16-byte-aligned
 // tensors).
