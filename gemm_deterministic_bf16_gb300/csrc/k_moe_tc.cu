@@ -5,7 +5,9 @@
 // CTA works the routing out for itself from the logits (one warp per token),
 // so that nothing is handed over through memory, then takes units in turn:
 //   gate/up: 64 rows of Wg[e] over the same 64 rows of Wu[e] (the MMA's 128
-//     rows) times the expert's tokens, K = H; h for those 64 features
+//     rows) times the expert's tokens, K = H; h for those 64 features.  Where
+//     that makes few units, 32 rows of each and twice the K to a stage: the
+//     MMA's other rows then read what follows and are not used
 //   down:    128 rows of Wd[e] times the expert's rows of h, K = I or a part of
 //     it; partial outputs y of the pairs
 // All gate/up units come before all down units, experts in ascending order.
@@ -20,11 +22,11 @@
 // The down projection's K is cut where H gives few tiles (into as many parts
 // as make 16 units of an expert, of two stages or more): one CTA alone is slow
 // to stream a whole row tile, as its ring holds six stages.  Four tokens of 6
-// experts, H = 616, I = 1376: 20.2 us whole, TODO us in parts.  The cut depends
+// experts, H = 616, I = 1376: 20.2 us whole, 16.1 in parts.  The cut depends
 // on H and I alone, and the parts are added in order.
 //
 // The work is the weights' bytes: each active expert's are read once, by TMA
-// boxes of 64 rows x 64 K (128-byte swizzle) into a ring of stages of 128 K,
+// boxes of 64 K (128-byte swizzle) into a ring of stages of 32 KB of weights,
 // and the tokens' rows by row gathers (x) or row boxes (h: the pairs of an
 // expert are neighbours).  h goes to the down projection as two terms, its
 // rounding to the stored type and the rounding of what that left (16 bits of
@@ -54,7 +56,7 @@ constexpr int kThreads = 512;     // all work out the routing; then warp 0 loads
                                   // 4-7 read the sums, 8-15 form the routing weights, and 4-15 out
 constexpr int kEpi0 = 4;          // first epilogue warp (its TMEM lane quarter is warp % 4)
 constexpr int kHelpers = kThreads / 32 - kEpi0 - 4;  // warps that form the routing weights
-constexpr int KS = 128;           // K positions of a stage
+constexpr int KS = 128;           // K positions of a down unit's stage
 constexpr int kBoxBytes = 64 * 128;              // 64 rows x 64 K
 constexpr int kWeightBytes = 4 * kBoxBytes;      // 128 rows x 128 K
 constexpr int kMaxStages = 8;
@@ -75,7 +77,7 @@ struct Args {
   MoeArgs m;
   int cols;          // most columns of a unit's sums: twice T rounded up to 8
   int ring;          // bytes for stages
-  int ta, tb;        // gate/up tiles and down tiles of an expert
+  int tb;            // down tiles of an expert
   int parts, kpart;  // parts of a down tile's K, stages of a part
   int* claim;        // units claimed by all CTAs
   int* ready;        // [E] gate/up units done
@@ -169,12 +171,12 @@ struct Unit {
   bool down;
   int a, tile, part, e, p0, n;   // active index, tile of the expert, part of K, expert, first pair, pairs
 };
-__device__ __forceinline__ Unit unit_at(int u, const Args& g, const Tables& t, int active) {
+__device__ __forceinline__ Unit unit_at(int u, const Args& g, const Tables& t, int active, int ta) {
   Unit r;
-  const int na = active * g.ta;
+  const int na = active * ta;
   r.down = u >= na;
   const int v = r.down ? u - na : u;
-  const int per = r.down ? g.tb * g.parts : g.ta;
+  const int per = r.down ? g.tb * g.parts : ta;
   r.a = v / per;
   r.tile = v - r.a * per;
   r.part = 0;
@@ -191,6 +193,7 @@ __device__ __forceinline__ Unit unit_at(int u, const Args& g, const Tables& t, i
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
     k_moe(const __grid_constant__ CUtensorMap mWg, const __grid_constant__ CUtensorMap mWu,
+          const __grid_constant__ CUtensorMap mWg32, const __grid_constant__ CUtensorMap mWu32,
           const __grid_constant__ CUtensorMap mWd, const __grid_constant__ CUtensorMap mX,
           const __grid_constant__ CUtensorMap mH, const __grid_constant__ Args g) {
   using El = typename Io<DT>::E;
@@ -365,14 +368,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = bars->tmem;
   const int active = bars->active;
-  // Stages: the weights, then for each half of K a token tile of NB rows (x; or
-  // the first terms of h and then the second, each in whole eights), as this
-  // call's largest expert needs it: with up to eight tokens an expert, six
-  // stages fit.
-  const int NB = 2 * ((bars->most + 7) / 8 * 8), stage_bytes = kWeightBytes + 2 * NB * 128;
+  // Rows of Wg and of Wu in a gate/up unit, and the units of an expert.  An MMA
+  // costs about 75 cycles whatever its columns, so half-filled ones halve what
+  // a CTA can take in, and pay only where half the CTAs would have no unit (one
+  // token of 2 experts, H = 4096, I = 1024: 27.7 us with 64 rows, 25.3 with 32;
+  // 55 of 11, 154 units of 64 rows: 68 us, and 81 with 32).
+  const bool few = 2 * active * (int)((m.I + 63) / 64) <= (int)gridDim.x;
+  const int R = few ? 32 : 64, ta = (int)((m.I + R - 1) / R);
+  // A stage: 32 KB of weights as slices of 64 K, then a token tile for each
+  // slice: of x (rows in whole sixteens), or the first terms of h and then the
+  // second (each in whole eights); as this call's largest expert needs them.
+  // With up to eight tokens an expert, six stages fit.
+  const int SL = 128 / R;   // slices of a gate/up stage; a down unit's has two
+  const int xtile = (bars->most + 15) / 16 * 2048, htile = (bars->most + 7) / 8 * 2048;
+  const int stage_bytes = kWeightBytes + max(SL * xtile, 2 * htile);
   const int NS = min(kMaxStages, g.ring / stage_bytes);
-  const int units = bars->go ? active * (g.ta + g.tb * g.parts) : 0;
-  const int ka = (int)((m.H + KS - 1) / KS), kb = (int)((m.I + KS - 1) / KS);
+  const int units = bars->go ? active * (ta + g.tb * g.parts) : 0;
+  const int ka = (int)((m.H + 64 * SL - 1) / (64 * SL)), kb = (int)((m.I + KS - 1) / KS);
 
   if (warp == 0) {
     // ---------------- loads ----------------
@@ -393,9 +405,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       ru.next(kUnits);
       if (u >= units) break;
-      const Unit q = unit_at(u, g, t, active);
+      const Unit q = unit_at(u, g, t, active, ta);
       const int k0 = q.part * g.kpart, nk = q.down ? min(g.kpart, kb - k0) : ka, quads = (q.n + 3) / 4, eights = (q.n + 7) / 8;
-      const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * eights * 1024u : 2u * quads * 512u);
+      const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * eights * 1024u : (uint32_t)SL * quads * 512u);
       // Lane j gathers tokens 4 j .. 4 j + 3 of the expert (rows past its last: zeros).
       int y[4];
 #pragma unroll
@@ -404,19 +416,25 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool wok = wait_or_abort(&bars->empty[r.slot], r.phase ^ 1u, limit, abort_flag, g.status);
         if (!__all_sync(0xffffffffu, wok)) return false;
         if (g.stall) return true;
+        unsigned char* d = stage(r.slot);
+        uint64_t* bar = &bars->full[r.slot];
         if (lane == 0) {
-          unsigned char* d = stage(r.slot);
-          uint64_t* bar = &bars->full[r.slot];
           mbar_arrive_expect_tx(bar, bytes);
           if (q.down) {
             for (int i = 0; i < 4; ++i)  // box i: K half i / 2, rows 64 (i % 2)
               tma_load_3d_hint(d + i * kBoxBytes, &mWd, (k0 + ks) * KS + (i >> 1) * 64, q.tile * 128 + (i & 1) * 64, q.e, bar, pol);
-          } else {
+          } else if (R == 64) {
             for (int i = 0; i < 2; ++i) {
               tma_load_3d_hint(d + 2 * i * kBoxBytes, &mWg, ks * KS + i * 64, q.tile * 64, q.e, bar, pol);
               tma_load_3d_hint(d + (2 * i + 1) * kBoxBytes, &mWu, ks * KS + i * 64, q.tile * 64, q.e, bar, pol);
             }
           }
+        }
+        __syncwarp();
+        if (!q.down && R < 64 && lane < 8) {
+          // Boxes of 32 rows, one a lane: slice, weight.
+          const int sl = lane >> 1, up = lane & 1;
+          tma_load_3d_hint(d + sl * R * 256 + up * R * 128, up ? &mWu32 : &mWg32, (ks * SL + sl) * 64, q.tile * R, q.e, bar, pol);
         }
         __syncwarp();
         return true;
@@ -429,12 +447,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane < 4 * eights) {
             // (the second terms' rows follow the first terms' of this unit)
             const int half = lane & 1, term = lane >> 1 & 1, b = lane >> 2;
-            tma_load_2d(d + half * NB * 128 + (term * eights + b) * 1024, &mH, (k0 + ks) * KS + half * 64,
+            tma_load_2d(d + half * htile + (term * eights + b) * 1024, &mH, (k0 + ks) * KS + half * 64,
                         term * P + q.p0 + b * 8, bar);
           }
         } else if (lane < quads) {
-          tma_gather4(d + lane * 512, &mX, ks * KS, y[0], y[1], y[2], y[3], bar);
-          tma_gather4(d + NB * 128 + lane * 512, &mX, ks * KS + 64, y[0], y[1], y[2], y[3], bar);
+          for (int sl = 0; sl < SL; ++sl)
+            tma_gather4(d + sl * xtile + lane * 512, &mX, (ks * SL + sl) * 64, y[0], y[1], y[2], y[3], bar);
         }
         __syncwarp();
       };
@@ -451,7 +469,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && lane == 0) {
           long long i = 0;
           for (; i < limit; ++i) {
-            if (ld_acquire(g.ready + q.e) >= g.ta) break;
+            if (ld_acquire(g.ready + q.e) >= ta) break;
             if ((i & 255) == 255 && *abort_flag) {
               i = limit;
               break;
@@ -501,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(&bars->uempty[ru.slot]);
       ru.next(kUnits);
       if (u >= units) break;
-      const Unit q = unit_at(u, g, t, active);
+      const Unit q = unit_at(u, g, t, active, ta);
       const int nk = q.down ? min(g.kpart, kb - q.part * g.kpart) : ka;
       const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, q.down ? (q.n + 7) / 8 * 16 : (q.n + 15) / 16 * 16);
       const uint32_t acc = tmem + (uint32_t)(rb.slot * g.cols);
@@ -516,13 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         unsigned char* d = smem + (size_t)rs.slot * stage_bytes;
         if (elect_one()) {
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const uint64_t da = smem_desc_sw128(d + half * 2 * kBoxBytes);
-            const uint64_t db = smem_desc_sw128(d + kWeightBytes + half * NB * 128);
+          const int slices = q.down ? 2 : SL, wstep = q.down ? 128 * 128 : R * 256, tstep = q.down ? htile : xtile;
+          for (int sl = 0; sl < slices; ++sl) {
+            const uint64_t da = smem_desc_sw128(d + sl * wstep);
+            const uint64_t db = smem_desc_sw128(d + kWeightBytes + sl * tstep);
 #pragma unroll
             for (int kk = 0; kk < 4; ++kk)
-              tc_mma_bf16(acc, da + 2u * kk, db + 2u * kk, idesc, ks > 0 || half > 0 || kk > 0 ? 1u : 0u);
+              tc_mma_bf16(acc, da + 2u * kk, db + 2u * kk, idesc, ks > 0 || sl > 0 || kk > 0 ? 1u : 0u);
           }
           tc_commit(&bars->empty[rs.slot]);
           if (ks == nk - 1) tc_commit(&bars->accf[rb.slot]);
@@ -562,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars->uempty[ru.slot]);
       ru.next(kUnits);
-      const Unit q = unit_at(aok && u < units ? u : 0, g, t, active);
+      const Unit q = unit_at(aok && u < units ? u : 0, g, t, active, ta);
       if (aok && u < units) aok = wait_or_abort(&bars->accf[rb.slot], rb.phase, limit, abort_flag, g.status);
       // One decision for the four warps: with a barrier each below, none may
       // leave alone.
@@ -584,17 +602,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                 g.y[((long long)q.part * P + q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]) + __uint_as_float(v2[i]);
           }
         } else {
-          // Gate rows are lanes 0..63 and up rows 64..127 of tensor memory: they
-          // meet in shared memory, and all threads take (feature, token) pairs.
+          // Gate rows are lanes 0 .. R - 1 of tensor memory and up rows R .. 2 R -
+          // 1: they meet in shared memory, and all threads take (feature, token)
+          // pairs.
           tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < 8; ++i) xch[i * 128 + row] = __uint_as_float(v[i]);
           epi_sync();
-          const long long r = q.tile * 64ll + (et & 63);
+          const int f = et & (R - 1);
+          const long long r = q.tile * (long long)R + f;
           if (r < m.I) {
 #pragma unroll 1
-            for (int i = et >> 6; i < 8 && c0 + i < q.n; i += 2) {
-              const float gt = xch[i * 128 + (et & 63)], hv = __fdividef(gt, 1.0f + __expf(-gt)) * xch[i * 128 + 64 + (et & 63)];
+            for (int i = et / R; i < 8 && c0 + i < q.n; i += 128 / R) {
+              const float gt = xch[i * 128 + f], hv = __fdividef(gt, 1.0f + __expf(-gt)) * xch[i * 128 + R + f];
               El* at = static_cast<El*>(m.h) + (long long)(q.p0 + c0 + i) * m.I + r;
               Io<DT>::st(at, hv);
               const float left = hv - Io<DT>::round(hv);
@@ -708,21 +728,21 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   });
   if (setup != cudaSuccess) return setup;
   const bool f16 = DT == DETFFN_F16;
-  CUtensorMap mWg, mWu, mWd, mX, mH;
+  CUtensorMap mWg, mWu, mWg32, mWu32, mWd, mX, mH;
   const long long dg[3] = {m.H, m.I, m.E}, dd[3] = {m.I, m.H, m.E}, dx[2] = {m.H, m.T}, dh[2] = {m.I, 2ll * m.T * m.k};
-  const int bw[3] = {64, 64, 1}, bx[2] = {64, 1}, bh[2] = {64, 8};
+  const int bw[3] = {64, 64, 1}, bw32[3] = {64, 32, 1}, bx[2] = {64, 1}, bh[2] = {64, 8};
   if (!tc_make_map_nd(&mWg, f16, m.Wg, 3, dg, bw) || !tc_make_map_nd(&mWu, f16, m.Wu, 3, dg, bw) ||
+      !tc_make_map_nd(&mWg32, f16, m.Wg, 3, dg, bw32) || !tc_make_map_nd(&mWu32, f16, m.Wu, 3, dg, bw32) ||
       !tc_make_map_nd(&mWd, f16, m.Wd, 3, dd, bw) || !tc_make_map_nd(&mX, f16, m.x, 2, dx, bx) ||
       !tc_make_map_nd(&mH, f16, m.h, 2, dh, bh))
     return cudaErrorInvalidValue;
   Args g{};
   g.m = m;
   g.cols = 2 * ((m.T + 7) / 8 * 8);
-  const int stage = kWeightBytes + 2 * g.cols * 128;  // the largest
+  const int stage = kWeightBytes + 4 * ((m.T + 15) / 16 * 2048);  // the largest
   const int rest = 1024 + (int)((sizeof(Bars) + 127) & ~127) + kXch + tables_bytes(m.E, m.T * m.k);
   g.ring = (kSmemMax - rest) & ~1023;
   if (g.ring < 2 * stage) return cudaErrorInvalidConfiguration;
-  g.ta = (int)((m.I + 63) / 64);
   g.tb = (int)((m.H + 127) / 128);
   moe_parts(m.H, m.I, &g.parts, &g.kpart);
   g.claim = sc.counters;
@@ -734,9 +754,9 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   g.stall = wt.stall;
   cudaError_t e = launch_moe_logits(m, sc.counters, 1 + m.E + g.tb, st);
   if (e != cudaSuccess) return e;
-  const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * (g.ta + g.tb * g.parts);
+  const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * ((m.I + 31) / 32 + g.tb * g.parts);
   const int grid = (int)(most < sm_count ? most : sm_count);
-  return launch_dependent(k_moe<DT>, dim3(grid), kThreads, kSmemMax, st, mWg, mWu, mWd, mX, mH, g);
+  return launch_dependent(k_moe<DT>, dim3(grid), kThreads, kSmemMax, st, mWg, mWu, mWg32, mWu32, mWd, mX, mH, g);
 }
 
 }  // namespace
