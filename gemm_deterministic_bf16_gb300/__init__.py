@@ -19,6 +19,6 @@ from .detffn import (  # noqa: F401
     detffn_workspace_size, workspace,
 )
 from .block import (  # noqa: F401
-    Ckpt8, JoinGrads, detffn_ckpt8_pack, detffn_ckpt8_silu_backward, detffn_ckpt8_unpack, detffn_join_backward,
+    Ckpt8, JoinGrads, detffn_backward_ckpt8, detffn_ckpt8_pack, detffn_ckpt8_silu_backward, detffn_ckpt8_unpack, detffn_join_backward,
     detffn_join_forward, detffn_join_workspace_size, detffn_moe_forward, detffn_moe_workspace_size,
 )

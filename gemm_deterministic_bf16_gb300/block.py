@@ -127,6 +127,31 @@ def detffn_ckpt8_silu_backward(dh, ckpt, dU=None, dG=None, h=None, stream=None):
     return _on(stream, f, *ckpt, dh, dU, dG, h)
 
 
+def detffn_backward_ckpt8(x, Wg, Wu, Wd, ckpt, dOut, dX=None, dWg=None, dWu=None, dWd=None, ws=None, shards=1,
+                          path=PATH_AUTO, stream=None, spin_limit=0, flags=0):
+    """detffn_backward with gate and up from an 8-bit checkpoint; returns (dX, dWg, dWu, dWd)."""
+    if stream is not None:
+        return _on(stream, detffn_backward_ckpt8, x, Wg, Wu, Wd, ckpt, dOut, dX, dWg, dWu, dWd, ws, shards, path, None,
+                   spin_limit, flags)
+    _d._bf16(x, Wg, Wu, Wd, dOut, dX, dWg, dWu, dWd)
+    M, H = x.shape
+    I = Wg.shape[0]
+    for t, dt, n in zip(ckpt, (torch.int8, torch.float32) * 2, (I, (I + 63) // 64) * 2):
+        if t.dtype != dt or t.shape != (M, n) or not t.is_contiguous() or t.device != x.device:
+            raise ValueError("checkpoint: expected contiguous CUDA codes [M, I] (int8) and scales [M, ceil(I / 64)] (float32)")
+    e = lambda t, *s: torch.empty(s, dtype=torch.bfloat16, device=x.device) if t is None else t  # noqa: E731
+    dX, dWg, dWu, dWd = e(dX, M, H), e(dWg, I, H), e(dWu, I, H), e(dWd, H, I)
+    if ws is None:
+        ws = _d.workspace(_d.OP_BACKWARD, M, H, I, shards, path, x.device)
+    f = _d.lib().detffn_backward_ckpt8
+    f.argtypes = [_d._vp] * 14 + [_d._ll] * 3 + [_d._vp, ctypes.c_size_t, _d._vp, ctypes.POINTER(_d.Options)]
+    p = [t.data_ptr() for t in (x, Wg, Wu, Wd, *ckpt, dOut, dX, dWg, dWu, dWd)]
+    _d._check(f(_d.handle(x.device), *p, M, H, I, ws.data_ptr(), ws.numel(),
+                torch.cuda.current_stream(x.device).cuda_stream, _d._opts(path, shards, spin_limit, flags)),
+              "detffn_backward_ckpt8")
+    return dX, dWg, dWu, dWd
+
+
 def detffn_moe_workspace_size(T, E, top_k, H, I, dtype=torch.bfloat16):
     """Bytes of scratch detffn_moe_forward needs."""
     f = _d.lib().detffn_moe_workspace_size

@@ -12,6 +12,7 @@
 #include <mutex>
 #include <vector>
 
+#include "block.h"
 #include "common.cuh"
 #include "decode.h"
 #include "handle.h"
@@ -906,15 +907,33 @@ namespace {
 
 // Row-wise backward stages for rows [r0, r0+rows): dh, then dU and dG (and h
 // again, for the down projection's weight gradient, in the same pass).
+// Gate and up as the training forward saved them: in BF16, or in 8 bits
+// (ckpt.gq not null).
+struct Saved {
+  const uint16_t* gate = nullptr;
+  const uint16_t* up = nullptr;
+  CkptArgs ckpt;
+};
+
 detffn_status rowwise_bwd(detffn_handle h, Family f, const uint16_t* dOut, const uint16_t* Wd,
-                          const uint16_t* gate, const uint16_t* up,
+                          const Saved& saved,
                           uint16_t* dh, uint16_t* dU, uint16_t* dG, uint16_t* hh, long long rows, long long H,
                           long long I, cudaStream_t st, const TcsScratch& sc) {
   // dh[m, i] = T_{n<H}(dOut[m, n], Wd[n, i]): B row i is column i of Wd (K stride I),
   // (read MN-major by the tensor family).
   const Strided B{Wd, 1, I};
   TRY(tree_gemm(h, f, Strided{dOut, H, 1}, B, rows, I, H, dh, I, st, sc));
-  return silu_bwd(h, dh, gate, up, dU, dG, hh, rows * I, st);
+  if (!saved.ckpt.gq) return silu_bwd(h, dh, saved.gate, saved.up, dU, dG, hh, rows * I, st);
+  CkptArgs c = saved.ckpt;
+  c.M = rows;
+  c.I = I;
+  c.dtype = DETFFN_BF16;
+  c.dh = dh;
+  c.dU = dU;
+  c.dG = dG;
+  c.h = hh;
+  return timed(h, st, "ckpt8_silu_bwd", (8.0 + 2.0 + 8.0 / kCkptBlock) * rows * I, 0.0,
+               [&] { return cu(launch_ckpt8_silu_bwd(c, h->sm_count, st)); });
 }
 
 // Weight gradients over K = M tokens from row-major [M, .] stage tensors (the
@@ -933,14 +952,15 @@ detffn_status wgrads(detffn_handle h, Family f, const uint16_t* x, const uint16_
 
 }  // namespace
 
-extern "C" detffn_status detffn_backward(detffn_handle h, const void* x, const void* Wg,
-                                         const void* Wu, const void* Wd, const void* gate,
-                                         const void* up, const void* dOut, void* dX, void* dWg,
-                                         void* dWu, void* dWd, void* dh_save, void* dU_save,
-                                         void* dG_save, long long M, long long H, long long I,
-                                         void* ws, size_t ws_bytes, void* stream,
-                                         const detffn_options* opts) {
-  if (!h || !gate || !up || !dOut || !dX || !dWg || !dWu || !dWd) return DETFFN_ERR_INVALID_ARG;
+namespace {
+
+detffn_status backward(detffn_handle h, const void* x, const void* Wg, const void* Wu, const void* Wd,
+                       const Saved& saved, const void* dOut, void* dX, void* dWg, void* dWu, void* dWd, void* dh_save,
+                       void* dU_save, void* dG_save, long long M, long long H, long long I, void* ws, size_t ws_bytes,
+                       void* stream, const detffn_options* opts) {
+  const bool q8 = saved.ckpt.gq != nullptr;
+  const void *gate = saved.gate, *up = saved.up;
+  if (!h || (!q8 && (!gate || !up)) || !dOut || !dX || !dWg || !dWu || !dWd) return DETFFN_ERR_INVALID_ARG;
   Opts o;
   TRY(read_opts(opts, &o));
   set_waits(h, o);
@@ -952,12 +972,14 @@ extern "C" detffn_status detffn_backward(detffn_handle h, const void* x, const v
   const int k = o.shards;
   if (k > 1 && (I % k != 0 || (I / k) % kLeaf != 0 || (I / k) / kLeaf < 2)) return DETFFN_ERR_SHAPE;
   const long long bx = 2 * M * H, bw = 2 * I * H, bmi = 2 * M * I;
-  const void* ins[7] = {x, Wg, Wu, Wd, gate, up, dOut};
-  const long long nin[7] = {bx, bw, bw, bw, bmi, bmi, bx};
+  const CkptArgs& c8 = saved.ckpt;
+  const long long bq = M * I, bs = 4 * M * ((I + kCkptBlock - 1) / kCkptBlock);
+  const void* ins[11] = {x, Wg, Wu, Wd, gate, up, dOut, c8.gq, c8.uq, c8.gs, c8.us};
+  const long long nin[11] = {bx, bw, bw, bw, bmi, bmi, bx, bq, bq, bs, bs};
   void* outs[7] = {dX, dWg, dWu, dWd, dh_save, dU_save, dG_save};
   const long long nout[7] = {bx, bw, bw, bw, bmi, bmi, bmi};
   for (int a = 0; a < 7; ++a) {
-    for (int b = 0; b < 7; ++b)
+    for (int b = 0; b < 11; ++b)
       if (overlap(outs[a], nout[a], ins[b], nin[b])) return DETFFN_ERR_INVALID_ARG;
     for (int b = a + 1; b < 7; ++b)
       if (overlap(outs[a], nout[a], outs[b], nout[b])) return DETFFN_ERR_INVALID_ARG;
@@ -989,11 +1011,9 @@ extern "C" detffn_status detffn_backward(detffn_handle h, const void* x, const v
   uint16_t* dh = dh_save ? (uint16_t*)dh_save : w.dh;
   uint16_t* dU = dU_save ? (uint16_t*)dU_save : w.dU;
   uint16_t* dG = dG_save ? (uint16_t*)dG_save : w.dG;
-  const uint16_t* G = (const uint16_t*)gate;
-  const uint16_t* U = (const uint16_t*)up;
   const uint16_t* WG = (const uint16_t*)Wg;
   const uint16_t* WU = (const uint16_t*)Wu;
-  TRY(rowwise_bwd(h, f, (const uint16_t*)dOut, (const uint16_t*)Wd, G, U, dh, dU, dG, w.h, M, H, I, st,
+  TRY(rowwise_bwd(h, f, (const uint16_t*)dOut, (const uint16_t*)Wd, saved, dh, dU, dG, w.h, M, H, I, st,
                   w.tcs));
   // dHidden: cg = T_i(dG[m, i], Wg[i, n]), cu = T_i(dU[m, i], Wu[i, n]); the two
   // trees stay separate until the final gate-then-up addition.  B row n is
@@ -1050,6 +1070,38 @@ extern "C" detffn_status detffn_backward(detffn_handle h, const void* x, const v
   }
   return wgrads(h, f, (const uint16_t*)x, (const uint16_t*)dOut, w.h, dU, dG, (uint16_t*)dWg,
                 (uint16_t*)dWu, (uint16_t*)dWd, M, H, I, st);
+}
+
+}  // namespace
+
+extern "C" detffn_status detffn_backward(detffn_handle h, const void* x, const void* Wg,
+                                         const void* Wu, const void* Wd, const void* gate,
+                                         const void* up, const void* dOut, void* dX, void* dWg,
+                                         void* dWu, void* dWd, void* dh_save, void* dU_save,
+                                         void* dG_save, long long M, long long H, long long I,
+                                         void* ws, size_t ws_bytes, void* stream,
+                                         const detffn_options* opts) {
+  Saved saved;
+  saved.gate = (const uint16_t*)gate;
+  saved.up = (const uint16_t*)up;
+  return backward(h, x, Wg, Wu, Wd, saved, dOut, dX, dWg, dWu, dWd, dh_save, dU_save, dG_save, M, H, I, ws, ws_bytes,
+                  stream, opts);
+}
+
+extern "C" detffn_status detffn_backward_ckpt8(detffn_handle h, const void* x, const void* Wg, const void* Wu,
+                                               const void* Wd, const void* gate_codes, const void* gate_scales,
+                                               const void* up_codes, const void* up_scales, const void* dOut, void* dX,
+                                               void* dWg, void* dWu, void* dWd, long long M, long long H, long long I,
+                                               void* ws, size_t ws_bytes, void* stream, const detffn_options* opts) {
+  if (!gate_codes || !gate_scales || !up_codes || !up_scales) return DETFFN_ERR_INVALID_ARG;
+  if (((uintptr_t)gate_scales & 3u) || ((uintptr_t)up_scales & 3u)) return DETFFN_ERR_ALIGN;
+  Saved saved;
+  saved.ckpt.gq = (int8_t*)gate_codes;
+  saved.ckpt.uq = (int8_t*)up_codes;
+  saved.ckpt.gs = (float*)gate_scales;
+  saved.ckpt.us = (float*)up_scales;
+  return backward(h, x, Wg, Wu, Wd, saved, dOut, dX, dWg, dWu, dWd, nullptr, nullptr, nullptr, M, H, I, ws, ws_bytes,
+                  stream, opts);
 }
 
 extern "C" detffn_status detffn_wgrad_chunked(detffn_handle h, int n_chunks,
@@ -1142,7 +1194,10 @@ extern "C" detffn_status detffn_wgrad_chunked(detffn_handle h, int n_chunks,
       gc = w.g + r0 * I;
       uc = w.u + r0 * I;
     }
-    TRY(rowwise_bwd(h, f, dOc, (const uint16_t*)Wd, gc, uc, w.dh + r0 * I, w.dU + r0 * I,
+    Saved saved;
+    saved.gate = gc;
+    saved.up = uc;
+    TRY(rowwise_bwd(h, f, dOc, (const uint16_t*)Wd, saved, w.dh + r0 * I, w.dU + r0 * I,
                     w.dG + r0 * I, w.h + r0 * I, t, H, I, st, w.tcs));
     r0 += t;
   }

@@ -432,6 +432,17 @@ DETFFN_API detffn_status detffn_ckpt8_silu_backward(const void* dh, const void* 
                                                     const void* up_codes, const void* up_scales, void* dU, void* dG,
                                                     void* h, long long M, long long I, int dtype, void* stream);
 
+/* detffn_backward with gate and up from an 8-bit checkpoint: the same tree
+ * contractions (and the same options and workspace, DETFFN_OP_BACKWARD) around
+ * the stage above, whose dU, dG and h are each rounded to BF16 once.  The
+ * activations a training step keeps for this call take 1 + 1/16 bytes an
+ * element instead of 2. */
+DETFFN_API detffn_status detffn_backward_ckpt8(detffn_handle h, const void* x, const void* Wg, const void* Wu,
+                                               const void* Wd, const void* gate_codes, const void* gate_scales,
+                                               const void* up_codes, const void* up_scales, const void* dOut, void* dX,
+                                               void* dWg, void* dWu, void* dWd, long long M, long long H, long long I,
+                                               void* ws, size_t ws_bytes, void* stream, const detffn_options* opts);
+
 /* A mixture-of-experts layer for T <= 64 tokens, E <= 512 experts of which
  * each token takes top_k <= 16 (H, I <= 65536):
  *   logits = x Wr^T; the top_k largest, in descending order, the lower index first among equals
