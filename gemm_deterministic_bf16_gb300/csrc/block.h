@@ -15,7 +15,7 @@ struct Rows {
 constexpr long long kJoinMaxH = 32768;
 // Column sums of the backward pass are taken over this many row sets at
 // most, whatever the GPU, so that their order depends on the sizes alone.
-constexpr int kJoinSets = 304;
+constexpr int kJoinSets = 152;
 
 struct JoinArgs {
   long long M = 0;

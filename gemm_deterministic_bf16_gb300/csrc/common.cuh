@@ -26,20 +26,29 @@ __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol
 // (programmatic dependent launch); the kernel waits in grid_dep_wait before
 // touching global memory, and lets its own successor launch with
 // grid_dep_launch (which takes effect once every one of its CTAs has run it).
+// With cluster > 1, in clusters of that many CTAs.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*k)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t st,
-                             Args&&... args) {
+cudaError_t launch_cluster(void (*k)(KArgs...), dim3 grid, int threads, int smem, int cluster, cudaStream_t st,
+                           Args&&... args) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = (size_t)smem;
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = (unsigned)cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, static_cast<Args&&>(args)...);
+}
+template <typename... KArgs, typename... Args>
+cudaError_t launch_dependent(void (*k)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t st,
+                             Args&&... args) {
+  return launch_cluster(k, grid, threads, smem, 1, st, static_cast<Args&&>(args)...);
 }
 
 constexpr int kLeaf = 64;        // leaf width (K positions per FP32 leaf)

@@ -1,6 +1,7 @@
 // k_join.cuh -- the norms before and after a block joined with its gate and
-// residual scale: kernels for one element type (each k_join_*.cu instantiates
-// one).
+// residual scale: the formulas, the forward kernel for few rows or very wide
+// ones, and the sums over row sets (each k_join_*.cu instantiates one element
+// type; k_join_ring.cuh has the kernels for the rest).
 //
 // Forward, for each token (a row of H features):
 //   n   = z / sqrt(mean(z^2) + eps) * w_post      (the norm after the block; n = z without w_post)
@@ -102,6 +103,7 @@ __device__ __forceinline__ void load_gate(const JoinArgs& a, long long m, int H,
   }
 }
 
+// One block of threads to a row, V units to a thread, the row in registers.
 template <int DT, int V, bool VEC>
 __global__ void __launch_bounds__(512) k_fwd(const __grid_constant__ JoinArgs a) {
   __shared__ float buf[2 * 32];
@@ -167,147 +169,14 @@ __global__ void __launch_bounds__(512) k_fwd(const __grid_constant__ JoinArgs a)
   }
 }
 
-// Row set s = blockIdx.x: rows s, s + gridDim.x, ...
-template <int DT, int V, bool VEC>
-__global__ void __launch_bounds__(512) k_bwd(const __grid_constant__ JoinArgs a) {
-  __shared__ float buf[2 * 3 * 32], buf2[2 * 2 * 32];
-  grid_dep_wait();
-  grid_dep_launch();
-  const int G = blockDim.x, t = threadIdx.x, H = a.H;
-  const float inv = 1.0f / (float)H;
-  int turn = 0, turn2 = 0;
-  const bool feature = a.dgate && a.gate_cs && !a.gate_rs, full = a.dgate && a.gate_cs && a.gate_rs;
-  const bool token = a.dgate && !a.gate_cs && a.gate_rs, scalar = a.dgate && !a.gate_cs && !a.gate_rs;
-  float wpre[V][8], wpost[V][8], wgate[V][8], whole = 0.0f;
-#pragma unroll
-  for (int i = 0; i < V; ++i)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) wpre[i][j] = wpost[i][j] = wgate[i][j] = 0.0f;
-  for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
-    float dx[V][8], z[V][8];
-    float s[3] = {0.0f, 0.0f, 0.0f};  // sum r^2, sum dy w_pre r, sum z^2
-    if (a.z.p) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        load<DT, VEC>(a.z.p, m * a.z.ld, H, i, G, t, z[i]);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[2] = fmaf(z[i][j], z[i][j], s[2]);
-      }
-    }
-    if (a.w_pre) {
-      float r[V][8], dy[V][8];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float w[8];
-        load<DT, VEC>(a.r.p, m * a.r.ld, H, i, G, t, r[i]);
-        load<DT, VEC>(a.dy.p, m * a.dy.ld, H, i, G, t, dy[i]);
-        load_param<DT, VEC>(a.w_pre, a.pdtype, 0, H, i, G, t, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          s[0] = fmaf(r[i][j], r[i][j], s[0]);
-          s[1] = fmaf(dy[i][j] * w[j], r[i][j], s[1]);
-        }
-      }
-      block_sums<3>(s, buf, turn);
-      const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * (q * q * q);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float w[8];
-        load_param<DT, VEC>(a.w_pre, a.pdtype, 0, H, i, G, t, w);
-        if (a.dr.p) {
-          load<DT, VEC>(a.dr.p, m * a.dr.ld, H, i, G, t, dx[i]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dx[i][j] = 0.0f;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float qd = q * dy[i][j];
-          dx[i][j] += fmaf(qd, w[j], -k * r[i][j]);
-          wpre[i][j] = fmaf(qd, r[i][j], wpre[i][j]);
-        }
-        store<DT, VEC>(const_cast<void*>(a.dx.p), m * a.dx.ld, H, i, G, t, dx[i]);
-      }
-    } else {
-      if (a.w_post) block_sums<3>(s, buf, turn);
-#pragma unroll
-      for (int i = 0; i < V; ++i) load<DT, VEC>(a.dr.p, m * a.dr.ld, H, i, G, t, dx[i]);
-    }
-    if (!a.dz.p) continue;
-    // dx becomes dn w_post, the gradient of the normalised z.
-    const float b = a.w_post ? rsqrtf(s[2] * inv + a.eps) : 1.0f;
-    float e[2] = {0.0f, 0.0f};  // sum dn w_post z, sum t n
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      float w[8], g[8];
-      if (a.w_post) {
-        load_param<DT, VEC>(a.w_post, a.pdtype, 0, H, i, G, t, w);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = 1.0f;
-      }
-      if (a.gate) {
-        load_gate<DT, VEC>(a, m, H, i, G, t, g);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) g[j] = 1.0f;
-      }
-      float dg[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = a.scale * dx[i][j], zn = a.z.p ? z[i][j] * b : 0.0f;
-        dg[j] = d * (zn * w[j]);
-        const float dn = d * g[j];
-        wpost[i][j] = fmaf(dn, zn, wpost[i][j]);
-        dx[i][j] = dn * w[j];
-        if (a.z.p) e[0] = fmaf(dx[i][j], z[i][j], e[0]);
-        e[1] += dg[j];
-        wgate[i][j] += dg[j];
-      }
-      if (full) {
-        if (DT == DETFFN_F32 || a.pdtype == DT) store<DT, VEC>(a.dgate, m * H, H, i, G, t, dg);
-        else store<DETFFN_F32, VEC>(a.dgate, m * H, H, i, G, t, dg);
-      }
-    }
-    if (a.w_post || token || scalar) {
-      block_sums<2>(e, buf2, turn2);
-      if (token && t == 0) put_param<DT>(a.dgate, a.pdtype, m, e[1]);
-      whole += e[1];
-    }
-    const float k = a.w_post ? e[0] * inv * (b * b * b) : 0.0f;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      if (a.w_post) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dx[i][j] = fmaf(b, dx[i][j], -k * z[i][j]);
-      }
-      store<DT, VEC>(const_cast<void*>(a.dz.p), m * a.dz.ld, H, i, G, t, dx[i]);
-    }
-  }
-  // This set's column sums.
-  float* p = a.part;
-  const long long sets = gridDim.x;
-#pragma unroll
-  for (int kind = 0; kind < 3; ++kind) {
-    if (kind == 0 ? !a.dw_post : kind == 1 ? !a.dw_pre : !feature) continue;
-    const float(&acc)[V][8] = kind == 0 ? wpost : kind == 1 ? wpre : wgate;
-#pragma unroll
-    for (int i = 0; i < V; ++i)
-      store<DETFFN_F32, VEC>(p, (long long)blockIdx.x * H, H, i, G, t, acc[i]);
-    p += sets * H;
-  }
-  if (scalar && t == 0) p[blockIdx.x] = whole;
-}
-
 constexpr int kSetReads = 10;
-static_assert(kJoinSets <= 32 * kSetReads, "a thread of k_sets reads at most kSetReads sets");
 
 // out[c] = sum over sets of part[s][c]: Q = blockDim / 32 threads per column
 // take sets q, q + Q, ... in order and their sums are added in order.
 template <int DT>
-__global__ void __launch_bounds__(1024) k_sets(const float* __restrict__ part, int sets, long long n, void* out0,
+__global__ void __launch_bounds__(512) k_sets(const float* __restrict__ part, int sets, long long n, void* out0,
                                               void* out1, void* out2, long long per, int pdtype) {
-  __shared__ float s[32][33];
+  __shared__ float s[16][33];
   grid_dep_wait();
   grid_dep_launch();
   const int lane = threadIdx.x & 31, q = threadIdx.x >> 5, Q = blockDim.x >> 5;
@@ -326,7 +195,8 @@ __global__ void __launch_bounds__(1024) k_sets(const float* __restrict__ part, i
     put_param<DT>(blockIdx.y == 0 ? out0 : blockIdx.y == 1 ? out1 : out2, pdtype, c, v);
   }
 }
-inline int sets_threads(int sets) { return sets <= 8 * kSetReads ? 256 : sets <= 16 * kSetReads ? 512 : 1024; }
+static_assert(kJoinSets <= 16 * kSetReads, "a thread of k_sets reads at most kSetReads sets");
+inline int sets_threads(int sets) { return sets <= 8 * kSetReads ? 256 : 512; }
 
 inline bool on16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 
@@ -341,16 +211,6 @@ bool vectors(const JoinArgs& a) {
   if (!on16(a.w_post) || !on16(a.w_pre)) return false;
   if (a.gate && a.gate_cs && (!on16(a.gate) || (a.gate_rs * pb) % 16 || !on16(a.dgate))) return false;
   return true;
-}
-
-// Threads of a row and the 8-feature units of each: one unit a thread up to
-// 512 threads, then more units.
-inline int pick(int H, int* threads) {
-  const int units = (H + 7) / 8;
-  int v = 1;
-  while (v < 8 && (units + v - 1) / v > 512) v *= 2;
-  *threads = ((units + v - 1) / v + 31) / 32 * 32;
-  return v;
 }
 
 }  // namespace join

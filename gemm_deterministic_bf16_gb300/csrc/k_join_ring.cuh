@@ -1,5 +1,5 @@
-// k_join_ring.cuh -- the residual join over many rows of whole 16-byte vectors
-// (the formulas are those of k_join.cuh).
+// k_join_ring.cuh -- the residual join over many rows (the formulas are those
+// of k_join.cuh).
 //
 // A CTA per SM holds groups of threads, one row at a time to a group and
 // eight features (a unit) to a thread.  What bounds these passes is HBM, and
@@ -8,6 +8,12 @@
 // loads of later rows run under the two sums of the current one.  The
 // parameters stay in registers for all rows of a group, and in the backward
 // pass so do the column sums.
+//
+// VEC: rows of whole 16-byte vectors on 16-byte boundaries; a unit is eight
+// features in a row.  Otherwise the copies take the 16-byte pieces that hold a
+// byte of the row (a piece never crosses an allocation's boundary), and a
+// thread's features lie G apart, so that a warp's accesses to shared and global
+// memory stay together wherever the row begins.
 #pragma once
 
 #include "k_join.cuh"
@@ -19,15 +25,17 @@ namespace join {
 constexpr int kRingBytes = 208 * 1024;   // shared memory for rows
 constexpr int kRingMaxStages = 8;
 constexpr int kRingMaxGroups = 16;       // 512 threads; groups of several warps (at most 8) have a named barrier each
-constexpr int kRingSets = 152;           // CTAs: column sums are taken per CTA, so not of the GPU at hand
+constexpr int kRingSets = kJoinSets;     // CTAs, whatever the GPU: column sums are taken per CTA
 
 struct RingPlan {
   int G = 0, R = 0, S = 0, grid = 0;     // threads of a group, groups of a CTA, rows of a ring, CTAs
   int n = 0;                             // tensors of a row
-  int bytes[5] = {};                     // their row bytes
+  int es[5] = {};                        // their element bytes
+  int off[5] = {};                       // where each lies in a slot
   const unsigned char* p[5] = {};
   long long step[5] = {};                // bytes between rows
-  int row = 0;                           // their sum
+  int row = 0;                           // bytes of a slot
+  int C = 1, width = 0;                  // CTAs that share a row, and the features of each but the last
 };
 
 __device__ __forceinline__ void group_barrier(int group, int G) {
@@ -77,16 +85,42 @@ struct Ring1 {
   uint32_t phase = 0;
 };
 
-// Issues the copies of row m into slot s (one thread).
-__device__ __forceinline__ void ring_fill(const RingPlan& p, const Ring1& r, int s, long long m) {
-  mbar_arrive_expect_tx(&r.full[s], (uint32_t)p.row);
+// Issues the copies of features [col, col + width) of row m into slot s (one
+// thread).
+template <bool VEC, bool WIDE>
+__device__ __forceinline__ void ring_fill(const RingPlan& p, const Ring1& r, int s, long long m, int col, int width) {
   unsigned char* d = r.base + (size_t)s * p.row;
+  if (VEC && !WIDE) {   // whole rows of whole pieces: a slot's bytes
+    mbar_arrive_expect_tx(&r.full[s], (uint32_t)p.row);
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (i < p.n) bulk_g2s(d + p.off[i], p.p[i] + m * p.step[i], (uint32_t)(width * p.es[i]), &r.full[s]);
+    return;
+  }
+  uint32_t size[5], all = 0;
 #pragma unroll
   for (int i = 0; i < 5; ++i)
     if (i < p.n) {
-      bulk_g2s(d, p.p[i] + m * p.step[i], (uint32_t)p.bytes[i], &r.full[s]);
-      d += p.bytes[i];
+      size[i] = (uint32_t)(width * p.es[i]);
+      if (!VEC) size[i] = ((uint32_t)((uintptr_t)(p.p[i] + m * p.step[i] + col * p.es[i]) & 15) + size[i] + 15) & ~15u;
+      all += size[i];
     }
+  mbar_arrive_expect_tx(&r.full[s], all);
+#pragma unroll
+  for (int i = 0; i < 5; ++i)
+    if (i < p.n) {
+      const uintptr_t at = (uintptr_t)(p.p[i] + m * p.step[i] + col * p.es[i]);
+      bulk_g2s(d + p.off[i], (const void*)(VEC ? at : at & ~(uintptr_t)15), size[i], &r.full[s]);
+    }
+}
+
+// Row m of tensor i in a slot, from feature col on.
+template <bool VEC>
+__device__ __forceinline__ const unsigned char* ring_row(const RingPlan& p, const unsigned char* slot, int i, long long m,
+                                                         int col) {
+  if (VEC) return slot + p.off[i];
+  return slot + p.off[i] +
+         (((uint32_t)(uintptr_t)p.p[i] + (uint32_t)m * (uint32_t)p.step[i] + (uint32_t)(col * p.es[i])) & 15u);
 }
 
 // Waits for the row in the current slot.  Its copies were issued by this very
@@ -96,21 +130,61 @@ __device__ __forceinline__ bool ring_wait(const Ring1& r) {
   return mbar_wait(&r.full[r.s], r.phase, kDefaultSpin, nullptr);
 }
 
-// Unit c / 8 of a row.
-template <int DT>
-__device__ __forceinline__ void unit(const void* row, int c, float (&v)[8]) {
-  Io<DT>::ld8(static_cast<const typename Io<DT>::E*>(row) + c, v);
+// One unit of a thread: with VEC features c .. c + 7 (a thread past the row's
+// end reads the last unit and counts for nothing: on is 0), else c + j step
+// where bit j of on is set, and zeros.
+struct Cols {
+  int c, step;
+  uint32_t on;
+};
+template <bool VEC>
+__device__ __forceinline__ Cols cols_of(int i, int G, int t, int H) {
+  Cols k;
+  k.step = G;
+  if (VEC) {
+    k.on = 8 * (i * G + t) < H;
+    k.c = k.on ? 8 * (i * G + t) : H - 8;
+  } else {
+    k.c = 8 * i * G + t;
+    k.on = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k.on |= (k.c + j * G < H ? 1u : 0u) << j;
+  }
+  return k;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void unit(const void* row, const Cols& k, float (&v)[8]) {
+  using E = typename Io<DT>::E;
+  const E* p = static_cast<const E*>(row) + k.c;
+  if (VEC) {
+    Io<DT>::ld8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = k.on >> j & 1 ? Io<DT>::ld(p + j * k.step) : 0.0f;
+  }
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void put_unit(void* row, const Cols& k, const float (&v)[8]) {
+  using E = typename Io<DT>::E;
+  E* p = static_cast<E*>(row) + k.c;
+  if (VEC) {
+    if (k.on) Io<DT>::st8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k.on >> j & 1) Io<DT>::st(p + j * k.step, v[j]);
+  }
 }
 // The same of a parameter, in the rows' type or FP32; `fill` where there is none.
-template <int DT>
-__device__ __forceinline__ void param_unit(const void* p, int pdtype, int c, float fill, float (&v)[8]) {
+template <int DT, bool VEC>
+__device__ __forceinline__ void param_unit(const void* p, int pdtype, const Cols& k, float fill, float (&v)[8]) {
   if (!p) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = fill;
   } else if (DT == DETFFN_F32 || pdtype == DT) {
-    unit<DT>(p, c, v);
+    unit<DT, VEC>(p, k, v);
   } else {
-    unit<DETFFN_F32>(p, c, v);
+    unit<DETFFN_F32, VEC>(p, k, v);
   }
 }
 __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
@@ -127,22 +201,18 @@ __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) 
 // Forward.  V units to a thread: two where a row of units fills two warps, which
 // halves what a row costs beside its elements.  PLAIN: both norms, and a gate
 // (if any) that is the same for every row.
-template <int DT, int V, bool PLAIN>
+template <int DT, int V, bool PLAIN, bool VEC>
 __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kRingMaxGroups * kRingMaxStages];
   __shared__ float sums[8 * 64];   // (groups of several warps: at most 8)
   using E = typename Io<DT>::E;
-  const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H, rb = H * Io<DT>::kBytes;
+  const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H;
   const bool has_z = PLAIN || a.z.p, has_post = PLAIN || a.w_post, has_pre = PLAIN || a.w_pre;
   const bool by_row = !PLAIN && a.gate && a.gate_rs;
-  bool on[V];
-  int c[V];
+  Cols k[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) {   // (threads past the row's end read its last unit and count for nothing)
-    on[i] = 8 * (i * G + t) < H;
-    c[i] = on[i] ? 8 * (i * G + t) : H - 8;
-  }
+  for (int i = 0; i < V; ++i) k[i] = cols_of<VEC>(i, G, t, H);
   const long long first = (long long)blockIdx.x * p.R + group, step = (long long)gridDim.x * p.R;
   Ring1 ring{smem + (size_t)group * p.S * p.row, full + group * p.S};
   float* buf = sums + (G == 32 ? 0 : group * 64);
@@ -154,14 +224,14 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
   grid_dep_launch();
   if (t == 0)
     for (int s = 0; s < p.S; ++s)
-      if (first + s * step < a.M) ring_fill(p, ring, s, first + s * step);
+      if (first + s * step < a.M) ring_fill<VEC, false>(p, ring, s, first + s * step, 0, H);
   float mix[V][8], pre[V][8];      // mix: scale * gate * w_post
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float w[8];
-    param_unit<DT>(has_pre ? a.w_pre : nullptr, a.pdtype, c[i], 1.0f, pre[i]);
-    param_unit<DT>(has_post ? a.w_post : nullptr, a.pdtype, c[i], 1.0f, w);
-    param_unit<DT>(a.gate && a.gate_cs && !by_row ? a.gate : nullptr, a.pdtype, c[i],
+    param_unit<DT, VEC>(has_pre ? a.w_pre : nullptr, a.pdtype, k[i], 1.0f, pre[i]);
+    param_unit<DT, VEC>(has_post ? a.w_post : nullptr, a.pdtype, k[i], 1.0f, w);
+    param_unit<DT, VEC>(a.gate && a.gate_cs && !by_row ? a.gate : nullptr, a.pdtype, k[i],
                    a.gate && !a.gate_cs && !by_row ? param<DT>(a.gate, a.pdtype, 0) : 1.0f, mix[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) mix[i][j] *= a.scale * w[j];
@@ -173,14 +243,14 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
   const long long out_step = step * a.out.ld, y_step = step * a.y.ld;
   __syncthreads();   // the barriers are initialised
   // The sum over z of the row in slot `s`.
-  auto sum_z = [&](int s) {
+  auto sum_z = [&](int s, long long m) {
     float v = 0.0f;
     if (has_post) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         float n[8];
-        unit<DT>(ring.base + (size_t)s * p.row + rb, c[i], n);
-        v += on[i] ? dot8(n, n) : 0.0f;
+        unit<DT, VEC>(ring_row<VEC>(p, ring.base + (size_t)s * p.row, 1, m, 0), k[i], n);
+        v += k[i].on ? dot8(n, n) : 0.0f;
       }
     }
     return v;
@@ -188,7 +258,7 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
   float sz = 0.0f;
   if (first < a.M) {
     const bool came = ring_wait(ring);
-    float v[2] = {came ? sum_z(0) : __int_as_float(0x7fc00000), 0.0f};
+    float v[2] = {came ? sum_z(0, first) : __int_as_float(0x7fc00000), 0.0f};
     group_sums<2>(v, buf, turn, G, group, t);
     sz = v[0];
   }
@@ -200,31 +270,31 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
       ring.phase ^= 1u;
     }
     float v[2] = {0.0f, 0.0f};
-    if (m + step < a.M) v[0] = ring_wait(ring) ? sum_z(ring.s) : __int_as_float(0x7fc00000);
+    if (m + step < a.M) v[0] = ring_wait(ring) ? sum_z(ring.s, m + step) : __int_as_float(0x7fc00000);
     float r[V][8];
     const float b = has_post ? rsqrtf(sz * inv + a.eps) : 1.0f;
     float g1 = 0.0f;
     if (by_row && !a.gate_cs) g1 = param<DT>(a.gate, a.pdtype, m * a.gate_rs);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      unit<DT>(row, c[i], r[i]);
+      unit<DT, VEC>(ring_row<VEC>(p, row, 0, m, 0), k[i], r[i]);
       if (has_z) {
         float n[8];
-        unit<DT>(row + rb, c[i], n);
+        unit<DT, VEC>(ring_row<VEC>(p, row, 1, m, 0), k[i], n);
         if (by_row) {
           float g[8];
-          param_unit<DT>(a.gate_cs ? row + 2 * rb : nullptr, a.pdtype, c[i], g1, g);
+          param_unit<DT, VEC>(a.gate_cs ? ring_row<VEC>(p, row, 2, m, 0) : nullptr, a.pdtype, k[i], g1, g);
 #pragma unroll
           for (int j = 0; j < 8; ++j) n[j] *= g[j];
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[i][j] = fmaf(b * n[j], mix[i][j], r[i][j]);
-        if (on[i]) Io<DT>::st8(out + c[i], r[i]);
+        put_unit<DT, VEC>(out, k[i], r[i]);
       }
-      if (has_pre) v[1] += on[i] ? dot8(r[i], r[i]) : 0.0f;
+      if (has_pre) v[1] += k[i].on ? dot8(r[i], r[i]) : 0.0f;
     }
     group_sums<2>(v, buf, turn, G, group, t);
-    if (t == 0 && m + p.S * step < a.M) ring_fill(p, ring, slot, m + p.S * step);
+    if (t == 0 && m + p.S * step < a.M) ring_fill<VEC, false>(p, ring, slot, m + p.S * step, 0, H);
     sz = v[0];
     if (has_pre) {
       const float q = rsqrtf(v[1] * inv + a.eps);
@@ -232,24 +302,61 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
       for (int i = 0; i < V; ++i) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) r[i][j] *= q * pre[i][j];
-        if (on[i]) Io<DT>::st8(y + c[i], r[i]);
+        put_unit<DT, VEC>(y, k[i], r[i]);
       }
     }
   }
 }
 
-// Backward (rows of up to 4096 features, one unit to a thread).  PLAIN: both
-// norms, dr given, and a gate (if any) that is the same for every row.
-template <int DT, bool PLAIN>
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums over the CTAs of a cluster: each CTA's values (the same in all its
+// threads) go to every CTA's shared memory and are added there by rank.
+// `buf`: [2][8][4] floats.
+template <int N>
+__device__ __forceinline__ void cluster_sums(float (&v)[N], float* buf, int& turn, int C, int rank) {
+  float* b = buf + turn * 32;
+  turn ^= 1;
+  if ((int)threadIdx.x < C) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      asm volatile(
+          "{\n\t.reg .b32 a;\n\t"
+          "mapa.shared::cluster.u32 a, %0, %1;\n\t"
+          "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_u32(b + rank * 4 + i)),
+          "r"(threadIdx.x), "f"(v[i])
+          : "memory");
+  }
+  cluster_barrier();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = b[i];
+    for (int r = 1; r < C; ++r) v[i] += b[r * 4 + i];
+  }
+}
+
+// Backward, one unit to a thread.  PLAIN: both norms, dr given, and a gate (if
+// any) that is the same for every row.  WIDE: a cluster of CTAs shares each row
+// of more than 4096 features, a run of columns each, and the row's sums meet
+// in shared memory across it.
+template <int DT, bool PLAIN, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kRingMaxGroups * kRingMaxStages];
   __shared__ float sums[8 * (128 + 64)];   // (groups of several warps: at most 8)
   using E = typename Io<DT>::E;
-  const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H, rb = H * Io<DT>::kBytes;
-  const bool on = 8 * t < H;              // (threads past the row's end read its last unit and count for nothing)
-  const int c = on ? 8 * t : H - 8;
-  const long long first = (long long)blockIdx.x * p.R + group, step = (long long)gridDim.x * p.R;
+  const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H;
+  int rank = 0;
+  if (WIDE) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  __shared__ float across[2 * 8 * 4];
+  const int col = rank * p.width, width = WIDE ? min(p.width, H - col) : H;
+  const Cols cs = cols_of<VEC>(0, G, t, width);
+  const bool on = cs.on != 0;
+  const long long set = blockIdx.x / (WIDE ? p.C : 1), sets = gridDim.x / (WIDE ? p.C : 1);
+  const long long first = set * p.R + group, step = sets * p.R;
   Ring1 ring{smem + (size_t)group * p.S * p.row, full + group * p.S};
   float *buf = sums + (G == 32 ? 0 : group * 192), *buf2 = buf + 128;
   if (t == 0) {
@@ -260,16 +367,18 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   grid_dep_launch();
   if (t == 0)
     for (int s = 0; s < p.S; ++s)
-      if (first + s * step < a.M) ring_fill(p, ring, s, first + s * step);
+      if (first + s * step < a.M) ring_fill<VEC, WIDE>(p, ring, s, first + s * step, col, width);
   const bool has_z = PLAIN || a.z.p, has_post = PLAIN || a.w_post, has_pre = PLAIN || a.w_pre, has_dr = PLAIN || a.dr.p;
   const bool feature = a.dgate && a.gate_cs && !a.gate_rs, scalar = a.dgate && !a.gate_cs && !a.gate_rs;
   const bool full_gate = !PLAIN && a.dgate && a.gate_cs && a.gate_rs, token = !PLAIN && a.dgate && !a.gate_cs && a.gate_rs;
-  // Row layout: z, r, dy, dr, gate, those that there are.
-  const int orr = has_z ? rb : 0, ody = orr + (has_pre ? rb : 0), odr = ody + (has_pre ? rb : 0), og = odr + (has_dr ? rb : 0);
+  // The tensors of a row: z, r, dy, dr, gate, those that there are.
+  const int ir = has_z, idy = ir + has_pre, idr = idy + has_pre, ig = idr + has_dr;
   float pre[8], post[8], sg[8];   // w_pre, w_post, scale * gate
-  param_unit<DT>(has_pre ? a.w_pre : nullptr, a.pdtype, c, 1.0f, pre);
-  param_unit<DT>(has_post ? a.w_post : nullptr, a.pdtype, c, 1.0f, post);
-  param_unit<DT>(feature ? a.gate : nullptr, a.pdtype, c, scalar ? param<DT>(a.gate, a.pdtype, 0) : 1.0f, sg);
+  const long long pcol = (long long)col * (a.pdtype == DETFFN_F32 ? 4 : 2);
+  auto from = [&](const void* q) { return static_cast<const void*>(static_cast<const char*>(q) + pcol); };
+  param_unit<DT, VEC>(has_pre ? from(a.w_pre) : nullptr, a.pdtype, cs, 1.0f, pre);
+  param_unit<DT, VEC>(has_post ? from(a.w_post) : nullptr, a.pdtype, cs, 1.0f, post);
+  param_unit<DT, VEC>(feature ? from(a.gate) : nullptr, a.pdtype, cs, scalar ? param<DT>(a.gate, a.pdtype, 0) : 1.0f, sg);
   float apre[8], apost[8], agate[8];   // this thread's columns of the sums over tokens
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -277,25 +386,30 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     apre[j] = apost[j] = agate[j] = 0.0f;
   }
   const float inv = 1.0f / (float)H;
-  int turn = 0, turn2 = 0;
-  E* dxp = static_cast<E*>(const_cast<void*>(a.dx.p)) + first * a.dx.ld + c;
-  E* dzp = static_cast<E*>(const_cast<void*>(a.dz.p)) + first * a.dz.ld + c;
+  int turn = 0, turn2 = 0, turn3 = 0;
+  E* dxp = static_cast<E*>(const_cast<void*>(a.dx.p)) + first * a.dx.ld + col;
+  E* dzp = static_cast<E*>(const_cast<void*>(a.dz.p)) + first * a.dz.ld + col;
   const long long dx_step = step * a.dx.ld, dz_step = step * a.dz.ld;
   __syncthreads();   // the barriers are initialised
+  if (WIDE) cluster_barrier();   // and every CTA of the cluster has started
+  auto sums4 = [&](float (&v)[4]) {
+    group_sums<4>(v, buf, turn, G, group, t);
+    if (WIDE) cluster_sums<4>(v, across, turn3, p.C, rank);
+  };
   // Of the row in slot s: sum r^2, sum dy w_pre r, sum z^2.
-  auto row_sums = [&](int s, float (&v)[4]) {
+  auto row_sums = [&](int s, long long m, float (&v)[4]) {
     const unsigned char* row = ring.base + (size_t)s * p.row;
     float x[8], w[8];
     if (has_pre) {
-      unit<DT>(row + orr, c, x);
-      unit<DT>(row + ody, c, w);
+      unit<DT, VEC>(ring_row<VEC>(p, row, ir, m, col), cs, x);
+      unit<DT, VEC>(ring_row<VEC>(p, row, idy, m, col), cs, w);
       v[0] = dot8(x, x);
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] *= pre[j];
       v[1] = dot8(x, w);
     }
     if (has_post) {
-      unit<DT>(row, c, x);
+      unit<DT, VEC>(ring_row<VEC>(p, row, 0, m, col), cs, x);
       v[2] = dot8(x, x);
     }
     if (!on) v[0] = v[1] = v[2] = 0.0f;
@@ -303,9 +417,9 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   float s[3] = {0.0f, 0.0f, 0.0f};
   if (first < a.M) {
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (ring_wait(ring)) row_sums(0, v);
+    if (ring_wait(ring)) row_sums(0, first, v);
     else v[0] = v[2] = __int_as_float(0x7fc00000);
-    group_sums<4>(v, buf, turn, G, group, t);
+    sums4(v);
     s[0] = v[0], s[1] = v[1], s[2] = v[2];
   }
   for (long long m = first; m < a.M; m += step, dxp += dx_step, dzp += dz_step) {
@@ -317,21 +431,21 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     }
     float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     if (m + step < a.M) {
-      if (ring_wait(ring)) row_sums(ring.s, v);
+      if (ring_wait(ring)) row_sums(ring.s, m + step, v);
       else v[0] = v[2] = __int_as_float(0x7fc00000);
     }
     // dx
     float d[8], z[8], x[8];
     if (has_dr) {
-      unit<DT>(row + odr, c, d);
+      unit<DT, VEC>(ring_row<VEC>(p, row, idr, m, col), cs, d);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] = 0.0f;
     }
     if (has_pre) {
       float dy[8];
-      unit<DT>(row + orr, c, x);
-      unit<DT>(row + ody, c, dy);
+      unit<DT, VEC>(ring_row<VEC>(p, row, ir, m, col), cs, x);
+      unit<DT, VEC>(ring_row<VEC>(p, row, idy, m, col), cs, dy);
       const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * (q * q * q);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -339,14 +453,14 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
         d[j] = fmaf(qd, pre[j], fmaf(-k, x[j], d[j]));
         apre[j] = fmaf(qd, x[j], apre[j]);
       }
-      if (on) Io<DT>::st8(dxp, d);
+      put_unit<DT, VEC>(dxp, cs, d);
     }
     const float b = has_post ? rsqrtf(s[2] * inv + a.eps) : 1.0f;
     float tok[2] = {0.0f, 0.0f};   // sum dx n
     if (has_z) {
-      unit<DT>(row, c, z);
+      unit<DT, VEC>(ring_row<VEC>(p, row, 0, m, col), cs, z);
       if (full_gate || token) {
-        param_unit<DT>(full_gate ? row + og : nullptr, a.pdtype, c, token ? param<DT>(a.gate, a.pdtype, m * a.gate_rs) : 0.0f, sg);
+        param_unit<DT, VEC>(full_gate ? ring_row<VEC>(p, row, ig, m, col) : nullptr, a.pdtype, cs, token ? param<DT>(a.gate, a.pdtype, m * a.gate_rs) : 0.0f, sg);
 #pragma unroll
         for (int j = 0; j < 8; ++j) sg[j] *= a.scale;
       }
@@ -362,21 +476,20 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
       if (token) tok[0] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
       if (!on) v[3] = tok[0] = 0.0f;
     }
-    group_sums<4>(v, buf, turn, G, group, t);
-    if (t == 0 && m + p.S * step < a.M) ring_fill(p, ring, slot, m + p.S * step);
+    sums4(v);
+    if (t == 0 && m + p.S * step < a.M) ring_fill<VEC, WIDE>(p, ring, slot, m + p.S * step, col, width);
     s[0] = v[0], s[1] = v[1], s[2] = v[2];
     if (!PLAIN && !a.dz.p) continue;
     if (full_gate) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) x[j] *= a.scale;
-      if (on) {
-        if (DT == DETFFN_F32 || a.pdtype == DT) Io<DT>::st8(static_cast<E*>(a.dgate) + m * H + c, x);
-        else Io<DETFFN_F32>::st8(static_cast<float*>(a.dgate) + m * H + c, x);
-      }
+      if (DT == DETFFN_F32 || a.pdtype == DT) put_unit<DT, VEC>(static_cast<E*>(a.dgate) + m * H + col, cs, x);
+      else put_unit<DETFFN_F32, VEC>(static_cast<float*>(a.dgate) + m * H + col, cs, x);
     }
     if (token) {
       group_sums<2>(tok, buf2, turn2, G, group, t);
-      if (t == 0) put_param<DT>(a.dgate, a.pdtype, m, a.scale * tok[0]);
+      if (WIDE) cluster_sums<2>(tok, across, turn3, p.C, rank);
+      if (t == 0 && rank == 0) put_param<DT>(a.dgate, a.pdtype, m, a.scale * tok[0]);
     }
     const float k = v[3] * inv * (b * b);
 #pragma unroll
@@ -384,7 +497,7 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
       d[j] *= sg[j] * post[j];
       if (has_post) d[j] = fmaf(b, d[j], -k * z[j]);
     }
-    if (on) Io<DT>::st8(dzp, d);
+    put_unit<DT, VEC>(dzp, cs, d);
   }
   // The CTA's column sums: its groups' added in order (the rings are done
   // with, so their memory holds them).  Little code, as it runs once and cold:
@@ -398,8 +511,9 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
       float w[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = scale * v[j];
-      if (p.R > 1) Io<DETFFN_F32>::st8(all + kind * 4096 + 8 * threadIdx.x, w);
-      else if (on) Io<DETFFN_F32>::st8(a.part + ((long long)kind * gridDim.x + blockIdx.x) * H + c, w);
+      // (a group's columns: G 8 floats, in their own order)
+      if (p.R == 1) put_unit<DETFFN_F32, VEC>(a.part + (kind * sets + set) * H + col, cs, w);
+      else put_unit<DETFFN_F32, VEC>(all + kind * 4096 + group * G * 8, cs, w);
       ++kind;
     };
     if (a.dw_post) put(apost, 1.0f);
@@ -408,9 +522,9 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   }
   if (p.R > 1) {
     __syncthreads();
-    float* part = a.part + (long long)blockIdx.x * H;
+    float* part = a.part + set * H;
 #pragma unroll 1
-    for (int kind = 0; kind < kinds; ++kind, part += (long long)gridDim.x * H)
+    for (int kind = 0; kind < kinds; ++kind, part += sets * H)
 #pragma unroll 1
       for (int i = threadIdx.x; i < H; i += blockDim.x) {
         float v = 0.0f;
@@ -429,42 +543,44 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     if (threadIdx.x == 0) {
       float w = 0.0f;
       for (int q = 0; q < (int)blockDim.x >> 5; ++q) w += all[q];
-      a.part[(long long)kinds * gridDim.x * H + blockIdx.x] = a.scale * w;
+      a.part[kinds * sets * H + blockIdx.x] = a.scale * w;
     }
   }
 }
 
 // The ring's layout for rows of these tensors; false where fewer than two
-// rows fit a group's ring.
+// rows fit a group's ring.  V: units to a thread.
 template <int DT>
-bool ring_plan(const JoinArgs& a, bool back, RingPlan* out) {
+bool ring_plan(const JoinArgs& a, bool back, bool vec, int V, RingPlan* out) {
   RingPlan p;
-  const int es = Io<DT>::kBytes, ps = a.pdtype == DETFFN_F32 ? 4 : 2, units = a.H / 8;
-  const int V = back || units < 64 ? 1 : 2, threads = 512;
+  const int es = Io<DT>::kBytes, ps = a.pdtype == DETFFN_F32 ? 4 : 2, threads = 512;
+  if (back)
+    while (a.H > p.C * threads * 8 && p.C < 8) p.C *= 2;
+  p.width = ((a.H + p.C - 1) / p.C + 7) / 8 * 8;
+  const int units = p.width / 8;
   p.G = ((units + V - 1) / V + 31) / 32 * 32;
   if (p.G > threads) return false;
   const bool full = a.gate && a.gate_cs && a.gate_rs;
-  auto add = [&](const void* q, long long ld, int bytes) {
+  auto add = [&](const void* q, long long step, int bytes) {
     p.p[p.n] = static_cast<const unsigned char*>(q);
-    p.step[p.n] = ld;
-    p.bytes[p.n] = bytes;
-    p.row += bytes;
-    if (bytes) ++p.n;
+    p.step[p.n] = step;
+    p.es[p.n] = bytes;
+    p.off[p.n++] = p.row;
+    p.row += (p.width * bytes + 15) / 16 * 16 + (vec ? 0 : 16);
   };
   const Rows* rows[4] = {back ? &a.z : &a.x, back ? &a.r : &a.z, &a.dy, &a.dr};
   for (int i = 0; i < (back ? 4 : 2); ++i)
-    if (rows[i]->p) add(rows[i]->p, rows[i]->ld * es, a.H * es);
-  if (full) add(a.gate, a.gate_rs * ps, a.H * ps);
-  for (int i = 0; i < p.n; ++i)
-    if (p.bytes[i] % 16) return false;
+    if (rows[i]->p) add(rows[i]->p, rows[i]->ld * es, es);
+  if (full) add(a.gate, a.gate_rs * ps, ps);
   // Few rows go to as many CTAs as there are before two share one.
-  p.R = threads / p.G;
-  if (p.R > (a.M + kRingSets - 1) / kRingSets) p.R = (int)((a.M + kRingSets - 1) / kRingSets);
-    p.S = kRingBytes / (p.R * p.row);
+  const int most = kRingSets / p.C;
+  p.R = p.C > 1 ? 1 : threads / p.G;
+  if (p.R > (a.M + most - 1) / most) p.R = (int)((a.M + most - 1) / most);
+  p.S = kRingBytes / (p.R * p.row);
   if (p.S < 2) return false;
   if (p.S > kRingMaxStages) p.S = kRingMaxStages;
   const long long need = (a.M + p.R - 1) / p.R;
-  p.grid = (int)(need < kRingSets ? need : kRingSets);
+  p.grid = (int)(need < most ? need : most) * p.C;
   *out = p;
   return true;
 }
@@ -474,59 +590,56 @@ cudaError_t ring_launch(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
   static const cudaError_t setup = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (setup != cudaSuccess) return setup;
   const int smem = p.R * p.S * p.row > 49152 ? p.R * p.S * p.row : 49152;   // (48 KB: the groups' column sums)
-  return launch_dependent(K, dim3(p.grid), p.G * p.R, smem, st, a, p);
+  return launch_cluster(K, dim3(p.grid), p.G * p.R, smem, p.C, st, a, p);
 }
 
-// Whether a forward pass takes the ring kernel: it wins once its rows hold
-// about 4 MB (measured, BF16, H = 4096: 152 rows 3.3 us without and 3.7 us with
-// it, 608 rows 7.9 and 5.4; H = 1024: 1216 rows 4.1 and 4.3, 4864 rows 14.0 and
-// 11.3), and always where the other kernel would have several units to a thread
-// (H = 8192, 8 rows: 4.1 and 4.0).  The backward pass takes it wherever a row
-// fits: from one row on it is no slower (H = 1024, 32 rows: 5.7 us without, 5.0
-// with it; 4864 rows 60.9 and 22.4).
-inline bool ring_forward(const JoinArgs& a, const RingPlan& p) { return a.M * p.row >= 4 << 20 || a.H > 4096; }
+// Whether a forward pass takes the ring kernel (for up to 8192 features): it
+// wins once its rows hold about 4 MB (measured, BF16, H = 4096: 152 rows 3.3 us
+// without and 3.7 us with it, 608 rows 7.9 and 5.4; H = 1024: 1216 rows 4.1 and
+// 4.3, 4864 rows 14.0 and 11.3), always where the other kernel would have
+// several units to a thread (H = 8192, 8 rows: 4.1 and 4.0), and always for rows
+// that are not whole vectors (H = 1031: one row 3.6 and 3.3 us, 16384 rows 100
+// and 55).
+inline bool ring_forward(const JoinArgs& a, const RingPlan& p, bool vec) {
+  return !vec || a.M * p.row >= 4 << 20 || a.H > 4096;
+}
 
 template <int DT>
 cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
-  int threads;
-  const int v = pick(a.H, &threads);
   const bool vec = vectors<DT>(a);
   RingPlan p;
-  if (vec && ring_plan<DT>(a, false, &p) && ring_forward(a, p)) {
+  const bool two = vec ? a.H >= 512 : a.H > 4096;   // units to a thread
+  if (ring_plan<DT>(a, false, vec, two ? 2 : 1, &p) && ring_forward(a, p, vec)) {
     const bool plain = a.z.p && a.w_post && a.w_pre && !(a.gate && a.gate_rs);
-    if (a.H >= 512) return plain ? ring_launch<k_fwd_ring<DT, 2, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 2, false>>(a, p, st);
-    return plain ? ring_launch<k_fwd_ring<DT, 1, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 1, false>>(a, p, st);
+    if (vec) {
+      if (two) return plain ? ring_launch<k_fwd_ring<DT, 2, true, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 2, false, true>>(a, p, st);
+      return plain ? ring_launch<k_fwd_ring<DT, 1, true, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 1, false, true>>(a, p, st);
+    }
+    return two ? ring_launch<k_fwd_ring<DT, 2, false, false>>(a, p, st) : ring_launch<k_fwd_ring<DT, 1, false, false>>(a, p, st);
   }
+  // Few rows of whole vectors, or rows of more than 8192 features.
+  const int units = (a.H + 7) / 8, v = units <= 512 ? 1 : units <= 2048 ? 4 : 8;
+  const int threads = ((units + v - 1) / v + 31) / 32 * 32;
   const long long most = 152ll * 16;
   const dim3 grid((unsigned)(a.M < most ? a.M : most));
   auto go = [&](auto k) { return launch_dependent(k, grid, threads, 0, st, a); };
-  switch (v) {
-    case 1: return go(vec ? k_fwd<DT, 1, true> : k_fwd<DT, 1, false>);
-    case 2: return go(vec ? k_fwd<DT, 2, true> : k_fwd<DT, 2, false>);
-    case 4: return go(vec ? k_fwd<DT, 4, true> : k_fwd<DT, 4, false>);
-    default: return go(vec ? k_fwd<DT, 8, true> : k_fwd<DT, 8, false>);
-  }
+  if (v == 1) return go(k_fwd<DT, 1, true>);
+  if (v == 4) return go(vec ? k_fwd<DT, 4, true> : k_fwd<DT, 4, false>);
+  return go(vec ? k_fwd<DT, 8, true> : k_fwd<DT, 8, false>);
 }
 
 template <int DT>
 cudaError_t backward(const JoinArgs& a, cudaStream_t st) {
-  int threads;
-  const int v = pick(a.H, &threads);
   const bool vec = vectors<DT>(a);
-  int sets = (int)(a.M < kJoinSets ? a.M : kJoinSets);
-  RingPlan p;
-  const bool ring = vec && ring_plan<DT>(a, true, &p);
   const bool plain = a.w_post && a.w_pre && a.dr.p && !(a.gate && a.gate_rs);
-  if (ring) sets = p.grid;
-  auto go = [&](auto k) { return launch_dependent(k, dim3(sets), threads, 0, st, a); };
+  RingPlan p;
+  if (!ring_plan<DT>(a, true, vec, 1, &p)) return cudaErrorInvalidConfiguration;   // (two rows always fit)
+  const int sets = p.grid / p.C;
   cudaError_t e;
-  if (ring) e = plain ? ring_launch<k_bwd_ring<DT, true>>(a, p, st) : ring_launch<k_bwd_ring<DT, false>>(a, p, st);
-  else switch (v) {
-    case 1: e = go(vec ? k_bwd<DT, 1, true> : k_bwd<DT, 1, false>); break;
-    case 2: e = go(vec ? k_bwd<DT, 2, true> : k_bwd<DT, 2, false>); break;
-    case 4: e = go(vec ? k_bwd<DT, 4, true> : k_bwd<DT, 4, false>); break;
-    default: e = go(vec ? k_bwd<DT, 8, true> : k_bwd<DT, 8, false>); break;
-  }
+  if (p.C > 1)
+    e = vec ? ring_launch<k_bwd_ring<DT, false, true, true>>(a, p, st) : ring_launch<k_bwd_ring<DT, false, false, true>>(a, p, st);
+  else if (!vec) e = ring_launch<k_bwd_ring<DT, false, false, false>>(a, p, st);
+  else e = plain ? ring_launch<k_bwd_ring<DT, true, true, false>>(a, p, st) : ring_launch<k_bwd_ring<DT, false, true, false>>(a, p, st);
   if (e != cudaSuccess) return e;
   void* out[3] = {};
   int n = 0;
@@ -539,7 +652,7 @@ cudaError_t backward(const JoinArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
   }
   if (a.dgate && !a.gate_cs && !a.gate_rs)
-    e = launch_dependent(k_sets<DT>, dim3(1), sets_threads(sets), 0, st, (const float*)a.part + (long long)n * sets * a.H, sets, 1ll,
+    e = launch_dependent(k_sets<DT>, dim3(1), sets_threads(p.grid), 0, st, (const float*)a.part + (long long)n * sets * a.H, p.grid, 1ll,
                          a.dgate, (void*)nullptr, (void*)nullptr, 0ll, a.pdtype);
   return e;
 }

@@ -9,7 +9,8 @@ relative error is at most 86 e, its inverse root's half that plus 2 ulp
 (rsqrt) -- below 48 e.  Each output then takes a handful of products and sums
 of terms whose absolute values sum to `mag`: |error| <= u |value| + 64 e mag
 for outputs without further sums, and + 150 e mag where two sums over the row
-enter.  Sums over tokens add at most ceil(M / 304) + 304 / 8 + 8 additions."""
+enter.  Sums over tokens add the M / 152 rows of a thread, up to 16 groups, 10
+sets and 16 threads: for the M here below ceil(M / 304) + 46 additions."""
 import numpy as np
 import pytest
 import torch
