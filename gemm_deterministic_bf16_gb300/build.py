@@ -86,7 +86,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         lib = os.path.join(torch_dir, "lib")
         tmp = NATIVE + ".tmp.%d" % os.getpid()
         run(["g++", "-shared", "-o", tmp, bind_obj, "-L" + PKG, "-l:libdetffn.so", "-Wl,-rpath,$ORIGIN", "-L" + lib,
-             "-ltorch_python", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + lib])
+             "-ltorch_python", "-ltorch_cuda", "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath," + lib])
         os.replace(tmp, NATIVE)
     return OUT
 

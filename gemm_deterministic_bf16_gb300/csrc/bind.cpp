@@ -9,7 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -138,8 +138,9 @@ void whole(const Tensor& t, int device, at::ScalarType type, at::IntArrayRef sha
 
 void* stream_of(int device) { return c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)device).stream(); }
 
+// A CUDA tensor beside `like`, from its allocator directly.
 Tensor empty(at::IntArrayRef shape, const Tensor& like, at::ScalarType type) {
-  return at::empty(shape, like.options().dtype(type));
+  return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
 #define BODY(n)                                                             \
