@@ -108,9 +108,11 @@ __global__ void __launch_bounds__(1024) k_select(const __grid_constant__ MoeArgs
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, P = a.T * a.k;
   for (int t = warp; t < a.T; t += blockDim.x / 32) {
     const float* l = a.logits + (long long)t * a.E;
-    uint32_t key[kMoeMaxExperts / 32];
-    moe_keys<kMoeMaxExperts / 32>(a.logits, a.T, a.E, t, lane, key);
-    const MoeChoice c = moe_choose<kMoeMaxExperts / 32>(key, a.k, lane);
+    uint32_t key[1][kMoeMaxExperts / 32];
+    MoeChoice chose[1];
+    moe_keys<kMoeMaxExperts / 32>(a.logits, a.T, a.E, t, lane, key[0]);
+    moe_choose<kMoeMaxExperts / 32, 1>(key, a.k, lane, chose);
+    const MoeChoice c = chose[0];
     if (lane < a.k) {
       a.experts[t * a.k + lane] = c.expert;
       chosen[t * a.k + lane] = c.logit;

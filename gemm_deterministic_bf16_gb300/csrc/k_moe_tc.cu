@@ -52,6 +52,7 @@ __device__ constexpr uint32_t idesc_f16(bool bf16, int M, int N) {
   return (1u << 4) | (bf16 ? (1u << 7) | (1u << 10) : 0u) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
+static_assert(kMoeMaxTokens <= 64, "16 warps take four tokens each; an expert's tokens are 64 bits");
 constexpr int kThreads = 512;     // all work out the routing; then warp 0 loads, warp 1 issues MMAs, warps
                                   // 4-7 read the sums, 8-15 form the routing weights, and 4-15 out
 constexpr int kEpi0 = 4;          // first epilogue warp (its TMEM lane quarter is warp % 4)
@@ -71,6 +72,7 @@ struct Bars {
   int unit[kUnits];  // claimed units; past the last: no more
   int active;   // experts with tokens
   int most;     // most tokens of one expert
+  unsigned char tok[kMoeMaxTokens];  // the loading warp's: the current unit's tokens
 };
 
 struct Args {
@@ -142,28 +144,26 @@ __device__ __forceinline__ bool epi_all(bool ok) {
 // expert's tokens are a mask of 64 bits, and a pair's place among the pairs
 // ordered by expert and token is the expert's first plus a count of bits.
 struct Tables {
-  uint32_t* mask;   // [E][2] tokens of each expert
+  unsigned long long* mask;   // [E] tokens of each expert
   int* first;       // [E + 1] first pair of each expert
   int* act;         // [E] active experts, ascending
   float* l;         // [P] chosen logits by pair (token * k + slot)
   float* w;         // [P] weights by pair
   uint16_t* id;     // [P] expert by pair
   uint16_t* pos;    // [P] place of a pair
-  uint16_t* tok;    // [P] token at each place
 };
 __host__ __device__ inline int tables_bytes(int E, int P) {
-  return ((4 * E + 1 + 2 * P) * 4 + 3 * P * 2 + 15) & ~15;
+  return ((4 * E + 1 + 2 * P) * 4 + 2 * P * 2 + 15) & ~15;
 }
 __device__ __forceinline__ Tables tables_at(unsigned char* p, int E, int P) {
   Tables t;
-  t.mask = reinterpret_cast<uint32_t*>(p);
-  t.first = reinterpret_cast<int*>(t.mask + 2 * E);
+  t.mask = reinterpret_cast<unsigned long long*>(p);
+  t.first = reinterpret_cast<int*>(t.mask + E);
   t.act = t.first + E + 1;
   t.l = reinterpret_cast<float*>(t.act + E);
   t.w = t.l + P;
   t.id = reinterpret_cast<uint16_t*>(t.w + P);
   t.pos = t.id + P;
-  t.tok = t.pos + P;
   return t;
 }
 
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&bars->tmem, tcols);
     tmem_relinquish();
   }
-  for (int e = threadIdx.x; e < 2 * m.E; e += kThreads) t.mask[e] = 0;
+  for (int e = threadIdx.x; e < m.E; e += kThreads) t.mask[e] = 0;
   grid_dep_wait();
   grid_dep_launch();
 
@@ -250,23 +250,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ---------------- the routing ----------------
-  if (m.E <= 128 && m.T * m.E * m.E <= 1 << 17) {
-    // Small: every logit's rank among its token's by comparing it with them
-    // all (one token of 128 experts: 0.3 us against 1.6 of k rounds of a warp;
-    // 64 of 64: 2 against 5), through the memory of the stages.
-    uint32_t* key = reinterpret_cast<uint32_t*>(smem);
-    const int ld = (m.E + 3) & ~3;   // (past the last expert: 0, below every key)
-    if (ld == m.E) {   // whole rows of 16 bytes
-      for (int i = threadIdx.x; i < m.T * ld / 4; i += kThreads) {
-        const float4 l = __ldcg(reinterpret_cast<const float4*>(m.logits) + i);
-        reinterpret_cast<uint4*>(key)[i] = make_uint4(moe_key(l.x), moe_key(l.y), moe_key(l.z), moe_key(l.w));
-      }
-    } else {
+  const int ld = (m.E + 3) & ~3;   // (past the last expert: 0, below every key)
+  const int items = (m.T * ld + kThreads - 1) / kThreads;
+  if (items * ld <= 24 * m.k + 40) {
+    // Every logit's rank by comparing it with its token's, a thread to a logit:
+    // about 10 instructions a pair of logits for each of a thread's items, where
+    // the rounds below take 240 a choice.  From the logits to the counts, 2 us of
+    // other work included: 55 tokens of 11 experts, 5 choices, 3.3 us, and by
+    // rounds 6.1; 49 of 38 experts, 5 choices, 6.2 by ranks, which is what the
+    // rounds take there.
+    uint32_t* key = reinterpret_cast<uint32_t*>(smem);   // (the stages' memory)
 #pragma unroll 4
-      for (int i = threadIdx.x; i < m.T * ld; i += kThreads) {
-        const int q = i / ld, e = i - q * ld;
-        key[i] = e < m.E ? moe_key(__ldcg(m.logits + (long long)q * m.E + e)) : 0u;
-      }
+    for (int i = threadIdx.x; i < m.T * ld; i += kThreads) {
+      const int q = i / ld, e = i - q * ld;
+      key[i] = e < m.E ? moe_key(__ldcg(m.logits + (long long)q * m.E + e)) : 0u;
     }
     __syncthreads();
     for (int i = threadIdx.x; i < m.T * ld; i += kThreads) {
@@ -285,41 +282,38 @@ __global__ void __launch_bounds__(kThreads, 1)
         t.l[q * m.k + rank] = moe_logit(mine);
       }
     }
+  } else if (m.E <= 128) {
+    // Rounds, up to four tokens of a warp side by side.
+    constexpr int kWarps = kThreads / 32;
+    uint32_t key[4][4];
+    MoeChoice c[4];
+#pragma unroll
+    for (int b = 0; b < 4; ++b) moe_keys<4>(m.logits, m.T, m.E, warp + b * kWarps, lane, key[b]);
+    moe_choose<4, 4>(key, m.k, lane, c);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int q = warp + b * kWarps;
+      if (q < m.T && lane < m.k) {
+        t.id[q * m.k + lane] = (uint16_t)c[b].expert;
+        t.l[q * m.k + lane] = c[b].logit;
+      }
+    }
   } else {
-    // Rounds, one warp to a token; up to 128 experts the logits of a warp's four
-    // tokens are read at once.
-    for (int q0 = warp; q0 < m.T; q0 += 4 * (kThreads / 32)) {
-      if (m.E <= 128) {
-        uint32_t key[4][4];
-#pragma unroll
-        for (int b = 0; b < 4; ++b) moe_keys<4>(m.logits, m.T, m.E, q0 + b * (kThreads / 32), lane, key[b]);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-          const int q = q0 + b * (kThreads / 32);
-          if (q >= m.T) break;
-          const MoeChoice c = moe_choose<4>(key[b], m.k, lane);
-          if (lane < m.k) {
-            t.id[q * m.k + lane] = (uint16_t)c.expert;
-            t.l[q * m.k + lane] = c.logit;
-          }
-        }
-      } else {
-        for (int q = q0; q < m.T && q < q0 + 4 * (kThreads / 32); q += kThreads / 32) {
-          uint32_t key[kMoeMaxExperts / 32];
-          moe_keys<kMoeMaxExperts / 32>(m.logits, m.T, m.E, q, lane, key);
-          const MoeChoice c = moe_choose<kMoeMaxExperts / 32>(key, m.k, lane);
-          if (lane < m.k) {
-            t.id[q * m.k + lane] = (uint16_t)c.expert;
-            t.l[q * m.k + lane] = c.logit;
-          }
-        }
+    for (int q = warp; q < m.T; q += kThreads / 32) {
+      uint32_t key[1][kMoeMaxExperts / 32];
+      MoeChoice c[1];
+      moe_keys<kMoeMaxExperts / 32>(m.logits, m.T, m.E, q, lane, key[0]);
+      moe_choose<kMoeMaxExperts / 32, 1>(key, m.k, lane, c);
+      if (lane < m.k) {
+        t.id[q * m.k + lane] = (uint16_t)c[0].expert;
+        t.l[q * m.k + lane] = c[0].logit;
       }
     }
   }
   __syncthreads();
   for (int p = threadIdx.x; p < P; p += kThreads) {
     const int q = p / m.k, e = t.id[p];
-    atomicOr(&t.mask[2 * e + (q >> 5)], 1u << (q & 31));
+    atomicOr(&t.mask[e], 1ull << q);
   }
   __syncthreads();
   if (warp == 0) {
@@ -327,8 +321,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // takes a run of experts.
     const int per = (m.E + 31) / 32, e0 = lane * per, e1 = min(m.E, e0 + per);
     int c = 0, on = 0, most = 0;
+#pragma unroll 4
     for (int e = e0; e < e1; ++e) {
-      const int n = __popc(t.mask[2 * e]) + __popc(t.mask[2 * e + 1]);
+      const int n = __popcll(t.mask[e]);
       c += n;
       on += n > 0;
       most = max(most, n);
@@ -341,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     int at = (s & 0xFFFF) - c, na = (s >> 16) - on;
     for (int e = e0; e < e1; ++e) {
-      const int n = __popc(t.mask[2 * e]) + __popc(t.mask[2 * e + 1]);
+      const int n = __popcll(t.mask[e]);
       t.first[e] = at;
       at += n;
       if (n > 0) t.act[na++] = e;
@@ -352,14 +347,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       bars->active = na;
       bars->most = most;
     }
-  }
-  __syncthreads();
-  for (int p = threadIdx.x; p < P; p += kThreads) {
-    const int e = t.id[p], q = p / m.k;
-    const uint64_t mask = ((uint64_t)t.mask[2 * e + 1] << 32) | t.mask[2 * e];
-    const int at = t.first[e] + __popcll(mask & ((1ull << q) - 1ull));
-    t.pos[p] = (uint16_t)at;
-    t.tok[at] = (uint16_t)q;
   }
   fence_proxy_async_smem();  // (the stages' memory held keys until here)
   tc_fence_before();
@@ -410,8 +397,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * eights * 1024u : (uint32_t)SL * quads * 512u);
       // Lane j gathers tokens 4 j .. 4 j + 3 of the expert (rows past its last: zeros).
       int y[4];
+      if (!q.down) {
+        const unsigned long long mask = t.mask[q.e];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[i] = !q.down && 4 * lane + i < q.n ? t.tok[q.p0 + 4 * lane + i] : m.T;
+        for (int i = 0; i < 2; ++i) {
+          const int tk = lane + 32 * i;
+          if (mask >> tk & 1) bars->tok[__popcll(mask & ((1ull << tk) - 1ull))] = (unsigned char)tk;
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[i] = 4 * lane + i < q.n ? bars->tok[4 * lane + i] : m.T;
+        __syncwarp();
+      }
       auto weights = [&](int ks, Ring r) -> bool {
         const bool wok = wait_or_abort(&bars->empty[r.slot], r.phase ^ 1u, limit, abort_flag, g.status);
         if (!__all_sync(0xffffffffu, wok)) return false;
@@ -554,15 +551,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncwarp();
     if (lane == 0) mbar_wait(&bars->fin, 0, kDefaultSpin, nullptr);
   } else if (warp >= kEpi0 + 4) {
-    // ---------------- routing weights, wanted only at the end ----------------
+    // ---------------- weights and places of the pairs, wanted only at the end ----------------
     for (int q = warp - kEpi0 - 4; q < m.T; q += kHelpers) {
       const float all = m.normalize ? -1.0f : moe_sum(m.logits + (long long)q * m.E, m.E, t.l[q * m.k], lane);
       const int p = q * m.k + lane;
       if (lane < m.k) {
         const float w = moe_weight(t.l + q * m.k, m.k, lane, all);
+        const int e = t.id[p];
         t.w[p] = w;
+        t.pos[p] = (uint16_t)(t.first[e] + __popcll(t.mask[e] & ((1ull << q) - 1ull)));
         if (blockIdx.x == 0) {
-          m.experts[p] = t.id[p];
+          m.experts[p] = e;
           m.weights[p] = w;
         }
       }

@@ -16,48 +16,68 @@ __device__ __forceinline__ float moe_logit(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
-// The k experts of one token and their logits, by one warp; lane l holds the
-// keys of experts l, l + 32, ..., E <= 32 N (0: no such expert).  Each round takes the largest
-// key, the lowest expert among equals: every lane keeps its own best, and the
-// lane that held the winner finds its next.  Lane j ends with choice j.
-struct MoeChoice {
-  int expert;
-  float logit;
-};
+// The keys of token q for moe_choose: lane l holds experts l, l + 32, ..., E <=
+// 32 N (0: no such expert, or no such token).
 template <int N>
 __device__ __forceinline__ void moe_keys(const float* logits, int T, int E, int q, int lane, uint32_t (&key)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i)
     key[i] = q < T && lane + 32 * i < E ? moe_key(__ldcg(logits + (long long)q * E + lane + 32 * i)) : 0u;
 }
-template <int N>
-__device__ __forceinline__ MoeChoice moe_choose(const uint32_t (&key)[N], int k, int lane) {
-  unsigned used = 0;
-  uint32_t best = 0, mine = 0;
-  int at = 0, choice = 0;
-  auto next = [&] {
-    best = 0;
+
+// The k experts of B tokens and their logits, by one warp; lane j ends with
+// choice j of each.  A round takes the largest key, the lowest expert among
+// equals: every lane keeps its own best, and the lane that held the winner
+// finds its next.  The tokens' rounds run side by side, as each is a chain of
+// exchanges that mostly waits.
+struct MoeChoice {
+  int expert;
+  float logit;
+};
+template <int N, int B>
+__device__ __forceinline__ void moe_choose(const uint32_t (&key)[B][N], int k, int lane, MoeChoice (&choice)[B]) {
+  unsigned used[B];
+  uint32_t best[B], mine[B];
+  int at[B];
+  auto next = [&](int b) {
+    best[b] = 0;
 #pragma unroll
     for (int i = N - 1; i >= 0; --i)
-      if (!(used >> i & 1) && key[i] != 0 && key[i] >= best) {
-        best = key[i];
-        at = i;
+      if (!(used[b] >> i & 1) && key[b][i] != 0 && key[b][i] >= best[b]) {
+        best[b] = key[b][i];
+        at[b] = i;
       }
   };
-  next();
+#pragma unroll
+  for (int b = 0; b < B; ++b) {
+    used[b] = mine[b] = 0;
+    at[b] = 0;
+    choice[b].expert = 0;
+    next(b);
+  }
+#pragma unroll 1
   for (int j = 0; j < k; ++j) {
-    const uint32_t high = __reduce_max_sync(0xffffffffu, best);
-    const int e = (int)__reduce_min_sync(0xffffffffu, best == high ? (unsigned)(lane + 32 * at) : 0x7FFFu);
-    if (lane == (e & 31)) {
-      used |= 1u << (e >> 5);
-      next();
-    }
-    if (lane == j) {
-      mine = high;
-      choice = e;
+    uint32_t high[B];
+    int e[B];
+#pragma unroll
+    for (int b = 0; b < B; ++b) high[b] = __reduce_max_sync(0xffffffffu, best[b]);
+#pragma unroll
+    for (int b = 0; b < B; ++b)
+      e[b] = (int)__reduce_min_sync(0xffffffffu, best[b] == high[b] ? (unsigned)(lane + 32 * at[b]) : 0x7FFFu);
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      if (lane == (e[b] & 31)) {
+        used[b] |= 1u << (e[b] >> 5);
+        next(b);
+      }
+      if (lane == j) {
+        mine[b] = high[b];
+        choice[b].expert = e[b];
+      }
     }
   }
-  return {choice, moe_logit(mine)};
+#pragma unroll
+  for (int b = 0; b < B; ++b) choice[b].logit = moe_logit(mine[b]);
 }
 
 // Sum over all experts of exp(logit - top), by one warp.
