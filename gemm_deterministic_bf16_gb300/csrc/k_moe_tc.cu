@@ -26,9 +26,16 @@
 // on H and I alone, and the parts are added in order.
 //
 // The work is the weights' bytes: each active expert's are read once, by TMA
-// boxes of 64 K (128-byte swizzle) into a ring of stages of 32 KB of weights,
-// and the tokens' rows by row gathers (x) or row boxes (h: the pairs of an
-// expert are neighbours).  h goes to the down projection as two terms, its
+// boxes of 64 K (128-byte swizzle) into a ring of stages of 32 KB of weights.
+// A gate/up unit multiplies them with the rows of all tokens, one box a slice,
+// and leaves the columns of other experts' tokens aside: a row gather of the
+// expert's own tokens holds the TMA unit for some 40 ns per four rows (64
+// tokens of 2 experts, H = 4096, I = 1024: 75 us gathered, 39 so; 55 of 11
+// experts: 74 and 59; 64 of 64 experts, 6 choices, 6.5 tokens an expert on
+// average: 371 and 369), and the MMA's time does not depend on its columns up
+// to 32.  A down unit's pairs are neighbours in h, and one box of 8, 16, 32 or
+// 64 rows takes them; the rows past the unit's are other units' and are not
+// used, whatever they hold.  h goes to the down projection as two terms, its
 // rounding to the stored type and the rounding of what that left (16 bits of
 // BF16, 22 of FP16), both multiplied into the same accumulator: with one term
 // the rounding of h alone doubles the variance of out's error (1.41 times the
@@ -72,12 +79,11 @@ struct Bars {
   int unit[kUnits];  // claimed units; past the last: no more
   int active;   // experts with tokens
   int most;     // most tokens of one expert
-  unsigned char tok[kMoeMaxTokens];  // the loading warp's: the current unit's tokens
 };
 
 struct Args {
   MoeArgs m;
-  int cols;          // most columns of a unit's sums: twice T rounded up to 8
+  int cols;          // most columns of a unit's sums
   int ring;          // bytes for stages
   int tb;            // down tiles of an expert
   int parts, kpart;  // parts of a down tile's K, stages of a part
@@ -107,16 +113,6 @@ __device__ __forceinline__ void tma_load_3d_hint(void* dst, const void* tmap, in
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
       "%4}], [%5], %6;" ::"r"(smem_u32(dst)),
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar)), "l"(policy)
-      : "memory");
-}
-// Four rows y0 .. y3 of a map whose box is one row high, to four consecutive
-// rows of shared memory; rows past the tensor's end read zeros.
-__device__ __forceinline__ void tma_gather4(void* dst, const void* tmap, int x, int y0, int y1, int y2, int y3,
-                                            uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cta.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, "
-      "%5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(y0), "r"(y1), "r"(y2), "r"(y3), "r"(smem_u32(bar))
       : "memory");
 }
 __device__ __forceinline__ int ld_acquire(const int* p) {
@@ -167,6 +163,9 @@ __device__ __forceinline__ Tables tables_at(unsigned char* p, int E, int P) {
   return t;
 }
 
+// Rows of h that a down unit of n pairs loads, by one box.
+__host__ __device__ inline int hrows(int n) { return n <= 8 ? 8 : n <= 16 ? 16 : n <= 32 ? 32 : 64; }
+
 struct Unit {
   bool down;
   int a, tile, part, e, p0, n;   // active index, tile of the expert, part of K, expert, first pair, pairs
@@ -195,7 +194,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     k_moe(const __grid_constant__ CUtensorMap mWg, const __grid_constant__ CUtensorMap mWu,
           const __grid_constant__ CUtensorMap mWg32, const __grid_constant__ CUtensorMap mWu32,
           const __grid_constant__ CUtensorMap mWd, const __grid_constant__ CUtensorMap mX,
-          const __grid_constant__ CUtensorMap mH, const __grid_constant__ Args g) {
+          const __grid_constant__ CUtensorMap mH8, const __grid_constant__ CUtensorMap mH16,
+          const __grid_constant__ CUtensorMap mH32, const __grid_constant__ CUtensorMap mH64,
+          const __grid_constant__ Args g) {
   using El = typename Io<DT>::E;
   extern __shared__ unsigned char raw[];
   unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -230,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefetch_tmap(&mWu);
     prefetch_tmap(&mWd);
     prefetch_tmap(&mX);
-    prefetch_tmap(&mH);
+    prefetch_tmap(&mH8);
   }
   const uint32_t tcols = g.cols <= 16 ? 32 : g.cols <= 32 ? 64 : g.cols <= 64 ? 128 : 256;  // two units' sums
   if (warp == 1) {
@@ -356,18 +357,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = bars->tmem;
   const int active = bars->active;
   // Rows of Wg and of Wu in a gate/up unit, and the units of an expert.  An MMA
-  // costs about 75 cycles whatever its columns, so half-filled ones halve what
-  // a CTA can take in, and pay only where half the CTAs would have no unit (one
-  // token of 2 experts, H = 4096, I = 1024: 27.7 us with 64 rows, 25.3 with 32;
-  // 55 of 11, 154 units of 64 rows: 68 us, and 81 with 32).
-  const bool few = 2 * active * (int)((m.I + 63) / 64) <= (int)gridDim.x;
+  // costs about 75 cycles whatever its columns (up to 32), so half-filled ones
+  // halve what a CTA can take in, and pay where units of 64 rows fill the grid
+  // badly: at most half of it (one token of 2 experts, H = 4096, I = 1024: 27.7
+  // us with 64 rows, 25.3 with 32), or once and at most half of it again, with
+  // rows long enough (7 tokens of 16 experts, H = 4096, I = 1416: 62.3 and 59.4;
+  // 32 of 8, 4 choices, H = 7168, I = 1248: 95 and 86; H = 1024: even).
+  // Elsewhere they cost 2 to 16 % (54 of 78, 663 units: 43.9 and 51.1).
+  const int wide = active * (int)((m.I + 63) / 64), grid = (int)gridDim.x;
+  const bool few = 2 * wide <= grid || (wide > grid && 2 * wide <= 3 * grid && m.H >= 2048);
   const int R = few ? 32 : 64, ta = (int)((m.I + R - 1) / R);
   // A stage: 32 KB of weights as slices of 64 K, then a token tile for each
-  // slice: of x (rows in whole sixteens), or the first terms of h and then the
-  // second (each in whole eights); as this call's largest expert needs them.
-  // With up to eight tokens an expert, six stages fit.
+  // slice: of x (all tokens, in whole sixteens), or the first terms of h and
+  // then the second, as this call's largest expert needs them.  With up to 16
+  // tokens, eight of an expert, six stages fit.
   const int SL = 128 / R;   // slices of a gate/up stage; a down unit's has two
-  const int xtile = (bars->most + 15) / 16 * 2048, htile = (bars->most + 7) / 8 * 2048;
+  const int xtile = (m.T + 15) / 16 * 2048, htile = 256 * hrows(bars->most);
   const int stage_bytes = kWeightBytes + max(SL * xtile, 2 * htile);
   const int NS = min(kMaxStages, g.ring / stage_bytes);
   const int units = bars->go ? active * (ta + g.tb * g.parts) : 0;
@@ -393,22 +398,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       ru.next(kUnits);
       if (u >= units) break;
       const Unit q = unit_at(u, g, t, active, ta);
-      const int k0 = q.part * g.kpart, nk = q.down ? min(g.kpart, kb - k0) : ka, quads = (q.n + 3) / 4, eights = (q.n + 7) / 8;
-      const uint32_t bytes = (uint32_t)kWeightBytes + (q.down ? 4u * eights * 1024u : (uint32_t)SL * quads * 512u);
-      // Lane j gathers tokens 4 j .. 4 j + 3 of the expert (rows past its last: zeros).
-      int y[4];
-      if (!q.down) {
-        const unsigned long long mask = t.mask[q.e];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int tk = lane + 32 * i;
-          if (mask >> tk & 1) bars->tok[__popcll(mask & ((1ull << tk) - 1ull))] = (unsigned char)tk;
-        }
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = 4 * lane + i < q.n ? bars->tok[4 * lane + i] : m.T;
-        __syncwarp();
-      }
+      const int k0 = q.part * g.kpart, nk = q.down ? min(g.kpart, kb - k0) : ka, rows = hrows(q.n);
+      const uint32_t bytes = (uint32_t)kWeightBytes + (uint32_t)(q.down ? 512 * rows : SL * xtile);
       auto weights = [&](int ks, Ring r) -> bool {
         const bool wok = wait_or_abort(&bars->empty[r.slot], r.phase ^ 1u, limit, abort_flag, g.status);
         if (!__all_sync(0xffffffffu, wok)) return false;
@@ -441,15 +432,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         unsigned char* d = stage(r.slot) + kWeightBytes;
         uint64_t* bar = &bars->full[r.slot];
         if (q.down) {
-          if (lane < 4 * eights) {
-            // (the second terms' rows follow the first terms' of this unit)
-            const int half = lane & 1, term = lane >> 1 & 1, b = lane >> 2;
-            tma_load_2d(d + half * htile + (term * eights + b) * 1024, &mH, (k0 + ks) * KS + half * 64,
-                        term * P + q.p0 + b * 8, bar);
-          }
-        } else if (lane < quads) {
-          for (int sl = 0; sl < SL; ++sl)
-            tma_gather4(d + sl * xtile + lane * 512, &mX, (ks * SL + sl) * 64, y[0], y[1], y[2], y[3], bar);
+          // K half, term: the second terms' rows follow the first terms' of this unit.
+          if (lane < 4)
+            tma_load_2d(d + (lane & 1) * htile + (lane >> 1) * rows * 128,
+                        rows == 8 ? &mH8 : rows == 16 ? &mH16 : rows == 32 ? &mH32 : &mH64,
+                        (k0 + ks) * KS + (lane & 1) * 64, (lane >> 1) * P + q.p0, bar);
+        } else if (lane < SL) {
+          tma_load_2d(d + lane * xtile, &mX, (ks * SL + lane) * 64, 0, bar);
         }
         __syncwarp();
       };
@@ -518,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u >= units) break;
       const Unit q = unit_at(u, g, t, active, ta);
       const int nk = q.down ? min(g.kpart, kb - q.part * g.kpart) : ka;
-      const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, q.down ? (q.n + 7) / 8 * 16 : (q.n + 15) / 16 * 16);
+      const uint32_t idesc = idesc_f16(DT == DETFFN_BF16, 128, q.down ? 2 * hrows(q.n) : (m.T + 15) / 16 * 16);
       const uint32_t acc = tmem + (uint32_t)(rb.slot * g.cols);
       wok = wait_or_abort(&bars->acce[rb.slot], rb.phase ^ 1u, limit, abort_flag, g.status);
       ok = __all_sync(0xffffffffu, wok) != 0;
@@ -586,18 +575,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!epi_all(aok) || u >= units) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * g.cols);
-      for (int c0 = 0; c0 < q.n; c0 += 8) {
+      // The columns that hold pairs of this expert.
+      const unsigned long long cols = q.down ? ~0ull >> (64 - q.n) : t.mask[q.e];
+      for (int c0 = 0; c0 < 64 && cols >> c0; c0 += 8) {
+        const unsigned here = (unsigned)(cols >> c0) & 0xFFu;
+        if (here == 0u) continue;
         uint32_t v[8];
         tmem_ld8(taddr + (uint32_t)c0, v);
         if (q.down) {
           uint32_t v2[8];   // the second terms' part
-          tmem_ld8(taddr + (uint32_t)((q.n + 7) / 8 * 8 + c0), v2);
+          tmem_ld8(taddr + (uint32_t)(hrows(q.n) + c0), v2);
           tmem_wait_ld();
           const long long r = q.tile * 128ll + row;
           if (r < m.H) {
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              if (c0 + i < q.n)
+              if (here >> i & 1)
                 g.y[((long long)q.part * P + q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]) + __uint_as_float(v2[i]);
           }
         } else {
@@ -612,13 +605,26 @@ __global__ void __launch_bounds__(kThreads, 1)
           const long long r = q.tile * (long long)R + f;
           if (r < m.I) {
 #pragma unroll 1
-            for (int i = et / R; i < 8 && c0 + i < q.n; i += 128 / R) {
-              const float gt = xch[i * 128 + f], hv = __fdividef(gt, 1.0f + __expf(-gt)) * xch[i * 128 + R + f];
-              El* at = static_cast<El*>(m.h) + (long long)(q.p0 + c0 + i) * m.I + r;
-              Io<DT>::st(at, hv);
-              const float left = hv - Io<DT>::round(hv);
-              // (Beyond the stored type's range the first term is an infinity and stays one.)
-              Io<DT>::st(at + P * m.I, fabsf(left) <= 3.4e38f ? left : 0.0f);
+            for (int i0 = et / R; i0 < 8; i0 += 256 / R) {
+              float gt[2], hv[2];
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const float* at = xch + (i0 + b * (128 / R)) * 128 + f;
+                gt[b] = at[0];
+                hv[b] = at[R];
+              }
+#pragma unroll
+              for (int b = 0; b < 2; ++b) hv[b] *= __fdividef(gt[b], 1.0f + __expf(-gt[b]));
+#pragma unroll
+              for (int b = 0; b < 2; ++b) {
+                const int i = i0 + b * (128 / R);
+                if (!(here >> i & 1)) continue;
+                El* at = static_cast<El*>(m.h) + (q.p0 + __popcll(cols & ((1ull << (c0 + i)) - 1ull))) * m.I + r;
+                Io<DT>::st(at, hv[b]);
+                const float left = hv[b] - Io<DT>::round(hv[b]);
+                // (Beyond the stored type's range the first term is an infinity and stays one.)
+                Io<DT>::st(at + P * m.I, fabsf(left) <= 3.4e38f ? left : 0.0f);
+              }
             }
           }
           epi_sync();
@@ -727,18 +733,27 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   });
   if (setup != cudaSuccess) return setup;
   const bool f16 = DT == DETFFN_F16;
-  CUtensorMap mWg, mWu, mWg32, mWu32, mWd, mX, mH;
+  CUtensorMap mWg, mWu, mWg32, mWu32, mWd, mX, mH[4];
   const long long dg[3] = {m.H, m.I, m.E}, dd[3] = {m.I, m.H, m.E}, dx[2] = {m.H, m.T}, dh[2] = {m.I, 2ll * m.T * m.k};
-  const int bw[3] = {64, 64, 1}, bw32[3] = {64, 32, 1}, bx[2] = {64, 1}, bh[2] = {64, 8};
+  const int bw[3] = {64, 64, 1}, bw32[3] = {64, 32, 1}, bx[2] = {64, (m.T + 15) / 16 * 16};
   if (!tc_make_map_nd(&mWg, f16, m.Wg, 3, dg, bw) || !tc_make_map_nd(&mWu, f16, m.Wu, 3, dg, bw) ||
       !tc_make_map_nd(&mWg32, f16, m.Wg, 3, dg, bw32) || !tc_make_map_nd(&mWu32, f16, m.Wu, 3, dg, bw32) ||
-      !tc_make_map_nd(&mWd, f16, m.Wd, 3, dd, bw) || !tc_make_map_nd(&mX, f16, m.x, 2, dx, bx) ||
-      !tc_make_map_nd(&mH, f16, m.h, 2, dh, bh))
+      !tc_make_map_nd(&mWd, f16, m.Wd, 3, dd, bw) || !tc_make_map_nd(&mX, f16, m.x, 2, dx, bx))
     return cudaErrorInvalidValue;
+  // h by 8, 16, 32 or 64 rows: those that an expert of this call can take.
+  for (int i = 0; i < 4; ++i) {
+    const int bh[2] = {64, 8 << i};
+    if (i > 0 && hrows(m.T) < 8 << i)
+      mH[i] = mH[0];
+    else if (!tc_make_map_nd(&mH[i], f16, m.h, 2, dh, bh))
+      return cudaErrorInvalidValue;
+  }
   Args g{};
   g.m = m;
-  g.cols = 2 * ((m.T + 7) / 8 * 8);
-  const int stage = kWeightBytes + 4 * ((m.T + 15) / 16 * 2048);  // the largest
+
+  g.cols = 2 * hrows(m.T);
+  const int xmost = 4 * ((m.T + 15) / 16 * 2048), hmost = 512 * hrows(m.T);
+  const int stage = kWeightBytes + (xmost > hmost ? xmost : hmost);  // the largest
   const int rest = 1024 + (int)((sizeof(Bars) + 127) & ~127) + kXch + tables_bytes(m.E, m.T * m.k);
   g.ring = (kSmemMax - rest) & ~1023;
   if (g.ring < 2 * stage) return cudaErrorInvalidConfiguration;
@@ -755,7 +770,8 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   if (e != cudaSuccess) return e;
   const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * ((m.I + 31) / 32 + g.tb * g.parts);
   const int grid = (int)(most < sm_count ? most : sm_count);
-  return launch_dependent(k_moe<DT>, dim3(grid), kThreads, kSmemMax, st, mWg, mWu, mWg32, mWu32, mWd, mX, mH, g);
+  return launch_dependent(k_moe<DT>, dim3(grid), kThreads, kSmemMax, st, mWg, mWu, mWg32, mWu32, mWd, mX, mH[0], mH[1],
+                          mH[2], mH[3], g);
 }
 
 }  // namespace
