@@ -106,64 +106,73 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
   return top < 0x7F800000u ? fminf(__fmul_rn(__uint_as_float(top), kInv127), kTopScale) : __int_as_float(0x7fc00000);
 }
 
-// Rows of whole 8-element vectors on 16-byte boundaries: eight lanes take one
-// block of 64 features, of gate and of up, lane l features 8 l .. 8 l + 7.
-// FLAT: no block is short (I a multiple of 64), so blocks follow one another
-// and nothing is divided.
+// Rows of whole 8-element vectors on 16-byte boundaries: four lanes take one
+// block of 64 features, of gate and of up, lane l features 8 l .. 8 l + 7 and
+// 32 more than those.  FLAT: no block is short (I a multiple of 64), so blocks
+// follow one another and nothing is divided.
 template <int DT, bool FLAT>
 __global__ void __launch_bounds__(kThreads) k_pack_vec(const __grid_constant__ CkptArgs a, uint32_t blocks, Div nb) {
   grid_dep_wait();
   grid_dep_launch();
   using E = typename Io<DT>::E;
-  const int l = threadIdx.x & 7;
-  const uint32_t step = gridDim.x * (kThreads / 8);
+  const int l = threadIdx.x & 3;
+  const uint32_t step = gridDim.x * (kThreads / 4);
   // Whole warps stay in the loop: the shuffles need all their lanes.
-  for (uint32_t b0 = (blockIdx.x * kThreads + (threadIdx.x & ~31u)) / 8; b0 < blocks; b0 += step) {
-    const uint32_t b = min(b0 + ((threadIdx.x & 31) >> 3), blocks - 1);   // (past the last: the last again)
+  for (uint32_t b0 = (blockIdx.x * kThreads + (threadIdx.x & ~31u)) / 4; b0 < blocks; b0 += step) {
+    const uint32_t b = min(b0 + ((threadIdx.x & 31) >> 2), blocks - 1);   // (past the last: the last again)
     long long at = 64ll * b + 8 * l;
-    bool on = true;
+    bool on[2] = {true, true};
     if (!FLAT) {
       const uint32_t m = quotient(b, nb), c = (b - m * nb.d) * kCkptBlock + 8 * l;
       at = (long long)m * a.I + c;
-      on = c < a.I;
+      on[0] = c < a.I;
+      on[1] = c + 32 < a.I;
     }
-    float v[2][8];
-    uint32_t top[2];
+    // Values 2 k + i: vector i of gate (k = 0) or up (1).
+    float v[4][8];
+    uint32_t top[2] = {0, 0};
+    if constexpr (DT == DETFFN_F32) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const E* p = static_cast<const E*>(k ? a.up : a.gate) + at;
-      if constexpr (DT == DETFFN_F32) {
-        if (on) {
-          Io<DT>::ld8(p, v[k]);
+      for (int i = 0; i < 4; ++i) {
+        const E* p = static_cast<const E*>(i >> 1 ? a.up : a.gate) + at + 32 * (i & 1);
+        if (on[i & 1]) {
+          Io<DT>::ld8(p, v[i]);
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[k][j] = 0.0f;
+          for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
         }
-        top[k] = 0;
+      }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top[k] = max(top[k], mag_bits(v[k][j]));
-      } else {
-        // The largest of 16-bit magnitudes, two to an instruction.
-        const uint4 q = on ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-        uint32_t t = 0;
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top[i >> 1] = max(top[i >> 1], mag_bits(v[i][j]));
+    } else {
+      uint4 q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const E* p = static_cast<const E*>(i >> 1 ? a.up : a.gate) + at + 32 * (i & 1);
+        q[i] = on[i & 1] ? *reinterpret_cast<const uint4*>(p) : make_uint4(0, 0, 0, 0);
+      }
+      // The largest of 16-bit magnitudes, two to an instruction.
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float2 f = Io<DT>::two(w[j]);
-          v[k][2 * j] = f.x;
-          v[k][2 * j + 1] = f.y;
-          t = __vmaxu2(t, w[j] & 0x7FFF7FFFu);
+          v[i][2 * j] = f.x;
+          v[i][2 * j + 1] = f.y;
+          top[i >> 1] = __vmaxu2(top[i >> 1], w[j] & 0x7FFF7FFFu);
         }
-        t = max(t & 0xFFFFu, t >> 16);
-        top[k] = mag_bits(Io<DT>::two(t).x);
       }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) top[k] = mag_bits(Io<DT>::two(max(top[k] & 0xFFFFu, top[k] >> 16)).x);
     }
     // Gate's and up's largest in one exchange less: lane bit 0 keeps one each.
     {
       const bool up = l & 1;
       uint32_t t = max(up ? top[1] : top[0], __shfl_xor_sync(0xffffffffu, up ? top[0] : top[1], 1));
       t = max(t, __shfl_xor_sync(0xffffffffu, t, 2));
-      t = max(t, __shfl_xor_sync(0xffffffffu, t, 4));
       const uint32_t o = __shfl_xor_sync(0xffffffffu, t, 1);
       top[0] = up ? o : t;
       top[1] = up ? t : o;
@@ -172,13 +181,16 @@ __global__ void __launch_bounds__(kThreads) k_pack_vec(const __grid_constant__ C
     for (int k = 0; k < 2; ++k) {
       const float s = scale_of(top[k]);
       if (l == 0) (k ? a.us : a.gs)[b] = s;
-      uint2 w = make_uint2(0, 0);
-      if (s > 0.0f) {
-        uint32_t q[8];
-        code_bits(v[k], s, q);
-        w = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        uint2 w = make_uint2(0, 0);
+        if (s > 0.0f) {
+          uint32_t q[8];
+          code_bits(v[2 * k + i], s, q);
+          w = make_uint2(pack4(q[0], q[1], q[2], q[3]), pack4(q[4], q[5], q[6], q[7]));
+        }
+        if (on[i]) *reinterpret_cast<uint2*>((k ? a.uq : a.gq) + at + 32 * i) = w;
       }
-      if (on) *reinterpret_cast<uint2*>((k ? a.uq : a.gq) + at) = w;
     }
   }
 }
@@ -422,7 +434,7 @@ cudaError_t pack(const CkptArgs& all, int sms, cudaStream_t st) {
   const bool vec = all.I % 8 == 0 && on16(all.gate) && on16(all.up) && on8(all.gq) && on8(all.uq);
   auto k = !vec ? k_pack_any<DT> : all.I % 64 ? k_pack_vec<DT, false> : k_pack_vec<DT, true>;
   return by_rows(all, [&](const CkptArgs& a) {
-    return launch_dependent(k, dim3(grid_for(a.M * nb * 8, sms)), kThreads, 0, st, a, (uint32_t)(a.M * nb),
+    return launch_dependent(k, dim3(grid_for(a.M * nb * (vec ? 4 : 8), sms)), kThreads, 0, st, a, (uint32_t)(a.M * nb),
                             div_by((uint32_t)nb));
   });
 }
