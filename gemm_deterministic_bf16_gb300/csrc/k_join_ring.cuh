@@ -35,92 +35,124 @@ struct RingPlan {
   const unsigned char* p[5] = {};
   long long step[5] = {};                // bytes between rows
   int row = 0;                           // bytes of a slot
+  int per = 0, rest = 0;                 // rows of every group, and how many groups have one more
   int C = 1, width = 0;                  // CTAs that share a row, and the features of each but the last
 };
-
-__device__ __forceinline__ void group_barrier(int group, int G) {
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(G) : "memory");
-}
 
 // Sums of N = 2 or 4 values over a group of G threads (whole warps, at most
 // 16), the same in every thread, in an order fixed by G.  Stage one halves the
 // values a lane carries with every exchange, so that lane l ends with the
-// warp's sum of value l % N; stage two adds the warps the same way.  `buf`:
+// warp's sum of value l % N; stage two adds the warps the same way, through
 // [2][16 N] floats.  One barrier; one warp alone: none but __syncwarp.
 template <int N>
-__device__ __forceinline__ void group_sums(float (&v)[N], float* buf, int& turn, int G, int group, int t) {
+struct GroupSums {
   static_assert(N == 2 || N == 4, "");
-  const int lane = t & 31;
-  const bool odd = lane & 1, high = lane & 2;
-  float x = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
-  if (N == 4) {
-    const float c = v[N - 2], d = v[N - 1];
-    const float y = (odd ? d : c) + __shfl_xor_sync(0xffffffffu, odd ? c : d, 1);
-    x = (high ? y : x) + __shfl_xor_sync(0xffffffffu, high ? x : y, 2);
+  float *put, *get;     // this thread's places, now in the first half
+  int other = 16 * N;   // the other half, from there
+  int warps, barrier, threads;
+  bool odd, high;
+  // `buf`: 32 N floats of the group.
+  __device__ __forceinline__ GroupSums(float* buf, int G, int group, int t) {
+    const int lane = t & 31;
+    put = buf + (t >> 5) * N + lane;
+    get = buf + lane;
+    warps = (G >> 5) * N - lane;   // 0 or less: no value for this lane
+    barrier = group + 1;
+    threads = G;
+    odd = lane & 1;
+    high = lane & 2;
   }
-#pragma unroll
-  for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  if (G > 32) {
-    float* b = buf + turn * (16 * N);
-    turn ^= 1;
-    if (lane < N) b[(t >> 5) * N + lane] = x;
-    group_barrier(group, G);
-    const int n = (G >> 5) * N;
-    x = lane < n ? b[lane] : 0.0f;
-    if (N == 4) x += lane + 32 < n ? b[lane + 32] : 0.0f;
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    float x = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
+    if (N == 4) {
+      const float c = v[N - 2], d = v[N - 1];
+      const float y = (odd ? d : c) + __shfl_xor_sync(0xffffffffu, odd ? c : d, 1);
+      x = (high ? y : x) + __shfl_xor_sync(0xffffffffu, high ? x : y, 2);
+    }
 #pragma unroll
     for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-  } else {
-    __syncwarp();
-  }
+    if (threads > 32) {
+      if ((int)(threadIdx.x & 31) < N) *put = x;
+      asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+      x = warps > 0 ? get[0] : 0.0f;
+      if (N == 4) x += warps > 32 ? get[32] : 0.0f;
+      put += other;
+      get += other;
+      other = -other;
 #pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, i);
-}
-
-// Where a group's rows live, and their arrival.
-struct Ring1 {
-  unsigned char* base;    // [S][row bytes]
-  uint64_t* full;         // [S]
-  int s = 0;
-  uint32_t phase = 0;
+      for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+    } else {
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, i);
+  }
 };
 
-// Issues the copies of features [col, col + width) of row m into slot s (one
-// thread).
-template <bool VEC, bool WIDE>
-__device__ __forceinline__ void ring_fill(const RingPlan& p, const Ring1& r, int s, long long m, int col, int width) {
-  unsigned char* d = r.base + (size_t)s * p.row;
-  if (VEC && !WIDE) {   // whole rows of whole pieces: a slot's bytes
-    mbar_arrive_expect_tx(&r.full[s], (uint32_t)p.row);
+// A group's ring of rows, in the order in which the group takes them.  Each
+// tensor of a row is one lane's, which keeps its source and issues its copy: one
+// thread for all took 170 instructions a row.
+struct Ring1 {
+  unsigned char *base, *at;        // [S][row bytes]; the slot of the next row to come
+  uint64_t* full;                  // [S]
+  int s = 0;                       // that slot
+  uint32_t phase = 0;
+  const unsigned char* src = nullptr;   // this lane's tensor: the next row to copy, from the CTA's first column on
+  long long step = 0;              // bytes from it to the group's next row
+  uint32_t off = 0, bytes = 0;     // where it lies in a slot; the bytes of its columns
+};
+// (Lanes t < p.n of the group's first warp copy.)
+__device__ __forceinline__ void ring_init(const RingPlan& p, Ring1& r, int t, long long first, long long step, int col, int width) {
 #pragma unroll
-    for (int i = 0; i < 5; ++i)
-      if (i < p.n) bulk_g2s(d + p.off[i], p.p[i] + m * p.step[i], (uint32_t)(width * p.es[i]), &r.full[s]);
-    return;
+  for (int i = 0; i < 5; ++i)
+    if (i == t && i < p.n) {
+      r.src = p.p[i] + first * p.step[i] + (long long)col * p.es[i];
+      r.step = step * p.step[i];
+      r.off = (uint32_t)p.off[i];
+      r.bytes = (uint32_t)(width * p.es[i]);
+    }
+  if (t == 0) {
+    for (int s = 0; s < p.S; ++s) mbar_init(&r.full[s], (uint32_t)p.n);
+    fence_mbar_init();
   }
-  uint32_t size[5], all = 0;
-#pragma unroll
-  for (int i = 0; i < 5; ++i)
-    if (i < p.n) {
-      size[i] = (uint32_t)(width * p.es[i]);
-      if (!VEC) size[i] = ((uint32_t)((uintptr_t)(p.p[i] + m * p.step[i] + col * p.es[i]) & 15) + size[i] + 15) & ~15u;
-      all += size[i];
-    }
-  mbar_arrive_expect_tx(&r.full[s], all);
-#pragma unroll
-  for (int i = 0; i < 5; ++i)
-    if (i < p.n) {
-      const uintptr_t at = (uintptr_t)(p.p[i] + m * p.step[i] + col * p.es[i]);
-      bulk_g2s(d + p.off[i], (const void*)(VEC ? at : at & ~(uintptr_t)15), size[i], &r.full[s]);
-    }
+}
+// Issues the copy of the next row of this lane's tensor into slot s, at `slot`.
+template <bool VEC>
+__device__ __forceinline__ void ring_fill(Ring1& r, int s, unsigned char* slot) {
+  const uintptr_t at = (uintptr_t)r.src;
+  const uint32_t size = VEC ? r.bytes : (((uint32_t)at & 15u) + r.bytes + 15u) & ~15u;
+  mbar_arrive_expect_tx(&r.full[s], size);
+  bulk_g2s(slot + r.off, (const void*)(VEC ? at : at & ~(uintptr_t)15), size, &r.full[s]);
+  r.src += r.step;
+}
+__device__ __forceinline__ void ring_next(const RingPlan& p, Ring1& r) {
+  r.at += p.row;
+  if (++r.s == p.S) {
+    r.s = 0;
+    r.at = r.base;
+    r.phase ^= 1u;
+  }
 }
 
-// Row m of tensor i in a slot, from feature col on.
+// Tensor i of a slot's row, which begins `off` bytes into the slot; rows that
+// are not whole pieces begin 16-byte piece and a remainder further, which the
+// address's low bits give: `low`, for the first row, and `step` more a row.
+struct Part {
+  uint32_t off, low, step;
+};
 template <bool VEC>
-__device__ __forceinline__ const unsigned char* ring_row(const RingPlan& p, const unsigned char* slot, int i, long long m,
-                                                         int col) {
-  if (VEC) return slot + p.off[i];
-  return slot + p.off[i] +
-         (((uint32_t)(uintptr_t)p.p[i] + (uint32_t)m * (uint32_t)p.step[i] + (uint32_t)(col * p.es[i])) & 15u);
+__device__ __forceinline__ Part part_of(const RingPlan& p, int i, long long first, long long step, int col) {
+  Part r = {(uint32_t)p.off[i], 0, 0};
+  if (!VEC) {
+    r.low = (uint32_t)(uintptr_t)p.p[i] + (uint32_t)first * (uint32_t)p.step[i] + (uint32_t)(col * p.es[i]);
+    r.step = (uint32_t)step * (uint32_t)p.step[i];
+  }
+  return r;
+}
+// The n-th row of the group.
+template <bool VEC>
+__device__ __forceinline__ const unsigned char* ring_row(const unsigned char* slot, const Part& p, uint32_t n) {
+  return slot + p.off + (VEC ? 0u : (p.low + n * p.step) & 15u);
 }
 
 // Waits for the row in the current slot.  Its copies were issued by this very
@@ -214,17 +246,16 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
 #pragma unroll
   for (int i = 0; i < V; ++i) k[i] = cols_of<VEC>(i, G, t, H);
   const long long first = (long long)blockIdx.x * p.R + group, step = (long long)gridDim.x * p.R;
-  Ring1 ring{smem + (size_t)group * p.S * p.row, full + group * p.S};
-  float* buf = sums + (G == 32 ? 0 : group * 64);
-  if (t == 0) {
-    for (int s = 0; s < p.S; ++s) mbar_init(&ring.full[s], 1);
-    fence_mbar_init();
-  }
+  unsigned char* base = smem + group * p.S * p.row;
+  Ring1 ring{base, base, full + group * p.S};
+  GroupSums<2> add(sums + (G == 32 ? 0 : group * 64), G, group, t);
+  ring_init(p, ring, t, first, step, 0, H);
+  __syncwarp();
   grid_dep_wait();
   grid_dep_launch();
-  if (t == 0)
-    for (int s = 0; s < p.S; ++s)
-      if (first + s * step < a.M) ring_fill<VEC, false>(p, ring, s, first + s * step, 0, H);
+  const int rows = p.per + (first < p.rest ? 1 : 0);   // of this group
+  if (t < p.n)
+    for (int s = 0; s < min(p.S, rows); ++s) ring_fill<VEC>(ring, s, base + s * p.row);
   float mix[V][8], pre[V][8];      // mix: scale * gate * w_post
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -237,64 +268,62 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
     for (int j = 0; j < 8; ++j) mix[i][j] *= a.scale * w[j];
   }
   const float inv = 1.0f / (float)H;
-  int turn = 0;
+  // The parts of a row: x, z, gate.
+  const Part px = part_of<VEC>(p, 0, first, step, 0), pz = part_of<VEC>(p, 1, first, step, 0), pg = part_of<VEC>(p, 2, first, step, 0);
   E* out = static_cast<E*>(const_cast<void*>(a.out.p)) + first * a.out.ld;
   E* y = static_cast<E*>(const_cast<void*>(a.y.p)) + first * a.y.ld;
   const long long out_step = step * a.out.ld, y_step = step * a.y.ld;
   __syncthreads();   // the barriers are initialised
-  // The sum over z of the row in slot `s`.
-  auto sum_z = [&](int s, long long m) {
+  // The sum over z of the n-th row, in the next slot.
+  auto sum_z = [&](int n) {
     float v = 0.0f;
+    if (!ring_wait(ring)) return __int_as_float(0x7fc00000);
     if (has_post) {
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        float n[8];
-        unit<DT, VEC>(ring_row<VEC>(p, ring.base + (size_t)s * p.row, 1, m, 0), k[i], n);
-        v += k[i].on ? dot8(n, n) : 0.0f;
+        float z[8];
+        unit<DT, VEC>(ring_row<VEC>(ring.at, pz, n), k[i], z);
+        v += k[i].on ? dot8(z, z) : 0.0f;
       }
     }
     return v;
   };
   float sz = 0.0f;
-  if (first < a.M) {
-    const bool came = ring_wait(ring);
-    float v[2] = {came ? sum_z(0, first) : __int_as_float(0x7fc00000), 0.0f};
-    group_sums<2>(v, buf, turn, G, group, t);
+  if (rows > 0) {
+    float v[2] = {sum_z(0), 0.0f};
+    add(v);
     sz = v[0];
   }
-  for (long long m = first; m < a.M; m += step, out += out_step, y += y_step) {
-    const unsigned char* row = ring.base + (size_t)ring.s * p.row;
+  for (int n = 0; n < rows; ++n, out += out_step, y += y_step) {
+    unsigned char* row = ring.at;
     const int slot = ring.s;
-    if (++ring.s == p.S) {
-      ring.s = 0;
-      ring.phase ^= 1u;
-    }
+    ring_next(p, ring);
     float v[2] = {0.0f, 0.0f};
-    if (m + step < a.M) v[0] = ring_wait(ring) ? sum_z(ring.s, m + step) : __int_as_float(0x7fc00000);
+    if (n + 1 < rows) v[0] = sum_z(n + 1);
     float r[V][8];
     const float b = has_post ? rsqrtf(sz * inv + a.eps) : 1.0f;
     float g1 = 0.0f;
-    if (by_row && !a.gate_cs) g1 = param<DT>(a.gate, a.pdtype, m * a.gate_rs);
+    if (by_row && !a.gate_cs) g1 = param<DT>(a.gate, a.pdtype, (first + n * step) * a.gate_rs);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      unit<DT, VEC>(ring_row<VEC>(p, row, 0, m, 0), k[i], r[i]);
+      unit<DT, VEC>(ring_row<VEC>(row, px, n), k[i], r[i]);
       if (has_z) {
-        float n[8];
-        unit<DT, VEC>(ring_row<VEC>(p, row, 1, m, 0), k[i], n);
+        float z[8];
+        unit<DT, VEC>(ring_row<VEC>(row, pz, n), k[i], z);
         if (by_row) {
           float g[8];
-          param_unit<DT, VEC>(a.gate_cs ? ring_row<VEC>(p, row, 2, m, 0) : nullptr, a.pdtype, k[i], g1, g);
+          param_unit<DT, VEC>(a.gate_cs ? ring_row<VEC>(row, pg, n) : nullptr, a.pdtype, k[i], g1, g);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) n[j] *= g[j];
+          for (int j = 0; j < 8; ++j) z[j] *= g[j];
         }
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = fmaf(b * n[j], mix[i][j], r[i][j]);
+        for (int j = 0; j < 8; ++j) r[i][j] = fmaf(b * z[j], mix[i][j], r[i][j]);
         put_unit<DT, VEC>(out, k[i], r[i]);
       }
       if (has_pre) v[1] += k[i].on ? dot8(r[i], r[i]) : 0.0f;
     }
-    group_sums<2>(v, buf, turn, G, group, t);
-    if (t == 0 && m + p.S * step < a.M) ring_fill<VEC, false>(p, ring, slot, m + p.S * step, 0, H);
+    add(v);
+    if (t < p.n && n + p.S < rows) ring_fill<VEC>(ring, slot, row);
     sz = v[0];
     if (has_pre) {
       const float q = rsqrtf(v[1] * inv + a.eps);
@@ -326,7 +355,7 @@ __device__ __forceinline__ void cluster_sums(float (&v)[N], float* buf, int& tur
       asm volatile(
           "{\n\t.reg .b32 a;\n\t"
           "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-          "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_u32(b + rank * 4 + i)),
+          "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_u32(b + rank * N + i)),
           "r"(threadIdx.x), "f"(v[i])
           : "memory");
   }
@@ -334,7 +363,7 @@ __device__ __forceinline__ void cluster_sums(float (&v)[N], float* buf, int& tur
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     v[i] = b[i];
-    for (int r = 1; r < C; ++r) v[i] += b[r * 4 + i];
+    for (int r = 1; r < C; ++r) v[i] += b[r * N + i];
   }
 }
 
@@ -342,11 +371,17 @@ __device__ __forceinline__ void cluster_sums(float (&v)[N], float* buf, int& tur
 // any) that is the same for every row.  WIDE: a cluster of CTAs shares each row
 // of more than 4096 features, a run of columns each, and the row's sums meet
 // in shared memory across it.
+//
+// With n = b z, D = dx and c = scale gate w_post, a row needs sum D c n, and
+// then dz = b D c - (sum D c n) b / H n.  The sums over tokens of dw_post and
+// of a gate that is the same for every row have the factors scale gate and
+// scale w_post of sum D n, so one accumulator serves both.  A row's r, dy and z
+// are converted once and stay in registers over the barrier of its first sums.
 template <int DT, bool PLAIN, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kRingMaxGroups * kRingMaxStages];
-  __shared__ float sums[8 * (128 + 64)];   // (groups of several warps: at most 8)
+  __shared__ float sums[8 * 128];   // (groups of several warps: at most 8)
   using E = typename Io<DT>::E;
   const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H;
   int rank = 0;
@@ -357,95 +392,93 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   const bool on = cs.on != 0;
   const long long set = blockIdx.x / (WIDE ? p.C : 1), sets = gridDim.x / (WIDE ? p.C : 1);
   const long long first = set * p.R + group, step = sets * p.R;
-  Ring1 ring{smem + (size_t)group * p.S * p.row, full + group * p.S};
-  float *buf = sums + (G == 32 ? 0 : group * 192), *buf2 = buf + 128;
-  if (t == 0) {
-    for (int s = 0; s < p.S; ++s) mbar_init(&ring.full[s], 1);
-    fence_mbar_init();
-  }
+  unsigned char* base = smem + group * p.S * p.row;
+  Ring1 ring{base, base, full + group * p.S};
+  GroupSums<4> add(sums + (G == 32 ? 0 : group * 128), G, group, t);
+  ring_init(p, ring, t, first, step, col, width);
+  __syncwarp();
   grid_dep_wait();
   grid_dep_launch();
-  if (t == 0)
-    for (int s = 0; s < p.S; ++s)
-      if (first + s * step < a.M) ring_fill<VEC, WIDE>(p, ring, s, first + s * step, col, width);
-  const bool has_z = PLAIN || a.z.p, has_post = PLAIN || a.w_post, has_pre = PLAIN || a.w_pre, has_dr = PLAIN || a.dr.p;
-  const bool feature = a.dgate && a.gate_cs && !a.gate_rs, scalar = a.dgate && !a.gate_cs && !a.gate_rs;
-  const bool full_gate = !PLAIN && a.dgate && a.gate_cs && a.gate_rs, token = !PLAIN && a.dgate && !a.gate_cs && a.gate_rs;
-  // The tensors of a row: z, r, dy, dr, gate, those that there are.
-  const int ir = has_z, idy = ir + has_pre, idr = idy + has_pre, ig = idr + has_dr;
-  float pre[8], post[8], sg[8];   // w_pre, w_post, scale * gate
+  const int rows = p.per + (first < p.rest ? 1 : 0);   // of this group
+  if (t < p.n)
+    for (int s = 0; s < min(p.S, rows); ++s) ring_fill<VEC>(ring, s, base + s * p.row);
+  // What there is, as bits of one register, so that each test is one instruction.
+  const bool uniform = a.dgate && !a.gate_rs;
+  uint32_t has = (a.z.p ? 1u : 0u) | (a.w_post ? 2u : 0u) | (a.w_pre ? 4u : 0u) | (a.dr.p ? 8u : 0u) | (a.dz.p ? 16u : 0u) |
+                 (a.dgate && a.gate_rs ? a.gate_cs ? 32u : 64u : 0u);
+  asm volatile("" : "+r"(has));
+  const bool has_z = PLAIN || has & 1, has_post = PLAIN || has & 2, has_pre = PLAIN || has & 4, has_dr = PLAIN || has & 8;
+  const bool has_dz = PLAIN || has & 16, full_gate = !PLAIN && has & 32, token = !PLAIN && has & 64;
+  const bool by_row = full_gate || token, feature = uniform && a.gate_cs, scalar = uniform && !a.gate_cs;
+  // The parts of a row: z, r, dy, dr, gate, those that there are.
+  const int ir = PLAIN ? 1 : has_z, idy = PLAIN ? 2 : ir + has_pre, idr = PLAIN ? 3 : idy + has_pre, ig = idr + has_dr;
+  const Part pz = part_of<VEC>(p, 0, first, step, col), pr = part_of<VEC>(p, ir, first, step, col),
+             pdy = part_of<VEC>(p, idy, first, step, col), pdr = part_of<VEC>(p, idr, first, step, col),
+             pg = part_of<VEC>(p, ig, first, step, col);
+  float pre[8], post[8], c[8];   // w_pre, w_post, scale * gate * w_post
   const long long pcol = (long long)col * (a.pdtype == DETFFN_F32 ? 4 : 2);
   auto from = [&](const void* q) { return static_cast<const void*>(static_cast<const char*>(q) + pcol); };
   param_unit<DT, VEC>(has_pre ? from(a.w_pre) : nullptr, a.pdtype, cs, 1.0f, pre);
   param_unit<DT, VEC>(has_post ? from(a.w_post) : nullptr, a.pdtype, cs, 1.0f, post);
-  param_unit<DT, VEC>(feature ? from(a.gate) : nullptr, a.pdtype, cs, scalar ? param<DT>(a.gate, a.pdtype, 0) : 1.0f, sg);
-  float apre[8], apost[8], agate[8];   // this thread's columns of the sums over tokens
+  // scale * gate, the same for every row: wanted again at the end.
+  auto gates = [&](float (&g)[8]) {
+    param_unit<DT, VEC>(feature ? from(a.gate) : nullptr, a.pdtype, cs, scalar ? param<DT>(a.gate, a.pdtype, 0) : 1.0f, g);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] *= a.scale;
+  };
+  gates(c);
+  float apre[8], apost[8];   // this thread's columns of the sums over tokens
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    sg[j] *= a.scale;
-    apre[j] = apost[j] = agate[j] = 0.0f;
+    c[j] *= post[j];
+    apre[j] = apost[j] = 0.0f;
   }
   const float inv = 1.0f / (float)H;
-  int turn = 0, turn2 = 0, turn3 = 0;
+  int turn = 0;
   E* dxp = static_cast<E*>(const_cast<void*>(a.dx.p)) + first * a.dx.ld + col;
   E* dzp = static_cast<E*>(const_cast<void*>(a.dz.p)) + first * a.dz.ld + col;
   const long long dx_step = step * a.dx.ld, dz_step = step * a.dz.ld;
   __syncthreads();   // the barriers are initialised
   if (WIDE) cluster_barrier();   // and every CTA of the cluster has started
   auto sums4 = [&](float (&v)[4]) {
-    group_sums<4>(v, buf, turn, G, group, t);
-    if (WIDE) cluster_sums<4>(v, across, turn3, p.C, rank);
+    add(v);
+    if (WIDE) cluster_sums<4>(v, across, turn, p.C, rank);
   };
-  // Of the row in slot s: sum r^2, sum dy w_pre r, sum z^2.
-  auto row_sums = [&](int s, long long m, float (&v)[4]) {
-    const unsigned char* row = ring.base + (size_t)s * p.row;
-    float x[8], w[8];
+  // The i-th row, in the next slot: r, dy, z, and sum r^2, sum dy w_pre r, sum z^2.
+  float x[8], dy[8], n[8];
+  auto arrive = [&](int i, float (&v)[4]) {
+    const bool came = ring_wait(ring);
     if (has_pre) {
-      unit<DT, VEC>(ring_row<VEC>(p, row, ir, m, col), cs, x);
-      unit<DT, VEC>(ring_row<VEC>(p, row, idy, m, col), cs, w);
+      unit<DT, VEC>(ring_row<VEC>(ring.at, pr, i), cs, x);
+      unit<DT, VEC>(ring_row<VEC>(ring.at, pdy, i), cs, dy);
       v[0] = dot8(x, x);
+      float w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] *= pre[j];
+      for (int j = 0; j < 8; ++j) w[j] = dy[j] * pre[j];
       v[1] = dot8(x, w);
     }
-    if (has_post) {
-      unit<DT, VEC>(ring_row<VEC>(p, row, 0, m, col), cs, x);
-      v[2] = dot8(x, x);
-    }
-    if (!on) v[0] = v[1] = v[2] = 0.0f;
+    if (has_z) unit<DT, VEC>(ring_row<VEC>(ring.at, pz, i), cs, n);
+    if (has_post) v[2] = dot8(n, n);
+    if (VEC && !on) v[0] = v[1] = v[2] = 0.0f;
+    if (!came) v[0] = v[2] = __int_as_float(0x7fc00000);
   };
-  float s[3] = {0.0f, 0.0f, 0.0f};
-  if (first < a.M) {
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (ring_wait(ring)) row_sums(0, first, v);
-    else v[0] = v[2] = __int_as_float(0x7fc00000);
-    sums4(v);
-    s[0] = v[0], s[1] = v[1], s[2] = v[2];
+  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (rows > 0) {
+    arrive(0, s);
+    sums4(s);
   }
-  for (long long m = first; m < a.M; m += step, dxp += dx_step, dzp += dz_step) {
-    const unsigned char* row = ring.base + (size_t)ring.s * p.row;
+  for (int i = 0; i < rows; ++i, dxp += dx_step, dzp += dz_step) {
+    unsigned char* row = ring.at;
     const int slot = ring.s;
-    if (++ring.s == p.S) {
-      ring.s = 0;
-      ring.phase ^= 1u;
-    }
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    if (m + step < a.M) {
-      if (ring_wait(ring)) row_sums(ring.s, m + step, v);
-      else v[0] = v[2] = __int_as_float(0x7fc00000);
-    }
-    // dx
-    float d[8], z[8], x[8];
+    ring_next(p, ring);
+    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d[8];
     if (has_dr) {
-      unit<DT, VEC>(ring_row<VEC>(p, row, idr, m, col), cs, d);
+      unit<DT, VEC>(ring_row<VEC>(row, pdr, i), cs, d);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) d[j] = 0.0f;
     }
     if (has_pre) {
-      float dy[8];
-      unit<DT, VEC>(ring_row<VEC>(p, row, ir, m, col), cs, x);
-      unit<DT, VEC>(ring_row<VEC>(p, row, idy, m, col), cs, dy);
       const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * (q * q * q);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -455,49 +488,57 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
       }
       put_unit<DT, VEC>(dxp, cs, d);
     }
+    // d becomes D c, n is b z (without z: dz = scale dx).
     const float b = has_post ? rsqrtf(s[2] * inv + a.eps) : 1.0f;
-    float tok[2] = {0.0f, 0.0f};   // sum dx n
+    float bn[8], gate = 1.0f;   // gate: scale times a token's gate
     if (has_z) {
-      unit<DT, VEC>(ring_row<VEC>(p, row, 0, m, col), cs, z);
-      if (full_gate || token) {
-        param_unit<DT, VEC>(full_gate ? ring_row<VEC>(p, row, ig, m, col) : nullptr, a.pdtype, cs, token ? param<DT>(a.gate, a.pdtype, m * a.gate_rs) : 0.0f, sg);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sg[j] *= a.scale;
-      }
+      for (int j = 0; j < 8; ++j) bn[j] = n[j] * b;
+    }
+    if (by_row) {
+      const long long m = first + i * step;
+      float g[8], u[8];
+      if (token) gate = a.scale * param<DT>(a.gate, a.pdtype, m * a.gate_rs);
+      param_unit<DT, VEC>(full_gate ? ring_row<VEC>(row, pg, i) : nullptr, a.pdtype, cs, gate, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float u = d[j] * (z[j] * b);
-        const float w = u * sg[j];
-        apost[j] += w;
-        v[3] = fmaf(w, post[j], v[3]);   // sum dn w_post z b
-        x[j] = u * post[j];              // dx n
-        agate[j] += x[j];
+        if (full_gate) g[j] *= a.scale;
+        u[j] = d[j] * bn[j];
+        apost[j] = fmaf(u[j], g[j], apost[j]);
+        u[j] *= post[j];
+        d[j] *= g[j] * post[j];
       }
-      if (token) tok[0] = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-      if (!on) v[3] = tok[0] = 0.0f;
+      if (token) {
+        v[3] = ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));   // sum D n w_post: dgate's
+      } else {
+        v[3] = dot8(d, bn);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) u[j] *= a.scale;
+        if (DT == DETFFN_F32 || a.pdtype == DT) put_unit<DT, VEC>(static_cast<E*>(a.dgate) + m * H + col, cs, u);
+        else put_unit<DETFFN_F32, VEC>(static_cast<float*>(a.dgate) + m * H + col, cs, u);
+      }
+    } else {
+      if (has_z) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) apost[j] = fmaf(d[j], bn[j], apost[j]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] *= c[j];
+      if (has_post) v[3] = dot8(d, bn);
     }
+    if (VEC && !on) v[3] = 0.0f;
+    // The next row's sums share this row's barrier.
+    if (i + 1 < rows) arrive(i + 1, v);
     sums4(v);
-    if (t == 0 && m + p.S * step < a.M) ring_fill<VEC, WIDE>(p, ring, slot, m + p.S * step, col, width);
+    if (t < p.n && i + p.S < rows) ring_fill<VEC>(ring, slot, row);
+    if (token && t == 0 && rank == 0) put_param<DT>(a.dgate, a.pdtype, first + i * step, a.scale * v[3]);
+    if (has_post) {
+      const float k = gate * v[3] * inv * b;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) d[j] = fmaf(b, d[j], -k * bn[j]);
+    }
+    if (has_dz) put_unit<DT, VEC>(dzp, cs, d);
     s[0] = v[0], s[1] = v[1], s[2] = v[2];
-    if (!PLAIN && !a.dz.p) continue;
-    if (full_gate) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] *= a.scale;
-      if (DT == DETFFN_F32 || a.pdtype == DT) put_unit<DT, VEC>(static_cast<E*>(a.dgate) + m * H + col, cs, x);
-      else put_unit<DETFFN_F32, VEC>(static_cast<float*>(a.dgate) + m * H + col, cs, x);
-    }
-    if (token) {
-      group_sums<2>(tok, buf2, turn2, G, group, t);
-      if (WIDE) cluster_sums<2>(tok, across, turn3, p.C, rank);
-      if (t == 0 && rank == 0) put_param<DT>(a.dgate, a.pdtype, m, a.scale * tok[0]);
-    }
-    const float k = v[3] * inv * (b * b);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      d[j] *= sg[j] * post[j];
-      if (has_post) d[j] = fmaf(b, d[j], -k * z[j]);
-    }
-    put_unit<DT, VEC>(dzp, cs, d);
   }
   // The CTA's column sums: its groups' added in order (the rings are done
   // with, so their memory holds them).  Little code, as it runs once and cold:
@@ -507,18 +548,24 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   const int kinds = (a.dw_post ? 1 : 0) + (a.dw_pre ? 1 : 0) + (feature ? 1 : 0);
   {
     int kind = 0;
-    auto put = [&](const float (&v)[8], float scale) {
-      float w[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = scale * v[j];
+    auto put = [&](const float (&w)[8]) {
       // (a group's columns: G 8 floats, in their own order)
       if (p.R == 1) put_unit<DETFFN_F32, VEC>(a.part + (kind * sets + set) * H + col, cs, w);
       else put_unit<DETFFN_F32, VEC>(all + kind * 4096 + group * G * 8, cs, w);
       ++kind;
     };
-    if (a.dw_post) put(apost, 1.0f);
-    if (a.dw_pre) put(apre, 1.0f);
-    if (feature) put(agate, a.scale);
+    // (apost: sum dx n, and with a gate of each row sum dx n scale gate)
+    float w[8];
+    if (a.dw_post) {
+      gates(w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = by_row ? apost[j] : w[j] * apost[j];
+      put(w);
+    }
+    if (a.dw_pre) put(apre);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) apost[j] *= a.scale * post[j];
+    if (feature) put(apost);
   }
   if (p.R > 1) {
     __syncthreads();
@@ -535,15 +582,15 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   }
   if (scalar) {
     // One number: every thread's columns, added by warp and then in order.
-    const float v = warp_sum(!on ? 0.0f : ((agate[0] + agate[1]) + (agate[2] + agate[3])) +
-                                              ((agate[4] + agate[5]) + (agate[6] + agate[7])));
+    const float v = warp_sum(!on ? 0.0f : ((apost[0] + apost[1]) + (apost[2] + apost[3])) +
+                                              ((apost[4] + apost[5]) + (apost[6] + apost[7])));
     __syncthreads();
     if ((threadIdx.x & 31) == 0) all[threadIdx.x >> 5] = v;
     __syncthreads();
     if (threadIdx.x == 0) {
       float w = 0.0f;
       for (int q = 0; q < (int)blockDim.x >> 5; ++q) w += all[q];
-      a.part[kinds * sets * H + blockIdx.x] = a.scale * w;
+      a.part[kinds * sets * H + blockIdx.x] = w;
     }
   }
 }
@@ -581,6 +628,8 @@ bool ring_plan(const JoinArgs& a, bool back, bool vec, int V, RingPlan* out) {
   if (p.S > kRingMaxStages) p.S = kRingMaxStages;
   const long long need = (a.M + p.R - 1) / p.R;
   p.grid = (int)(need < most ? need : most) * p.C;
+  p.per = (int)(a.M / ((long long)(p.grid / p.C) * p.R));
+  p.rest = (int)(a.M % ((long long)(p.grid / p.C) * p.R));
   *out = p;
   return true;
 }
