@@ -16,6 +16,8 @@
 // memory stay together wherever the row begins.
 #pragma once
 
+#include <type_traits>
+
 #include "k_join.cuh"
 #include "ptx.cuh"
 
@@ -288,7 +290,8 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
     }
     return v;
   };
-  float sz = 0.0f;
+  // A token's gate is read a row ahead.
+  float sz = 0.0f, next_gate = by_row && !a.gate_cs && rows > 0 ? param<DT>(a.gate, a.pdtype, first * a.gate_rs) : 0.0f;
   if (rows > 0) {
     float v[2] = {sum_z(0), 0.0f};
     add(v);
@@ -302,8 +305,8 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
     if (n + 1 < rows) v[0] = sum_z(n + 1);
     float r[V][8];
     const float b = has_post ? rsqrtf(sz * inv + a.eps) : 1.0f;
-    float g1 = 0.0f;
-    if (by_row && !a.gate_cs) g1 = param<DT>(a.gate, a.pdtype, (first + n * step) * a.gate_rs);
+    const float g1 = next_gate;
+    if (by_row && !a.gate_cs && n + 1 < rows) next_gate = param<DT>(a.gate, a.pdtype, (first + (n + 1) * step) * a.gate_rs);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       unit<DT, VEC>(ring_row<VEC>(row, px, n), k[i], r[i]);
@@ -367,8 +370,19 @@ __device__ __forceinline__ void cluster_sums(float (&v)[N], float* buf, int& tur
   }
 }
 
-// Backward, one unit to a thread.  PLAIN: both norms, dr given, and a gate (if
-// any) that is the same for every row.  WIDE: a cluster of CTAs shares each row
+// What a backward pass has, when it is compiled for it: dr and dz always, and
+// z where it is read.  A pass compiled for any of it tests bits as it goes, and
+// each test ends a run of instructions that the compiler can interleave: BF16,
+// 8192 x 4096, only the post-norm 73 us so and 47 compiled for it; only the
+// pre-norm 86 and 57; both, 16384 x 2048, a gate per token 114 and 94.
+enum Has : uint32_t { kPost = 2, kPre = 4, kZ = 1, kDr = 8, kDz = 16, kFull = 32, kToken = 64, kAny = 0 };
+
+__host__ __device__ inline uint32_t has_of(const JoinArgs& a) {
+  return (a.z.p ? kZ : 0u) | (a.w_post ? kPost : 0u) | (a.w_pre ? kPre : 0u) | (a.dr.p ? kDr : 0u) | (a.dz.p ? kDz : 0u) |
+         (a.dgate && a.gate_rs ? a.gate_cs ? kFull : kToken : 0u);
+}
+
+// Backward, one unit to a thread.  HAS: what there is (kAny: found out).  WIDE: a cluster of CTAs shares each row
 // of more than 4096 features, a run of columns each, and the row's sums meet
 // in shared memory across it.
 //
@@ -377,7 +391,7 @@ __device__ __forceinline__ void cluster_sums(float (&v)[N], float* buf, int& tur
 // of a gate that is the same for every row have the factors scale gate and
 // scale w_post of sum D n, so one accumulator serves both.  A row's r, dy and z
 // are converted once and stay in registers over the barrier of its first sums.
-template <int DT, bool PLAIN, bool VEC, bool WIDE>
+template <int DT, uint32_t HAS, bool VEC, bool WIDE>
 __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kRingMaxGroups * kRingMaxStages];
@@ -402,16 +416,18 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   const int rows = p.per + (first < p.rest ? 1 : 0);   // of this group
   if (t < p.n)
     for (int s = 0; s < min(p.S, rows); ++s) ring_fill<VEC>(ring, s, base + s * p.row);
-  // What there is, as bits of one register, so that each test is one instruction.
   const bool uniform = a.dgate && !a.gate_rs;
-  uint32_t has = (a.z.p ? 1u : 0u) | (a.w_post ? 2u : 0u) | (a.w_pre ? 4u : 0u) | (a.dr.p ? 8u : 0u) | (a.dz.p ? 16u : 0u) |
-                 (a.dgate && a.gate_rs ? a.gate_cs ? 32u : 64u : 0u);
-  asm volatile("" : "+r"(has));
-  const bool has_z = PLAIN || has & 1, has_post = PLAIN || has & 2, has_pre = PLAIN || has & 4, has_dr = PLAIN || has & 8;
-  const bool has_dz = PLAIN || has & 16, full_gate = !PLAIN && has & 32, token = !PLAIN && has & 64;
+  uint32_t has = HAS;
+  if (HAS == kAny) {
+    has = has_of(a);
+    asm volatile("" : "+r"(has));   // (one register, so that a test is one instruction)
+  }
+  const bool has_z = has & kZ, has_post = has & kPost, has_pre = has & kPre, has_dr = has & kDr, has_dz = has & kDz;
+  const bool full_gate = has & kFull, token = has & kToken;
   const bool by_row = full_gate || token, feature = uniform && a.gate_cs, scalar = uniform && !a.gate_cs;
   // The parts of a row: z, r, dy, dr, gate, those that there are.
-  const int ir = PLAIN ? 1 : has_z, idy = PLAIN ? 2 : ir + has_pre, idr = PLAIN ? 3 : idy + has_pre, ig = idr + has_dr;
+  // (z is in a slot where it is given, whether it is read or not)
+  const int ir = a.z.p != nullptr, idy = ir + has_pre, idr = idy + has_pre, ig = idr + has_dr;
   const Part pz = part_of<VEC>(p, 0, first, step, col), pr = part_of<VEC>(p, ir, first, step, col),
              pdy = part_of<VEC>(p, idy, first, step, col), pdr = part_of<VEC>(p, idr, first, step, col),
              pg = part_of<VEC>(p, ig, first, step, col);
@@ -462,6 +478,8 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     if (VEC && !on) v[0] = v[1] = v[2] = 0.0f;
     if (!came) v[0] = v[2] = __int_as_float(0x7fc00000);
   };
+  // A token's gate is read a row ahead.
+  float next_gate = token && rows > 0 ? a.scale * param<DT>(a.gate, a.pdtype, first * a.gate_rs) : 1.0f;
   float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   if (rows > 0) {
     arrive(0, s);
@@ -490,7 +508,8 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     }
     // d becomes D c, n is b z (without z: dz = scale dx).
     const float b = has_post ? rsqrtf(s[2] * inv + a.eps) : 1.0f;
-    float bn[8], gate = 1.0f;   // gate: scale times a token's gate
+    float bn[8];
+    const float gate = next_gate;   // scale times a token's gate, or 1
     if (has_z) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) bn[j] = n[j] * b;
@@ -498,7 +517,7 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     if (by_row) {
       const long long m = first + i * step;
       float g[8], u[8];
-      if (token) gate = a.scale * param<DT>(a.gate, a.pdtype, m * a.gate_rs);
+      if (token && i + 1 < rows) next_gate = a.scale * param<DT>(a.gate, a.pdtype, (m + step) * a.gate_rs);
       param_unit<DT, VEC>(full_gate ? ring_row<VEC>(row, pg, i) : nullptr, a.pdtype, cs, gate, g);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -677,18 +696,36 @@ cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
   return go(vec ? k_fwd<DT, 8, true> : k_fwd<DT, 8, false>);
 }
 
+template <uint32_t H>
+using Kind = std::integral_constant<uint32_t, H>;
+
 template <int DT>
 cudaError_t backward(const JoinArgs& a, cudaStream_t st) {
   const bool vec = vectors<DT>(a);
-  const bool plain = a.w_post && a.w_pre && a.dr.p && !(a.gate && a.gate_rs);
   RingPlan p;
   if (!ring_plan<DT>(a, true, vec, 1, &p)) return cudaErrorInvalidConfiguration;   // (two rows always fit)
   const int sets = p.grid / p.C;
-  cudaError_t e;
-  if (p.C > 1)
-    e = vec ? ring_launch<k_bwd_ring<DT, false, true, true>>(a, p, st) : ring_launch<k_bwd_ring<DT, false, false, true>>(a, p, st);
-  else if (!vec) e = ring_launch<k_bwd_ring<DT, false, false, false>>(a, p, st);
-  else e = plain ? ring_launch<k_bwd_ring<DT, true, true, false>>(a, p, st) : ring_launch<k_bwd_ring<DT, false, true, false>>(a, p, st);
+  // The passes that are compiled for what they have (over a cluster: those
+  // without a gate of each row).
+  uint32_t has = has_of(a);
+  if (!(has & kPost) && !a.dgate) has &= ~kZ;   // (z is not read)
+  cudaError_t e = cudaErrorInvalidConfiguration;
+  auto one = [&](auto h) {
+    constexpr uint32_t HAS = decltype(h)::value;
+    if (HAS != kAny && HAS != has) return false;
+    if (p.C > 1) {
+      if constexpr (HAS & (kFull | kToken)) return false;
+      else e = vec ? ring_launch<k_bwd_ring<DT, HAS, true, true>>(a, p, st) : ring_launch<k_bwd_ring<DT, HAS, false, true>>(a, p, st);
+    } else {
+      e = vec ? ring_launch<k_bwd_ring<DT, HAS, true, false>>(a, p, st) : ring_launch<k_bwd_ring<DT, HAS, false, false>>(a, p, st);
+    }
+    return true;
+  };
+  constexpr uint32_t kBoth = kPost | kPre, kIn = kDr | kDz, kInZ = kIn | kZ;
+  auto any_of = [&](auto... h) { return (one(h) || ...); };
+  any_of(Kind<kBoth | kInZ>{}, Kind<kBoth | kInZ | kToken>{}, Kind<kBoth | kInZ | kFull>{},
+         Kind<kPost | kInZ>{}, Kind<kPost | kInZ | kToken>{}, Kind<kPost | kInZ | kFull>{},
+         Kind<kPre | kIn>{}, Kind<kPre | kInZ>{}, Kind<kPre | kInZ | kToken>{}, Kind<kPre | kInZ | kFull>{}, Kind<kAny>{});
   if (e != cudaSuccess) return e;
   void* out[3] = {};
   int n = 0;
