@@ -149,6 +149,18 @@ def test_backward(G, M, H, dt, pt, gate, post, pre):
         assert (getattr(got, name) is None) == (name not in ref)
 
 
+# Many rows to every group of threads, so that rings turn several times: whole
+# vectors, other rows, and rows that several thread blocks share.  (The chains of
+# the column sums: rows of a thread, groups of a block, 152 blocks or fewer; the
+# bound of test_backward holds them all.)
+@pytest.mark.parametrize("gate", ["none", "feature", "scalar", "token", "full"])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, True), (True, False)])
+@pytest.mark.parametrize("M,H,dt", [(10949, 264, "bf16"), (10949, 261, "f16"), (4001, 264, "f32"), (687, 4104, "bf16")])
+def test_many_rows(G, M, H, dt, gate, post, pre):
+    test_forward(G, M, H, dt, dt, gate, post, pre)
+    test_backward(G, M, H, dt, dt, gate, post, pre)
+
+
 def test_backward_without_dr(G):
     s = inputs(6, 300, "f32", "f32", "feature", 5)
     got = G.detffn_join_backward(s["x"], s["z"], None, s["dy"], s["w_post"], s["gate"], 1.0, s["w_pre"])
