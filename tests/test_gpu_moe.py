@@ -92,6 +92,27 @@ def test_layer(G, T, E, k, H, I, dt, normalize):
     check(G, inputs(T, E, H, I, dt, T + E + H, k), k, normalize, dt)
 
 
+@pytest.mark.parametrize("T,E,k,H,I", [(12, 8, 8, 2048, 1416), (48, 3, 2, 2056, 4104), (9, 5, 5, 2048, 2000)])
+def test_units_that_fill_a_second_round_in_part(G, T, E, k, H, I):
+    check(G, inputs(T, E, H, I, "bf16", T + H, k), k, True, "bf16")
+
+
+@pytest.mark.parametrize("path", [0, 1])
+@pytest.mark.parametrize("T,E,k", [(20, 4, 3), (64, 3, 2), (40, 16, 2)])
+def test_tokens_that_are_not_finite_stay_alone(G, T, E, k, path):
+    """All tokens share tiles with one of NaN, one of infinities and one that overflows h."""
+    s = inputs(T, E, 256, 192, "bf16", 3 * T, k)
+    rest = (s["Wr"], s["Wg"], s["Wu"], s["Wd"], k)
+    want = G.detffn_moe_forward(s["x"], *rest, path=path)
+    x = s["x"].clone()
+    x[3], x[7], x[11] = float("nan"), float("inf"), 3e38
+    got = G.detffn_moe_forward(x, *rest, path=path)
+    assert G.detffn_get_status() == 0
+    keep = [t for t in range(T) if t not in (3, 7, 11)]
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(got, want))
+    assert bool(got[0][3].isnan().all())
+
+
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 2, 1, 1, 1), (3, 5, 2, 33, 17), (9, 4, 3, 255, 129), (64, 6, 2, 100, 36)])
 @pytest.mark.parametrize("dt", list(DT))
 def test_odd_widths(G, T, E, k, H, I, dt):
