@@ -413,7 +413,7 @@ detffn_status detffn_moe_forward(detffn_handle h, const void* x, const void* Wr,
   TRYCU(cudaGetDevice(&prev));
   if (prev != h->device) TRYCU(cudaSetDevice(h->device));
   const cudaError_t e = tensor ? launch_moe_tensor(a, sc, wt, h->sm_count, (cudaStream_t)stream)
-                               : launch_moe_general(a, (cudaStream_t)stream);
+                               : launch_moe_general(a, sc, (cudaStream_t)stream);
   if (prev != h->device) cudaSetDevice(prev);
   return cu(e);
 }

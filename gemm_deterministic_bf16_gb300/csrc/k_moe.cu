@@ -24,6 +24,26 @@ __device__ __forceinline__ float warp_dot(const typename Io<DT>::E* a, const typ
   return warp_sum(s);
 }
 
+// Sums over a warp of sixteen values of every lane, in sixteen exchanges instead
+// of eighty: lane l keeps the half of the values that bit 0, 1, 2, 3 of l names
+// in turn and ends with value sum16_of(l), then both halves of the warp add.
+__device__ __forceinline__ int sum16_of(int lane) {
+  return ((lane & 1) << 3) | ((lane & 2) << 1) | ((lane & 4) >> 1) | ((lane & 8) >> 3);
+}
+__device__ __forceinline__ float sum16(float (&v)[16], int lane) {
+#pragma unroll
+  for (int b = 0; b < 4; ++b) {
+    const int half = 8 >> b;
+    const bool up = lane >> b & 1;
+#pragma unroll
+    for (int i = 0; i < half; ++i) {
+      const float send = up ? v[i] : v[i + half];
+      v[i] = (up ? v[i + half] : v[i]) + __shfl_xor_sync(0xffffffffu, send, 1 << b);
+    }
+  }
+  return v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+}
+
 // Router logits of four tokens and four experts by one block: each of eight
 // warps takes an eighth of H (in 16-byte vectors; a token's sum is split by H
 // alone), the sixteen sums of a warp meet in sixteen exchanges instead of
@@ -60,20 +80,8 @@ __global__ void __launch_bounds__(256) k_logits_tile(const __grid_constant__ Moe
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[i] = fmaf(p[i >> 2][j], q[i & 3][j], v[i]);
   }
-  // Lane l keeps the half of the values that bit 0, 1, 2, 3 of l names in turn:
-  // it ends with value l & 15 (bits reversed), then both halves of the warp add.
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const int half = 8 >> b;
-    const bool up = lane >> b & 1;
-#pragma unroll
-    for (int i = 0; i < half; ++i) {
-      const float send = up ? v[i] : v[i + half];
-      v[i] = (up ? v[i + half] : v[i]) + __shfl_xor_sync(0xffffffffu, send, 1 << b);
-    }
-  }
-  v[0] += __shfl_xor_sync(0xffffffffu, v[0], 16);
-  if (lane < 16) part[warp][((lane & 1) << 3) | ((lane & 2) << 1) | ((lane & 4) >> 1) | ((lane & 8) >> 3)] = v[0];
+  const float mine = sum16(v, lane);
+  if (lane < 16) part[warp][sum16_of(lane)] = mine;
   __syncthreads();
   if (threadIdx.x < 16) {
     const int t = threadIdx.x >> 2, e = threadIdx.x & 3;
@@ -144,44 +152,111 @@ __global__ void __launch_bounds__(1024) k_select(const __grid_constant__ MoeArgs
   }
 }
 
-// h of expert blockIdx.y: one warp per feature i of I.
-template <int DT>
+// N consecutive elements: one, four of FP32 or eight.
+template <int DT, int N>
+__device__ __forceinline__ void load_n(const typename Io<DT>::E* p, float (&f)[N]) {
+  if constexpr (N == 8) {
+    Io<DT>::ld8(p, f);
+  } else if constexpr (N == 4) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
+  } else {
+    f[0] = Io<DT>::ld(p);
+  }
+}
+
+// Products of four rows of x (of type XT) with four rows of weights over K, by
+// one warp: value 4 i + j is x_i . w_j.  VEC: 16-byte vectors of weights.
+template <int DT, int XT, bool VEC>
+__device__ __forceinline__ void tile16(const typename Io<XT>::E* const (&x)[4], const typename Io<DT>::E* const (&w)[4],
+                                       long long K, int lane, float (&v)[16]) {
+  constexpr int N = !VEC ? 1 : DT == DETFFN_F32 ? 4 : 8;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = 0.0f;
+#pragma unroll 2
+  for (long long k = (long long)lane * N; k < K; k += 32 * N) {
+    float a[4][N], b[4][N];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_n<DT, N>(w[i] + k, b[i]);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) load_n<XT, N>(x[i] + k, a[i]);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[i] = fmaf(a[i >> 2][j], b[i & 3][j], v[i]);
+  }
+}
+
+// What bounds the two kernels below is HBM for a few pairs of an expert and the
+// L2 beyond: an expert's weights are read once for every four of its pairs.  A
+// warp takes two features of gate and of up, or four of the output, so that
+// what it loads of x serves sixteen sums (FP32, 64 tokens, 6 of 64 experts,
+// H = 4096, I = 1536: 1538 us, and 7319 with one sum to a warp; 7 tokens, 2 of
+// 16, I = 1416: 130 and 312, the weights alone take 101).
+
+// h of expert blockIdx.y: features 2 i and 2 i + 1 by one warp.
+template <int DT, bool VEC>
 __global__ void __launch_bounds__(256) k_gateup(const __grid_constant__ MoeArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   using E = typename Io<DT>::E;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y;
-  const long long i = blockIdx.x * 8ll + warp;
-  if (i >= a.I) return;
+  const long long i0 = 2 * (blockIdx.x * 8ll + warp), i1 = min(i0 + 1, a.I - 1);
+  if (i0 >= a.I) return;
   const int p0 = a.first[e], p1 = a.first[e + 1];
-  const E* wg = static_cast<const E*>(a.Wg) + (e * a.I + i) * a.H;
-  const E* wu = static_cast<const E*>(a.Wu) + (e * a.I + i) * a.H;
-  for (int p = p0; p < p1; ++p) {
-    const E* x = static_cast<const E*>(a.x) + (a.pair[p] / a.k) * a.H;
-    const float g = warp_dot<DT>(x, wg, a.H, lane), u = warp_dot<DT>(x, wu, a.H, lane);
-    if (lane == 0) static_cast<float*>(a.h)[p * a.I + i] = g / (1.0f + expf(-g)) * u;
+  const E *wg = static_cast<const E*>(a.Wg) + e * a.I * a.H, *wu = static_cast<const E*>(a.Wu) + e * a.I * a.H;
+  const E* const w[4] = {wg + i0 * a.H, wu + i0 * a.H, wg + i1 * a.H, wu + i1 * a.H};
+  for (int p = p0; p < p1; p += 4) {
+    const E* x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)   // (past the last pair: the last again)
+      x[i] = static_cast<const E*>(a.x) + (a.pair[min(p + i, p1 - 1)] / a.k) * a.H;
+    float v[16];
+    tile16<DT, DT, VEC>(x, w, a.H, lane, v);
+    // Lanes l and l + 8 hold gate and up of one feature and pair.
+    const float g = sum16(v, lane), u = __shfl_xor_sync(0xffffffffu, g, 8);
+    const int of = sum16_of(lane), q = p + (of >> 2), f = of >> 1 & 1;
+    if (lane < 8 && q < p1 && i0 + f < a.I) static_cast<float*>(a.h)[q * a.I + i0 + f] = g / (1.0f + expf(-g)) * u;
   }
 }
 
-// out of token blockIdx.y: one warp per feature r of H.
-template <int DT>
-__global__ void __launch_bounds__(256) k_down(const __grid_constant__ MoeArgs a) {
+// y of the pairs of expert blockIdx.y: features 4 r .. 4 r + 3 by one warp.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(256) k_down(const __grid_constant__ MoeArgs a, float* y) {
   grid_dep_wait();
   grid_dep_launch();
   using E = typename Io<DT>::E;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, t = blockIdx.y;
-  const long long r = blockIdx.x * 8ll + warp;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, e = blockIdx.y;
+  const long long r = 4 * (blockIdx.x * 8ll + warp);
+  if (r >= a.H) return;
+  const int p0 = a.first[e], p1 = a.first[e + 1];
+  const E* w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = static_cast<const E*>(a.Wd) + (e * a.H + min(r + i, a.H - 1)) * a.I;
+  for (int p = p0; p < p1; p += 4) {
+    const float* h[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = static_cast<const float*>(a.h) + min(p + i, p1 - 1) * a.I;
+    float v[16];
+    tile16<DT, DETFFN_F32, VEC>(h, w, a.I, lane, v);
+    const float s = sum16(v, lane);
+    const int of = sum16_of(lane), q = p + (of >> 2);
+    const long long c = r + (of & 3);
+    if (lane < 16 && q < p1 && c < a.H) y[q * a.H + c] = s;
+  }
+}
+
+// out of token blockIdx.y: its pairs in the order of its choices.
+template <int DT>
+__global__ void __launch_bounds__(256) k_combine(const __grid_constant__ MoeArgs a, const float* y) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int t = blockIdx.y;
+  const long long r = blockIdx.x * 256ll + threadIdx.x;
   if (r >= a.H) return;
   float s = 0.0f;
-  for (int j = 0; j < a.k; ++j) {
-    const int q = t * a.k + j;
-    const E* w = static_cast<const E*>(a.Wd) + (a.experts[q] * a.H + r) * a.I;
-    const float* hp = static_cast<const float*>(a.h) + a.pos[q] * a.I;
-    float y = 0.0f;
-    for (long long i = lane; i < a.I; i += 32) y = fmaf(Io<DT>::ld(w + i), hp[i], y);
-    s = fmaf(a.weights[q], warp_sum(y), s);
-  }
-  if (lane == 0) Io<DT>::st(static_cast<E*>(a.out) + t * a.H + r, s);
+  for (int j = 0; j < a.k; ++j) s = fmaf(a.weights[t * a.k + j], y[a.pos[t * a.k + j] * a.H + r], s);
+  Io<DT>::st(static_cast<typename Io<DT>::E*>(a.out) + t * a.H + r, s);
 }
 
 template <int DT>
@@ -192,11 +267,18 @@ cudaError_t logits(const MoeArgs& a, int* counters, int n, cudaStream_t st) {
 }
 
 template <int DT>
-cudaError_t general(const MoeArgs& a, cudaStream_t st) {
+cudaError_t general(const MoeArgs& a, float* y, cudaStream_t st) {
+  const int per = DT == DETFFN_F32 ? 4 : 8;
+  auto on16 = [](const void* p) { return ((uintptr_t)p & 15u) == 0; };
+  const bool up = a.H % per == 0 && on16(a.x) && on16(a.Wg) && on16(a.Wu), down = a.I % per == 0 && on16(a.Wd);
   cudaError_t e = launch_moe_logits(a, nullptr, 0, st);
   if (e == cudaSuccess) e = launch_dependent(k_select, dim3(1), 1024, 0, st, a);
-  if (e == cudaSuccess) e = launch_dependent(k_gateup<DT>, dim3((unsigned)((a.I + 7) / 8), a.E), 256, 0, st, a);
-  if (e == cudaSuccess) e = launch_dependent(k_down<DT>, dim3((unsigned)((a.H + 7) / 8), a.T), 256, 0, st, a);
+  if (e == cudaSuccess)
+    e = launch_dependent(up ? k_gateup<DT, true> : k_gateup<DT, false>, dim3((unsigned)((a.I + 15) / 16), a.E), 256, 0, st, a);
+  if (e == cudaSuccess)
+    e = launch_dependent(down ? k_down<DT, true> : k_down<DT, false>, dim3((unsigned)((a.H + 31) / 32), a.E), 256, 0, st, a, y);
+  if (e == cudaSuccess)
+    e = launch_dependent(k_combine<DT>, dim3((unsigned)((a.H + 255) / 256), a.T), 256, 0, st, a, (const float*)y);
   return e;
 }
 
@@ -207,9 +289,9 @@ cudaError_t launch_moe_logits(const MoeArgs& a, int* counters, int n, cudaStream
          : a.dtype == DETFFN_F16 ? logits<DETFFN_F16>(a, counters, n, st) : logits<DETFFN_BF16>(a, counters, n, st);
 }
 
-cudaError_t launch_moe_general(const MoeArgs& a, cudaStream_t st) {
-  return a.dtype == DETFFN_F32 ? general<DETFFN_F32>(a, st)
-         : a.dtype == DETFFN_F16 ? general<DETFFN_F16>(a, st) : general<DETFFN_BF16>(a, st);
+cudaError_t launch_moe_general(const MoeArgs& a, const MoeScratch& sc, cudaStream_t st) {
+  return a.dtype == DETFFN_F32 ? general<DETFFN_F32>(a, sc.y, st)
+         : a.dtype == DETFFN_F16 ? general<DETFFN_F16>(a, sc.y, st) : general<DETFFN_BF16>(a, sc.y, st);
 }
 
 }  // namespace detffn

@@ -27,8 +27,8 @@ struct MoeArgs {
   void* h = nullptr;
 };
 
-// Workspace of the tensor kernel alone: counters [1 + E + ceil(H / 128)] and the
-// pairs' outputs y [parts][T * k][H] in FP32.
+// More workspace: the tensor kernel's counters [1 + E + ceil(H / 128)], and the
+// pairs' outputs y [parts][T * k][H] in FP32 (the general kernels use one part).
 struct MoeScratch {
   int* counters = nullptr;
   float* y = nullptr;
@@ -46,6 +46,6 @@ bool moe_tensor_covers(const MoeArgs& a);
 cudaError_t launch_moe_tensor(const MoeArgs& a, const MoeScratch& sc, const Waits& wt, int sm_count, cudaStream_t st);
 
 // CUDA-core kernels for any sizes (FP32, FP16 or BF16).
-cudaError_t launch_moe_general(const MoeArgs& a, cudaStream_t st);
+cudaError_t launch_moe_general(const MoeArgs& a, const MoeScratch& sc, cudaStream_t st);
 
 }  // namespace detffn
