@@ -13,6 +13,10 @@
 // its three outputs once:
 //   sigma = 1 / (1 + exp(-g)), a = g sigma
 //   dU = dh a,  dG = dh u sigma (1 + g (1 - sigma)),  h = a u
+//
+// All of it is bound by HBM where vectors carry it: 4096 x 12288 BF16 packs in
+// 49.6 us (93 % of the copy rate), unpacks in 46.5 (99 %), and the backward stage
+// takes 75.5 (100 %).
 #include <type_traits>
 
 #include "block.h"
@@ -108,7 +112,8 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
 
 // Rows of whole 8-element vectors on 16-byte boundaries: four lanes take one
 // block of 64 features, of gate and of up, lane l features 8 l .. 8 l + 7 and
-// 32 more than those.  FLAT: no block is short (I a multiple of 64), so blocks
+// 32 more than those: four loads under way, and three exchanges for 32 values (56
+// us at 4096 x 12288 BF16 with eight lanes and half of both, 49.6 so).  FLAT: no block is short (I a multiple of 64), so blocks
 // follow one another and nothing is divided.
 template <int DT, bool FLAT>
 __global__ void __launch_bounds__(kThreads) k_pack_vec(const __grid_constant__ CkptArgs a, uint32_t blocks, Div nb) {
@@ -197,6 +202,9 @@ __global__ void __launch_bounds__(kThreads) k_pack_vec(const __grid_constant__ C
 
 // Any row length and alignment: a warp takes four blocks, a lane features
 // lane and lane + 32 of each (64 bytes of a row to an access), of gate and up.
+// Bound by issue, as every element is loaded, coded and stored by itself: 4096 x
+// 12283 BF16 109 us (42 % of the copy rate).  Aligned vectors whose blocks' maxima meet in shared memory
+// by atomics took 121.
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_pack_any(const __grid_constant__ CkptArgs a, uint32_t blocks, Div nb) {
   grid_dep_wait();
@@ -257,6 +265,8 @@ __global__ void __launch_bounds__(kThreads) k_pack_any(const __grid_constant__ C
 //   kMixed: vectors of the tensor as one array, whatever I >= 8 is: up to three
 //          blocks meet in one (a block's end, a short block, a row's end);
 //   kOne:  element by element.
+// kMixed costs selects: 4096 x 12283 BF16 unpacks in 62.5 us (74 % of the copy
+// rate, kFlat 99 %), and its backward stage takes 97 (78 %, kFlat 100 %).
 enum Mode { kFlat, kRows, kMixed, kOne };
 
 // The scales of one vector: element j has s[0] for j < e0, s[1] for j < e1,

@@ -104,6 +104,7 @@ __device__ __forceinline__ void load_gate(const JoinArgs& a, long long m, int H,
 }
 
 // One block of threads to a row, V units to a thread, the row in registers.
+// Bound by latency (its loads, two sums): one row of 4096 features, BF16, 3.0 us.
 template <int DT, int V, bool VEC>
 __global__ void __launch_bounds__(512) k_fwd(const __grid_constant__ JoinArgs a) {
   __shared__ float buf[2 * 32];
@@ -169,10 +170,11 @@ __global__ void __launch_bounds__(512) k_fwd(const __grid_constant__ JoinArgs a)
   }
 }
 
-constexpr int kSetReads = 10;
+constexpr int kSetReads = 10;   // (152 sets in 16 runs)
 
 // out[c] = sum over sets of part[s][c]: Q = blockDim / 32 threads per column
-// take sets q, q + Q, ... in order and their sums are added in order.
+// take sets q, q + Q, ... in order and their sums are added in order.  Bound by
+// latency, so a thread's reads are all under way at once.
 template <int DT>
 __global__ void __launch_bounds__(512) k_sets(const float* __restrict__ part, int sets, long long n, void* out0,
                                               void* out1, void* out2, long long per, int pdtype) {

@@ -43,6 +43,13 @@
 // which is idle here.  A row's sum over K is one accumulation in FP32 in
 // tensor memory, whatever the other columns are, so a token's result does not
 // depend on the other tokens.
+//
+// HBM bounds it once the weights take longer than the chain around them (of the
+// measured copy rate: 64 tokens, 6 of 64 experts, H = 4096, I = 1536, 2.4 GB of
+// weights: 369 us, 98 %; 7 tokens, 2 of 16, I = 1416: 59.3 us, 85 %).  Below that
+// the chain does: one token, 8 of 128, H = 2048, I = 768 takes 27.2 us, 11.4 of them for the
+// weights; 1.5 us for the logits, 3 for the routing, 2 to 3 until the first
+// stage, 8 of gate/up, 3 until h is seen, 3 of down, 4 for the sums.
 #include <mutex>
 
 #include "elt.cuh"
@@ -258,8 +265,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // about 10 instructions a pair of logits for each of a thread's items, where
     // the rounds below take 240 a choice.  From the logits to the counts, 2 us of
     // other work included: 55 tokens of 11 experts, 5 choices, 3.3 us, and by
-    // rounds 6.1; 49 of 38 experts, 5 choices, 6.2 by ranks, which is what the
-    // rounds take there.
+    // rounds 6.1; 49 of 38 experts 6.2 by ranks, and 64 of 64, 6 choices, 6.5 by
+    // rounds.
     uint32_t* key = reinterpret_cast<uint32_t*>(smem);   // (the stages' memory)
 #pragma unroll 4
     for (int i = threadIdx.x; i < m.T * ld; i += kThreads) {
