@@ -143,6 +143,42 @@ Tensor empty(at::IntArrayRef shape, const Tensor& like, at::ScalarType type) {
   return Tensor(at::detail::empty_cuda(shape, type, like.device(), std::nullopt));
 }
 
+// Results that belong together (a checkpoint's four, the parameters'
+// gradients) share an allocation, 256-byte aligned each: an allocation takes
+// 0.9 us of a call, a tensor on part of one 0.2.
+class Together {
+ public:
+  void add(Tensor* out, at::IntArrayRef shape, at::ScalarType type) {
+    long long n = (long long)c10::elementSize(type);
+    for (long long d : shape) n *= d;
+    piece_[n_++] = {out, at::DimVector(shape), type, bytes_};
+    bytes_ += (n + 255) / 256 * 256;
+  }
+  void allocate(const Tensor& like) {
+    if (n_ == 0) return;
+    const Tensor all = empty({bytes_}, like, at::kByte);
+    for (int i = 0; i < n_; ++i) {
+      const Piece& p = piece_[i];
+      *p.out = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(),
+                                                        c10::scalarTypeToTypeMeta(p.type));
+      c10::TensorImpl* t = p.out->unsafeGetTensorImpl();
+      t->set_storage_offset(p.at / (long long)c10::elementSize(p.type));
+      t->set_sizes_contiguous(p.shape);
+    }
+  }
+
+ private:
+  struct Piece {
+    Tensor* out;
+    at::DimVector shape;
+    at::ScalarType type;
+    long long at;
+  };
+  Piece piece_[4];
+  int n_ = 0;
+  long long bytes_ = 0;
+};
+
 #define BODY(n)                                                             \
   HANDLE_TH_ERRORS                                                          \
   if (nargs != (n)) {                                                       \
@@ -212,9 +248,15 @@ PyObject* join_backward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (z && !dz) dz = &(t_dz = empty({M, H}, *lead, st));
   if (w_pre && !dx) dx = &(t_dx = empty({M, H}, *lead, st));
   const long long lddx = w_pre ? ROWS(dx, lead) : 0, lddz = ROWS(dz, lead);
-  if (gate) dgate = &(t_gate = empty(gate->sizes(), *lead, pt));
-  if (w_post) dw_post = &(t_post = empty({H}, *lead, pt));
-  if (w_pre) dw_pre = &(t_pre = empty({H}, *lead, pt));
+  Together grads;
+  if (gate && gate->numel() > H) t_gate = empty(gate->sizes(), *lead, pt);
+  else if (gate) grads.add(&t_gate, gate->sizes(), pt);
+  if (w_post) grads.add(&t_post, {H}, pt);
+  if (w_pre) grads.add(&t_pre, {H}, pt);
+  grads.allocate(*lead);
+  if (gate) dgate = &t_gate;
+  if (w_post) dw_post = &t_post;
+  if (w_pre) dw_pre = &t_pre;
   size_t bytes = 0;
   if (!ws) {
     check(detffn_join_workspace_size(M, H, &bytes), "detffn_join_workspace_size");
@@ -275,10 +317,13 @@ PyObject* ckpt8_pack(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
     q0 = c.gq, s0 = c.gs, q1 = c.uq, s1 = c.us;
   } else {
     const long long nb = (I + 63) / 64;
-    q0 = &(gq = empty({M, I}, *gate, at::kChar));
-    s0 = &(gs = empty({M, nb}, *gate, at::kFloat));
-    q1 = &(uq = empty({M, I}, *gate, at::kChar));
-    s1 = &(us = empty({M, nb}, *gate, at::kFloat));
+    Together all;
+    all.add(&gq, {M, I}, at::kChar);
+    all.add(&uq, {M, I}, at::kChar);
+    all.add(&gs, {M, nb}, at::kFloat);
+    all.add(&us, {M, nb}, at::kFloat);
+    all.allocate(*gate);
+    q0 = &gq, s0 = &gs, q1 = &uq, s1 = &us;
   }
   check(detffn_ckpt8_pack(gate->data_ptr(), up->data_ptr(), q0->data_ptr(), s0->data_ptr(), q1->data_ptr(),
                           s1->data_ptr(), M, I, type_of(gate->scalar_type()), stream_of(dev)),
@@ -353,8 +398,12 @@ PyObject* moe_forward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   check(detffn_moe_workspace_size(T, E, k < 0 || k > 1 << 20 ? -1 : (int)k, H, I, dt, &bytes), "detffn_moe_workspace_size");
   Tensor t_out, t_experts, t_weights, t_ws;
   if (!out) out = &(t_out = empty({T, H}, *x, st));
-  if (!experts) experts = &(t_experts = empty({T, k}, *x, at::kInt));
-  if (!weights) weights = &(t_weights = empty({T, k}, *x, at::kFloat));
+  Together routing;
+  if (!experts) routing.add(&t_experts, {T, k}, at::kInt);
+  if (!weights) routing.add(&t_weights, {T, k}, at::kFloat);
+  routing.allocate(*x);
+  if (!experts) experts = &t_experts;
+  if (!weights) weights = &t_weights;
   if (!ws) ws = &(t_ws = empty({(long long)(bytes < 256 ? 256 : bytes)}, *x, at::kByte));
   WHOLE(*out, dev, st, {T, H});
   WHOLE(*experts, dev, at::kInt, {T, k});
