@@ -352,30 +352,58 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
-// Sums over the CTAs of a cluster: each CTA's values (the same in all its
-// threads) go to every CTA's shared memory and are added there by rank.
-// `buf`: [2][8][4] floats.
-template <int N>
-__device__ __forceinline__ void cluster_sums(float (&v)[N], float* buf, int& turn, int C, int rank) {
-  float* b = buf + turn * 32;
-  turn ^= 1;
-  if ((int)threadIdx.x < C) {
-#pragma unroll
-    for (int i = 0; i < N; ++i)
+// Sums over the CTAs of a cluster: each CTA's four values (the same in all its
+// threads) go to every CTA's shared memory, count there against a barrier of
+// that CTA, and are added by rank.  `buf`: [2][8][4] floats; `bars`: one for each
+// half, of one arrival.  Two halves are enough: a CTA sends exchange k + 2 only
+// after every other has sent k + 1, and with it read k.  (With a barrier of the
+// cluster instead 4864 x 8192 takes 146 us, and so 103.)
+struct ClusterSums {
+  float* buf;
+  uint64_t* bars;
+  int C, rank, half = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void operator()(float (&v)[4]) {
+    float* b = buf + half * 32;
+    uint64_t* bar = bars + half;
+    if ((int)threadIdx.x < C) {
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, 16u * C);
       asm volatile(
-          "{\n\t.reg .b32 a;\n\t"
-          "mapa.shared::cluster.u32 a, %0, %1;\n\t"
-          "st.shared::cluster.f32 [a], %2;\n\t}" ::"r"(smem_u32(b + rank * N + i)),
-          "r"(threadIdx.x), "f"(v[i])
+          "{\n\t.reg .b32 a, m;\n\t"
+          "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+          "mapa.shared::cluster.u32 m, %1, %2;\n\t"
+          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [m];\n\t}" ::"r"(
+              smem_u32(b + rank * 4)),
+          "r"(smem_u32(bar)), "r"(threadIdx.x), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
           : "memory");
+    }
+    // Every CTA of the cluster has started and takes the same rows, so the wait
+    // ends; it is bounded all the same, and would read as NaN.
+    bool came = false;
+    for (long long i = 0; i < kDefaultSpin && !came; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(phase)
+          : "memory");
+      came = ok != 0;
+    }
+    float4 t = *reinterpret_cast<const float4*>(b);
+    for (int r = 1; r < C; ++r) {
+      const float4 o = *reinterpret_cast<const float4*>(b + r * 4);
+      t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
+    }
+    v[0] = came ? t.x : __int_as_float(0x7fc00000);
+    v[1] = t.y;
+    v[2] = came ? t.z : __int_as_float(0x7fc00000);
+    v[3] = t.w;
+    phase ^= (uint32_t)half;
+    half ^= 1;
   }
-  cluster_barrier();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    v[i] = b[i];
-    for (int r = 1; r < C; ++r) v[i] += b[r * N + i];
-  }
-}
+};
 
 // What a backward pass has, when it is compiled for it: dr and dz always, and
 // z where it is read.  A pass compiled for any of it tests bits as it goes, and
@@ -407,7 +435,13 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H;
   int rank = 0;
   if (WIDE) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
-  __shared__ float across[2 * 8 * 4];
+  __shared__ __align__(16) float across[2 * 8 * 4];
+  __shared__ uint64_t crossed[2];
+  ClusterSums cross{across, crossed, p.C, rank};
+  if (WIDE && threadIdx.x == 0) {
+    mbar_init(&crossed[0], 1);
+    mbar_init(&crossed[1], 1);
+  }
   const int col = rank * p.width, width = WIDE ? min(p.width, H - col) : H;
   const Cols cs = cols_of<VEC>(0, G, t, width);
   const bool on = cs.on != 0;
@@ -457,7 +491,6 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     apre[j] = apost[j] = 0.0f;
   }
   const float inv = 1.0f / (float)H;
-  int turn = 0;
   E* dxp = static_cast<E*>(const_cast<void*>(a.dx.p)) + first * a.dx.ld + col;
   E* dzp = static_cast<E*>(const_cast<void*>(a.dz.p)) + first * a.dz.ld + col;
   const long long dx_step = step * a.dx.ld, dz_step = step * a.dz.ld;
@@ -465,7 +498,7 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   if (WIDE) cluster_barrier();   // and every CTA of the cluster has started
   auto sums4 = [&](float (&v)[4]) {
     add(v);
-    if (WIDE) cluster_sums<4>(v, across, turn, p.C, rank);
+    if (WIDE) cross(v);
   };
   // The i-th row, in the next slot: r, dy, z, and sum r^2, sum dy w_pre r, sum z^2.
   float x[8], dy[8], n[8];
@@ -646,7 +679,9 @@ bool ring_plan(const JoinArgs& a, bool back, bool vec, int V, RingPlan* out) {
     if (rows[i]->p) add(rows[i]->p, rows[i]->ld * es, es);
   if (full) add(a.gate, a.gate_rs * ps, ps);
   // Few rows go to as many CTAs as there are before two share one.
-  const int most = kRingSets / p.C;
+  // (Clusters of four fit 36 times on this GPU's SMs, and of eight 15 times: with
+  // 38 the last two wait for a second round, 2432 x 16384 198 us and 110 so.)
+  const int most = p.C == 4 ? 36 : p.C == 8 ? 15 : kRingSets / p.C;
   p.R = p.C > 1 ? 1 : threads / p.G;
   if (p.R > (a.M + most - 1) / most) p.R = (int)((a.M + most - 1) / most);
   p.S = kRingBytes / (p.R * p.row);
@@ -712,20 +747,15 @@ cudaError_t backward(const JoinArgs& a, cudaStream_t st) {
   RingPlan p;
   if (!ring_plan<DT>(a, true, vec, 1, &p)) return cudaErrorInvalidConfiguration;   // (two rows always fit)
   const int sets = p.grid / p.C;
-  // The passes that are compiled for what they have (over a cluster: those
-  // without a gate of each row).
+  // The passes that are compiled for what they have.
   uint32_t has = has_of(a);
   if (!(has & kPost) && !a.dgate) has &= ~kZ;   // (z is not read)
   cudaError_t e = cudaErrorInvalidConfiguration;
   auto one = [&](auto h) {
     constexpr uint32_t HAS = decltype(h)::value;
     if (HAS != kAny && HAS != has) return false;
-    if (p.C > 1) {
-      if constexpr (HAS & (kFull | kToken)) return false;
-      else e = vec ? ring_launch<k_bwd_ring<DT, HAS, true, true>>(a, p, st) : ring_launch<k_bwd_ring<DT, HAS, false, true>>(a, p, st);
-    } else {
-      e = vec ? ring_launch<k_bwd_ring<DT, HAS, true, false>>(a, p, st) : ring_launch<k_bwd_ring<DT, HAS, false, false>>(a, p, st);
-    }
+    if (p.C > 1) e = vec ? ring_launch<k_bwd_ring<DT, HAS, true, true>>(a, p, st) : ring_launch<k_bwd_ring<DT, HAS, false, true>>(a, p, st);
+    else e = vec ? ring_launch<k_bwd_ring<DT, HAS, true, false>>(a, p, st) : ring_launch<k_bwd_ring<DT, HAS, false, false>>(a, p, st);
     return true;
   };
   constexpr uint32_t kBoth = kPost | kPre, kIn = kDr | kDz, kInZ = kIn | kZ;
