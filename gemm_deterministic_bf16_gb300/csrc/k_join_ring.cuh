@@ -16,9 +16,9 @@
 //
 // VEC: rows of whole 16-byte vectors on 16-byte boundaries; a unit is eight
 // features in a row.  Otherwise the copies take the 16-byte pieces that hold a
-// byte of the row (a piece never crosses an allocation's boundary), and a
-// thread's features lie G apart, so that a warp's accesses to shared and global
-// memory stay together wherever the row begins; what bounds these is issue, an
+// byte of the row (a piece never crosses an allocation's boundary), and a unit
+// is eight features 32 apart, a warp's 256 in a row, so that a warp's accesses to
+// shared and global memory stay together wherever the row begins; what bounds these is issue, an
 // instruction or two for each element where a vector's eight share one (16384 x
 // 1031: 50 us forward, 78 backward, 40 % of the copy rate).
 #pragma once
@@ -172,24 +172,23 @@ __device__ __forceinline__ bool ring_wait(const Ring1& r) {
 }
 
 // One unit of a thread: with VEC features c .. c + 7 (a thread past the row's
-// end reads the last unit and counts for nothing: on is 0), else c + j step
-// where bit j of on is set, and zeros.
+// end reads the last unit and counts for nothing: on is 0), else c + 32 j where
+// bit j of on is set, and zeros.
 struct Cols {
-  int c, step;
+  int c;
   uint32_t on;
 };
 template <bool VEC>
 __device__ __forceinline__ Cols cols_of(int i, int G, int t, int H) {
   Cols k;
-  k.step = G;
   if (VEC) {
     k.on = 8 * (i * G + t) < H;
     k.c = k.on ? 8 * (i * G + t) : H - 8;
   } else {
-    k.c = 8 * i * G + t;
+    k.c = 256 * (i * (G >> 5) + (t >> 5)) + (t & 31);
     k.on = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) k.on |= (k.c + j * G < H ? 1u : 0u) << j;
+    for (int j = 0; j < 8; ++j) k.on |= (k.c + 32 * j < H ? 1u : 0u) << j;
   }
   return k;
 }
@@ -201,7 +200,7 @@ __device__ __forceinline__ void unit(const void* row, const Cols& k, float (&v)[
     Io<DT>::ld8(p, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = k.on >> j & 1 ? Io<DT>::ld(p + j * k.step) : 0.0f;
+    for (int j = 0; j < 8; ++j) v[j] = k.on >> j & 1 ? Io<DT>::ld(p + 32 * j) : 0.0f;
   }
 }
 template <int DT, bool VEC>
@@ -213,7 +212,7 @@ __device__ __forceinline__ void put_unit(void* row, const Cols& k, const float (
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (k.on >> j & 1) Io<DT>::st(p + j * k.step, v[j]);
+      if (k.on >> j & 1) Io<DT>::st(p + 32 * j, v[j]);
   }
 }
 // The same of a parameter, in the rows' type or FP32; `fill` where there is none.
