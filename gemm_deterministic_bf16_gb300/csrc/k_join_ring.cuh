@@ -17,10 +17,11 @@
 // VEC: rows of whole 16-byte vectors on 16-byte boundaries; a unit is eight
 // features in a row.  Otherwise the copies take the 16-byte pieces that hold a
 // byte of the row (a piece never crosses an allocation's boundary), and a unit
-// is eight features 32 apart, a warp's 256 in a row, so that a warp's accesses to
-// shared and global memory stay together wherever the row begins; what bounds these is issue, an
-// instruction or two for each element where a vector's eight share one (16384 x
-// 1031: 50 us forward, 78 backward, 40 % of the copy rate).
+// is eight features 32 apart, a warp's 256 in a row, so that a warp's accesses
+// to shared and global memory stay together wherever the row begins.  What
+// bounds these is issue, an instruction or two for each element where a
+// vector's eight share one (16384 x 1031: 44 us forward, 59 backward, 46 and 51 %
+// of the copy rate).
 #pragma once
 
 #include <type_traits>
@@ -282,67 +283,82 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
   E* y = static_cast<E*>(const_cast<void*>(a.y.p)) + first * a.y.ld;
   const long long out_step = step * a.out.ld, y_step = step * a.y.ld;
   __syncthreads();   // the barriers are initialised
-  // The sum over z of the n-th row, in the next slot.
-  auto sum_z = [&](int n) {
-    float v = 0.0f;
-    if (!ring_wait(ring)) return __int_as_float(0x7fc00000);
-    if (has_post) {
+  auto all_rows = [&](const Cols (&k)[V]) __attribute__((always_inline)) {
+    // The sum over z of the n-th row, in the next slot.
+    auto sum_z = [&](int n) {
+      float v = 0.0f;
+      if (!ring_wait(ring)) return __int_as_float(0x7fc00000);
+      if (has_post) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float z[8];
-        unit<DT, VEC>(ring_row<VEC>(ring.at, pz, n), k[i], z);
-        v += k[i].on ? dot8(z, z) : 0.0f;
-      }
-    }
-    return v;
-  };
-  // A token's gate is read a row ahead.
-  float sz = 0.0f, next_gate = by_row && !a.gate_cs && rows > 0 ? param<DT>(a.gate, a.pdtype, first * a.gate_rs) : 0.0f;
-  if (rows > 0) {
-    float v[2] = {sum_z(0), 0.0f};
-    add(v);
-    sz = v[0];
-  }
-  for (int n = 0; n < rows; ++n, out += out_step, y += y_step) {
-    unsigned char* row = ring.at;
-    const int slot = ring.s;
-    ring_next(p, ring);
-    float v[2] = {0.0f, 0.0f};
-    if (n + 1 < rows) v[0] = sum_z(n + 1);
-    float r[V][8];
-    const float b = has_post ? rsqrtf(sz * inv + a.eps) : 1.0f;
-    const float g1 = next_gate;
-    if (by_row && !a.gate_cs && n + 1 < rows) next_gate = param<DT>(a.gate, a.pdtype, (first + (n + 1) * step) * a.gate_rs);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      unit<DT, VEC>(ring_row<VEC>(row, px, n), k[i], r[i]);
-      if (has_z) {
-        float z[8];
-        unit<DT, VEC>(ring_row<VEC>(row, pz, n), k[i], z);
-        if (by_row) {
-          float g[8];
-          param_unit<DT, VEC>(a.gate_cs ? ring_row<VEC>(row, pg, n) : nullptr, a.pdtype, k[i], g1, g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) z[j] *= g[j];
+        for (int i = 0; i < V; ++i) {
+          float z[8];
+          unit<DT, VEC>(ring_row<VEC>(ring.at, pz, n), k[i], z);
+          v += k[i].on ? dot8(z, z) : 0.0f;
         }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = fmaf(b * z[j], mix[i][j], r[i][j]);
-        put_unit<DT, VEC>(out, k[i], r[i]);
       }
-      if (has_pre) v[1] += k[i].on ? dot8(r[i], r[i]) : 0.0f;
+      return v;
+    };
+    // A token's gate is read a row ahead.
+    float sz = 0.0f, next_gate = by_row && !a.gate_cs && rows > 0 ? param<DT>(a.gate, a.pdtype, first * a.gate_rs) : 0.0f;
+    if (rows > 0) {
+      float v[2] = {sum_z(0), 0.0f};
+      add(v);
+      sz = v[0];
     }
-    add(v);
-    if (t < p.n && n + p.S < rows) ring_fill<VEC>(ring, slot, row);
-    sz = v[0];
-    if (has_pre) {
-      const float q = rsqrtf(v[1] * inv + a.eps);
+    for (int n = 0; n < rows; ++n, out += out_step, y += y_step) {
+      unsigned char* row = ring.at;
+      const int slot = ring.s;
+      ring_next(p, ring);
+      float v[2] = {0.0f, 0.0f};
+      if (n + 1 < rows) v[0] = sum_z(n + 1);
+      float r[V][8];
+      const float b = has_post ? rsqrtf(sz * inv + a.eps) : 1.0f;
+      const float g1 = next_gate;
+      if (by_row && !a.gate_cs && n + 1 < rows) next_gate = param<DT>(a.gate, a.pdtype, (first + (n + 1) * step) * a.gate_rs);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
+        unit<DT, VEC>(ring_row<VEC>(row, px, n), k[i], r[i]);
+        if (has_z) {
+          float z[8];
+          unit<DT, VEC>(ring_row<VEC>(row, pz, n), k[i], z);
+          if (by_row) {
+            float g[8];
+            param_unit<DT, VEC>(a.gate_cs ? ring_row<VEC>(row, pg, n) : nullptr, a.pdtype, k[i], g1, g);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] *= q * pre[i][j];
-        put_unit<DT, VEC>(y, k[i], r[i]);
+            for (int j = 0; j < 8; ++j) z[j] *= g[j];
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[i][j] = fmaf(b * z[j], mix[i][j], r[i][j]);
+          put_unit<DT, VEC>(out, k[i], r[i]);
+        }
+        if (has_pre) v[1] += k[i].on ? dot8(r[i], r[i]) : 0.0f;
+      }
+      add(v);
+      if (t < p.n && n + p.S < rows) ring_fill<VEC>(ring, slot, row);
+      sz = v[0];
+      if (has_pre) {
+        const float q = rsqrtf(v[1] * inv + a.eps);
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[i][j] *= q * pre[i][j];
+          put_unit<DT, VEC>(y, k[i], r[i]);
+        }
       }
     }
+  };
+  // (In rows that are not whole vectors all but the last warps have no feature
+  // past the end, and are compiled for that.)
+  bool whole = !VEC;
+#pragma unroll
+  for (int i = 0; i < V; ++i) whole = whole && __all_sync(0xffffffffu, k[i].on == 0xFFu);
+  if (whole) {
+    Cols w[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) w[i] = Cols{k[i].c, 0xFFu};
+    all_rows(w);
+  } else {
+    all_rows(k);
   }
 }
 
@@ -499,105 +515,111 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     add(v);
     if (WIDE) cross(v);
   };
-  // The i-th row, in the next slot: r, dy, z, and sum r^2, sum dy w_pre r, sum z^2.
-  float x[8], dy[8], n[8];
-  auto arrive = [&](int i, float (&v)[4]) {
-    const bool came = ring_wait(ring);
-    if (has_pre) {
-      unit<DT, VEC>(ring_row<VEC>(ring.at, pr, i), cs, x);
-      unit<DT, VEC>(ring_row<VEC>(ring.at, pdy, i), cs, dy);
-      v[0] = dot8(x, x);
-      float w[8];
+  // The rows.  In rows that are not whole vectors all but the last warp have no
+  // feature past the end, and are compiled for that.
+  auto all_rows = [&](const Cols cs) __attribute__((always_inline)) {
+    // The i-th row, in the next slot: r, dy, z, and sum r^2, sum dy w_pre r, sum z^2.
+    float x[8], dy[8], n[8];
+    auto arrive = [&](int i, float (&v)[4]) {
+      const bool came = ring_wait(ring);
+      if (has_pre) {
+        unit<DT, VEC>(ring_row<VEC>(ring.at, pr, i), cs, x);
+        unit<DT, VEC>(ring_row<VEC>(ring.at, pdy, i), cs, dy);
+        v[0] = dot8(x, x);
+        float w[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) w[j] = dy[j] * pre[j];
-      v[1] = dot8(x, w);
-    }
-    if (has_z) unit<DT, VEC>(ring_row<VEC>(ring.at, pz, i), cs, n);
-    if (has_post) v[2] = dot8(n, n);
-    if (VEC && !on) v[0] = v[1] = v[2] = 0.0f;
-    if (!came) v[0] = v[2] = __int_as_float(0x7fc00000);
-  };
-  // A token's gate is read a row ahead.
-  float next_gate = token && rows > 0 ? a.scale * param<DT>(a.gate, a.pdtype, first * a.gate_rs) : 1.0f;
-  float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (rows > 0) {
-    arrive(0, s);
-    sums4(s);
-  }
-  for (int i = 0; i < rows; ++i, dxp += dx_step, dzp += dz_step) {
-    unsigned char* row = ring.at;
-    const int slot = ring.s;
-    ring_next(p, ring);
-    float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d[8];
-    if (has_dr) {
-      unit<DT, VEC>(ring_row<VEC>(row, pdr, i), cs, d);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = 0.0f;
-    }
-    if (has_pre) {
-      const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * (q * q * q);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float qd = q * dy[j];
-        d[j] = fmaf(qd, pre[j], fmaf(-k, x[j], d[j]));
-        apre[j] = fmaf(qd, x[j], apre[j]);
+        for (int j = 0; j < 8; ++j) w[j] = dy[j] * pre[j];
+        v[1] = dot8(x, w);
       }
-      put_unit<DT, VEC>(dxp, cs, d);
+      if (has_z) unit<DT, VEC>(ring_row<VEC>(ring.at, pz, i), cs, n);
+      if (has_post) v[2] = dot8(n, n);
+      if (VEC && !on) v[0] = v[1] = v[2] = 0.0f;
+      if (!came) v[0] = v[2] = __int_as_float(0x7fc00000);
+    };
+    // A token's gate is read a row ahead.
+    float next_gate = token && rows > 0 ? a.scale * param<DT>(a.gate, a.pdtype, first * a.gate_rs) : 1.0f;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (rows > 0) {
+      arrive(0, s);
+      sums4(s);
     }
-    // d becomes D c, n is b z (without z: dz = scale dx).
-    const float b = has_post ? rsqrtf(s[2] * inv + a.eps) : 1.0f;
-    float bn[8];
-    const float gate = next_gate;   // scale times a token's gate, or 1
-    if (has_z) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) bn[j] = n[j] * b;
-    }
-    if (by_row) {
-      const long long m = first + i * step;
-      float g[8], u[8];
-      if (token && i + 1 < rows) next_gate = a.scale * param<DT>(a.gate, a.pdtype, (m + step) * a.gate_rs);
-      param_unit<DT, VEC>(full_gate ? ring_row<VEC>(row, pg, i) : nullptr, a.pdtype, cs, gate, g);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (full_gate) g[j] *= a.scale;
-        u[j] = d[j] * bn[j];
-        apost[j] = fmaf(u[j], g[j], apost[j]);
-        u[j] *= post[j];
-        d[j] *= g[j] * post[j];
-      }
-      if (token) {
-        v[3] = ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));   // sum D n w_post: dgate's
+    for (int i = 0; i < rows; ++i, dxp += dx_step, dzp += dz_step) {
+      unsigned char* row = ring.at;
+      const int slot = ring.s;
+      ring_next(p, ring);
+      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, d[8];
+      if (has_dr) {
+        unit<DT, VEC>(ring_row<VEC>(row, pdr, i), cs, d);
       } else {
-        v[3] = dot8(d, bn);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) u[j] *= a.scale;
-        if (DT == DETFFN_F32 || a.pdtype == DT) put_unit<DT, VEC>(static_cast<E*>(a.dgate) + m * H + col, cs, u);
-        else put_unit<DETFFN_F32, VEC>(static_cast<float*>(a.dgate) + m * H + col, cs, u);
+        for (int j = 0; j < 8; ++j) d[j] = 0.0f;
       }
-    } else {
+      if (has_pre) {
+        const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * (q * q * q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float qd = q * dy[j];
+          d[j] = fmaf(qd, pre[j], fmaf(-k, x[j], d[j]));
+          apre[j] = fmaf(qd, x[j], apre[j]);
+        }
+        put_unit<DT, VEC>(dxp, cs, d);
+      }
+      // d becomes D c, n is b z (without z: dz = scale dx).
+      const float b = has_post ? rsqrtf(s[2] * inv + a.eps) : 1.0f;
+      float bn[8];
+      const float gate = next_gate;   // scale times a token's gate, or 1
       if (has_z) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) apost[j] = fmaf(d[j], bn[j], apost[j]);
+        for (int j = 0; j < 8; ++j) bn[j] = n[j] * b;
       }
+      if (by_row) {
+        const long long m = first + i * step;
+        float g[8], u[8];
+        if (token && i + 1 < rows) next_gate = a.scale * param<DT>(a.gate, a.pdtype, (m + step) * a.gate_rs);
+        param_unit<DT, VEC>(full_gate ? ring_row<VEC>(row, pg, i) : nullptr, a.pdtype, cs, gate, g);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] *= c[j];
-      if (has_post) v[3] = dot8(d, bn);
-    }
-    if (VEC && !on) v[3] = 0.0f;
-    // The next row's sums share this row's barrier.
-    if (i + 1 < rows) arrive(i + 1, v);
-    sums4(v);
-    if (t < p.n && i + p.S < rows) ring_fill<VEC>(ring, slot, row);
-    if (token && t == 0 && rank == 0) put_param<DT>(a.dgate, a.pdtype, first + i * step, a.scale * v[3]);
-    if (has_post) {
-      const float k = gate * v[3] * inv * b;
+        for (int j = 0; j < 8; ++j) {
+          if (full_gate) g[j] *= a.scale;
+          u[j] = d[j] * bn[j];
+          apost[j] = fmaf(u[j], g[j], apost[j]);
+          u[j] *= post[j];
+          d[j] *= g[j] * post[j];
+        }
+        if (token) {
+          v[3] = ((u[0] + u[1]) + (u[2] + u[3])) + ((u[4] + u[5]) + (u[6] + u[7]));   // sum D n w_post: dgate's
+        } else {
+          v[3] = dot8(d, bn);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) d[j] = fmaf(b, d[j], -k * bn[j]);
+          for (int j = 0; j < 8; ++j) u[j] *= a.scale;
+          if (DT == DETFFN_F32 || a.pdtype == DT) put_unit<DT, VEC>(static_cast<E*>(a.dgate) + m * H + col, cs, u);
+          else put_unit<DETFFN_F32, VEC>(static_cast<float*>(a.dgate) + m * H + col, cs, u);
+        }
+      } else {
+        if (has_z) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) apost[j] = fmaf(d[j], bn[j], apost[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] *= c[j];
+        if (has_post) v[3] = dot8(d, bn);
+      }
+      if (VEC && !on) v[3] = 0.0f;
+      // The next row's sums share this row's barrier.
+      if (i + 1 < rows) arrive(i + 1, v);
+      sums4(v);
+      if (t < p.n && i + p.S < rows) ring_fill<VEC>(ring, slot, row);
+      if (token && t == 0 && rank == 0) put_param<DT>(a.dgate, a.pdtype, first + i * step, a.scale * v[3]);
+      if (has_post) {
+        const float k = gate * v[3] * inv * b;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(b, d[j], -k * bn[j]);
+      }
+      if (has_dz) put_unit<DT, VEC>(dzp, cs, d);
+      s[0] = v[0], s[1] = v[1], s[2] = v[2];
     }
-    if (has_dz) put_unit<DT, VEC>(dzp, cs, d);
-    s[0] = v[0], s[1] = v[1], s[2] = v[2];
-  }
+  };
+  if (!VEC && __all_sync(0xffffffffu, cs.on == 0xFFu)) all_rows(Cols{cs.c, 0xFFu});
+  else all_rows(cs);
   // The CTA's column sums: its groups' added in order (the rings are done
   // with, so their memory holds them).  Little code, as it runs once and cold:
   // unrolled per kind and group it took 3 us more.
@@ -708,7 +730,7 @@ cudaError_t ring_launch(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
 // 4.3, 4864 rows 14.0 and 11.3), always where the other kernel would have
 // several units to a thread (H = 8192, 8 rows: 4.1 and 4.0), and always for rows
 // that are not whole vectors (H = 1031: one row 3.6 and 3.3 us, 16384 rows 100
-// and 50).
+// and 44).
 inline bool ring_forward(const JoinArgs& a, const RingPlan& p, bool vec) {
   return !vec || a.M * p.row >= 4 << 20 || a.H > 4096;
 }
