@@ -53,15 +53,17 @@ __device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v
 // remainder gives that (Markstein, "Computation of elementary functions on the
 // IBM RISC System/6000 processor", 1990); scales so small that a step could
 // underflow divide instead.
+constexpr float kPlainScale = 1e-30f;
+__device__ __forceinline__ uint32_t code_at(float v, float s, float inv) {   // (s >= kPlainScale)
+  const float t = v * inv;
+  return __float_as_uint(fmaf(fmaf(-t, s, v), inv, t) + kMagic);
+}
 template <int N>
 __device__ __forceinline__ void code_bits(const float (&v)[N], float s, uint32_t (&q)[N]) {
   const float inv = __fdividef(1.0f, s);
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    const float t = v[j] * inv;
-    q[j] = __float_as_uint(fmaf(fmaf(-t, s, v[j]), inv, t) + kMagic);
-  }
-  if (s < 1e-30f) {
+  for (int j = 0; j < N; ++j) q[j] = code_at(v[j], s, inv);
+  if (s < kPlainScale) {
 #pragma unroll
     for (int j = 0; j < N; ++j)
       q[j] = __float_as_uint(fminf(fmaxf(rintf(__fdiv_rn(v[j], s)), -127.0f), 127.0f) + kMagic);
@@ -202,9 +204,11 @@ __global__ void __launch_bounds__(kThreads) k_pack_vec(const __grid_constant__ C
 
 // Any row length and alignment: a warp takes four blocks, a lane features
 // lane and lane + 32 of each (64 bytes of a row to an access), of gate and up.
-// Bound by issue, as every element is loaded, coded and stored by itself: 4096 x
-// 12283 BF16 109 us (42 % of the copy rate).  Aligned vectors whose blocks' maxima meet in shared memory
-// by atomics took 121.
+// Bound by issue, as every element is loaded, coded and stored by itself; four
+// whole blocks of one row, which most are, share an address and need no tests
+// (4096 x 12283 BF16: 109 us without that case, 77 so, 60 % of the copy
+// rate; aligned vectors whose blocks' maxima meet in shared memory by atomics
+// took 121).
 template <int DT>
 __global__ void __launch_bounds__(kThreads) k_pack_any(const __grid_constant__ CkptArgs a, uint32_t blocks, Div nb) {
   grid_dep_wait();
@@ -213,48 +217,64 @@ __global__ void __launch_bounds__(kThreads) k_pack_any(const __grid_constant__ C
   const int lane = threadIdx.x & 31;
   const uint32_t step = gridDim.x * (kThreads / 32) * 4;
   for (uint32_t b0 = (blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5)) * 4; b0 < blocks; b0 += step) {
-    long long at[4];
-    int n[4];
-    float v[8][2];     // value 2 i + k: block i of gate (0) or up (1)
-    uint32_t top[8];
+    const uint32_t m0 = quotient(b0, nb), c0 = (b0 - m0 * nb.d) * kCkptBlock;
+    const long long at0 = (long long)m0 * a.I + c0 + lane;
+    auto four = [&](const bool whole) __attribute__((always_inline)) {
+      long long at[4];
+      int n[4];
+      float v[8][2];     // value 2 i + k: block i of gate (0) or up (1)
+      uint32_t top[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t b = min(b0 + i, blocks - 1), m = quotient(b, nb), c = (b - m * nb.d) * kCkptBlock;
-      at[i] = (long long)m * a.I + c + lane;
-      n[i] = (int)min(a.I - c, (long long)kCkptBlock) - lane;
+      for (int i = 0; i < 4; ++i) {
+        if (whole) {
+          at[i] = at0 + 64 * i;
+          n[i] = 64;
+        } else {
+          const uint32_t b = min(b0 + i, blocks - 1), m = quotient(b, nb), c = (b - m * nb.d) * kCkptBlock;
+          at[i] = (long long)m * a.I + c + lane;
+          n[i] = (int)min(a.I - c, (long long)kCkptBlock) - lane;
+        }
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const E* p = static_cast<const E*>(k ? a.up : a.gate) + at[i];
-        v[2 * i + k][0] = n[i] > 0 ? Io<DT>::ld(p) : 0.0f;
-        v[2 * i + k][1] = n[i] > 32 ? Io<DT>::ld(p + 32) : 0.0f;
+        for (int k = 0; k < 2; ++k) {
+          const E* p = static_cast<const E*>(k ? a.up : a.gate) + at[i];
+          v[2 * i + k][0] = n[i] > 0 ? Io<DT>::ld(p) : 0.0f;
+          v[2 * i + k][1] = n[i] > 32 ? Io<DT>::ld(p + 32) : 0.0f;
+        }
       }
-    }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top[i] = max(mag_bits(v[i][0]), mag_bits(v[i][1]));
-    // Lane l ends with the largest of value l & 7 (each exchange halves what a
-    // lane carries), and every lane then fetches all eight.
+      for (int i = 0; i < 8; ++i) top[i] = max(mag_bits(v[i][0]), mag_bits(v[i][1]));
+      // Lane l ends with the largest of value l & 7 (each exchange halves what a
+      // lane carries), and every lane then fetches all eight.
 #pragma unroll
-    for (int d = 0; d < 3; ++d) {
-      const bool up = lane >> d & 1;
+      for (int d = 0; d < 3; ++d) {
+        const bool up = lane >> d & 1;
 #pragma unroll
-      for (int i = 0; i < 4 >> d; ++i) {
-        const uint32_t lo = top[2 * i], hi = top[2 * i + 1];
-        top[i] = max(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, 1 << d));
+        for (int i = 0; i < 4 >> d; ++i) {
+          const uint32_t lo = top[2 * i], hi = top[2 * i + 1];
+          top[i] = max(up ? hi : lo, __shfl_xor_sync(0xffffffffu, up ? lo : hi, 1 << d));
+        }
       }
-    }
-    top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], 8));
-    top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], 16));
-    const float mine = scale_of(top[0]);
-    if (lane < 8 && b0 + (lane >> 1) < blocks) (lane & 1 ? a.us : a.gs)[b0 + (lane >> 1)] = mine;
+      top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], 8));
+      top[0] = max(top[0], __shfl_xor_sync(0xffffffffu, top[0], 16));
+      const float mine = scale_of(top[0]);
+      if (lane < 8 && (whole || b0 + (lane >> 1) < blocks)) (lane & 1 ? a.us : a.gs)[b0 + (lane >> 1)] = mine;
+      const float inv = __fdividef(1.0f, mine);
+      const bool plain = __all_sync(0xffffffffu, mine >= kPlainScale);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float s = __shfl_sync(0xffffffffu, mine, i);
-      uint32_t q[2] = {0, 0};
-      if (s > 0.0f) code_bits(v[i], s, q);
-      int8_t* p = (i & 1 ? a.uq : a.gq) + at[i >> 1];
-      if (n[i >> 1] > 0) p[0] = (int8_t)q[0];
-      if (n[i >> 1] > 32) p[32] = (int8_t)q[1];
-    }
+      for (int i = 0; i < 8; ++i) {
+        const float s = __shfl_sync(0xffffffffu, mine, i), r = __shfl_sync(0xffffffffu, inv, i);
+        uint32_t q[2] = {code_at(v[i][0], s, r), code_at(v[i][1], s, r)};
+        if (!plain) {   // (a scale is 0, NaN or tiny)
+          q[0] = q[1] = 0;
+          if (s > 0.0f) code_bits(v[i], s, q);
+        }
+        int8_t* p = (i & 1 ? a.uq : a.gq) + at[i >> 1];
+        if (n[i >> 1] > 0) p[0] = (int8_t)q[0];
+        if (n[i >> 1] > 32) p[32] = (int8_t)q[1];
+      }
+    };
+    if (c0 + 4 * kCkptBlock <= a.I) four(true);
+    else four(false);
   }
 }
 
