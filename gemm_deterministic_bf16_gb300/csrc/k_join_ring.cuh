@@ -34,7 +34,7 @@ namespace join {
 
 constexpr int kRingBytes = 208 * 1024;   // shared memory for rows
 constexpr int kRingMaxStages = 8;
-constexpr int kRingMaxGroups = 16;       // 512 threads; groups of several warps (at most 8) have a named barrier each
+constexpr int kRingMaxGroups = 16;       // groups of several warps (at most 10) have a named barrier each
 constexpr int kRingSets = kJoinSets;     // CTAs, whatever the GPU: column sums are taken per CTA
 
 struct RingPlan {
@@ -50,18 +50,18 @@ struct RingPlan {
 };
 
 // Sums of N = 2 or 4 values over a group of G threads (whole warps, at most
-// 16), the same in every thread, in an order fixed by G.  Stage one halves the
+// 20), the same in every thread, in an order fixed by G.  Stage one halves the
 // values a lane carries with every exchange, so that lane l ends with the
 // warp's sum of value l % N; stage two adds the warps the same way, through
-// [2][16 N] floats.  One barrier; one warp alone: none but __syncwarp.
-template <int N>
+// [2][20 N] floats.  One barrier; one warp alone: none but __syncwarp.
+template <int N, int THREADS = 512>
 struct GroupSums {
   static_assert(N == 2 || N == 4, "");
   float *put, *get;     // this thread's places, now in the first half
-  int other = 16 * N;   // the other half, from there
+  int other = 20 * N;   // the other half, from there
   int warps, barrier, threads;
   bool odd, high;
-  // `buf`: 32 N floats of the group.
+  // `buf`: 40 N floats of the group.
   __device__ __forceinline__ GroupSums(float* buf, int G, int group, int t) {
     const int lane = t & 31;
     put = buf + (t >> 5) * N + lane;
@@ -86,6 +86,7 @@ struct GroupSums {
       asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
       x = warps > 0 ? get[0] : 0.0f;
       if (N == 4) x += warps > 32 ? get[32] : 0.0f;
+      if (N == 4 && THREADS > 512) x += warps > 64 ? get[64] : 0.0f;
       put += other;
       get += other;
       other = -other;
@@ -246,7 +247,7 @@ template <int DT, int V, bool PLAIN, bool VEC>
 __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kRingMaxGroups * kRingMaxStages];
-  __shared__ float sums[8 * 64];   // (groups of several warps: at most 8)
+  __shared__ float sums[8 * 80];   // (groups of several warps: at most 8)
   using E = typename Io<DT>::E;
   const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H;
   const bool has_z = PLAIN || a.z.p, has_post = PLAIN || a.w_post, has_pre = PLAIN || a.w_pre;
@@ -257,7 +258,7 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
   const long long first = (long long)blockIdx.x * p.R + group, step = (long long)gridDim.x * p.R;
   unsigned char* base = smem + group * p.S * p.row;
   Ring1 ring{base, base, full + group * p.S};
-  GroupSums<2> add(sums + (G == 32 ? 0 : group * 64), G, group, t);
+  GroupSums<2> add(sums + (G == 32 ? 0 : group * 80), G, group, t);
   ring_init(p, ring, t, first, step, 0, H);
   __syncwarp();
   grid_dep_wait();
@@ -441,11 +442,11 @@ __host__ __device__ inline uint32_t has_of(const JoinArgs& a) {
 // of a gate that is the same for every row have the factors scale gate and
 // scale w_post of sum D n, so one accumulator serves both.  A row's r, dy and z
 // are converted once and stay in registers over the barrier of its first sums.
-template <int DT, uint32_t HAS, bool VEC, bool WIDE>
-__global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
+template <int DT, uint32_t HAS, bool VEC, bool WIDE, int THREADS = 512>
+__global__ void __launch_bounds__(THREADS, 1) k_bwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kRingMaxGroups * kRingMaxStages];
-  __shared__ float sums[8 * 128];   // (groups of several warps: at most 8)
+  __shared__ float sums[10 * 160];   // (groups of several warps: at most 10)
   using E = typename Io<DT>::E;
   const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H;
   int rank = 0;
@@ -464,7 +465,7 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
   const long long first = set * p.R + group, step = sets * p.R;
   unsigned char* base = smem + group * p.S * p.row;
   Ring1 ring{base, base, full + group * p.S};
-  GroupSums<4> add(sums + (G == 32 ? 0 : group * 128), G, group, t);
+  GroupSums<4, THREADS> add(sums + (G == 32 ? 0 : group * 160), G, group, t);
   ring_init(p, ring, t, first, step, col, width);
   __syncwarp();
   grid_dep_wait();
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
     auto put = [&](const float (&w)[8]) {
       // (a group's columns: G 8 floats, in their own order)
       if (p.R == 1) put_unit<DETFFN_F32, VEC>(a.part + (kind * sets + set) * H + col, cs, w);
-      else put_unit<DETFFN_F32, VEC>(all + kind * 4096 + group * G * 8, cs, w);
+      else put_unit<DETFFN_F32, VEC>(all + kind * 5120 + group * G * 8, cs, w);
       ++kind;
     };
     // (apost: sum dx n, and with a gate of each row sum dx n scale gate)
@@ -656,7 +657,7 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
       for (int i = threadIdx.x; i < H; i += blockDim.x) {
         float v = 0.0f;
 #pragma unroll 1
-        for (int q = 0; q < p.R; ++q) v += all[kind * 4096 + q * G * 8 + i];
+        for (int q = 0; q < p.R; ++q) v += all[kind * 5120 + q * G * 8 + i];
         part[i] = v;
       }
   }
@@ -678,9 +679,9 @@ __global__ void __launch_bounds__(512, 1) k_bwd_ring(const __grid_constant__ Joi
 // The ring's layout for rows of these tensors; false where fewer than two
 // rows fit a group's ring.  V: units to a thread.
 template <int DT>
-bool ring_plan(const JoinArgs& a, bool back, bool vec, int V, RingPlan* out) {
+bool ring_plan(const JoinArgs& a, bool back, bool vec, int V, int threads, RingPlan* out) {
   RingPlan p;
-  const int es = Io<DT>::kBytes, ps = a.pdtype == DETFFN_F32 ? 4 : 2, threads = 512;
+  const int es = Io<DT>::kBytes, ps = a.pdtype == DETFFN_F32 ? 4 : 2;
   if (back)
     while (a.H > p.C * threads * 8 && p.C < 8) p.C *= 2;
   p.width = ((a.H + p.C - 1) / p.C + 7) / 8 * 8;
@@ -704,6 +705,7 @@ bool ring_plan(const JoinArgs& a, bool back, bool vec, int V, RingPlan* out) {
   // 38 the last two wait for a second round, 2432 x 16384 198 us and 110 so.)
   const int most = p.C == 4 ? 36 : p.C == 8 ? 15 : kRingSets / p.C;
   p.R = p.C > 1 ? 1 : threads / p.G;
+  if (p.R > kRingMaxGroups) p.R = kRingMaxGroups;
   if (p.R > (a.M + most - 1) / most) p.R = (int)((a.M + most - 1) / most);
   p.S = kRingBytes / (p.R * p.row);
   if (p.S < 2) return false;
@@ -720,7 +722,8 @@ template <auto K>
 cudaError_t ring_launch(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
   static const cudaError_t setup = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
   if (setup != cudaSuccess) return setup;
-  const int smem = p.R * p.S * p.row > 49152 ? p.R * p.S * p.row : 49152;   // (48 KB: the groups' column sums)
+  const int least = 3 * 5120 * 4;   // the groups' column sums
+  const int smem = p.R * p.S * p.row > least ? p.R * p.S * p.row : least;
   return launch_cluster(K, dim3(p.grid), p.G * p.R, smem, p.C, st, a, p);
 }
 
@@ -740,7 +743,7 @@ cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
   const bool vec = vectors<DT>(a);
   RingPlan p;
   const bool two = vec ? a.H >= 512 : a.H > 4096;   // units to a thread
-  if (ring_plan<DT>(a, false, vec, two ? 2 : 1, &p) && ring_forward(a, p, vec)) {
+  if (ring_plan<DT>(a, false, vec, two ? 2 : 1, 512, &p) && ring_forward(a, p, vec)) {
     const bool plain = a.z.p && a.w_post && a.w_pre && !(a.gate && a.gate_rs);
     if (vec) {
       if (two) return plain ? ring_launch<k_fwd_ring<DT, 2, true, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 2, false, true>>(a, p, st);
@@ -759,6 +762,28 @@ cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
   return go(vec ? k_fwd<DT, 8, true> : k_fwd<DT, 8, false>);
 }
 
+// Whether a backward pass takes 640 threads instead of 512 to a CTA, and 96
+// registers a thread instead of 128: with one norm its values fit, and a row of
+// 5120 features needs no second CTA (BF16, the pre-norm alone, 8192 x 5120: 118 us
+// with 512, 70 with 640; 8192 x 2560: 49 and 37; shorter rows even).  With z
+// beside the pre-norm registers spill (16384 x 1024, a gate per feature: 36 and
+// 49), which pays for rows of more than 4096 features alone (8192 x 5120, a gate
+// per token: 150 and 118).  768 threads are slower (16384 x 1024: 33 and 41).
+template <int DT>
+bool one_norm(uint32_t has, int H) {
+  if (DT == DETFFN_F32 || H > 5120 || !(has & kDr) || !(has & kDz)) return false;
+  if ((has & kPre) && (has & kPost)) return false;
+  if ((has & kPre) && (has & kZ)) return H > 4096;
+  return (has & (kPre | kPost)) != 0;
+}
+template <int DT, uint32_t HAS>
+cudaError_t wide_cta(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
+  // (one_norm holds for no other pass)
+  if constexpr (DT != DETFFN_F32 && HAS != kAny && !((HAS & kPre) && (HAS & kPost)))
+    return ring_launch<k_bwd_ring<DT, HAS, true, false, 640>>(a, p, st);
+  else return cudaErrorInvalidConfiguration;
+}
+
 template <uint32_t H>
 using Kind = std::integral_constant<uint32_t, H>;
 
@@ -766,16 +791,18 @@ template <int DT>
 cudaError_t backward(const JoinArgs& a, cudaStream_t st) {
   const bool vec = vectors<DT>(a);
   RingPlan p;
-  if (!ring_plan<DT>(a, true, vec, 1, &p)) return cudaErrorInvalidConfiguration;   // (two rows always fit)
-  const int sets = p.grid / p.C;
-  // The passes that are compiled for what they have.
   uint32_t has = has_of(a);
   if (!(has & kPost) && !a.dgate) has &= ~kZ;   // (z is not read)
+  const int threads = vec && one_norm<DT>(has, a.H) ? 640 : 512;
+  if (!ring_plan<DT>(a, true, vec, 1, threads, &p)) return cudaErrorInvalidConfiguration;   // (two rows always fit)
+  const int sets = p.grid / p.C;
+  // The passes that are compiled for what they have.
   cudaError_t e = cudaErrorInvalidConfiguration;
   auto one = [&](auto h) {
     constexpr uint32_t HAS = decltype(h)::value;
     if (HAS != kAny && HAS != has) return false;
     if (p.C > 1) e = vec ? ring_launch<k_bwd_ring<DT, HAS, true, true>>(a, p, st) : ring_launch<k_bwd_ring<DT, HAS, false, true>>(a, p, st);
+    else if (threads > 512) e = wide_cta<DT, HAS>(a, p, st);
     else e = vec ? ring_launch<k_bwd_ring<DT, HAS, true, false>>(a, p, st) : ring_launch<k_bwd_ring<DT, HAS, false, false>>(a, p, st);
     return true;
   };
