@@ -20,7 +20,7 @@
 // is eight features 32 apart, a warp's 256 in a row, so that a warp's accesses
 // to shared and global memory stay together wherever the row begins.  What
 // bounds these is issue, an instruction or two for each element where a
-// vector's eight share one (16384 x 1031: 44 us forward, 59 backward, 46 and 51 %
+// vector's eight share one (16384 x 1031: 36 us forward, 59 backward, 55 and 51 %
 // of the copy rate).
 #pragma once
 
@@ -236,22 +236,39 @@ __device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) 
   return s + q;
 }
 
+// What a pass has, when it is compiled for it (backward: z where it is read).  A
+// pass compiled for any of it tests bits as it goes, and each test ends a run of
+// instructions that the compiler can interleave: BF16, backward, 8192 x 4096, only
+// the post-norm 73 us so and 47 compiled for it; only the pre-norm 86 and 57;
+// both, 16384 x 2048, a gate per token 114 and 94, forward 57 and 53;
+// forward, 16384 x 1031, 44 and 36.
+enum Has : uint32_t { kZ = 1, kPost = 2, kPre = 4, kDr = 8, kDz = 16, kFull = 32, kToken = 64, kAny = 0 };
+
+__host__ __device__ inline uint32_t has_of(const JoinArgs& a) {
+  return (a.z.p ? kZ : 0u) | (a.w_post ? kPost : 0u) | (a.w_pre ? kPre : 0u) | (a.dr.p ? kDr : 0u) | (a.dz.p ? kDz : 0u) |
+         (a.gate && a.gate_rs ? a.gate_cs ? kFull : kToken : 0u);
+}
+
 // One sum and one barrier a row: the sum over z of the next row is taken
 // together with the sum over out of this one.  A slot's row is read twice,
 // once for each, and its slot is free after the barrier of the second.
 //
 // Forward.  V units to a thread: two where a row of units fills two warps, which
-// halves what a row costs beside its elements.  PLAIN: both norms, and a gate
-// (if any) that is the same for every row.
-template <int DT, int V, bool PLAIN, bool VEC>
+// halves what a row costs beside its elements.
+template <int DT, int V, uint32_t HAS, bool VEC>
 __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kRingMaxGroups * kRingMaxStages];
   __shared__ float sums[8 * 80];   // (groups of several warps: at most 8)
   using E = typename Io<DT>::E;
   const int G = p.G, group = threadIdx.x / G, t = threadIdx.x - group * G, H = a.H;
-  const bool has_z = PLAIN || a.z.p, has_post = PLAIN || a.w_post, has_pre = PLAIN || a.w_pre;
-  const bool by_row = !PLAIN && a.gate && a.gate_rs;
+  uint32_t has = HAS;
+  if (HAS == kAny) {
+    has = has_of(a);
+    asm volatile("" : "+r"(has));   // (one register, so that a test is one instruction)
+  }
+  const bool has_z = has & kZ, has_post = has & kPost, has_pre = has & kPre, full_gate = has & kFull, token = has & kToken;
+  const bool by_row = full_gate || token;
   Cols k[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) k[i] = cols_of<VEC>(i, G, t, H);
@@ -324,7 +341,7 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
           unit<DT, VEC>(ring_row<VEC>(row, pz, n), k[i], z);
           if (by_row) {
             float g[8];
-            param_unit<DT, VEC>(a.gate_cs ? ring_row<VEC>(row, pg, n) : nullptr, a.pdtype, k[i], g1, g);
+            param_unit<DT, VEC>(full_gate ? ring_row<VEC>(row, pg, n) : nullptr, a.pdtype, k[i], g1, g);
 #pragma unroll
             for (int j = 0; j < 8; ++j) z[j] *= g[j];
           }
@@ -421,21 +438,9 @@ struct ClusterSums {
   }
 };
 
-// What a backward pass has, when it is compiled for it: dr and dz always, and
-// z where it is read.  A pass compiled for any of it tests bits as it goes, and
-// each test ends a run of instructions that the compiler can interleave: BF16,
-// 8192 x 4096, only the post-norm 73 us so and 47 compiled for it; only the
-// pre-norm 86 and 57; both, 16384 x 2048, a gate per token 114 and 94.
-enum Has : uint32_t { kPost = 2, kPre = 4, kZ = 1, kDr = 8, kDz = 16, kFull = 32, kToken = 64, kAny = 0 };
-
-__host__ __device__ inline uint32_t has_of(const JoinArgs& a) {
-  return (a.z.p ? kZ : 0u) | (a.w_post ? kPost : 0u) | (a.w_pre ? kPre : 0u) | (a.dr.p ? kDr : 0u) | (a.dz.p ? kDz : 0u) |
-         (a.dgate && a.gate_rs ? a.gate_cs ? kFull : kToken : 0u);
-}
-
-// Backward, one unit to a thread.  HAS: what there is (kAny: found out).  WIDE: a cluster of CTAs shares each row
-// of more than 4096 features, a run of columns each, and the row's sums meet
-// in shared memory across it.
+// Backward, one unit to a thread.  WIDE: a cluster of CTAs shares each row of
+// more than 4096 features, a run of columns each, and the row's sums meet in
+// shared memory across it.
 //
 // With n = b z, D = dx and c = scale gate w_post, a row needs sum D c n, and
 // then dz = b D c - (sum D c n) b / H n.  The sums over tokens of dw_post and
@@ -733,10 +738,13 @@ cudaError_t ring_launch(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
 // 4.3, 4864 rows 14.0 and 11.3), always where the other kernel would have
 // several units to a thread (H = 8192, 8 rows: 4.1 and 4.0), and always for rows
 // that are not whole vectors (H = 1031: one row 3.6 and 3.3 us, 16384 rows 100
-// and 44).
+// and 36).
 inline bool ring_forward(const JoinArgs& a, const RingPlan& p, bool vec) {
   return !vec || a.M * p.row >= 4 << 20 || a.H > 4096;
 }
+
+template <uint32_t H>
+using Kind = std::integral_constant<uint32_t, H>;
 
 template <int DT>
 cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
@@ -744,12 +752,30 @@ cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
   RingPlan p;
   const bool two = vec ? a.H >= 512 : a.H > 4096;   // units to a thread
   if (ring_plan<DT>(a, false, vec, two ? 2 : 1, 512, &p) && ring_forward(a, p, vec)) {
-    const bool plain = a.z.p && a.w_post && a.w_pre && !(a.gate && a.gate_rs);
-    if (vec) {
-      if (two) return plain ? ring_launch<k_fwd_ring<DT, 2, true, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 2, false, true>>(a, p, st);
-      return plain ? ring_launch<k_fwd_ring<DT, 1, true, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 1, false, true>>(a, p, st);
-    }
-    return two ? ring_launch<k_fwd_ring<DT, 2, false, false>>(a, p, st) : ring_launch<k_fwd_ring<DT, 1, false, false>>(a, p, st);
+    // The passes that are compiled for what they have: a unit to a thread of rows
+    // that are not whole vectors and two of those that are, and else both norms
+    // with a gate (if any) that is the same for every row.
+    const uint32_t has = has_of(a);
+    cudaError_t e = cudaErrorInvalidConfiguration;
+    auto one = [&](auto h) {
+      constexpr uint32_t HAS = decltype(h)::value;
+      if (HAS != kAny && HAS != has) return false;
+      if constexpr (HAS == kAny || HAS == (kPost | kPre | kZ)) {
+        if (two != vec) {
+          e = vec ? ring_launch<k_fwd_ring<DT, 1, HAS, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 2, HAS, false>>(a, p, st);
+          return true;
+        }
+      } else if (two != vec) {
+        return false;
+      }
+      e = vec ? ring_launch<k_fwd_ring<DT, 2, HAS, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 1, HAS, false>>(a, p, st);
+      return true;
+    };
+    auto any_of = [&](auto... h) { return (one(h) || ...); };
+    any_of(Kind<kPost | kPre | kZ>{}, Kind<kPost | kPre | kZ | kToken>{}, Kind<kPost | kPre | kZ | kFull>{},
+           Kind<kPost | kZ>{}, Kind<kPost | kZ | kToken>{}, Kind<kPost | kZ | kFull>{},
+           Kind<kPre | kZ>{}, Kind<kPre | kZ | kToken>{}, Kind<kPre | kZ | kFull>{}, Kind<kPre>{}, Kind<kAny>{});
+    return e;
   }
   // Few rows of whole vectors, or rows of more than 8192 features.
   const int units = (a.H + 7) / 8, v = units <= 512 ? 1 : units <= 2048 ? 4 : 8;
@@ -783,9 +809,6 @@ cudaError_t wide_cta(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
     return ring_launch<k_bwd_ring<DT, HAS, true, false, 640>>(a, p, st);
   else return cudaErrorInvalidConfiguration;
 }
-
-template <uint32_t H>
-using Kind = std::integral_constant<uint32_t, H>;
 
 template <int DT>
 cudaError_t backward(const JoinArgs& a, cudaStream_t st) {
