@@ -1,7 +1,7 @@
 // k_join.cuh -- the norms before and after a block joined with its gate and
-// residual scale: the formulas, the forward kernel for few rows or very wide
-// ones, and the sums over row sets (each k_join_*.cu instantiates one element
-// type; k_join_ring.cuh has the kernels for the rest).
+// residual scale: the formulas, the forward kernel for few rows, and the sums
+// over row sets (each k_join_*.cu instantiates one element type;
+// k_join_ring.cuh has the kernels for the rest).
 //
 // Forward, for each token (a row of H features):
 //   n   = z / sqrt(mean(z^2) + eps) * w_post      (the norm after the block; n = z without w_post)
@@ -28,56 +28,26 @@
 namespace detffn {
 namespace join {
 
-// A thread's 8 V features of a row: with VEC unit i is features
-// 8 (i G + t) .. + 7 (16-byte accesses), else features (8 i + j) G + t.
-template <bool VEC>
-__device__ __forceinline__ int col(int i, int j, int G, int t) {
-  return VEC ? 8 * (i * G + t) + j : (8 * i + j) * G + t;
-}
-
-template <int DT, bool VEC>
-__device__ __forceinline__ void load(const void* base, long long off, int H, int i, int G, int t, float (&v)[8]) {
+// Features c .. c + 7 of a row or a parameter; zeros past the row's end.
+template <int DT>
+__device__ __forceinline__ void load(const void* base, long long off, int c, int H, float (&v)[8]) {
   using E = typename Io<DT>::E;
-  const E* p = static_cast<const E*>(base) + off;
-  if (VEC) {
-    const int c = col<VEC>(i, 0, G, t);
-    if (c < H) {
-      Io<DT>::ld8(p + c, v);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-    }
+  if (c < H) {
+    Io<DT>::ld8(static_cast<const E*>(base) + off + c, v);
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = col<VEC>(i, j, G, t);
-      v[j] = c < H ? Io<DT>::ld(p + c) : 0.0f;
-    }
+    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
   }
 }
-
-template <int DT, bool VEC>
-__device__ __forceinline__ void store(void* base, long long off, int H, int i, int G, int t, const float (&v)[8]) {
-  using E = typename Io<DT>::E;
-  E* p = static_cast<E*>(base) + off;
-  if (VEC) {
-    const int c = col<VEC>(i, 0, G, t);
-    if (c < H) Io<DT>::st8(p + c, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int c = col<VEC>(i, j, G, t);
-      if (c < H) Io<DT>::st(p + c, v[j]);
-    }
-  }
+template <int DT>
+__device__ __forceinline__ void store(void* base, long long off, int c, int H, const float (&v)[8]) {
+  if (c < H) Io<DT>::st8(static_cast<typename Io<DT>::E*>(base) + off + c, v);
 }
-
-// A parameter vector, in the elements' type or in FP32.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_param(const void* base, int pdtype, long long off, int H, int i, int G, int t,
-                                           float (&v)[8]) {
-  if (DT == DETFFN_F32 || pdtype == DT) load<DT, VEC>(base, off, H, i, G, t, v);
-  else load<DETFFN_F32, VEC>(base, off, H, i, G, t, v);
+// A parameter, in the elements' type or in FP32.
+template <int DT>
+__device__ __forceinline__ void load_param(const void* base, int pdtype, long long off, int c, int H, float (&v)[8]) {
+  if (DT == DETFFN_F32 || pdtype == DT) load<DT>(base, off, c, H, v);
+  else load<DETFFN_F32>(base, off, c, H, v);
 }
 
 template <int DT>
@@ -91,81 +61,63 @@ __device__ __forceinline__ void put_param(void* base, int pdtype, long long i, f
   else static_cast<float*>(base)[i] = v;
 }
 
-// The gate's values for unit i of token m.
-template <int DT, bool VEC>
-__device__ __forceinline__ void load_gate(const JoinArgs& a, long long m, int H, int i, int G, int t, float (&v)[8]) {
-  if (a.gate_cs) {
-    load_param<DT, VEC>(a.gate, a.pdtype, m * a.gate_rs, H, i, G, t, v);
-  } else {
-    const float g = param<DT>(a.gate, a.pdtype, m * a.gate_rs);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = g;
-  }
-}
-
-// One block of threads to a row, V units to a thread, the row in registers.
-// Bound by latency (its loads, two sums): one row of 4096 features, BF16, 3.0 us.
-template <int DT, int V, bool VEC>
+// A few rows of whole 16-byte vectors and at most 4096 features: one block of
+// threads to a row, eight features to a thread, in registers.  Bound by latency,
+// so all of a row's loads go out before its sums (one row of 4096 features, BF16:
+// 3.1 us).
+template <int DT>
 __global__ void __launch_bounds__(512) k_fwd(const __grid_constant__ JoinArgs a) {
   __shared__ float buf[2 * 32];
   grid_dep_wait();
   grid_dep_launch();
-  const int G = blockDim.x, t = threadIdx.x, H = a.H;
+  const int c = 8 * threadIdx.x, H = a.H;
   const float inv = 1.0f / (float)H;
   int turn = 0;
+  auto gate_of = [&](long long m, float (&g)[8]) {
+    if (!a.gate) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = 1.0f;
+    } else if (a.gate_cs) {
+      load_param<DT>(a.gate, a.pdtype, m * a.gate_rs, c, H, g);
+    } else {
+      const float one = param<DT>(a.gate, a.pdtype, m * a.gate_rs);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g[j] = one;
+    }
+  };
+  float post[8], pre[8], gate[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) post[j] = pre[j] = 1.0f;
+  if (a.w_post) load_param<DT>(a.w_post, a.pdtype, 0, c, H, post);
+  if (a.w_pre) load_param<DT>(a.w_pre, a.pdtype, 0, c, H, pre);
+  if (!a.gate_rs) gate_of(0, gate);
   for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
-    float r[V][8];
-#pragma unroll
-    for (int i = 0; i < V; ++i) load<DT, VEC>(a.x.p, m * a.x.ld, H, i, G, t, r[i]);
+    float r[8], n[8];
+    load<DT>(a.x.p, m * a.x.ld, c, H, r);
+    if (a.z.p) load<DT>(a.z.p, m * a.z.ld, c, H, n);
+    if (a.gate_rs) gate_of(m, gate);
     if (a.z.p) {
-      float n[V][8];
-#pragma unroll
-      for (int i = 0; i < V; ++i) load<DT, VEC>(a.z.p, m * a.z.ld, H, i, G, t, n[i]);
+      float b = 1.0f;
       if (a.w_post) {
         float s[1] = {0.0f};
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) s[0] = fmaf(n[i][j], n[i][j], s[0]);
+        for (int j = 0; j < 8; ++j) s[0] = fmaf(n[j], n[j], s[0]);
         block_sums<1>(s, buf, turn);
-        const float b = rsqrtf(s[0] * inv + a.eps);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-          float w[8];
-          load_param<DT, VEC>(a.w_post, a.pdtype, 0, H, i, G, t, w);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) n[i][j] *= b * w[j];
-        }
+        b = rsqrtf(s[0] * inv + a.eps);
       }
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float g[8];
-        if (a.gate) {
-          load_gate<DT, VEC>(a, m, H, i, G, t, g);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) n[i][j] *= g[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] = fmaf(a.scale, n[i][j], r[i][j]);
-        store<DT, VEC>(const_cast<void*>(a.out.p), m * a.out.ld, H, i, G, t, r[i]);
-      }
+      for (int j = 0; j < 8; ++j) r[j] = fmaf(a.scale, n[j] * (b * post[j]) * gate[j], r[j]);
+      store<DT>(const_cast<void*>(a.out.p), m * a.out.ld, c, H, r);
     }
     if (a.w_pre) {
       float s[1] = {0.0f};
 #pragma unroll
-      for (int i = 0; i < V; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] = fmaf(r[i][j], r[i][j], s[0]);
+      for (int j = 0; j < 8; ++j) s[0] = fmaf(r[j], r[j], s[0]);
       block_sums<1>(s, buf, turn);
       const float q = rsqrtf(s[0] * inv + a.eps);
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        float w[8];
-        load_param<DT, VEC>(a.w_pre, a.pdtype, 0, H, i, G, t, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) r[i][j] *= q * w[j];
-        store<DT, VEC>(const_cast<void*>(a.y.p), m * a.y.ld, H, i, G, t, r[i]);
-      }
+      for (int j = 0; j < 8; ++j) r[j] *= q * pre[j];
+      store<DT>(const_cast<void*>(a.y.p), m * a.y.ld, c, H, r);
     }
   }
 }

@@ -249,13 +249,72 @@ __host__ __device__ inline uint32_t has_of(const JoinArgs& a) {
          (a.gate && a.gate_rs ? a.gate_cs ? kFull : kToken : 0u);
 }
 
+__device__ __forceinline__ void cluster_barrier() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// Sums over the CTAs of a cluster: each CTA's four values (the same in all its
+// threads) go to every CTA's shared memory, count there against a barrier of
+// that CTA, and are added by rank.  `buf`: [2][8][4] floats; `bars`: one for each
+// half, of one arrival.  Two halves are enough: a CTA sends exchange k + 2 only
+// after every other has sent k + 1, and with it read k.  (With a barrier of the
+// cluster instead 4864 x 8192 takes 146 us, and so 103.)
+struct ClusterSums {
+  float* buf;
+  uint64_t* bars;
+  int C, rank, half = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void operator()(float (&v)[4]) {
+    float* b = buf + half * 32;
+    uint64_t* bar = bars + half;
+    if ((int)threadIdx.x < C) {
+      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, 16u * C);
+      asm volatile(
+          "{\n\t.reg .b32 a, m;\n\t"
+          "mapa.shared::cluster.u32 a, %0, %2;\n\t"
+          "mapa.shared::cluster.u32 m, %1, %2;\n\t"
+          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [m];\n\t}" ::"r"(
+              smem_u32(b + rank * 4)),
+          "r"(smem_u32(bar)), "r"(threadIdx.x), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
+          : "memory");
+    }
+    // Every CTA of the cluster has started and takes the same rows, so the wait
+    // ends; it is bounded all the same, and would read as NaN.
+    bool came = false;
+    for (long long i = 0; i < kDefaultSpin && !came; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{\n\t.reg .pred p;\n\t"
+          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+          "selp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(phase)
+          : "memory");
+      came = ok != 0;
+    }
+    float4 t = *reinterpret_cast<const float4*>(b);
+    for (int r = 1; r < C; ++r) {
+      const float4 o = *reinterpret_cast<const float4*>(b + r * 4);
+      t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
+    }
+    v[0] = came ? t.x : __int_as_float(0x7fc00000);
+    v[1] = t.y;
+    v[2] = came ? t.z : __int_as_float(0x7fc00000);
+    v[3] = t.w;
+    phase ^= (uint32_t)half;
+    half ^= 1;
+  }
+};
+
 // One sum and one barrier a row: the sum over z of the next row is taken
 // together with the sum over out of this one.  A slot's row is read twice,
 // once for each, and its slot is free after the barrier of the second.
 //
 // Forward.  V units to a thread: two where a row of units fills two warps, which
-// halves what a row costs beside its elements.
-template <int DT, int V, uint32_t HAS, bool VEC>
+// halves what a row costs beside its elements.  WIDE: a cluster of CTAs shares
+// each row of more than 8192 features, as in the backward pass.
+template <int DT, int V, uint32_t HAS, bool VEC, bool WIDE = false>
 __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ JoinArgs a, const __grid_constant__ RingPlan p) {
   extern __shared__ __align__(128) unsigned char smem[];
   __shared__ uint64_t full[kRingMaxGroups * kRingMaxStages];
@@ -269,38 +328,61 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
   }
   const bool has_z = has & kZ, has_post = has & kPost, has_pre = has & kPre, full_gate = has & kFull, token = has & kToken;
   const bool by_row = full_gate || token;
+  int rank = 0;
+  if (WIDE) asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  __shared__ __align__(16) float across[2 * 8 * 4];
+  __shared__ uint64_t crossed[2];
+  ClusterSums cross{across, crossed, p.C, rank};
+  if (WIDE && threadIdx.x == 0) {
+    mbar_init(&crossed[0], 1);
+    mbar_init(&crossed[1], 1);
+  }
+  const int col = rank * p.width, width = WIDE ? min(p.width, H - col) : H;
   Cols k[V];
 #pragma unroll
-  for (int i = 0; i < V; ++i) k[i] = cols_of<VEC>(i, G, t, H);
-  const long long first = (long long)blockIdx.x * p.R + group, step = (long long)gridDim.x * p.R;
+  for (int i = 0; i < V; ++i) k[i] = cols_of<VEC>(i, G, t, width);
+  const long long set = blockIdx.x / (WIDE ? p.C : 1), sets = gridDim.x / (WIDE ? p.C : 1);
+  const long long first = set * p.R + group, step = sets * p.R;
   unsigned char* base = smem + group * p.S * p.row;
   Ring1 ring{base, base, full + group * p.S};
-  GroupSums<2> add(sums + (G == 32 ? 0 : group * 80), G, group, t);
-  ring_init(p, ring, t, first, step, 0, H);
+  GroupSums<2> sum2(sums + (G == 32 ? 0 : group * 80), G, group, t);
+  ring_init(p, ring, t, first, step, col, width);
   __syncwarp();
   grid_dep_wait();
   grid_dep_launch();
   const int rows = p.per + (first < p.rest ? 1 : 0);   // of this group
   if (t < p.n)
     for (int s = 0; s < min(p.S, rows); ++s) ring_fill<VEC>(ring, s, base + s * p.row);
+  const long long pcol = (long long)col * (a.pdtype == DETFFN_F32 ? 4 : 2);
+  auto from = [&](const void* w) { return static_cast<const void*>(static_cast<const char*>(w) + pcol); };
   float mix[V][8], pre[V][8];      // mix: scale * gate * w_post
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     float w[8];
-    param_unit<DT, VEC>(has_pre ? a.w_pre : nullptr, a.pdtype, k[i], 1.0f, pre[i]);
-    param_unit<DT, VEC>(has_post ? a.w_post : nullptr, a.pdtype, k[i], 1.0f, w);
-    param_unit<DT, VEC>(a.gate && a.gate_cs && !by_row ? a.gate : nullptr, a.pdtype, k[i],
+    param_unit<DT, VEC>(has_pre ? from(a.w_pre) : nullptr, a.pdtype, k[i], 1.0f, pre[i]);
+    param_unit<DT, VEC>(has_post ? from(a.w_post) : nullptr, a.pdtype, k[i], 1.0f, w);
+    param_unit<DT, VEC>(a.gate && a.gate_cs && !by_row ? from(a.gate) : nullptr, a.pdtype, k[i],
                    a.gate && !a.gate_cs && !by_row ? param<DT>(a.gate, a.pdtype, 0) : 1.0f, mix[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) mix[i][j] *= a.scale * w[j];
   }
   const float inv = 1.0f / (float)H;
   // The parts of a row: x, z, gate.
-  const Part px = part_of<VEC>(p, 0, first, step, 0), pz = part_of<VEC>(p, 1, first, step, 0), pg = part_of<VEC>(p, 2, first, step, 0);
-  E* out = static_cast<E*>(const_cast<void*>(a.out.p)) + first * a.out.ld;
-  E* y = static_cast<E*>(const_cast<void*>(a.y.p)) + first * a.y.ld;
+  const Part px = part_of<VEC>(p, 0, first, step, col), pz = part_of<VEC>(p, 1, first, step, col),
+             pg = part_of<VEC>(p, 2, first, step, col);
+  E* out = static_cast<E*>(const_cast<void*>(a.out.p)) + first * a.out.ld + col;
+  E* y = static_cast<E*>(const_cast<void*>(a.y.p)) + first * a.y.ld + col;
   const long long out_step = step * a.out.ld, y_step = step * a.y.ld;
   __syncthreads();   // the barriers are initialised
+  if (WIDE) cluster_barrier();   // and every CTA of the cluster has started
+  auto add = [&](float (&v)[2]) {
+    sum2(v);
+    if (WIDE) {
+      float w[4] = {v[0], v[1], 0.0f, 0.0f};
+      cross(w);
+      v[0] = w[0], v[1] = w[1];
+    }
+  };
   auto all_rows = [&](const Cols (&k)[V]) __attribute__((always_inline)) {
     // The sum over z of the n-th row, in the next slot.
     auto sum_z = [&](int n) {
@@ -379,64 +461,6 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
     all_rows(k);
   }
 }
-
-__device__ __forceinline__ void cluster_barrier() {
-  __syncwarp();
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Sums over the CTAs of a cluster: each CTA's four values (the same in all its
-// threads) go to every CTA's shared memory, count there against a barrier of
-// that CTA, and are added by rank.  `buf`: [2][8][4] floats; `bars`: one for each
-// half, of one arrival.  Two halves are enough: a CTA sends exchange k + 2 only
-// after every other has sent k + 1, and with it read k.  (With a barrier of the
-// cluster instead 4864 x 8192 takes 146 us, and so 103.)
-struct ClusterSums {
-  float* buf;
-  uint64_t* bars;
-  int C, rank, half = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void operator()(float (&v)[4]) {
-    float* b = buf + half * 32;
-    uint64_t* bar = bars + half;
-    if ((int)threadIdx.x < C) {
-      if (threadIdx.x == 0) mbar_arrive_expect_tx(bar, 16u * C);
-      asm volatile(
-          "{\n\t.reg .b32 a, m;\n\t"
-          "mapa.shared::cluster.u32 a, %0, %2;\n\t"
-          "mapa.shared::cluster.u32 m, %1, %2;\n\t"
-          "st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.v4.f32 [a], {%3, %4, %5, %6}, [m];\n\t}" ::"r"(
-              smem_u32(b + rank * 4)),
-          "r"(smem_u32(bar)), "r"(threadIdx.x), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3])
-          : "memory");
-    }
-    // Every CTA of the cluster has started and takes the same rows, so the wait
-    // ends; it is bounded all the same, and would read as NaN.
-    bool came = false;
-    for (long long i = 0; i < kDefaultSpin && !came; ++i) {
-      uint32_t ok;
-      asm volatile(
-          "{\n\t.reg .pred p;\n\t"
-          "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-          "selp.u32 %0, 1, 0, p;\n\t}"
-          : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(phase)
-          : "memory");
-      came = ok != 0;
-    }
-    float4 t = *reinterpret_cast<const float4*>(b);
-    for (int r = 1; r < C; ++r) {
-      const float4 o = *reinterpret_cast<const float4*>(b + r * 4);
-      t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
-    }
-    v[0] = came ? t.x : __int_as_float(0x7fc00000);
-    v[1] = t.y;
-    v[2] = came ? t.z : __int_as_float(0x7fc00000);
-    v[3] = t.w;
-    phase ^= (uint32_t)half;
-    half ^= 1;
-  }
-};
 
 // Backward, one unit to a thread.  WIDE: a cluster of CTAs shares each row of
 // more than 4096 features, a run of columns each, and the row's sums meet in
@@ -687,8 +711,7 @@ template <int DT>
 bool ring_plan(const JoinArgs& a, bool back, bool vec, int V, int threads, RingPlan* out) {
   RingPlan p;
   const int es = Io<DT>::kBytes, ps = a.pdtype == DETFFN_F32 ? 4 : 2;
-  if (back)
-    while (a.H > p.C * threads * 8 && p.C < 8) p.C *= 2;
+  while (a.H > p.C * threads * 8 * V && p.C < 8) p.C *= 2;
   p.width = ((a.H + p.C - 1) / p.C + 7) / 8 * 8;
   const int units = p.width / 8;
   p.G = ((units + V - 1) / V + 31) / 32 * 32;
@@ -732,13 +755,12 @@ cudaError_t ring_launch(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
   return launch_cluster(K, dim3(p.grid), p.G * p.R, smem, p.C, st, a, p);
 }
 
-// Whether a forward pass takes the ring kernel (for up to 8192 features): it
-// wins once its rows hold about 4 MB (measured, BF16, H = 4096: 152 rows 3.3 us
-// without and 3.7 us with it, 608 rows 7.9 and 5.4; H = 1024: 1216 rows 4.1 and
-// 4.3, 4864 rows 14.0 and 11.3), always where the other kernel would have
-// several units to a thread (H = 8192, 8 rows: 4.1 and 4.0), and always for rows
-// that are not whole vectors (H = 1031: one row 3.6 and 3.3 us, 16384 rows 100
-// and 36).
+// Whether a forward pass takes the ring kernel: it wins once its rows hold about
+// 4 MB (measured, BF16, H = 4096: 152 rows 3.3 us without and 3.7 us with it, 608
+// rows 7.9 and 5.4; H = 1024: 1216 rows 4.1 and 4.3, 4864 rows 14.0 and 11.3),
+// where the other kernel would have several units to a thread (H = 8192, 8 rows:
+// 4.1 and 4.0), and for rows that are not whole vectors (H = 1031: one row 3.6 and
+// 3.3 us, 16384 rows 100 and 36).
 inline bool ring_forward(const JoinArgs& a, const RingPlan& p, bool vec) {
   return !vec || a.M * p.row >= 4 << 20 || a.H > 4096;
 }
@@ -751,7 +773,8 @@ cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
   const bool vec = vectors<DT>(a);
   RingPlan p;
   const bool two = vec ? a.H >= 512 : a.H > 4096;   // units to a thread
-  if (ring_plan<DT>(a, false, vec, two ? 2 : 1, 512, &p) && ring_forward(a, p, vec)) {
+  if (!ring_plan<DT>(a, false, vec, two ? 2 : 1, 512, &p)) return cudaErrorInvalidConfiguration;   // (two rows always fit)
+  if (ring_forward(a, p, vec)) {
     // The passes that are compiled for what they have: a unit to a thread of rows
     // that are not whole vectors and two of those that are, and else both norms
     // with a gate (if any) that is the same for every row.
@@ -761,11 +784,15 @@ cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
       constexpr uint32_t HAS = decltype(h)::value;
       if (HAS != kAny && HAS != has) return false;
       if constexpr (HAS == kAny || HAS == (kPost | kPre | kZ)) {
+        if (p.C > 1) {
+          e = vec ? ring_launch<k_fwd_ring<DT, 2, HAS, true, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 2, HAS, false, true>>(a, p, st);
+          return true;
+        }
         if (two != vec) {
           e = vec ? ring_launch<k_fwd_ring<DT, 1, HAS, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 2, HAS, false>>(a, p, st);
           return true;
         }
-      } else if (two != vec) {
+      } else if (p.C > 1 || two != vec) {
         return false;
       }
       e = vec ? ring_launch<k_fwd_ring<DT, 2, HAS, true>>(a, p, st) : ring_launch<k_fwd_ring<DT, 1, HAS, false>>(a, p, st);
@@ -777,15 +804,9 @@ cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
            Kind<kPre | kZ>{}, Kind<kPre | kZ | kToken>{}, Kind<kPre | kZ | kFull>{}, Kind<kPre>{}, Kind<kAny>{});
     return e;
   }
-  // Few rows of whole vectors, or rows of more than 8192 features.
-  const int units = (a.H + 7) / 8, v = units <= 512 ? 1 : units <= 2048 ? 4 : 8;
-  const int threads = ((units + v - 1) / v + 31) / 32 * 32;
+  // Few rows of whole vectors.
   const long long most = 152ll * 16;
-  const dim3 grid((unsigned)(a.M < most ? a.M : most));
-  auto go = [&](auto k) { return launch_dependent(k, grid, threads, 0, st, a); };
-  if (v == 1) return go(k_fwd<DT, 1, true>);
-  if (v == 4) return go(vec ? k_fwd<DT, 4, true> : k_fwd<DT, 4, false>);
-  return go(vec ? k_fwd<DT, 8, true> : k_fwd<DT, 8, false>);
+  return launch_dependent(k_fwd<DT>, dim3((unsigned)(a.M < most ? a.M : most)), ((a.H + 7) / 8 + 31) / 32 * 32, 0, st, a);
 }
 
 // Whether a backward pass takes 640 threads instead of 512 to a CTA, and 96

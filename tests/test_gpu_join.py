@@ -156,7 +156,8 @@ def test_backward(G, M, H, dt, pt, gate, post, pre):
 @pytest.mark.parametrize("gate", ["none", "feature", "scalar", "token", "full"])
 @pytest.mark.parametrize("post,pre", [(True, True), (False, True), (True, False)])
 @pytest.mark.parametrize("M,H,dt", [(10949, 264, "bf16"), (10949, 261, "f16"), (4001, 264, "f32"), (687, 4104, "bf16"),
-                                    (1301, 2560, "f16"), (900, 5120, "bf16"), (450, 9216, "bf16"), (300, 12296, "f16")])
+                                    (1301, 2560, "f16"), (900, 5120, "bf16"), (450, 9216, "bf16"), (300, 12296, "f16"),
+                                    (310, 9001, "f16")])
 def test_many_rows(G, M, H, dt, gate, post, pre):
     test_forward(G, M, H, dt, dt, gate, post, pre)
     test_backward(G, M, H, dt, dt, gate, post, pre)
