@@ -47,10 +47,10 @@
 // HBM bounds it once the weights take longer than the chain around them (of the
 // measured copy rate: 64 tokens, 6 of 64 experts, H = 4096, I = 1536, 2.4 GB of
 // weights: 367 us, 98 %; 7 tokens, 2 of 16, I = 1416: 59 to 66 us by the
-// experts hit, 75 to 85 %).  Below that the chain does: one token, 8 of 128, H = 2048, I = 768 takes 27.2
-// us, 11.4 of them for the weights; 1.5 us for the logits, 3 for the routing, 2 to
-// 3 until the first stage, 8 of gate/up, 3 until h is seen, 3 of down, 4 for the
-// sums.
+// experts hit, 75 to 85 %).  Below that the chain does: one token, 8 of 128, H =
+// 2048, I = 768 takes 27.2 us, 11.4 of them for the weights; 1.5 us for the
+// logits, 3 for the routing, 2 to 3 until the first stage, 8 of gate/up, 3 until
+// h is seen, 3 of down, 4 for the sums.
 #include <mutex>
 
 #include "elt.cuh"
