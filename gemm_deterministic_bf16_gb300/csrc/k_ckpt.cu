@@ -114,9 +114,10 @@ __device__ __forceinline__ float scale_of(uint32_t top) {
 
 // Rows of whole 8-element vectors on 16-byte boundaries: four lanes take one
 // block of 64 features, of gate and of up, lane l features 8 l .. 8 l + 7 and
-// 32 more than those: four loads under way, and three exchanges for 32 values (56
-// us at 4096 x 12288 BF16 with eight lanes and half of both, 49.6 so).  FLAT: no block is short (I a multiple of 64), so blocks
-// follow one another and nothing is divided.
+// 32 more than those: four loads under way, and three exchanges for 32 values
+// (56 us at 4096 x 12288 BF16 with eight lanes and half of both, 49.6 so).
+// FLAT: no block is short (I a multiple of 64), so blocks follow one another and
+// nothing is divided.
 template <int DT, bool FLAT>
 __global__ void __launch_bounds__(kThreads) k_pack_vec(const __grid_constant__ CkptArgs a, uint32_t blocks, Div nb) {
   grid_dep_wait();
