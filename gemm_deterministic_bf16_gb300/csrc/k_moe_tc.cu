@@ -474,11 +474,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             rok = false;
             *abort_flag = 1;
             if (g.status) atomicExch(g.status, (int)DETFFN_ERR_TIMEOUT);
-          } else {
-            fence_proxy_async_global();  // the TMA loads below read what generic stores wrote
           }
         }
         ok = __shfl_sync(0xffffffffu, (int)rok, 0) != 0;
+        __syncwarp();                // (lane 0's acquire comes before the loads of all; a shuffle orders no memory)
+        fence_proxy_async_global();  // the TMA loads below read what generic stores wrote
         if (ahead == nk && lane == 0) claimed = atomicAdd(g.claim, 1);
         // (Also after a stop: stages with their weights out get their tokens, so that each completes.)
         for (int ks = 0; ks < ahead; ++ks, rs.next(NS)) tokens(ks, rs);

@@ -240,3 +240,19 @@ def test_refusals(G):
         with pytest.raises(G.DetFFNError) as e:
             G.detffn_moe_forward(s["x"], *rest, 2, **bad)
         assert e.value.status == 1
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("T,E,k,H,I", [(7, 16, 2, 2048, 1416), (64, 32, 4, 512, 320), (1, 8, 8, 1024, 768)])
+def test_h_of_other_thread_blocks_is_seen(G, T, E, k, H, I, dt):
+    """Down units load rows of h that other thread blocks have just written.  The
+    workspace is filled with NaN before each call, so a load that came too early
+    would show."""
+    s = inputs(T, E, H, I, dt, T + 31, k)
+    rest = (s["Wr"], s["Wg"], s["Wu"], s["Wd"], k)
+    want = check(G, s, k, True, dt)
+    ws = torch.empty(G.detffn_moe_workspace_size(T, E, k, H, I, DT[dt][0]), dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        ws.fill_(255)
+        assert torch.equal(G.detffn_moe_forward(s["x"], *rest, ws=ws)[0], want)
+    assert G.detffn_get_status() == 0
