@@ -134,11 +134,20 @@ def detffn_backward_ckpt8(x, Wg, Wu, Wd, ckpt, dOut, dX=None, dWg=None, dWu=None
         return _on(stream, detffn_backward_ckpt8, x, Wg, Wu, Wd, ckpt, dOut, dX, dWg, dWu, dWd, ws, shards, path, None,
                    spin_limit, flags)
     _d._bf16(x, Wg, Wu, Wd, dOut, dX, dWg, dWu, dWd)
+    if len(x.shape) != 2 or len(Wg.shape) != 2:
+        raise ValueError("expected x [M, H] and Wg [I, H]")
     M, H = x.shape
     I = Wg.shape[0]
+    # The C call sees addresses only, so every extent is checked here.
+    for name, t, s in (("Wg", Wg, (I, H)), ("Wu", Wu, (I, H)), ("Wd", Wd, (H, I)), ("dOut", dOut, (M, H)),
+                       ("dX", dX, (M, H)), ("dWg", dWg, (I, H)), ("dWu", dWu, (I, H)), ("dWd", dWd, (H, I))):
+        if t is not None and (tuple(t.shape) != s or t.device != x.device):
+            raise ValueError("%s: expected %s on the device of x" % (name, list(s)))
     for t, dt, n in zip(ckpt, (torch.int8, torch.float32) * 2, (I, (I + 63) // 64) * 2):
-        if t.dtype != dt or t.shape != (M, n) or not t.is_contiguous() or t.device != x.device:
+        if t.dtype != dt or tuple(t.shape) != (M, n) or not t.is_contiguous() or t.device != x.device:
             raise ValueError("checkpoint: expected contiguous CUDA codes [M, I] (int8) and scales [M, ceil(I / 64)] (float32)")
+    if ws is not None and (ws.device != x.device or not ws.is_contiguous()):
+        raise ValueError("ws: expected a contiguous buffer on the device of x")
     e = lambda t, *s: torch.empty(s, dtype=torch.bfloat16, device=x.device) if t is None else t  # noqa: E731
     dX, dWg, dWu, dWd = e(dX, M, H), e(dWg, I, H), e(dWu, I, H), e(dWd, H, I)
     if ws is None:
@@ -146,7 +155,7 @@ def detffn_backward_ckpt8(x, Wg, Wu, Wd, ckpt, dOut, dX=None, dWg=None, dWu=None
     f = _d.lib().detffn_backward_ckpt8
     f.argtypes = [_d._vp] * 14 + [_d._ll] * 3 + [_d._vp, ctypes.c_size_t, _d._vp, ctypes.POINTER(_d.Options)]
     p = [t.data_ptr() for t in (x, Wg, Wu, Wd, *ckpt, dOut, dX, dWg, dWu, dWd)]
-    _d._check(f(_d.handle(x.device), *p, M, H, I, ws.data_ptr(), ws.numel(),
+    _d._check(f(_d.handle(x.device), *p, M, H, I, ws.data_ptr(), ws.numel() * ws.element_size(),
                 torch.cuda.current_stream(x.device).cuda_stream, _d._opts(path, shards, spin_limit, flags)),
               "detffn_backward_ckpt8")
     return dX, dWg, dWu, dWd

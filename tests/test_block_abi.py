@@ -4,6 +4,7 @@ workspaces.  The pointers below are made up and never read."""
 import ctypes
 
 import pytest
+import torch
 
 F32, F16, BF16 = 0, 1, 2
 OK, INVALID, SHAPE, ALIGN, UNSUPPORTED, WORKSPACE = range(6)
@@ -125,3 +126,43 @@ def test_workspace_sizes(call):
 
 def test_moe_without_a_handle(call):
     assert call("detffn_moe_forward", None, *A[:8], 1, 8, 2, 1, 64, 64, BF16, A[8], 1 << 20, None, None) == INVALID
+
+
+class _OnGpu:
+    """What a contiguous CUDA tensor shows to the checks; it has no memory."""
+    is_cuda = True
+
+    def __init__(self, shape, dtype=torch.bfloat16, device="cuda:0"):
+        self.shape, self.dtype, self.device = torch.Size(shape), dtype, torch.device(device)
+
+    def is_contiguous(self):
+        return True
+
+
+@pytest.mark.parametrize("bad", [
+    dict(Wu=_OnGpu((128, 256))), dict(Wu=_OnGpu((256, 192))), dict(Wd=_OnGpu((192, 256))), dict(Wd=_OnGpu((256, 128))),
+    dict(dOut=_OnGpu((4, 256))), dict(dOut=_OnGpu((8, 192))), dict(dOut=_OnGpu((8 * 256,))), dict(dX=_OnGpu((4, 256))),
+    dict(dWg=_OnGpu((128, 256))), dict(dWu=_OnGpu((192, 255))), dict(dWd=_OnGpu((192, 256))), dict(x=_OnGpu((2, 4, 256))),
+    dict(x=_OnGpu((8 * 256,))), dict(Wg=_OnGpu((192,))), dict(Wg=_OnGpu((192, 128))), dict(Wu=_OnGpu((192, 256), device="cuda:1")),
+    dict(dOut=_OnGpu((8, 256), device="cuda:1")), dict(dWd=_OnGpu((256, 192), device="cuda:1")),
+    dict(ws=_OnGpu((1 << 30,), torch.uint8, "cuda:1")), dict(ws=_OnGpu((1 << 30,), torch.uint8, "cpu")),
+    dict(gate_codes=_OnGpu((4, 192), torch.int8)), dict(up_scales=_OnGpu((8, 4), torch.float32)),
+    dict(up_codes=_OnGpu((8, 192), torch.int8, "cuda:1"))])
+def test_backward_ckpt8_checks_every_extent(monkeypatch, bad):
+    """Tensors whose extents do not fit are refused before any address is taken."""
+    from gemm_deterministic_bf16_gb300 import block, detffn
+
+    def reached(*_):
+        raise AssertionError("the call went past its checks")
+    for name in ("lib", "handle", "workspace"):
+        monkeypatch.setattr(detffn, name, reached)
+    M, H, I = 8, 256, 192
+    t = dict(x=_OnGpu((M, H)), Wg=_OnGpu((I, H)), Wu=_OnGpu((I, H)), Wd=_OnGpu((H, I)), dOut=_OnGpu((M, H)),
+             dX=_OnGpu((M, H)), dWg=_OnGpu((I, H)), dWu=_OnGpu((I, H)), dWd=_OnGpu((H, I)), ws=None)
+    c = dict(gate_codes=_OnGpu((M, I), torch.int8), gate_scales=_OnGpu((M, 3), torch.float32),
+             up_codes=_OnGpu((M, I), torch.int8), up_scales=_OnGpu((M, 3), torch.float32))
+    with pytest.raises(AssertionError):   # what fits gets there
+        block.detffn_backward_ckpt8(ckpt=block.Ckpt8(**c), **t)
+    (t if next(iter(bad)) in t else c).update(bad)
+    with pytest.raises(ValueError):
+        block.detffn_backward_ckpt8(ckpt=block.Ckpt8(**c), **t)
