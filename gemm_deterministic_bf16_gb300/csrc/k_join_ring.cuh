@@ -585,7 +585,8 @@ __global__ void __launch_bounds__(THREADS, 1) k_bwd_ring(const __grid_constant__
         for (int j = 0; j < 8; ++j) d[j] = 0.0f;
       }
       if (has_pre) {
-        const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * (q * q * q);
+        // (in this order: q^3 alone leaves FP32's range for rows of 2e15 on)
+        const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * q * q * q;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float qd = q * dy[j];

@@ -315,3 +315,29 @@ def test_refusals(G):
                                ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 5
     assert np.isfinite(float(G.detffn_join_forward(x, z)[0].float().sum()))  # still works
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, True), (True, False)])
+@pytest.mark.parametrize("M,H", [(6, 256), (5, 1031), (3, 8192)])
+@pytest.mark.parametrize("size,eps", [(1e17, 1e-6), (1e15, 1e-6), (1e13, 1e-6), (1e-6, 0.0), (1e-13, 0.0), (1e-16, 0.0),
+                                      (1e-15, 1e-30)])
+def test_rows_far_from_one(G, size, eps, M, H, post, pre, dt):
+    """Rows whose cube leaves FP32's range while their squares' sum stays in it.
+    dy goes along r and dr's part along z, so that the projections taken off are
+    as large as what they are taken from; the bounds are those of the other tests."""
+    s = inputs(M, H, dt, "f32", "feature", M + H, post, pre)
+    s["x"], s["z"] = (s["x"].float() * size).to(DT[dt][0]), (s["z"].float() * size).to(DT[dt][0])
+    unit = lambda t: t.float() / size  # noqa: E731
+    if pre:
+        s["dy"] = (s["dy"].float() * 0.1 + unit(s["x"])).to(DT[dt][0])
+        s["dr"] = (s["dr"].float() / size * 0.1 + unit(s["z"]) / size).to(DT[dt][0])
+    out, y = G.detffn_join_forward(s["x"], s["z"], s["w_post"], s["gate"], 0.75, s["w_pre"], eps)
+    r, mag, yr = forward64(s["x"], s["z"], s["w_post"], s["gate"], 0.75, s["w_pre"], eps)
+    close(out, r, mag, dt, 64)
+    if pre:
+        rms = (r.square().mean(-1, keepdim=True) + eps).sqrt()
+        close(y, yr, mag / rms * d(s["w_pre"]).abs() + yr.abs(), dt, 150)
+    got = G.detffn_join_backward(s["x"], s["z"], s["dr"], s["dy"], s["w_post"], s["gate"], 0.75, s["w_pre"], eps)
+    for name, (v, m) in backward64(s, s["x"], 0.75, eps).items():
+        close(getattr(got, name), v, m, "f32" if name in ("dw_pre", "dw_post", "dgate") else dt, 350)
