@@ -340,10 +340,11 @@ MoeArgs moe_plan(Arena& w, long long T, long long E, long long k, long long H, l
   a.pair = w.take<int>(T * k);
   a.first = w.take<int>(E + 1);
   a.h = w.take<char>(T * k * I * 4);
-  sc->counters = w.take<int>(1 + E + (H + 127) / 128);
+  sc->counters = w.take<int>(1 + E + (H + 127) / 128 + T * k);
   int parts = 1, stages = 0;
   moe_parts(H, I, &parts, &stages);
   sc->y = w.take<float>(parts * T * k * H);
+  if (dtype == DETFFN_F16) sc->h32 = w.take<float>(T * k * I);
   return a;
 }
 

@@ -36,13 +36,17 @@
 // to 32.  A down unit's pairs are neighbours in h, and one box of 8, 16, 32 or
 // 64 rows takes them; the rows past the unit's are other units' and are not
 // used, whatever they hold.  h goes to the down projection as two terms, its
-// rounding to the stored type and the rounding of what that left (16 bits of
-// BF16, 22 of FP16), both multiplied into the same accumulator: with one term
-// the rounding of h alone doubles the variance of out's error (1.41 times the
-// error of one rounding, measured), and the second costs only tensor time,
-// which is idle here.  A row's sum over K is one accumulation in FP32 in
-// tensor memory, whatever the other columns are, so a token's result does not
-// depend on the other tokens.
+// rounding to the stored type and the rounding of what that left, in columns of
+// their own, which meet when y is read out: with one term the rounding of h
+// alone doubles the variance of out's error (1.41 times the error of one
+// rounding, measured), and the second costs only tensor time, which is idle
+// here.  BF16 has FP32's range, so the two hold 16 bits of any h.  FP16 has
+// not: each term has a power of two of its own (Terms below), which holds 16
+// bits of h from 2^-13 to 2^23 and 2^-29 below.  A pair whose largest |h| lies
+// outside that range (or is not finite) is multiplied again at the end, on the
+// CUDA cores from h in FP32; its columns on the tensor cores are not used.  A
+// row's sum over K is one accumulation in FP32 in tensor memory, whatever the
+// other columns are, so a token's result does not depend on the other tokens.
 //
 // HBM bounds it once the weights take longer than the chain around them (of the
 // measured copy rate: 64 tokens, 6 of 64 experts, H = 4096, I = 1536, 2.4 GB of
@@ -99,6 +103,8 @@ struct Args {
   int* ready;        // [E] gate/up units done
   int* tickets;      // [tb] down units done
   float* y;          // [parts][T * k][H]
+  unsigned* top;     // [T * k] FP16: bits of the largest |h| of each pair
+  float* h32;        // [T * k][I] FP16: h
   int* status;
   long long spin;
   int stall;
@@ -169,6 +175,56 @@ __device__ __forceinline__ Tables tables_at(unsigned char* p, int E, int P) {
   t.id = reinterpret_cast<uint16_t*>(t.w + P);
   t.pos = t.id + P;
   return t;
+}
+
+// h as two terms of the stored type, and y of the two terms' sums.
+template <int DT> struct Terms;
+template <> struct Terms<DETFFN_BF16> {
+  static constexpr float kMax = 0x1.fep127f;   // the largest BF16: h may round beyond it
+  __device__ static float first(float h) { return Io<DETFFN_BF16>::round(fminf(fmaxf(h, -kMax), kMax)); }
+  // (An infinity or a NaN of h is the second term's.)
+  __device__ static float second(float h, float first) { return h - first; }
+  __device__ static float sum(float y1, float y2) { return y1 + y2; }
+};
+template <> struct Terms<DETFFN_F16> {
+  // Of |h| <= 2^23 the first is at most 2^15, and the second, 16 times what its
+  // rounding left (half of 2^4 2^8 at most), too.
+  static constexpr float kTop = 0x1p23f, kLow = 0x1p-13f;   // the largest |h| of a pair that they are for
+  __device__ static float first(float h) { return Io<DETFFN_F16>::round(h * 0x1p-8f); }
+  __device__ static float second(float h, float first) { return (h - first * 0x1p8f) * 0x1p4f; }
+  __device__ static float sum(float y1, float y2) { return fmaf(y1, 0x1p8f, y2 * 0x1p-4f); }
+  // `top`: bits of a pair's largest |h|.
+  __device__ static bool hold(uint32_t top) {
+    return top == 0u || (top >= __float_as_uint(kLow) && top <= __float_as_uint(kTop));
+  }
+};
+
+// y of one pair on the CUDA cores: products of h in FP32 with `rows` (at most
+// 128) rows of weights, by one warp; lane l ends with those of rows 4 l ..
+// 4 l + 3.  Out of line, as it is hardly ever called.
+template <int DT>
+__device__ __noinline__ float4 down_rows(const typename Io<DT>::E* w, const float* h, long long I, int rows, int lane) {
+  float4 mine = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 1
+  for (int f = 0; 4 * f < rows; ++f, w += 4 * I) {
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 1
+    for (long long k = 8 * lane; k < I; k += 256) {
+      const float4 a0 = __ldcg(reinterpret_cast<const float4*>(h + k)), a1 = __ldcg(reinterpret_cast<const float4*>(h + k) + 1);
+      const float a[8] = {a0.x, a0.y, a0.z, a0.w, a1.x, a1.y, a1.z, a1.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float b[8];
+        Io<DT>::ld8(w + i * I + k, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i] = fmaf(a[j], b[j], s[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = warp_sum(s[i]);
+    if (lane == f) mine = make_float4(s[0], s[1], s[2], s[3]);
+  }
+  return mine;
 }
 
 // Rows of h that a down unit of n pairs loads, by one box.
@@ -599,7 +655,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               if (here >> i & 1)
-                g.y[((long long)q.part * P + q.p0 + c0 + i) * m.H + r] = __uint_as_float(v[i]) + __uint_as_float(v2[i]);
+                g.y[((long long)q.part * P + q.p0 + c0 + i) * m.H + r] =
+                    Terms<DT>::sum(__uint_as_float(v[i]), __uint_as_float(v2[i]));
           }
         } else {
           // Gate rows are lanes 0 .. R - 1 of tensor memory and up rows R .. 2 R -
@@ -611,27 +668,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           epi_sync();
           const int f = et & (R - 1);
           const long long r = q.tile * (long long)R + f;
-          if (r < m.I) {
+          const bool in = r < m.I;
 #pragma unroll 1
-            for (int i0 = et / R; i0 < 8; i0 += 256 / R) {
-              float gt[2], hv[2];
+          for (int i0 = et / R; i0 < 8; i0 += 256 / R) {
+            float gt[2], hv[2];
 #pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const float* at = xch + (i0 + b * (128 / R)) * 128 + f;
-                gt[b] = at[0];
-                hv[b] = at[R];
+            for (int b = 0; b < 2; ++b) {
+              const float* at = xch + (i0 + b * (128 / R)) * 128 + f;
+              gt[b] = at[0];
+              hv[b] = at[R];
+            }
+#pragma unroll
+            for (int b = 0; b < 2; ++b) hv[b] *= __fdividef(gt[b], 1.0f + __expf(-gt[b]));
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              const int i = i0 + b * (128 / R);   // (the same in all threads of a warp)
+              if (!(here >> i & 1)) continue;
+              const int place = q.p0 + __popcll(cols & ((1ull << (c0 + i)) - 1ull));
+              if constexpr (DT == DETFFN_F16) {
+                const unsigned top = __reduce_max_sync(0xffffffffu, in ? __float_as_uint(fabsf(hv[b])) : 0u);
+                if (lane == 0) atomicMax(g.top + place, top);
+                if (in) g.h32[place * m.I + r] = hv[b];
               }
-#pragma unroll
-              for (int b = 0; b < 2; ++b) hv[b] *= __fdividef(gt[b], 1.0f + __expf(-gt[b]));
-#pragma unroll
-              for (int b = 0; b < 2; ++b) {
-                const int i = i0 + b * (128 / R);
-                if (!(here >> i & 1)) continue;
-                El* at = static_cast<El*>(m.h) + (q.p0 + __popcll(cols & ((1ull << (c0 + i)) - 1ull))) * m.I + r;
-                Io<DT>::st(at, hv[b]);
-                const float left = hv[b] - Io<DT>::round(hv[b]);
-                // (Beyond the stored type's range the first term is an infinity and stays one.)
-                Io<DT>::st(at + P * m.I, fabsf(left) <= 3.4e38f ? left : 0.0f);
+              if (in) {
+                El* at = static_cast<El*>(m.h) + place * m.I + r;
+                const float first = Terms<DT>::first(hv[b]);
+                Io<DT>::st(at, first);
+                Io<DT>::st(at + P * m.I, Terms<DT>::second(hv[b], first));
               }
             }
           }
@@ -688,9 +751,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
       __syncwarp();   // (lane 0's acquire comes before the reads of all)
+      if (!ok) continue;
       const long long r = tile * 128ll + 4 * lane;
-      if (!ok || r >= m.H) continue;
-      const float* y = g.y + r;
+      const float* y = g.y + min(r, m.H - 4);   // (lanes past the last feature read the last and write nothing)
+      // The choices whose h the two terms do not hold.  (Released with `ready`,
+      // which the down units that were waited for have acquired.)
+      unsigned again = 0;
+      if constexpr (DT == DETFFN_F16)
+        again = __ballot_sync(0xffffffffu, lane < m.k && !Terms<DT>::hold(__ldcg(g.top + t.pos[tk * m.k + min(lane, m.k - 1)])));
       float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), one = s;
       int j = tk * m.k, part = 0;      // of the next read
       int ja = j, parta = 0;           // of the next addition
@@ -712,6 +780,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float4 v = mine[i * 32];
           one = parta == 0 ? v : make_float4(one.x + v.x, one.y + v.y, one.z + v.z, one.w + v.w);
           if (++parta == g.parts) {
+            if constexpr (DT == DETFFN_F16) {
+              if (again >> (ja - tk * m.k) & 1)
+                one = down_rows<DT>(static_cast<const El*>(m.Wd) + (t.id[ja] * m.H + tile * 128ll) * m.I, g.h32 + t.pos[ja] * m.I,
+                                    m.I, (int)min(128ll, m.H - tile * 128ll), lane);
+            }
             const float w = t.w[ja];
             s = make_float4(fmaf(w, one.x, s.x), fmaf(w, one.y, s.y), fmaf(w, one.z, s.z), fmaf(w, one.w, s.w));
             parta = 0;
@@ -719,8 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      *reinterpret_cast<uint2*>(static_cast<El*>(m.out) + tk * m.H + r) =
-          make_uint2(Io<DT>::pair(s.x, s.y), Io<DT>::pair(s.z, s.w));
+      if (r < m.H)
+        *reinterpret_cast<uint2*>(static_cast<El*>(m.out) + tk * m.H + r) =
+            make_uint2(Io<DT>::pair(s.x, s.y), Io<DT>::pair(s.z, s.w));
     }
   }
 
@@ -771,10 +845,12 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   g.ready = sc.counters + 1;
   g.tickets = g.ready + m.E;
   g.y = sc.y;
+  g.top = reinterpret_cast<unsigned*>(g.tickets + g.tb);
+  g.h32 = sc.h32;
   g.status = wt.status;
   g.spin = wt.spin;
   g.stall = wt.stall;
-  cudaError_t e = launch_moe_logits(m, sc.counters, 1 + m.E + g.tb, st);
+  cudaError_t e = launch_moe_logits(m, sc.counters, 1 + m.E + g.tb + (f16 ? m.T * m.k : 0), st);
   if (e != cudaSuccess) return e;
   const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * ((m.I + 31) / 32 + g.tb * g.parts);
   const int grid = (int)(most < sm_count ? most : sm_count);

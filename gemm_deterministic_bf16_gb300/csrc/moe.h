@@ -27,11 +27,13 @@ struct MoeArgs {
   void* h = nullptr;
 };
 
-// More workspace: the tensor kernel's counters [1 + E + ceil(H / 128)], and the
-// pairs' outputs y [parts][T * k][H] in FP32 (the general kernels use one part).
+// More workspace: the tensor kernel's counters [1 + E + ceil(H / 128) + T * k],
+// the pairs' outputs y [parts][T * k][H] in FP32 (the general kernels use one
+// part), and for FP16 the tensor kernel's h in FP32, [T * k][I].
 struct MoeScratch {
   int* counters = nullptr;
   float* y = nullptr;
+  float* h32 = nullptr;
 };
 
 // Router logits; block 0 clears n counters.

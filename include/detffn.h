@@ -451,8 +451,11 @@ DETFFN_API detffn_status detffn_backward_ckpt8(detffn_handle h, const void* x, c
  * x [T, H], Wr [E, H], Wg, Wu [E, I, H], Wd [E, H, I], out [T, H], contiguous,
  * of `dtype`.  experts (int) and weights (FP32) [T, top_k] receive the
  * routing where not NULL.  Sums are FP32, the hidden activation keeps at least
- * 16 significant bits, and out is rounded once.  A token's result does not depend on the other tokens of
- * the call.  A NaN logit is taken first and makes the token's weights NaN.
+ * 16 significant bits (FP16 on the tensor cores: of each value, or of 2^-13 where
+ * that is more, of a pair whose largest lies in [2^-13, 2^23]; all other pairs
+ * keep FP32), and out is rounded once.  A token's result does not depend on the
+ * other tokens of the call.  A NaN logit is taken first and makes the token's
+ * weights NaN.
  * options->path: EXACT takes the CUDA-core kernels (any sizes and types).
  * `ws` is of detffn_moe_workspace_size bytes, 256-byte aligned. */
 DETFFN_API detffn_status detffn_moe_workspace_size(long long T, long long E, int top_k, long long H, long long I,

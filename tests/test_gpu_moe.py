@@ -256,3 +256,80 @@ def test_h_of_other_thread_blocks_is_seen(G, T, E, k, H, I, dt):
         ws.fill_(255)
         assert torch.equal(G.detffn_moe_forward(s["x"], *rest, ws=ws)[0], want)
     assert G.detffn_get_status() == 0
+
+
+def moe64_wide(s, ids, w, u):
+    """As moe64, with the bound of h as the header states it: 2^-16 of a value, or of
+    2^-13 where that is more."""
+    x = s["x"].double()
+    out, bound = torch.zeros_like(x), torch.zeros_like(x)
+    H, I = s["Wg"].shape[2], s["Wg"].shape[1]
+    for e in ids.unique().tolist():
+        t, j = torch.nonzero(ids == e, as_tuple=True)
+        wg, wu, wd = (s[n][e].double() for n in ("Wg", "Wu", "Wd"))
+        g, up = x[t] @ wg.T, x[t] @ wu.T
+        eg, eu = 2 * H * E24 * (x[t].abs() @ wg.abs().T), 2 * H * E24 * (x[t].abs() @ wu.abs().T)
+        a = g * torch.sigmoid(g)
+        h = a * up
+        top = h.abs().amax(-1, keepdim=True)
+        low = torch.where(top >= 2.0 ** -13 * (1 - 1e-3), 2.0 ** -13, 0.0)
+        eh = 1.1 * eg * up.abs() + (a.abs() + 1.1 * eg) * eu + (2.0 ** -16 + 16 * E24) * torch.maximum(h.abs(), low)
+        wt = w[t, j, None]
+        out[t] += wt * (h @ wd.T)
+        bound[t] += wt * (eh @ wd.abs().T + (2 * I + 40) * E24 * (h.abs() @ wd.abs().T))
+    return out, bound * (1 + u) + u * out.abs() + 2.0 ** -25
+
+
+# The size of h and the standard deviation of Wd.
+@pytest.mark.parametrize("size,wd", [(1e5, 2e-3), (2e6, 1e-4), (3e7, 1e-5), (1e9, 3e-7), (1e-4, 30.0), (1e-5, 300.0), (1e-7, 1e4)])
+@pytest.mark.parametrize("T,E,k,H,I", [(1, 8, 2, 256, 128), (9, 8, 3, 264, 200), (64, 6, 2, 512, 320), (3, 2, 1, 2056, 1000)])
+@pytest.mark.parametrize("path", [1, 2])
+def test_fp16_hidden_values_far_from_one(G, size, wd, T, E, k, H, I, path):
+    """h beyond FP16's largest number, and so small that FP16's steps are coarse,
+    where the output itself is an ordinary number."""
+    s = inputs(T, E, H, I, "f16", T + H, k)
+    f = size ** 0.5
+    s["Wg"], s["Wu"] = ((s[n].float() * f).half() for n in ("Wg", "Wu"))
+    if size < 1:
+        # SiLU(g) is g / 2 there
+        s["Wg"] = (s["Wg"].float() * 2).half()
+    s["Wd"] = (s["Wd"].float() * (I ** 0.5 * wd)).half()
+    out, ids, w = G.detffn_moe_forward(s["x"], s["Wr"], s["Wg"], s["Wu"], s["Wd"], k, path=path)
+    assert G.detffn_get_status() == 0
+    wr, idr = route64(s["x"], s["Wr"], k, True)
+    assert torch.equal(ids.long(), idr)
+    ref, bound = moe64_wide(s, idr, wr, DT["f16"][1])
+    assert float(ref.abs().max()) < 65504 and bool(out.isfinite().all())
+    bad = ~((out.double() - ref).abs() <= bound + 2e-5 * ref.abs())
+    assert not bool(bad.any()), float(((out.double() - ref).abs() / bound).max())
+
+
+def test_fp16_tokens_of_any_size_stay_alone(G):
+    """Tokens whose h the tensor cores' two terms hold, and others, in one call."""
+    T, E, H, I, k = 24, 4, 512, 328, 2
+    s = inputs(T, E, H, I, "f16", 77, k)
+    s["Wd"] = (s["Wd"].float() * 1e-3).half()
+    rest = (s["Wr"], s["Wg"], s["Wu"], s["Wd"], k)
+    want = G.detffn_moe_forward(s["x"], *rest)
+    x = s["x"].clone()
+    x[2], x[3], x[9], x[10], x[17] = x[2] * 3000, x[3] * 1e-4, 0.0, float("inf"), float("nan")
+    got = G.detffn_moe_forward(x, *rest)
+    keep = [t for t in range(T) if t not in (2, 3, 9, 10, 17)]
+    assert all(torch.equal(a[keep], b[keep]) for a, b in zip(got, want))
+    for t in (2, 3, 9, 10, 17):   # and each is what it is alone
+        assert torch.equal(G.detffn_moe_forward(x[t:t + 1].contiguous(), *rest)[0][0].nan_to_num(7.0), got[0][t].nan_to_num(7.0))
+    assert bool(got[0][2].isfinite().all()) and not bool(got[0][9].any()) and bool(got[0][17].isnan().all())
+
+
+@pytest.mark.parametrize("path", [1, 2])
+def test_bf16_hidden_values_beyond_its_largest(G, path):
+    """h = 2^128 (1 - 2^-10) is an FP32 number that rounds to BF16's infinity."""
+    x = torch.zeros((1, 64), dtype=torch.bfloat16, device="cuda")
+    x[0, :2] = 1
+    Wg, Wu = (torch.zeros((1, 64, 64), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    Wg[0, :, 0], Wg[0, :, 1], Wu[0, :, 0] = 2.0 ** 64, -2.0 ** 54, 2.0 ** 64
+    Wd = torch.zeros((1, 64, 64), dtype=torch.bfloat16, device="cuda")
+    Wd[0, :, 5] = 2.0 ** -120
+    out = G.detffn_moe_forward(x, torch.zeros((1, 64), dtype=torch.bfloat16, device="cuda"), Wg, Wu, Wd, 1, path=path)[0]
+    assert torch.equal(out.float(), torch.full_like(out, 256.0, dtype=torch.float32))
+
