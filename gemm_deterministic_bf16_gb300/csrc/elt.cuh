@@ -1,5 +1,5 @@
 // elt.cuh -- reading and writing FP32, FP16 and BF16 elements as FP32 values,
-// one at a time or eight at once, and sums over a group of threads.
+// one at a time or eight at once, and sums over a warp.
 #pragma once
 
 #include "common.cuh"
@@ -83,32 +83,6 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
   return v;
-}
-
-// Sums of N values over all threads of the block (a multiple of 32, at most
-// 32 warps), the same in every thread.  `buf` is [2][N][32] floats of shared
-// memory; `turn` alternates between calls, so that one barrier per call is
-// enough: a half is written again only after the barrier of the call between.
-// The order of the additions depends on the block size alone.
-template <int N>
-__device__ __forceinline__ void block_sums(float (&v)[N], float* buf, int& turn) {
-  const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-#pragma unroll
-  for (int i = 0; i < N; ++i) v[i] = warp_sum(v[i]);
-  if (warps == 1) return;
-  float* b = buf + turn * N * 32;
-  turn ^= 1;
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) b[i * 32 + warp] = v[i];
-  }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    float s = 0.0f;
-    for (int w = 0; w < warps; ++w) s += b[i * 32 + w];
-    v[i] = s;
-  }
 }
 
 }  // namespace detffn

@@ -28,28 +28,6 @@
 namespace detffn {
 namespace join {
 
-// Features c .. c + 7 of a row or a parameter; zeros past the row's end.
-template <int DT>
-__device__ __forceinline__ void load(const void* base, long long off, int c, int H, float (&v)[8]) {
-  using E = typename Io<DT>::E;
-  if (c < H) {
-    Io<DT>::ld8(static_cast<const E*>(base) + off + c, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-  }
-}
-template <int DT>
-__device__ __forceinline__ void store(void* base, long long off, int c, int H, const float (&v)[8]) {
-  if (c < H) Io<DT>::st8(static_cast<typename Io<DT>::E*>(base) + off + c, v);
-}
-// A parameter, in the elements' type or in FP32.
-template <int DT>
-__device__ __forceinline__ void load_param(const void* base, int pdtype, long long off, int c, int H, float (&v)[8]) {
-  if (DT == DETFFN_F32 || pdtype == DT) load<DT>(base, off, c, H, v);
-  else load<DETFFN_F32>(base, off, c, H, v);
-}
-
 template <int DT>
 __device__ __forceinline__ float param(const void* base, int pdtype, long long i) {
   if (DT == DETFFN_F32 || pdtype == DT) return Io<DT>::ld(static_cast<const typename Io<DT>::E*>(base) + i);
@@ -61,63 +39,186 @@ __device__ __forceinline__ void put_param(void* base, int pdtype, long long i, f
   else static_cast<float*>(base)[i] = v;
 }
 
+// Sums of N = 2 or 4 values over a group of G threads (whole warps, at most
+// 20), the same in every thread, in an order fixed by G.  Stage one halves the
+// values a lane carries with every exchange, so that lane l ends with the
+// warp's sum of value l % N; stage two adds the warps the same way, through
+// [2][20 N] floats.  One barrier; one warp alone: none but __syncwarp.
+template <int N, int THREADS = 512>
+struct GroupSums {
+  static_assert(N == 2 || N == 4, "");
+  float *put, *get;     // this thread's places, now in the first half
+  int other = 20 * N;   // the other half, from there
+  int warps, barrier, threads;
+  bool odd, high;
+  // `buf`: 40 N floats of the group.
+  __device__ __forceinline__ GroupSums(float* buf, int G, int group, int t) {
+    const int lane = t & 31;
+    put = buf + (t >> 5) * N + lane;
+    get = buf + lane;
+    warps = (G >> 5) * N - lane;   // 0 or less: no value for this lane
+    barrier = group + 1;
+    threads = G;
+    odd = lane & 1;
+    high = lane & 2;
+  }
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+    float x = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
+    if (N == 4) {
+      const float c = v[N - 2], d = v[N - 1];
+      const float y = (odd ? d : c) + __shfl_xor_sync(0xffffffffu, odd ? c : d, 1);
+      x = (high ? y : x) + __shfl_xor_sync(0xffffffffu, high ? x : y, 2);
+    }
+#pragma unroll
+    for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+    if (threads > 32) {
+      if ((int)(threadIdx.x & 31) < N) *put = x;
+      asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+      x = warps > 0 ? get[0] : 0.0f;
+      if (N == 4) x += warps > 32 ? get[32] : 0.0f;
+      if (N == 4 && THREADS > 512) x += warps > 64 ? get[64] : 0.0f;
+      put += other;
+      get += other;
+      other = -other;
+#pragma unroll
+      for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+    } else {
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, i);
+  }
+};
+
+// One unit of a thread: with VEC features c .. c + 7 (a thread past the row's
+// end reads the last unit and counts for nothing: on is 0), else c + 32 j where
+// bit j of on is set, and zeros.
+struct Cols {
+  int c;
+  uint32_t on;
+};
+template <bool VEC>
+__device__ __forceinline__ Cols cols_of(int i, int G, int t, int H) {
+  Cols k;
+  if (VEC) {
+    k.on = 8 * (i * G + t) < H;
+    k.c = k.on ? 8 * (i * G + t) : H - 8;
+  } else {
+    k.c = 256 * (i * (G >> 5) + (t >> 5)) + (t & 31);
+    k.on = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) k.on |= (k.c + 32 * j < H ? 1u : 0u) << j;
+  }
+  return k;
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void unit(const void* row, const Cols& k, float (&v)[8]) {
+  using E = typename Io<DT>::E;
+  const E* p = static_cast<const E*>(row) + k.c;
+  if (VEC) {
+    Io<DT>::ld8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = k.on >> j & 1 ? Io<DT>::ld(p + 32 * j) : 0.0f;
+  }
+}
+template <int DT, bool VEC>
+__device__ __forceinline__ void put_unit(void* row, const Cols& k, const float (&v)[8]) {
+  using E = typename Io<DT>::E;
+  E* p = static_cast<E*>(row) + k.c;
+  if (VEC) {
+    if (k.on) Io<DT>::st8(p, v);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (k.on >> j & 1) Io<DT>::st(p + 32 * j, v[j]);
+  }
+}
+// The same of a parameter, in the rows' type or FP32; `fill` where there is none.
+template <int DT, bool VEC>
+__device__ __forceinline__ void param_unit(const void* p, int pdtype, const Cols& k, float fill, float (&v)[8]) {
+  if (!p) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = fill;
+  } else if (DT == DETFFN_F32 || pdtype == DT) {
+    unit<DT, VEC>(p, k, v);
+  } else {
+    unit<DETFFN_F32, VEC>(p, k, v);
+  }
+}
+__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
+  float s = a[0] * b[0], q = a[1] * b[1];
+#pragma unroll
+  for (int j = 2; j < 8; j += 2) s = fmaf(a[j], b[j], s), q = fmaf(a[j + 1], b[j + 1], q);
+  return s + q;
+}
+
+// Sum over a block of at most 16 warps, the same in every thread: a tree over the
+// lanes, then over the warps, neighbours first -- as GroupSums adds one value.
+// `buf`: [2][16] floats; one barrier, as its halves take turns.
+__device__ __forceinline__ float tree_sum(float x, float* buf, int& turn) {
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int s = 1; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+  if (warps == 1) return x;
+  float* b = buf + turn * 16;
+  turn ^= 1;
+  if (lane == 0) b[threadIdx.x >> 5] = x;
+  __syncthreads();
+  x = lane < warps ? b[lane] : 0.0f;
+#pragma unroll
+  for (int s = 1; s < 16; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
+  return __shfl_sync(0xffffffffu, x, 0);
+}
+
 // A few rows of whole 16-byte vectors and at most 4096 features: one block of
-// threads to a row, eight features to a thread, in registers.  Bound by latency,
-// so all of a row's loads go out before its sums (one row of 4096 features, BF16:
-// 3.1 us).
-template <int DT>
+// threads to a row, a unit to a thread, in registers.  Every sum and product is
+// the ring kernel's, in its order, so that a row's bits do not depend on how many
+// rows the call has: where a thread there holds units t and G + t, neighbours
+// hold them here (PAIR), and their sum is the first of the tree.  Bound by
+// latency, so all of a row's loads go out before its sums (one row of 4096
+// features, BF16: 2.9 us; with two units to a thread, 3.5).
+template <int DT, bool PAIR>
 __global__ void __launch_bounds__(512) k_fwd(const __grid_constant__ JoinArgs a) {
-  __shared__ float buf[2 * 32];
+  __shared__ float buf[2 * 16];
   grid_dep_wait();
   grid_dep_launch();
-  const int c = 8 * threadIdx.x, H = a.H;
+  const int H = a.H, t = threadIdx.x;
   const float inv = 1.0f / (float)H;
+  const bool by_row = a.gate && a.gate_rs;
   int turn = 0;
-  auto gate_of = [&](long long m, float (&g)[8]) {
-    if (!a.gate) {
+  const Cols k = cols_of<true>(0, 0, PAIR ? (t >> 1) + (t & 1) * (int)(blockDim.x >> 1) : t, H);
+  float mix[8], pre[8];      // mix: scale * gate * w_post
+  {
+    float w[8];
+    param_unit<DT, true>(a.w_pre, a.pdtype, k, 1.0f, pre);
+    param_unit<DT, true>(a.w_post, a.pdtype, k, 1.0f, w);
+    param_unit<DT, true>(a.gate_cs && !by_row ? a.gate : nullptr, a.pdtype, k,
+                         a.gate && !a.gate_cs && !by_row ? param<DT>(a.gate, a.pdtype, 0) : 1.0f, mix);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = 1.0f;
-    } else if (a.gate_cs) {
-      load_param<DT>(a.gate, a.pdtype, m * a.gate_rs, c, H, g);
-    } else {
-      const float one = param<DT>(a.gate, a.pdtype, m * a.gate_rs);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) g[j] = one;
-    }
-  };
-  float post[8], pre[8], gate[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) post[j] = pre[j] = 1.0f;
-  if (a.w_post) load_param<DT>(a.w_post, a.pdtype, 0, c, H, post);
-  if (a.w_pre) load_param<DT>(a.w_pre, a.pdtype, 0, c, H, pre);
-  if (!a.gate_rs) gate_of(0, gate);
+    for (int j = 0; j < 8; ++j) mix[j] *= a.scale * w[j];
+  }
   for (long long m = blockIdx.x; m < a.M; m += gridDim.x) {
-    float r[8], n[8];
-    load<DT>(a.x.p, m * a.x.ld, c, H, r);
-    if (a.z.p) load<DT>(a.z.p, m * a.z.ld, c, H, n);
-    if (a.gate_rs) gate_of(m, gate);
+    auto row = [&](const Rows& r) { return static_cast<const typename Io<DT>::E*>(r.p) + m * r.ld; };
+    float r[8], z[8], g[8];
+    unit<DT, true>(row(a.x), k, r);
+    if (a.z.p) unit<DT, true>(row(a.z), k, z);
+    if (by_row) {
+      const char* gate = static_cast<const char*>(a.gate) + m * a.gate_rs * (a.pdtype == DETFFN_F32 ? 4 : 2);
+      param_unit<DT, true>(a.gate_cs ? gate : nullptr, a.pdtype, k, a.gate_cs ? 0.0f : param<DT>(gate, a.pdtype, 0), g);
+    }
     if (a.z.p) {
       float b = 1.0f;
-      if (a.w_post) {
-        float s[1] = {0.0f};
+      if (a.w_post) b = rsqrtf(fmaf(tree_sum(k.on ? dot8(z, z) : 0.0f, buf, turn), inv, a.eps));
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[0] = fmaf(n[j], n[j], s[0]);
-        block_sums<1>(s, buf, turn);
-        b = rsqrtf(s[0] * inv + a.eps);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = fmaf(a.scale, n[j] * (b * post[j]) * gate[j], r[j]);
-      store<DT>(const_cast<void*>(a.out.p), m * a.out.ld, c, H, r);
+      for (int j = 0; j < 8; ++j) r[j] = fmaf(b * z[j], by_row ? g[j] * mix[j] : mix[j], r[j]);
+      put_unit<DT, true>(const_cast<typename Io<DT>::E*>(row(a.out)), k, r);
     }
     if (a.w_pre) {
-      float s[1] = {0.0f};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s[0] = fmaf(r[j], r[j], s[0]);
-      block_sums<1>(s, buf, turn);
-      const float q = rsqrtf(s[0] * inv + a.eps);
+      const float q = rsqrtf(fmaf(tree_sum(k.on ? dot8(r, r) : 0.0f, buf, turn), inv, a.eps));
 #pragma unroll
       for (int j = 0; j < 8; ++j) r[j] *= q * pre[j];
-      store<DT>(const_cast<void*>(a.y.p), m * a.y.ld, c, H, r);
+      put_unit<DT, true>(const_cast<typename Io<DT>::E*>(row(a.y)), k, r);
     }
   }
 }

@@ -49,57 +49,6 @@ struct RingPlan {
   int C = 1, width = 0;                  // CTAs that share a row, and the features of each but the last
 };
 
-// Sums of N = 2 or 4 values over a group of G threads (whole warps, at most
-// 20), the same in every thread, in an order fixed by G.  Stage one halves the
-// values a lane carries with every exchange, so that lane l ends with the
-// warp's sum of value l % N; stage two adds the warps the same way, through
-// [2][20 N] floats.  One barrier; one warp alone: none but __syncwarp.
-template <int N, int THREADS = 512>
-struct GroupSums {
-  static_assert(N == 2 || N == 4, "");
-  float *put, *get;     // this thread's places, now in the first half
-  int other = 20 * N;   // the other half, from there
-  int warps, barrier, threads;
-  bool odd, high;
-  // `buf`: 40 N floats of the group.
-  __device__ __forceinline__ GroupSums(float* buf, int G, int group, int t) {
-    const int lane = t & 31;
-    put = buf + (t >> 5) * N + lane;
-    get = buf + lane;
-    warps = (G >> 5) * N - lane;   // 0 or less: no value for this lane
-    barrier = group + 1;
-    threads = G;
-    odd = lane & 1;
-    high = lane & 2;
-  }
-  __device__ __forceinline__ void operator()(float (&v)[N]) {
-    float x = (odd ? v[1] : v[0]) + __shfl_xor_sync(0xffffffffu, odd ? v[0] : v[1], 1);
-    if (N == 4) {
-      const float c = v[N - 2], d = v[N - 1];
-      const float y = (odd ? d : c) + __shfl_xor_sync(0xffffffffu, odd ? c : d, 1);
-      x = (high ? y : x) + __shfl_xor_sync(0xffffffffu, high ? x : y, 2);
-    }
-#pragma unroll
-    for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    if (threads > 32) {
-      if ((int)(threadIdx.x & 31) < N) *put = x;
-      asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
-      x = warps > 0 ? get[0] : 0.0f;
-      if (N == 4) x += warps > 32 ? get[32] : 0.0f;
-      if (N == 4 && THREADS > 512) x += warps > 64 ? get[64] : 0.0f;
-      put += other;
-      get += other;
-      other = -other;
-#pragma unroll
-      for (int s = N; s < 32; s <<= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
-    } else {
-      __syncwarp();
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i) v[i] = __shfl_sync(0xffffffffu, x, i);
-  }
-};
-
 // A group's ring of rows, in the order in which the group takes them.  Each
 // tensor of a row is one lane's, which keeps its source and issues its copy: one
 // thread for all took 170 instructions a row.
@@ -171,69 +120,6 @@ __device__ __forceinline__ const unsigned char* ring_row(const unsigned char* sl
 // came would read as NaN.
 __device__ __forceinline__ bool ring_wait(const Ring1& r) {
   return mbar_wait(&r.full[r.s], r.phase, kDefaultSpin, nullptr);
-}
-
-// One unit of a thread: with VEC features c .. c + 7 (a thread past the row's
-// end reads the last unit and counts for nothing: on is 0), else c + 32 j where
-// bit j of on is set, and zeros.
-struct Cols {
-  int c;
-  uint32_t on;
-};
-template <bool VEC>
-__device__ __forceinline__ Cols cols_of(int i, int G, int t, int H) {
-  Cols k;
-  if (VEC) {
-    k.on = 8 * (i * G + t) < H;
-    k.c = k.on ? 8 * (i * G + t) : H - 8;
-  } else {
-    k.c = 256 * (i * (G >> 5) + (t >> 5)) + (t & 31);
-    k.on = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) k.on |= (k.c + 32 * j < H ? 1u : 0u) << j;
-  }
-  return k;
-}
-template <int DT, bool VEC>
-__device__ __forceinline__ void unit(const void* row, const Cols& k, float (&v)[8]) {
-  using E = typename Io<DT>::E;
-  const E* p = static_cast<const E*>(row) + k.c;
-  if (VEC) {
-    Io<DT>::ld8(p, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = k.on >> j & 1 ? Io<DT>::ld(p + 32 * j) : 0.0f;
-  }
-}
-template <int DT, bool VEC>
-__device__ __forceinline__ void put_unit(void* row, const Cols& k, const float (&v)[8]) {
-  using E = typename Io<DT>::E;
-  E* p = static_cast<E*>(row) + k.c;
-  if (VEC) {
-    if (k.on) Io<DT>::st8(p, v);
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (k.on >> j & 1) Io<DT>::st(p + 32 * j, v[j]);
-  }
-}
-// The same of a parameter, in the rows' type or FP32; `fill` where there is none.
-template <int DT, bool VEC>
-__device__ __forceinline__ void param_unit(const void* p, int pdtype, const Cols& k, float fill, float (&v)[8]) {
-  if (!p) {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = fill;
-  } else if (DT == DETFFN_F32 || pdtype == DT) {
-    unit<DT, VEC>(p, k, v);
-  } else {
-    unit<DETFFN_F32, VEC>(p, k, v);
-  }
-}
-__device__ __forceinline__ float dot8(const float (&a)[8], const float (&b)[8]) {
-  float s = a[0] * b[0], q = a[1] * b[1];
-#pragma unroll
-  for (int j = 2; j < 8; j += 2) s = fmaf(a[j], b[j], s), q = fmaf(a[j + 1], b[j + 1], q);
-  return s + q;
 }
 
 // What a pass has, when it is compiled for it (backward: z where it is read).  A
@@ -412,7 +298,7 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
       float v[2] = {0.0f, 0.0f};
       if (n + 1 < rows) v[0] = sum_z(n + 1);
       float r[V][8];
-      const float b = has_post ? rsqrtf(sz * inv + a.eps) : 1.0f;
+      const float b = has_post ? rsqrtf(fmaf(sz, inv, a.eps)) : 1.0f;
       const float g1 = next_gate;
       if (by_row && !a.gate_cs && n + 1 < rows) next_gate = param<DT>(a.gate, a.pdtype, (first + (n + 1) * step) * a.gate_rs);
 #pragma unroll
@@ -421,14 +307,11 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
         if (has_z) {
           float z[8];
           unit<DT, VEC>(ring_row<VEC>(row, pz, n), k[i], z);
-          if (by_row) {
-            float g[8];
-            param_unit<DT, VEC>(full_gate ? ring_row<VEC>(row, pg, n) : nullptr, a.pdtype, k[i], g1, g);
+          float g[8];
+          if (by_row) param_unit<DT, VEC>(full_gate ? ring_row<VEC>(row, pg, n) : nullptr, a.pdtype, k[i], g1, g);
+          // (gate * (scale * w_post) first, as it is for a gate that all rows share)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) z[j] *= g[j];
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) r[i][j] = fmaf(b * z[j], mix[i][j], r[i][j]);
+          for (int j = 0; j < 8; ++j) r[i][j] = fmaf(b * z[j], by_row ? g[j] * mix[i][j] : mix[i][j], r[i][j]);
           put_unit<DT, VEC>(out, k[i], r[i]);
         }
         if (has_pre) v[1] += k[i].on ? dot8(r[i], r[i]) : 0.0f;
@@ -437,7 +320,7 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
       if (t < p.n && n + p.S < rows) ring_fill<VEC>(ring, slot, row);
       sz = v[0];
       if (has_pre) {
-        const float q = rsqrtf(v[1] * inv + a.eps);
+        const float q = rsqrtf(fmaf(v[1], inv, a.eps));
 #pragma unroll
         for (int i = 0; i < V; ++i) {
 #pragma unroll
@@ -586,7 +469,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_bwd_ring(const __grid_constant__
       }
       if (has_pre) {
         // (in this order: q^3 alone leaves FP32's range for rows of 2e15 on)
-        const float q = rsqrtf(s[0] * inv + a.eps), k = s[1] * inv * q * q * q;
+        const float q = rsqrtf(fmaf(s[0], inv, a.eps)), k = s[1] * inv * q * q * q;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float qd = q * dy[j];
@@ -596,7 +479,7 @@ __global__ void __launch_bounds__(THREADS, 1) k_bwd_ring(const __grid_constant__
         put_unit<DT, VEC>(dxp, cs, d);
       }
       // d becomes D c, n is b z (without z: dz = scale dx).
-      const float b = has_post ? rsqrtf(s[2] * inv + a.eps) : 1.0f;
+      const float b = has_post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.0f;
       float bn[8];
       const float gate = next_gate;   // scale times a token's gate, or 1
       if (has_z) {
@@ -805,9 +688,10 @@ cudaError_t forward(const JoinArgs& a, cudaStream_t st) {
            Kind<kPre | kZ>{}, Kind<kPre | kZ | kToken>{}, Kind<kPre | kZ | kFull>{}, Kind<kPre>{}, Kind<kAny>{});
     return e;
   }
-  // Few rows of whole vectors.
+  // Few rows of whole vectors (a thread's two units go to two threads).
   const long long most = 152ll * 16;
-  return launch_dependent(k_fwd<DT>, dim3((unsigned)(a.M < most ? a.M : most)), ((a.H + 7) / 8 + 31) / 32 * 32, 0, st, a);
+  return launch_dependent(two ? k_fwd<DT, true> : k_fwd<DT, false>, dim3((unsigned)(a.M < most ? a.M : most)),
+                          two ? 2 * p.G : p.G, 0, st, a);
 }
 
 // Whether a backward pass takes 640 threads instead of 512 to a CTA, and 96

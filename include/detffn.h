@@ -382,6 +382,10 @@ DETFFN_API detffn_status detffn_selfcheck_fused_schedule(unsigned long long *cas
  * rows' type or FP32.  The gate of token m and feature c is
  * gate[m * gate_rs + c * gate_cs], gate_cs in {0, 1}: (0, 0) one number,
  * (0, 1) one per feature, (s, 0) one per token, (s, 1) one per element.
+ * A row's out and y do not depend on the other rows or on M: one decoded token
+ * has the bits that it has in a prompt, whatever shape the gate is given in.
+ * (They do depend, in their last bits, on whether the call's rows and parameters
+ * all lie on 16-byte boundaries.)
  * out may be exactly x (in place); no other output overlaps anything. */
 DETFFN_API detffn_status detffn_join_forward(const void* x, long long ldx, const void* z, long long ldz,
                                              const void* w_post, const void* gate, long long gate_rs,

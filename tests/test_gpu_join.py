@@ -341,3 +341,26 @@ def test_rows_far_from_one(G, size, eps, M, H, post, pre, dt):
     got = G.detffn_join_backward(s["x"], s["z"], s["dr"], s["dy"], s["w_post"], s["gate"], 0.75, s["w_pre"], eps)
     for name, (v, m) in backward64(s, s["x"], 0.75, eps).items():
         close(getattr(got, name), v, m, "f32" if name in ("dw_pre", "dw_post", "dgate") else dt, 350)
+
+
+@pytest.mark.parametrize("gate", ["none", "feature", "scalar", "token", "full"])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, True), (True, False)])
+@pytest.mark.parametrize("M,H,dt,pt", [(4096, 4096, "bf16", "bf16"), (2048, 1024, "bf16", "f32"), (9000, 256, "f16", "f16"),
+                                       (1200, 2056, "f32", "f32"), (700, 8192, "bf16", "bf16"), (900, 1031, "bf16", "f32"),
+                                       (200, 12288, "f16", "f16")])
+def test_a_row_does_not_depend_on_the_others(G, M, H, dt, pt, gate, post, pre):
+    """A row's out, y, dx and dz have the same bits in a call of one row, of a few and
+    of all (a decoded token's and a prompt's): so has dgate where it is a row's own."""
+    s = inputs(M, H, dt, pt, gate, 3 * M + H, post, pre)
+    row = lambda t, a, b: t if t is None or t.shape[0] != M or t.dim() < 2 else t[a:b]  # noqa: E731
+    f = lambda v: G.detffn_join_forward(v["x"], v["z"], v["w_post"], v["gate"], 0.75, v["w_pre"])  # noqa: E731
+    full = f(s)
+    for a, b in ((0, 1), (M - 1, M), (3, 7), (0, M // 2 + 1), (M // 3, M)):
+        part = f({n: row(t, a, b) for n, t in s.items()})
+        assert all(p is None or torch.equal(p, w[a:b]) for p, w in zip(part, full)), (a, b)
+    g = lambda v: G.detffn_join_backward(v["x"], v["z"], v["dr"], v["dy"], v["w_post"], v["gate"], 0.75, v["w_pre"])  # noqa: E731
+    full = g(s)
+    for a, b in ((0, 2), (M - 5, M), (M // 3, M)):   # (a token's gate of one row is a shared one)
+        part = g({n: row(t, a, b) for n, t in s.items()})
+        for n in ("dx", "dz") + (("dgate",) if gate in ("token", "full") else ()):
+            assert torch.equal(getattr(part, n), getattr(full, n)[a:b]), (n, a, b)
