@@ -12,6 +12,7 @@
 #include <stdint.h>
 
 #include "../../include/detffn.h"
+#include "per_device.h"
 
 namespace detffn {
 
@@ -45,6 +46,14 @@ cudaError_t launch_cluster(void (*k)(KArgs...), dim3 grid, int threads, int smem
   cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, k, static_cast<Args&&>(args)...);
 }
+// set() once for the current device (per_device.h).
+template <class F>
+cudaError_t once_per_device(PerDevice& done, F&& set) {
+  int device = 0;
+  const cudaError_t e = cudaGetDevice(&device);
+  return e == cudaSuccess ? done.once(device, static_cast<F&&>(set)) : e;
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t launch_dependent(void (*k)(KArgs...), dim3 grid, int threads, int smem, cudaStream_t st,
                              Args&&... args) {

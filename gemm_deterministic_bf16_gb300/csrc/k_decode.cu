@@ -20,7 +20,7 @@
 // ticket; nothing waits on another CTA) applies the top of the tree over the
 // block roots and the epilogue: a plain BF16 store, or for the gate/up pair
 // the fused stage boundary h = bf16(bf16(SiLU(gate)) * up).
-#include <mutex>
+#include <atomic>
 
 #include "common.cuh"
 #include "decode.h"
@@ -308,20 +308,21 @@ template <int MT, int S>
 cudaError_t launch_ms(DecArgs a, int NB, int sm_count, cudaStream_t st) {
   using G = Geo<S>;
   // Resident CTAs per SM for this instance (registers, threads, smem), worked
-  // out once; concurrent first calls (several host threads, the handle path
-  // and the allocation-free entry point) all wait for the one set-up.
-  static std::once_flag once;
-  static cudaError_t setup_err = cudaSuccess;
-  static int per_sm = 0;
-  std::call_once(once, [] {
-    setup_err = cudaFuncSetAttribute(k_decode<MT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
-    if (setup_err == cudaSuccess)
-      setup_err = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, k_decode<MT, S>, G::THREADS, G::SMEM);
-    if (per_sm < 1) per_sm = 1;
+  // out once per device (all are of one kind, and it is the same on each).
+  // Concurrent first calls (several host threads, the handle path and the
+  // allocation-free entry point) each do the set-up before they read it.
+  static PerDevice ready;
+  static std::atomic<int> per_sm{1};
+  const cudaError_t setup_err = once_per_device(ready, [] {
+    cudaError_t e = cudaFuncSetAttribute(k_decode<MT, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
+    int n = 0;
+    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_decode<MT, S>, G::THREADS, G::SMEM);
+    if (e == cudaSuccess) per_sm.store(n < 1 ? 1 : n);
+    return e;
   });
   if (setup_err != cudaSuccess) return setup_err;
   // Rows per tile so that the grid is one wave of resident CTAs.
-  long long tiles = ((long long)sm_count * per_sm) / NB;
+  long long tiles = ((long long)sm_count * per_sm.load()) / NB;
   if (tiles < 1) tiles = 1;
   long long rt = (a.N + tiles - 1) / tiles;
   if (rt < 1) rt = 1;

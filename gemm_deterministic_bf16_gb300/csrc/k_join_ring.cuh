@@ -632,8 +632,10 @@ bool ring_plan(const JoinArgs& a, bool back, bool vec, int V, int threads, RingP
 
 template <auto K>
 cudaError_t ring_launch(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
-  static const cudaError_t setup = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-  if (setup != cudaSuccess) return setup;
+  static PerDevice ready;
+  const cudaError_t e =
+      once_per_device(ready, [] { return cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes); });
+  if (e != cudaSuccess) return e;
   const int least = 3 * 5120 * 4;   // the groups' column sums
   const int smem = p.R * p.S * p.row > least ? p.R * p.S * p.row : least;
   return launch_cluster(K, dim3(p.grid), p.G * p.R, smem, p.C, st, a, p);

@@ -55,8 +55,6 @@
 // 2048, I = 768 takes 27.2 us, 11.4 of them for the weights; 1.5 us for the
 // logits, 3 for the routing, 2 to 3 until the first stage, 8 of gate/up, 3 until
 // h is seen, 3 of down, 4 for the sums.
-#include <mutex>
-
 #include "elt.cuh"
 #include "moe.cuh"
 #include "ptx.cuh"
@@ -808,12 +806,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 template <int DT>
 cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int sm_count, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t setup = cudaSuccess;
-  std::call_once(once, [] {
-    setup = cudaFuncSetAttribute(k_moe<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
-  });
-  if (setup != cudaSuccess) return setup;
+  static PerDevice ready;
+  cudaError_t e =
+      once_per_device(ready, [] { return cudaFuncSetAttribute(k_moe<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax); });
+  if (e != cudaSuccess) return e;
   const bool f16 = DT == DETFFN_F16;
   CUtensorMap mWg, mWu, mWg32, mWu32, mWd, mX, mH[4];
   const long long dg[3] = {m.H, m.I, m.E}, dd[3] = {m.I, m.H, m.E}, dx[2] = {m.H, m.T}, dh[2] = {m.I, 2ll * m.T * m.k};
@@ -850,7 +846,7 @@ cudaError_t tensor(const MoeArgs& m, const MoeScratch& sc, const Waits& wt, int 
   g.status = wt.status;
   g.spin = wt.spin;
   g.stall = wt.stall;
-  cudaError_t e = launch_moe_logits(m, sc.counters, 1 + m.E + g.tb + (f16 ? m.T * m.k : 0), st);
+  e = launch_moe_logits(m, sc.counters, 1 + m.E + g.tb + (f16 ? m.T * m.k : 0), st);
   if (e != cudaSuccess) return e;
   const long long most = (long long)(m.T * m.k < m.E ? m.T * m.k : m.E) * ((m.I + 31) / 32 + g.tb * g.parts);
   const int grid = (int)(most < sm_count ? most : sm_count);

@@ -783,17 +783,16 @@ namespace {
 
 template <int BN, int GG, bool DUMP, bool KC, int LAY>
 cudaError_t launch_bng(const CUtensorMap* m, const TcArgs& a, const KChunkMaps& kcm, int sm_count, cudaStream_t st) {
-  static std::once_flag once;
-  static cudaError_t setup_err = cudaSuccess;
-  std::call_once(once, [] {
-    setup_err = cudaFuncSetAttribute(k_tc<BN, GG, DUMP, KC, LAY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     TcGeo<BN>::MAX_SMEM);
-    if (setup_err != cudaSuccess) return;
+  static PerDevice ready;
+  const cudaError_t setup_err = once_per_device(ready, [] {
+    cudaError_t e = cudaFuncSetAttribute(k_tc<BN, GG, DUMP, KC, LAY>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         TcGeo<BN>::MAX_SMEM);
+    if (e != cudaSuccess) return e;
     // The in-kernel register split (setmaxnreg) hands over exactly the
     // launch's registers; with any other count it could not complete.
     cudaFuncAttributes fa;
-    setup_err = cudaFuncGetAttributes(&fa, k_tc<BN, GG, DUMP, KC, LAY>);
-    if (setup_err == cudaSuccess && fa.numRegs != kRegsLaunch) setup_err = cudaErrorInvalidConfiguration;
+    e = cudaFuncGetAttributes(&fa, k_tc<BN, GG, DUMP, KC, LAY>);
+    return e == cudaSuccess && fa.numRegs != kRegsLaunch ? cudaErrorInvalidConfiguration : e;
   });
   if (setup_err != cudaSuccess) return setup_err;
   const int units = a.num_m * a.num_n * a.np;

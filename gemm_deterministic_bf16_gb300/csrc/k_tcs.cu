@@ -1407,11 +1407,10 @@ bool tcs_plan(long long R, long long C, long long K, int np, int max_ctas, bool 
 
 namespace {
 
-// One-time kernel attributes (shared memory limits and carve-out).
+// Kernel attributes (shared memory limits and carve-out), once per device.
 cudaError_t tcs_setup() {
-  static std::once_flag once;
-  static cudaError_t setup_err = cudaSuccess;
-  std::call_once(once, [] {
+  static PerDevice ready;
+  return once_per_device(ready, [] {
     cudaError_t e = cudaSuccess;
     void (*ks[6])(CUtensorMap, CUtensorMap, CUtensorMap, CUtensorMap, TcsArgs) = {
         k_tcs<1, false>, k_tcs<2, false>, k_tcs<3, false>, k_tcs<1, true>, k_tcs<2, true>, k_tcs<3, true>};
@@ -1434,9 +1433,8 @@ cudaError_t tcs_setup() {
       if (e == cudaSuccess)
         e = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
     }
-    setup_err = e;
+    return e;
   });
-  return setup_err;
 }
 
 cudaError_t tcs_launch(const TcsPlan& plan, const TcsProblem* pr, long long ldo, uint16_t* h, const uint16_t* silu,
