@@ -1,4 +1,5 @@
-"""Builds libdetffn.so in-tree for sm_103a (GB300), and the native binding.
+"""Builds libdetffn.so in-tree for sm_103a (GB300), and where PyTorch is
+installed the native binding.
 
 Each ``csrc/*.cu`` file is compiled in parallel with nvcc and the objects are
 linked into ``gemm_deterministic_bf16_gb300/libdetffn.so``; ``csrc/bind.cpp``
@@ -34,8 +35,9 @@ def _nvcc():
 
 
 def _torch():
-    """PyTorch's folder, without importing it."""
-    return os.path.dirname(importlib.util.find_spec("torch").origin)
+    """PyTorch's folder, without importing it; None where it is not installed."""
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec and spec.origin else None
 
 
 def _stale(obj, src, deps):
@@ -46,7 +48,8 @@ def _stale(obj, src, deps):
 
 
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    """Compiles every source and links libdetffn.so and _native.so; returns the former's path."""
+    """Compiles every source and links libdetffn.so and _native.so (without
+    PyTorch the library alone); returns the former's path."""
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     srcs = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
@@ -60,7 +63,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
 
     torch_dir = _torch()
     bind_src, bind_obj = os.path.join(CSRC, "bind.cpp"), os.path.join(BUILD, "bind.o")
-    bind = force or _stale(bind_obj, bind_src, deps + [os.path.join(torch_dir, "version.py")])
+    bind = torch_dir is not None and (force or _stale(bind_obj, bind_src, deps + [os.path.join(torch_dir, "version.py")]))
     if bind:
         inc = [os.path.join(ROOT, "include"), sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
                os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
@@ -82,7 +85,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         tmp = OUT + ".tmp.%d" % os.getpid()
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart_static", "-ldl", "-lrt", "-lpthread"])
         os.replace(tmp, OUT)
-    if bind or not os.path.exists(NATIVE):
+    if torch_dir is not None and (bind or not os.path.exists(NATIVE)):
         lib = os.path.join(torch_dir, "lib")
         tmp = NATIVE + ".tmp.%d" % os.getpid()
         run(["g++", "-shared", "-o", tmp, bind_obj, "-L" + PKG, "-l:libdetffn.so", "-Wl,-rpath,$ORIGIN", "-L" + lib,
