@@ -413,10 +413,18 @@ detffn_status detffn_moe_forward(detffn_handle h, const void* x, const void* Wr,
   int prev = 0;
   TRYCU(cudaGetDevice(&prev));
   if (prev != h->device) TRYCU(cudaSetDevice(h->device));
-  const cudaError_t e = tensor ? launch_moe_tensor(a, sc, wt, h->sm_count, (cudaStream_t)stream)
-                               : launch_moe_general(a, sc, (cudaStream_t)stream);
+  // (the weights of as many experts as the pairs can reach; the host does not know how many they do)
+  const double pairs = (double)T * top_k, hit = pairs < E ? pairs : E, width = 3.0 * H * I;
+  const detffn_status s = timed(
+      h, (cudaStream_t)stream, tensor ? "moe_tensor" : "moe_general", es * (2.0 * T * H + (double)E * H + hit * width),
+      2.0 * T * E * H + 2.0 * pairs * width,
+      [&] {
+        return cu(tensor ? launch_moe_tensor(a, sc, wt, h->sm_count, (cudaStream_t)stream)
+                         : launch_moe_general(a, sc, (cudaStream_t)stream));
+      },
+      tensor ? 2 : 5);
   if (prev != h->device) cudaSetDevice(prev);
-  return cu(e);
+  return s;
 }
 
 }  // extern "C"

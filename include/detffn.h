@@ -266,7 +266,10 @@ DETFFN_API detffn_status detffn_silu_tables(detffn_handle h, unsigned short *sil
  * and flops (operands read once, outputs written once); detffn_profiling(h, 0)
  * stops recording.  detffn_profile_read synchronises the device, sums the
  * records per kernel name into out[0..*n) (at most `max` entries), and clears
- * them.  Profiling adds an event record between launches and nothing else. */
+ * them.  Profiling adds an event record between launches and nothing else.
+ * detffn_moe_forward's launches are one record ("moe_tensor" or "moe_general"),
+ * with the weights of min(T * top_k, E) experts; calls without a handle record
+ * nothing. */
 typedef struct {
     char name[48];
     int launches;

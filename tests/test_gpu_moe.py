@@ -333,3 +333,21 @@ def test_bf16_hidden_values_beyond_its_largest(G, path):
     out = G.detffn_moe_forward(x, torch.zeros((1, 64), dtype=torch.bfloat16, device="cuda"), Wg, Wu, Wd, 1, path=path)[0]
     assert torch.equal(out.float(), torch.full_like(out, 256.0, dtype=torch.float32))
 
+
+
+@pytest.mark.parametrize("path,name,launches", [(2, "moe_tensor", 2), (1, "moe_general", 5)])
+def test_profiling_records_the_layer(G, path, name, launches):
+    T, E, k, H, I = 3, 8, 2, 256, 192
+    s = inputs(T, E, H, I, "bf16", 41, k)
+    rest = (s["Wr"], s["Wg"], s["Wu"], s["Wd"], k)
+    want = G.detffn_moe_forward(s["x"], *rest, path=path)
+    G.detffn_profiling(True)
+    got = [G.detffn_moe_forward(s["x"], *rest, path=path) for _ in range(4)]
+    ops = G.detffn_profile_read()
+    G.detffn_profiling(False)
+    assert list(ops) == [name] and ops[name]["launches"] == 4 * launches and ops[name]["ms"] > 0
+    assert ops[name]["bytes"] == 4 * 2 * (2 * T * H + E * H + T * k * 3 * H * I)
+    assert ops[name]["flops"] == 4 * (2 * T * E * H + 6 * T * k * H * I)
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
+    G.detffn_moe_forward(s["x"], *rest, path=path)
+    assert not G.detffn_profile_read()
