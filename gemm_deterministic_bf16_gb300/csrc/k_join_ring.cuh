@@ -116,8 +116,8 @@ __device__ __forceinline__ const unsigned char* ring_row(const unsigned char* sl
 }
 
 // Waits for the row in the current slot.  Its copies were issued by this very
-// group, so the wait ends; it is bounded all the same, and a row that never
-// came would read as NaN.
+// group, so the wait ends; it is bounded all the same, and what is formed from a
+// row that never came is NaN.
 __device__ __forceinline__ bool ring_wait(const Ring1& r) {
   return mbar_wait(&r.full[r.s], r.phase, kDefaultSpin, nullptr);
 }
@@ -166,7 +166,7 @@ struct ClusterSums {
           : "memory");
     }
     // Every CTA of the cluster has started and takes the same rows, so the wait
-    // ends; it is bounded all the same, and would read as NaN.
+    // ends; it is bounded all the same, and sums that never came are NaN.
     bool came = false;
     for (long long i = 0; i < kDefaultSpin && !came; ++i) {
       uint32_t ok;
@@ -184,10 +184,11 @@ struct ClusterSums {
       const float4 o = *reinterpret_cast<const float4*>(b + r * 4);
       t.x += o.x, t.y += o.y, t.z += o.z, t.w += o.w;
     }
-    v[0] = came ? t.x : __int_as_float(0x7fc00000);
-    v[1] = t.y;
-    v[2] = came ? t.z : __int_as_float(0x7fc00000);
-    v[3] = t.w;
+    const float none = __int_as_float(0x7fc00000);
+    v[0] = came ? t.x : none;
+    v[1] = came ? t.y : none;
+    v[2] = came ? t.z : none;
+    v[3] = came ? t.w : none;
     phase ^= (uint32_t)half;
     half ^= 1;
   }
@@ -270,7 +271,8 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
     }
   };
   auto all_rows = [&](const Cols (&k)[V]) __attribute__((always_inline)) {
-    // The sum over z of the n-th row, in the next slot.
+    // The sum over z of the n-th row, in the next slot (0 where it is not wanted,
+    // and NaN where the row never came: both reach every thread).
     auto sum_z = [&](int n) {
       float v = 0.0f;
       if (!ring_wait(ring)) return __int_as_float(0x7fc00000);
@@ -298,7 +300,7 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
       float v[2] = {0.0f, 0.0f};
       if (n + 1 < rows) v[0] = sum_z(n + 1);
       float r[V][8];
-      const float b = has_post ? rsqrtf(fmaf(sz, inv, a.eps)) : 1.0f;
+      const float b = has_post ? rsqrtf(fmaf(sz, inv, a.eps)) : 1.0f + sz;
       const float g1 = next_gate;
       if (by_row && !a.gate_cs && n + 1 < rows) next_gate = param<DT>(a.gate, a.pdtype, (first + (n + 1) * step) * a.gate_rs);
 #pragma unroll
@@ -316,6 +318,7 @@ __global__ void __launch_bounds__(512, 1) k_fwd_ring(const __grid_constant__ Joi
         }
         if (has_pre) v[1] += k[i].on ? dot8(r[i], r[i]) : 0.0f;
       }
+      if (!has_z) v[1] += sz;
       add(v);
       if (t < p.n && n + p.S < rows) ring_fill<VEC>(ring, slot, row);
       sz = v[0];
@@ -477,6 +480,10 @@ __global__ void __launch_bounds__(THREADS, 1) k_bwd_ring(const __grid_constant__
           apre[j] = fmaf(qd, x[j], apre[j]);
         }
         put_unit<DT, VEC>(dxp, cs, d);
+      }
+      if (!has_pre && !has_post && s[2] != s[2]) {   // (the row never came; the norms' factors would show it)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = s[2];
       }
       // d becomes D c, n is b z (without z: dz = scale dx).
       const float b = has_post ? rsqrtf(fmaf(s[2], inv, a.eps)) : 1.0f;

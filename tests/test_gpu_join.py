@@ -364,3 +364,13 @@ def test_a_row_does_not_depend_on_the_others(G, M, H, dt, pt, gate, post, pre):
         part = g({n: row(t, a, b) for n, t in s.items()})
         for n in ("dx", "dz") + (("dgate",) if gate in ("token", "full") else ()):
             assert torch.equal(getattr(part, n), getattr(full, n)[a:b]), (n, a, b)
+
+
+# Many rows to every cluster of four and of eight thread blocks, forward and
+# backward: the exchanged sums take turns in two halves and the rings turn.
+@pytest.mark.parametrize("gate", ["none", "feature", "scalar", "token", "full"])
+@pytest.mark.parametrize("post,pre", [(True, True), (False, True), (True, False), (False, False)])
+@pytest.mark.parametrize("M,H,dt", [(200, 20480, "bf16"), (200, 32761, "f16"), (133, 32768, "f32"), (301, 16392, "bf16")])
+def test_many_rows_over_clusters(G, M, H, dt, gate, post, pre):
+    test_forward(G, M, H, dt, dt, gate, post, pre)
+    test_backward(G, M, H, dt, dt, gate, post, pre)
