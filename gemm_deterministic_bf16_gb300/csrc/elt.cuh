@@ -79,6 +79,20 @@ template <> struct Io<DETFFN_BF16> {
   }
 };
 
+// sigma(g) = 1 / (1 + exp(-g)) and 1 - sigma(g), from exp(-|g|) so that nothing
+// overflows and neither loses digits to a subtraction.  FAST: by __expf and
+// __fdividef, whose error is about (1.2 |g| + 4) 2^-23 of either (2^-16 at the
+// most, where exp leaves the type's range): for results of 16 bits.
+struct Sigma {
+  float s, rest;
+};
+template <bool FAST>
+__device__ __forceinline__ Sigma sigma(float g) {
+  const float e = FAST ? __expf(-fabsf(g)) : expf(-fabsf(g));
+  const float big = FAST ? __fdividef(1.0f, 1.0f + e) : 1.0f / (1.0f + e), small = e * big;
+  return g < 0.0f ? Sigma{small, big} : Sigma{big, small};
+}
+
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);

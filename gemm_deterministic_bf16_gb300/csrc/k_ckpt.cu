@@ -361,11 +361,12 @@ __global__ void __launch_bounds__(kThreads) k_unpack(const __grid_constant__ Ckp
   }
 }
 
+template <int DT>
 __device__ __forceinline__ void silu_stage(float dh, float g, float u, float& dU, float& dG, float& h) {
-  const float sig = __fdividef(1.0f, 1.0f + __expf(-g));
-  const float act = g * sig;
+  const Sigma sig = sigma<DT != DETFFN_F32>(g);
+  const float act = g * sig.s;
   dU = dh * act;
-  dG = dh * u * (sig * (1.0f + g * (1.0f - sig)));
+  dG = dh * u * (sig.s * (1.0f + g * sig.rest));
   h = act * u;
 }
 
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kThreads) k_bwd(const __grid_constant__ CkptAr
     E *oU = static_cast<E*>(a.dU) + at, *oG = static_cast<E*>(a.dG) + at, *oh = a.h ? static_cast<E*>(a.h) + at : nullptr;
     auto one = [&](int j, float sg, float su) {
       float vU, vG, vh;
-      silu_stage(Io<DT>::ld(dh + j), __fmul_rn((float)a.gq[at + j], sg), __fmul_rn((float)a.uq[at + j], su), vU, vG, vh);
+      silu_stage<DT>(Io<DT>::ld(dh + j), __fmul_rn((float)a.gq[at + j], sg), __fmul_rn((float)a.uq[at + j], su), vU, vG, vh);
       Io<DT>::st(oU + j, vU);
       Io<DT>::st(oG + j, vG);
       if (oh) Io<DT>::st(oh + j, vh);
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(kThreads) k_bwd(const __grid_constant__ CkptAr
       load_codes<DT>(a.uq + at, qu);
 #pragma unroll
       for (int j = 0; j < PER; ++j)
-        silu_stage(d[j], code_value(qg[j / 4], j % 4) * sg.of(j), code_value(qu[j / 4], j % 4) * su.of(j), vU[j], vG[j], vh[j]);
+        silu_stage<DT>(d[j], code_value(qg[j / 4], j % 4) * sg.of(j), code_value(qu[j / 4], j % 4) * su.of(j), vU[j], vG[j], vh[j]);
       store_vec<DT>(oU, vU);
       store_vec<DT>(oG, vG);
       if (oh) store_vec<DT>(oh, vh);

@@ -218,7 +218,7 @@ __global__ void __launch_bounds__(256) k_gateup(const __grid_constant__ MoeArgs 
     // Lanes l and l + 8 hold gate and up of one feature and pair.
     const float g = sum16(v, lane), u = __shfl_xor_sync(0xffffffffu, g, 8);
     const int of = sum16_of(lane), q = p + (of >> 2), f = of >> 1 & 1;
-    if (lane < 8 && q < p1 && i0 + f < a.I) static_cast<float*>(a.h)[q * a.I + i0 + f] = g / (1.0f + expf(-g)) * u;
+    if (lane < 8 && q < p1 && i0 + f < a.I) static_cast<float*>(a.h)[q * a.I + i0 + f] = g * sigma<false>(g).s * u;
   }
 }
 

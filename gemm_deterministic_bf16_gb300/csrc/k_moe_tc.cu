@@ -677,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               hv[b] = at[R];
             }
 #pragma unroll
-            for (int b = 0; b < 2; ++b) hv[b] *= __fdividef(gt[b], 1.0f + __expf(-gt[b]));
+            for (int b = 0; b < 2; ++b) hv[b] *= gt[b] * sigma<false>(gt[b]).s;
 #pragma unroll
             for (int b = 0; b < 2; ++b) {
               const int i = i0 + b * (128 / R);   // (the same in all threads of a warp)

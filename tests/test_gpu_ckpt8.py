@@ -186,3 +186,36 @@ def test_refusals(G):
     with pytest.raises(G.DetFFNError) as e:
         G.detffn_ckpt8_pack(v, v, c._replace(up_codes=c.gate_codes))
     assert e.value.status == 1
+
+
+@pytest.mark.parametrize("M,I", [(64, 1024), (7, 5003)])
+def test_silu_backward_in_fp32_for_any_gate(G, M, I):
+    """FP32: with e = 2^-24, exp is off by at most 2 ulp (4 e), 1 + exp and its
+    reciprocal by e each, so sigma by 6 e and 1 - sigma by 11 e; a product or a sum
+    adds e.  The longest chain, dG's, ends below 24 e, whatever the gate."""
+    g = torch.Generator().manual_seed(I)
+    gate = ((torch.rand((M, I), generator=g) * 2 - 1) * 86).cuda()
+    gate[:, :64] = -88.0
+    c = G.detffn_ckpt8_pack(gate, data(M, I, "f32", 6))
+    dh = data(M, I, "f32", 7)
+    got = dict(zip(("dU", "dG", "h"), G.detffn_ckpt8_silu_backward(dh, c)))
+    gd, u = (t.cpu().double().numpy() for t in G.detffn_ckpt8_unpack(c, dtype=torch.float32))
+    for n, (v, mag) in stage64(dh.cpu().double().numpy(), gd, u).items():
+        err = np.abs(got[n].cpu().double().numpy() - v)
+        assert (err <= 24 * 2.0 ** -24 * mag + 1e-42).all(), (n, float((err / (24 * 2.0 ** -24 * mag)).max()))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_silu_backward_of_gates_at_the_end_of_the_range(G, dt):
+    """exp(88) is a number, though more than 2^126: its reciprocal times a large
+    factor is an ordinary number."""
+    g = torch.tensor([-80.0, -86.0, -87.5, -88.0]).repeat_interleave(64).expand(3, 256).contiguous().cuda()
+    c = G.detffn_ckpt8_pack(g, torch.full_like(g, 2.0 ** 120))
+    dh = torch.full_like(g, 2.0 ** 118).to(DT[dt][0])
+    dU, dG, h = G.detffn_ckpt8_silu_backward(dh, c)
+    gd, u = (t.cpu().double().numpy() for t in G.detffn_ckpt8_unpack(c, dtype=torch.float32))
+    ref = stage64(np.full_like(gd, 2.0 ** 118), gd, u)
+    for got, n in ((dU, "dU"), (h, "h")):   # (dG's factors alone leave the range)
+        v, mag = ref[n]
+        err = np.abs(got.cpu().double().numpy() - v)
+        assert (err <= DT[dt][1] * np.abs(v) + (np.abs(gd) + 8) * 2.0 ** -22 * mag).all(), n

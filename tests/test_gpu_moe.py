@@ -351,3 +351,20 @@ def test_profiling_records_the_layer(G, path, name, launches):
     assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))
     G.detffn_moe_forward(s["x"], *rest, path=path)
     assert not G.detffn_profile_read()
+
+
+@pytest.mark.parametrize("path", [1, 2])
+def test_gates_at_the_end_of_the_range(G, path):
+    """SiLU(-88) is -88 exp(-88), and exp(88) is a number, though more than 2^126;
+    exp(90) is not one, and SiLU(-90) is.  One feature's h to each output."""
+    H = I = 64
+    g = torch.tensor([-80.0, -86.0, -87.5, -88.0, -88.5, -89.0, -89.5, -90.0]).repeat(8)
+    x, Wr = torch.zeros((1, H)), torch.zeros((1, H))
+    Wg, Wu = torch.zeros((1, I, H)), torch.zeros((1, I, H))
+    x[0, 0] = 1
+    Wg[0, :, 0], Wu[0, :, 0] = g, 2.0 ** 120
+    t = [v.bfloat16().cuda() for v in (x, Wr, Wg, Wu, torch.eye(I)[None])]
+    out = G.detffn_moe_forward(*t, 1, path=path)[0][0].cpu().double()
+    h = g.double() * torch.sigmoid(g.double()) * 2.0 ** 120
+    # (exp(-90) is subnormal in FP32, in steps of 2^-19 of it at the most)
+    assert bool(((out - h).abs() <= (2.0 ** -8 + 2.0 ** -15) * h.abs()).all()), (out / h)
