@@ -344,7 +344,8 @@ MoeArgs moe_plan(Arena& w, long long T, long long E, long long k, long long H, l
   int parts = 1, stages = 0;
   moe_parts(H, I, &parts, &stages);
   sc->y = w.take<float>(parts * T * k * H);
-  if (dtype == DETFFN_F16) sc->h32 = w.take<float>(T * k * I);
+  // (FP16's, but a workspace sized for BF16 serves FP16 too)
+  if (dtype != DETFFN_F32) sc->h32 = w.take<float>(T * k * I);
   return a;
 }
 

@@ -192,6 +192,14 @@ def test_empty_streams_and_workspace(G):
         assert all(torch.equal(a, b) for a, b in zip(ref, got))
 
 
+def test_a_workspace_of_either_16_bit_type_serves_both(G):
+    size = lambda dt: G.detffn_moe_workspace_size(6, 8, 2, 256, 192, dtype=dt)  # noqa: E731
+    assert size(torch.float16) == size(torch.bfloat16)
+    s = inputs(6, 8, 256, 192, "f16", 19, 2)
+    ws = torch.empty(G.detffn_moe_workspace_size(6, 8, 2, 256, 192), dtype=torch.uint8, device="cuda")
+    check(G, s, 2, True, "f16", ws=ws)
+
+
 def test_stalled_wait_times_out_and_recovers(G):
     """The test-only stall flag withholds the copies, so the bounded waits run
     out: the call returns, the status says so, a call before it is read leaves
