@@ -9,7 +9,8 @@ gate and the residual scale around the FFN in one pass each way:
     y    = rmsnorm(r) * w_next                     (the next block's norm, same pass)
 
 Serving runs a few tokens through the same joins with a mixture of experts in
-the FFN's place.
+the FFN's place.  (The layer keeps FP32 sums where the FFN follows its tree, so
+one expert served is a rounding apart from the same FFN trained.)
 
     python examples/ffn_block.py [--tokens 512] [--width 1024] [--hidden 4096]
 """

@@ -75,8 +75,8 @@ def detffn_join_backward(r, z=None, dr=None, dy=None, w_post=None, gate=None, sc
                          dx=None, dz=None, ws=None, stream=None):
     """Gradients of detffn_join_forward from r, its out as stored (x where
     there was no z), the block output z, and the gradients dr of out and dy of
-    y (one may be None: zero).  Without w_pre the residual's gradient dx is dr
-    itself.  dx may be dr and dz may be z (in place)."""
+    y (dr may be None, zero, where dy is given; dy goes with w_pre).  Without
+    w_pre the residual's gradient dx is dr itself.  dx may be dr and dz may be z (in place)."""
     f = (_LIB or _native()).join_backward
     if stream is None:
         return JoinGrads(*f(r, z, dr, dy, w_post, gate, scale, w_pre, eps, dx, dz, ws))

@@ -905,8 +905,6 @@ extern "C" detffn_status detffn_forward_sharded(detffn_handle h, const void* x, 
 
 namespace {
 
-// Row-wise backward stages for rows [r0, r0+rows): dh, then dU and dG (and h
-// again, for the down projection's weight gradient, in the same pass).
 // Gate and up as the training forward saved them: in BF16, or in 8 bits
 // (ckpt.gq not null).
 struct Saved {
@@ -915,6 +913,8 @@ struct Saved {
   CkptArgs ckpt;
 };
 
+// Row-wise backward stages for rows [r0, r0+rows): dh, then dU and dG (and h
+// again, for the down projection's weight gradient, in the same pass).
 detffn_status rowwise_bwd(detffn_handle h, Family f, const uint16_t* dOut, const uint16_t* Wd,
                           const Saved& saved,
                           uint16_t* dh, uint16_t* dU, uint16_t* dG, uint16_t* hh, long long rows, long long H,

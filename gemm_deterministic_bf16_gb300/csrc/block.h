@@ -14,7 +14,8 @@ struct Rows {
 
 constexpr long long kJoinMaxH = 32768;
 // Column sums of the backward pass are taken over this many row sets at
-// most, whatever the GPU, so that their order depends on the sizes alone.
+// most, whatever the GPU, so that their order depends on the call alone (its
+// sizes, types, operands and 16-byte alignment).
 constexpr int kJoinSets = 152;
 
 struct JoinArgs {
@@ -35,7 +36,6 @@ struct JoinArgs {
   float* part = nullptr;      // backward: column partials [kind][set][H], then [set] for a scalar gate
 };
 
-size_t join_partials(long long M, long long H, bool post, bool pre, bool gate_feature, bool gate_scalar);
 cudaError_t join_forward_f32(const JoinArgs& a, cudaStream_t st);
 cudaError_t join_forward_f16(const JoinArgs& a, cudaStream_t st);
 cudaError_t join_forward_bf16(const JoinArgs& a, cudaStream_t st);

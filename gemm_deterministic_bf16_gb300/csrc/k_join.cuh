@@ -19,7 +19,9 @@
 // dgate is summed over what the gate is broadcast over (features, tokens or
 // both).  Sums over tokens: each block of threads adds the rows of its set
 // (rows s, s + sets, ...) in order, and a second kernel adds the sets in a
-// fixed order, so results do not depend on the run.
+// fixed order, so results do not depend on the run.  What a set is depends on the
+// sizes, the types, the norms and gate there are and the alignment; a row's own
+// results depend on H, the types and the alignment.
 #pragma once
 
 #include "block.h"

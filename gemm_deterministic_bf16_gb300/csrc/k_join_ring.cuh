@@ -648,12 +648,12 @@ cudaError_t ring_launch(const JoinArgs& a, const RingPlan& p, cudaStream_t st) {
   return launch_cluster(K, dim3(p.grid), p.G * p.R, smem, p.C, st, a, p);
 }
 
-// Whether a forward pass takes the ring kernel: it wins once its rows hold about
-// 4 MB (measured, BF16, H = 4096: 152 rows 3.3 us without and 3.7 us with it, 608
-// rows 7.9 and 5.4; H = 1024: 1216 rows 4.1 and 4.3, 4864 rows 14.0 and 11.3),
-// where the other kernel would have several units to a thread (H = 8192, 8 rows:
-// 4.1 and 4.0), and for rows that are not whole vectors (H = 1031: one row 3.6 and
-// 3.3 us, 16384 rows 100 and 36).
+// Whether a forward pass takes the ring kernel: it wins once its rows hold some
+// 4 to 7 MB (measured, BF16, H = 4096: 152 rows 3.1 us without and 3.6 us with it,
+// 304 rows 3.9 and 4.2, 456 rows 6.3 and 5.3, 1216 rows 15.1 and 11.7; H = 1024: 1216
+// rows 3.8 and 4.4, 2432 rows 6.6 and 5.5; H = 256: 8192 rows 5.0 and 5.0, 16384
+// rows 11.3 and 9.2; FP32, H = 4096: even from 152 rows on), and takes what the other
+// does not: rows of more than 4096 features and rows that are not whole vectors.
 inline bool ring_forward(const JoinArgs& a, const RingPlan& p, bool vec) {
   return !vec || a.M * p.row >= 4 << 20 || a.H > 4096;
 }

@@ -44,7 +44,9 @@
 // not: each term has a power of two of its own (Terms below), which holds 16
 // bits of h from 2^-13 to 2^23 and 2^-29 below.  A pair whose largest |h| lies
 // outside that range (or is not finite) is multiplied again at the end, on the
-// CUDA cores from h in FP32; its columns on the tensor cores are not used.  A
+// CUDA cores from h in FP32; its columns on the tensor cores are not used (one
+// token, 8 of 128 experts, H = 2048, I = 768: 28 us, and 313 with all pairs again;
+// 64 tokens, 6 of 64, H = 4096, I = 1536: 370 and 2041).  A
 // row's sum over K is one accumulation in FP32 in tensor memory, whatever the
 // other columns are, so a token's result does not depend on the other tokens.
 //

@@ -370,7 +370,10 @@ DETFFN_API detffn_status detffn_selfcheck_fused_schedule(unsigned long long *cas
  * mixture-of-experts layer for a few tokens.  Unlike the tree contractions
  * above these keep every sum in FP32 and round each output once; their
  * results do not depend on the stream or the run either.  Calls without a
- * handle run on the current device.
+ * handle run on the current device.  The mixture-of-experts layer is therefore
+ * not one of the tree contractions: with one expert its bits are not those of
+ * detffn_forward, and a model that is trained by detffn_backward and served by
+ * the layer runs two arithmetics, a rounding apart.
  * ------------------------------------------------------------------------ */
 
 /* The residual join (forward).  For each token m < M, over H <= 32768
@@ -400,15 +403,21 @@ DETFFN_API detffn_status detffn_join_forward(const void* x, long long ldx, const
 DETFFN_API detffn_status detffn_join_workspace_size(long long M, long long H, size_t* bytes);
 
 /* The residual join's gradients.  r is the forward's out as it was stored
- * (x where there was no z), dr and dy the gradients of out and y (either may
- * be NULL: zero; dy goes with w_pre).
+ * (x where there was no z), dr and dy the gradients of out and y.  dr may be
+ * NULL (zero) where dy is given; dy is given exactly where w_pre is.
  *   dx = dr + the norm's gradient of dy         (where w_pre; else dx is dr itself, pass NULL)
  *   dz, dgate, dw_post, dw_pre as the formulas above give them
  * dgate has the gate's own shape, contiguous ([1], [H], [M] or [M, H]); it,
  * dw_post and dw_pre are `param_dtype`, written (not added to), and given
  * exactly where the parameter is.  dz NULL: no block output (w_post, gate and
  * z are NULL too).  z is read only with w_post or a gate.  dx may be exactly
- * dr and dz exactly z.  Sums over tokens run in an order fixed by M alone. */
+ * dr and dz exactly z.
+ * The same call gives the same bits.  A row's dx and dz do not depend on the
+ * other rows or on M (nor does its dgate, with gate_rs).  Sums over tokens run in
+ * an order that M, H, the types, the operands given (norms, dr, the gate's
+ * strides) and whether all rows and parameters lie on 16-byte boundaries fix
+ * together: a call that differs in one of these may differ in the last bits of
+ * dw_post, dw_pre and a shared gate's dgate. */
 DETFFN_API detffn_status detffn_join_backward(const void* r, long long ldr, const void* dr, long long lddr,
                                               const void* dy, long long lddy, const void* z, long long ldz,
                                               const void* w_post, const void* gate, long long gate_rs,
@@ -421,7 +430,7 @@ DETFFN_API detffn_status detffn_join_backward(const void* r, long long ldr, cons
  * codes [M, I] signed bytes and scales [M, ceil(I / 64)] FP32, one scale per
  * 64 consecutive features of a token (the last block of a row may be short).
  *   scale = max|v| * (1 / 127),  code = rint(v / scale) in [-127, 127],  value = code * scale
- * A block of zeros has scale 0; a block that holds an infinity or a NaN has
+ * A block of zeros has scale 0 (as has one whose scale rounds to 0); a block that holds an infinity or a NaN has
  * scale NaN, and all its values read back as NaN. */
 DETFFN_API detffn_status detffn_ckpt8_pack(const void* gate, const void* up, void* gate_codes, void* gate_scales,
                                            void* up_codes, void* up_scales, long long M, long long I, int dtype,
