@@ -22,3 +22,8 @@ from .block import (  # noqa: F401
     Ckpt8, JoinGrads, detffn_backward_ckpt8, detffn_ckpt8_pack, detffn_ckpt8_silu_backward, detffn_ckpt8_unpack, detffn_join_backward,
     detffn_join_forward, detffn_join_workspace_size, detffn_moe_forward, detffn_moe_workspace_size,
 )
+from .products import (  # noqa: F401
+    W4, detffn_dropout_backward, detffn_dropout_forward, detffn_grouped_backward, detffn_grouped_forward,
+    detffn_grouped_workspace_size, detffn_w4_forward, detffn_w4_matvec, detffn_w4_pack, detffn_w4_unpack,
+    detffn_w4_workspace_size,
+)

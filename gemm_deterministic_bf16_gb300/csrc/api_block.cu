@@ -5,52 +5,12 @@
 #include <math.h>
 
 #include "block.h"
-#include "handle.h"
+#include "checks.h"
 #include "moe.h"
 
 using namespace detffn;
 
 namespace {
-
-bool good_type(int t) { return t == DETFFN_F32 || t == DETFFN_F16 || t == DETFFN_BF16; }
-long long bytes_of(int t) { return t == DETFFN_F32 ? 4 : 2; }
-bool on(const void* p, long long n) { return ((uintptr_t)p % (uintptr_t)n) == 0; }
-
-// One operand of a call, for the overlap checks: `rows` rows of `row` bytes,
-// `step` bytes apart.
-struct Span {
-  const void* p = nullptr;
-  long long rows = 0, row = 0, step = 0;
-};
-
-// Whether two operands share a byte.  Rows of equal step may interleave (the
-// column halves of one buffer); otherwise their whole extents count.
-bool meet(const Span& a, const Span& b) {
-  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.row <= 0 || b.row <= 0) return false;
-  if (!overlap(a.p, (a.rows - 1) * a.step + a.row, b.p, (b.rows - 1) * b.step + b.row)) return false;
-  if (a.rows > 1 && b.rows > 1 && a.step == b.step && a.step > 0) {
-    const long long d = (long long)(((uintptr_t)b.p - (uintptr_t)a.p) % (uintptr_t)a.step);
-    const long long up = (uintptr_t)b.p >= (uintptr_t)a.p
-                             ? d
-                             : (a.step - (long long)(((uintptr_t)a.p - (uintptr_t)b.p) % (uintptr_t)a.step)) % a.step;
-    return !(up >= a.row && a.step - up >= b.row);
-  }
-  return true;
-}
-
-bool same(const Span& a, const Span& b) { return a.p == b.p && (a.step == b.step || a.rows <= 1); }
-
-// Every output against every input and every other output.  Output `o` may be
-// exactly input alias[o] (in place); -1: no input.
-detffn_status check_overlap(const Span* in, int ni, const Span* out, int no, const int* alias) {
-  for (int o = 0; o < no; ++o) {
-    for (int i = 0; i < ni; ++i)
-      if (meet(out[o], in[i]) && !(alias[o] == i && same(out[o], in[i]))) return DETFFN_ERR_INVALID_ARG;
-    for (int q = o + 1; q < no; ++q)
-      if (meet(out[o], out[q])) return DETFFN_ERR_INVALID_ARG;
-  }
-  return DETFFN_OK;
-}
 
 detffn_status join_sizes(long long M, long long H, int dtype, int pdtype) {
   if (!good_type(dtype) || !good_type(pdtype)) return DETFFN_ERR_INVALID_ARG;
@@ -65,11 +25,6 @@ detffn_status join_gate(const void* gate, long long rs, long long cs, long long 
   if (cs == 1 && rs != 0 && M > 1 && rs < H) return DETFFN_ERR_SHAPE;
   return DETFFN_OK;
 }
-
-Span rows_span(const void* p, long long M, long long H, long long ld, long long es) {
-  return Span{p, M, H * es, ld * es};
-}
-Span flat_span(const void* p, long long bytes) { return Span{p, 1, bytes, bytes}; }
 
 // The kernels index rows with the row stride alone, so one row of a tensor
 // may have any stride.
@@ -89,12 +44,6 @@ cudaError_t run_join(const JoinArgs& a, bool back, cudaStream_t st) {
   if (a.dtype == DETFFN_F32) return back ? join_backward_f32(a, st) : join_forward_f32(a, st);
   if (a.dtype == DETFFN_F16) return back ? join_backward_f16(a, st) : join_forward_f16(a, st);
   return back ? join_backward_bf16(a, st) : join_forward_bf16(a, st);
-}
-
-detffn_status current_sms(int* sms) {
-  int dev = 0;
-  TRYCU(cudaGetDevice(&dev));
-  return cu(cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev));
 }
 
 detffn_status ckpt_check(long long M, long long I, int dtype, const void* gq, const void* gs, const void* uq,

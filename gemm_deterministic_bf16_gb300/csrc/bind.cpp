@@ -377,6 +377,16 @@ PyObject* ckpt8_silu_backward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END_BODY
 }
 
+detffn_options options(PyObject* path, PyObject* spin_limit, PyObject* flags) {
+  detffn_options o{};
+  o.leaf_width = 64;
+  o.path = (int)integer(path);
+  o.shards = 1;
+  o.spin_limit = integer(spin_limit);
+  o.flags = (int)integer(flags);
+  return o;
+}
+
 // (handle, x, Wr, Wg, Wu, Wd, top_k, normalize, out, experts, weights, ws, path, spin_limit, flags)
 PyObject* moe_forward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   BODY(15)
@@ -409,12 +419,7 @@ PyObject* moe_forward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   WHOLE(*experts, dev, at::kInt, {T, k});
   WHOLE(*weights, dev, at::kFloat, {T, k});
   need(ws->is_cuda() && ws->get_device() == dev && ws->is_contiguous(), "ws: expected a contiguous CUDA buffer");
-  detffn_options o{};
-  o.leaf_width = 64;
-  o.path = (int)integer(a[12]);
-  o.shards = 1;
-  o.spin_limit = integer(a[13]);
-  o.flags = (int)integer(a[14]);
+  const detffn_options o = options(a[12], a[13], a[14]);
   const int normalize = PyObject_IsTrue(a[7]);
   if (normalize < 0) throw Refused();
   check(detffn_moe_forward(reinterpret_cast<detffn_handle>(integer(a[0])), x->data_ptr(), Wr->data_ptr(),
@@ -423,6 +428,258 @@ PyObject* moe_forward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
                            (int)k, normalize, H, I, dt, ws->data_ptr(), (size_t)ws->nbytes(), stream_of(dev), &o),
         "detffn_moe_forward");
   return tuple({out, experts, weights});
+  END_BODY
+}
+
+// What a grouped call's tensors share: x or dOut [R, ...], W [E, N, K], offsets.
+struct Groups {
+  long long R, E, K, N;
+  int device, type;
+  const int* offsets;
+};
+Groups groups(const Tensor* rows_of, const Tensor* W, const Tensor* offsets) {
+  need(rows_of && W && offsets && rows_of->is_cuda() && rows_of->dim() == 2 && W->dim() == 3 &&
+           type_of(rows_of->scalar_type()) >= 0,
+       "expected x [R, K] and W [E, N, K] in float32, float16 or bfloat16 on a CUDA device, and offsets");
+  Groups g;
+  g.R = rows_of->size(0), g.E = W->size(0), g.N = W->size(1), g.K = W->size(2);
+  g.device = (int)rows_of->get_device();
+  g.type = type_of(rows_of->scalar_type());
+  WHOLE(*W, g.device, rows_of->scalar_type(), {g.E, g.N, g.K});
+  whole(*offsets, g.device, at::kInt, {g.E + 1}, "offsets: expected a contiguous int32 CUDA tensor [E + 1]");
+  g.offsets = static_cast<const int*>(offsets->data_ptr());
+  return g;
+}
+// Rows [R, width] of a grouped call.
+long long group_rows(const Tensor* t, const Groups& g, long long width, const Tensor* like, const char* what) {
+  need(t && t->dim() == 2 && t->size(0) == g.R && t->size(1) == width && t->scalar_type() == like->scalar_type() &&
+           t->get_device() == like->get_device(),
+       what);
+  return rows(t, nullptr, what);
+}
+#define GROUP_ROWS(t, width, like) \
+  group_rows(t, g, width, like, #t ": expected a 2-D CUDA tensor of contiguous rows with the call's shape, dtype and device")
+
+const Tensor* group_scratch(const Groups& g, const Tensor* ws, const Tensor* like, Tensor* own) {
+  size_t bytes = 0;
+  check(detffn_grouped_workspace_size(g.R, g.E, g.K, g.N, g.type, &bytes), "detffn_grouped_workspace_size");
+  if (!ws && bytes) ws = &(*own = empty({(long long)bytes}, *like, at::kByte));
+  need(!ws || (ws->is_cuda() && ws->get_device() == g.device && ws->is_contiguous()), "ws: expected a contiguous CUDA buffer");
+  return ws;
+}
+
+// (handle, x, W, offsets, out, ws, path, spin_limit, flags)
+PyObject* grouped_forward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  BODY(9)
+  const Tensor *x = tensor(a[1], "x"), *W = tensor(a[2], "W"), *offsets = tensor(a[3], "offsets"),
+               *out = tensor(a[4], "out"), *ws = tensor(a[5], "ws");
+  const Groups g = groups(x, W, offsets);
+  const long long ldx = GROUP_ROWS(x, g.K, x);
+  const c10::cuda::CUDAGuard guard(x->device());
+  Tensor t_out, t_ws;
+  if (!out) out = &(t_out = empty({g.R, g.N}, *x, x->scalar_type()));
+  const long long ldo = GROUP_ROWS(out, g.N, x);
+  ws = group_scratch(g, ws, x, &t_ws);
+  const detffn_options o = options(a[6], a[7], a[8]);
+  check(detffn_grouped_forward(reinterpret_cast<detffn_handle>(integer(a[0])), x->data_ptr(), ldx, W->data_ptr(),
+                               g.offsets, out->data_ptr(), ldo, g.R, g.E, g.K, g.N, g.type, const_cast<void*>(ptr(ws)),
+                               ws ? (size_t)ws->nbytes() : 0, stream_of(g.device), &o),
+        "detffn_grouped_forward");
+  return tuple({out});
+  END_BODY
+}
+
+// (handle, x, W, offsets, dOut, dX, dW, need_dX, need_dW, ws, path, spin_limit, flags)
+PyObject* grouped_backward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  BODY(13)
+  const Tensor *x = tensor(a[1], "x"), *W = tensor(a[2], "W"), *offsets = tensor(a[3], "offsets"),
+               *dOut = tensor(a[4], "dOut"), *dX = tensor(a[5], "dX"), *dW = tensor(a[6], "dW"), *ws = tensor(a[9], "ws");
+  const bool want_x = PyObject_IsTrue(a[7]) == 1, want_w = PyObject_IsTrue(a[8]) == 1;
+  need(want_x || want_w, "nothing to form: need_dX and need_dW are both false");
+  need((want_x || !dX) && (want_w || !dW), "dX and dW go with need_dX and need_dW");
+  const Groups g = groups(dOut, W, offsets);
+  const long long lddo = GROUP_ROWS(dOut, g.N, dOut), ldx = want_w || x ? GROUP_ROWS(x, g.K, dOut) : 0;
+  const c10::cuda::CUDAGuard guard(dOut->device());
+  Tensor t_x, t_w, t_ws;
+  if (want_x && !dX) dX = &(t_x = empty({g.R, g.K}, *dOut, dOut->scalar_type()));
+  if (want_w && !dW) dW = &(t_w = empty({g.E, g.N, g.K}, *dOut, dOut->scalar_type()));
+  const long long lddx = want_x ? GROUP_ROWS(dX, g.K, dOut) : 0;
+  if (want_w) WHOLE(*dW, g.device, dOut->scalar_type(), {g.E, g.N, g.K});
+  ws = group_scratch(g, ws, dOut, &t_ws);
+  const detffn_options o = options(a[10], a[11], a[12]);
+  check(detffn_grouped_backward(reinterpret_cast<detffn_handle>(integer(a[0])), ptr(x), ldx, W->data_ptr(), g.offsets,
+                                dOut->data_ptr(), lddo, const_cast<void*>(ptr(dX)), lddx, const_cast<void*>(ptr(dW)), g.R,
+                                g.E, g.K, g.N, g.type, const_cast<void*>(ptr(ws)), ws ? (size_t)ws->nbytes() : 0,
+                                stream_of(g.device), &o),
+        "detffn_grouped_backward");
+  return tuple({dX, dW});
+  END_BODY
+}
+
+at::ScalarType scalar_of(long long code) {
+  need(code >= DETFFN_F32 && code <= DETFFN_BF16, "dtype: expected float32, float16 or bfloat16");
+  return code == DETFFN_F32 ? at::kFloat : code == DETFFN_F16 ? at::kHalf : at::kBFloat16;
+}
+long long bounded(PyObject* o, const char* what) {
+  const long long v = integer(o);
+  need(v >= 1 && v <= 1 << 20, what);
+  return v;
+}
+
+// A 4-bit matrix at a[0 .. 3]: codes, scales, K, group.
+struct Bits4 {
+  const Tensor *codes, *scales;
+  long long N, K, group;
+  int device, type;
+};
+Bits4 bits4(PyObject* const* a) {
+  Bits4 m;
+  m.codes = tensor(a[0], "codes");
+  m.scales = tensor(a[1], "scales");
+  m.K = bounded(a[2], "K: expected 1 to 2^20");
+  m.group = bounded(a[3], "group: expected 32, 64 or 128");
+  const char* what = "expected contiguous CUDA codes [N, 64 ceil(K / 128)] (uint8) and scales [N, ceil(K / group)] (float32, float16 or bfloat16)";
+  need(m.codes && m.scales && m.codes->dim() == 2 && m.codes->is_cuda() && type_of(m.scales->scalar_type()) >= 0, what);
+  m.N = m.codes->size(0);
+  m.device = (int)m.codes->get_device();
+  m.type = type_of(m.scales->scalar_type());
+  whole(*m.codes, m.device, at::kByte, {m.N, (m.K + 127) / 128 * 64}, what);
+  whole(*m.scales, m.device, m.scales->scalar_type(), {m.N, (m.K + m.group - 1) / m.group}, what);
+  return m;
+}
+
+// (w, group, scale dtype code, codes, scales) with the last two both None or neither
+PyObject* w4_pack(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  BODY(5)
+  const Tensor *w = tensor(a[0], "w"), *codes = tensor(a[3], "codes"), *scales = tensor(a[4], "scales");
+  need(w != nullptr, "w must be given");
+  const long long ldw = ROWS(w, nullptr), N = w->size(0), K = w->size(1), group = bounded(a[1], "group: expected 32, 64 or 128");
+  const at::ScalarType st = scalar_of(integer(a[2]));
+  const int dev = (int)w->get_device();
+  const c10::cuda::CUDAGuard guard(w->device());
+  need(!codes == !scales, "codes and scales go together");
+  Tensor c, s;
+  if (!codes) {
+    Together both;
+    both.add(&c, {N, (K + 127) / 128 * 64}, at::kByte);
+    both.add(&s, {N, (K + group - 1) / group}, st);
+    both.allocate(*w);
+    codes = &c, scales = &s;
+  }
+  WHOLE(*codes, dev, at::kByte, {N, (K + 127) / 128 * 64});
+  WHOLE(*scales, dev, st, {N, (K + group - 1) / group});
+  check(detffn_w4_pack(w->data_ptr(), ldw, codes->data_ptr(), scales->data_ptr(), N, K, (int)group, type_of(w->scalar_type()),
+                       type_of(st), stream_of(dev)),
+        "detffn_w4_pack");
+  return tuple({codes, scales});
+  END_BODY
+}
+
+// (codes, scales, K, group, dtype code, out)
+PyObject* w4_unpack(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  BODY(6)
+  const Bits4 m = bits4(a);
+  const at::ScalarType st = scalar_of(integer(a[4]));
+  const Tensor* out = tensor(a[5], "out");
+  const c10::cuda::CUDAGuard guard(m.codes->device());
+  Tensor t;
+  if (!out) out = &(t = empty({m.N, m.K}, *m.codes, st));
+  const long long ldo = ROWS(out, nullptr);
+  need(out->size(0) == m.N && out->size(1) == m.K && out->scalar_type() == st && out->get_device() == m.device,
+       "out: expected [N, K] of dtype on the device of the codes");
+  check(detffn_w4_unpack(m.codes->data_ptr(), m.scales->data_ptr(), out->data_ptr(), ldo, m.N, m.K, (int)m.group, type_of(st),
+                         m.type, stream_of(m.device)),
+        "detffn_w4_unpack");
+  return tuple({out});
+  END_BODY
+}
+
+// (x, codes, scales, K, group, out)
+PyObject* w4_matvec(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  BODY(6)
+  const Tensor *x = tensor(a[0], "x"), *out = tensor(a[5], "out");
+  need(x != nullptr, "x must be given");
+  const Bits4 m = bits4(a + 1);
+  const long long ldx = ROWS(x, nullptr), T = x->size(0);
+  need(x->size(1) == m.K && x->get_device() == m.device, "x: expected [T, K] on the device of the codes");
+  const c10::cuda::CUDAGuard guard(x->device());
+  Tensor t;
+  if (!out) out = &(t = empty({T, m.N}, *x, x->scalar_type()));
+  const long long ldo = ROWS(out, nullptr);
+  need(out->size(0) == T && out->size(1) == m.N && out->scalar_type() == x->scalar_type() && out->get_device() == m.device,
+       "out: expected [T, N] of x's dtype on its device");
+  check(detffn_w4_matvec(x->data_ptr(), ldx, m.codes->data_ptr(), m.scales->data_ptr(), out->data_ptr(), ldo, T, m.N, m.K,
+                         (int)m.group, type_of(x->scalar_type()), m.type, stream_of(m.device)),
+        "detffn_w4_matvec");
+  return tuple({out});
+  END_BODY
+}
+
+// (x, gate's four, up's four, down's four, out, ws)
+PyObject* w4_forward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  BODY(15)
+  const Tensor *x = tensor(a[0], "x"), *out = tensor(a[13], "out"), *ws = tensor(a[14], "ws");
+  need(x != nullptr, "x must be given");
+  const Bits4 g = bits4(a + 1), u = bits4(a + 5), d = bits4(a + 9);
+  const long long ldx = ROWS(x, nullptr), T = x->size(0), H = g.K, I = g.N;
+  need(x->size(1) == H && x->get_device() == g.device, "x: expected [T, H] on the device of the codes");
+  need(u.K == H && u.N == I && d.K == I && d.N == H && u.group == g.group && d.group == g.group && u.type == g.type &&
+           d.type == g.type && u.device == g.device && d.device == g.device,
+       "expected gate and up [I, H] and down [H, I] of one group, scale dtype and device");
+  const c10::cuda::CUDAGuard guard(x->device());
+  Tensor t, t_ws;
+  if (!out) out = &(t = empty({T, H}, *x, x->scalar_type()));
+  const long long ldo = ROWS(out, x);
+  size_t bytes = 0;
+  check(detffn_w4_workspace_size(T, H, I, &bytes), "detffn_w4_workspace_size");
+  if (!ws) ws = &(t_ws = empty({(long long)(bytes < 256 ? 256 : bytes)}, *x, at::kByte));
+  need(ws->is_cuda() && ws->get_device() == g.device && ws->is_contiguous(), "ws: expected a contiguous CUDA buffer");
+  check(detffn_w4_forward(x->data_ptr(), ldx, g.codes->data_ptr(), g.scales->data_ptr(), u.codes->data_ptr(),
+                          u.scales->data_ptr(), d.codes->data_ptr(), d.scales->data_ptr(), out->data_ptr(), ldo, T, H, I,
+                          (int)g.group, type_of(x->scalar_type()), g.type, ws->data_ptr(), (size_t)ws->nbytes(),
+                          stream_of(g.device)),
+        "detffn_w4_forward");
+  return tuple({out});
+  END_BODY
+}
+
+// The low 64 bits of an integer in [0, 2^64).
+unsigned long long word64(PyObject* o, const char* what) {
+  const unsigned long long v = PyLong_AsUnsignedLongLong(o);
+  if (v == (unsigned long long)-1 && PyErr_Occurred()) {
+    if (!PyErr_ExceptionMatches(PyExc_OverflowError)) throw Refused();
+    PyErr_Clear();
+    refuse(what);
+  }
+  return v;
+}
+
+// (x, p, seed (a number or a tensor), offset, residual, out, backward)
+PyObject* dropout(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
+  BODY(7)
+  const Tensor *x = tensor(a[0], "x"), *residual = tensor(a[4], "residual"), *out = tensor(a[5], "out");
+  need(x != nullptr, "x must be given");
+  const long long ldx = ROWS(x, nullptr), ldr = ROWS(residual, x), M = x->size(0), H = x->size(1);
+  const int dev = (int)x->get_device();
+  const Tensor* state = THPVariable_Check(a[2]) ? tensor(a[2], "seed") : nullptr;
+  if (state) whole(*state, dev, at::kLong, {2}, "seed: expected a number or a contiguous int64 CUDA tensor [2]");
+  const unsigned long long seed = state ? 0 : word64(a[2], "seed: expected 0 to 2^64 - 1"),
+                           offset = word64(a[3], "offset: expected 0 to 2^64 - 1");
+  const c10::cuda::CUDAGuard guard(x->device());
+  Tensor t;
+  if (!out) out = &(t = empty({M, H}, *x, x->scalar_type()));
+  const long long ldo = ROWS(out, x);
+  const unsigned long long* words = static_cast<const unsigned long long*>(ptr(state));
+  const int type = type_of(x->scalar_type());
+  if (PyObject_IsTrue(a[6]) == 1)
+    check(detffn_dropout_backward(x->data_ptr(), ldx, out->data_ptr(), ldo, number(a[1]), seed, offset, words, M, H, type,
+                                  stream_of(dev)),
+          "detffn_dropout_backward");
+  else
+    check(detffn_dropout_forward(x->data_ptr(), ldx, ptr(residual), ldr, out->data_ptr(), ldo, number(a[1]), seed, offset,
+                                 words, M, H, type, stream_of(dev)),
+          "detffn_dropout_forward");
+  return tuple({out});
   END_BODY
 }
 
@@ -436,6 +693,9 @@ PyObject* set_error(PyObject*, PyObject* e) {
 #define FAST(name) {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {FAST(join_forward),  FAST(join_backward),       FAST(ckpt8_pack),
                          FAST(ckpt8_unpack),  FAST(ckpt8_silu_backward), FAST(moe_forward),
+                         FAST(grouped_forward), FAST(grouped_backward),
+                         FAST(w4_pack),         FAST(w4_unpack),      FAST(w4_matvec),
+                         FAST(w4_forward),      FAST(dropout),
                          {"set_error", set_error, METH_O, nullptr},      {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

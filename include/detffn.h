@@ -482,6 +482,96 @@ DETFFN_API detffn_status detffn_moe_forward(detffn_handle h, const void* x, cons
                                             long long I, int dtype, void* ws, size_t ws_bytes, void* stream,
                                             const detffn_options* opts);
 
+/* Matrix products grouped by expert.  Expert e < E <= 1024 has the matrix W[e]
+ * ([N, K], W contiguous) and the rows [offsets[e], offsets[e + 1]) of x [R, K]
+ * and of out and dOut [R, N] (row strides ldx, ... in elements):
+ *   out[r]  = W[e] x[r]
+ *   dX[r]   = W[e]^T dOut[r]
+ *   dW[e]   = sum over the expert's rows r, ascending, of dOut[r] x[r]^T   (0 where it has none)
+ * of `dtype`, every sum FP32 and rounded once; dX or dW NULL: not formed (x, or
+ * W, may then be NULL).  `offsets` are E + 1 ascending ints on the device, read
+ * there: no host waits for them.  They may begin after row 0 and end before row
+ * R; rows of no expert are left as they were in out and dX.  Ends beyond R are
+ * taken as R, and an end before its beginning as no rows.  R < 2^31, K, N <= 65536.
+ * options->path: EXACT takes the CUDA-core kernels (any sizes and types), TENSOR
+ * the tensor cores (DETFFN_ERR_UNSUPPORTED where they do not cover the call).
+ * `ws` is of detffn_grouped_workspace_size bytes, 256-byte aligned; NULL where
+ * that is 0. */
+DETFFN_API detffn_status detffn_grouped_workspace_size(long long R, long long E, long long K, long long N, int dtype,
+                                                       size_t* bytes);
+DETFFN_API detffn_status detffn_grouped_forward(detffn_handle h, const void* x, long long ldx, const void* W,
+                                                const int* offsets, void* out, long long ldo, long long R, long long E,
+                                                long long K, long long N, int dtype, void* ws, size_t ws_bytes,
+                                                void* stream, const detffn_options* opts);
+DETFFN_API detffn_status detffn_grouped_backward(detffn_handle h, const void* x, long long ldx, const void* W,
+                                                 const int* offsets, const void* dOut, long long lddo, void* dX,
+                                                 long long lddx, void* dW, long long R, long long E, long long K,
+                                                 long long N, int dtype, void* ws, size_t ws_bytes, void* stream,
+                                                 const detffn_options* opts);
+
+/* 4-bit weights: a matrix [N, K] (N, K <= 2^20) as codes 0 .. 15 and one scale
+ * for each `group` (32, 64 or 128) consecutive codes of a row, the last group of
+ * a row short where K ends in it:
+ *   value[n, k] = (code[n, k] - 8) * scale[n, k / group]
+ * scales [N, ceil(K / group)] are FP32, FP16 or BF16 (`scale_dtype`).  codes:
+ * bytes [N, 64 ceil(K / 128)], 16-byte aligned.  A run of 128 codes takes 64
+ * bytes, 16 words of eight: word 4 t + g of a run (little-endian) holds the codes
+ * k = 32 g + 8 t + j, j < 8, of it, code j in bits 4 p .. 4 p + 3 with p = j / 2 +
+ * 4 (j mod 2).  Codes past K are ignored.
+ * detffn_w4_pack: scale = max|w| / 7 of the group, rounded to scale_dtype; code =
+ * 8 + rint(w / scale), from 1 to 15.  A group of zeros has scale 0 and codes 8 (as
+ * has one whose scale rounds to 0); one with an infinity or a NaN, or whose scale
+ * leaves its type, has scale NaN. */
+DETFFN_API detffn_status detffn_w4_pack(const void* w, long long ldw, void* codes, void* scales, long long N,
+                                        long long K, int group, int dtype, int scale_dtype, void* stream);
+/* The values, rounded once to `dtype`. */
+DETFFN_API detffn_status detffn_w4_unpack(const void* codes, const void* scales, void* w, long long ldw, long long N,
+                                          long long K, int group, int dtype, int scale_dtype, void* stream);
+
+/* out[t, n] = sum over k of x[t, k] * value[n, k] for T <= 64 tokens: x [T, K] and
+ * out [T, N] of `dtype` (any row strides).  A group's products are exact (FP16
+ * and BF16 x; FP32 x in three terms of eight bits) and summed in FP32, the
+ * group's sum scaled and added in FP32, out rounded once.  A token's result does
+ * not depend on the other tokens. */
+DETFFN_API detffn_status detffn_w4_matvec(const void* x, long long ldx, const void* codes, const void* scales, void* out,
+                                          long long ldo, long long T, long long N, long long K, int group, int dtype,
+                                          int scale_dtype, void* stream);
+
+/* The gated FFN of T <= 64 tokens from three 4-bit matrices of one group and
+ * scale type, gate and up [I, H], down [H, I]:
+ *   out = ((SiLU(x Wg^T) * (x Wu^T)) Wd^T
+ * as above; the hidden activation is kept in FP32, of which the down projection
+ * uses 24 significant bits (FP32) or 16.  out may be exactly x.  Not the tree of
+ * detffn_forward.  `ws`: detffn_w4_workspace_size bytes, 256-byte aligned. */
+DETFFN_API detffn_status detffn_w4_workspace_size(long long T, long long H, long long I, size_t* bytes);
+DETFFN_API detffn_status detffn_w4_forward(const void* x, long long ldx, const void* gate_codes, const void* gate_scales,
+                                           const void* up_codes, const void* up_scales, const void* down_codes,
+                                           const void* down_scales, void* out, long long ldo, long long T, long long H,
+                                           long long I, int group, int dtype, int scale_dtype, void* ws, size_t ws_bytes,
+                                           void* stream);
+
+/* Dropout whose mask is formed from a counter and never stored.  For m < M, c <
+ * H (any row strides):
+ *   word(m, c) = word c mod 4 of Philox4x32-10 (Salmon et al., SC 2011) of the counter
+ *                (c / 4, m, offset low, offset high) under the key (seed low, seed high)
+ *   out = residual + (word(m, c) >= floor(p 2^32) ? x * (1 / (1 - p)) : 0)
+ * for 0 <= p <= 1 (p = 1 keeps nothing), `residual` 0 where NULL; product and sum
+ * FP32, rounded once.  An element's word depends on its row, column, seed and
+ * offset alone.  state not NULL: two 64-bit words on the device, read when the
+ * kernel runs (a captured call draws a new mask at each replay that follows a
+ * change of them): the seed, instead of `seed`, and a number added to `offset`
+ * (mod 2^64).  out may be exactly x or the residual.
+ * The backward pass forms the same mask again: dX = kept ? dOut * (1 / (1 - p)) :
+ * 0; the residual's gradient is dOut itself. */
+DETFFN_API detffn_status detffn_dropout_forward(const void* x, long long ldx, const void* residual, long long ldr,
+                                                void* out, long long ldo, double p, unsigned long long seed,
+                                                unsigned long long offset, const unsigned long long* state, long long M,
+                                                long long H, int dtype, void* stream);
+DETFFN_API detffn_status detffn_dropout_backward(const void* dOut, long long lddo, void* dX, long long lddx, double p,
+                                                 unsigned long long seed, unsigned long long offset,
+                                                 const unsigned long long* state, long long M, long long H, int dtype,
+                                                 void* stream);
+
 /* Synchronises `stream`, then returns and clears the handle's device status
  * word (DETFFN_OK or DETFFN_ERR_TIMEOUT from a bounded wait).  The word is
  * sticky: once a wait has run out, every later streaming kernel launched

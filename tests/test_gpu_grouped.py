@@ -1,0 +1,237 @@
+"""Matrix products grouped by expert against 64-bit products.
+
+Tolerance: a sum of n FP32 products, in any order and each step off by at most
+one unit of FP32's last place (2^-23: the tensor cores may cut off), is off by at
+most n 2^-23 of the sum of the products' magnitudes; rounding to the stored type
+adds half a step of the result, and half the smallest step of FP16."""
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+HALF = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11, torch.float32: 2.0 ** -24}
+AUTO, EXACT, TENSOR = 0, 1, 2
+
+
+@pytest.fixture(scope="module")
+def G():
+    import gemm_deterministic_bf16_gb300 as G
+    from gemm_deterministic_bf16_gb300 import build
+    build.build()
+    assert G.detffn_get_status() == 0
+    yield G
+    assert G.detffn_get_status() == 0
+
+
+def make(sizes, K, N, dtype, seed=0, first=0, behind=0):
+    """x, W, dOut and offsets of experts with `sizes` rows, after `first` rows of none and before `behind`."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    R = first + sum(sizes) + behind
+    r = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    ends = [first]
+    for n in sizes:
+        ends.append(ends[-1] + n)
+    return r(R, K), r(len(sizes), N, K), r(R, N), torch.tensor(ends, dtype=torch.int32, device="cuda"), ends
+
+
+def close(got, want, bound, n, dtype):
+    tol = n * 2.0 ** -23 * bound + HALF[dtype] * want.abs() * (1 + 2.0 ** -8) + (2.0 ** -25 if dtype == torch.float16 else 0.0)
+    bad = ~((got.double() - want).abs() <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), float((got.double() - want).abs().max()), torch.nonzero(bad)[:4].tolist())
+
+
+def check_forward(G, x, W, off, ends, out, before):
+    for e in range(W.shape[0]):
+        a, b = ends[e], ends[e + 1]
+        x64, w64 = x[a:b].double(), W[e].double()
+        close(out[a:b], x64 @ w64.T, x64.abs() @ w64.abs().T, x.shape[1], x.dtype)
+    assert torch.equal(out[:ends[0]], before[:ends[0]]) and torch.equal(out[ends[-1]:], before[ends[-1]:])
+
+
+def check_backward(G, x, W, d, ends, dX, dW, before):
+    for e in range(W.shape[0]):
+        a, b = ends[e], ends[e + 1]
+        x64, w64, d64 = x[a:b].double(), W[e].double(), d[a:b].double()
+        close(dX[a:b], d64 @ w64, d64.abs() @ w64.abs(), W.shape[1], x.dtype)
+        close(dW[e], d64.T @ x64, d64.abs().T @ x64.abs(), max(b - a, 1), x.dtype)
+    assert torch.equal(dX[:ends[0]], before[:ends[0]]) and torch.equal(dX[ends[-1]:], before[ends[-1]:])
+
+
+def run(G, sizes, K, N, dtype, path=AUTO, seed=0, first=0, behind=0):
+    x, W, d, off, ends = make(sizes, K, N, dtype, seed, first, behind)
+    before = torch.randn((x.shape[0], N), device="cuda").to(dtype)
+    out = G.detffn_grouped_forward(x, W, off, out=before.clone(), path=path)
+    check_forward(G, x, W, off, ends, out, before)
+    before = torch.randn((x.shape[0], K), device="cuda").to(dtype)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d, dX=before.clone(), path=path)
+    check_backward(G, x, W, d, ends, dX, dW, before)
+    return out, dX, dW
+
+
+SIZES = [[1], [0, 1, 0], [16], [64, 64], [17, 0, 0, 255, 31], [300], [257, 1, 511, 128], [5] * 37, [0, 0, 1030]]
+WIDTHS = [(64, 64), (128, 256), (8, 8), (264, 520), (1, 1), (65, 33), (1031, 130), (72, 300)]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("K,N", WIDTHS)
+@pytest.mark.parametrize("sizes", SIZES, ids=lambda s: "-".join(map(str, s[:5])))
+def test_products(G, sizes, K, N, dtype):
+    run(G, sizes, K, N, dtype, seed=K + N)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("sizes", SIZES[3:7], ids=lambda s: "-".join(map(str, s[:5])))
+def test_cuda_core_path(G, sizes, dtype):
+    run(G, sizes, 264, 520, dtype, path=EXACT, seed=3)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("K,N", [(256, 136), (77, 100)])
+def test_rows_of_no_expert_stay(G, K, N, dtype):
+    run(G, [40, 0, 333], K, N, dtype, first=19, behind=70)
+
+
+@pytest.mark.parametrize("dtype,K,N", [(torch.bfloat16, 2048, 768), (torch.float16, 1416, 4096), (torch.bfloat16, 4096, 1536)])
+def test_larger(G, dtype, K, N):
+    run(G, [700, 0, 1033, 12, 255], K, N, dtype, seed=5)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("K,N", [(256, 512), (100, 66)])
+def test_row_strides(G, K, N, dtype):
+    """Rows inside wider buffers, aligned and not."""
+    sizes = [33, 0, 200]
+    x, W, d, off, ends = make(sizes, K, N, dtype)
+    for pad, at in ((64, 0), (64, 8), (3, 1)):
+        wide = lambda t: torch.full((t.shape[0], t.shape[1] + pad), float("nan"), dtype=dtype, device="cuda")  # noqa: E731
+        xs, ds, outs, dXs = wide(x), wide(d), wide(d), wide(x)
+        cut = lambda t, n: t[:, at:at + n] if pad > at else t[:, :n]  # noqa: E731
+        cut(xs, K).copy_(x)
+        cut(ds, N).copy_(d)
+        out = G.detffn_grouped_forward(cut(xs, K), W, off, out=cut(outs, N))
+        dX, dW = G.detffn_grouped_backward(cut(xs, K), W, off, cut(ds, N), dX=cut(dXs, K))
+        check_forward(G, x, W, off, ends, out, out)
+        check_backward(G, x, W, d, ends, dX, dW, dX)
+        for t, n in ((outs, N), (dXs, K)):
+            rest = torch.cat((t[:, :at], t[:, at + n:]), 1) if pad > at else t[:, n:]
+            assert bool(rest.isnan().all())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("sizes", [[37, 50, 13], [64, 3, 129], [1, 1, 1]])
+def test_rows_that_are_not_finite_stay_their_own(G, dtype, bad, sizes):
+    """An expert's rows, and rows of none, that hold an infinity or a NaN reach no other expert's results."""
+    K, N = 136, 264
+    x, W, d, off, ends = make(sizes, K, N, dtype, first=7, behind=90)
+    own = slice(ends[1], ends[2])
+    keep = [t.clone() for t in (x, d)]
+    for t in (x, d):
+        t[:ends[0]] = bad
+        t[own] = bad
+        t[ends[-1]:] = bad
+    out = G.detffn_grouped_forward(x, W, off)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d)
+    x, d = keep
+    for e in (0, 2):
+        a, b = ends[e], ends[e + 1]
+        x64, w64, d64 = x[a:b].double(), W[e].double(), d[a:b].double()
+        close(out[a:b], x64 @ w64.T, x64.abs() @ w64.abs().T, K, dtype)
+        close(dX[a:b], d64 @ w64, d64.abs() @ w64.abs(), N, dtype)
+        close(dW[e], d64.T @ x64, d64.abs().T @ x64.abs(), b - a, dtype)
+    assert not bool(out[own].isfinite().any()) and not bool(dW[1].isfinite().any())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_ends_out_of_order_or_range(G, dtype):
+    """Ends beyond R are R, an end before its beginning gives no rows; nothing else is touched."""
+    K, N, R = 128, 64, 100
+    x, W, d, _, _ = make([R], K, N, dtype)
+    W = torch.randn((3, N, K), device="cuda").to(dtype)
+    off = torch.tensor([10, 50, 40, 1000], dtype=torch.int32, device="cuda")
+    before = torch.randn((R, N), device="cuda").to(dtype)
+    out = G.detffn_grouped_forward(x, W, off, out=before.clone())
+    assert torch.equal(out[:10], before[:10])
+    x64 = x.double()
+    for e, a, b in ((0, 10, 40), (2, 50, 100)):
+        w64 = W[e].double()
+        close(out[a:b], x64[a:b] @ w64.T, x64[a:b].abs() @ w64.abs().T, K, dtype)
+    off = torch.tensor([-5, -1, 0, 0], dtype=torch.int32, device="cuda")
+    assert torch.equal(G.detffn_grouped_forward(x, W, off, out=before.clone()), before)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d, dX=x.clone())
+    assert torch.equal(dX, x) and not bool(dW.any())
+
+
+def test_gradient_by_differences(G):
+    """dX and dW against central differences of the forward in FP32: the sum of
+    out * dOut is linear in each input, so a step of 1 has no truncation error
+    and leaves the rounding of two sums of 50 * 24 products."""
+    x, W, d, off, _ = make([20, 0, 30], 16, 24, torch.float32)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d)
+    g = torch.Generator(device="cuda").manual_seed(9)
+    f = lambda x, W: float((G.detffn_grouped_forward(x, W, off).double() * d.double()).sum())  # noqa: E731
+    for t, grad, at in ((x, dX, 0), (W, dW, 1)):
+        v = torch.randn(t.shape, generator=g, device="cuda")
+        hi, lo = (f(*((t + s * v) if i == at else (x, W)[i] for i in range(2))) for s in (1.0, -1.0))
+        want = (hi - lo) / 2
+        size = float((d.abs().double() * 16 * 10).sum())   # |x W| summed, entries below 10
+        assert abs(float((grad.double() * v.double()).sum()) - want) <= 32 * 2.0 ** -23 * size
+
+
+@pytest.mark.parametrize("dtype,K,N", [(torch.bfloat16, 256, 384), (torch.float32, 100, 60)])
+def test_parts_streams_graphs_and_repeats(G, dtype, K, N):
+    x, W, d, off, _ = make([100, 3, 0, 61], K, N, dtype)
+    out = G.detffn_grouped_forward(x, W, off)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d)
+    assert torch.equal(out, G.detffn_grouped_forward(x, W, off))
+    a, none = G.detffn_grouped_backward(None, W, off, d, need_dW=False)
+    assert none is None and torch.equal(a, dX)
+    none, b = G.detffn_grouped_backward(x, W, off, d, need_dX=False)
+    assert none is None and torch.equal(b, dW)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    o2 = G.detffn_grouped_forward(x, W, off, stream=side)
+    x2, w2 = G.detffn_grouped_backward(x, W, off, d, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(out, o2) and torch.equal(dX, x2) and torch.equal(dW, w2)
+    graph = torch.cuda.CUDAGraph()
+    buf = torch.zeros_like(out)
+    with torch.cuda.graph(graph):
+        G.detffn_grouped_forward(x, W, off, out=buf)
+        gx, gw = G.detffn_grouped_backward(x, W, off, d)
+    # A replay reads the offsets as they are then.
+    for ends in ([0, 100, 103, 103, 164], [0, 1, 64, 100, 164]):
+        off.copy_(torch.tensor(ends, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(buf, G.detffn_grouped_forward(x, W, off))
+        ex, ew = G.detffn_grouped_backward(x, W, off, d)
+        assert torch.equal(gx, ex) and torch.equal(gw, ew)
+
+
+def test_no_rows(G):
+    x, W, d, off, _ = make([0, 0], 64, 32, torch.bfloat16)
+    assert G.detffn_grouped_forward(x, W, off).shape == (0, 32)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d)
+    assert dX.shape == (0, 64) and dW.shape == (2, 32, 64) and not bool(dW.any())
+
+
+def test_refusals(G):
+    x, W, d, off, _ = make([8, 8], 64, 32, torch.bfloat16)
+    for bad in ((x.float(), W, off), (x[:, :63], W, off), (x, W[0], off), (x, W, off[:2]), (x, W, off.long()),
+                (x.cpu(), W, off), (x, W.transpose(1, 2), off), (x.t(), W, off)):
+        with pytest.raises(ValueError):
+            G.detffn_grouped_forward(*bad)
+    with pytest.raises(ValueError):
+        G.detffn_grouped_forward(x, W, off, out=torch.empty((15, 32), dtype=x.dtype, device="cuda"))
+    with pytest.raises(ValueError):
+        G.detffn_grouped_backward(x, W, off, d[:8])
+    with pytest.raises(ValueError):
+        G.detffn_grouped_backward(None, W, off, d)
+    with pytest.raises(ValueError):
+        G.detffn_grouped_backward(x, W, off, d, need_dX=False, need_dW=False)
+    with pytest.raises(G.DetFFNError) as e:
+        G.detffn_grouped_forward(x, torch.randn((2, 64, 64), device="cuda").bfloat16(), off, out=x)
+    assert e.value.status == 1
+    with pytest.raises(G.DetFFNError) as e:
+        G.detffn_grouped_forward(x.float(), W.float(), off, path=TENSOR)
+    assert e.value.status == 4
