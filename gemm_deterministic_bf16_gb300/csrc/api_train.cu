@@ -51,12 +51,22 @@ detffn_status on_device(detffn_handle h, F&& f) {
 
 detffn_status run_grouped(detffn_handle h, const GroupedArgs& a, Grouped what, const detffn_options* o, cudaStream_t st) {
   const int path = o ? o->path : DETFFN_PATH_AUTO;
-  if (path == DETFFN_PATH_TENSOR) return DETFFN_ERR_UNSUPPORTED;
+  const bool tensor = path != DETFFN_PATH_EXACT && grouped_tensor_covers(a, what);
+  if (path == DETFFN_PATH_TENSOR && !tensor) return DETFFN_ERR_UNSUPPORTED;
+  Waits wt;
+  wt.status = h->d_status;
+  if (o) {
+    wt.spin = o->spin_limit;
+    wt.stall = (o->flags & DETFFN_FLAG_TEST_STALL) ? 1 : 0;
+  }
   const double es = (double)bytes_of(a.dtype), flops = 2.0 * a.R * a.K * a.N;
   // (the weights of as many experts as the rows can reach; the host does not know how many they do)
   const double w = what == Grouped::kWeight || a.R > a.E ? a.E : (double)a.R;
-  return timed(h, st, "grouped_general", es * ((double)a.R * (a.K + a.N) + w * a.K * a.N), flops,
-               [&] { return cu(launch_grouped_general(a, what, h->sm_count, st)); });
+  return timed(h, st, tensor ? "grouped_tensor" : "grouped_general", es * ((double)a.R * (a.K + a.N) + w * a.K * a.N), flops,
+               [&] {
+                 return cu(tensor ? launch_grouped_tensor(a, what, wt, h->sm_count, st)
+                                  : launch_grouped_general(a, what, h->sm_count, st));
+               });
 }
 
 // ---------------------------------------------------------------------------

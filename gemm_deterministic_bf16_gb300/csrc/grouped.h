@@ -23,6 +23,11 @@ struct GroupedArgs {
 
 enum class Grouped { kForward, kInput, kWeight };   // out, dx, dW
 
+// Tensor-core kernel: BF16 and FP16, K and N multiples of 8, x, W and dout on
+// 16-byte boundaries.
+bool grouped_tensor_covers(const GroupedArgs& a, Grouped what);
+cudaError_t launch_grouped_tensor(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_count, cudaStream_t st);
+
 // CUDA-core kernels for any sizes, strides and types.
 cudaError_t launch_grouped_general(const GroupedArgs& a, Grouped what, int sm_count, cudaStream_t st);
 

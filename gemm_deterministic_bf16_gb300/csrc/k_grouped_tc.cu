@@ -1,0 +1,440 @@
+// k_grouped_tc.cu -- matrix products grouped by expert on the tensor cores, BF16
+// and FP16 (the formulas are those of k_grouped.cu).
+//
+// Persistent pairs of CTAs (cta_group::2), one pair on two SMs, take output
+// tiles of 256 features x up to 256 rows in turn:
+//
+//            MMA rows (256)          MMA columns (up to 256)   contraction
+//   out      features n of W[e]      rows of x                 K
+//   dx       features k of W[e]      rows of dout              N
+//   dW       features k of x         features n of dout        rows of the expert
+//
+// so that the 32 lanes of a warp hold neighbours of one output row, and the
+// ragged side, the rows of an expert, is the one whose size an MMA can choose
+// (in steps of 32): an expert's rows are cut into equal tiles, and a tile's
+// MMAs cover its rows, not 256.  Operands that run across the contraction in
+// memory (W for dx, x and dout for dW) are read MN-major, without a copy.
+//
+// Each CTA of a pair loads its 128 rows of A and half of B by TMA, 64 of the
+// contraction to a stage, counted by barriers of the first CTA, which issues the
+// MMAs of both; FP32 sums in two halves of tensor memory, so that the next
+// tile's MMAs run while four warps of each CTA write the last one out.
+//
+// For dW the contraction ends with the expert's rows: those that the last 16 of
+// it take in beyond are another expert's and are cleared in shared memory, in
+// both operands (0 times an infinity is a NaN), by a warp that the last stage of
+// a tile goes through.
+//
+// The experts' rows are read on the device.  Every pair works out all tiles
+// from them and takes every (number of pairs)-th; the cut of the rows (the
+// widest tile) is the one whose rounds of tiles, each at the cost of its widest
+// tile, take least.
+#include "elt.cuh"
+#include "grouped.h"
+#include "ptx.cuh"
+#include "tc.h"
+
+namespace detffn {
+namespace {
+
+constexpr int kThreads = 256;       // warp 0 loads, 1 issues MMAs, 2 clears, 3 cuts the rows into tiles, 4-7 write out
+constexpr int kStages = 6;
+constexpr int kHalf = 128 * 128;    // bytes of an operand's part of a stage: 128 x 64
+constexpr int kStage = 2 * kHalf;
+constexpr int kCols = 256;          // columns of tensor memory to a tile's sums
+constexpr int kSuper = 8;           // feature tiles that are taken together
+
+struct Bars {
+  uint64_t full[kStages];    // first CTA: both CTAs' copies have landed
+  uint64_t empty[kStages];   // both: the stage's MMAs are done
+  uint64_t tail[kStages];    // both: this CTA's copies of a stage that is to be cleared have landed
+  uint64_t accf[2];          // both: a tile's sums are done
+  uint64_t acce[2];          // first CTA: both CTAs have read them
+  uint64_t fin;
+  uint32_t tmem;
+  int abort, cap, total;
+};
+
+struct Args {
+  int what;                  // 0 out, 1 dx, 2 dW
+  int E;
+  long long R;               // rows of all experts
+  const int* off;
+  int F;                     // output features (MMA rows' side)
+  int C;                     // contraction (out, dx)
+  int N;                     // dW: output rows
+  uint16_t* out;
+  long long ldo, stride;     // row stride; dW: elements of a matrix
+  int* status;
+  long long spin;
+  int stall;
+};
+
+// First row, rows, and the tiles before each expert's.
+struct Tables {
+  int *beg, *cnt, *pre;
+};
+__host__ __device__ inline int tables_bytes(int E) { return ((3 * E + 1) * 4 + 15) & ~15; }
+__device__ __forceinline__ Tables tables_at(unsigned char* p, int E) {
+  Tables t;
+  t.beg = reinterpret_cast<int*>(p);
+  t.cnt = t.beg + E;
+  t.pre = t.cnt + E;
+  return t;
+}
+
+struct Tile {
+  int e, f0;        // expert, first feature
+  int r0, rows;     // first output row (of the expert; of dW[e]), output rows
+  int nt;           // MMA columns: the rows in whole 32s
+  int steps;        // stages of the contraction
+  int last;         // positions of the last one
+};
+
+__device__ __forceinline__ int up32(int n) { return (n + 31) & ~31; }
+
+// Tile `id`; e: the expert of an earlier one.
+__device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tables& t, int cap) {
+  while (id >= t.pre[e + 1]) ++e;
+  Tile q;
+  q.e = e;
+  const int n = g.what == 2 ? g.N : t.cnt[e];
+  const int rt = (n + cap - 1) / cap, ft = (g.F + 255) / 256;
+  const int l = id - t.pre[e], sb = l / (kSuper * rt), m = l - sb * kSuper * rt, w = min(kSuper, ft - sb * kSuper);
+  const int r = m / w;
+  q.f0 = (sb * kSuper + m - r * w) * 256;
+  const int wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
+  q.r0 = r * wide;
+  q.rows = min(wide, n - q.r0);
+  q.nt = up32(q.rows);
+  const int c = g.what == 2 ? t.cnt[e] : g.C;
+  q.steps = (c + 63) / 64;
+  q.last = c - (q.steps - 1) * 64;
+  return q;
+}
+
+struct Abort {
+  volatile int* mine;
+  uint32_t other;
+  int* status;
+  long long limit;
+};
+// (All lanes together; acquire at cluster scope, as the other CTA arrives too.)
+__device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, const Abort& a) {
+  bool ok = false, timeout = true;
+  for (long long i = 0; i < a.limit; ++i) {
+    if (mbar_try_wait_cluster(bar, parity)) {
+      ok = true;
+      timeout = false;
+      break;
+    }
+    if ((i & 1023) == 1023 && *a.mine) {
+      timeout = false;
+      break;
+    }
+  }
+  if (timeout) {
+    *a.mine = 1;
+    cluster_st(a.other, 1);
+    if (a.status) atomicExch(a.status, (int)DETFFN_ERR_TIMEOUT);
+  }
+  return __all_sync(0xffffffffu, ok) != 0;
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_grouped_tc(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const __grid_constant__ Args g) {
+  extern __shared__ unsigned char raw[];
+  // (The same offset in both CTAs: dynamic shared memory starts at the same address in each.)
+  unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
+  Bars* bars = reinterpret_cast<Bars*>(smem + kStages * kStage);
+  const Tables t = tables_at(reinterpret_cast<unsigned char*>(bars) + ((sizeof(Bars) + 127) & ~127), g.E);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
+  const Abort ab{&bars->abort, cluster_addr(&bars->abort, rank ^ 1u), g.status, g.spin > 0 ? g.spin : kDefaultSpin};
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&bars->full[s], 2);
+      mbar_init(&bars->empty[s], 1);
+      mbar_init(&bars->tail[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&bars->accf[b], 1);
+      mbar_init(&bars->acce[b], 8);   // four warps of each CTA
+    }
+    mbar_init(&bars->fin, 1);
+    bars->abort = 0;
+    fence_mbar_init();
+    prefetch_tmap(&mA);
+    prefetch_tmap(&mB);
+  }
+  if (warp == 1) pair_tmem_alloc(&bars->tmem, 2 * kCols);
+  tc_fence_before();
+  cluster_sync_all();   // (the other CTA's shared memory is written from here on)
+  tc_fence_after();
+  grid_dep_wait();
+  grid_dep_launch();
+  if (warp == 3) {
+    // Each lane takes a run of experts.  (Rows out of the tensors, or before the
+    // expert's first, are none of its.)
+    const int per = (g.E + 31) / 32, e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
+    const int ft = (g.F + 255) / 256;
+    for (int e = e0; e < e1; ++e) {
+      const long long b = min(max((long long)__ldg(g.off + e), 0ll), g.R);
+      const long long n = max(min((long long)__ldg(g.off + e + 1), g.R) - b, 0ll);
+      t.beg[e] = (int)b;
+      t.cnt[e] = (int)n;
+    }
+    __syncwarp();
+    // The widest tile.
+    int cap = 256;
+    if (g.what != 2) {
+      int best = 0x7FFFFFFF;
+      for (int c = 256; c >= 32; c -= 32) {
+        int n = 0;
+        for (int e = e0; e < e1; ++e) n += (t.cnt[e] + c - 1) / c;
+        n = __reduce_add_sync(0xffffffffu, n);
+        const int cost = (int)min((long long)((n * (long long)ft + pairs - 1) / pairs) * (c + 32), 0x7FFFFFFELL);
+        if (cost < best) {
+          best = cost;
+          cap = c;
+        }
+      }
+    }
+    int n = 0;
+    for (int e = e0; e < e1; ++e) n += ((g.what == 2 ? g.N : t.cnt[e]) + cap - 1) / cap * ft;
+    int s = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += v;
+    }
+    int at = s - n;
+    for (int e = e0; e < e1; ++e) {
+      t.pre[e] = at;
+      at += ((g.what == 2 ? g.N : t.cnt[e]) + cap - 1) / cap * ft;
+    }
+    if (lane == 31) {
+      t.pre[g.E] = s;
+      bars->total = s;
+      bars->cap = cap;
+    }
+    // A timeout recorded earlier stops this launch: one reading for both CTAs.
+    if (lane == 0 && rank == 0 && g.status && *(volatile int*)g.status) {
+      bars->abort = 1;
+      cluster_st(ab.other, 1);
+    }
+  }
+  cluster_sync_all();
+  const uint32_t tmem = bars->tmem;
+  const int cap = bars->cap, total = *ab.mine ? 0 : bars->total;
+
+  if (warp == 0) {
+    // ---------------- loads ----------------
+    Ring rs;
+    int e = 0;
+    bool ok = true;
+    const uint32_t r0 = rank;
+    for (int id = pair; id < total && ok; id += pairs) {
+      const Tile q = tile_at(id, e, g, t, cap);
+      const int half = q.nt / 2, beg = t.beg[q.e];
+      const int fa = q.f0 + (int)r0 * 128;
+      const int nb = g.what == 2 ? (half + 63) / 64 : (half + 31) / 32;
+      const uint32_t bytes = kHalf + (uint32_t)nb * (g.what == 2 ? 8192u : 4096u);
+      for (int ks = 0; ks < q.steps; ++ks, rs.next(kStages)) {
+        ok = wait_pair(&bars->empty[rs.slot], rs.phase ^ 1u, ab);
+        if (!ok) break;
+        if (g.stall) continue;
+        if (lane == 0) {
+          const bool clear = g.what == 2 && ks == q.steps - 1 && (q.last & 15) != 0;
+          unsigned char* a = smem + rs.slot * kStage;
+          unsigned char* b = a + kHalf;
+          const uint32_t bar = clear ? cluster_addr(&bars->tail[rs.slot], rank) : cluster_addr(&bars->full[rs.slot], 0);
+          cluster_arrive_expect_tx(bar, bytes);
+          if (g.what == 0) {
+            pair_load_3d(a, &mA, ks * 64, fa, q.e, bar);
+          } else if (g.what == 1) {
+            pair_load_3d(a, &mA, fa, ks * 64, q.e, bar);
+            pair_load_3d(a + 8192, &mA, fa + 64, ks * 64, q.e, bar);
+          } else {
+            pair_load_2d(a, &mA, fa, beg + ks * 64, bar);
+            pair_load_2d(a + 8192, &mA, fa + 64, beg + ks * 64, bar);
+          }
+          if (g.what == 2) {
+            for (int i = 0; i < nb; ++i) pair_load_2d(b + i * 8192, &mB, q.r0 + (int)r0 * half + i * 64, beg + ks * 64, bar);
+          } else {
+            for (int i = 0; i < nb; ++i) pair_load_2d(b + i * 4096, &mB, ks * 64, beg + q.r0 + (int)r0 * half + i * 32, bar);
+          }
+        }
+        __syncwarp();
+      }
+    }
+  } else if (warp == 1 && rank == 0) {
+    // ---------------- MMA issue, for both CTAs ----------------
+    Ring rs, rb;
+    int e = 0;
+    bool ok = true;
+    const uint32_t base = (1u << 4) | (DT == DETFFN_BF16 ? (1u << 7) | (1u << 10) : 0u) | (16u << 24) |
+                          (g.what != 0 ? kIdescTransA : 0u) | (g.what == 2 ? kIdescTransB : 0u);
+    const uint32_t astep = g.what != 0 ? 128u : 2u, bstep = g.what == 2 ? 128u : 2u;
+    for (int id = pair; id < total && ok; id += pairs) {
+      const Tile q = tile_at(id, e, g, t, cap);
+      if (q.steps == 0) continue;
+      ok = wait_pair(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t idesc = base | (uint32_t)(q.nt >> 3) << 17, acc = tmem + (uint32_t)(rb.slot * kCols);
+      for (int ks = 0; ks < q.steps; ++ks, rs.next(kStages)) {
+        ok = wait_pair(&bars->full[rs.slot], rs.phase, ab);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          unsigned char* a = smem + rs.slot * kStage;
+          const uint64_t da = g.what != 0 ? smem_desc_sw128_mn(a) : smem_desc_sw128(a);
+          const uint64_t db = g.what == 2 ? smem_desc_sw128_mn(a + kHalf) : smem_desc_sw128(a + kHalf);
+          const int n = ks == q.steps - 1 ? (q.last + 15) / 16 : 4;
+          for (int kk = 0; kk < n; ++kk)
+            pair_mma_f16(acc, da + (uint64_t)(astep * kk), db + (uint64_t)(bstep * kk), idesc, ks > 0 || kk > 0 ? 1u : 0u);
+          pair_commit(&bars->empty[rs.slot]);
+          if (ks == q.steps - 1) pair_commit(&bars->accf[rb.slot]);
+        }
+        __syncwarp();
+      }
+      rb.next(2);
+    }
+    if (!ok) {   // stopped: the MMAs under way end before the shared memory is given up
+      if (elect_one()) pair_commit(&bars->fin);
+      __syncwarp();
+      mbar_wait(&bars->fin, 0, kDefaultSpin, nullptr);
+    }
+  } else if (warp == 2 && g.what == 2) {
+    // ---------------- rows beyond an expert's last, cleared ----------------
+    Ring rs;
+    int e = 0;
+    uint32_t used = 0;   // parity of each stage's tail barrier
+    for (int id = pair; id < total; id += pairs) {
+      const Tile q = tile_at(id, e, g, t, cap);
+      if (q.steps == 0 || (q.last & 15) == 0) {
+        rs.adv(q.steps, kStages);
+        continue;
+      }
+      rs.adv(q.steps - 1, kStages);
+      if (!wait_pair(&bars->tail[rs.slot], used >> rs.slot & 1u, ab)) break;
+      used ^= 1u << rs.slot;
+      const int from = q.last * 128, to = (q.last + 15) / 16 * 2048, boxes = 2 + (q.nt / 2 + 63) / 64;
+      unsigned char* a = smem + rs.slot * kStage;
+      for (int i = 0; i < boxes; ++i)
+        for (int o = from + lane * 16; o < to; o += 512)
+          *reinterpret_cast<uint4*>(a + i * 8192 + o) = make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) cluster_arrive(cluster_addr(&bars->full[rs.slot], 0));
+      __syncwarp();
+      rs.next(kStages);
+    }
+  } else if (warp >= 4) {
+    // ---------------- outputs ----------------
+    const int quarter = warp & 3;
+    Ring rb;
+    int e = 0;
+    for (int id = pair; id < total; id += pairs) {
+      const Tile q = tile_at(id, e, g, t, cap);
+      const int f = q.f0 + (int)rank * 128 + quarter * 32 + lane;
+      uint16_t* out = g.out + (g.what == 2 ? q.e * g.stride + q.r0 * g.ldo : (t.beg[q.e] + (long long)q.r0) * g.ldo) + f;
+      const bool in = f < g.F;
+      if (q.steps == 0) {   // an empty sum
+        for (int i = 0; i < q.rows; ++i, out += g.ldo)
+          if (in) *out = 0;
+        continue;
+      }
+      if (!wait_pair(&bars->accf[rb.slot], rb.phase, ab)) break;
+      tc_fence_after();
+      const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * kCols);
+      for (int c0 = 0; c0 < q.rows; c0 += 32) {
+        uint32_t v[32];
+        tmem_ld32(taddr + (uint32_t)c0, v);
+        tmem_wait_ld();
+        const int n = in ? q.rows - c0 : 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i, out += g.ldo)
+          if (i < n) Io<DT>::st(out, __uint_as_float(v[i]));
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) cluster_arrive(cluster_addr(&bars->acce[rb.slot], 0));
+      __syncwarp();
+      rb.next(2);
+    }
+  }
+  __syncwarp();
+  // Stopped by a timeout: what copies are under way land (they take microseconds).
+  if (*ab.mine && total > 0 && !g.stall)
+    for (int i = 0; i < 200; ++i) __nanosleep(10000);
+  tc_fence_before();
+  cluster_sync_all();   // (neither CTA's barriers or shared memory are used by the other from here on)
+  tc_fence_after();
+  if (warp == 1) pair_tmem_dealloc(tmem, 2 * kCols);
+}
+
+int smem_bytes(int E) { return 1024 + kStages * kStage + (int)((sizeof(Bars) + 127) & ~127) + tables_bytes(E); }
+
+bool boundary(const Rows& r, long long R) { return (uintptr_t)r.p % 16 == 0 && (R <= 1 || r.ld % 8 == 0); }
+
+template <int DT>
+cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_count, cudaStream_t st) {
+  static PerDevice ready;
+  const cudaError_t e = once_per_device(ready, [] {
+    return cudaFuncSetAttribute(k_grouped_tc<DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(kGroupedMaxExperts));
+  });
+  if (e != cudaSuccess) return e;
+  const bool f16 = DT == DETFFN_F16;
+  // (The stride of a single row is never used; the tensor map wants a multiple of 16 bytes.)
+  const long long ldx = a.R > 1 ? a.x.ld : (a.K + 7) / 8 * 8, ldd = a.R > 1 ? a.dout.ld : (a.N + 7) / 8 * 8;
+  const long long dw[3] = {a.K, a.N, a.E};
+  CUtensorMap mA, mB;
+  Args g{};
+  bool ok;
+  long long rt;
+  if (what == Grouped::kForward) {
+    const int box[3] = {64, 128, 1};
+    ok = tc_make_map_nd(&mA, f16, a.W, 3, dw, box) && tc_make_map_rows(&mB, f16, a.x.p, a.R, a.K, ldx, 64, 32);
+    g.what = 0, g.F = (int)a.N, g.C = (int)a.K, g.out = static_cast<uint16_t*>(const_cast<void*>(a.out.p)), g.ldo = a.out.ld;
+    rt = a.R / 32 + a.E;
+  } else if (what == Grouped::kInput) {
+    const int box[3] = {64, 64, 1};
+    ok = tc_make_map_nd(&mA, f16, a.W, 3, dw, box) && tc_make_map_rows(&mB, f16, a.dout.p, a.R, a.N, ldd, 64, 32);
+    g.what = 1, g.F = (int)a.K, g.C = (int)a.N, g.out = static_cast<uint16_t*>(const_cast<void*>(a.dx.p)), g.ldo = a.dx.ld;
+    rt = a.R / 32 + a.E;
+  } else {
+    ok = tc_make_map_rows(&mA, f16, a.x.p, a.R, a.K, ldx, 64, 64) && tc_make_map_rows(&mB, f16, a.dout.p, a.R, a.N, ldd, 64, 64);
+    g.what = 2, g.F = (int)a.K, g.N = (int)a.N, g.out = static_cast<uint16_t*>(a.dW), g.ldo = a.K, g.stride = a.N * a.K;
+    rt = (a.N + 255) / 256 * a.E;
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  g.E = a.E;
+  g.R = a.R;
+  g.off = a.off;
+  g.status = wt.status;
+  g.spin = wt.spin;
+  g.stall = wt.stall;
+  const long long most = rt * ((g.F + 255) / 256);
+  const int pairs = (int)(most < sm_count / 2 ? most : sm_count / 2);
+  return launch_cluster(k_grouped_tc<DT>, dim3(2 * pairs), kThreads, smem_bytes(a.E), 2, st, mA, mB, g);
+}
+
+}  // namespace
+
+bool grouped_tensor_covers(const GroupedArgs& a, Grouped what) {
+  if (a.dtype == DETFFN_F32 || a.K % 8 != 0 || a.N % 8 != 0) return false;
+  if (what != Grouped::kInput && !boundary(a.x, a.R)) return false;
+  if (what != Grouped::kForward && !boundary(a.dout, a.R)) return false;
+  return what == Grouped::kWeight || (uintptr_t)a.W % 16 == 0;
+}
+
+cudaError_t launch_grouped_tensor(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_count, cudaStream_t st) {
+  return a.dtype == DETFFN_F16 ? run<DETFFN_F16>(a, what, wt, sm_count, st) : run<DETFFN_BF16>(a, what, wt, sm_count, st);
+}
+
+}  // namespace detffn

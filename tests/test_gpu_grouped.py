@@ -235,3 +235,23 @@ def test_refusals(G):
     with pytest.raises(G.DetFFNError) as e:
         G.detffn_grouped_forward(x.float(), W.float(), off, path=TENSOR)
     assert e.value.status == 4
+
+
+@pytest.mark.parametrize("what", ["forward", "dX", "dW"])
+def test_a_wait_that_runs_out_is_reported(G, what):
+    """No copies are issued: the first wait ends at its limit, the status says so,
+    calls until it is read leave their outputs unwritten, and later ones are whole."""
+    x, W, d, off, _ = make([100, 60], 256, 264, torch.bfloat16)
+    out = torch.zeros((160, 264), dtype=x.dtype, device="cuda")
+    kw = dict(path=TENSOR, spin_limit=2000, flags=G.FLAG_TEST_STALL)
+    if what == "forward":
+        G.detffn_grouped_forward(x, W, off, out=out, **kw)
+    else:
+        G.detffn_grouped_backward(x, W, off, d, need_dX=what == "dX", need_dW=what == "dW", **kw)
+    torch.cuda.synchronize()
+    G.detffn_grouped_forward(x, W, off, out=out, path=TENSOR)
+    assert not bool(out.any())
+    assert G.detffn_get_status() == 7 and G.detffn_get_status() == 0
+    got = G.detffn_grouped_forward(x, W, off, out=out, path=TENSOR)
+    want = torch.cat([x[:100].double() @ W[0].double().T, x[100:].double() @ W[1].double().T])
+    assert float((got.double() - want).norm() / want.norm()) < 2.0 ** -8
