@@ -119,11 +119,13 @@ struct Abort {
   int* status;
   long long limit;
 };
-// (All lanes together; acquire at cluster scope, as the other CTA arrives too.)
+// (All lanes together.  REMOTE: what the other CTA's threads wrote before they
+// arrived is seen after it.)
+template <bool REMOTE = false>
 __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, const Abort& a) {
   bool ok = false, timeout = true;
   for (long long i = 0; i < a.limit; ++i) {
-    if (mbar_try_wait_cluster(bar, parity)) {
+    if (REMOTE ? mbar_try_wait_cluster(bar, parity) : mbar_try_wait(bar, parity)) {
       ok = true;
       timeout = false;
       break;
@@ -143,7 +145,9 @@ __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, const 
 
 template <int DT>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_grouped_tc(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB, const __grid_constant__ Args g) {
+    k_grouped_tc(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
+                 const __grid_constant__ CUtensorMap mB64, const __grid_constant__ CUtensorMap mB32,
+                 const __grid_constant__ Args g) {
   extern __shared__ unsigned char raw[];
   // (The same offset in both CTAs: dynamic shared memory starts at the same address in each.)
   unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
@@ -241,8 +245,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile q = tile_at(id, e, g, t, cap);
       const int half = q.nt / 2, beg = t.beg[q.e];
       const int fa = q.f0 + (int)r0 * 128;
-      const int nb = g.what == 2 ? (half + 63) / 64 : (half + 31) / 32;
-      const uint32_t bytes = kHalf + (uint32_t)nb * (g.what == 2 ? 8192u : 4096u);
+      const int nb = up32(half);   // rows of B, by boxes of 128, or of 64 and 32 (dW: features by boxes of 64)
+      const uint32_t bytes = kHalf + (g.what == 2 ? (uint32_t)(half + 63) / 64 * 8192u : (uint32_t)nb * 128u);
       for (int ks = 0; ks < q.steps; ++ks, rs.next(kStages)) {
         ok = wait_pair(&bars->empty[rs.slot], rs.phase ^ 1u, ab);
         if (!ok) break;
@@ -263,9 +267,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             pair_load_2d(a + 8192, &mA, fa + 64, beg + ks * 64, bar);
           }
           if (g.what == 2) {
-            for (int i = 0; i < nb; ++i) pair_load_2d(b + i * 8192, &mB, q.r0 + (int)r0 * half + i * 64, beg + ks * 64, bar);
+            pair_load_2d(b, &mB, q.r0 + (int)r0 * half, beg + ks * 64, bar);
+            if (half > 64) pair_load_2d(b + 8192, &mB, q.r0 + (int)r0 * half + 64, beg + ks * 64, bar);
           } else {
-            for (int i = 0; i < nb; ++i) pair_load_2d(b + i * 4096, &mB, ks * 64, beg + q.r0 + (int)r0 * half + i * 32, bar);
+            const int y = beg + q.r0 + (int)r0 * half;
+            if (nb == 128) {
+              pair_load_2d(b, &mB, ks * 64, y, bar);
+            } else {
+              if (nb >= 64) pair_load_2d(b, &mB64, ks * 64, y, bar);
+              if (nb & 32) pair_load_2d(b + (nb & 64) * 128, &mB32, ks * 64, y + (nb & 64), bar);
+            }
           }
         }
         __syncwarp();
@@ -282,12 +293,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int id = pair; id < total && ok; id += pairs) {
       const Tile q = tile_at(id, e, g, t, cap);
       if (q.steps == 0) continue;
-      ok = wait_pair(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
+      ok = wait_pair<true>(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
       if (!ok) break;
       tc_fence_after();
       const uint32_t idesc = base | (uint32_t)(q.nt >> 3) << 17, acc = tmem + (uint32_t)(rb.slot * kCols);
       for (int ks = 0; ks < q.steps; ++ks, rs.next(kStages)) {
-        ok = wait_pair(&bars->full[rs.slot], rs.phase, ab);
+        ok = g.what == 2 && ks == q.steps - 1 ? wait_pair<true>(&bars->full[rs.slot], rs.phase, ab)
+                                              : wait_pair(&bars->full[rs.slot], rs.phase, ab);
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
@@ -393,22 +405,27 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
   // (The stride of a single row is never used; the tensor map wants a multiple of 16 bytes.)
   const long long ldx = a.R > 1 ? a.x.ld : (a.K + 7) / 8 * 8, ldd = a.R > 1 ? a.dout.ld : (a.N + 7) / 8 * 8;
   const long long dw[3] = {a.K, a.N, a.E};
-  CUtensorMap mA, mB;
+  CUtensorMap mA, mB, mB64, mB32;
   Args g{};
   bool ok;
   long long rt;
+  auto rows_maps = [&](const void* p, long long width, long long ld) {
+    return tc_make_map_rows(&mB, f16, p, a.R, width, ld, 64, 128) && tc_make_map_rows(&mB64, f16, p, a.R, width, ld, 64, 64) &&
+           tc_make_map_rows(&mB32, f16, p, a.R, width, ld, 64, 32);
+  };
   if (what == Grouped::kForward) {
     const int box[3] = {64, 128, 1};
-    ok = tc_make_map_nd(&mA, f16, a.W, 3, dw, box) && tc_make_map_rows(&mB, f16, a.x.p, a.R, a.K, ldx, 64, 32);
+    ok = tc_make_map_nd(&mA, f16, a.W, 3, dw, box) && rows_maps(a.x.p, a.K, ldx);
     g.what = 0, g.F = (int)a.N, g.C = (int)a.K, g.out = static_cast<uint16_t*>(const_cast<void*>(a.out.p)), g.ldo = a.out.ld;
     rt = a.R / 32 + a.E;
   } else if (what == Grouped::kInput) {
     const int box[3] = {64, 64, 1};
-    ok = tc_make_map_nd(&mA, f16, a.W, 3, dw, box) && tc_make_map_rows(&mB, f16, a.dout.p, a.R, a.N, ldd, 64, 32);
+    ok = tc_make_map_nd(&mA, f16, a.W, 3, dw, box) && rows_maps(a.dout.p, a.N, ldd);
     g.what = 1, g.F = (int)a.K, g.C = (int)a.N, g.out = static_cast<uint16_t*>(const_cast<void*>(a.dx.p)), g.ldo = a.dx.ld;
     rt = a.R / 32 + a.E;
   } else {
     ok = tc_make_map_rows(&mA, f16, a.x.p, a.R, a.K, ldx, 64, 64) && tc_make_map_rows(&mB, f16, a.dout.p, a.R, a.N, ldd, 64, 64);
+    mB64 = mB32 = mB;
     g.what = 2, g.F = (int)a.K, g.N = (int)a.N, g.out = static_cast<uint16_t*>(a.dW), g.ldo = a.K, g.stride = a.N * a.K;
     rt = (a.N + 255) / 256 * a.E;
   }
@@ -421,7 +438,7 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
   g.stall = wt.stall;
   const long long most = rt * ((g.F + 255) / 256);
   const int pairs = (int)(most < sm_count / 2 ? most : sm_count / 2);
-  return launch_cluster(k_grouped_tc<DT>, dim3(2 * pairs), kThreads, smem_bytes(a.E), 2, st, mA, mB, g);
+  return launch_cluster(k_grouped_tc<DT>, dim3(2 * pairs), kThreads, smem_bytes(a.E), 2, st, mA, mB, mB64, mB32, g);
 }
 
 }  // namespace
