@@ -24,6 +24,6 @@ from .block import (  # noqa: F401
 )
 from .products import (  # noqa: F401
     W4, detffn_dropout_backward, detffn_dropout_forward, detffn_grouped_backward, detffn_grouped_forward,
-    detffn_grouped_workspace_size, detffn_w4_forward, detffn_w4_matvec, detffn_w4_pack, detffn_w4_unpack,
+    detffn_grouped_workspace_size, detffn_w4_forward, detffn_w4_matvec, detffn_w4_matvec_workspace_size, detffn_w4_pack, detffn_w4_unpack,
     detffn_w4_workspace_size,
 )

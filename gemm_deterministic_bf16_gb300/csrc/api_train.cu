@@ -82,9 +82,24 @@ detffn_status w4_sizes(long long N, long long K, int group, int dtype, int stype
   if (N < 1 || N > kW4MaxWidth || K < 1 || K > kW4MaxWidth) return DETFFN_ERR_SHAPE;
   return DETFFN_OK;
 }
-detffn_status w4_pointers(const void* codes, const void* scales, int stype) {
+detffn_status w4_pointers(const void* codes, const void* scales) {
   if (!codes || !scales) return DETFFN_ERR_INVALID_ARG;
-  return on(codes, 16) && on(scales, bytes_of(stype)) ? DETFFN_OK : DETFFN_ERR_ALIGN;
+  return on(codes, 16) && on(scales, 4) ? DETFFN_OK : DETFFN_ERR_ALIGN;
+}
+// Rows as the kernels read them: where they are, or laid out at `to` by a launch of their own.
+detffn_status w4_rows(const void* x, long long ldx, long long T, long long K, int dtype, void* to, int sms, cudaStream_t st,
+                      W4Rows* r) {
+  r->f16 = dtype == DETFFN_F16;
+  if (dtype != DETFFN_F32 && w4_in_place(x, ldx, T, K)) {
+    r->p = x;
+    r->ld = T > 1 ? ldx : K;
+    return DETFFN_OK;
+  }
+  r->p = to;
+  r->ld = w4_pad(K);
+  r->plane = T * r->ld;
+  r->terms = dtype == DETFFN_F32 ? 3 : 1;
+  return cu(launch_w4_rows(x, ldx, dtype, T, K, r->terms, to, sms, st));
 }
 W4Matrix w4_matrix(const void* codes, const void* scales, long long N, long long K, int group, int stype) {
   W4Matrix m;
@@ -190,7 +205,7 @@ detffn_status detffn_grouped_backward(detffn_handle h, const void* x, long long 
 detffn_status detffn_w4_pack(const void* w, long long ldw, void* codes, void* scales, long long N, long long K, int group,
                              int dtype, int scale_dtype, void* stream) {
   TRY(w4_sizes(N, K, group, dtype, scale_dtype));
-  TRY(w4_pointers(codes, scales, scale_dtype));
+  TRY(w4_pointers(codes, scales));
   const long long es = bytes_of(dtype);
   TRY(matrix(w, ldw, N, K, es));
   const Span in[] = {rows_span(w, N, K, ldw, es)};
@@ -205,7 +220,7 @@ detffn_status detffn_w4_pack(const void* w, long long ldw, void* codes, void* sc
 detffn_status detffn_w4_unpack(const void* codes, const void* scales, void* w, long long ldw, long long N, long long K,
                                int group, int dtype, int scale_dtype, void* stream) {
   TRY(w4_sizes(N, K, group, dtype, scale_dtype));
-  TRY(w4_pointers(codes, scales, scale_dtype));
+  TRY(w4_pointers(codes, scales));
   const long long es = bytes_of(dtype);
   TRY(matrix(w, ldw, N, K, es));
   const Span in[] = {flat_span(codes, w4_code_bytes(N, K)), flat_span(scales, w4_scale_bytes(N, K, group, scale_dtype))};
@@ -217,39 +232,49 @@ detffn_status detffn_w4_unpack(const void* codes, const void* scales, void* w, l
   return cu(launch_w4_unpack(w4_matrix(codes, scales, N, K, group, scale_dtype), w, ldw, dtype, sms, (cudaStream_t)stream));
 }
 
+detffn_status detffn_w4_matvec_workspace_size(long long T, long long K, int dtype, size_t* bytes) {
+  if (!bytes || !good_type(dtype)) return DETFFN_ERR_INVALID_ARG;
+  if (T < 0 || T > kW4MaxTokens || K < 1 || K > kW4MaxWidth) return DETFFN_ERR_SHAPE;
+  *bytes = (size_t)((dtype == DETFFN_F32 ? 3 : 1) * T * w4_pad(K) * 2 + 255) & ~(size_t)255;
+  return DETFFN_OK;
+}
+
 detffn_status detffn_w4_matvec(const void* x, long long ldx, const void* codes, const void* scales, void* out,
                                long long ldo, long long T, long long N, long long K, int group, int dtype,
-                               int scale_dtype, void* stream) {
+                               int scale_dtype, void* ws, size_t ws_bytes, void* stream) {
   TRY(w4_sizes(N, K, group, dtype, scale_dtype));
-  if (T < 0 || T > kW4MaxTokens) return DETFFN_ERR_SHAPE;
+  size_t need = 0;
+  TRY(detffn_w4_matvec_workspace_size(T, K, dtype, &need));
   if (T == 0) return DETFFN_OK;
-  TRY(w4_pointers(codes, scales, scale_dtype));
+  TRY(w4_pointers(codes, scales));
   const long long es = bytes_of(dtype);
   TRY(matrix(x, ldx, T, K, es));
   TRY(matrix(out, ldo, T, N, es));
+  if (dtype != DETFFN_F32 && w4_in_place(x, ldx, T, K)) need = 0;
+  if (need && (!ws || !on(ws, 256) || ws_bytes < need)) return DETFFN_ERR_WORKSPACE;
   const Span in[] = {rows_span(x, T, K, ldx, es), flat_span(codes, w4_code_bytes(N, K)),
                      flat_span(scales, w4_scale_bytes(N, K, group, scale_dtype))};
-  const Span outs[] = {rows_span(out, T, N, ldo, es)};
-  const int alias[] = {-1};
-  TRY(check_overlap(in, 3, outs, 1, alias));
+  const Span outs[] = {rows_span(out, T, N, ldo, es), flat_span(ws, (long long)need)};
+  const int alias[] = {-1, -1};
+  TRY(check_overlap(in, 3, outs, 2, alias));
+  int sms = 0;
+  TRY(current_sms(&sms));
   W4Args a;
   a.w = w4_matrix(codes, scales, N, K, group, scale_dtype);
-  a.x = x;
-  a.ldx = ldx;
+  TRY(w4_rows(x, ldx, T, K, dtype, ws, sms, (cudaStream_t)stream, &a.x));
   a.out = out;
   a.ldo = ldo;
   a.T = (int)T;
-  a.xtype = a.otype = dtype;
-  a.terms = 3;
-  int sms = 0;
-  TRY(current_sms(&sms));
+  a.otype = dtype;
   return cu(launch_w4_matvec(a, sms, (cudaStream_t)stream));
 }
 
-detffn_status detffn_w4_workspace_size(long long T, long long H, long long I, size_t* bytes) {
+detffn_status detffn_w4_workspace_size(long long T, long long H, long long I, int dtype, size_t* bytes) {
+  size_t x = 0, h = 0;
+  TRY(detffn_w4_matvec_workspace_size(T, H, dtype, &x));
   if (!bytes) return DETFFN_ERR_INVALID_ARG;
-  if (T < 0 || T > kW4MaxTokens || H < 1 || H > kW4MaxWidth || I < 1 || I > kW4MaxWidth) return DETFFN_ERR_SHAPE;
-  *bytes = (size_t)(T * I * 4 + 255) & ~(size_t)255;
+  TRY(detffn_w4_matvec_workspace_size(T, I, DETFFN_F32, &h));
+  *bytes = x + h;
   return DETFFN_OK;
 }
 
@@ -258,12 +283,13 @@ detffn_status detffn_w4_forward(const void* x, long long ldx, const void* gate_c
                                 const void* down_scales, void* out, long long ldo, long long T, long long H, long long I,
                                 int group, int dtype, int scale_dtype, void* ws, size_t ws_bytes, void* stream) {
   TRY(w4_sizes(I, H, group, dtype, scale_dtype));
-  size_t need = 0;
-  TRY(detffn_w4_workspace_size(T, H, I, &need));
+  size_t need = 0, hbytes = 0;
+  TRY(detffn_w4_workspace_size(T, H, I, dtype, &need));
+  TRY(detffn_w4_matvec_workspace_size(T, I, DETFFN_F32, &hbytes));
   if (T == 0) return DETFFN_OK;
-  TRY(w4_pointers(gate_codes, gate_scales, scale_dtype));
-  TRY(w4_pointers(up_codes, up_scales, scale_dtype));
-  TRY(w4_pointers(down_codes, down_scales, scale_dtype));
+  TRY(w4_pointers(gate_codes, gate_scales));
+  TRY(w4_pointers(up_codes, up_scales));
+  TRY(w4_pointers(down_codes, down_scales));
   const long long es = bytes_of(dtype);
   TRY(matrix(x, ldx, T, H, es));
   TRY(matrix(out, ldo, T, H, es));
@@ -274,33 +300,33 @@ detffn_status detffn_w4_forward(const void* x, long long ldx, const void* gate_c
                      flat_span(up_codes, c1),     flat_span(up_scales, s1),  flat_span(down_codes, c2),
                      flat_span(down_scales, s2)};
   const Span outs[] = {rows_span(out, T, H, ldo, es), flat_span(ws, (long long)need)};
-  const int alias[] = {0, -1};   // (x is read by the first launch alone)
+  const int alias[] = {0, -1};   // (x is read before the last launch)
   TRY(check_overlap(in, 7, outs, 2, alias));
+  int sms = 0;
+  TRY(current_sms(&sms));
+  cudaStream_t st = (cudaStream_t)stream;
   W4Args a;
   a.w = w4_matrix(gate_codes, gate_scales, I, H, group, scale_dtype);
   a.w2 = w4_matrix(up_codes, up_scales, I, H, group, scale_dtype);
-  a.x = x;
-  a.ldx = ldx;
-  a.out = ws;
-  a.ldo = I;
+  TRY(w4_rows(x, ldx, T, H, dtype, static_cast<char*>(ws) + hbytes, sms, st, &a.x));
   a.T = (int)T;
-  a.xtype = dtype;
-  a.otype = DETFFN_F32;
-  a.terms = 3;
-  int sms = 0;
-  TRY(current_sms(&sms));
-  TRYCU(launch_w4_matvec(a, sms, (cudaStream_t)stream));
+  // The hidden activation: terms planes of [T][I padded].
+  a.out = ws;
+  a.ldo = w4_pad(I);
+  a.plane = T * w4_pad(I);
+  a.terms = dtype == DETFFN_F32 ? 3 : 2;
+  TRYCU(launch_w4_matvec(a, sms, st));
   W4Args d;
   d.w = w4_matrix(down_codes, down_scales, H, I, group, scale_dtype);
-  d.x = ws;
-  d.ldx = I;
+  d.x.p = ws;
+  d.x.ld = a.ldo;
+  d.x.plane = a.plane;
+  d.x.terms = a.terms;
+  d.T = (int)T;
   d.out = out;
   d.ldo = ldo;
-  d.T = (int)T;
-  d.xtype = DETFFN_F32;
   d.otype = dtype;
-  d.terms = dtype == DETFFN_F32 ? 3 : 2;
-  return cu(launch_w4_matvec(d, sms, (cudaStream_t)stream));
+  return cu(launch_w4_matvec(d, sms, st));
 }
 
 detffn_status detffn_dropout_forward(const void* x, long long ldx, const void* residual, long long ldr, void* out,

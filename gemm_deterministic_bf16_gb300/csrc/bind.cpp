@@ -594,10 +594,10 @@ PyObject* w4_unpack(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   END_BODY
 }
 
-// (x, codes, scales, K, group, out)
+// (x, codes, scales, K, group, out, ws)
 PyObject* w4_matvec(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
-  BODY(6)
-  const Tensor *x = tensor(a[0], "x"), *out = tensor(a[5], "out");
+  BODY(7)
+  const Tensor *x = tensor(a[0], "x"), *out = tensor(a[5], "out"), *ws = tensor(a[6], "ws");
   need(x != nullptr, "x must be given");
   const Bits4 m = bits4(a + 1);
   const long long ldx = ROWS(x, nullptr), T = x->size(0);
@@ -608,8 +608,17 @@ PyObject* w4_matvec(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   const long long ldo = ROWS(out, nullptr);
   need(out->size(0) == T && out->size(1) == m.N && out->scalar_type() == x->scalar_type() && out->get_device() == m.device,
        "out: expected [T, N] of x's dtype on its device");
+  const int dt = type_of(x->scalar_type());
+  Tensor t_ws;
+  if (!ws && (dt == DETFFN_F32 || (uintptr_t)x->data_ptr() % 16 || m.K % 8 || (T > 1 && ldx % 8))) {
+    size_t bytes = 0;
+    check(detffn_w4_matvec_workspace_size(T, m.K, dt, &bytes), "detffn_w4_matvec_workspace_size");
+    ws = &(t_ws = empty({(long long)(bytes < 256 ? 256 : bytes)}, *x, at::kByte));
+  }
+  need(!ws || (ws->is_cuda() && ws->get_device() == m.device && ws->is_contiguous()), "ws: expected a contiguous CUDA buffer");
   check(detffn_w4_matvec(x->data_ptr(), ldx, m.codes->data_ptr(), m.scales->data_ptr(), out->data_ptr(), ldo, T, m.N, m.K,
-                         (int)m.group, type_of(x->scalar_type()), m.type, stream_of(m.device)),
+                         (int)m.group, dt, m.type, const_cast<void*>(ptr(ws)), ws ? (size_t)ws->nbytes() : 0,
+                         stream_of(m.device)),
         "detffn_w4_matvec");
   return tuple({out});
   END_BODY
@@ -631,7 +640,7 @@ PyObject* w4_forward(PyObject*, PyObject* const* a, Py_ssize_t nargs) {
   if (!out) out = &(t = empty({T, H}, *x, x->scalar_type()));
   const long long ldo = ROWS(out, x);
   size_t bytes = 0;
-  check(detffn_w4_workspace_size(T, H, I, &bytes), "detffn_w4_workspace_size");
+  check(detffn_w4_workspace_size(T, H, I, type_of(x->scalar_type()), &bytes), "detffn_w4_workspace_size");
   if (!ws) ws = &(t_ws = empty({(long long)(bytes < 256 ? 256 : bytes)}, *x, at::kByte));
   need(ws->is_cuda() && ws->get_device() == g.device && ws->is_contiguous(), "ws: expected a contiguous CUDA buffer");
   check(detffn_w4_forward(x->data_ptr(), ldx, g.codes->data_ptr(), g.scales->data_ptr(), u.codes->data_ptr(),

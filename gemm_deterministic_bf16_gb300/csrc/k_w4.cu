@@ -13,10 +13,10 @@
 // are all products with a 16-bit x.  A group's sum is one accumulation in FP32,
 // scaled and added to the row's FP32 sum.
 //
-// An FP32 activation is three BF16 terms (each the leading eight bits of what
-// the ones before left, together all 24), in columns of their own.  The hidden
-// activation of the gated FFN goes from one launch to the next in FP32, and as
-// two terms (16 bits) where the result is a 16-bit type.
+// An FP32 activation is three BF16 terms (together all 24 bits), in columns of
+// their own; a small kernel lays them out first, and rows that are not on
+// 16-byte boundaries.  The hidden activation of the gated FFN goes from one
+// launch to the next as two terms (16 bits), three for FP32.
 //
 // The order of the codes makes this a matter of plain vectors: lane 4 r + t of
 // a warp holds row r (and r + 8) of the 16-row operand and columns 2 t, 2 t + 1,
@@ -24,6 +24,12 @@
 // of 128 codes (16 bytes) holds what lane t needs of it: word g the codes 32 g +
 // 8 t .. + 7 of group quarter g, nibble p of it code 2 (p mod 4) + p / 4, so
 // that a mask and a shift leave neighbours in the two halves of a register.
+//
+// Converting 2048 weights takes a warp some 90 instructions besides the loads,
+// which is most of what an SM can issue in the time their bytes take; so the
+// loop has little else.  Codes and scales come by cp.async, each lane's own
+// pieces some items ahead in a ring of shared memory that outlasts the row
+// tiles, x from L1 without tests.
 #include "elt.cuh"
 #include "w4.h"
 
@@ -58,13 +64,16 @@ __device__ __forceinline__ uint32_t pair(uint32_t word, int i) {
   return r;
 }
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "l"(p));
-  return v;
+__device__ __forceinline__ void copy16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
 }
+// The first n of four bytes, zeros behind.
+__device__ __forceinline__ void copy4(void* to, const void* from, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(n)
+               : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 __device__ __forceinline__ float ld_scale(const void* p, long long i, int type) {
   if (type == DETFFN_F32) return __ldg(static_cast<const float*>(p) + i);
@@ -72,198 +81,278 @@ __device__ __forceinline__ float ld_scale(const void* p, long long i, int type) 
   return type == DETFFN_F16 ? __half2float(__ushort_as_half(v)) : bf2f(v);
 }
 
-// Term `term` of eight FP32 values, as BF16 pairs.  An infinity or a NaN is the
-// first term's alone.
-__device__ __forceinline__ void terms_of(const float (&v)[8], int term, uint32_t (&b)[4]) {
-  uint32_t t[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t u = __float_as_uint(v[i]);
-    const bool finite = (u & 0x7F800000u) != 0x7F800000u;
-    const float first = __uint_as_float(u & 0xFFFF0000u), left = v[i] - first;
-    const float second = __uint_as_float(__float_as_uint(left) & 0xFFFF0000u);
-    // (A NaN whose set bits are cut off would be an infinity.)
-    if (term == 0) t[i] = v[i] != v[i] ? 0x7FC00000u : u & 0xFFFF0000u;
-    else t[i] = finite ? __float_as_uint(term == 1 ? second : left - second) & 0xFFFF0000u : 0u;
+// Terms of an FP32 value: the leading eight bits of what the ones before left,
+// the last one rounded.  An infinity or a NaN is the first term's alone.
+__device__ __forceinline__ void terms_of(float v, int n, uint16_t (&t)[3]) {
+  const uint32_t u = __float_as_uint(v);
+  t[1] = t[2] = 0;
+  if ((u & 0x7F800000u) == 0x7F800000u) {
+    t[0] = v != v ? 0x7FC0u : (uint16_t)(u >> 16);   // (a NaN's set bits may be the low ones)
+    return;
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) b[i] = t[2 * i] >> 16 | t[2 * i + 1];
+  t[0] = (uint16_t)(u >> 16);
+  const float left = v - bf2f(t[0]);
+  t[1] = n == 2 ? f2bf(left) : (uint16_t)(__float_as_uint(left) >> 16);
+  if (n == 3) t[2] = f2bf(left - bf2f(t[1]));
 }
 
-// XK: 0 BF16, 1 FP16, 2 FP32 (TERMS columns a token).  MT row tiles of 16 to a
-// warp (GATED: of gate and of up), NT column tiles of 8.  Eight warps share K.
-template <int XK, int TERMS, int MT, int NT, bool GATED, int GROUP>
-__global__ void __launch_bounds__(kWarps * 32) k_w4(const W4Args a) {
-  constexpr bool BF = XK != 1;
-  constexpr int ROWS = GATED ? 16 : 16 * MT;      // output features of a CTA
-  constexpr int COLS = 8 * NT, TOK = COLS / TERMS;
-  __shared__ float red[kWarps][16 * MT][COLS + 1];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane >> 2, t = lane & 3;
-  const long long n0 = (long long)blockIdx.x * ROWS;
-  const int t0 = blockIdx.y * TOK;
-  const int tokens = min(TOK, a.T - t0), cols = tokens * TERMS;
-  const long long K = a.w.K, N = a.w.N, runs = (K + kW4Run - 1) / kW4Run, pitch = runs * 64;
-  const long long groups = (K + GROUP - 1) / GROUP;
-  float sum[MT][NT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int c = 0; c < 4; ++c) sum[i][j][c] = 0.0f;
+// Items of a warp's ring: one is used while the others are on their way (of
+// four row tiles one, whose arithmetic takes as long as its bytes).
+template <int MT> constexpr int kRing = MT < 4 ? 4 : 2;
 
-  // Rows q and q + 8 of each row tile; past the last row the last again, not stored.
-  const uint8_t* codes[MT][2];
-  const void* scales[MT];
-  long long row[MT][2];
+// Shared memory of a warp's ring item: codes [row half][lane], then scales [row][4 words].
+template <int MT> struct Item {
+  uint4 code[2 * MT][32];
+  uint32_t scale[16 * MT][4];
+};
+template <int MT, int NT> struct Smem {
+  static constexpr int kRed = MT < 4 ? 2 : 1;
+  Item<MT> ring[kWarps][kRing<MT>];
+  float red[kRed][kWarps][16 * MT][8 * NT + 1];
+};
+
+// MT row tiles of 16 to a warp (GATED: half of gate, half of up), NT column
+// tiles of 8.  The eight warps share K, a run of 128 each in turn.
+template <bool BF, int MT, int NT, bool GATED, int GROUP>
+__global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ? 2 : 1) k_w4(const W4Args a) {
+  constexpr int ROWS = GATED ? 8 * MT : 16 * MT;  // output features of a tile
+  constexpr int PER = kW4Run / GROUP;             // groups of a run
+  extern __shared__ __align__(16) unsigned char raw[];
+  Smem<MT, NT>& sm = *reinterpret_cast<Smem<MT, NT>*>(raw);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, q = lane >> 2, t = lane & 3;
+  const int terms = a.x.terms, tok = 8 * NT / terms, t0 = blockIdx.y * tok, tokens = min(tok, a.T - t0), cols = tokens * terms;
+  const int N = (int)a.w.N, K = (int)a.w.K, runs = (K + kW4Run - 1) / kW4Run, groups = (K + GROUP - 1) / GROUP;
+  const int tiles = (N + ROWS - 1) / ROWS, Kx = (K + 7) & ~7;
+  const bool wide = a.w.stype == DETFFN_F32;
+  // Words of scales of a run that a lane copies: word t of its rows.
+  const int words = wide ? PER : PER / 2 + 1;
+  const long long scale_bytes = (long long)N * groups * (wide ? 4 : 2);
+
+  // Columns past the last read the last one's x; their sums are not used.
+  const uint16_t* x[NT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int j = 0; j < NT; ++j) {
+    const int col = min(8 * j + q, cols - 1);
+    x[j] = static_cast<const uint16_t*>(a.x.p) + (col % terms) * a.x.plane + (long long)(t0 + col / terms) * a.x.ld + 8 * t;
+  }
+
+  // The matrix, and the row of it, of row q + 8 h of row tile i; past the last row the last again, not stored.
+  auto matrix_of = [&](int i) -> const W4Matrix& { return GATED && i >= MT / 2 ? a.w2 : a.w; };
+  auto row_of = [&](int tile, int i, int h) {
+    return min(tile * ROWS + 16 * (GATED && i >= MT / 2 ? i - MT / 2 : i) + q + 8 * h, N - 1);
+  };
+  const uint8_t* code_at[MT][2];   // of the next copies
+  long long scale_at[MT][2];       // (index of a scale)
+  auto aim = [&](int tile, int run) {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const W4Matrix& w = GATED && i == 1 ? a.w2 : a.w;
-      row[i][h] = min(n0 + (GATED ? 0 : 16 * i) + q + 8 * h, N - 1);
-      codes[i][h] = w.codes + row[i][h] * pitch + 16 * t;
-      row[i][h] *= groups;
-      scales[i] = w.scales;
-    }
-  constexpr int U = MT * NT >= 4 ? 2 : 4;   // runs whose codes are loaded at once
-  grid_dep_wait();
-  grid_dep_launch();
-  for (long long b0 = warp; b0 < runs; b0 += U * kWarps) {
-    uint4 code[U][MT][2];
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int h = 0; h < 2; ++h) {
+        const long long r = row_of(tile, i, h);
+        code_at[i][h] = matrix_of(i).codes + (r * runs + run) * 64 + 16 * t;
+        scale_at[i][h] = r * groups + run * PER;
+      }
+  };
+  int ntile = blockIdx.x, nrun = warp, slot = 0;
+  if (warp >= runs) ntile = tiles;   // (no run for this warp)
+  auto copy_next = [&]() {
+    if (ntile < tiles) {
+      Item<MT>& it = sm.ring[warp][slot];
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          code[u][i][h] = b0 + u * kWarps < runs ? ld_stream(codes[i][h] + (b0 + u * kWarps) * 64) : make_uint4(0, 0, 0, 0);
+        for (int h = 0; h < 2; ++h) {
+          copy16(&it.code[2 * i + h][lane], code_at[i][h]);
+          if (t < words) {
+            const long long at = (wide ? scale_at[i][h] : scale_at[i][h] >> 1) * 4 + 4 * t;
+            const int n = (int)min(max(scale_bytes - at, 0ll), 4ll);
+            copy4(&it.scale[16 * i + 8 * h + q][t], static_cast<const char*>(matrix_of(i).scales) + (n > 0 ? at : 0), n);
+          }
+          code_at[i][h] += kWarps * 64;
+          scale_at[i][h] += kWarps * PER;
+        }
+      nrun += kWarps;
+      if (nrun >= runs) {
+        nrun = warp;
+        ntile += gridDim.x;
+        if (ntile < tiles) aim(ntile, nrun);
+      }
+    }
+    copies_commit();
+    slot = (slot + 1) % kRing<MT>;
+  };
+
+  if (ntile < tiles) {
+    aim(ntile, nrun);
+    // The first codes on their way to L2 (where nothing the launch before may write can go stale).
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const long long b = b0 + u * kWarps;
-      if (b >= runs) break;
-      float c[MT][NT][4];
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        if (g * 32 % GROUP == 0) {
+      for (int h = 0; h < 2; ++h) asm volatile("prefetch.global.L2 [%0];" ::"l"(code_at[i][h]));
+  }
+  grid_dep_wait();
+  grid_dep_launch();
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
+  for (int i = 0; i < kRing<MT> - 1; ++i) copy_next();
+
+  int use = 0, buf = 0;
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
+    float sum[MT][NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) sum[i][j][v] = 0.0f;
+    for (int run = warp; run < runs; run += kWarps) {
+      uint4 xv[4][NT];
+      const bool whole = run * kW4Run + kW4Run <= Kx;
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+          const uint16_t* p = x[j] + run * kW4Run + 32 * g;
+          xv[g][j] = make_uint4(0, 0, 0, 0);
+          if (whole || run * kW4Run + 32 * g + 8 * t < Kx) xv[g][j] = *reinterpret_cast<const uint4*>(p);
+        }
+      __syncwarp();   // (all lanes are done with the item that is written next)
+      copy_next();
+      copies_wait<kRing<MT> - 1>();
+      __syncwarp();   // (scales are copied for neighbours too)
+      const Item<MT>& it = sm.ring[warp][use];
+      use = (use + 1) % kRing<MT>;
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const uint4 c0 = it.code[2 * i][lane], c1 = it.code[2 * i + 1][lane];
+        float c[NT][4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          if (g * 32 % GROUP == 0) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int v = 0; v < 4; ++v) c[i][j][v] = 0.0f;
-        }
-        const long long k = b * kW4Run + g * 32 + t * 8;
-        uint32_t xb[NT][4];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const int col = 8 * j + q;
-          xb[j][0] = xb[j][1] = xb[j][2] = xb[j][3] = 0u;
-          if (col < cols && k < K) {
-            const long long at = (long long)(t0 + col / TERMS) * a.ldx + k;
-            if constexpr (XK == 2) {
-              const float* p = static_cast<const float*>(a.x) + at;
-              float v[8];
-              if (k + 8 <= K && ((uintptr_t)p & 15u) == 0) {
-                Io<DETFFN_F32>::ld8(p, v);
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[e] = k + e < K ? p[e] : 0.0f;
-              }
-              terms_of(v, col % TERMS, xb[j]);
-            } else {
-              const uint16_t* p = static_cast<const uint16_t*>(a.x) + at;
-              if (k + 8 <= K && ((uintptr_t)p & 15u) == 0) {
-                const uint4 v = *reinterpret_cast<const uint4*>(p);
-                xb[j][0] = v.x, xb[j][1] = v.y, xb[j][2] = v.z, xb[j][3] = v.w;
-              } else {
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                  if (k + e < K) xb[j][e / 2] |= (uint32_t)p[e] << (16 * (e % 2));
-              }
-            }
+              for (int v = 0; v < 4; ++v) c[j][v] = 0.0f;
           }
-        }
+          const uint32_t w0 = g == 0 ? c0.x : g == 1 ? c0.y : g == 2 ? c0.z : c0.w;
+          const uint32_t w1 = g == 0 ? c1.x : g == 1 ? c1.y : g == 2 ? c1.z : c1.w;
+          const uint32_t a0 = pair<BF>(w0, 0), a1 = pair<BF>(w1, 0), a2 = pair<BF>(w0, 1), a3 = pair<BF>(w1, 1);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          const uint32_t w0 = g == 0 ? code[u][i][0].x : g == 1 ? code[u][i][0].y : g == 2 ? code[u][i][0].z : code[u][i][0].w;
-          const uint32_t w1 = g == 0 ? code[u][i][1].x : g == 1 ? code[u][i][1].y : g == 2 ? code[u][i][1].z : code[u][i][1].w;
+          for (int j = 0; j < NT; ++j) mma<BF>(c[j], a0, a1, a2, a3, xv[g][j].x, xv[g][j].y);
+          const uint32_t b0 = pair<BF>(w0, 2), b1 = pair<BF>(w1, 2), b2 = pair<BF>(w0, 3), b3 = pair<BF>(w1, 3);
 #pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const uint32_t a0 = pair<BF>(w0, 2 * s), a1 = pair<BF>(w1, 2 * s), a2 = pair<BF>(w0, 2 * s + 1),
-                           a3 = pair<BF>(w1, 2 * s + 1);
+          for (int j = 0; j < NT; ++j) mma<BF>(c[j], b0, b1, b2, b3, xv[g][j].z, xv[g][j].w);
+          if ((g + 1) * 32 % GROUP == 0) {
+            const int n = g * 32 / GROUP;   // group of the run
+            float s[2];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) mma<BF>(c[i][j], a0, a1, a2, a3, xb[j][2 * s], xb[j][2 * s + 1]);
-          }
-        }
-        if ((g + 1) * 32 % GROUP == 0) {
-          const long long at = (b * kW4Run + g * 32) / GROUP;
-          if (at < groups) {   // (a group past the last column of K has no scale)
-#pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              const float s0 = ld_scale(scales[i], row[i][0] + at, a.w.stype), s1 = ld_scale(scales[i], row[i][1] + at, a.w.stype);
-#pragma unroll
-              for (int j = 0; j < NT; ++j) {
-                sum[i][j][0] = fmaf(s0, c[i][j][0], sum[i][j][0]);
-                sum[i][j][1] = fmaf(s0, c[i][j][1], sum[i][j][1]);
-                sum[i][j][2] = fmaf(s1, c[i][j][2], sum[i][j][2]);
-                sum[i][j][3] = fmaf(s1, c[i][j][3], sum[i][j][3]);
+            for (int h = 0; h < 2; ++h) {
+              const uint32_t* ws = it.scale[16 * i + 8 * h + q];
+              if (wide) {
+                s[h] = __uint_as_float(ws[n]);
+              } else {
+                // (an odd row of an odd number of groups begins in the middle of a word)
+                const int at = n + ((row_of(tile, i, h) * groups + run * PER) & 1);
+                const uint32_t v = ws[at >> 1] >> (16 * (at & 1)) & 0xFFFFu;
+                s[h] = a.w.stype == DETFFN_F16 ? __half2float(__ushort_as_half((uint16_t)v)) : __uint_as_float(v << 16);
               }
+              if (!whole && run * PER + n >= groups) s[h] = 0.0f;   // (a group past the last column of K has no scale)
             }
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+              for (int v = 0; v < 4; ++v) sum[i][j][v] = fmaf(s[v / 2], c[j][v], sum[i][j][v]);
           }
         }
       }
     }
-  }
+    float (&red)[kWarps][16 * MT][8 * NT + 1] = sm.red[Smem<MT, NT>::kRed == 2 ? buf : 0];
+    if (Smem<MT, NT>::kRed == 1) __syncthreads();   // (the last tile's readers)
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int v = 0; v < 4; ++v) red[warp][16 * i + q + 8 * (v / 2)][8 * j + 2 * t + v % 2] = sum[i][j][v];
-  __syncthreads();
-  // The warps' sums in order, a token's terms from the smallest.
-  for (int o = threadIdx.x; o < ROWS * tokens; o += kWarps * 32) {
-    const int r = o % ROWS, tk = o / ROWS;
-    float v[GATED ? 2 : 1];
+        for (int v = 0; v < 4; ++v) red[warp][16 * i + q + 8 * (v / 2)][8 * j + 2 * t + v % 2] = sum[i][j][v];
+    __syncthreads();   // (with two buffers one a tile: the other's readers are past it when it is written again)
+    // The warps' sums in order, a token's terms from the smallest.
+    for (int o = threadIdx.x; o < ROWS * tokens; o += kWarps * 32) {
+      const int r = o % ROWS, tk = o / ROWS, n = tile * ROWS + r;
+      float v[2];
 #pragma unroll
-    for (int i = 0; i < (GATED ? 2 : 1); ++i) {
-      v[i] = 0.0f;
+      for (int i = 0; i < (GATED ? 2 : 1); ++i) {
+        v[i] = 0.0f;
+        for (int e = terms - 1; e >= 0; --e) {
+          float s = 0.0f;
 #pragma unroll
-      for (int e = TERMS - 1; e >= 0; --e) {
-        float s = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) s += red[w][16 * i + r][tk * TERMS + e];
-        v[i] += s;
+          for (int w = 0; w < kWarps; ++w) s += red[w][ROWS * i + r][tk * terms + e];
+          v[i] += s;
+        }
+      }
+      if (n >= (GATED ? (N + 7) & ~7 : N)) continue;
+      const long long at = (t0 + tk) * a.ldo + n;
+      if constexpr (GATED) {
+        uint16_t h[3];
+        terms_of(n < N ? v[0] * sigma<false>(v[0]).s * v[1] : 0.0f, a.terms, h);   // (zeros to a multiple of 8)
+        for (int e = 0; e < a.terms; ++e) static_cast<uint16_t*>(a.out)[at + e * a.plane] = h[e];
+      } else if (a.otype == DETFFN_F32) {
+        static_cast<float*>(a.out)[at] = v[0];
+      } else {
+        static_cast<uint16_t*>(a.out)[at] = a.otype == DETFFN_F16 ? __half_as_ushort(__float2half_rn(v[0])) : f2bf(v[0]);
       }
     }
-    if (n0 + r >= N) continue;
-    const float y = GATED ? v[0] * sigma<false>(v[0]).s * v[GATED ? 1 : 0] : v[0];
-    const long long at = (t0 + tk) * a.ldo + n0 + r;
-    if (a.otype == DETFFN_F32) static_cast<float*>(a.out)[at] = y;
-    else if (a.otype == DETFFN_F16) Io<DETFFN_F16>::st(static_cast<uint16_t*>(a.out) + at, y);
-    else Io<DETFFN_BF16>::st(static_cast<uint16_t*>(a.out) + at, y);
   }
 }
 
-template <int XK, int TERMS, int MT, int NT, bool GATED>
-cudaError_t run_group(const W4Args& a, cudaStream_t st) {
-  constexpr int ROWS = GATED ? 16 : 16 * MT, TOK = 8 * NT / TERMS;
-  const dim3 grid((unsigned)((a.w.N + ROWS - 1) / ROWS), (unsigned)((a.T + TOK - 1) / TOK));
-  if (a.w.group == 32) return launch_dependent(k_w4<XK, TERMS, MT, NT, GATED, 32>, grid, kWarps * 32, 0, st, a);
-  if (a.w.group == 64) return launch_dependent(k_w4<XK, TERMS, MT, NT, GATED, 64>, grid, kWarps * 32, 0, st, a);
-  return launch_dependent(k_w4<XK, TERMS, MT, NT, GATED, 128>, grid, kWarps * 32, 0, st, a);
+template <bool BF, int MT, int NT, bool GATED, int GROUP>
+cudaError_t run_one(const W4Args& a, int sm_count, cudaStream_t st) {
+  constexpr int ROWS = GATED ? 8 * MT : 16 * MT, SM = MT * NT <= 2 ? 3 : MT * NT <= 4 ? 2 : 1;
+  static PerDevice ready;
+  const cudaError_t e = once_per_device(ready, [] {
+    return cudaFuncSetAttribute(k_w4<BF, MT, NT, GATED, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)sizeof(Smem<MT, NT>));
+  });
+  if (e != cudaSuccess) return e;
+  const int tok = 8 * NT / a.x.terms, passes = (a.T + tok - 1) / tok;
+  const long long tiles = (a.w.N + ROWS - 1) / ROWS, slots = (long long)SM * sm_count;
+  return launch_dependent(k_w4<BF, MT, NT, GATED, GROUP>, dim3((unsigned)(tiles < slots ? tiles : slots), (unsigned)passes),
+                          kWarps * 32, (int)sizeof(Smem<MT, NT>), st, a);
 }
-
-template <int XK, int TERMS>
-cudaError_t run(const W4Args& a, cudaStream_t st) {
-  const int cols = a.T * TERMS;
+template <bool BF, int MT, int NT, bool GATED>
+cudaError_t run_group(const W4Args& a, int sm_count, cudaStream_t st) {
+  if (a.w.group == 32) return run_one<BF, MT, NT, GATED, 32>(a, sm_count, st);
+  if (a.w.group == 64) return run_one<BF, MT, NT, GATED, 64>(a, sm_count, st);
+  return run_one<BF, MT, NT, GATED, 128>(a, sm_count, st);
+}
+template <bool BF>
+cudaError_t run(const W4Args& a, int sm_count, cudaStream_t st) {
+  const int cols = a.T * a.x.terms;
   if (a.w2.codes) {
-    if (cols <= 8) return run_group<XK, TERMS, 2, 1, true>(a, st);
-    return run_group<XK, TERMS, 2, 2, true>(a, st);
+    if (cols <= 8) return run_group<BF, 2, 1, true>(a, sm_count, st);
+    if (cols <= 16) return run_group<BF, 2, 2, true>(a, sm_count, st);
+    return run_group<BF, 4, 4, true>(a, sm_count, st);
   }
-  if (cols <= 8) return run_group<XK, TERMS, 1, 1, false>(a, st);
-  return run_group<XK, TERMS, 2, 2, false>(a, st);
+  if (cols <= 8) return run_group<BF, 1, 1, false>(a, sm_count, st);
+  if (cols <= 16) return run_group<BF, 2, 2, false>(a, sm_count, st);
+  return run_group<BF, 4, 4, false>(a, sm_count, st);
+}
+
+// Rows as 16-bit terms, K padded with zeros to a multiple of 8.
+template <int DT>
+__global__ void __launch_bounds__(256) k_rows(const typename Io<DT>::E* x, long long ldx, long long T, long long K, int terms,
+                                              uint16_t* to) {
+  const long long Kp = w4_pad(K), n = T * Kp;
+  grid_dep_wait();
+  grid_dep_launch();
+  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += 256ll * gridDim.x) {
+    const long long r = i / Kp, k = i - r * Kp;
+    if constexpr (DT == DETFFN_F32) {
+      uint16_t h[3] = {0, 0, 0};
+      if (k < K) terms_of(x[r * ldx + k], terms, h);
+      for (int e = 0; e < terms; ++e) to[i + e * n] = h[e];
+    } else {
+      to[i] = k < K ? x[r * ldx + k] : (uint16_t)0;
+    }
+  }
 }
 
 // One warp takes runs of 128 weights of a row, four neighbours a lane.
@@ -336,10 +425,17 @@ unsigned pack_grid(const W4Matrix& m, int sm_count) {
 
 }  // namespace
 
-cudaError_t launch_w4_matvec(const W4Args& a, int, cudaStream_t st) {
-  if (a.xtype == DETFFN_BF16) return run<0, 1>(a, st);
-  if (a.xtype == DETFFN_F16) return run<1, 1>(a, st);
-  return a.terms == 2 ? run<2, 2>(a, st) : run<2, 3>(a, st);
+cudaError_t launch_w4_rows(const void* x, long long ldx, int dtype, long long T, long long K, int terms, void* to,
+                           int sm_count, cudaStream_t st) {
+  const long long want = (T * w4_pad(K) + 255) / 256, most = 4ll * sm_count;
+  const dim3 grid((unsigned)(want < most ? want : most));
+  uint16_t* p = static_cast<uint16_t*>(to);
+  if (dtype == DETFFN_F32) return launch_dependent(k_rows<DETFFN_F32>, grid, 256, 0, st, static_cast<const float*>(x), ldx, T, K, terms, p);
+  return launch_dependent(k_rows<DETFFN_BF16>, grid, 256, 0, st, static_cast<const uint16_t*>(x), ldx, T, K, terms, p);
+}
+
+cudaError_t launch_w4_matvec(const W4Args& a, int sm_count, cudaStream_t st) {
+  return a.x.f16 ? run<false>(a, sm_count, st) : run<true>(a, sm_count, st);
 }
 
 cudaError_t launch_w4_pack(const void* w, long long ld, int dtype, const W4Matrix& to, int sm_count, cudaStream_t st) {

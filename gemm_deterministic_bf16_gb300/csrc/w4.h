@@ -17,19 +17,35 @@ struct W4Matrix {
   int group = 0, stype = 0;
 };
 
-// out[t * N + n] (xtype, or FP32 where out32) of x[t * ldx + k] (xtype).
+// Activations as the kernels read them: 16-bit values (BF16 or FP16) on 16-byte
+// boundaries, row strides a multiple of 8.  An FP32 activation is the sum of
+// `terms` BF16 values, `plane` elements apart.
+struct W4Rows {
+  const void* p = nullptr;
+  long long ld = 0, plane = 0;
+  int terms = 1;
+  bool f16 = false;
+};
+constexpr long long w4_pad(long long n) { return (n + 7) / 8 * 8; }
+// Whether rows of a 16-bit type can be read where they are.
+inline bool w4_in_place(const void* p, long long ld, long long T, long long K) {
+  return (uintptr_t)p % 16 == 0 && K % 8 == 0 && (T <= 1 || ld % 8 == 0);
+}
+
+// out[t * ldo + n] in otype; with w2 = up's matrix (w gate's), SiLU(gate) up as
+// `terms` planes of BF16.
 struct W4Args {
-  W4Matrix w, w2;                 // w2.codes: gate w and up w2, out = SiLU(gate) up
-  const void* x = nullptr;
-  long long ldx = 0;
-  void* out = nullptr;
-  long long ldo = 0;
+  W4Matrix w, w2;
+  W4Rows x;
   int T = 0;
-  int xtype = 0;
-  int otype = 0;
-  int terms = 0;                  // of an FP32 x: 3 (all 24 bits) or 2 (16 bits)
+  void* out = nullptr;
+  long long ldo = 0, plane = 0;
+  int otype = 0, terms = 1;
 };
 
+// x [T, K] of a type as W4Rows at `to` (terms planes of [T][w4_pad(K)]).
+cudaError_t launch_w4_rows(const void* x, long long ldx, int dtype, long long T, long long K, int terms, void* to,
+                           int sm_count, cudaStream_t st);
 cudaError_t launch_w4_matvec(const W4Args& a, int sm_count, cudaStream_t st);
 cudaError_t launch_w4_pack(const void* w, long long ld, int dtype, const W4Matrix& to, int sm_count, cudaStream_t st);
 cudaError_t launch_w4_unpack(const W4Matrix& from, void* w, long long ld, int dtype, int sm_count, cudaStream_t st);

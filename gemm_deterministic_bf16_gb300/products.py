@@ -79,20 +79,29 @@ def detffn_w4_unpack(w4, out=None, dtype=torch.bfloat16, stream=None):
     return (f(*args) if stream is None else _on(stream, f, *args))[0]
 
 
-def detffn_w4_matvec(x, w4, out=None, stream=None):
+def detffn_w4_matvec_workspace_size(T, K, dtype=torch.bfloat16):
+    """Bytes of scratch detffn_w4_matvec needs where x is FP32 or not on 16-byte boundaries."""
+    f = _d.lib().detffn_w4_matvec_workspace_size
+    f.argtypes = [_d._ll] * 2 + [_d._int, ctypes.POINTER(ctypes.c_size_t)]
+    n = ctypes.c_size_t()
+    _d._check(f(T, K, _CODE[dtype], ctypes.byref(n)), "detffn_w4_matvec_workspace_size")
+    return max(n.value, 256)
+
+
+def detffn_w4_matvec(x, w4, out=None, ws=None, stream=None):
     """x [T, K] times the transpose of a 4-bit matrix [N, K], for up to 64 tokens: [T, N]."""
     f = (_b._LIB or _native()).w4_matvec
     if stream is None:
-        return f(x, *w4, out)[0]
-    return _on(stream, f, x, *w4, out)[0]
+        return f(x, *w4, out, ws)[0]
+    return _on(stream, f, x, *w4, out, ws)[0]
 
 
-def detffn_w4_workspace_size(T, H, I):
+def detffn_w4_workspace_size(T, H, I, dtype=torch.bfloat16):
     """Bytes of scratch detffn_w4_forward needs."""
     f = _d.lib().detffn_w4_workspace_size
-    f.argtypes = [_d._ll] * 3 + [ctypes.POINTER(ctypes.c_size_t)]
+    f.argtypes = [_d._ll] * 3 + [_d._int, ctypes.POINTER(ctypes.c_size_t)]
     n = ctypes.c_size_t()
-    _d._check(f(T, H, I, ctypes.byref(n)), "detffn_w4_workspace_size")
+    _d._check(f(T, H, I, _CODE[dtype], ctypes.byref(n)), "detffn_w4_workspace_size")
     return max(n.value, 256)
 
 

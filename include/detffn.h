@@ -532,18 +532,21 @@ DETFFN_API detffn_status detffn_w4_unpack(const void* codes, const void* scales,
  * out [T, N] of `dtype` (any row strides).  A group's products are exact (FP16
  * and BF16 x; FP32 x in three terms of eight bits) and summed in FP32, the
  * group's sum scaled and added in FP32, out rounded once.  A token's result does
- * not depend on the other tokens. */
+ * not depend on the other tokens.  codes on 16-byte boundaries, scales on 4-byte
+ * ones.  `ws`: detffn_w4_matvec_workspace_size bytes, 256-byte aligned; it may be
+ * NULL for FP16 or BF16 rows on 16-byte boundaries with K a multiple of 8. */
+DETFFN_API detffn_status detffn_w4_matvec_workspace_size(long long T, long long K, int dtype, size_t* bytes);
 DETFFN_API detffn_status detffn_w4_matvec(const void* x, long long ldx, const void* codes, const void* scales, void* out,
                                           long long ldo, long long T, long long N, long long K, int group, int dtype,
-                                          int scale_dtype, void* stream);
+                                          int scale_dtype, void* ws, size_t ws_bytes, void* stream);
 
 /* The gated FFN of T <= 64 tokens from three 4-bit matrices of one group and
  * scale type, gate and up [I, H], down [H, I]:
- *   out = ((SiLU(x Wg^T) * (x Wu^T)) Wd^T
- * as above; the hidden activation is kept in FP32, of which the down projection
- * uses 24 significant bits (FP32) or 16.  out may be exactly x.  Not the tree of
- * detffn_forward.  `ws`: detffn_w4_workspace_size bytes, 256-byte aligned. */
-DETFFN_API detffn_status detffn_w4_workspace_size(long long T, long long H, long long I, size_t* bytes);
+ *   out = (SiLU(x Wg^T) * (x Wu^T)) Wd^T
+ * as above; the hidden activation is handed on with 24 significant bits (FP32)
+ * or 16.  out may be exactly x.  Not the tree of detffn_forward.  `ws`:
+ * detffn_w4_workspace_size bytes, 256-byte aligned. */
+DETFFN_API detffn_status detffn_w4_workspace_size(long long T, long long H, long long I, int dtype, size_t* bytes);
 DETFFN_API detffn_status detffn_w4_forward(const void* x, long long ldx, const void* gate_codes, const void* gate_scales,
                                            const void* up_codes, const void* up_scales, const void* down_codes,
                                            const void* down_scales, void* out, long long ldo, long long T, long long H,

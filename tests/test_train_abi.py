@@ -16,8 +16,9 @@ _ARGS = {
                                 _vp, _vp],
     "detffn_w4_pack": [_vp, _ll, _vp, _vp, _ll, _ll, _int, _int, _int, _vp],
     "detffn_w4_unpack": [_vp, _vp, _vp, _ll, _ll, _ll, _int, _int, _int, _vp],
-    "detffn_w4_matvec": [_vp, _ll, _vp, _vp, _vp, _ll, _ll, _ll, _ll, _int, _int, _int, _vp],
-    "detffn_w4_workspace_size": [_ll, _ll, _ll, ctypes.POINTER(_sz)],
+    "detffn_w4_matvec_workspace_size": [_ll, _ll, _int, ctypes.POINTER(_sz)],
+    "detffn_w4_matvec": [_vp, _ll, _vp, _vp, _vp, _ll, _ll, _ll, _ll, _int, _int, _int, _vp, _sz, _vp],
+    "detffn_w4_workspace_size": [_ll, _ll, _ll, _int, ctypes.POINTER(_sz)],
     "detffn_w4_forward": [_vp, _ll] + [_vp] * 7 + [_ll, _ll, _ll, _ll, _int, _int, _int, _vp, _sz, _vp],
     "detffn_dropout_forward": [_vp, _ll, _vp, _ll, _vp, _ll, ctypes.c_double, _u64, _u64, _vp, _ll, _ll, _int, _vp],
     "detffn_dropout_backward": [_vp, _ll, _vp, _ll, ctypes.c_double, _u64, _u64, _vp, _ll, _ll, _int, _vp],
@@ -64,7 +65,8 @@ def test_grouped_refusals(call):
 
 PACK = dict(w=A[0], ldw=200, codes=A[1], scales=A[2], N=8, K=200, group=64, dt=BF16, st=F32, stream=None)
 UNPACK = dict(codes=A[1], scales=A[2], w=A[0], ldw=200, N=8, K=200, group=64, dt=BF16, st=F32, stream=None)
-MV = dict(x=A[0], ldx=200, codes=A[1], scales=A[2], out=A[3], ldo=8, T=4, N=8, K=200, group=64, dt=BF16, st=F32, stream=None)
+MV = dict(x=A[0], ldx=200, codes=A[1], scales=A[2], out=A[3], ldo=8, T=4, N=8, K=200, group=64, dt=BF16, st=F32,
+          ws=None, n=0, stream=None)
 W4F = dict(x=A[0], ldx=200, gc=A[1], gs=A[2], uc=A[3], us=A[4], dc=A[5], ds=A[6], out=A[7], ldo=200, T=4, H=200, I=96,
            group=64, dt=BF16, st=F32, ws=A[8], n=1 << 20, stream=None)
 
@@ -86,14 +88,18 @@ def test_w4_refusals(call):
         assert call("detffn_w4_matvec", MV, **bad) == SHAPE, bad
     assert call("detffn_w4_matvec", MV, T=0, x=None, out=None, codes=None, scales=None) == OK
     assert call("detffn_w4_matvec", MV, out=A[0] + 2) == INVALID and call("detffn_w4_matvec", MV, x=None) == INVALID
+    for odd in (dict(x=A[0] + 2), dict(K=199), dict(ldx=201), dict(dt=F32)):   # rows that are laid out first need scratch
+        assert call("detffn_w4_matvec", MV, **odd) == WORKSPACE, odd
+        assert call("detffn_w4_matvec", MV, ws=A[5], n=1023, **odd) == WORKSPACE, odd
+        assert call("detffn_w4_matvec", MV, ws=A[1], n=1 << 20, **odd) == INVALID, odd
     for bad in (dict(ws=None), dict(ws=A[8] + 128), dict(n=4 * 96 * 4 - 1)):
         assert call("detffn_w4_forward", W4F, **bad) == WORKSPACE, bad
     for bad in (dict(uc=None), dict(ds=None), dict(out=A[5]), dict(out=A[0] + 2), dict(ws=A[7]), dict(dt=9)):
         assert call("detffn_w4_forward", W4F, **bad) == INVALID, bad
     assert call("detffn_w4_forward", W4F, T=0, ws=None) == OK and call("detffn_w4_forward", W4F, I=0) == SHAPE
     n = _sz()
-    assert call("detffn_w4_workspace_size", dict(T=4, H=200, I=96, n=ctypes.byref(n))) == OK and n.value >= 4 * 96 * 4
-    assert call("detffn_w4_workspace_size", dict(T=65, H=200, I=96, n=ctypes.byref(n))) == SHAPE
+    assert call("detffn_w4_workspace_size", dict(T=4, H=200, I=96, dt=BF16, n=ctypes.byref(n))) == OK and n.value >= 4 * 96 * 4
+    assert call("detffn_w4_workspace_size", dict(T=65, H=200, I=96, dt=BF16, n=ctypes.byref(n))) == SHAPE
 
 
 DROP = dict(x=A[0], ldx=64, res=A[1], ldr=64, out=A[2], ldo=64, p=0.1, seed=1, offset=0, state=None, M=4, H=64, dt=BF16,
