@@ -30,6 +30,10 @@
 // loop has little else.  Codes and scales come by cp.async, each lane's own
 // pieces some items ahead in a ring of shared memory that outlasts the row
 // tiles, x from L1 without tests.
+#include <stddef.h>
+
+#include <type_traits>
+
 #include "elt.cuh"
 #include "w4.h"
 
@@ -51,26 +55,39 @@ __device__ __forceinline__ void mma(float (&c)[4], uint32_t a0, uint32_t a1, uin
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with nothing to add to.
+template <bool BF16>
+__device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  if constexpr (BF16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // Codes 2 i and 2 i + 1 of a word, less 8, in the halves of a register.
 template <bool BF16>
 __device__ __forceinline__ uint32_t pair(uint32_t word, int i) {
-  const uint32_t v = word >> (4 * i) & 0x000F000Fu;
-  uint32_t r;
-  if constexpr (BF16) {
-    asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v | 0x43004300u), "r"(0x43084308u));  // 128 + code - 136
-  } else {
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v | 0x64006400u), "r"(0x64086408u));   // 1024 + code - 1032
-  }
+  uint32_t v, r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000F000F), "r"(BF16 ? 0x43004300 : 0x64006400));
+  if constexpr (BF16) asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));  // 128 + code - 136
+  else asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x64086408u));                  // 1024 + code - 1032
   return r;
 }
 
-__device__ __forceinline__ void copy16(void* to, const void* from) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from) : "memory");
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
 }
 // The first n of four bytes, zeros behind.
-__device__ __forceinline__ void copy4(void* to, const void* from, int n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"((uint32_t)__cvta_generic_to_shared(to)), "l"(from), "r"(n)
-               : "memory");
+__device__ __forceinline__ void copy4(uint32_t to, const void* from, int n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(to), "l"(from), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -124,16 +141,18 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
   const int N = (int)a.w.N, K = (int)a.w.K, runs = (K + kW4Run - 1) / kW4Run, groups = (K + GROUP - 1) / GROUP;
   const int tiles = (N + ROWS - 1) / ROWS, Kx = (K + 7) & ~7;
   const bool wide = a.w.stype == DETFFN_F32;
-  // Words of scales of a run that a lane copies: word t of its rows.
-  const int words = wide ? PER : PER / 2 + 1;
-  const long long scale_bytes = (long long)N * groups * (wide ? 4 : 2);
+  // Words of scales of a run that a lane copies: word t of its rows; a run's
+  // first scale of 16 bits may be the upper half of its word.
+  const int words = wide ? PER : PER / 2 + 1, es = wide ? 4 : 2;
+  const long long row_scales = (long long)groups * es;
 
   // Columns past the last read the last one's x; their sums are not used.
   const uint16_t* x[NT];
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
     const int col = min(8 * j + q, cols - 1);
-    x[j] = static_cast<const uint16_t*>(a.x.p) + (col % terms) * a.x.plane + (long long)(t0 + col / terms) * a.x.ld + 8 * t;
+    x[j] = static_cast<const uint16_t*>(a.x.p) + (col % terms) * a.x.plane + (long long)(t0 + col / terms) * a.x.ld + 8 * t +
+           warp * kW4Run;
   }
 
   // The matrix, and the row of it, of row q + 8 h of row tile i; past the last row the last again, not stored.
@@ -141,54 +160,79 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
   auto row_of = [&](int tile, int i, int h) {
     return min(tile * ROWS + 16 * (GATED && i >= MT / 2 ? i - MT / 2 : i) + q + 8 * h, N - 1);
   };
-  const uint8_t* code_at[MT][2];   // of the next copies
-  long long scale_at[MT][2];       // (index of a scale)
-  auto aim = [&](int tile, int run) {
+  // The next copies: pointers of rows q, distances to rows q + 8 (both in a tile).
+  const uint8_t* code_at[MT];
+  const char* scale_at[MT];
+  uint32_t code_8[MT], scale_8[MT];
+  bool inside = false;   // the words of the tile's scales all lie in the array (a run's may reach 16 bytes past its row)
+  auto aim = [&](int tile) {
+    inside = (N - (tile + 1ll) * ROWS) * row_scales >= 16;
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const long long r = row_of(tile, i, h);
-        code_at[i][h] = matrix_of(i).codes + (r * runs + run) * 64 + 16 * t;
-        scale_at[i][h] = r * groups + run * PER;
-      }
+    for (int i = 0; i < MT; ++i) {
+      const long long r = row_of(tile, i, 0), r8 = row_of(tile, i, 1);
+      code_at[i] = matrix_of(i).codes + (r * runs + warp) * 64 + 16 * t;
+      code_8[i] = (uint32_t)(r8 - r) * (uint32_t)runs * 64;
+      const char* s = static_cast<const char*>(matrix_of(i).scales) + 4 * t;
+      const long long at = (r * row_scales + warp * PER * es) & ~3ll, at8 = (r8 * row_scales + warp * PER * es) & ~3ll;
+      scale_at[i] = s + at;
+      scale_8[i] = (uint32_t)(at8 - at);
+    }
   };
-  int ntile = blockIdx.x, nrun = warp, slot = 0;
+  constexpr uint32_t ITEM = sizeof(Item<MT>);
+  const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0]), lane_code = lane * 16,
+                 lane_scale = (uint32_t)offsetof(Item<MT>, scale) + q * 16 + 4 * t;
+  uint32_t put = ring;
+  int ntile = blockIdx.x, nrun = warp;
   if (warp >= runs) ntile = tiles;   // (no run for this warp)
   auto copy_next = [&]() {
     if (ntile < tiles) {
-      Item<MT>& it = sm.ring[warp][slot];
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < MT; ++i) {
+        copy16(put + lane_code + i * 1024, code_at[i]);
+        copy16(put + lane_code + i * 1024 + 512, code_at[i] + code_8[i]);
+        code_at[i] += kWarps * 64;
+      }
+      if (t < words) {
+        if (inside) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          copy16(&it.code[2 * i + h][lane], code_at[i][h]);
-          if (t < words) {
-            const long long at = (wide ? scale_at[i][h] : scale_at[i][h] >> 1) * 4 + 4 * t;
-            const int n = (int)min(max(scale_bytes - at, 0ll), 4ll);
-            copy4(&it.scale[16 * i + 8 * h + q][t], static_cast<const char*>(matrix_of(i).scales) + (n > 0 ? at : 0), n);
+          for (int i = 0; i < MT; ++i) {
+            copy4(put + lane_scale + i * 256, scale_at[i]);
+            copy4(put + lane_scale + i * 256 + 128, scale_at[i] + scale_8[i]);
           }
-          code_at[i][h] += kWarps * 64;
-          scale_at[i][h] += kWarps * PER;
+        } else {   // (the array's end: two bytes of a word, or none)
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const char* base = static_cast<const char*>(matrix_of(i).scales);
+              const char* from = scale_at[i] + (h ? scale_8[i] : 0);
+              const long long left = (long long)N * row_scales - (from - base);
+              copy4(put + lane_scale + i * 256 + h * 128, left > 0 ? from : base, (int)min(max(left, 0ll), 4ll));
+            }
         }
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) scale_at[i] += kWarps * PER * es;
       nrun += kWarps;
       if (nrun >= runs) {
         nrun = warp;
         ntile += gridDim.x;
-        if (ntile < tiles) aim(ntile, nrun);
+        if (ntile < tiles) aim(ntile);
       }
     }
     copies_commit();
-    slot = (slot + 1) % kRing<MT>;
+    put += ITEM;
+    if (put == ring + kRing<MT> * ITEM) put = ring;
   };
 
   if (ntile < tiles) {
-    aim(ntile, nrun);
+    aim(ntile);
     // The first codes on their way to L2 (where nothing the launch before may write can go stale).
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) asm volatile("prefetch.global.L2 [%0];" ::"l"(code_at[i][h]));
+    for (int i = 0; i < MT; ++i) {
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(code_at[i]));
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(code_at[i] + code_8[i]));
+    }
   }
   grid_dep_wait();
   grid_dep_launch();
@@ -196,6 +240,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
   for (int i = 0; i < kRing<MT> - 1; ++i) copy_next();
 
   int use = 0, buf = 0;
+  const int full = Kx / kW4Run;   // whole runs
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
     float sum[MT][NT][4];
 #pragma unroll
@@ -204,17 +249,32 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int v = 0; v < 4; ++v) sum[i][j][v] = 0.0f;
-    for (int run = warp; run < runs; run += kWarps) {
+    int half[MT][2];   // 16, where the runs' first scale is the upper half of its word
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) half[i][h] = ((row_of(tile, i, h) & groups) + warp * PER & 1) * 16;
+    const uint16_t* xr[NT];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) xr[j] = x[j];
+    // One run; LAST: the one that K ends in.
+    auto step = [&](auto last, int run) {
+      constexpr bool LAST = decltype(last)::value;
       uint4 xv[4][NT];
-      const bool whole = run * kW4Run + kW4Run <= Kx;
 #pragma unroll
-      for (int g = 0; g < 4; ++g)
+      for (int j = 0; j < NT; ++j) {
+        const uint4* p = reinterpret_cast<const uint4*>(xr[j]);
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-          const uint16_t* p = x[j] + run * kW4Run + 32 * g;
-          xv[g][j] = make_uint4(0, 0, 0, 0);
-          if (whole || run * kW4Run + 32 * g + 8 * t < Kx) xv[g][j] = *reinterpret_cast<const uint4*>(p);
+        for (int g = 0; g < 4; ++g) {
+          if constexpr (LAST) {
+            xv[g][j] = make_uint4(0, 0, 0, 0);
+            if (run * kW4Run + 32 * g + 8 * t < Kx) xv[g][j] = p[4 * g];
+          } else {
+            xv[g][j] = p[4 * g];
+          }
         }
+        xr[j] += kWarps * kW4Run;
+      }
       __syncwarp();   // (all lanes are done with the item that is written next)
       copy_next();
       copies_wait<kRing<MT> - 1>();
@@ -224,47 +284,57 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
         const uint4 c0 = it.code[2 * i][lane], c1 = it.code[2 * i + 1][lane];
+        float s[2][PER];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t* ws = it.scale[16 * i + 8 * h + q];
+          if (wide) {
+#pragma unroll
+            for (int n = 0; n < PER; ++n) s[h][n] = __uint_as_float(ws[n]);
+          } else {
+            uint32_t v[(PER + 1) / 2];
+#pragma unroll
+            for (int n = 0; n < (PER + 1) / 2; ++n)
+              v[n] = PER == 1 ? ws[0] >> half[i][h] : __funnelshift_r(ws[n], ws[n + 1], half[i][h]);
+#pragma unroll
+            for (int n = 0; n < PER; ++n) {
+              if (a.w.stype == DETFFN_F16) s[h][n] = __half2float(__ushort_as_half((uint16_t)(v[n / 2] >> (n % 2 * 16))));
+              else s[h][n] = __uint_as_float(n % 2 ? v[n / 2] & 0xFFFF0000u : v[n / 2] << 16);
+            }
+          }
+          if constexpr (LAST) {   // (a group past the last column of K has no scale)
+#pragma unroll
+            for (int n = 0; n < PER; ++n)
+              if (run * PER + n >= groups) s[h][n] = 0.0f;
+          }
+        }
         float c[NT][4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          if (g * 32 % GROUP == 0) {
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-              for (int v = 0; v < 4; ++v) c[j][v] = 0.0f;
-          }
           const uint32_t w0 = g == 0 ? c0.x : g == 1 ? c0.y : g == 2 ? c0.z : c0.w;
           const uint32_t w1 = g == 0 ? c1.x : g == 1 ? c1.y : g == 2 ? c1.z : c1.w;
           const uint32_t a0 = pair<BF>(w0, 0), a1 = pair<BF>(w1, 0), a2 = pair<BF>(w0, 1), a3 = pair<BF>(w1, 1);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma<BF>(c[j], a0, a1, a2, a3, xv[g][j].x, xv[g][j].y);
+          for (int j = 0; j < NT; ++j) {
+            if (g * 32 % GROUP == 0) mma_first<BF>(c[j], a0, a1, a2, a3, xv[g][j].x, xv[g][j].y);
+            else mma<BF>(c[j], a0, a1, a2, a3, xv[g][j].x, xv[g][j].y);
+          }
           const uint32_t b0 = pair<BF>(w0, 2), b1 = pair<BF>(w1, 2), b2 = pair<BF>(w0, 3), b3 = pair<BF>(w1, 3);
 #pragma unroll
           for (int j = 0; j < NT; ++j) mma<BF>(c[j], b0, b1, b2, b3, xv[g][j].z, xv[g][j].w);
           if ((g + 1) * 32 % GROUP == 0) {
-            const int n = g * 32 / GROUP;   // group of the run
-            float s[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t* ws = it.scale[16 * i + 8 * h + q];
-              if (wide) {
-                s[h] = __uint_as_float(ws[n]);
-              } else {
-                // (an odd row of an odd number of groups begins in the middle of a word)
-                const int at = n + ((row_of(tile, i, h) * groups + run * PER) & 1);
-                const uint32_t v = ws[at >> 1] >> (16 * (at & 1)) & 0xFFFFu;
-                s[h] = a.w.stype == DETFFN_F16 ? __half2float(__ushort_as_half((uint16_t)v)) : __uint_as_float(v << 16);
-              }
-              if (!whole && run * PER + n >= groups) s[h] = 0.0f;   // (a group past the last column of K has no scale)
-            }
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int v = 0; v < 4; ++v) sum[i][j][v] = fmaf(s[v / 2], c[j][v], sum[i][j][v]);
+              for (int v = 0; v < 4; ++v) sum[i][j][v] = fmaf(s[v / 2][g * 32 / GROUP], c[j][v], sum[i][j][v]);
           }
         }
       }
-    }
+    };
+    int run = warp;
+#pragma unroll 1
+    for (; run < full; run += kWarps) step(std::false_type(), run);
+    if (run < runs) step(std::true_type(), run);
     float (&red)[kWarps][16 * MT][8 * NT + 1] = sm.red[Smem<MT, NT>::kRed == 2 ? buf : 0];
     if (Smem<MT, NT>::kRed == 1) __syncthreads();   // (the last tile's readers)
 #pragma unroll
