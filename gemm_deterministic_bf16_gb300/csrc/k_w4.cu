@@ -69,14 +69,29 @@ __device__ __forceinline__ void mma_first(float (&c)[4], uint32_t a0, uint32_t a
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
-// Codes 2 i and 2 i + 1 of a word, less 8, in the halves of a register.
-template <bool BF16>
-__device__ __forceinline__ uint32_t pair(uint32_t word, int i) {
-  uint32_t v, r;
-  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(v) : "r"(word >> (4 * i)), "r"(0x000F000F), "r"(BF16 ? 0x43004300 : 0x64006400));
-  if constexpr (BF16) asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x43084308u));  // 128 + code - 136
-  else asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x64086408u));                  // 1024 + code - 1032
+__device__ __forceinline__ uint32_t and_or(uint32_t v, uint32_t mask, uint32_t bits) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(v), "r"(mask), "r"(bits));
   return r;
+}
+
+// The four pairs of codes 2 i and 2 i + 1 of a word, less 8, in the halves of a
+// register: 128 + code - 136 in BF16; 1024 + code - 1032, or (1024 + 16 code) / 16 -
+// 72 without a shift, in FP16.  All exact.
+template <bool BF16>
+__device__ __forceinline__ void pairs_of(uint32_t word, uint32_t (&r)[4]) {
+  if constexpr (BF16) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(and_or(word >> (4 * i), 0x000F000Fu, 0x43004300u)), "r"(0x3F803F80u), "r"(0xC308C308u));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = i < 2 ? word : word >> 8;
+      if (i % 2 == 0) asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(and_or(w, 0x000F000Fu, 0x64006400u)), "r"(0x3C003C00u), "r"(0xE408E408u));
+      else asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[i]) : "r"(and_or(w, 0x00F000F0u, 0x64006400u)), "r"(0x2C002C00u), "r"(0xD480D480u));
+    }
+  }
 }
 
 __device__ __forceinline__ void copy16(uint32_t to, const void* from) {
@@ -113,18 +128,20 @@ __device__ __forceinline__ void terms_of(float v, int n, uint16_t (&t)[3]) {
   if (n == 3) t[2] = f2bf(left - bf2f(t[1]));
 }
 
-// Items of a warp's ring: one is used while the others are on their way (of
-// four row tiles one, whose arithmetic takes as long as its bytes).
-template <int MT> constexpr int kRing = MT < 4 ? 4 : 2;
+// Runs of an item (of one row and column tile two, which halve what a run costs
+// besides its conversion), and items of a warp's ring: one is used while the
+// other is on its way.  More would leave the activations no room in L1.
+template <int MT, int NT> constexpr int kRuns = MT * NT == 1 ? 2 : 1;
+template <int MT, int NT> constexpr int kRing = 2;
 
 // Shared memory of a warp's ring item: codes [row half][lane], then scales [row][4 words].
-template <int MT> struct Item {
-  uint4 code[2 * MT][32];
-  uint32_t scale[16 * MT][4];
+template <int MT, int NT> struct Item {
+  uint4 code[kRuns<MT, NT>][2 * MT][32];
+  uint32_t scale[kRuns<MT, NT>][16 * MT][4];
 };
 template <int MT, int NT> struct Smem {
   static constexpr int kRed = MT < 4 ? 2 : 1;
-  Item<MT> ring[kWarps][kRing<MT>];
+  Item<MT, NT> ring[kWarps][kRing<MT, NT>];
   float red[kRed][kWarps][16 * MT][8 * NT + 1];
 };
 
@@ -178,42 +195,51 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
       scale_8[i] = (uint32_t)(at8 - at);
     }
   };
-  constexpr uint32_t ITEM = sizeof(Item<MT>);
+  using It = Item<MT, NT>;
+  constexpr uint32_t ITEM = sizeof(It);
   const uint32_t ring = (uint32_t)__cvta_generic_to_shared(&sm.ring[warp][0]), lane_code = lane * 16,
-                 lane_scale = (uint32_t)offsetof(Item<MT>, scale) + q * 16 + 4 * t;
+                 lane_scale = (uint32_t)offsetof(It, scale) + q * 16 + 4 * t;
   uint32_t put = ring;
   int ntile = blockIdx.x, nrun = warp;
   if (warp >= runs) ntile = tiles;   // (no run for this warp)
-  auto copy_next = [&]() {
-    if (ntile < tiles) {
+  auto copy_run = [&](auto run_of_item) {
+    constexpr int u = decltype(run_of_item)::value;
+    const uint32_t code_to = put + lane_code + u * MT * 1024, scale_to = put + lane_scale + u * MT * 256;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      copy16(code_to + i * 1024, code_at[i] + u * kWarps * 64);
+      copy16(code_to + i * 1024 + 512, code_at[i] + code_8[i] + u * kWarps * 64);
+    }
+    if (t >= words) return;
+    const int step = u * kWarps * PER * es;
+    if (inside) {
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        copy16(put + lane_code + i * 1024, code_at[i]);
-        copy16(put + lane_code + i * 1024 + 512, code_at[i] + code_8[i]);
-        code_at[i] += kWarps * 64;
+        copy4(scale_to + i * 256, scale_at[i] + step);
+        copy4(scale_to + i * 256 + 128, scale_at[i] + scale_8[i] + step);
       }
-      if (t < words) {
-        if (inside) {
+    } else {   // (the array's end: two bytes of a word, or none)
 #pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            copy4(put + lane_scale + i * 256, scale_at[i]);
-            copy4(put + lane_scale + i * 256 + 128, scale_at[i] + scale_8[i]);
-          }
-        } else {   // (the array's end: two bytes of a word, or none)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-          for (int i = 0; i < MT; ++i)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const char* base = static_cast<const char*>(matrix_of(i).scales);
-              const char* from = scale_at[i] + (h ? scale_8[i] : 0);
-              const long long left = (long long)N * row_scales - (from - base);
-              copy4(put + lane_scale + i * 256 + h * 128, left > 0 ? from : base, (int)min(max(left, 0ll), 4ll));
-            }
+        for (int h = 0; h < 2; ++h) {
+          const char* base = static_cast<const char*>(matrix_of(i).scales);
+          const char* from = scale_at[i] + (h ? scale_8[i] : 0) + step;
+          const long long left = (long long)N * row_scales - (from - base);
+          copy4(scale_to + i * 256 + h * 128, left > 0 ? from : base, (int)min(max(left, 0ll), 4ll));
         }
-      }
+    }
+  };
+  auto copy_next = [&]() {
+    if (ntile < tiles) {
+      copy_run(std::integral_constant<int, 0>());
+      if (kRuns<MT, NT> == 2 && nrun + kWarps < runs) copy_run(std::integral_constant<int, kRuns<MT, NT> - 1>());
 #pragma unroll
-      for (int i = 0; i < MT; ++i) scale_at[i] += kWarps * PER * es;
-      nrun += kWarps;
+      for (int i = 0; i < MT; ++i) {
+        code_at[i] += kRuns<MT, NT> * kWarps * 64;
+        scale_at[i] += kRuns<MT, NT> * kWarps * PER * es;
+      }
+      nrun += kRuns<MT, NT> * kWarps;
       if (nrun >= runs) {
         nrun = warp;
         ntile += gridDim.x;
@@ -222,7 +248,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
     }
     copies_commit();
     put += ITEM;
-    if (put == ring + kRing<MT> * ITEM) put = ring;
+    if (put == ring + kRing<MT, NT> * ITEM) put = ring;
   };
 
   if (ntile < tiles) {
@@ -237,7 +263,7 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
   grid_dep_wait();
   grid_dep_launch();
 #pragma unroll
-  for (int i = 0; i < kRing<MT> - 1; ++i) copy_next();
+  for (int i = 0; i < kRing<MT, NT> - 1; ++i) copy_next();
 
   int use = 0, buf = 0;
   const int full = Kx / kW4Run;   // whole runs
@@ -257,13 +283,14 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
     const uint16_t* xr[NT];
 #pragma unroll
     for (int j = 0; j < NT; ++j) xr[j] = x[j];
-    // One run; LAST: the one that K ends in.
-    auto step = [&](auto last, int run) {
+    // Run u of an item; LAST: the one that K ends in.
+    auto one_run = [&](auto last, auto run_of_item, int run) {
       constexpr bool LAST = decltype(last)::value;
+      constexpr int u = decltype(run_of_item)::value;
       uint4 xv[4][NT];
 #pragma unroll
       for (int j = 0; j < NT; ++j) {
-        const uint4* p = reinterpret_cast<const uint4*>(xr[j]);
+        const uint4* p = reinterpret_cast<const uint4*>(xr[j] + u * kWarps * kW4Run);
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           if constexpr (LAST) {
@@ -273,21 +300,21 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
             xv[g][j] = p[4 * g];
           }
         }
-        xr[j] += kWarps * kW4Run;
       }
-      __syncwarp();   // (all lanes are done with the item that is written next)
-      copy_next();
-      copies_wait<kRing<MT> - 1>();
-      __syncwarp();   // (scales are copied for neighbours too)
-      const Item<MT>& it = sm.ring[warp][use];
-      use = (use + 1) % kRing<MT>;
+      if constexpr (u == 0) {
+        __syncwarp();   // (all lanes are done with the item that is written next)
+        copy_next();
+        copies_wait<kRing<MT, NT> - 1>();
+        __syncwarp();   // (scales are copied for neighbours too)
+      }
+      const It& it = sm.ring[warp][use];
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        const uint4 c0 = it.code[2 * i][lane], c1 = it.code[2 * i + 1][lane];
+        const uint4 c0 = it.code[u][2 * i][lane], c1 = it.code[u][2 * i + 1][lane];
         float s[2][PER];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const uint32_t* ws = it.scale[16 * i + 8 * h + q];
+          const uint32_t* ws = it.scale[u][16 * i + 8 * h + q];
           if (wide) {
 #pragma unroll
             for (int n = 0; n < PER; ++n) s[h][n] = __uint_as_float(ws[n]);
@@ -313,15 +340,16 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
         for (int g = 0; g < 4; ++g) {
           const uint32_t w0 = g == 0 ? c0.x : g == 1 ? c0.y : g == 2 ? c0.z : c0.w;
           const uint32_t w1 = g == 0 ? c1.x : g == 1 ? c1.y : g == 2 ? c1.z : c1.w;
-          const uint32_t a0 = pair<BF>(w0, 0), a1 = pair<BF>(w1, 0), a2 = pair<BF>(w0, 1), a3 = pair<BF>(w1, 1);
+          uint32_t p0[4], p1[4];
+          pairs_of<BF>(w0, p0);
+          pairs_of<BF>(w1, p1);
 #pragma unroll
           for (int j = 0; j < NT; ++j) {
-            if (g * 32 % GROUP == 0) mma_first<BF>(c[j], a0, a1, a2, a3, xv[g][j].x, xv[g][j].y);
-            else mma<BF>(c[j], a0, a1, a2, a3, xv[g][j].x, xv[g][j].y);
+            if (g * 32 % GROUP == 0) mma_first<BF>(c[j], p0[0], p1[0], p0[1], p1[1], xv[g][j].x, xv[g][j].y);
+            else mma<BF>(c[j], p0[0], p1[0], p0[1], p1[1], xv[g][j].x, xv[g][j].y);
           }
-          const uint32_t b0 = pair<BF>(w0, 2), b1 = pair<BF>(w1, 2), b2 = pair<BF>(w0, 3), b3 = pair<BF>(w1, 3);
 #pragma unroll
-          for (int j = 0; j < NT; ++j) mma<BF>(c[j], b0, b1, b2, b3, xv[g][j].z, xv[g][j].w);
+          for (int j = 0; j < NT; ++j) mma<BF>(c[j], p0[2], p1[2], p0[3], p1[3], xv[g][j].z, xv[g][j].w);
           if ((g + 1) * 32 % GROUP == 0) {
 #pragma unroll
             for (int j = 0; j < NT; ++j)
@@ -331,10 +359,30 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
         }
       }
     };
+    auto next_item = [&]() {
+      if (++use == kRing<MT, NT>) use = 0;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) xr[j] += kRuns<MT, NT> * kWarps * kW4Run;
+    };
+    using First = std::integral_constant<int, 0>;
+    using Second = std::integral_constant<int, kRuns<MT, NT> - 1>;
     int run = warp;
 #pragma unroll 1
-    for (; run < full; run += kWarps) step(std::false_type(), run);
-    if (run < runs) step(std::true_type(), run);
+    for (; run + (kRuns<MT, NT> - 1) * kWarps < full; run += kRuns<MT, NT> * kWarps) {
+      one_run(std::false_type(), First(), run);
+      if constexpr (kRuns<MT, NT> == 2) one_run(std::false_type(), Second(), run + kWarps);
+      next_item();
+    }
+    // What is left: a run with none or the last behind it, or the last.
+    if (run < runs) {
+      if (kRuns<MT, NT> == 2 && run < full) {
+        one_run(std::false_type(), First(), run);
+        if (run + kWarps < runs) one_run(std::true_type(), Second(), run + kWarps);
+      } else {
+        one_run(std::true_type(), First(), run);
+      }
+      next_item();
+    }
     float (&red)[kWarps][16 * MT][8 * NT + 1] = sm.red[Smem<MT, NT>::kRed == 2 ? buf : 0];
     if (Smem<MT, NT>::kRed == 1) __syncthreads();   // (the last tile's readers)
 #pragma unroll
