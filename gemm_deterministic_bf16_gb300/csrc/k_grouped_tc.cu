@@ -29,6 +29,14 @@
 // from them and takes every (number of pairs)-th; the cut of the rows (the
 // widest tile) is the one whose rounds of tiles, each at the cost of its widest
 // tile, take least.
+//
+// At the MMA's full rate an SM takes in 64 bytes a cycle from L2, which is more
+// than it gets: without loads 16384 x 4096 x 4096 run at 1822 TFLOP/s, with A's
+// alone at 1740, with both at 1407 (each on one box).  So clusters of two pairs
+// take the same rows and neighbouring features: B is loaded once for both, in
+// turn by the one pair and the other, and multicast.
+#include <atomic>
+
 #include "elt.cuh"
 #include "grouped.h"
 #include "ptx.cuh"
@@ -45,11 +53,11 @@ constexpr int kCols = 256;          // columns of tensor memory to a tile's sums
 constexpr int kSuper = 8;           // feature tiles that are taken together
 
 struct Bars {
-  uint64_t full[kStages];    // first CTA: both CTAs' copies have landed
-  uint64_t empty[kStages];   // both: the stage's MMAs are done
+  uint64_t full[kStages];    // first CTA of a pair: both CTAs' copies have landed
+  uint64_t empty[kStages];   // all: the stage's MMAs of all pairs are done
   uint64_t tail[kStages];    // both: this CTA's copies of a stage that is to be cleared have landed
   uint64_t accf[2];          // both: a tile's sums are done
-  uint64_t acce[2];          // first CTA: both CTAs have read them
+  uint64_t acce[2];          // first CTA of a pair: both CTAs have read them
   uint64_t fin;
   uint32_t tmem;
   int abort, cap, total;
@@ -68,6 +76,7 @@ struct Args {
   int* status;
   long long spin;
   int stall;
+  int pairs;                 // of a cluster
 };
 
 // First row, rows, and the tiles before each expert's.
@@ -93,16 +102,19 @@ struct Tile {
 
 __device__ __forceinline__ int up32(int n) { return (n + 31) & ~31; }
 
-// Tile `id`; e: the expert of an earlier one.
-__device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tables& t, int cap) {
+// Feature tiles of all pairs of a cluster count as one.
+__device__ __forceinline__ int feature_tiles(const Args& g) { return (g.F + 256 * g.pairs - 1) / (256 * g.pairs); }
+
+// Tile `id` of a cluster as its pair `pair` takes it; e: the expert of an earlier one.
+__device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tables& t, int cap, int pair) {
   while (id >= t.pre[e + 1]) ++e;
   Tile q;
   q.e = e;
   const int n = g.what == 2 ? g.N : t.cnt[e];
-  const int rt = (n + cap - 1) / cap, ft = (g.F + 255) / 256;
-  const int l = id - t.pre[e], sb = l / (kSuper * rt), m = l - sb * kSuper * rt, w = min(kSuper, ft - sb * kSuper);
+  const int rt = (n + cap - 1) / cap, ft = feature_tiles(g), super = kSuper / g.pairs;
+  const int l = id - t.pre[e], sb = l / (super * rt), m = l - sb * super * rt, w = min(super, ft - sb * super);
   const int r = m / w;
-  q.f0 = (sb * kSuper + m - r * w) * 256;
+  q.f0 = ((sb * super + m - r * w) * g.pairs + pair) * 256;
   const int wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
   q.r0 = r * wide;
   q.rows = min(wide, n - q.r0);
@@ -114,8 +126,8 @@ __device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tab
 }
 
 struct Abort {
-  volatile int* mine;
-  uint32_t other;
+  int* mine;
+  int ctas;
   int* status;
   long long limit;
 };
@@ -130,14 +142,13 @@ __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, const 
       timeout = false;
       break;
     }
-    if ((i & 1023) == 1023 && *a.mine) {
+    if ((i & 1023) == 1023 && *(volatile int*)a.mine) {
       timeout = false;
       break;
     }
   }
   if (timeout) {
-    *a.mine = 1;
-    cluster_st(a.other, 1);
+    for (int c = 0; c < a.ctas; ++c) cluster_st(cluster_addr(a.mine, c), 1);
     if (a.status) atomicExch(a.status, (int)DETFFN_ERR_TIMEOUT);
   }
   return __all_sync(0xffffffffu, ok) != 0;
@@ -154,14 +165,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   Bars* bars = reinterpret_cast<Bars*>(smem + kStages * kStage);
   const Tables t = tables_at(reinterpret_cast<unsigned char*>(bars) + ((sizeof(Bars) + 127) & ~127), g.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
-  const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
-  const Abort ab{&bars->abort, cluster_addr(&bars->abort, rank ^ 1u), g.status, g.spin > 0 ? g.spin : kDefaultSpin};
+  const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;   // of the cluster; of the pair; the pair's first
+  const int mypair = (int)(crank / 2);
+  const int cluster = (int)blockIdx.x / (2 * g.pairs), clusters = (int)gridDim.x / (2 * g.pairs);
+  const Abort ab{&bars->abort, 2 * g.pairs, g.status, g.spin > 0 ? g.spin : kDefaultSpin};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full[s], 2);
-      mbar_init(&bars->empty[s], 1);
+      mbar_init(&bars->empty[s], g.pairs);
       mbar_init(&bars->tail[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -184,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Each lane takes a run of experts.  (Rows out of the tensors, or before the
     // expert's first, are none of its.)
     const int per = (g.E + 31) / 32, e0 = min(lane * per, g.E), e1 = min(e0 + per, g.E);
-    const int ft = (g.F + 255) / 256;
+    const int ft = feature_tiles(g);
     for (int e = e0; e < e1; ++e) {
       const long long b = min(max((long long)__ldg(g.off + e), 0ll), g.R);
       const long long n = max(min((long long)__ldg(g.off + e + 1), g.R) - b, 0ll);
@@ -200,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         int n = 0;
         for (int e = e0; e < e1; ++e) n += (t.cnt[e] + c - 1) / c;
         n = __reduce_add_sync(0xffffffffu, n);
-        const int cost = (int)min((long long)((n * (long long)ft + pairs - 1) / pairs) * (c + 32), 0x7FFFFFFELL);
+        const int cost = (int)min((long long)((n * (long long)ft + clusters - 1) / clusters) * (c + 32), 0x7FFFFFFELL);
         if (cost < best) {
           best = cost;
           cap = c;
@@ -225,26 +237,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       bars->total = s;
       bars->cap = cap;
     }
-    // A timeout recorded earlier stops this launch: one reading for both CTAs.
-    if (lane == 0 && rank == 0 && g.status && *(volatile int*)g.status) {
-      bars->abort = 1;
-      cluster_st(ab.other, 1);
-    }
+    // A timeout recorded earlier stops this launch: one reading for all CTAs of the cluster.
+    if (lane == 0 && crank == 0 && g.status && *(volatile int*)g.status)
+      for (int c = 0; c < ab.ctas; ++c) cluster_st(cluster_addr(ab.mine, c), 1);
   }
   cluster_sync_all();
   const uint32_t tmem = bars->tmem;
-  const int cap = bars->cap, total = *ab.mine ? 0 : bars->total;
+  const int cap = bars->cap, total = *(volatile int*)ab.mine ? 0 : bars->total;
 
   if (warp == 0) {
     // ---------------- loads ----------------
     Ring rs;
     int e = 0;
     bool ok = true;
-    const uint32_t r0 = rank;
-    for (int id = pair; id < total && ok; id += pairs) {
-      const Tile q = tile_at(id, e, g, t, cap);
+    for (int id = cluster; id < total && ok; id += clusters) {
+      const Tile q = tile_at(id, e, g, t, cap, mypair);
       const int half = q.nt / 2, beg = t.beg[q.e];
-      const int fa = q.f0 + (int)r0 * 128;
+      const int fa = q.f0 + (int)rank * 128;
       const int nb = up32(half);   // rows of B, by boxes of 128, or of 64 and 32 (dW: features by boxes of 64)
       const uint32_t bytes = kHalf + (g.what == 2 ? (uint32_t)(half + 63) / 64 * 8192u : (uint32_t)nb * 128u);
       for (int ks = 0; ks < q.steps; ++ks, rs.next(kStages)) {
@@ -255,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool clear = g.what == 2 && ks == q.steps - 1 && (q.last & 15) != 0;
           unsigned char* a = smem + rs.slot * kStage;
           unsigned char* b = a + kHalf;
-          const uint32_t bar = clear ? cluster_addr(&bars->tail[rs.slot], rank) : cluster_addr(&bars->full[rs.slot], 0);
+          const uint32_t bar = clear ? cluster_addr(&bars->tail[rs.slot], crank) : cluster_addr(&bars->full[rs.slot], lead);
           cluster_arrive_expect_tx(bar, bytes);
           if (g.what == 0) {
             pair_load_3d(a, &mA, ks * 64, fa, q.e, bar);
@@ -266,16 +275,25 @@ __global__ void __launch_bounds__(kThreads, 1)
             pair_load_2d(a, &mA, fa, beg + ks * 64, bar);
             pair_load_2d(a + 8192, &mA, fa + 64, beg + ks * 64, bar);
           }
-          if (g.what == 2) {
-            pair_load_2d(b, &mB, q.r0 + (int)r0 * half, beg + ks * 64, bar);
-            if (half > 64) pair_load_2d(b + 8192, &mB, q.r0 + (int)r0 * half + 64, beg + ks * 64, bar);
-          } else {
-            const int y = beg + q.r0 + (int)r0 * half;
-            if (nb == 128) {
-              pair_load_2d(b, &mB, ks * 64, y, bar);
+          // B, for all pairs or (a stage that is cleared, one pair) for this CTA alone.
+          const bool shared = g.pairs == 2 && !clear;
+          if (!shared || (ks & 1) == mypair) {
+            const uint16_t mask = (uint16_t)(5u << rank);
+            auto load = [&](unsigned char* to, const CUtensorMap* map, int x, int y) {
+              if (shared) pair_load_2d_multicast(to, map, x, y, bar, mask);
+              else pair_load_2d(to, map, x, y, bar);
+            };
+            if (g.what == 2) {
+              load(b, &mB, q.r0 + (int)rank * half, beg + ks * 64);
+              if (half > 64) load(b + 8192, &mB, q.r0 + (int)rank * half + 64, beg + ks * 64);
             } else {
-              if (nb >= 64) pair_load_2d(b, &mB64, ks * 64, y, bar);
-              if (nb & 32) pair_load_2d(b + (nb & 64) * 128, &mB32, ks * 64, y + (nb & 64), bar);
+              const int y = beg + q.r0 + (int)rank * half;
+              if (nb == 128) {
+                load(b, &mB, ks * 64, y);
+              } else {
+                if (nb >= 64) load(b, &mB64, ks * 64, y);
+                if (nb & 32) load(b + (nb & 64) * 128, &mB32, ks * 64, y + (nb & 64));
+              }
             }
           }
         }
@@ -287,11 +305,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring rs, rb;
     int e = 0;
     bool ok = true;
+    const uint16_t all = g.pairs == 2 ? 15 : 3, mine = (uint16_t)(3u << lead);
     const uint32_t base = (1u << 4) | (DT == DETFFN_BF16 ? (1u << 7) | (1u << 10) : 0u) | (16u << 24) |
                           (g.what != 0 ? kIdescTransA : 0u) | (g.what == 2 ? kIdescTransB : 0u);
     const uint32_t astep = g.what != 0 ? 128u : 2u, bstep = g.what == 2 ? 128u : 2u;
-    for (int id = pair; id < total && ok; id += pairs) {
-      const Tile q = tile_at(id, e, g, t, cap);
+    for (int id = cluster; id < total && ok; id += clusters) {
+      const Tile q = tile_at(id, e, g, t, cap, mypair);
       if (q.steps == 0) continue;
       ok = wait_pair<true>(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
       if (!ok) break;
@@ -309,15 +328,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int n = ks == q.steps - 1 ? (q.last + 15) / 16 : 4;
           for (int kk = 0; kk < n; ++kk)
             pair_mma_f16(acc, da + (uint64_t)(astep * kk), db + (uint64_t)(bstep * kk), idesc, ks > 0 || kk > 0 ? 1u : 0u);
-          pair_commit(&bars->empty[rs.slot]);
-          if (ks == q.steps - 1) pair_commit(&bars->accf[rb.slot]);
+          pair_commit(&bars->empty[rs.slot], all);
+          if (ks == q.steps - 1) pair_commit(&bars->accf[rb.slot], mine);
         }
         __syncwarp();
       }
       rb.next(2);
     }
     if (!ok) {   // stopped: the MMAs under way end before the shared memory is given up
-      if (elect_one()) pair_commit(&bars->fin);
+      if (elect_one()) pair_commit(&bars->fin, mine);
       __syncwarp();
       mbar_wait(&bars->fin, 0, kDefaultSpin, nullptr);
     }
@@ -326,8 +345,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     Ring rs;
     int e = 0;
     uint32_t used = 0;   // parity of each stage's tail barrier
-    for (int id = pair; id < total; id += pairs) {
-      const Tile q = tile_at(id, e, g, t, cap);
+    for (int id = cluster; id < total; id += clusters) {
+      const Tile q = tile_at(id, e, g, t, cap, mypair);
       if (q.steps == 0 || (q.last & 15) == 0) {
         rs.adv(q.steps, kStages);
         continue;
@@ -342,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           *reinterpret_cast<uint4*>(a + i * 8192 + o) = make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) cluster_arrive(cluster_addr(&bars->full[rs.slot], 0));
+      if (lane == 0) cluster_arrive(cluster_addr(&bars->full[rs.slot], lead));
       __syncwarp();
       rs.next(kStages);
     }
@@ -351,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3;
     Ring rb;
     int e = 0;
-    for (int id = pair; id < total; id += pairs) {
-      const Tile q = tile_at(id, e, g, t, cap);
+    for (int id = cluster; id < total; id += clusters) {
+      const Tile q = tile_at(id, e, g, t, cap, mypair);
       const int f = q.f0 + (int)rank * 128 + quarter * 32 + lane;
       uint16_t* out = g.out + (g.what == 2 ? q.e * g.stride + q.r0 * g.ldo : (t.beg[q.e] + (long long)q.r0) * g.ldo) + f;
       const bool in = f < g.F;
@@ -375,14 +394,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_arrive(cluster_addr(&bars->acce[rb.slot], 0));
+      if (lane == 0) cluster_arrive(cluster_addr(&bars->acce[rb.slot], lead));
       __syncwarp();
       rb.next(2);
     }
   }
   __syncwarp();
   // Stopped by a timeout: what copies are under way land (they take microseconds).
-  if (*ab.mine && total > 0 && !g.stall)
+  if (*(volatile int*)ab.mine && total > 0 && !g.stall)
     for (int i = 0; i < 200; ++i) __nanosleep(10000);
   tc_fence_before();
   cluster_sync_all();   // (neither CTA's barriers or shared memory are used by the other from here on)
@@ -391,6 +410,30 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 int smem_bytes(int E) { return 1024 + kStages * kStage + (int)((sizeof(Bars) + 127) & ~127) + tables_bytes(E); }
+
+// Clusters of two pairs that a device holds at once (asked for once).
+template <int DT>
+cudaError_t rooms(int* n) {
+  static std::atomic<int> known[PerDevice::kDevices];
+  int device = 0;
+  cudaError_t e = cudaGetDevice(&device);
+  if (e != cudaSuccess) return e;
+  const bool keep = device >= 0 && device < PerDevice::kDevices;
+  if (keep && (*n = known[device].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(4);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem_bytes(kGroupedMaxExperts);
+  cudaLaunchAttribute at;
+  at.id = cudaLaunchAttributeClusterDimension;
+  at.val.clusterDim.x = 4;
+  at.val.clusterDim.y = at.val.clusterDim.z = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  e = cudaOccupancyMaxActiveClusters(n, k_grouped_tc<DT>, &cfg);
+  if (e == cudaSuccess && keep) known[device].store(*n, std::memory_order_relaxed);
+  return e;
+}
 
 bool boundary(const Rows& r, long long R) { return (uintptr_t)r.p % 16 == 0 && (R <= 1 || r.ld % 8 == 0); }
 
@@ -436,9 +479,21 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
   g.status = wt.status;
   g.spin = wt.spin;
   g.stall = wt.stall;
-  const long long most = rt * ((g.F + 255) / 256);
-  const int pairs = (int)(most < sm_count / 2 ? most : sm_count / 2);
-  return launch_cluster(k_grouped_tc<DT>, dim3(2 * pairs), kThreads, smem_bytes(a.E), 2, st, mA, mB, mB64, mB32, g);
+  // Two pairs where their features come out even, or nearly so: a pair past the
+  // last feature works for nothing.
+  const int ft = (g.F + 255) / 256;
+  int room = 0;
+  g.pairs = 1;
+  if (ft % 2 == 0 || ft >= 7) {
+    const cudaError_t r = rooms<DT>(&room);
+    if (r != cudaSuccess) return r;
+    if (room > 0) g.pairs = 2;
+  }
+  if (g.pairs == 1) room = sm_count / 2;
+  const long long most = rt * ((ft + g.pairs - 1) / g.pairs);
+  const int clusters = (int)(most < room ? most : room);
+  return launch_cluster(k_grouped_tc<DT>, dim3(2 * g.pairs * clusters), kThreads, smem_bytes(a.E), 2 * g.pairs, st, mA, mB, mB64,
+                        mB32, g);
 }
 
 }  // namespace
