@@ -50,6 +50,8 @@ constexpr int kStages = 6;
 constexpr int kHalf = 128 * 128;    // bytes of an operand's part of a stage: 128 x 64
 constexpr int kStage = 2 * kHalf;
 constexpr int kCols = 256;          // columns of tensor memory to a tile's sums
+constexpr int kChunk = 32;          // output rows that are staged at once
+constexpr int kOutBytes = 2 * kChunk * 256;   // two buffers of kChunk rows x 128 features
 constexpr int kSuper = 8;           // feature tiles that are taken together
 
 struct Bars {
@@ -60,7 +62,7 @@ struct Bars {
   uint64_t acce[2];          // first CTA of a pair: both CTAs have read them
   uint64_t fin;
   uint32_t tmem;
-  int abort, cap, total;
+  int abort, cap, total, whole, parts;
 };
 
 struct Args {
@@ -77,6 +79,7 @@ struct Args {
   long long spin;
   int stall;
   int pairs;                 // of a cluster
+  int vec;                   // output rows lie on 16-byte boundaries
 };
 
 // First row, rows, and the tiles before each expert's.
@@ -105,8 +108,21 @@ __device__ __forceinline__ int up32(int n) { return (n + 31) & ~31; }
 // Feature tiles of all pairs of a cluster count as one.
 __device__ __forceinline__ int feature_tiles(const Args& g) { return (g.F + 256 * g.pairs - 1) / (256 * g.pairs); }
 
-// Tile `id` of a cluster as its pair `pair` takes it; e: the expert of an earlier one.
-__device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tables& t, int cap, int pair) {
+// How the experts' rows are cut: tiles of at most `cap` rows; those from `whole`
+// on, the last round, in `parts` each.
+struct Cut {
+  int cap, whole, parts;
+};
+
+// Unit `id` of a cluster as its pair `pair` takes it; e: the expert of an earlier one.
+__device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tables& t, const Cut& cut, int pair) {
+  const int cap = cut.cap;
+  int part = 0, parts = 1;
+  if (id >= cut.whole) {
+    parts = cut.parts;
+    part = (id - cut.whole) % parts;
+    id = cut.whole + (id - cut.whole) / parts;
+  }
   while (id >= t.pre[e + 1]) ++e;
   Tile q;
   q.e = e;
@@ -118,11 +134,32 @@ __device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tab
   const int wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
   q.r0 = r * wide;
   q.rows = min(wide, n - q.r0);
+  if (parts > 1) {
+    const int piece = up32((q.rows + parts - 1) / parts), skip = part * piece;
+    q.r0 += skip;
+    q.rows = max(min(piece, q.rows - skip), 0);
+  }
   q.nt = up32(q.rows);
-  const int c = g.what == 2 ? t.cnt[e] : g.C;
+  const int c = q.rows == 0 ? 0 : g.what == 2 ? t.cnt[e] : g.C;   // (a part may be left without rows)
   q.steps = (c + 63) / 64;
   q.last = c - (q.steps - 1) * 64;
   return q;
+}
+
+// The four warps that write out.
+__device__ __forceinline__ void out_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// The same barrier; whether `ok` held in all 128 threads.
+__device__ __forceinline__ bool out_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
 }
 
 struct Abort {
@@ -162,7 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ unsigned char raw[];
   // (The same offset in both CTAs: dynamic shared memory starts at the same address in each.)
   unsigned char* smem = reinterpret_cast<unsigned char*>(((uintptr_t)raw + 1023) & ~(uintptr_t)1023);
-  Bars* bars = reinterpret_cast<Bars*>(smem + kStages * kStage);
+  unsigned char* staged = smem + kStages * kStage;
+  Bars* bars = reinterpret_cast<Bars*>(staged + kOutBytes);
   const Tables t = tables_at(reinterpret_cast<unsigned char*>(bars) + ((sizeof(Bars) + 127) & ~127), g.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;   // of the cluster; of the pair; the pair's first
@@ -204,15 +242,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.cnt[e] = (int)n;
     }
     __syncwarp();
-    // The widest tile.
+    // The widest tile: rounds of whole tiles, each at the cost of the widest, and
+    // a last one of parts.  Below some 160 rows a tile costs what its features'
+    // loads do.
+    auto parts_of = [&](int left) { return left > 0 ? min(clusters / left, 8) : 1; };
+    auto cost_of = [&](int rows) { return max(rows, 160) + 32; };
     int cap = 256;
     if (g.what != 2) {
-      int best = 0x7FFFFFFF;
+      long long best = 0x7FFFFFFFFFFFFFFFll;
       for (int c = 256; c >= 32; c -= 32) {
         int n = 0;
         for (int e = e0; e < e1; ++e) n += (t.cnt[e] + c - 1) / c;
-        n = __reduce_add_sync(0xffffffffu, n);
-        const int cost = (int)min((long long)((n * (long long)ft + clusters - 1) / clusters) * (c + 32), 0x7FFFFFFELL);
+        n = __reduce_add_sync(0xffffffffu, n) * ft;
+        const int left = n % clusters;
+        const long long cost = (long long)(n / clusters) * cost_of(c) + (left > 0 ? cost_of(up32((c + parts_of(left) - 1) / parts_of(left))) : 0);
         if (cost < best) {
           best = cost;
           cap = c;
@@ -233,9 +276,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       at += ((g.what == 2 ? g.N : t.cnt[e]) + cap - 1) / cap * ft;
     }
     if (lane == 31) {
+      const int left = s % clusters, parts = parts_of(left);
       t.pre[g.E] = s;
-      bars->total = s;
       bars->cap = cap;
+      bars->whole = s - left;
+      bars->parts = parts;
+      bars->total = s - left + left * parts;
     }
     // A timeout recorded earlier stops this launch: one reading for all CTAs of the cluster.
     if (lane == 0 && crank == 0 && g.status && *(volatile int*)g.status)
@@ -243,7 +289,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   cluster_sync_all();
   const uint32_t tmem = bars->tmem;
-  const int cap = bars->cap, total = *(volatile int*)ab.mine ? 0 : bars->total;
+  const Cut cut{bars->cap, bars->whole, bars->parts};
+  const int total = *(volatile int*)ab.mine ? 0 : bars->total;
 
   if (warp == 0) {
     // ---------------- loads ----------------
@@ -251,7 +298,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int e = 0;
     bool ok = true;
     for (int id = cluster; id < total && ok; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cap, mypair);
+      const Tile q = tile_at(id, e, g, t, cut, mypair);
       const int half = q.nt / 2, beg = t.beg[q.e];
       const int fa = q.f0 + (int)rank * 128;
       const int nb = up32(half);   // rows of B, by boxes of 128, or of 64 and 32 (dW: features by boxes of 64)
@@ -310,9 +357,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                           (g.what != 0 ? kIdescTransA : 0u) | (g.what == 2 ? kIdescTransB : 0u);
     const uint32_t astep = g.what != 0 ? 128u : 2u, bstep = g.what == 2 ? 128u : 2u;
     for (int id = cluster; id < total && ok; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cap, mypair);
+      const Tile q = tile_at(id, e, g, t, cut, mypair);
       if (q.steps == 0) continue;
-      ok = wait_pair<true>(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
+      ok = wait_pair(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
       if (!ok) break;
       tc_fence_after();
       const uint32_t idesc = base | (uint32_t)(q.nt >> 3) << 17, acc = tmem + (uint32_t)(rb.slot * kCols);
@@ -346,7 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int e = 0;
     uint32_t used = 0;   // parity of each stage's tail barrier
     for (int id = cluster; id < total; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cap, mypair);
+      const Tile q = tile_at(id, e, g, t, cut, mypair);
       if (q.steps == 0 || (q.last & 15) == 0) {
         rs.adv(q.steps, kStages);
         continue;
@@ -369,32 +416,59 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ---------------- outputs ----------------
     const int quarter = warp & 3;
     Ring rb;
-    int e = 0;
+    int e = 0, buf = 0;
     for (int id = cluster; id < total; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cap, mypair);
+      const Tile q = tile_at(id, e, g, t, cut, mypair);
       const int f = q.f0 + (int)rank * 128 + quarter * 32 + lane;
       uint16_t* out = g.out + (g.what == 2 ? q.e * g.stride + q.r0 * g.ldo : (t.beg[q.e] + (long long)q.r0) * g.ldo) + f;
       const bool in = f < g.F;
       if (q.steps == 0) {   // an empty sum
-        for (int i = 0; i < q.rows; ++i, out += g.ldo)
-          if (in) *out = 0;
+        const int at = lane % 16 * 8;
+        if (!g.vec) {
+          for (int i = 0; i < q.rows; ++i, out += g.ldo)
+            if (in) *out = 0;
+        } else if (f - quarter * 32 - lane + at < g.F) {
+          out += at - quarter * 32 - lane;
+          for (int i = 2 * quarter + lane / 16; i < q.rows; i += 8)
+            *reinterpret_cast<uint4*>(out + i * g.ldo) = make_uint4(0, 0, 0, 0);
+        }
         continue;
       }
-      if (!wait_pair(&bars->accf[rb.slot], rb.phase, ab)) break;
+      // (One decision for the four warps: with barriers below, none may leave alone.)
+      if (!out_all(wait_pair(&bars->accf[rb.slot], rb.phase, ab))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * kCols);
-      for (int c0 = 0; c0 < q.rows; c0 += 32) {
-        uint32_t v[32];
+      for (int c0 = 0; c0 < q.rows; c0 += kChunk, buf ^= 1) {
+        uint32_t v[kChunk];
         tmem_ld32(taddr + (uint32_t)c0, v);
         tmem_wait_ld();
-        const int n = in ? q.rows - c0 : 0;
+        const int n = min(q.rows - c0, kChunk);
+        if (g.vec) {
+          // Through shared memory, [row][feature], and out in vectors, two rows of
+          // 128 features to a store: element by element from the registers a
+          // tile's 65536 results take 1024 stores of 64 bytes of each CTA.  (A bulk
+          // copy for each row takes some 100 cycles: five times as long.)
+          unsigned char* at = staged + buf * kChunk * 256;
+          uint16_t* to = reinterpret_cast<uint16_t*>(at) + quarter * 32 + lane;
 #pragma unroll
-        for (int i = 0; i < 32; ++i, out += g.ldo)
-          if (i < n) Io<DT>::st(out, __uint_as_float(v[i]));
+          for (int i = 0; i < kChunk; ++i) Io<DT>::st(to + i * 128, __uint_as_float(v[i]));
+          out_sync();   // (one a chunk: the other buffer's readers are past it when it is written again)
+          const int r = 8 * quarter + lane / 16, x = lane % 16 * 8;
+          uint16_t* row = out - quarter * 32 - lane + x + r * g.ldo;
+#pragma unroll
+          for (int i = 0; i < 8; i += 2, row += 2 * g.ldo)
+            if (r + i < n && f - quarter * 32 - lane + x < g.F)
+              *reinterpret_cast<uint4*>(row) = *reinterpret_cast<const uint4*>(at + (r + i) * 256 + x * 2);
+          out += kChunk * g.ldo;
+        } else {
+#pragma unroll
+          for (int i = 0; i < kChunk; ++i, out += g.ldo)
+            if (i < n && in) Io<DT>::st(out, __uint_as_float(v[i]));
+        }
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_arrive(cluster_addr(&bars->acce[rb.slot], lead));
+      if (lane == 0) cluster_arrive_relaxed(cluster_addr(&bars->acce[rb.slot], lead));
       __syncwarp();
       rb.next(2);
     }
@@ -409,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 1) pair_tmem_dealloc(tmem, 2 * kCols);
 }
 
-int smem_bytes(int E) { return 1024 + kStages * kStage + (int)((sizeof(Bars) + 127) & ~127) + tables_bytes(E); }
+int smem_bytes(int E) { return 1024 + kStages * kStage + kOutBytes + (int)((sizeof(Bars) + 127) & ~127) + tables_bytes(E); }
 
 // Clusters of two pairs that a device holds at once (asked for once).
 template <int DT>
@@ -473,6 +547,8 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
     rt = (a.N + 255) / 256 * a.E;
   }
   if (!ok) return cudaErrorInvalidValue;
+  const bool one = what != Grouped::kWeight && a.R == 1;
+  g.vec = (uintptr_t)g.out % 16 == 0 && (one || g.ldo % 8 == 0);
   g.E = a.E;
   g.R = a.R;
   g.off = a.off;

@@ -344,6 +344,11 @@ __device__ __forceinline__ void cluster_st(uint32_t addr, int v) {
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
+// For what tensor memory fences order alone.  (A release at cluster scope waits for all
+// of the thread's stores to global memory.)
+__device__ __forceinline__ void cluster_arrive_relaxed(uint32_t bar) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
 // (Relaxed: it orders nothing; the bytes it announces do that.)
 __device__ __forceinline__ void cluster_arrive_expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.relaxed.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes)
