@@ -8,20 +8,33 @@
 // All three are D[i, j] = sum_c A(i, c) B(j, c), where A and B run along c or
 // across it in memory.  A CTA takes a tile of TI x 128 of one expert after
 // another; the experts' rows are read on the device, so no host needs to know
-// them.  What bounds it is the FP32 multiply-add rate: a thread holds TI / 16 x
-// 8 sums and reads TI / 16 + 8 values of shared memory for each step of c, and
-// the two FP32 multiply-adds of fma.rn.f32x2 share an issue slot.
+// them.  What bounds it is the FP32 multiply-add rate: a thread of a 128 x 128
+// tile holds 8 x 8 sums and reads 16 values of shared memory for each step of c,
+// and the two FP32 multiply-adds of fma.rn.f32x2 share an issue slot.  Tiles are
+// 64 x 64 where larger ones would not fill the SMs twice; four sets of threads
+// then share the steps of c, for with 4 x 4 sums a thread is bound by the reads of
+// shared memory (16 experts of 16 rows, K = N = 1024, FP32: 124 us).
+#include <type_traits>
+
 #include "elt.cuh"
 #include "grouped.h"
 
 namespace detffn {
 namespace {
 
-constexpr int TJ = 128, TC = 16, kThreads = 256;
+constexpr int kThreads = 256;
+// Steps of c to a round: more for small tiles, whose arithmetic hides less of the
+// loads for the next round.
+template <int T> constexpr int kSteps = T == 128 ? 16 : 32;
 
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add_f32x2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t two(float lo, float hi) {
@@ -29,45 +42,76 @@ __device__ __forceinline__ uint64_t two(float lo, float hi) {
 }
 
 // An operand tile of T rows (i) and TC columns (c) on its way to shared memory
-// s[c][i]: ALONG, memory runs along c.  A thread holds T * TC / 256 values.
+// s[c][i]; ALONG: memory runs along c.  A thread holds two runs of four
+// neighbours in memory, and neighbouring threads a row's.
 template <int DT, int T, bool ALONG>
 struct Tile {
   using El = typename Io<DT>::E;
-  static constexpr int V = T * TC / kThreads;   // 8 (T = 128) or 2 (T = 32)
+  static constexpr int TC = kSteps<T>, RUNS = T * TC / (4 * kThreads);
   static constexpr int PITCH = T + 4;
-  float v[V];
-  __device__ __forceinline__ static int i_of(int u) {
-    return ALONG ? (u * kThreads + (int)threadIdx.x) / TC : (u * kThreads + (int)threadIdx.x) % T;
-  }
-  __device__ __forceinline__ static int c_of(int u) {
-    return ALONG ? (u * kThreads + (int)threadIdx.x) % TC : (u * kThreads + (int)threadIdx.x) / T;
-  }
-  // Element (i, c) at p + i * ld + c (ALONG) or p + c * ld + i; zero from ni, nc on.
-  __device__ __forceinline__ void load(const El* p, long long ld, long long ni, long long nc) {
+  static constexpr int LANES = (ALONG ? TC : T) / 4, DOWN = kThreads / LANES;   // threads along memory; rows of a run's threads
+  const El* at[RUNS];  // this thread's first elements of the next step
+  long long step;
+  int i, c, ni;        // its place; rows of the tile that there are
+  bool plain;          // all rows, FP32 in whole vectors
+  float v[RUNS][4];
+  __device__ __forceinline__ int row(int r) const { return ALONG ? i + DOWN * r : i; }
+  __device__ __forceinline__ int col(int r) const { return ALONG ? c : c + DOWN * r; }
+  // Element (i, c) at p + i * ld + c (ALONG) or p + c * ld + i, for i < ni.
+  __device__ __forceinline__ void aim(const El* p, long long ld, long long rows) {
+    const int along = (int)threadIdx.x % LANES * 4, down = (int)threadIdx.x / LANES;
+    i = ALONG ? down : along;
+    c = ALONG ? along : down;
+    ni = (int)min(rows, (long long)T);
 #pragma unroll
-    for (int u = 0; u < V; ++u) {
-      const int i = i_of(u), c = c_of(u);
-      v[u] = i < ni && c < nc ? Io<DT>::ld(p + (ALONG ? i * ld + c : c * ld + i)) : 0.0f;
+    for (int r = 0; r < RUNS; ++r) at[r] = p + (down + DOWN * r) * ld + along;
+    step = ALONG ? TC : TC * ld;
+    plain = rows >= T && (DT != DETFFN_F32 || (((uintptr_t)p & 15) == 0 && (ld & 3) == 0));
+  }
+  // The next TC columns, of which `nc` are there.  PLAIN: all of them, all rows,
+  // and FP32 in whole vectors.  (Without branches: each costs a wait for its loads.)
+  template <bool PLAIN>
+  __device__ __forceinline__ void load(long long nc) {
+#pragma unroll
+    for (int r = 0; r < RUNS; ++r) {
+      if constexpr (PLAIN && DT == DETFFN_F32) {
+        *reinterpret_cast<float4*>(v[r]) = *reinterpret_cast<const float4*>(at[r]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          v[r][u] = 0.0f;
+          if (PLAIN || (ALONG ? row(r) < ni && c + u < nc : col(r) < nc && i + u < ni)) v[r][u] = Io<DT>::ld(at[r] + u);
+        }
+      }
+      at[r] += step;
     }
   }
   __device__ __forceinline__ void store(float* s) const {
 #pragma unroll
-    for (int u = 0; u < V; ++u) s[c_of(u) * PITCH + i_of(u)] = v[u];
+    for (int r = 0; r < RUNS; ++r) {
+      if constexpr (ALONG) {
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[(c + u) * PITCH + row(r)] = v[r][u];
+      } else {
+        *reinterpret_cast<float4*>(s + col(r) * PITCH + i) = *reinterpret_cast<const float4*>(v[r]);
+      }
+    }
   }
 };
 
-template <int DT, Grouped WHAT, int TI>
-__global__ void __launch_bounds__(kThreads) k_grouped(const GroupedArgs a) {
+template <int DT, Grouped WHAT, int T>
+__global__ void __launch_bounds__(kThreads, 2) k_grouped(const GroupedArgs a) {
   using El = typename Io<DT>::E;
   constexpr bool AA = WHAT != Grouped::kWeight, BA = WHAT == Grouped::kForward;
-  constexpr int RI = TI / 16;                    // sums of a thread: RI x 8
-  using TA = Tile<DT, TI, AA>;
-  using TB = Tile<DT, TJ, BA>;
+  constexpr int TC = kSteps<T>;
+  constexpr int S = 8, SIDE = T / S, SETS = kThreads / (SIDE * SIDE);   // sums of a thread: S x S
+  using TA = Tile<DT, T, AA>;
+  using TB = Tile<DT, T, BA>;
   __shared__ __align__(16) float sa[2][TC * TA::PITCH];
   __shared__ __align__(16) float sb[2][TC * TB::PITCH];
-  const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+  const int set = threadIdx.x / (SIDE * SIDE), ty = threadIdx.x / SIDE % SIDE, tx = threadIdx.x % SIDE;
   const long long J = WHAT == Grouped::kForward ? a.N : a.K;
-  const long long tj = (J + TJ - 1) / TJ;
+  const long long tj = (J + T - 1) / T;
   grid_dep_wait();
   grid_dep_launch();
   long long next = blockIdx.x, first = 0;        // this CTA's next tile; the first tile of expert e
@@ -77,76 +121,96 @@ __global__ void __launch_bounds__(kThreads) k_grouped(const GroupedArgs a) {
     const long long n = max(min((long long)__ldg(a.off + e + 1), a.R) - b, 0ll);
     const long long I = WHAT == Grouped::kWeight ? a.N : n;
     const long long C = WHAT == Grouped::kForward ? a.K : WHAT == Grouped::kInput ? a.N : n;
-    const long long tiles = (I + TI - 1) / TI * tj;
+    const long long tiles = (I + T - 1) / T * tj;
     for (; next < first + tiles; next += gridDim.x) {
-      const long long i0 = (next - first) / tj * TI, j0 = (next - first) % tj * TJ;
+      const long long i0 = (next - first) / tj * T, j0 = (next - first) % tj * T;
       const El* W = static_cast<const El*>(a.W) + (long long)e * a.N * a.K;
-      // A(i, c) and B(j, c) of this tile.
-      const El *pa, *pb;
-      long long la, lb;
-      if constexpr (WHAT == Grouped::kForward) {
-        pa = static_cast<const El*>(a.x.p) + (b + i0) * a.x.ld, la = a.x.ld;
-        pb = W + j0 * a.K, lb = a.K;
-      } else if constexpr (WHAT == Grouped::kInput) {
-        pa = static_cast<const El*>(a.dout.p) + (b + i0) * a.dout.ld, la = a.dout.ld;
-        pb = W + j0, lb = a.K;
-      } else {
-        pa = static_cast<const El*>(a.dout.p) + b * a.dout.ld + i0, la = a.dout.ld;
-        pb = static_cast<const El*>(a.x.p) + b * a.x.ld + j0, lb = a.x.ld;
-      }
-      uint64_t sum[RI][4];
-#pragma unroll
-      for (int i = 0; i < RI; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) sum[i][j] = 0;
       TA ra;
       TB rb;
-      ra.load(pa, la, I - i0, C);
-      rb.load(pb, lb, J - j0, C);
-      int s = 0;
-      for (long long c0 = 0; c0 < C; c0 += TC, s ^= 1) {
-        ra.store(sa[s]);
-        rb.store(sb[s]);
-        __syncthreads();   // (the other buffer's readers are past it when it is written again)
-        if (c0 + TC < C) {
-          ra.load(pa + (AA ? c0 + TC : (c0 + TC) * la), la, I - i0, C - c0 - TC);
-          rb.load(pb + (BA ? c0 + TC : (c0 + TC) * lb), lb, J - j0, C - c0 - TC);
-        }
-#pragma unroll
-        for (int c = 0; c < TC; ++c) {
-          float x[RI];
-          uint64_t y[4];
-          const float* fa = sa[s] + c * TA::PITCH;
-          const float* fb = sb[s] + c * TB::PITCH;
-          // Rows ty * 4 .. + 3 of each 64 (or two of 32); columns tx * 4 .. + 3 of each 64.
-          if constexpr (RI == 8) {
-            *reinterpret_cast<float4*>(x) = *reinterpret_cast<const float4*>(fa + 4 * ty);
-            *reinterpret_cast<float4*>(x + 4) = *reinterpret_cast<const float4*>(fa + 64 + 4 * ty);
-          } else {
-#pragma unroll
-            for (int i = 0; i < RI; ++i) x[i] = fa[RI * ty + i];
-          }
-          *reinterpret_cast<ulonglong2*>(y) = *reinterpret_cast<const ulonglong2*>(fb + 4 * tx);
-          *reinterpret_cast<ulonglong2*>(y + 2) = *reinterpret_cast<const ulonglong2*>(fb + 64 + 4 * tx);
-#pragma unroll
-          for (int i = 0; i < RI; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) sum[i][j] = fma_f32x2(two(x[i], x[i]), y[j], sum[i][j]);
-        }
+      if constexpr (WHAT == Grouped::kForward) {
+        ra.aim(static_cast<const El*>(a.x.p) + (b + i0) * a.x.ld, a.x.ld, I - i0);
+        rb.aim(W + j0 * a.K, a.K, J - j0);
+      } else if constexpr (WHAT == Grouped::kInput) {
+        ra.aim(static_cast<const El*>(a.dout.p) + (b + i0) * a.dout.ld, a.dout.ld, I - i0);
+        rb.aim(W + j0, a.K, J - j0);
+      } else {
+        ra.aim(static_cast<const El*>(a.dout.p) + b * a.dout.ld + i0, a.dout.ld, I - i0);
+        rb.aim(static_cast<const El*>(a.x.p) + b * a.x.ld + j0, a.x.ld, J - j0);
       }
-      __syncthreads();   // (the next tile writes the buffers)
+      uint64_t sum[S][S / 2];
+#pragma unroll
+      for (int i = 0; i < S; ++i)
+#pragma unroll
+        for (int j = 0; j < S / 2; ++j) sum[i][j] = 0;
+      auto rounds = [&](auto p, long long c0, long long c1) {   // columns c0 .. c1 - 1
+        constexpr bool PLAIN = decltype(p)::value;
+        ra.template load<PLAIN>(C - c0);
+        rb.template load<PLAIN>(C - c0);
+        int s = 0;
+        for (; c0 < c1; c0 += TC, s ^= 1) {
+          ra.store(sa[s]);
+          rb.store(sb[s]);
+          __syncthreads();   // (the other buffer's readers are past it when it is written again)
+          if (c0 + TC < c1) {
+            ra.template load<PLAIN>(C - c0 - TC);
+            rb.template load<PLAIN>(C - c0 - TC);
+          }
+#pragma unroll
+          for (int k = 0; k < TC / SETS; ++k) {
+            // Rows ty * 4 .. + 3 and columns tx * 4 .. + 3 of each half.
+            const int c = set * (TC / SETS) + k;
+            float x[S];
+            uint64_t y[S / 2];
+#pragma unroll
+            for (int h = 0; h < S / 4; ++h) {
+              *reinterpret_cast<float4*>(x + 4 * h) = *reinterpret_cast<const float4*>(sa[s] + c * TA::PITCH + T / 2 * h + 4 * ty);
+              *reinterpret_cast<ulonglong2*>(y + 2 * h) = *reinterpret_cast<const ulonglong2*>(sb[s] + c * TB::PITCH + T / 2 * h + 4 * tx);
+            }
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+              for (int j = 0; j < S / 2; ++j) sum[i][j] = fma_f32x2(two(x[i], x[i]), y[j], sum[i][j]);
+          }
+        }
+        __syncthreads();   // (the buffers are written again)
+      };
+      const long long whole = ra.plain && rb.plain ? C / TC * TC : 0;
+      if (whole > 0) rounds(std::true_type(), 0, whole);
+      if (whole < C) rounds(std::false_type(), whole, C);
+      if constexpr (SETS > 1) {   // the sets' sums, in order
+        static_assert(sizeof(sa) >= T * T * 4, "one set's sums");
+        float* r = &sa[0][0] + threadIdx.x % (SIDE * SIDE);
+        for (int from = 1; from < SETS; ++from) {
+          if (set == from) {
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+              for (int j = 0; j < S; ++j) r[(i * S + j) * SIDE * SIDE] = __uint_as_float((uint32_t)(sum[i][j / 2] >> (32 * (j % 2))));
+          }
+          __syncthreads();
+          if (set == 0) {
+#pragma unroll
+            for (int i = 0; i < S; ++i)
+#pragma unroll
+              for (int j = 0; j < S / 2; ++j)
+                sum[i][j] = add_f32x2(sum[i][j], two(r[(i * S + 2 * j) * SIDE * SIDE], r[(i * S + 2 * j + 1) * SIDE * SIDE]));
+          }
+          __syncthreads();
+        }
+        if (set > 0) continue;
+      }
       El* out;
       long long lo;
       if constexpr (WHAT == Grouped::kForward) out = static_cast<El*>(const_cast<void*>(a.out.p)) + b * a.out.ld, lo = a.out.ld;
       else if constexpr (WHAT == Grouped::kInput) out = static_cast<El*>(const_cast<void*>(a.dx.p)) + b * a.dx.ld, lo = a.dx.ld;
       else out = static_cast<El*>(a.dW) + (long long)e * a.N * a.K, lo = a.K;
 #pragma unroll
-      for (int i = 0; i < RI; ++i) {
-        const long long r = i0 + (RI == 8 ? i / 4 * 64 + 4 * ty + i % 4 : RI * ty + i);
+      for (int i = 0; i < S; ++i) {
+        const long long r = i0 + i / 4 * (T / 2) + 4 * ty + i % 4;
         if (r >= I) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const long long c = j0 + j / 4 * 64 + 4 * tx + j % 4;
+        for (int j = 0; j < S; ++j) {
+          const long long c = j0 + j / 4 * (T / 2) + 4 * tx + j % 4;
           if (c < J) Io<DT>::st(out + r * lo + c, __uint_as_float((uint32_t)(sum[i][j / 2] >> (32 * (j % 2)))));
         }
       }
@@ -157,17 +221,20 @@ __global__ void __launch_bounds__(kThreads) k_grouped(const GroupedArgs a) {
 
 template <int DT, Grouped WHAT>
 cudaError_t run(const GroupedArgs& a, int sm_count, cudaStream_t st) {
-  // Rows of the tile: 32 where an expert has that many on average, or fewer;
-  // 128 would then multiply padding.
-  const long long I = WHAT == Grouped::kWeight ? a.N : (a.R + a.E - 1) / a.E;
   const long long J = WHAT == Grouped::kForward ? a.N : a.K;
-  const bool few = I <= 32;
-  const int TI = few ? 32 : 128;
-  const long long most = (WHAT == Grouped::kWeight ? a.E * ((a.N + TI - 1) / TI) : a.R / TI + a.E) * ((J + TJ - 1) / TJ);
-  const long long slots = 2ll * sm_count;
-  const dim3 grid((unsigned)(most < slots ? most : slots));
-  return few ? launch_dependent(k_grouped<DT, WHAT, 32>, grid, kThreads, 0, st, a)
-             : launch_dependent(k_grouped<DT, WHAT, 128>, grid, kThreads, 0, st, a);
+  // Tiles of T x T, taking an expert's rows as the average.
+  auto tiles = [&](long long T) {
+    const long long rows = (a.R + a.E - 1) / a.E;
+    return a.E * (((WHAT == Grouped::kWeight ? a.N : rows) + T - 1) / T) * ((J + T - 1) / T);
+  };
+  auto most = [&](long long T) {
+    return (WHAT == Grouped::kWeight ? a.E * ((a.N + T - 1) / T) : a.R / T + a.E) * ((J + T - 1) / T);
+  };
+  const bool small = tiles(128) < 2ll * sm_count || (WHAT != Grouped::kWeight && a.R <= 64ll * a.E);
+  const long long slots = 2ll * sm_count, n = most(small ? 64 : 128);
+  const dim3 grid((unsigned)(n < slots ? n : slots));
+  return small ? launch_dependent(k_grouped<DT, WHAT, 64>, grid, kThreads, 0, st, a)
+               : launch_dependent(k_grouped<DT, WHAT, 128>, grid, kThreads, 0, st, a);
 }
 
 template <int DT>

@@ -18,7 +18,8 @@
 // Each CTA of a pair loads its 128 rows of A and half of B by TMA, 64 of the
 // contraction to a stage, counted by barriers of the first CTA, which issues the
 // MMAs of both; FP32 sums in two halves of tensor memory, so that the next
-// tile's MMAs run while four warps of each CTA write the last one out.
+// tile's MMAs run while four warps of each CTA (eight, where
+// contractions are short) write the last one out.
 //
 // For dW the contraction ends with the expert's rows: those that the last 16 of
 // it take in beyond are another expert's and are cleared in shared memory, in
@@ -46,12 +47,13 @@ namespace detffn {
 namespace {
 
 constexpr int kThreads = 256;       // warp 0 loads, 1 issues MMAs, 2 clears, 3 cuts the rows into tiles, 4-7 write out
+constexpr int kMostThreads = 384;   // and 8-11 too
 constexpr int kStages = 6;
 constexpr int kHalf = 128 * 128;    // bytes of an operand's part of a stage: 128 x 64
 constexpr int kStage = 2 * kHalf;
 constexpr int kCols = 256;          // columns of tensor memory to a tile's sums
 constexpr int kChunk = 32;          // output rows that are staged at once
-constexpr int kOutBytes = 2 * kChunk * 256;   // two buffers of kChunk rows x 128 features
+constexpr int kOutBytes = 2 * kChunk * 256;   // for each four warps that write out, kChunk rows x 128 features
 constexpr int kSuper = 8;           // feature tiles that are taken together
 
 struct Bars {
@@ -62,7 +64,7 @@ struct Bars {
   uint64_t acce[2];          // first CTA of a pair: both CTAs have read them
   uint64_t fin;
   uint32_t tmem;
-  int abort, cap, total, whole, parts;
+  int abort, cap, total;
 };
 
 struct Args {
@@ -79,6 +81,7 @@ struct Args {
   long long spin;
   int stall;
   int pairs;                 // of a cluster
+  int sets;                  // of four warps that write out: 1 or 2
   int vec;                   // output rows lie on 16-byte boundaries
 };
 
@@ -108,21 +111,8 @@ __device__ __forceinline__ int up32(int n) { return (n + 31) & ~31; }
 // Feature tiles of all pairs of a cluster count as one.
 __device__ __forceinline__ int feature_tiles(const Args& g) { return (g.F + 256 * g.pairs - 1) / (256 * g.pairs); }
 
-// How the experts' rows are cut: tiles of at most `cap` rows; those from `whole`
-// on, the last round, in `parts` each.
-struct Cut {
-  int cap, whole, parts;
-};
-
-// Unit `id` of a cluster as its pair `pair` takes it; e: the expert of an earlier one.
-__device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tables& t, const Cut& cut, int pair) {
-  const int cap = cut.cap;
-  int part = 0, parts = 1;
-  if (id >= cut.whole) {
-    parts = cut.parts;
-    part = (id - cut.whole) % parts;
-    id = cut.whole + (id - cut.whole) / parts;
-  }
+// Tile `id` of a cluster as its pair `pair` takes it; e: the expert of an earlier one.
+__device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tables& t, int cap, int pair) {
   while (id >= t.pre[e + 1]) ++e;
   Tile q;
   q.e = e;
@@ -134,30 +124,25 @@ __device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tab
   const int wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
   q.r0 = r * wide;
   q.rows = min(wide, n - q.r0);
-  if (parts > 1) {
-    const int piece = up32((q.rows + parts - 1) / parts), skip = part * piece;
-    q.r0 += skip;
-    q.rows = max(min(piece, q.rows - skip), 0);
-  }
   q.nt = up32(q.rows);
-  const int c = q.rows == 0 ? 0 : g.what == 2 ? t.cnt[e] : g.C;   // (a part may be left without rows)
+  const int c = g.what == 2 ? t.cnt[e] : g.C;
   q.steps = (c + 63) / 64;
   q.last = c - (q.steps - 1) * 64;
   return q;
 }
 
-// The four warps that write out.
-__device__ __forceinline__ void out_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Four of the warps that write out (set 0 or 1).
+__device__ __forceinline__ void out_sync(int set) { asm volatile("bar.sync %0, 128;" ::"r"(set + 1) : "memory"); }
 // The same barrier; whether `ok` held in all 128 threads.
-__device__ __forceinline__ bool out_all(bool ok) {
+__device__ __forceinline__ bool out_all(int set, bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, 128, p;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "bar.red.and.pred q, %1, 128, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)ok)
+      : "r"(set + 1), "r"((uint32_t)ok)
       : "memory");
   return r != 0;
 }
@@ -192,7 +177,7 @@ __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, const 
 }
 
 template <int DT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kMostThreads, 1)
     k_grouped_tc(const __grid_constant__ CUtensorMap mA, const __grid_constant__ CUtensorMap mB,
                  const __grid_constant__ CUtensorMap mB64, const __grid_constant__ CUtensorMap mB32,
                  const __grid_constant__ Args g) {
@@ -216,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&bars->accf[b], 1);
-      mbar_init(&bars->acce[b], 8);   // four warps of each CTA
+      mbar_init(&bars->acce[b], 8 * g.sets);   // the warps of both CTAs that write out
     }
     mbar_init(&bars->fin, 1);
     bars->abort = 0;
@@ -242,20 +227,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       t.cnt[e] = (int)n;
     }
     __syncwarp();
-    // The widest tile: rounds of whole tiles, each at the cost of the widest, and
-    // a last one of parts.  Below some 160 rows a tile costs what its features'
-    // loads do.
-    auto parts_of = [&](int left) { return left > 0 ? min(clusters / left, 8) : 1; };
-    auto cost_of = [&](int rows) { return max(rows, 160) + 32; };
+    // The widest tile: rounds of tiles at the cost of the widest, which below some
+    // 160 rows is that of its features' loads.
     int cap = 256;
     if (g.what != 2) {
       long long best = 0x7FFFFFFFFFFFFFFFll;
       for (int c = 256; c >= 32; c -= 32) {
         int n = 0;
         for (int e = e0; e < e1; ++e) n += (t.cnt[e] + c - 1) / c;
-        n = __reduce_add_sync(0xffffffffu, n) * ft;
-        const int left = n % clusters;
-        const long long cost = (long long)(n / clusters) * cost_of(c) + (left > 0 ? cost_of(up32((c + parts_of(left) - 1) / parts_of(left))) : 0);
+        n = __reduce_add_sync(0xffffffffu, n);
+        const long long cost = (n * (long long)ft + clusters - 1) / clusters * (max(c, 160) + 32);
         if (cost < best) {
           best = cost;
           cap = c;
@@ -276,12 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       at += ((g.what == 2 ? g.N : t.cnt[e]) + cap - 1) / cap * ft;
     }
     if (lane == 31) {
-      const int left = s % clusters, parts = parts_of(left);
       t.pre[g.E] = s;
+      bars->total = s;
       bars->cap = cap;
-      bars->whole = s - left;
-      bars->parts = parts;
-      bars->total = s - left + left * parts;
     }
     // A timeout recorded earlier stops this launch: one reading for all CTAs of the cluster.
     if (lane == 0 && crank == 0 && g.status && *(volatile int*)g.status)
@@ -289,8 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   cluster_sync_all();
   const uint32_t tmem = bars->tmem;
-  const Cut cut{bars->cap, bars->whole, bars->parts};
-  const int total = *(volatile int*)ab.mine ? 0 : bars->total;
+  const int cap = bars->cap, total = *(volatile int*)ab.mine ? 0 : bars->total;
 
   if (warp == 0) {
     // ---------------- loads ----------------
@@ -298,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int e = 0;
     bool ok = true;
     for (int id = cluster; id < total && ok; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cut, mypair);
+      const Tile q = tile_at(id, e, g, t, cap, mypair);
       const int half = q.nt / 2, beg = t.beg[q.e];
       const int fa = q.f0 + (int)rank * 128;
       const int nb = up32(half);   // rows of B, by boxes of 128, or of 64 and 32 (dW: features by boxes of 64)
@@ -357,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                           (g.what != 0 ? kIdescTransA : 0u) | (g.what == 2 ? kIdescTransB : 0u);
     const uint32_t astep = g.what != 0 ? 128u : 2u, bstep = g.what == 2 ? 128u : 2u;
     for (int id = cluster; id < total && ok; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cut, mypair);
+      const Tile q = tile_at(id, e, g, t, cap, mypair);
       if (q.steps == 0) continue;
       ok = wait_pair(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
       if (!ok) break;
@@ -393,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int e = 0;
     uint32_t used = 0;   // parity of each stage's tail barrier
     for (int id = cluster; id < total; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cut, mypair);
+      const Tile q = tile_at(id, e, g, t, cap, mypair);
       if (q.steps == 0 || (q.last & 15) == 0) {
         rs.adv(q.steps, kStages);
         continue;
@@ -414,57 +391,63 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ---------------- outputs ----------------
-    const int quarter = warp & 3;
+    const int quarter = warp & 3, set = warp / 8;   // lanes of tensor memory; which chunks
+    unsigned char* at = staged + set * kChunk * 256;
     Ring rb;
-    int e = 0, buf = 0;
+    int e = 0;
     for (int id = cluster; id < total; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cut, mypair);
+      const Tile q = tile_at(id, e, g, t, cap, mypair);
       const int f = q.f0 + (int)rank * 128 + quarter * 32 + lane;
       uint16_t* out = g.out + (g.what == 2 ? q.e * g.stride + q.r0 * g.ldo : (t.beg[q.e] + (long long)q.r0) * g.ldo) + f;
       const bool in = f < g.F;
       if (q.steps == 0) {   // an empty sum
-        const int at = lane % 16 * 8;
+        const int x = lane % 16 * 8;
         if (!g.vec) {
           for (int i = 0; i < q.rows; ++i, out += g.ldo)
-            if (in) *out = 0;
-        } else if (f - quarter * 32 - lane + at < g.F) {
-          out += at - quarter * 32 - lane;
-          for (int i = 2 * quarter + lane / 16; i < q.rows; i += 8)
+            if (in && set == 0) *out = 0;
+        } else if (f - quarter * 32 - lane + x < g.F) {
+          out += x - quarter * 32 - lane;
+          for (int i = 2 * (warp - 4) + lane / 16; i < q.rows; i += 8 * g.sets)
             *reinterpret_cast<uint4*>(out + i * g.ldo) = make_uint4(0, 0, 0, 0);
         }
         continue;
       }
       // (One decision for the four warps: with barriers below, none may leave alone.)
-      if (!out_all(wait_pair(&bars->accf[rb.slot], rb.phase, ab))) break;
+      if (!out_all(set, wait_pair(&bars->accf[rb.slot], rb.phase, ab))) break;
       tc_fence_after();
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * kCols);
-      for (int c0 = 0; c0 < q.rows; c0 += kChunk, buf ^= 1) {
+      out += set * kChunk * g.ldo;
+      for (int c0 = set * kChunk; c0 < q.rows; c0 += g.sets * kChunk) {
         uint32_t v[kChunk];
         tmem_ld32(taddr + (uint32_t)c0, v);
         tmem_wait_ld();
         const int n = min(q.rows - c0, kChunk);
-        if (g.vec) {
-          // Through shared memory, [row][feature], and out in vectors, two rows of
-          // 128 features to a store: element by element from the registers a
-          // tile's 65536 results take 1024 stores of 64 bytes of each CTA.  (A bulk
-          // copy for each row takes some 100 cycles: five times as long.)
-          unsigned char* at = staged + buf * kChunk * 256;
+        if (g.vec && q.steps <= 4) {
+          // A short contraction is bound by what follows it: through shared memory,
+          // [row][feature], and out in vectors, two rows of 128 features to a
+          // store, where element by element from the registers a tile's 65536
+          // results take 1024 stores of 64 bytes of each CTA (dW of 16 experts of
+          // 94 rows, K = 1416, N = 4096: 92 and 69 us).  Longer ones lose more to
+          // the shared memory that the MMAs read meanwhile (16384 rows, K = 4096, N
+          // = 1536, forward and backward: 518 and 549 us).  A bulk copy for each row
+          // takes some 100 cycles: 267 us of the first.
           uint16_t* to = reinterpret_cast<uint16_t*>(at) + quarter * 32 + lane;
+          out_sync(set);   // (the last chunk's readers)
 #pragma unroll
           for (int i = 0; i < kChunk; ++i) Io<DT>::st(to + i * 128, __uint_as_float(v[i]));
-          out_sync();   // (one a chunk: the other buffer's readers are past it when it is written again)
+          out_sync(set);
           const int r = 8 * quarter + lane / 16, x = lane % 16 * 8;
           uint16_t* row = out - quarter * 32 - lane + x + r * g.ldo;
 #pragma unroll
           for (int i = 0; i < 8; i += 2, row += 2 * g.ldo)
             if (r + i < n && f - quarter * 32 - lane + x < g.F)
               *reinterpret_cast<uint4*>(row) = *reinterpret_cast<const uint4*>(at + (r + i) * 256 + x * 2);
-          out += kChunk * g.ldo;
         } else {
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i, out += g.ldo)
-            if (i < n && in) Io<DT>::st(out, __uint_as_float(v[i]));
+          for (int i = 0; i < kChunk; ++i)
+            if (i < n && in) Io<DT>::st(out + i * g.ldo, __uint_as_float(v[i]));
         }
+        out += g.sets * kChunk * g.ldo;
       }
       tc_fence_before();
       __syncwarp();
@@ -496,7 +479,7 @@ cudaError_t rooms(int* n) {
   if (keep && (*n = known[device].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(4);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kMostThreads);
   cfg.dynamicSmemBytes = (size_t)smem_bytes(kGroupedMaxExperts);
   cudaLaunchAttribute at;
   at.id = cudaLaunchAttributeClusterDimension;
@@ -547,6 +530,10 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
     rt = (a.N + 255) / 256 * a.E;
   }
   if (!ok) return cudaErrorInvalidValue;
+  // Contractions of up to 4 stages on average: the results' way out bounds them
+  // (kMostThreads: dW of 16 experts of 94 rows, K = 1416, N = 4096: 79 and 69 us); with
+  // long ones four more warps cost 2 % (16384 rows, K = 4096, N = 1536).
+  g.sets = (what == Grouped::kWeight ? a.R / a.E : (long long)g.C) <= 256 ? 2 : 1;
   const bool one = what != Grouped::kWeight && a.R == 1;
   g.vec = (uintptr_t)g.out % 16 == 0 && (one || g.ldo % 8 == 0);
   g.E = a.E;
@@ -568,7 +555,7 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
   if (g.pairs == 1) room = sm_count / 2;
   const long long most = rt * ((ft + g.pairs - 1) / g.pairs);
   const int clusters = (int)(most < room ? most : room);
-  return launch_cluster(k_grouped_tc<DT>, dim3(2 * g.pairs * clusters), kThreads, smem_bytes(a.E), 2 * g.pairs, st, mA, mB, mB64,
+  return launch_cluster(k_grouped_tc<DT>, dim3(2 * g.pairs * clusters), g.sets == 2 ? kMostThreads : kThreads, smem_bytes(a.E), 2 * g.pairs, st, mA, mB, mB64,
                         mB32, g);
 }
 
