@@ -3,6 +3,8 @@
 // before it launches anything, and allocates nothing.
 #include <math.h>
 
+#include <initializer_list>
+
 #include "checks.h"
 #include "dropout.h"
 #include "grouped.h"
@@ -49,24 +51,72 @@ detffn_status on_device(detffn_handle h, F&& f) {
   return s;
 }
 
-detffn_status run_grouped(detffn_handle h, const GroupedArgs& a, Grouped what, const detffn_options* o, cudaStream_t st) {
-  const int path = o ? o->path : DETFFN_PATH_AUTO;
-  const bool tensor = path != DETFFN_PATH_EXACT && grouped_tensor_covers(a, what);
-  if (path == DETFFN_PATH_TENSOR && !tensor) return DETFFN_ERR_UNSUPPORTED;
+// Scratch: rows whose width is not a multiple of 8 laid out on 16-byte boundaries.
+struct GroupedScratch {
+  uint16_t *x = nullptr, *W = nullptr, *dout = nullptr;
+};
+GroupedScratch grouped_plan(Arena& w, long long R, long long E, long long K, long long N, int dtype) {
+  GroupedScratch s;
+  if (dtype == DETFFN_F32) return s;
+  if (K % 8) {
+    s.x = w.take<uint16_t>(R * grouped_pad(K));
+    s.W = w.take<uint16_t>(E * N * grouped_pad(K));
+  }
+  if (N % 8) s.dout = w.take<uint16_t>(R * grouped_pad(N));
+  return s;
+}
+
+Waits grouped_waits(detffn_handle h, const detffn_options* o) {
   Waits wt;
   wt.status = h->d_status;
   if (o) {
     wt.spin = o->spin_limit;
     wt.stall = (o->flags & DETFFN_FLAG_TEST_STALL) ? 1 : 0;
   }
+  return wt;
+}
+
+// The products of `a` that `what` lists: on the tensor cores where the rows lie, or
+// can be laid out, on 16-byte boundaries.
+detffn_status run_grouped(detffn_handle h, const GroupedArgs& a, std::initializer_list<Grouped> what, void* ws,
+                          const detffn_options* o, cudaStream_t st) {
+  const int path = o ? o->path : DETFFN_PATH_AUTO;
   const double es = (double)bytes_of(a.dtype), flops = 2.0 * a.R * a.K * a.N;
   // (the weights of as many experts as the rows can reach; the host does not know how many they do)
-  const double w = what == Grouped::kWeight || a.R > a.E ? a.E : (double)a.R;
-  return timed(h, st, tensor ? "grouped_tensor" : "grouped_general", es * ((double)a.R * (a.K + a.N) + w * a.K * a.N), flops,
-               [&] {
-                 return cu(tensor ? launch_grouped_tensor(a, what, wt, h->sm_count, st)
-                                  : launch_grouped_general(a, what, h->sm_count, st));
-               });
+  const double most = a.R > a.E ? a.E : (double)a.R;
+  GroupedArgs t = a;   // as the tensor kernel is to read it
+  Arena w(ws);
+  const GroupedScratch s = grouped_plan(w, a.R, a.E, a.K, a.N, a.dtype);
+  const Rows W{a.W, a.ldw};
+  bool lay_x = false, lay_W = false, lay_d = false, tensor = path != DETFFN_PATH_EXACT && a.dtype != DETFFN_F32;
+  for (Grouped g : what) {
+    if (g != Grouped::kInput) lay_x |= !grouped_boundary(a.x, a.R);
+    if (g != Grouped::kWeight) lay_W |= !grouped_boundary(W, a.E * a.N);
+    if (g != Grouped::kForward) lay_d |= !grouped_boundary(a.dout, a.R);
+  }
+  tensor = tensor && (!lay_x || s.x) && (!lay_W || s.W) && (!lay_d || s.dout);
+  if (path == DETFFN_PATH_TENSOR && !tensor) return DETFFN_ERR_UNSUPPORTED;
+  if (tensor) {
+    if (lay_x) t.x = Rows{s.x, grouped_pad(a.K)};
+    if (lay_W) t.W = s.W, t.ldw = grouped_pad(a.K);
+    if (lay_d) t.dout = Rows{s.dout, grouped_pad(a.N)};
+    const double rows = (lay_x ? (double)a.R * a.K : 0.0) + (lay_W ? (double)a.E * a.N * a.K : 0.0) + (lay_d ? (double)a.R * a.N : 0.0);
+    if (rows > 0.0)
+      TRY(timed(h, st, "grouped_rows", 2.0 * es * rows, 0.0, [&]() -> detffn_status {
+        if (lay_x) TRYCU(launch_grouped_rows(a.x, a.R, a.K, s.x, h->sm_count, st));
+        if (lay_W) TRYCU(launch_grouped_rows(W, a.E * a.N, a.K, s.W, h->sm_count, st));
+        if (lay_d) TRYCU(launch_grouped_rows(a.dout, a.R, a.N, s.dout, h->sm_count, st));
+        return DETFFN_OK;
+      }, (lay_x ? 1 : 0) + (lay_W ? 1 : 0) + (lay_d ? 1 : 0)));
+  }
+  const Waits wt = grouped_waits(h, o);
+  for (Grouped g : what)
+    TRY(timed(h, st, tensor ? "grouped_tensor" : "grouped_general",
+              es * ((double)a.R * (a.K + a.N) + (g == Grouped::kWeight ? a.E : most) * a.K * a.N), flops, [&] {
+                return cu(tensor ? launch_grouped_tensor(t, g, wt, h->sm_count, st)
+                                 : launch_grouped_general(a, g, h->sm_count, st));
+              }));
+  return DETFFN_OK;
 }
 
 // ---------------------------------------------------------------------------
@@ -119,7 +169,9 @@ extern "C" {
 detffn_status detffn_grouped_workspace_size(long long R, long long E, long long K, long long N, int dtype, size_t* bytes) {
   if (!bytes) return DETFFN_ERR_INVALID_ARG;
   TRY(grouped_sizes(R, E, K, N, dtype));
-  *bytes = 0;
+  Arena w(nullptr);
+  grouped_plan(w, R, E, K, N, dtype);
+  *bytes = (w.off + 255) & ~(size_t)255;
   return DETFFN_OK;
 }
 
@@ -152,7 +204,8 @@ detffn_status detffn_grouped_forward(detffn_handle h, const void* x, long long l
   a.x = Rows{x, ldx};
   a.out = Rows{out, ldo};
   a.W = W;
-  return on_device(h, [&] { return run_grouped(h, a, Grouped::kForward, opts, (cudaStream_t)stream); });
+  a.ldw = K;
+  return on_device(h, [&] { return run_grouped(h, a, {Grouped::kForward}, ws, opts, (cudaStream_t)stream); });
 }
 
 detffn_status detffn_grouped_backward(detffn_handle h, const void* x, long long ldx, const void* W, const int* offsets,
@@ -192,13 +245,13 @@ detffn_status detffn_grouped_backward(detffn_handle h, const void* x, long long 
   a.off = offsets;
   a.x = Rows{x, ldx};
   a.W = W;
+  a.ldw = K;
   a.dout = Rows{dOut, lddo};
   a.dx = Rows{dX, lddx};
   a.dW = dW;
   return on_device(h, [&]() -> detffn_status {
-    if (dX) TRY(run_grouped(h, a, Grouped::kInput, opts, st));
-    if (dW) TRY(run_grouped(h, a, Grouped::kWeight, opts, st));
-    return DETFFN_OK;
+    if (dX && dW) return run_grouped(h, a, {Grouped::kInput, Grouped::kWeight}, ws, opts, st);
+    return dX ? run_grouped(h, a, {Grouped::kInput}, ws, opts, st) : run_grouped(h, a, {Grouped::kWeight}, ws, opts, st);
   });
 }
 

@@ -16,16 +16,25 @@ struct GroupedArgs {
   int E = 0, dtype = 0;
   const int* off = nullptr;
   Rows x, out;                     // forward: out[r] = W[e] x[r]
-  const void* W = nullptr;
+  const void* W = nullptr;         // [E * N][K], rows ldw apart (the CUDA-core kernels: K)
+  long long ldw = 0;
   Rows dout, dx;                   // backward: dx[r] = W[e]^T dout[r]
   void* dW = nullptr;              //   dW[e] = sum over the expert's rows of dout[r] x[r]^T
 };
 
 enum class Grouped { kForward, kInput, kWeight };   // out, dx, dW
 
-// Tensor-core kernel: BF16 and FP16, K and N multiples of 8, x, W and dout on
+// Whether rows of a 16-bit type lie on 16-byte boundaries, as the tensor kernel's
+// loads need them.
+inline bool grouped_boundary(const Rows& r, long long rows) {
+  return (uintptr_t)r.p % 16 == 0 && (rows <= 1 || r.ld % 8 == 0);
+}
+constexpr long long grouped_pad(long long n) { return (n + 7) / 8 * 8; }
+// to[r * grouped_pad(width) + c] = from's element (r, c), 16-bit types.
+cudaError_t launch_grouped_rows(const Rows& from, long long rows, long long width, uint16_t* to, int sm_count, cudaStream_t st);
+
+// Tensor-core kernel: BF16 and FP16, rows of x, W and dout (those it reads) on
 // 16-byte boundaries.
-bool grouped_tensor_covers(const GroupedArgs& a, Grouped what);
 cudaError_t launch_grouped_tensor(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_count, cudaStream_t st);
 
 // CUDA-core kernels for any sizes, strides and types.

@@ -492,8 +492,6 @@ cudaError_t rooms(int* n) {
   return e;
 }
 
-bool boundary(const Rows& r, long long R) { return (uintptr_t)r.p % 16 == 0 && (R <= 1 || r.ld % 8 == 0); }
-
 template <int DT>
 cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_count, cudaStream_t st) {
   static PerDevice ready;
@@ -503,8 +501,9 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
   if (e != cudaSuccess) return e;
   const bool f16 = DT == DETFFN_F16;
   // (The stride of a single row is never used; the tensor map wants a multiple of 16 bytes.)
-  const long long ldx = a.R > 1 ? a.x.ld : (a.K + 7) / 8 * 8, ldd = a.R > 1 ? a.dout.ld : (a.N + 7) / 8 * 8;
-  const long long dw[3] = {a.K, a.N, a.E};
+  const long long ldx = a.R > 1 ? a.x.ld : grouped_pad(a.K), ldd = a.R > 1 ? a.dout.ld : grouped_pad(a.N);
+  const long long ldw = a.E * a.N > 1 ? a.ldw : grouped_pad(a.K);
+  const long long dw[3] = {a.K, a.N, a.E}, sw[2] = {ldw, a.N * ldw};
   CUtensorMap mA, mB, mB64, mB32;
   Args g{};
   bool ok;
@@ -515,12 +514,12 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
   };
   if (what == Grouped::kForward) {
     const int box[3] = {64, 128, 1};
-    ok = tc_make_map_nd(&mA, f16, a.W, 3, dw, box) && rows_maps(a.x.p, a.K, ldx);
+    ok = tc_make_map_3d(&mA, f16, a.W, dw, sw, box) && rows_maps(a.x.p, a.K, ldx);
     g.what = 0, g.F = (int)a.N, g.C = (int)a.K, g.out = static_cast<uint16_t*>(const_cast<void*>(a.out.p)), g.ldo = a.out.ld;
     rt = a.R / 32 + a.E;
   } else if (what == Grouped::kInput) {
     const int box[3] = {64, 64, 1};
-    ok = tc_make_map_nd(&mA, f16, a.W, 3, dw, box) && rows_maps(a.dout.p, a.N, ldd);
+    ok = tc_make_map_3d(&mA, f16, a.W, dw, sw, box) && rows_maps(a.dout.p, a.N, ldd);
     g.what = 1, g.F = (int)a.K, g.C = (int)a.N, g.out = static_cast<uint16_t*>(const_cast<void*>(a.dx.p)), g.ldo = a.dx.ld;
     rt = a.R / 32 + a.E;
   } else {
@@ -535,7 +534,7 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
   // long ones four more warps cost 2 % (16384 rows, K = 4096, N = 1536).
   g.sets = (what == Grouped::kWeight ? a.R / a.E : (long long)g.C) <= 256 ? 2 : 1;
   const bool one = what != Grouped::kWeight && a.R == 1;
-  g.vec = (uintptr_t)g.out % 16 == 0 && (one || g.ldo % 8 == 0);
+  g.vec = (uintptr_t)g.out % 16 == 0 && g.F % 8 == 0 && (one || g.ldo % 8 == 0);
   g.E = a.E;
   g.R = a.R;
   g.off = a.off;
@@ -560,13 +559,6 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
 }
 
 }  // namespace
-
-bool grouped_tensor_covers(const GroupedArgs& a, Grouped what) {
-  if (a.dtype == DETFFN_F32 || a.K % 8 != 0 || a.N % 8 != 0) return false;
-  if (what != Grouped::kInput && !boundary(a.x, a.R)) return false;
-  if (what != Grouped::kForward && !boundary(a.dout, a.R)) return false;
-  return what == Grouped::kWeight || (uintptr_t)a.W % 16 == 0;
-}
 
 cudaError_t launch_grouped_tensor(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_count, cudaStream_t st) {
   return a.dtype == DETFFN_F16 ? run<DETFFN_F16>(a, what, wt, sm_count, st) : run<DETFFN_BF16>(a, what, wt, sm_count, st);

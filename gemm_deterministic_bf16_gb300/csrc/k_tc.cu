@@ -767,6 +767,22 @@ bool tc_make_map_nd(CUtensorMap* m, bool f16, const void* base, int nd, const lo
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tc_make_map_3d(CUtensorMap* m, bool f16, const void* base, const long long* dim, const long long* stride, const int* box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  cuuint64_t dims[3], strides[2];
+  cuuint32_t bx[3];
+  const cuuint32_t es[3] = {1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i] = (cuuint64_t)dim[i];
+    bx[i] = (cuuint32_t)box[i];
+    if (i < 2) strides[i] = (cuuint64_t)stride[i] * 2;
+  }
+  return enc(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims,
+             strides, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool tc_make_map_rows(CUtensorMap* m, bool f16, const void* base, long long rows, long long width, long long ld, int box_x,
                       int box_rows) {
   EncodeTiledFn enc = encode_fn();

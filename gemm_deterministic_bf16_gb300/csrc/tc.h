@@ -63,6 +63,9 @@ bool tc_make_map(CUtensorMap* m, const uint16_t* base, long long rows, long long
 // BF16 or FP16, rows a multiple of 16 bytes), 128-byte swizzle.
 bool tc_make_map_nd(CUtensorMap* m, bool f16, const void* base, int nd, const long long* dim, const int* box);
 
+// The same over three axes with the strides (elements, multiples of 8) of the outer two.
+bool tc_make_map_3d(CUtensorMap* m, bool f16, const void* base, const long long* dim, const long long* stride, const int* box);
+
 // A 2-D BF16 or FP16 tensor map over rows x width (row stride ld elements, a
 // multiple of 8), 128-byte swizzle, boxes of box_x x box_rows.
 bool tc_make_map_rows(CUtensorMap* m, bool f16, const void* base, long long rows, long long width, long long ld, int box_x,

@@ -80,8 +80,32 @@ def test_products(G, sizes, K, N, dtype):
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("sizes", SIZES[3:7], ids=lambda s: "-".join(map(str, s[:5])))
-def test_cuda_core_path(G, sizes, dtype):
-    run(G, sizes, 264, 520, dtype, path=EXACT, seed=3)
+@pytest.mark.parametrize("K,N", [(264, 520), (65, 33), (131, 72)])
+def test_cuda_core_path(G, sizes, K, N, dtype):
+    run(G, sizes, K, N, dtype, path=EXACT, seed=3)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("K,N", [(1, 1), (65, 33), (131, 72), (136, 77), (1023, 515)])
+def test_tensor_path_of_any_width(G, K, N, dtype):
+    """Rows that lie on no 16-byte boundary are laid out in the workspace first."""
+    run(G, [17, 0, 255, 300], K, N, dtype, path=TENSOR, seed=4, first=3, behind=5)
+
+
+def test_workspace_of_the_caller(G):
+    x, W, d, off, ends = make([30, 50], 65, 33, torch.bfloat16)
+    n = G.detffn_grouped_workspace_size(80, 2, 65, 33)
+    assert n > 0 and G.detffn_grouped_workspace_size(80, 2, 64, 32) == 0
+    assert G.detffn_grouped_workspace_size(80, 2, 65, 33, torch.float32) == 0
+    ws = torch.full((n + 512,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = G.detffn_grouped_forward(x, W, off, ws=ws)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d, ws=ws)
+    check_forward(G, x, W, off, ends, out, out)
+    check_backward(G, x, W, d, ends, dX, dW, dX)
+    assert bool((ws[n:] == 0xFF).all())
+    with pytest.raises(G.DetFFNError) as e:
+        G.detffn_grouped_forward(x, W, off, ws=ws[:n - 256])
+    assert e.value.status == 5
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])

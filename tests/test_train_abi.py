@@ -60,6 +60,11 @@ def test_grouped_refusals(call):
         assert call("detffn_grouped_backward", BWD, **bad) == INVALID, bad
     n = _sz(7)
     assert call("detffn_grouped_workspace_size", dict(R=16, E=2, K=64, N=32, dt=BF16, n=ctypes.byref(n))) == OK and n.value == 0
+    assert call("detffn_grouped_workspace_size", dict(R=16, E=2, K=63, N=32, dt=BF16, n=ctypes.byref(n))) == OK
+    assert n.value >= (16 + 2 * 32) * 64 * 2
+    for name, kw in (("detffn_grouped_forward", FWD), ("detffn_grouped_backward", BWD)):
+        for bad in (dict(ws=None), dict(ws=kw["ws"] + 128), dict(n=n.value - 1)):
+            assert call(name, kw, K=63, **bad) == WORKSPACE, bad
     assert call("detffn_grouped_workspace_size", dict(R=16, E=0, K=64, N=32, dt=BF16, n=ctypes.byref(n))) == SHAPE
 
 
