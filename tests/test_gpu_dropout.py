@@ -152,3 +152,16 @@ def test_no_rows_and_refusals(G):
     with pytest.raises(G.DetFFNError) as e:
         G.detffn_dropout_forward(x[:2], 0.1, 1, out=x[1:3])
     assert e.value.status == 1
+
+
+def test_addresses_beyond_32_bits(G):
+    """More than 2^32 elements: the words of the last rows, and rows of a wide stride."""
+    M, H, p, seed = (1 << 20) + 5, 4104, 0.3, 11
+    x = torch.ones((M, H), dtype=torch.bfloat16, device="cuda")
+    out = G.detffn_dropout_forward(x, p, seed, 2, out=x)
+    limit = int(p * 4294967296.0)
+    for m in (0, 1 << 19, M - 1):
+        for c in (0, 1, 2051, H - 1):
+            assert bool(out[m, c] != 0) == (philox((c // 4, m, 2, 0), (seed, 0))[c % 4] >= limit)
+    last = torch.ones((M, 8), dtype=torch.bfloat16, device="cuda")
+    assert torch.equal(G.detffn_dropout_forward(last, p, seed, 2)[M - 9:], out[M - 9:, :8])

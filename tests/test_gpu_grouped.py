@@ -279,3 +279,34 @@ def test_a_wait_that_runs_out_is_reported(G, what):
     got = G.detffn_grouped_forward(x, W, off, out=out, path=TENSOR)
     want = torch.cat([x[:100].double() @ W[0].double().T, x[100:].double() @ W[1].double().T])
     assert float((got.double() - want).norm() / want.norm()) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype,K,N", [(torch.bfloat16, 64, 40), (torch.float32, 33, 20)])
+def test_as_many_experts_as_there_may_be(G, dtype, K, N):
+    g = torch.Generator().manual_seed(1)
+    run(G, torch.randint(0, 4, (1024,), generator=g).tolist(), K, N, dtype, seed=6)
+
+
+@pytest.mark.parametrize("dtype,E", [(torch.bfloat16, 65), (torch.float32, 33)])
+def test_addresses_beyond_32_bits(G, dtype, E):
+    """W and dW of more than 2^32 (FP32: 2^31) elements: the first and the last expert's results."""
+    K = N = 8192
+    sizes = [70] + [0] * (E - 2) + [130]
+    W = torch.zeros((E, N, K), dtype=dtype, device="cuda")
+    ends = [0] + [70] * (E - 1) + [200]
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    r = lambda *s: torch.randn(s, generator=gen, device="cuda").to(dtype)  # noqa: E731
+    for e in (0, E - 1):
+        W[e] = r(N, K)
+    x, d = r(200, K), r(200, N)
+    out = G.detffn_grouped_forward(x, W, off)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d)
+    for e in (0, E - 1):
+        a, b = ends[e], ends[e + 1]
+        assert b - a == sizes[e]
+        x64, w64, d64 = x[a:b].double(), W[e].double(), d[a:b].double()
+        close(out[a:b], x64 @ w64.T, x64.abs() @ w64.abs().T, K, dtype)
+        close(dX[a:b], d64 @ w64, d64.abs() @ w64.abs(), N, dtype)
+        close(dW[e], d64.T @ x64, d64.abs().T @ x64.abs(), b - a, dtype)
+    assert not bool(dW[1].any()) and not bool(dW[E - 2].any())

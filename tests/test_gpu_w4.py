@@ -205,3 +205,21 @@ def test_refusals(G):
     with pytest.raises(G.DetFFNError) as e:
         G.detffn_w4_matvec(x, w._replace(codes=torch.zeros(16 * 64 + 8, dtype=torch.uint8, device="cuda")[8:].view(16, 64)))
     assert e.value.status == 3
+
+
+def test_addresses_beyond_32_bits(G):
+    """Codes of more than 2^32 bytes: the first and the last rows' products."""
+    N, K = 1 << 20, 8320
+    w = G.W4(torch.zeros((N, K // 2), dtype=torch.uint8, device="cuda"), torch.zeros((N, K // 128), dtype=torch.bfloat16, device="cuda"), K, 128)
+    part = matrix(G, 64, K, 128, torch.bfloat16)
+    for at in (slice(0, 64), slice(N - 64, N)):
+        w.codes[at] = part.codes
+        w.scales[at] = part.scales
+    x = torch.randn((3, K), device="cuda").bfloat16()
+    out = G.detffn_w4_matvec(x, w)
+    want = G.detffn_w4_matvec(x, part)
+    assert torch.equal(out[:, :64], want) and torch.equal(out[:, N - 64:], want) and not bool(out[:, 64:N - 64].any())
+    check(want, x, values64(part), torch.bfloat16, K)
+    v = torch.empty((64, K), dtype=torch.float32, device="cuda")
+    last = w._replace(codes=w.codes[N - 64:], scales=w.scales[N - 64:])
+    assert torch.equal(G.detffn_w4_unpack(last, out=v), values64(part).float())
