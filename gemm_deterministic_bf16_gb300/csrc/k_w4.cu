@@ -441,6 +441,11 @@ cudaError_t run_group(const W4Args& a, int sm_count, cudaStream_t st) {
   if (a.w.group == 64) return run_one<BF, MT, NT, GATED, 64>(a, sm_count, st);
   return run_one<BF, MT, NT, GATED, 128>(a, sm_count, st);
 }
+// Columns in passes of 8, 16 or 32, weights read again (from L2) for each.  Four
+// row and column tiles read x from L1 half as often as two, and leave an SM eight
+// warps instead of sixteen: they pay for gate and up from 17 columns on (FFN of 8
+// tokens in FP32, H = 4096, I = 12288: 59 and 55 us), else from 33 (16 tokens in BF16: 52 and
+// 41.5 us with two tiles; 32 tokens, 64 columns: 70.6 and 74.6).
 template <bool BF>
 cudaError_t run(const W4Args& a, int sm_count, cudaStream_t st) {
   const int cols = a.T * a.x.terms;
@@ -450,7 +455,7 @@ cudaError_t run(const W4Args& a, int sm_count, cudaStream_t st) {
     return run_group<BF, 4, 4, true>(a, sm_count, st);
   }
   if (cols <= 8) return run_group<BF, 1, 1, false>(a, sm_count, st);
-  if (cols <= 16) return run_group<BF, 2, 2, false>(a, sm_count, st);
+  if (cols <= 32) return run_group<BF, 2, 2, false>(a, sm_count, st);
   return run_group<BF, 4, 4, false>(a, sm_count, st);
 }
 
