@@ -53,7 +53,8 @@ constexpr int kHalf = 128 * 128;    // bytes of an operand's part of a stage: 12
 constexpr int kStage = 2 * kHalf;
 constexpr int kCols = 256;          // columns of tensor memory to a tile's sums
 constexpr int kChunk = 32;          // output rows that are staged at once
-constexpr int kOutBytes = 2 * kChunk * 256;   // for each four warps that write out, kChunk rows x 128 features
+constexpr int kPitch = 256 + 16;    // of a staged row of 128 features: eight rows of a transposed store meet no bank twice
+constexpr int kOutBytes = 2 * kChunk * kPitch;   // for each four warps that write out, kChunk rows
 constexpr int kSuper = 8;           // feature tiles that are taken together
 
 struct Bars {
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(kMostThreads, 1)
   } else if (warp >= 4) {
     // ---------------- outputs ----------------
     const int quarter = warp & 3, set = warp / 8;   // lanes of tensor memory; which chunks
-    unsigned char* at = staged + set * kChunk * 256;
+    unsigned char* at = staged + set * kChunk * kPitch;
     Ring rb;
     int e = 0;
     for (int id = cluster; id < total; id += clusters) {
@@ -418,31 +419,45 @@ __global__ void __launch_bounds__(kMostThreads, 1)
       const uint32_t taddr = tmem + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(rb.slot * kCols);
       out += set * kChunk * g.ldo;
       for (int c0 = set * kChunk; c0 < q.rows; c0 += g.sets * kChunk) {
-        uint32_t v[kChunk];
-        tmem_ld32(taddr + (uint32_t)c0, v);
-        tmem_wait_ld();
         const int n = min(q.rows - c0, kChunk);
         if (g.vec && q.steps <= 4) {
           // A short contraction is bound by what follows it: through shared memory,
           // [row][feature], and out in vectors, two rows of 128 features to a
           // store, where element by element from the registers a tile's 65536
           // results take 1024 stores of 64 bytes of each CTA (dW of 16 experts of
-          // 94 rows, K = 1416, N = 4096: 92 and 69 us).  Longer ones lose more to
+          // 94 rows, K = 1416, N = 4096: 92 and %%% us).  Longer ones lose more to
           // the shared memory that the MMAs read meanwhile (16384 rows, K = 4096, N
           // = 1536, forward and backward: 518 and 549 us).  A bulk copy for each row
           // takes some 100 cycles: 267 us of the first.
-          uint16_t* to = reinterpret_cast<uint16_t*>(at) + quarter * 32 + lane;
+          uint32_t v[2][16];
+          tmem_ld_frag(taddr + (uint32_t)c0, v[0]);
+          tmem_ld_frag(taddr + (16u << 16) + (uint32_t)c0, v[1]);
+          tmem_wait_ld();
           out_sync(set);   // (the last chunk's readers)
 #pragma unroll
-          for (int i = 0; i < kChunk; ++i) Io<DT>::st(to + i * 128, __uint_as_float(v[i]));
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < 4; b += 2) {
+              uint32_t w[4];
+#pragma unroll
+              for (int m = 0; m < 4; ++m) {
+                const int i = 4 * (b + m / 2) + 2 * (m % 2);
+                w[m] = Io<DT>::pair(__uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1]));
+              }
+              const int row = 8 * (b + lane / 16) + lane % 8, feature = quarter * 32 + 16 * h + lane / 8 % 2 * 8;
+              store_transposed(smem_u32(at + row * kPitch + feature * 2), w[0], w[1], w[2], w[3]);
+            }
           out_sync(set);
           const int r = 8 * quarter + lane / 16, x = lane % 16 * 8;
           uint16_t* row = out - quarter * 32 - lane + x + r * g.ldo;
 #pragma unroll
           for (int i = 0; i < 8; i += 2, row += 2 * g.ldo)
             if (r + i < n && f - quarter * 32 - lane + x < g.F)
-              *reinterpret_cast<uint4*>(row) = *reinterpret_cast<const uint4*>(at + (r + i) * 256 + x * 2);
+              *reinterpret_cast<uint4*>(row) = *reinterpret_cast<const uint4*>(at + (r + i) * kPitch + x * 2);
         } else {
+          uint32_t v[kChunk];
+          tmem_ld32(taddr + (uint32_t)c0, v);
+          tmem_wait_ld();
 #pragma unroll
           for (int i = 0; i < kChunk; ++i)
             if (i < n && in) Io<DT>::st(out + i * g.ldo, __uint_as_float(v[i]));
