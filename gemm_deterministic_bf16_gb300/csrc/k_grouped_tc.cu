@@ -112,25 +112,55 @@ __device__ __forceinline__ int up32(int n) { return (n + 31) & ~31; }
 // Feature tiles of all pairs of a cluster count as one.
 __device__ __forceinline__ int feature_tiles(const Args& g) { return (g.F + 256 * g.pairs - 1) / (256 * g.pairs); }
 
-// Tile `id` of a cluster as its pair `pair` takes it; e: the expert of an earlier one.
-__device__ __forceinline__ Tile tile_at(int id, int& e, const Args& g, const Tables& t, int cap, int pair) {
-  while (id >= t.pre[e + 1]) ++e;
-  Tile q;
-  q.e = e;
-  const int n = g.what == 2 ? g.N : t.cnt[e];
-  const int rt = (n + cap - 1) / cap, ft = feature_tiles(g), super = kSuper / g.pairs;
-  const int l = id - t.pre[e], sb = l / (super * rt), m = l - sb * super * rt, w = min(super, ft - sb * super);
-  const int r = m / w;
-  q.f0 = ((sb * super + m - r * w) * g.pairs + pair) * 256;
-  const int wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
-  q.r0 = r * wide;
-  q.rows = min(wide, n - q.r0);
-  q.nt = up32(q.rows);
-  const int c = g.what == 2 ? t.cnt[e] : g.C;
-  q.steps = (c + 63) / 64;
-  q.last = c - (q.steps - 1) * 64;
-  return q;
+// l / d by m = (2^32 - 1) / d, for l < 2^31: the estimate is at most one short.
+__device__ __forceinline__ int quotient(int l, int d, uint32_t m) {
+  const int q = (int)__umulhi((uint32_t)l, m);
+  return l - q * d >= d ? q + 1 : q;
 }
+
+// The tiles of a cluster in order, as one of its pairs takes them.  What a tile's
+// place needs of divisions is kept for the expert, as all roles wait for it (dW of 16
+// experts of 94 rows, K = 1416, N = 4096: 64 us with divisions, 60 without).
+struct Walk {
+  int e = -1, next = 0;                 // expert; the first tile of the one after it
+  int first = 0, n = 0, wide = 0, steps = 0, last = 0;
+  int area = 1, log, full, left;        // tiles of kSuper features; whole ones of them, features of the last
+  uint32_t by_area = 0, by_left;
+  __device__ __forceinline__ explicit Walk(const Args& g) {
+    const int ft = feature_tiles(g);
+    log = g.pairs == 2 ? 2 : 3;
+    static_assert(kSuper == 8, "log");
+    full = ft >> log;
+    left = ft & ((1 << log) - 1);
+    by_left = 0xFFFFFFFFu / (uint32_t)max(left, 1);
+  }
+  __device__ __forceinline__ Tile at(int id, const Args& g, const Tables& t, int cap, int pair) {
+    if (id >= next) {
+      do ++e;
+      while (id >= t.pre[e + 1]);
+      next = t.pre[e + 1];
+      first = t.pre[e];
+      n = g.what == 2 ? g.N : t.cnt[e];
+      const int rt = (n + cap - 1) / cap, c = g.what == 2 ? t.cnt[e] : g.C;
+      wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
+      steps = (c + 63) / 64;
+      last = c - (steps - 1) * 64;
+      area = rt << log;
+      by_area = 0xFFFFFFFFu / (uint32_t)area;
+    }
+    const int l = id - first, sb = quotient(l, area, by_area), m = l - sb * area;
+    const int r = sb < full ? m >> log : quotient(m, left, by_left), c = m - (sb < full ? r << log : r * left);
+    Tile q;
+    q.e = e;
+    q.f0 = (((sb << log) + c) * g.pairs + pair) * 256;
+    q.r0 = r * wide;
+    q.rows = min(wide, n - q.r0);
+    q.nt = up32(q.rows);
+    q.steps = steps;
+    q.last = last;
+    return q;
+  }
+};
 
 // Four of the warps that write out (set 0 or 1).
 __device__ __forceinline__ void out_sync(int set) { asm volatile("bar.sync %0, 128;" ::"r"(set + 1) : "memory"); }
@@ -273,10 +303,10 @@ __global__ void __launch_bounds__(kMostThreads, 1)
   if (warp == 0) {
     // ---------------- loads ----------------
     Ring rs;
-    int e = 0;
+    Walk walk(g);
     bool ok = true;
     for (int id = cluster; id < total && ok; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cap, mypair);
+      const Tile q = walk.at(id, g, t, cap, mypair);
       const int half = q.nt / 2, beg = t.beg[q.e];
       const int fa = q.f0 + (int)rank * 128;
       const int nb = up32(half);   // rows of B, by boxes of 128, or of 64 and 32 (dW: features by boxes of 64)
@@ -328,14 +358,14 @@ __global__ void __launch_bounds__(kMostThreads, 1)
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issue, for both CTAs ----------------
     Ring rs, rb;
-    int e = 0;
+    Walk walk(g);
     bool ok = true;
     const uint16_t all = g.pairs == 2 ? 15 : 3, mine = (uint16_t)(3u << lead);
     const uint32_t base = (1u << 4) | (DT == DETFFN_BF16 ? (1u << 7) | (1u << 10) : 0u) | (16u << 24) |
                           (g.what != 0 ? kIdescTransA : 0u) | (g.what == 2 ? kIdescTransB : 0u);
     const uint32_t astep = g.what != 0 ? 128u : 2u, bstep = g.what == 2 ? 128u : 2u;
     for (int id = cluster; id < total && ok; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cap, mypair);
+      const Tile q = walk.at(id, g, t, cap, mypair);
       if (q.steps == 0) continue;
       ok = wait_pair(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
       if (!ok) break;
@@ -368,10 +398,10 @@ __global__ void __launch_bounds__(kMostThreads, 1)
   } else if (warp == 2 && g.what == 2) {
     // ---------------- rows beyond an expert's last, cleared ----------------
     Ring rs;
-    int e = 0;
+    Walk walk(g);
     uint32_t used = 0;   // parity of each stage's tail barrier
     for (int id = cluster; id < total; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cap, mypair);
+      const Tile q = walk.at(id, g, t, cap, mypair);
       if (q.steps == 0 || (q.last & 15) == 0) {
         rs.adv(q.steps, kStages);
         continue;
@@ -395,9 +425,9 @@ __global__ void __launch_bounds__(kMostThreads, 1)
     const int quarter = warp & 3, set = warp / 8;   // lanes of tensor memory; which chunks
     unsigned char* at = staged + set * kChunk * kPitch;
     Ring rb;
-    int e = 0;
+    Walk walk(g);
     for (int id = cluster; id < total; id += clusters) {
-      const Tile q = tile_at(id, e, g, t, cap, mypair);
+      const Tile q = walk.at(id, g, t, cap, mypair);
       const int f = q.f0 + (int)rank * 128 + quarter * 32 + lane;
       uint16_t* out = g.out + (g.what == 2 ? q.e * g.stride + q.r0 * g.ldo : (t.beg[q.e] + (long long)q.r0) * g.ldo) + f;
       const bool in = f < g.F;
@@ -425,7 +455,7 @@ __global__ void __launch_bounds__(kMostThreads, 1)
           // [row][feature], and out in vectors, two rows of 128 features to a
           // store, where element by element from the registers a tile's 65536
           // results take 1024 stores of 64 bytes of each CTA (dW of 16 experts of
-          // 94 rows, K = 1416, N = 4096: 92 and %%% us).  Longer ones lose more to
+          // 94 rows, K = 1416, N = 4096: 92 and 60 us).  Longer ones lose more to
           // the shared memory that the MMAs read meanwhile (16384 rows, K = 4096, N
           // = 1536, forward and backward: 518 and 549 us).  A bulk copy for each row
           // takes some 100 cycles: 267 us of the first.
