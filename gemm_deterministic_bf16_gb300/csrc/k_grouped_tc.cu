@@ -15,7 +15,7 @@
 // MMAs cover its rows, not 256.  Operands that run across the contraction in
 // memory (W for dx, x and dout for dW) are read MN-major, without a copy.
 //
-// Each CTA of a pair loads its 128 rows of A and half of B by TMA, 64 of the
+// Each CTA of a pair loads its 128 rows of A and half of B by TMA, 128 of the
 // contraction to a stage, counted by barriers of the first CTA, which issues the
 // MMAs of both; FP32 sums in two halves of tensor memory, so that the next
 // tile's MMAs run while four warps of each CTA (eight, where
@@ -48,9 +48,11 @@ namespace {
 
 constexpr int kThreads = 256;       // warp 0 loads, 1 issues MMAs, 2 clears, 3 cuts the rows into tiles, 4-7 write out
 constexpr int kMostThreads = 384;   // and 8-11 too
-constexpr int kStages = 6;
-constexpr int kHalf = 128 * 128;    // bytes of an operand's part of a stage: 128 x 64
-constexpr int kStage = 2 * kHalf;
+constexpr int kStages = 3;
+constexpr int kHalf = 128 * 128;    // bytes of an operand's part of a slice of 64 of the contraction
+constexpr int kSlice = 2 * kHalf;
+constexpr int kStep = 128;          // of the contraction to a stage: two slices
+constexpr int kStage = 2 * kSlice;
 constexpr int kCols = 256;          // columns of tensor memory to a tile's sums
 constexpr int kChunk = 32;          // output rows that are staged at once
 constexpr int kPitch = 256 + 16;    // of a staged row of 128 features: eight rows of a transposed store meet no bank twice
@@ -143,8 +145,8 @@ struct Walk {
       n = g.what == 2 ? g.N : t.cnt[e];
       const int rt = (n + cap - 1) / cap, c = g.what == 2 ? t.cnt[e] : g.C;
       wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
-      steps = (c + 63) / 64;
-      last = c - (steps - 1) * 64;
+      steps = (c + kStep - 1) / kStep;
+      last = c - (steps - 1) * kStep;
       area = rt << log;
       by_area = 0xFFFFFFFFu / (uint32_t)area;
     }
@@ -310,44 +312,48 @@ __global__ void __launch_bounds__(kMostThreads, 1)
       const int half = q.nt / 2, beg = t.beg[q.e];
       const int fa = q.f0 + (int)rank * 128;
       const int nb = up32(half);   // rows of B, by boxes of 128, or of 64 and 32 (dW: features by boxes of 64)
-      const uint32_t bytes = kHalf + (g.what == 2 ? (uint32_t)(half + 63) / 64 * 8192u : (uint32_t)nb * 128u);
+      const uint32_t slice = kHalf + (g.what == 2 ? (uint32_t)(half + 63) / 64 * 8192u : (uint32_t)nb * 128u);
       for (int ks = 0; ks < q.steps; ++ks, rs.next(kStages)) {
         ok = wait_pair(&bars->empty[rs.slot], rs.phase ^ 1u, ab);
         if (!ok) break;
         if (g.stall) continue;
         if (lane == 0) {
           const bool clear = g.what == 2 && ks == q.steps - 1 && (q.last & 15) != 0;
-          unsigned char* a = smem + rs.slot * kStage;
-          unsigned char* b = a + kHalf;
+          const int slices = ks == q.steps - 1 && q.last <= 64 ? 1 : 2;
           const uint32_t bar = clear ? cluster_addr(&bars->tail[rs.slot], crank) : cluster_addr(&bars->full[rs.slot], lead);
-          cluster_arrive_expect_tx(bar, bytes);
-          if (g.what == 0) {
-            pair_load_3d(a, &mA, ks * 64, fa, q.e, bar);
-          } else if (g.what == 1) {
-            pair_load_3d(a, &mA, fa, ks * 64, q.e, bar);
-            pair_load_3d(a + 8192, &mA, fa + 64, ks * 64, q.e, bar);
-          } else {
-            pair_load_2d(a, &mA, fa, beg + ks * 64, bar);
-            pair_load_2d(a + 8192, &mA, fa + 64, beg + ks * 64, bar);
-          }
-          // B, for all pairs or (a stage that is cleared, one pair) for this CTA alone.
           const bool shared = g.pairs == 2 && !clear;
-          if (!shared || (ks & 1) == mypair) {
-            const uint16_t mask = (uint16_t)(5u << rank);
+          const uint16_t mask = (uint16_t)(5u << rank);
+          cluster_arrive_expect_tx(bar, slices * slice);
+          for (int sl = 0; sl < slices; ++sl) {
+            unsigned char* a = smem + rs.slot * kStage + sl * kSlice;
+            unsigned char* b = a + kHalf;
+            const int k = ks * kStep + sl * 64;
+            if (g.what == 0) {
+              pair_load_3d(a, &mA, k, fa, q.e, bar);
+            } else if (g.what == 1) {
+              pair_load_3d(a, &mA, fa, k, q.e, bar);
+              pair_load_3d(a + 8192, &mA, fa + 64, k, q.e, bar);
+            } else {
+              pair_load_2d(a, &mA, fa, beg + k, bar);
+              pair_load_2d(a + 8192, &mA, fa + 64, beg + k, bar);
+            }
+            // B, for all pairs (a slice each) or (a stage that is cleared, one pair) for this CTA alone.
+            if (shared && sl != mypair && slices == 2) continue;
+            if (shared && slices == 1 && mypair != 0) continue;
             auto load = [&](unsigned char* to, const CUtensorMap* map, int x, int y) {
               if (shared) pair_load_2d_multicast(to, map, x, y, bar, mask);
               else pair_load_2d(to, map, x, y, bar);
             };
             if (g.what == 2) {
-              load(b, &mB, q.r0 + (int)rank * half, beg + ks * 64);
-              if (half > 64) load(b + 8192, &mB, q.r0 + (int)rank * half + 64, beg + ks * 64);
+              load(b, &mB, q.r0 + (int)rank * half, beg + k);
+              if (half > 64) load(b + 8192, &mB, q.r0 + (int)rank * half + 64, beg + k);
             } else {
               const int y = beg + q.r0 + (int)rank * half;
               if (nb == 128) {
-                load(b, &mB, ks * 64, y);
+                load(b, &mB, k, y);
               } else {
-                if (nb >= 64) load(b, &mB64, ks * 64, y);
-                if (nb & 32) load(b + (nb & 64) * 128, &mB32, ks * 64, y + (nb & 64));
+                if (nb >= 64) load(b, &mB64, k, y);
+                if (nb & 32) load(b + (nb & 64) * 128, &mB32, k, y + (nb & 64));
               }
             }
           }
@@ -377,12 +383,14 @@ __global__ void __launch_bounds__(kMostThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (elect_one()) {
-          unsigned char* a = smem + rs.slot * kStage;
-          const uint64_t da = g.what != 0 ? smem_desc_sw128_mn(a) : smem_desc_sw128(a);
-          const uint64_t db = g.what == 2 ? smem_desc_sw128_mn(a + kHalf) : smem_desc_sw128(a + kHalf);
-          const int n = ks == q.steps - 1 ? (q.last + 15) / 16 : 4;
-          for (int kk = 0; kk < n; ++kk)
-            pair_mma_f16(acc, da + (uint64_t)(astep * kk), db + (uint64_t)(bstep * kk), idesc, ks > 0 || kk > 0 ? 1u : 0u);
+          const int n = ks == q.steps - 1 ? (q.last + 15) / 16 : kStep / 16;
+          for (int k0 = 0; k0 < n; k0 += 4) {
+            unsigned char* a = smem + rs.slot * kStage + k0 / 4 * kSlice;
+            const uint64_t da = g.what != 0 ? smem_desc_sw128_mn(a) : smem_desc_sw128(a);
+            const uint64_t db = g.what == 2 ? smem_desc_sw128_mn(a + kHalf) : smem_desc_sw128(a + kHalf);
+            for (int kk = 0; kk < 4 && k0 + kk < n; ++kk)
+              pair_mma_f16(acc, da + (uint64_t)(astep * kk), db + (uint64_t)(bstep * kk), idesc, ks + k0 + kk > 0 ? 1u : 0u);
+          }
           pair_commit(&bars->empty[rs.slot], all);
           if (ks == q.steps - 1) pair_commit(&bars->accf[rb.slot], mine);
         }
@@ -409,8 +417,9 @@ __global__ void __launch_bounds__(kMostThreads, 1)
       rs.adv(q.steps - 1, kStages);
       if (!wait_pair(&bars->tail[rs.slot], used >> rs.slot & 1u, ab)) break;
       used ^= 1u << rs.slot;
-      const int from = q.last * 128, to = (q.last + 15) / 16 * 2048, boxes = 2 + (q.nt / 2 + 63) / 64;
-      unsigned char* a = smem + rs.slot * kStage;
+      const int in = q.last % 64;   // rows of the last slice (not 0: a whole one needs no clearing)
+      const int from = in * 128, to = (in + 15) / 16 * 2048, boxes = 2 + (q.nt / 2 + 63) / 64;
+      unsigned char* a = smem + rs.slot * kStage + q.last / 64 * kSlice;
       for (int i = 0; i < boxes; ++i)
         for (int o = from + lane * 16; o < to; o += 512)
           *reinterpret_cast<uint4*>(a + i * 8192 + o) = make_uint4(0, 0, 0, 0);
@@ -450,7 +459,7 @@ __global__ void __launch_bounds__(kMostThreads, 1)
       out += set * kChunk * g.ldo;
       for (int c0 = set * kChunk; c0 < q.rows; c0 += g.sets * kChunk) {
         const int n = min(q.rows - c0, kChunk);
-        if (g.vec && q.steps <= 4) {
+        if (g.vec && q.steps <= 2) {
           // A short contraction is bound by what follows it: through shared memory,
           // [row][feature], and out in vectors, two rows of 128 features to a
           // store, where element by element from the registers a tile's 65536
