@@ -459,14 +459,12 @@ __global__ void __launch_bounds__(kMostThreads, 1)
       out += set * kChunk * g.ldo;
       for (int c0 = set * kChunk; c0 < q.rows; c0 += g.sets * kChunk) {
         const int n = min(q.rows - c0, kChunk);
-        if (g.vec && q.steps <= 2) {
-          // A short contraction is bound by what follows it: through shared memory,
-          // [row][feature], and out in vectors, two rows of 128 features to a
-          // store, where element by element from the registers a tile's 65536
-          // results take 1024 stores of 64 bytes of each CTA (dW of 16 experts of
-          // 94 rows, K = 1416, N = 4096: 92 and 60 us).  Longer ones lose more to
-          // the shared memory that the MMAs read meanwhile (16384 rows, K = 4096, N
-          // = 1536, forward and backward: 518 and 549 us).  A bulk copy for each row
+        if (g.vec) {
+          // Through shared memory, [row][feature], by transposed matrix stores, and out
+          // in vectors, two rows of 128 features to a store; element by element from
+          // the registers a tile's 65536 results take 1024 stores of 64 bytes of each
+          // CTA (dW of 16 experts of 94 rows, K = 1416, N = 4096: 92 and 59 us; 16384
+          // rows of 16, K = 4096, N = 1536: 153 and 145 us).  A bulk copy for each row
           // takes some 100 cycles: 267 us of the first.
           uint32_t v[2][16];
           tmem_ld_frag(taddr + (uint32_t)c0, v[0]);
