@@ -231,10 +231,20 @@ cudaError_t run(const GroupedArgs& a, int sm_count, cudaStream_t st) {
     return (WHAT == Grouped::kWeight ? a.E * ((a.N + T - 1) / T) : a.R / T + a.E) * ((J + T - 1) / T);
   };
   const bool small = tiles(128) < 2ll * sm_count || (WHAT != Grouped::kWeight && a.R <= 64ll * a.E);
-  const long long slots = 2ll * sm_count, n = most(small ? 64 : 128);
+  // With no more small tiles than SMs, shared memory that is not used keeps two CTAs
+  // from one SM while others have none (777 rows of 5 experts, K = 1031, N = 515: 62
+  // and 44 us).
+  const bool lone = small && tiles(64) <= sm_count;
+  const long long slots = (lone ? 1ll : 2ll) * sm_count, n = most(small ? 64 : 128);
   const dim3 grid((unsigned)(n < slots ? n : slots));
-  return small ? launch_dependent(k_grouped<DT, WHAT, 64>, grid, kThreads, 0, st, a)
-               : launch_dependent(k_grouped<DT, WHAT, 128>, grid, kThreads, 0, st, a);
+  if (!small) return launch_dependent(k_grouped<DT, WHAT, 128>, grid, kThreads, 0, st, a);
+  static PerDevice ready;
+  constexpr int kUnused = 100 * 1024;
+  const cudaError_t e = once_per_device(ready, [] {
+    return cudaFuncSetAttribute(k_grouped<DT, WHAT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUnused);
+  });
+  if (e != cudaSuccess) return e;
+  return launch_dependent(k_grouped<DT, WHAT, 64>, grid, kThreads, lone ? kUnused : 0, st, a);
 }
 
 template <int DT>
