@@ -424,16 +424,21 @@ __global__ void __launch_bounds__(kWarps * 32, MT * NT <= 2 ? 3 : MT * NT <= 4 ?
 template <bool BF, int MT, int NT, bool GATED, int GROUP>
 cudaError_t run_one(const W4Args& a, int sm_count, cudaStream_t st) {
   constexpr int ROWS = GATED ? 8 * MT : 16 * MT, SM = MT * NT <= 2 ? 3 : MT * NT <= 4 ? 2 : 1;
+  // Where one or two tiles an SM are all there are, more shared memory than is used
+  // keeps more CTAs than that from one SM while others have fewer (N = 4096, K = 12288,
+  // one token: 12.1 and 9.5 us).
+  constexpr int kAlone = 120 * 1024, kTwo = 80 * 1024, kUsed = (int)sizeof(Smem<MT, NT>);
   static PerDevice ready;
   const cudaError_t e = once_per_device(ready, [] {
     return cudaFuncSetAttribute(k_w4<BF, MT, NT, GATED, GROUP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)sizeof(Smem<MT, NT>));
+                                kUsed > kAlone ? kUsed : kAlone);
   });
   if (e != cudaSuccess) return e;
   const int tok = 8 * NT / a.x.terms, passes = (a.T + tok - 1) / tok;
-  const long long tiles = (a.w.N + ROWS - 1) / ROWS, slots = (long long)SM * sm_count;
+  const long long tiles = (a.w.N + ROWS - 1) / ROWS, slots = (long long)SM * sm_count, ctas = (tiles < slots ? tiles : slots) * passes;
+  const int least = ctas <= sm_count ? kAlone : ctas <= 2ll * sm_count ? kTwo : 0;
   return launch_dependent(k_w4<BF, MT, NT, GATED, GROUP>, dim3((unsigned)(tiles < slots ? tiles : slots), (unsigned)passes),
-                          kWarps * 32, (int)sizeof(Smem<MT, NT>), st, a);
+                          kWarps * 32, kUsed > least ? kUsed : least, st, a);
 }
 template <bool BF, int MT, int NT, bool GATED>
 cudaError_t run_group(const W4Args& a, int sm_count, cudaStream_t st) {
