@@ -12,6 +12,11 @@
 //
 // A word is 32 bits, so p is met to 2^-32.  The product x * scale and the sum
 // are FP32, rounded once to the stored type.
+//
+// The ten rounds bind it where bytes are few: 20 wide multiplications and 20 logic
+// operations for four elements keep the pipes that issue one in two cycles at 40 and 64 %
+// (16384 x 4096 BF16: 62 us without a residual, 65 % of the copy rate; 70 with one, 86 %;
+// FP32 89 us, 90 %; rows of 4095 94 us, element by element).
 #include "dropout.h"
 #include "elt.cuh"
 

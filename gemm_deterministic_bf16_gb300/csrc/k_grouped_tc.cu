@@ -31,11 +31,22 @@
 // widest tile) is the one whose rounds of tiles, each at the cost of its widest
 // tile, take least.
 //
-// At the MMA's full rate an SM takes in 64 bytes a cycle from L2, which is more
-// than it gets: without loads 16384 x 4096 x 4096 run at 1822 TFLOP/s, with A's
-// alone at 1740, with both at 1407 (each on one box).  So clusters of two pairs
-// take the same rows and neighbouring features: B is loaded once for both, in
-// turn by the one pair and the other, and multicast.
+// What bounds it: at the MMA's full rate an SM takes in 64 bytes a cycle from L2, and
+// its shared memory is read and written by 128.  Without loads 16384 x 4096 x 4096 run at
+// 1822 TFLOP/s, with A's alone at 1740, with both at 1407 (stages of 64).  So clusters
+// of two pairs take the same rows and neighbouring features: B is loaded once for
+// both, half a stage by each pair, and multicast (148 us for 16384 rows of 16 experts,
+// K = 4096, N = 1536, 165 without).  A stage holds 128 of the contraction, as a wait and
+// a commit for every 64 cost the issuing thread what their MMAs take (352 us for 16384 x
+// 4096 x 4096, 322 with 128).  More stages in flight, and prefetches into L2 ahead of
+// them, gain nothing or cost half the rate.
+//
+// BF16, 16384 x 4096 x 4096: 315 us forward, 319 dx, 364 dW (92, 91 and 79 % of the
+// measured matrix rate); 16384 uneven rows of 16 experts, K = 4096, N = 1536: 155 us forward, 333 both
+// gradients (70 and 65 %: five to six rounds of tiles on 36 clusters, the last in part
+// empty); 99 rows of 64 experts, K = 2048, N = 768: 34.5 us (66 % of the copy rate); 1499
+// rows of 16 experts, K = 1416, N = 4096, FP16: 120 us (both gradients; 48 % of the copy
+// rate: two rounds for dx, the results' way out for dW).
 #include <atomic>
 
 #include "elt.cuh"

@@ -487,16 +487,19 @@ DETFFN_API detffn_status detffn_moe_forward(detffn_handle h, const void* x, cons
  * and of out and dOut [R, N] (row strides ldx, ... in elements):
  *   out[r]  = W[e] x[r]
  *   dX[r]   = W[e]^T dOut[r]
- *   dW[e]   = sum over the expert's rows r, ascending, of dOut[r] x[r]^T   (0 where it has none)
- * of `dtype`, every sum FP32 and rounded once; dX or dW NULL: not formed (x, or
- * W, may then be NULL).  `offsets` are E + 1 ascending ints on the device, read
+ *   dW[e]   = sum over the expert's rows r of dOut[r] x[r]^T   (0 where it has none)
+ * of `dtype`, every sum FP32 and rounded once; dX or dW NULL: not formed (W, or
+ * x, may then be NULL).  The same call gives the same bits; on the tensor cores a
+ * row's out and dX do not depend on the other rows (on the CUDA cores the order of
+ * a sum follows from the sizes).  `offsets` are E + 1 ascending ints on the device, read
  * there: no host waits for them.  They may begin after row 0 and end before row
  * R; rows of no expert are left as they were in out and dX.  Ends beyond R are
  * taken as R, and an end before its beginning as no rows.  R < 2^31, K, N <= 65536.
  * options->path: EXACT takes the CUDA-core kernels (any sizes and types), TENSOR
- * the tensor cores (DETFFN_ERR_UNSUPPORTED where they do not cover the call).
+ * the tensor cores (FP16 and BF16, any widths; where K and N are multiples of 8, rows
+ * on 16-byte boundaries; else DETFFN_ERR_UNSUPPORTED), AUTO these where they can.
  * `ws` is of detffn_grouped_workspace_size bytes, 256-byte aligned; NULL where
- * that is 0. */
+ * that is 0 (FP32, or K and N multiples of 8). */
 DETFFN_API detffn_status detffn_grouped_workspace_size(long long R, long long E, long long K, long long N, int dtype,
                                                        size_t* bytes);
 DETFFN_API detffn_status detffn_grouped_forward(detffn_handle h, const void* x, long long ldx, const void* W,
