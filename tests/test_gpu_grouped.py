@@ -310,3 +310,33 @@ def test_addresses_beyond_32_bits(G, dtype, E):
         close(dX[a:b], d64 @ w64, d64.abs() @ w64.abs(), N, dtype)
         close(dW[e], d64.T @ x64, d64.abs().T @ x64.abs(), b - a, dtype)
     assert not bool(dW[1].any()) and not bool(dW[E - 2].any())
+
+
+def test_two_streams_at_once(G):
+    """Calls that overlap on the GPU, tensor cores and CUDA cores, share nothing."""
+    jobs = []
+    for i, (dtype, K, N) in enumerate(((torch.bfloat16, 512, 1024), (torch.float16, 1031, 260), (torch.float32, 300, 200))):
+        x, W, d, off, _ = make([300, 0, 77, 1200], K, N, dtype, seed=i)
+        jobs.append((x, W, d, off, G.detffn_grouped_forward(x, W, off), *G.detffn_grouped_backward(x, W, off, d)))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = []
+    for n in range(12):
+        x, W, d, off = jobs[n % 3][:4]
+        s = streams[n % 2]
+        got.append((n % 3, G.detffn_grouped_forward(x, W, off, stream=s), *G.detffn_grouped_backward(x, W, off, d, stream=s)))
+    torch.cuda.synchronize()
+    for j, out, dX, dW in got:
+        assert torch.equal(out, jobs[j][4]) and torch.equal(dX, jobs[j][5]) and torch.equal(dW, jobs[j][6])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+def test_a_row_does_not_depend_on_the_others(G, dtype):
+    """On the tensor cores a row has the same bits in a batch of any size, with any number of experts."""
+    x, W, d, off, ends = make([3, 700, 0, 41, 256], 1032, 520, dtype)
+    out = G.detffn_grouped_forward(x, W, off)
+    dX, _ = G.detffn_grouped_backward(x, W, off, d, need_dW=False)
+    for e, a, b in ((0, 1, 2), (1, 100, 133), (4, 744, 1000), (3, 703, 744)):
+        o = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
+        assert torch.equal(G.detffn_grouped_forward(x[a:b], W[e:e + 1], o), out[a:b])
+        assert torch.equal(G.detffn_grouped_backward(None, W[e:e + 1], o, d[a:b], need_dW=False)[0], dX[a:b])

@@ -223,3 +223,22 @@ def test_addresses_beyond_32_bits(G):
     v = torch.empty((64, K), dtype=torch.float32, device="cuda")
     last = w._replace(codes=w.codes[N - 64:], scales=w.scales[N - 64:])
     assert torch.equal(G.detffn_w4_unpack(last, out=v), values64(part).float())
+
+
+@pytest.mark.parametrize("dtype", ALL)
+def test_long_rows(G, dtype):
+    for T in (1, 9):
+        w = matrix(G, 24, 100003, 128, torch.float32)
+        x = torch.randn((T, 100003), generator=torch.Generator(device="cuda").manual_seed(T), device="cuda").to(dtype)
+        check(G.detffn_w4_matvec(x, w), x, values64(w), dtype, 100003)
+
+
+def test_two_streams_at_once(G):
+    ws = [matrix(G, 512, 256, 128, torch.bfloat16, i) for i in range(2)] + [matrix(G, 256, 512, 128, torch.bfloat16, 2)]
+    xs = [torch.randn((t, 256), device="cuda").bfloat16() for t in (1, 20)]
+    want = [G.detffn_w4_forward(x, *ws) for x in xs]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [(n % 2, G.detffn_w4_forward(xs[n % 2], *ws, stream=streams[n // 2 % 2])) for n in range(16)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, want[i]) for i, y in got)
