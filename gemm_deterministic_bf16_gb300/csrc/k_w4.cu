@@ -34,9 +34,13 @@
 // groups of 64, 78 us (floor 43); the FFN of one token, H = 4096, I = 12288, BF16, groups of
 // 128, 26.6 us (floor 11.6); one token through 4096 x 4096 4.7 us (floor 1.3).  A run of
 // 128 codes of 16 rows takes 190 to 210 instructions, of which the integer pipe, which
-// issues one in two cycles, has 72 to 83.  With more columns the legacy matrix
-// instructions bind (one in two cycles for an SM: 22 us of the 70 us of the FFN of 32
-// tokens) and the reads of x.
+// issues one in two cycles, has 72 to 83.  With more columns it is latency: in the
+// FFN of 32 tokens (70 us; 22 of them the matrix instructions', one in two cycles for an
+// SM) eight warps an SM, all that the sums leave registers for, issue in 31 % of the
+// cycles and wait for results of a fixed latency most, then for x from L2; 2.5 tiles
+// an SM and 128 CTAs leave a sixth of it idle.  Neither sixteen warps that share x in
+// shared memory (92 us), nor x in each warp's ring (96), nor four by two tiles with two
+// CTAs an SM (93) does better: all three add more instructions than they hide.
 #include <stddef.h>
 
 #include <type_traits>
