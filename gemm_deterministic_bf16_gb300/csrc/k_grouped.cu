@@ -221,6 +221,145 @@ __global__ void __launch_bounds__(kThreads, 2) k_grouped(const GroupedArgs a) {
   }
 }
 
+// out for few rows of an expert, FP32: tiles of four features by eight rows, the
+// lanes of a warp along K, so that a matrix is read once for eight rows and nothing
+// waits for the rounds of a 64 x 64 tile.  SPLIT warps share a tile's K, 128 in turn:
+// all eight of a CTA where there are fewer tiles than warps.  What bounds it is HBM up
+// to eight rows (64 experts of one row, K = 2048, N = 768: 79 us, 76 % of the copy rate),
+// then the reads of x from L1, twice the matrix's.
+// VEC: rows of W and x lie on 16-byte boundaries.
+constexpr int kFewRows = 8, kFewFeatures = 4;
+
+template <bool VEC>
+__device__ __forceinline__ void few_load(const float* p, int left, int lane, float (&v)[4]) {   // left: of the row from p on
+  if constexpr (VEC) {
+    const float4 q = 4 * lane < left ? __ldg(reinterpret_cast<const float4*>(p) + lane) : make_float4(0, 0, 0, 0);
+    v[0] = q.x, v[1] = q.y, v[2] = q.z, v[3] = q.w;
+  } else {
+#pragma unroll
+    for (int u = 0; u < 4; ++u) v[u] = lane + 32 * u < left ? __ldg(p + lane + 32 * u) : 0.0f;
+  }
+}
+
+// Sums of features f .. f + 3 by ROWS rows at x over this warp's part of K; the lanes
+// of feature i and row r, lane / (8 / ROWS) = ROWS * i + r, have its sum.
+template <int ROWS, int SPLIT, bool VEC>
+__device__ __forceinline__ float few_sums(const float* const (&w)[kFewFeatures], const float* x, long long ldx, int rows, int K,
+                                          int part, int lane) {
+  constexpr int F = kFewFeatures, STEP = 128 * SPLIT;
+  float v[F * ROWS];
+#pragma unroll
+  for (int i = 0; i < F * ROWS; ++i) v[i] = 0.0f;
+  float next[F][4];
+  int c = 128 * part;
+#pragma unroll
+  for (int i = 0; i < F; ++i) few_load<VEC>(w[i] + c, K - c, lane, next[i]);
+  for (; c < K; c += STEP) {
+    float now[F][4];
+#pragma unroll
+    for (int i = 0; i < F; ++i)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) now[i][u] = next[i][u];
+    if (c + STEP < K) {
+#pragma unroll
+      for (int i = 0; i < F; ++i) few_load<VEC>(w[i] + c + STEP, K - c - STEP, lane, next[i]);
+    }
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      float y[4];
+      few_load<VEC>(x + min(r, rows - 1) * ldx + c, K - c, lane, y);   // (a row past the last: its sum is not used)
+#pragma unroll
+      for (int i = 0; i < F; ++i)
+#pragma unroll
+        for (int u = 0; u < 4; ++u) v[ROWS * i + r] = fmaf(now[i][u], y[u], v[ROWS * i + r]);
+    }
+  }
+  // Half of the sums to each half of the lanes, while there are any to halve.
+  int n = F * ROWS;
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    if (n > 1) {
+      n /= 2;
+#pragma unroll
+      for (int j = 0; j < F * ROWS / 2; ++j)
+        if (j < n) {
+          const bool up = (lane & d) != 0;
+          const float keep = up ? v[j + n] : v[j], send = up ? v[j] : v[j + n];
+          v[j] = keep + __shfl_xor_sync(0xffffffffu, send, d);
+        }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], d);
+    }
+  }
+  return v[0];
+}
+
+template <int SPLIT, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) k_grouped_few(const GroupedArgs a) {
+  constexpr int WARPS = kThreads / 32, F = kFewFeatures;
+  static_assert(SPLIT == 1 || SPLIT == WARPS, "a tile to a warp, or to a CTA");
+  __shared__ float red[2][WARPS][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = SPLIT == 1 ? 0 : warp, K = (int)a.K;
+  const long long teams = SPLIT == 1 ? (long long)gridDim.x * WARPS : gridDim.x, groups = (a.N + F - 1) / F;
+  grid_dep_wait();
+  grid_dep_launch();
+  long long next = SPLIT == 1 ? (long long)blockIdx.x * WARPS + warp : blockIdx.x, first = 0;
+  int buf = 0;
+  for (int e0 = 0; e0 < a.E; e0 += 32) {   // an expert to a lane
+    long long b = 0, n = 0;
+    if (e0 + lane < a.E) {   // (rows out of the tensors, or before the expert's first, are none of its)
+      b = min(max((long long)__ldg(a.off + e0 + lane), 0ll), a.R);
+      n = max(min((long long)__ldg(a.off + e0 + lane + 1), a.R) - b, 0ll);
+    }
+    const long long tiles = (n + kFewRows - 1) / kFewRows * groups;
+    long long end = tiles;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, end, d);
+      if (lane >= d) end += v;
+    }
+    end += first;
+    first = __shfl_sync(0xffffffffu, end, 31);
+    for (; next < first; next += teams) {
+      const int owner = __popc(__ballot_sync(0xffffffffu, end <= next));
+      const long long tile = next - __shfl_sync(0xffffffffu, end - tiles, owner), chunk = tile / groups;
+      const long long f = (tile - chunk * groups) * F, r0 = __shfl_sync(0xffffffffu, b, owner) + chunk * kFewRows;
+      const int rows = (int)min((long long)kFewRows, __shfl_sync(0xffffffffu, n, owner) - chunk * kFewRows);
+      const float* w[F];
+#pragma unroll
+      for (int i = 0; i < F; ++i) w[i] = static_cast<const float*>(a.W) + ((e0 + owner) * a.N + min(f + i, a.N - 1)) * a.K;
+      const float* x = static_cast<const float*>(a.x.p) + r0 * a.x.ld;
+      const bool pair = rows <= 2;
+      float v = pair ? few_sums<2, SPLIT, VEC>(w, x, a.x.ld, rows, K, part, lane)
+                     : few_sums<kFewRows, SPLIT, VEC>(w, x, a.x.ld, rows, K, part, lane);
+      if constexpr (SPLIT > 1) {   // the warps' sums, in order
+        red[buf][warp][lane] = v;
+        __syncthreads();   // (one a tile: the other buffer's reader is past it when it is written again)
+        if (warp == 0) {
+          v = 0.0f;
+#pragma unroll
+          for (int k = 0; k < WARPS; ++k) v += red[buf][k][lane];
+        }
+        buf ^= 1;
+        if (warp != 0) continue;
+      }
+      const int at = pair ? lane / 4 : lane, i = pair ? at / 2 : at / kFewRows, r = pair ? at % 2 : at % kFewRows;
+      if ((!pair || lane % 4 == 0) && r < rows && f + i < a.N)
+        static_cast<float*>(const_cast<void*>(a.out.p))[(r0 + r) * a.out.ld + f + i] = v;
+    }
+  }
+}
+
+cudaError_t run_few(const GroupedArgs& a, int sm_count, cudaStream_t st) {
+  const bool vec = a.K % 4 == 0 && (uintptr_t)a.W % 16 == 0 && (uintptr_t)a.x.p % 16 == 0 && (a.R <= 1 || a.x.ld % 4 == 0);
+  const long long groups = (a.N + kFewFeatures - 1) / kFewFeatures, tiles = (a.R < a.E ? a.R : a.E) * groups,
+                  warps = 2ll * sm_count * (kThreads / 32);
+  const dim3 grid(2 * sm_count);
+  if (tiles < warps)
+    return vec ? launch_dependent(k_grouped_few<8, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few<8, false>, grid, kThreads, 0, st, a);
+  return vec ? launch_dependent(k_grouped_few<1, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few<1, false>, grid, kThreads, 0, st, a);
+}
+
 template <int DT, Grouped WHAT>
 cudaError_t run(const GroupedArgs& a, int sm_count, cudaStream_t st) {
   const long long J = WHAT == Grouped::kForward ? a.N : a.K;
@@ -294,6 +433,12 @@ cudaError_t launch_grouped_rows(const Rows& from, long long rows, long long widt
 }
 
 cudaError_t launch_grouped_general(const GroupedArgs& a, Grouped what, int sm_count, cudaStream_t st) {
+  // Tiles of 64 x 64 take what K's rounds of loads do however few rows there are: 64
+  // experts, K = 2048, N = 768, 1, 8, 16 and 32 rows of each: 411, 413, 413 and 414 us,
+  // and 79, 121, 216 and 413 by rows of eight; one expert of 32, 64 and 128 rows, K = 1024,
+  // N = 512: 47, 34 and 34 us, and 6.4, 9.9 and 16.
+  if (a.dtype == DETFFN_F32 && what == Grouped::kForward && (a.R <= 16ll * a.E || a.R * a.N <= 1 << 17))
+    return run_few(a, sm_count, st);
   if (a.dtype == DETFFN_F32) return run<DETFFN_F32>(a, what, sm_count, st);
   if (a.dtype == DETFFN_F16) return run<DETFFN_F16>(a, what, sm_count, st);
   return run<DETFFN_BF16>(a, what, sm_count, st);

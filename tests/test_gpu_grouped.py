@@ -340,3 +340,56 @@ def test_a_row_does_not_depend_on_the_others(G, dtype):
         o = torch.tensor([0, b - a], dtype=torch.int32, device="cuda")
         assert torch.equal(G.detffn_grouped_forward(x[a:b], W[e:e + 1], o), out[a:b])
         assert torch.equal(G.detffn_grouped_backward(None, W[e:e + 1], o, d[a:b], need_dW=False)[0], dX[a:b])
+
+
+FEW = [[1], [2], [3], [8], [9], [1] * 40, [0, 7, 0, 16, 2, 8, 1], [0] * 33 + [5, 0, 11], [40, 0, 0, 0]]
+
+
+@pytest.mark.parametrize("K,N", [(1, 1), (4, 3), (124, 6), (128, 5), (132, 64), (131, 33), (1031, 130), (2056, 83), (1160, 1028)])
+@pytest.mark.parametrize("sizes", FEW, ids=lambda s: "-".join(map(str, s[:5])))
+def test_few_rows_in_32_bits(G, sizes, K, N):
+    """Up to eight rows of an expert at a time; an expert's row of each length, whole and cut runs of K."""
+    out, dX, _ = run(G, sizes, K, N, torch.float32, seed=K + 7 * N, first=2, behind=3)
+    again, dX2, _ = run(G, sizes, K, N, torch.float32, seed=K + 7 * N, first=2, behind=3)
+    a, b = 2, 2 + sum(sizes)
+    assert torch.equal(out[a:b], again[a:b]) and torch.equal(dX[a:b], dX2[a:b])
+
+
+@pytest.mark.parametrize("per", [15, 16, 17, 64, 65])
+@pytest.mark.parametrize("N", [512, 2048])
+def test_where_few_rows_end(G, per, N):
+    run(G, [per, 0, 2 * per, per], 264, N, torch.float32, seed=per)
+
+
+@pytest.mark.parametrize("K,N,ld,shift", [(132, 64, 136, 0), (132, 64, 133, 0), (132, 64, 132, 1), (130, 66, 140, 2)])
+def test_few_rows_where_they_lie(G, K, N, ld, shift):
+    """Rows on and off 16-byte boundaries, and others' values that are not finite beside them."""
+    x, W, d, off, ends = make([3, 0, 9, 1], K, N, torch.float32, seed=5)
+    R = x.shape[0]
+    bad = torch.full((R * ld + shift + 8,), float("nan"), device="cuda")
+    xs = bad[shift:shift + R * ld].view(R, ld)[:, :K]
+    xs.copy_(x)
+    ldd = N + ld - K
+    other = torch.full((R * ldd + shift + 8,), float("nan"), device="cuda")
+    ds = other[shift:shift + R * ldd].view(R, ldd)[:, :N]
+    ds.copy_(d)
+    out = torch.full((R, N + 3), 7.0, device="cuda")
+    G.detffn_grouped_forward(xs, W, off, out=out[:, :N])
+    check_forward(G, x, W, off, ends, out[:, :N], out[:, :N])
+    assert bool((out[:, N:] == 7.0).all())
+    dX = torch.full((R, K + 5), 7.0, device="cuda")
+    _, dW = G.detffn_grouped_backward(xs, W, off, ds, dX=dX[:, :K])
+    check_backward(G, x, W, d, ends, dX[:, :K], dW, dX[:, :K])
+    assert bool((dX[:, K:] == 7.0).all())
+
+
+def test_few_rows_keep_what_is_not_finite_to_themselves(G):
+    x, W, d, off, ends = make([1, 4, 0, 11], 200, 60, torch.float32, seed=6)
+    clean = G.detffn_grouped_forward(x, W, off)
+    gone = G.detffn_grouped_backward(x, W, off, d, need_dW=False)[0]
+    y, e = x.clone(), d.clone()
+    y[2, 5], y[7, 199], e[2, 5], e[7, 59] = float("nan"), float("inf"), float("nan"), float("inf")
+    out, dX = G.detffn_grouped_forward(y, W, off), G.detffn_grouped_backward(y, W, off, e, need_dW=False)[0]
+    rows = [i for i in range(16) if i not in (2, 7)]
+    assert torch.equal(out[rows], clean[rows]) and torch.equal(dX[rows], gone[rows])
+    assert not bool(out[[2, 7]].isfinite().any()) and not bool(dX[[2, 7]].isfinite().any())
