@@ -7,12 +7,15 @@
 //
 // All three are D[i, j] = sum_c A(i, c) B(j, c), where A and B run along c or
 // across it in memory.  A CTA takes one tile of an expert after another; the
-// experts' rows are read on the device, so no host needs to know them.  What bounds it is the FP32 multiply-add rate: a thread of a 128 x 128
-// tile holds 8 x 8 sums and reads 16 values of shared memory for each step of c,
+// experts' rows are read on the device, so no host needs to know them.  What bounds
+// it is the FP32 multiply-add rate: a thread of a 128 x 128 tile holds 8 x 8 sums and reads 16 values of shared memory for each step of c,
 // and the two FP32 multiply-adds of fma.rn.f32x2 share an issue slot.  Tiles are
 // 64 x 64 where larger ones would not fill the SMs twice; four sets of threads
 // then share the steps of c, for with 4 x 4 sums a thread is bound by the reads of
 // shared memory (16 experts of 16 rows, K = N = 1024, FP32: 124 us, and 75 so).
+//
+// With few rows of an expert in FP32 the matrices bind, and out and dx have kernels of
+// their own that read each once for eight rows.
 //
 // FP32, 8192 rows of 8 experts, K = 2048, N = 1024: 680 us forward, 602 dx, 627 dW (51 to 57
 // TFLOP/s); 777 rows of 5 experts, K = 1031, N = 515: 44, 39 and 36 us.
@@ -24,7 +27,7 @@
 namespace detffn {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 // Steps of c to a round: more for small tiles, whose arithmetic hides less of the
 // loads for the next round.
 template <int T> constexpr int kSteps = T == 128 ? 16 : 32;
@@ -294,17 +297,12 @@ __device__ __forceinline__ float few_sums(const float* const (&w)[kFewFeatures],
   return v[0];
 }
 
-template <int SPLIT, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) k_grouped_few(const GroupedArgs a) {
-  constexpr int WARPS = kThreads / 32, F = kFewFeatures;
-  static_assert(SPLIT == 1 || SPLIT == WARPS, "a tile to a warp, or to a CTA");
-  __shared__ float red[2][WARPS][32];
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = SPLIT == 1 ? 0 : warp, K = (int)a.K;
-  const long long teams = SPLIT == 1 ? (long long)gridDim.x * WARPS : gridDim.x, groups = (a.N + F - 1) / F;
-  grid_dep_wait();
-  grid_dep_launch();
-  long long next = SPLIT == 1 ? (long long)blockIdx.x * WARPS + warp : blockIdx.x, first = 0;
-  int buf = 0;
+// f(expert, group of features, first row, rows) for tiles `next`, next + teams, ... of
+// all experts' rows by eights and `groups` groups of features.  All lanes together.
+template <class F>
+__device__ __forceinline__ void few_tiles(const GroupedArgs& a, long long groups, long long next, long long teams, F&& f) {
+  const int lane = threadIdx.x % 32;
+  long long first = 0;
   for (int e0 = 0; e0 < a.E; e0 += 32) {   // an expert to a lane
     long long b = 0, n = 0;
     if (e0 + lane < a.E) {   // (rows out of the tensors, or before the expert's first, are none of its)
@@ -323,37 +321,156 @@ __global__ void __launch_bounds__(kThreads, 2) k_grouped_few(const GroupedArgs a
     for (; next < first; next += teams) {
       const int owner = __popc(__ballot_sync(0xffffffffu, end <= next));
       const long long tile = next - __shfl_sync(0xffffffffu, end - tiles, owner), chunk = tile / groups;
-      const long long f = (tile - chunk * groups) * F, r0 = __shfl_sync(0xffffffffu, b, owner) + chunk * kFewRows;
+      const long long r0 = __shfl_sync(0xffffffffu, b, owner) + chunk * kFewRows;
       const int rows = (int)min((long long)kFewRows, __shfl_sync(0xffffffffu, n, owner) - chunk * kFewRows);
-      const float* w[F];
-#pragma unroll
-      for (int i = 0; i < F; ++i) w[i] = static_cast<const float*>(a.W) + ((e0 + owner) * a.N + min(f + i, a.N - 1)) * a.K;
-      const float* x = static_cast<const float*>(a.x.p) + r0 * a.x.ld;
-      const bool pair = rows <= 2;
-      float v = pair ? few_sums<2, SPLIT, VEC>(w, x, a.x.ld, rows, K, part, lane)
-                     : few_sums<kFewRows, SPLIT, VEC>(w, x, a.x.ld, rows, K, part, lane);
-      if constexpr (SPLIT > 1) {   // the warps' sums, in order
-        red[buf][warp][lane] = v;
-        __syncthreads();   // (one a tile: the other buffer's reader is past it when it is written again)
-        if (warp == 0) {
-          v = 0.0f;
-#pragma unroll
-          for (int k = 0; k < WARPS; ++k) v += red[buf][k][lane];
-        }
-        buf ^= 1;
-        if (warp != 0) continue;
-      }
-      const int at = pair ? lane / 4 : lane, i = pair ? at / 2 : at / kFewRows, r = pair ? at % 2 : at % kFewRows;
-      if ((!pair || lane % 4 == 0) && r < rows && f + i < a.N)
-        static_cast<float*>(const_cast<void*>(a.out.p))[(r0 + r) * a.out.ld + f + i] = v;
+      f(e0 + owner, tile - chunk * groups, r0, rows);
     }
   }
+}
+
+template <int SPLIT, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) k_grouped_few(const GroupedArgs a) {
+  constexpr int F = kFewFeatures;
+  static_assert(SPLIT == 1 || SPLIT == kWarps, "a tile to a warp, or to a CTA");
+  __shared__ float red[2][kWarps][32];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, part = SPLIT == 1 ? 0 : warp, K = (int)a.K;
+  grid_dep_wait();
+  grid_dep_launch();
+  int buf = 0;
+  auto tile = [&](int e, long long group, long long r0, int rows) {
+    const long long f = group * F;
+    const float* w[F];
+#pragma unroll
+    for (int i = 0; i < F; ++i) w[i] = static_cast<const float*>(a.W) + (e * a.N + min(f + i, a.N - 1)) * a.K;
+    const float* x = static_cast<const float*>(a.x.p) + r0 * a.x.ld;
+    const bool pair = rows <= 2;
+    float v = pair ? few_sums<2, SPLIT, VEC>(w, x, a.x.ld, rows, K, part, lane)
+                   : few_sums<kFewRows, SPLIT, VEC>(w, x, a.x.ld, rows, K, part, lane);
+    if constexpr (SPLIT > 1) {   // the warps' sums, in order
+      red[buf][warp][lane] = v;
+      __syncthreads();   // (one a tile: the other buffer's reader is past it when it is written again)
+      if (warp == 0) {
+        v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < kWarps; ++k) v += red[buf][k][lane];
+      }
+      buf ^= 1;
+      if (warp != 0) return;
+    }
+    const int at = pair ? lane / 4 : lane, i = pair ? at / 2 : at / kFewRows, r = pair ? at % 2 : at % kFewRows;
+    if ((!pair || lane % 4 == 0) && r < rows && f + i < a.N)
+      static_cast<float*>(const_cast<void*>(a.out.p))[(r0 + r) * a.out.ld + f + i] = v;
+  };
+  const long long groups = (a.N + F - 1) / F;
+  if constexpr (SPLIT == 1) few_tiles(a, groups, (long long)blockIdx.x * kWarps + warp, (long long)gridDim.x * kWarps, tile);
+  else few_tiles(a, groups, blockIdx.x, gridDim.x, tile);
+}
+
+// dx for few rows of an expert, FP32: a CTA takes tiles of eight rows by 128 columns of
+// W, four to a lane (WIDE), or 32, its warps 4 (16) rows of W in turn; dout's values are the
+// same for all lanes.  VEC: rows of dout lie on 16-byte boundaries.  Up to two rows
+// HBM bounds it (64 experts of one row, K = 2048, N = 768: 82 us, 73 % of the copy rate),
+// from there the reads of dout, a vector for 16 multiply-adds of a lane.
+template <int ROWS, bool WIDE, bool VEC>
+__device__ __forceinline__ void few_inputs(const float* W, long long ldw, int columns, const float* d, long long ldd, int rows,
+                                           int N, int warp, int lane, float* red) {
+  constexpr int STEP = WIDE ? 4 : 16, U = WIDE ? 4 : 1;   // rows of W at once; columns of a lane
+  const bool in = U * lane < columns;
+  float next[STEP][U], v[ROWS][U];
+  auto load = [&](int n) {
+#pragma unroll
+    for (int i = 0; i < STEP; ++i) {
+      const bool there = in && n + i < N;
+      const float* p = W + (n + i) * ldw + U * lane;
+      if constexpr (WIDE) {
+        const float4 q = there ? __ldg(reinterpret_cast<const float4*>(p)) : make_float4(0, 0, 0, 0);
+        next[i][0] = q.x, next[i][1] = q.y, next[i][2] = q.z, next[i][3] = q.w;
+      } else {
+        next[i][0] = there ? __ldg(p) : 0.0f;
+      }
+    }
+  };
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int u = 0; u < U; ++u) v[r][u] = 0.0f;
+  load(STEP * warp);
+  for (int n = STEP * warp; n < N; n += STEP * kWarps) {
+    float now[STEP][U];
+#pragma unroll
+    for (int i = 0; i < STEP; ++i)
+#pragma unroll
+      for (int u = 0; u < U; ++u) now[i][u] = next[i][u];
+    if (n + STEP * kWarps < N) load(n + STEP * kWarps);
+#pragma unroll
+    for (int r = 0; r < ROWS; ++r) {
+      const float* y = d + min(r, rows - 1) * ldd + n;   // (a row past the last: its sums are not used)
+#pragma unroll
+      for (int i = 0; i < STEP; i += 4) {
+        float q[4] = {};
+        if constexpr (VEC) {
+          if (n + i < N) {
+            const float4 f = __ldg(reinterpret_cast<const float4*>(y + i));
+            q[0] = f.x, q[1] = f.y, q[2] = f.z, q[3] = f.w;
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (n + i + k < N) q[k] = __ldg(y + i + k);
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int u = 0; u < U; ++u) v[r][u] = fmaf(q[k], now[i + k][u], v[r][u]);
+      }
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+    for (int u = 0; u < U; ++u) red[r * 32 * U + 32 * u + lane] = v[r][u];
+}
+
+template <bool WIDE, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) k_grouped_few_inputs(const GroupedArgs a) {
+  constexpr int U = WIDE ? 4 : 1, COLUMNS = 32 * U;
+  __shared__ float red[kWarps][kFewRows * COLUMNS];   // [row][column of the lanes][lane]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, N = (int)a.N;
+  grid_dep_wait();
+  grid_dep_launch();
+  few_tiles(a, (a.K + COLUMNS - 1) / COLUMNS, blockIdx.x, gridDim.x, [&](int e, long long group, long long r0, int rows) {
+    const long long k0 = group * COLUMNS;
+    const int columns = (int)min((long long)COLUMNS, a.K - k0);
+    const float *W = static_cast<const float*>(a.W) + e * a.N * a.K + k0,
+                *d = static_cast<const float*>(a.dout.p) + r0 * a.dout.ld;
+    __syncthreads();   // (the readers of the last tile's sums)
+    if (rows <= 2) few_inputs<2, WIDE, VEC>(W, a.K, columns, d, a.dout.ld, rows, N, warp, lane, red[warp]);
+    else few_inputs<kFewRows, WIDE, VEC>(W, a.K, columns, d, a.dout.ld, rows, N, warp, lane, red[warp]);
+    __syncthreads();
+    for (int o = threadIdx.x; o < rows * COLUMNS; o += kThreads) {   // the warps' sums, in order
+      const int r = o / COLUMNS, c = o % COLUMNS;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) v += red[w][r * COLUMNS + c % U * 32 + c / U];
+      if (c < columns) static_cast<float*>(const_cast<void*>(a.dx.p))[(r0 + r) * a.dx.ld + k0 + c] = v;
+    }
+  });
+}
+
+cudaError_t run_few_inputs(const GroupedArgs& a, int sm_count, cudaStream_t st) {
+  // Narrow tiles where wide ones leave SMs without any.
+  const bool wide = a.K % 4 == 0 && (uintptr_t)a.W % 16 == 0 && (a.R < a.E ? a.R : a.E) * ((a.K + 127) / 128) >= sm_count;
+  const bool vec = a.N % 4 == 0 && (uintptr_t)a.dout.p % 16 == 0 && (a.R <= 1 || a.dout.ld % 4 == 0);
+  const dim3 grid(2 * sm_count);
+  if (wide)
+    return vec ? launch_dependent(k_grouped_few_inputs<true, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few_inputs<true, false>, grid, kThreads, 0, st, a);
+  return vec ? launch_dependent(k_grouped_few_inputs<false, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few_inputs<false, false>, grid, kThreads, 0, st, a);
 }
 
 cudaError_t run_few(const GroupedArgs& a, int sm_count, cudaStream_t st) {
   const bool vec = a.K % 4 == 0 && (uintptr_t)a.W % 16 == 0 && (uintptr_t)a.x.p % 16 == 0 && (a.R <= 1 || a.x.ld % 4 == 0);
   const long long groups = (a.N + kFewFeatures - 1) / kFewFeatures, tiles = (a.R < a.E ? a.R : a.E) * groups,
-                  warps = 2ll * sm_count * (kThreads / 32);
+                  warps = 2ll * sm_count * kWarps;
   const dim3 grid(2 * sm_count);
   if (tiles < warps)
     return vec ? launch_dependent(k_grouped_few<8, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few<8, false>, grid, kThreads, 0, st, a);
@@ -439,6 +556,9 @@ cudaError_t launch_grouped_general(const GroupedArgs& a, Grouped what, int sm_co
   // N = 512: 47, 34 and 34 us, and 6.4, 9.9 and 16.
   if (a.dtype == DETFFN_F32 && what == Grouped::kForward && (a.R <= 16ll * a.E || a.R * a.N <= 1 << 17))
     return run_few(a, sm_count, st);
+  // (dx of the same: 360, 361, 362 and 366 us, and 82, 138, 241 and 447; 25 to 18 us, and 9 to 16.)
+  if (a.dtype == DETFFN_F32 && what == Grouped::kInput && (a.R <= 16ll * a.E || a.R * a.K <= 1 << 17))
+    return run_few_inputs(a, sm_count, st);
   if (a.dtype == DETFFN_F32) return run<DETFFN_F32>(a, what, sm_count, st);
   if (a.dtype == DETFFN_F16) return run<DETFFN_F16>(a, what, sm_count, st);
   return run<DETFFN_BF16>(a, what, sm_count, st);

@@ -491,7 +491,7 @@ DETFFN_API detffn_status detffn_moe_forward(detffn_handle h, const void* x, cons
  * of `dtype`, every sum FP32 and rounded once; dX or dW NULL: not formed (W, or
  * x, may then be NULL).  The same call gives the same bits; on the tensor cores a
  * row's out and dX do not depend on the other rows (on the CUDA cores the order of
- * a sum follows from the sizes).  `offsets` are E + 1 ascending ints on the device, read
+ * a sum follows from the sizes and from which rows lie on 16-byte boundaries).  `offsets` are E + 1 ascending ints on the device, read
  * there: no host waits for them.  They may begin after row 0 and end before row
  * R; rows of no expert are left as they were in out and dX.  Ends beyond R are
  * taken as R, and an end before its beginning as no rows.  R < 2^31, K, N <= 65536.
