@@ -8,11 +8,12 @@
 // All three are D[i, j] = sum_c A(i, c) B(j, c), where A and B run along c or
 // across it in memory.  A CTA takes one tile of an expert after another; the
 // experts' rows are read on the device, so no host needs to know them.  What bounds
-// it is the FP32 multiply-add rate: a thread of a 128 x 128 tile holds 8 x 8 sums and reads 16 values of shared memory for each step of c,
-// and the two FP32 multiply-adds of fma.rn.f32x2 share an issue slot.  Tiles are
-// 64 x 64 where larger ones would not fill the SMs twice; four sets of threads
-// then share the steps of c, for with 4 x 4 sums a thread is bound by the reads of
-// shared memory (16 experts of 16 rows, K = N = 1024, FP32: 124 us, and 75 so).
+// it is the FP32 multiply-add rate: a thread of a 128 x 128 tile holds 8 x 8 sums and
+// reads 16 values of shared memory for each step of c, and the two FP32 multiply-adds
+// of fma.rn.f32x2 share an issue slot.  Tiles are 64 x 64 where larger ones would not
+// fill the SMs twice; four sets of threads then share the steps of c, for with 4 x 4
+// sums a thread is bound by the reads of shared memory (16 experts of 16 rows, K = N =
+// 1024, FP32, by such tiles: 124 us, and 75 so).
 //
 // With few rows of an expert in FP32 the matrices bind, and out and dx have kernels of
 // their own that read each once for eight rows.
@@ -457,24 +458,30 @@ __global__ void __launch_bounds__(kThreads, 2) k_grouped_few_inputs(const Groupe
   });
 }
 
+// Tiles of eight rows that there are at least, where experts have rows alike.
+long long few_chunks(const GroupedArgs& a) {
+  const long long reached = a.R < a.E ? a.R : a.E, chunks = a.R / kFewRows;
+  return reached > chunks ? reached : chunks;
+}
+
 cudaError_t run_few_inputs(const GroupedArgs& a, int sm_count, cudaStream_t st) {
   // Narrow tiles where wide ones leave SMs without any.
-  const bool wide = a.K % 4 == 0 && (uintptr_t)a.W % 16 == 0 && (a.R < a.E ? a.R : a.E) * ((a.K + 127) / 128) >= sm_count;
+  const bool wide = a.K % 4 == 0 && (uintptr_t)a.W % 16 == 0 && few_chunks(a) * ((a.K + 127) / 128) >= sm_count;
   const bool vec = a.N % 4 == 0 && (uintptr_t)a.dout.p % 16 == 0 && (a.R <= 1 || a.dout.ld % 4 == 0);
   const dim3 grid(2 * sm_count);
-  if (wide)
-    return vec ? launch_dependent(k_grouped_few_inputs<true, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few_inputs<true, false>, grid, kThreads, 0, st, a);
-  return vec ? launch_dependent(k_grouped_few_inputs<false, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few_inputs<false, false>, grid, kThreads, 0, st, a);
+  auto go = [&](auto* kernel) { return launch_dependent(kernel, grid, kThreads, 0, st, a); };
+  if (wide) return vec ? go(k_grouped_few_inputs<true, true>) : go(k_grouped_few_inputs<true, false>);
+  return vec ? go(k_grouped_few_inputs<false, true>) : go(k_grouped_few_inputs<false, false>);
 }
 
 cudaError_t run_few(const GroupedArgs& a, int sm_count, cudaStream_t st) {
   const bool vec = a.K % 4 == 0 && (uintptr_t)a.W % 16 == 0 && (uintptr_t)a.x.p % 16 == 0 && (a.R <= 1 || a.x.ld % 4 == 0);
-  const long long groups = (a.N + kFewFeatures - 1) / kFewFeatures, tiles = (a.R < a.E ? a.R : a.E) * groups,
+  const long long groups = (a.N + kFewFeatures - 1) / kFewFeatures, tiles = few_chunks(a) * groups,
                   warps = 2ll * sm_count * kWarps;
   const dim3 grid(2 * sm_count);
-  if (tiles < warps)
-    return vec ? launch_dependent(k_grouped_few<8, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few<8, false>, grid, kThreads, 0, st, a);
-  return vec ? launch_dependent(k_grouped_few<1, true>, grid, kThreads, 0, st, a) : launch_dependent(k_grouped_few<1, false>, grid, kThreads, 0, st, a);
+  auto go = [&](auto* kernel) { return launch_dependent(kernel, grid, kThreads, 0, st, a); };
+  if (tiles < warps) return vec ? go(k_grouped_few<kWarps, true>) : go(k_grouped_few<kWarps, false>);
+  return vec ? go(k_grouped_few<1, true>) : go(k_grouped_few<1, false>);
 }
 
 template <int DT, Grouped WHAT>
