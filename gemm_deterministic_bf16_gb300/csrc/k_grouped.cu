@@ -19,11 +19,12 @@
 // their own that read each once for eight rows.
 //
 // FP32, 8192 rows of 8 experts, K = 2048, N = 1024: 680 us forward, 602 dx, 627 dW (51 to 57
-// TFLOP/s); 777 rows of 5 experts, K = 1031, N = 515: 44, 39 and 36 us.
+// TFLOP/s); 777 rows of 5 experts, K = 1031, N = 515: 39, 37 and 36 us.
 #include <type_traits>
 
 #include "elt.cuh"
 #include "grouped.h"
+#include "ptx.cuh"
 
 namespace detffn {
 namespace {
@@ -105,7 +106,9 @@ struct Tile {
   }
 };
 
-template <int DT, Grouped WHAT, int T>
+// PARTS > 1: the CTAs of a cluster take equal parts of a tile's contraction, and the
+// first adds the others' sums in order.
+template <int DT, Grouped WHAT, int T, int PARTS>
 __global__ void __launch_bounds__(kThreads, 2) k_grouped(const GroupedArgs a) {
   using El = typename Io<DT>::E;
   constexpr bool AA = WHAT != Grouped::kWeight, BA = WHAT == Grouped::kForward;
@@ -120,28 +123,31 @@ __global__ void __launch_bounds__(kThreads, 2) k_grouped(const GroupedArgs a) {
   const long long tj = (J + T - 1) / T;
   grid_dep_wait();
   grid_dep_launch();
-  long long next = blockIdx.x, first = 0;        // this CTA's next tile; the first tile of expert e
+  const int rank = PARTS == 1 ? 0 : (int)cluster_rank();
+  long long next = blockIdx.x / PARTS, first = 0;   // this CTA's next tile; the first tile of expert e
   for (int e = 0; e < a.E; ++e) {
     // (Rows out of the tensors, or before the expert's first, are none of its.)
     const long long b = min(max((long long)__ldg(a.off + e), 0ll), a.R);
     const long long n = max(min((long long)__ldg(a.off + e + 1), a.R) - b, 0ll);
     const long long I = WHAT == Grouped::kWeight ? a.N : n;
-    const long long C = WHAT == Grouped::kForward ? a.K : WHAT == Grouped::kInput ? a.N : n;
+    const long long all = WHAT == Grouped::kForward ? a.K : WHAT == Grouped::kInput ? a.N : n;
+    const long long span = PARTS == 1 ? all : (all + PARTS * TC - 1) / (PARTS * TC) * TC;   // whole rounds
+    const long long from = min(rank * span, all), C = min(span, all - from);               // of this CTA
     const long long tiles = (I + T - 1) / T * tj;
-    for (; next < first + tiles; next += gridDim.x) {
+    for (; next < first + tiles; next += gridDim.x / PARTS) {
       const long long i0 = (next - first) / tj * T, j0 = (next - first) % tj * T;
       const El* W = static_cast<const El*>(a.W) + (long long)e * a.N * a.K;
       TA ra;
       TB rb;
       if constexpr (WHAT == Grouped::kForward) {
-        ra.aim(static_cast<const El*>(a.x.p) + (b + i0) * a.x.ld, a.x.ld, I - i0);
-        rb.aim(W + j0 * a.K, a.K, J - j0);
+        ra.aim(static_cast<const El*>(a.x.p) + (b + i0) * a.x.ld + from, a.x.ld, I - i0);
+        rb.aim(W + j0 * a.K + from, a.K, J - j0);
       } else if constexpr (WHAT == Grouped::kInput) {
-        ra.aim(static_cast<const El*>(a.dout.p) + (b + i0) * a.dout.ld, a.dout.ld, I - i0);
-        rb.aim(W + j0, a.K, J - j0);
+        ra.aim(static_cast<const El*>(a.dout.p) + (b + i0) * a.dout.ld + from, a.dout.ld, I - i0);
+        rb.aim(W + from * a.K + j0, a.K, J - j0);
       } else {
-        ra.aim(static_cast<const El*>(a.dout.p) + b * a.dout.ld + i0, a.dout.ld, I - i0);
-        rb.aim(static_cast<const El*>(a.x.p) + b * a.x.ld + j0, a.x.ld, J - j0);
+        ra.aim(static_cast<const El*>(a.dout.p) + (b + from) * a.dout.ld + i0, a.dout.ld, I - i0);
+        rb.aim(static_cast<const El*>(a.x.p) + (b + from) * a.x.ld + j0, a.x.ld, J - j0);
       }
       uint64_t sum[S][S / 2];
 #pragma unroll
@@ -186,8 +192,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_grouped(const GroupedArgs a) {
       if constexpr (SETS > 1) {   // the sets' sums, in order
         static_assert(sizeof(sa) >= T * T * 4, "one set's sums");
         float* r = &sa[0][0] + threadIdx.x % (SIDE * SIDE);
-        for (int from = 1; from < SETS; ++from) {
-          if (set == from) {
+        for (int other = 1; other < SETS; ++other) {
+          if (set == other) {
 #pragma unroll
             for (int i = 0; i < S; ++i)
 #pragma unroll
@@ -203,7 +209,28 @@ __global__ void __launch_bounds__(kThreads, 2) k_grouped(const GroupedArgs a) {
           }
           __syncthreads();
         }
-        if (set > 0) continue;
+        if constexpr (PARTS > 1) {
+          for (int other = 1; other < PARTS; ++other) {
+            cluster_sync_all();   // (the first CTA is done with its shared memory)
+            if (rank == other && set == 0) {
+#pragma unroll
+              for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int j = 0; j < S; ++j)
+                  cluster_st(cluster_addr(r + (i * S + j) * SIDE * SIDE, 0), (int)(uint32_t)(sum[i][j / 2] >> (32 * (j % 2))));
+            }
+            cluster_sync_all();
+            if (rank == 0 && set == 0) {
+#pragma unroll
+              for (int i = 0; i < S; ++i)
+#pragma unroll
+                for (int j = 0; j < S / 2; ++j)
+                  sum[i][j] = add_f32x2(sum[i][j], two(r[(i * S + 2 * j) * SIDE * SIDE], r[(i * S + 2 * j + 1) * SIDE * SIDE]));
+            }
+          }
+          __syncthreads();   // (the buffer is written again)
+        }
+        if (set > 0 || rank > 0) continue;
       }
       El* out;
       long long lo;
@@ -496,20 +523,24 @@ cudaError_t run(const GroupedArgs& a, int sm_count, cudaStream_t st) {
     return (WHAT == Grouped::kWeight ? a.E * ((a.N + T - 1) / T) : a.R / T + a.E) * ((J + T - 1) / T);
   };
   const bool small = tiles(128) < 2ll * sm_count || (WHAT != Grouped::kWeight && a.R <= 64ll * a.E);
-  // With no more small tiles than SMs, shared memory that is not used keeps two CTAs
-  // from one SM while others have none (777 rows of 5 experts, K = 1031, N = 515: 62
-  // and 44 us).
-  const bool lone = small && tiles(64) <= sm_count;
-  const long long slots = (lone ? 1ll : 2ll) * sm_count, n = most(small ? 64 : 128);
+  const long long n = most(small ? 64 : 128), slots = 2ll * sm_count;
+  // FP32, and no more small tiles than half (a quarter) of the CTAs that there is room for:
+  // clusters of two (four) take a tile each, where a contraction has rounds enough to
+  // share: 777 rows of 5 experts, K = 1031, N = 515 44 and 39 us; 300 rows, K = N = 512 23 and
+  // 15 (with four 16); 256 rows of 4 experts, K = N = 1024 34, 33 and 22; dW of 2000 rows, K
+  // = N = 128 60, 35 and 22.
+  if constexpr (DT == DETFFN_F32) {
+    const long long c = WHAT == Grouped::kForward ? a.K : WHAT == Grouped::kInput ? a.N : a.R / a.E;
+    auto parts = [&](auto* kernel, long long p) {
+      const long long clusters = n < slots / p ? n : slots / p;
+      return launch_cluster(kernel, dim3((unsigned)(p * clusters)), kThreads, 0, (int)p, st, a);
+    };
+    if (small && 4 * tiles(64) <= slots && c >= 1024) return parts(k_grouped<DT, WHAT, 64, 4>, 4);
+    if (small && 2 * tiles(64) <= slots && c > 64) return parts(k_grouped<DT, WHAT, 64, 2>, 2);
+  }
   const dim3 grid((unsigned)(n < slots ? n : slots));
-  if (!small) return launch_dependent(k_grouped<DT, WHAT, 128>, grid, kThreads, 0, st, a);
-  static PerDevice ready;
-  constexpr int kUnused = 100 * 1024;
-  const cudaError_t e = once_per_device(ready, [] {
-    return cudaFuncSetAttribute(k_grouped<DT, WHAT, 64>, cudaFuncAttributeMaxDynamicSharedMemorySize, kUnused);
-  });
-  if (e != cudaSuccess) return e;
-  return launch_dependent(k_grouped<DT, WHAT, 64>, grid, kThreads, lone ? kUnused : 0, st, a);
+  return small ? launch_dependent(k_grouped<DT, WHAT, 64, 1>, grid, kThreads, 0, st, a)
+               : launch_dependent(k_grouped<DT, WHAT, 128, 1>, grid, kThreads, 0, st, a);
 }
 
 template <int DT>

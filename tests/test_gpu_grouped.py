@@ -393,3 +393,17 @@ def test_few_rows_keep_what_is_not_finite_to_themselves(G):
     rows = [i for i in range(16) if i not in (2, 7)]
     assert torch.equal(out[rows], clean[rows]) and torch.equal(dX[rows], gone[rows])
     assert not bool(out[[2, 7]].isfinite().any()) and not bool(dX[[2, 7]].isfinite().any())
+
+
+@pytest.mark.parametrize("sizes,K,N", [
+    ([300], 1100, 512), ([300], 512, 1100), ([300], 1025, 513), ([100, 0, 250, 3], 1056, 400), ([64, 63, 65], 1024, 1024),
+    ([300], 200, 512), ([300], 65, 512), ([300], 96, 515), ([2000], 128, 128), ([3500, 5, 0], 64, 72), ([900, 1, 33], 130, 66)],
+    ids=str)
+def test_a_contraction_in_parts(G, sizes, K, N):
+    """FP32 with few tiles: parts of whole rounds, a last part that is short or has nothing, experts of few or no rows."""
+    a = run(G, sizes, K, N, torch.float32, seed=K + N)
+    b = run(G, sizes, K, N, torch.float32, seed=K + N)
+    assert all(torch.equal(u, v) for u, v in zip(a, b))
+    x, W, d, off, ends = make(sizes, K, N, torch.float32, seed=9, first=1, behind=70)
+    before = torch.randn((x.shape[0], N), device="cuda")
+    check_forward(G, x, W, off, ends, G.detffn_grouped_forward(x, W, off, out=before.clone()), before)
