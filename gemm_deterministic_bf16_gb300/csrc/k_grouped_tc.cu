@@ -32,23 +32,19 @@
 // tile, take least.
 //
 // What bounds it: at the MMA's full rate an SM takes in 64 bytes a cycle from L2, and
-// its shared memory is read and written by 128.  Without loads 16384 x 4096 x 4096 run at
-// 1822 TFLOP/s, with A's alone at 1740, with both at 1407 (stages of 64).  So clusters
-// of two pairs take the same rows and neighbouring features: B is loaded once for
-// both, half a stage by each pair, and multicast (148 us for 16384 rows of 16 experts,
-// K = 4096, N = 1536, 165 without).  A stage holds 128 of the contraction, as a wait and
-// a commit for every 64 cost the issuing thread what their MMAs take (352 us for 16384 x
-// 4096 x 4096, 322 with 128).  More stages in flight, and prefetches into L2 ahead of
-// them, gain nothing or cost half the rate.
+// its shared memory is read and written by 128.  A stage holds 128 of the contraction,
+// as a wait and a commit for every 64 cost the issuing thread what their MMAs take.
+// More stages in flight, and prefetches into L2 ahead of them, gain nothing or cost
+// half the rate.  (Rows that two pairs share are loaded by each, not by multicast:
+// the library also serves programs on several GPUs.  That was no faster: 315 us for
+// 16384 x 4096 x 4096, 298 as it is.)
 //
-// BF16, 16384 x 4096 x 4096: 315 us forward, 319 dx, 364 dW (92, 91 and 79 % of the
-// measured matrix rate); 16384 uneven rows of 16 experts, K = 4096, N = 1536: 155 us forward, 333 both
-// gradients (70 and 65 %: five to six rounds of tiles on 36 clusters, the last in part
-// empty); 99 rows of 64 experts, K = 2048, N = 768: 34.5 us (66 % of the copy rate); 1499
-// rows of 16 experts, K = 1416, N = 4096, FP16: 120 us (both gradients; 48 % of the copy
+// BF16, 16384 x 4096 x 4096: 298 us forward, 300 dx, 347 dW (97, 97 and 83 % of the
+// measured matrix rate); 16384 uneven rows of 16 experts, K = 4096, N = 1536: 151 us forward, 312 both
+// gradients (72 and 70 %: six rounds of tiles on 76 pairs, the last in part
+// empty); 99 rows of 64 experts, K = 2048, N = 768: 38 us (60 % of the copy rate); 1499
+// rows of 16 experts, K = 1416, N = 4096, FP16: 123 us (both gradients; 48 % of the copy
 // rate: two rounds for dx, the results' way out for dW).
-#include <atomic>
-
 #include "elt.cuh"
 #include "grouped.h"
 #include "ptx.cuh"
@@ -71,11 +67,11 @@ constexpr int kOutBytes = 2 * kChunk * kPitch;   // for each four warps that wri
 constexpr int kSuper = 8;           // feature tiles that are taken together
 
 struct Bars {
-  uint64_t full[kStages];    // first CTA of a pair: both CTAs' copies have landed
-  uint64_t empty[kStages];   // all: the stage's MMAs of all pairs are done
+  uint64_t full[kStages];    // first CTA: both CTAs' copies have landed
+  uint64_t empty[kStages];   // both: the stage's MMAs are done
   uint64_t tail[kStages];    // both: this CTA's copies of a stage that is to be cleared have landed
   uint64_t accf[2];          // both: a tile's sums are done
-  uint64_t acce[2];          // first CTA of a pair: both CTAs have read them
+  uint64_t acce[2];          // first CTA: both CTAs have read them
   uint64_t fin;
   uint32_t tmem;
   int abort, cap, total;
@@ -94,7 +90,6 @@ struct Args {
   int* status;
   long long spin;
   int stall;
-  int pairs;                 // of a cluster
   int sets;                  // of four warps that write out: 1 or 2
   int vec;                   // output rows lie on 16-byte boundaries
 };
@@ -122,8 +117,7 @@ struct Tile {
 
 __device__ __forceinline__ int up32(int n) { return (n + 31) & ~31; }
 
-// Feature tiles of all pairs of a cluster count as one.
-__device__ __forceinline__ int feature_tiles(const Args& g) { return (g.F + 256 * g.pairs - 1) / (256 * g.pairs); }
+__device__ __forceinline__ int feature_tiles(const Args& g) { return (g.F + 255) / 256; }
 
 // l / d by m = (2^32 - 1) / d, for l < 2^31: the estimate is at most one short.
 __device__ __forceinline__ int quotient(int l, int d, uint32_t m) {
@@ -131,23 +125,21 @@ __device__ __forceinline__ int quotient(int l, int d, uint32_t m) {
   return l - q * d >= d ? q + 1 : q;
 }
 
-// The tiles of a cluster in order, as one of its pairs takes them.  What a tile's
+// The tiles of a pair in order.  What a tile's
 // place needs of divisions is kept for the expert, as all roles wait for it (dW of 16
 // experts of 94 rows, K = 1416, N = 4096: 64 us with divisions, 60 without).
 struct Walk {
   int e = -1, next = 0;                 // expert; the first tile of the one after it
   int first = 0, n = 0, wide = 0, steps = 0, last = 0;
-  int area = 1, log, full, left;        // tiles of kSuper features; whole ones of them, features of the last
+  int area = 1, full, left;             // tiles of kSuper features; whole ones of them, features of the last
   uint32_t by_area = 0, by_left;
   __device__ __forceinline__ explicit Walk(const Args& g) {
     const int ft = feature_tiles(g);
-    log = g.pairs == 2 ? 2 : 3;
-    static_assert(kSuper == 8, "log");
-    full = ft >> log;
-    left = ft & ((1 << log) - 1);
+    full = ft / kSuper;
+    left = ft % kSuper;
     by_left = 0xFFFFFFFFu / (uint32_t)max(left, 1);
   }
-  __device__ __forceinline__ Tile at(int id, const Args& g, const Tables& t, int cap, int pair) {
+  __device__ __forceinline__ Tile at(int id, const Args& g, const Tables& t, int cap) {
     if (id >= next) {
       do ++e;
       while (id >= t.pre[e + 1]);
@@ -158,14 +150,14 @@ struct Walk {
       wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
       steps = (c + kStep - 1) / kStep;
       last = c - (steps - 1) * kStep;
-      area = rt << log;
+      area = rt * kSuper;
       by_area = 0xFFFFFFFFu / (uint32_t)area;
     }
     const int l = id - first, sb = quotient(l, area, by_area), m = l - sb * area;
-    const int r = sb < full ? m >> log : quotient(m, left, by_left), c = m - (sb < full ? r << log : r * left);
+    const int r = sb < full ? m / kSuper : quotient(m, left, by_left), c = m - r * (sb < full ? kSuper : left);
     Tile q;
     q.e = e;
-    q.f0 = (((sb << log) + c) * g.pairs + pair) * 256;
+    q.f0 = (sb * kSuper + c) * 256;
     q.r0 = r * wide;
     q.rows = min(wide, n - q.r0);
     q.nt = up32(q.rows);
@@ -193,7 +185,6 @@ __device__ __forceinline__ bool out_all(int set, bool ok) {
 
 struct Abort {
   int* mine;
-  int ctas;
   int* status;
   long long limit;
 };
@@ -214,7 +205,7 @@ __device__ __forceinline__ bool wait_pair(uint64_t* bar, uint32_t parity, const 
     }
   }
   if (timeout) {
-    for (int c = 0; c < a.ctas; ++c) cluster_st(cluster_addr(a.mine, c), 1);
+    for (int c = 0; c < 2; ++c) cluster_st(cluster_addr(a.mine, c), 1);
     if (a.status) atomicExch(a.status, (int)DETFFN_ERR_TIMEOUT);
   }
   return __all_sync(0xffffffffu, ok) != 0;
@@ -232,15 +223,14 @@ __global__ void __launch_bounds__(kMostThreads, 1)
   Bars* bars = reinterpret_cast<Bars*>(staged + kOutBytes);
   const Tables t = tables_at(reinterpret_cast<unsigned char*>(bars) + ((sizeof(Bars) + 127) & ~127), g.E);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t crank = cluster_rank(), rank = crank & 1, lead = crank & ~1u;   // of the cluster; of the pair; the pair's first
-  const int mypair = (int)(crank / 2);
-  const int cluster = (int)blockIdx.x / (2 * g.pairs), clusters = (int)gridDim.x / (2 * g.pairs);
-  const Abort ab{&bars->abort, 2 * g.pairs, g.status, g.spin > 0 ? g.spin : kDefaultSpin};
+  const uint32_t rank = cluster_rank();
+  const int pair = (int)blockIdx.x / 2, pairs = (int)gridDim.x / 2;
+  const Abort ab{&bars->abort, g.status, g.spin > 0 ? g.spin : kDefaultSpin};
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full[s], 2);
-      mbar_init(&bars->empty[s], g.pairs);
+      mbar_init(&bars->empty[s], 1);
       mbar_init(&bars->tail[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -280,7 +270,7 @@ __global__ void __launch_bounds__(kMostThreads, 1)
         int n = 0;
         for (int e = e0; e < e1; ++e) n += (t.cnt[e] + c - 1) / c;
         n = __reduce_add_sync(0xffffffffu, n);
-        const long long cost = (n * (long long)ft + clusters - 1) / clusters * (max(c, 160) + 32);
+        const long long cost = (n * (long long)ft + pairs - 1) / pairs * (max(c, 160) + 32);
         if (cost < best) {
           best = cost;
           cap = c;
@@ -305,9 +295,9 @@ __global__ void __launch_bounds__(kMostThreads, 1)
       bars->total = s;
       bars->cap = cap;
     }
-    // A timeout recorded earlier stops this launch: one reading for all CTAs of the cluster.
-    if (lane == 0 && crank == 0 && g.status && *(volatile int*)g.status)
-      for (int c = 0; c < ab.ctas; ++c) cluster_st(cluster_addr(ab.mine, c), 1);
+    // A timeout recorded earlier stops this launch: one reading for both CTAs.
+    if (lane == 0 && rank == 0 && g.status && *(volatile int*)g.status)
+      for (int c = 0; c < 2; ++c) cluster_st(cluster_addr(ab.mine, c), 1);
   }
   cluster_sync_all();
   const uint32_t tmem = bars->tmem;
@@ -318,8 +308,8 @@ __global__ void __launch_bounds__(kMostThreads, 1)
     Ring rs;
     Walk walk(g);
     bool ok = true;
-    for (int id = cluster; id < total && ok; id += clusters) {
-      const Tile q = walk.at(id, g, t, cap, mypair);
+    for (int id = pair; id < total && ok; id += pairs) {
+      const Tile q = walk.at(id, g, t, cap);
       const int half = q.nt / 2, beg = t.beg[q.e];
       const int fa = q.f0 + (int)rank * 128;
       const int nb = up32(half);   // rows of B, by boxes of 128, or of 64 and 32 (dW: features by boxes of 64)
@@ -331,9 +321,7 @@ __global__ void __launch_bounds__(kMostThreads, 1)
         if (lane == 0) {
           const bool clear = g.what == 2 && ks == q.steps - 1 && (q.last & 15) != 0;
           const int slices = ks == q.steps - 1 && q.last <= 64 ? 1 : 2;
-          const uint32_t bar = clear ? cluster_addr(&bars->tail[rs.slot], crank) : cluster_addr(&bars->full[rs.slot], lead);
-          const bool shared = g.pairs == 2 && !clear;
-          const uint16_t mask = (uint16_t)(5u << rank);
+          const uint32_t bar = clear ? cluster_addr(&bars->tail[rs.slot], rank) : cluster_addr(&bars->full[rs.slot], 0);
           cluster_arrive_expect_tx(bar, slices * slice);
           for (int sl = 0; sl < slices; ++sl) {
             unsigned char* a = smem + rs.slot * kStage + sl * kSlice;
@@ -348,23 +336,16 @@ __global__ void __launch_bounds__(kMostThreads, 1)
               pair_load_2d(a, &mA, fa, beg + k, bar);
               pair_load_2d(a + 8192, &mA, fa + 64, beg + k, bar);
             }
-            // B, for all pairs (a slice each) or (a stage that is cleared, one pair) for this CTA alone.
-            if (shared && sl != mypair && slices == 2) continue;
-            if (shared && slices == 1 && mypair != 0) continue;
-            auto load = [&](unsigned char* to, const CUtensorMap* map, int x, int y) {
-              if (shared) pair_load_2d_multicast(to, map, x, y, bar, mask);
-              else pair_load_2d(to, map, x, y, bar);
-            };
             if (g.what == 2) {
-              load(b, &mB, q.r0 + (int)rank * half, beg + k);
-              if (half > 64) load(b + 8192, &mB, q.r0 + (int)rank * half + 64, beg + k);
+              pair_load_2d(b, &mB, q.r0 + (int)rank * half, beg + k, bar);
+              if (half > 64) pair_load_2d(b + 8192, &mB, q.r0 + (int)rank * half + 64, beg + k, bar);
             } else {
               const int y = beg + q.r0 + (int)rank * half;
               if (nb == 128) {
-                load(b, &mB, k, y);
+                pair_load_2d(b, &mB, k, y, bar);
               } else {
-                if (nb >= 64) load(b, &mB64, k, y);
-                if (nb & 32) load(b + (nb & 64) * 128, &mB32, k, y + (nb & 64));
+                if (nb >= 64) pair_load_2d(b, &mB64, k, y, bar);
+                if (nb & 32) pair_load_2d(b + (nb & 64) * 128, &mB32, k, y + (nb & 64), bar);
               }
             }
           }
@@ -377,12 +358,11 @@ __global__ void __launch_bounds__(kMostThreads, 1)
     Ring rs, rb;
     Walk walk(g);
     bool ok = true;
-    const uint16_t all = g.pairs == 2 ? 15 : 3, mine = (uint16_t)(3u << lead);
     const uint32_t base = (1u << 4) | (DT == DETFFN_BF16 ? (1u << 7) | (1u << 10) : 0u) | (16u << 24) |
                           (g.what != 0 ? kIdescTransA : 0u) | (g.what == 2 ? kIdescTransB : 0u);
     const uint32_t astep = g.what != 0 ? 128u : 2u, bstep = g.what == 2 ? 128u : 2u;
-    for (int id = cluster; id < total && ok; id += clusters) {
-      const Tile q = walk.at(id, g, t, cap, mypair);
+    for (int id = pair; id < total && ok; id += pairs) {
+      const Tile q = walk.at(id, g, t, cap);
       if (q.steps == 0) continue;
       ok = wait_pair(&bars->acce[rb.slot], rb.phase ^ 1u, ab);
       if (!ok) break;
@@ -402,15 +382,15 @@ __global__ void __launch_bounds__(kMostThreads, 1)
             for (int kk = 0; kk < 4 && k0 + kk < n; ++kk)
               pair_mma_f16(acc, da + (uint64_t)(astep * kk), db + (uint64_t)(bstep * kk), idesc, ks + k0 + kk > 0 ? 1u : 0u);
           }
-          pair_commit(&bars->empty[rs.slot], all);
-          if (ks == q.steps - 1) pair_commit(&bars->accf[rb.slot], mine);
+          pair_commit(&bars->empty[rs.slot]);
+          if (ks == q.steps - 1) pair_commit(&bars->accf[rb.slot]);
         }
         __syncwarp();
       }
       rb.next(2);
     }
     if (!ok) {   // stopped: the MMAs under way end before the shared memory is given up
-      if (elect_one()) pair_commit(&bars->fin, mine);
+      if (elect_one()) pair_commit(&bars->fin);
       __syncwarp();
       mbar_wait(&bars->fin, 0, kDefaultSpin, nullptr);
     }
@@ -419,8 +399,8 @@ __global__ void __launch_bounds__(kMostThreads, 1)
     Ring rs;
     Walk walk(g);
     uint32_t used = 0;   // parity of each stage's tail barrier
-    for (int id = cluster; id < total; id += clusters) {
-      const Tile q = walk.at(id, g, t, cap, mypair);
+    for (int id = pair; id < total; id += pairs) {
+      const Tile q = walk.at(id, g, t, cap);
       if (q.steps == 0 || (q.last & 15) == 0) {
         rs.adv(q.steps, kStages);
         continue;
@@ -436,7 +416,7 @@ __global__ void __launch_bounds__(kMostThreads, 1)
           *reinterpret_cast<uint4*>(a + i * 8192 + o) = make_uint4(0, 0, 0, 0);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) cluster_arrive(cluster_addr(&bars->full[rs.slot], lead));
+      if (lane == 0) cluster_arrive(cluster_addr(&bars->full[rs.slot], 0));
       __syncwarp();
       rs.next(kStages);
     }
@@ -446,8 +426,8 @@ __global__ void __launch_bounds__(kMostThreads, 1)
     unsigned char* at = staged + set * kChunk * kPitch;
     Ring rb;
     Walk walk(g);
-    for (int id = cluster; id < total; id += clusters) {
-      const Tile q = walk.at(id, g, t, cap, mypair);
+    for (int id = pair; id < total; id += pairs) {
+      const Tile q = walk.at(id, g, t, cap);
       const int f = q.f0 + (int)rank * 128 + quarter * 32 + lane;
       uint16_t* out = g.out + (g.what == 2 ? q.e * g.stride + q.r0 * g.ldo : (t.beg[q.e] + (long long)q.r0) * g.ldo) + f;
       const bool in = f < g.F;
@@ -514,7 +494,7 @@ __global__ void __launch_bounds__(kMostThreads, 1)
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) cluster_arrive_relaxed(cluster_addr(&bars->acce[rb.slot], lead));
+      if (lane == 0) cluster_arrive_relaxed(cluster_addr(&bars->acce[rb.slot], 0));
       __syncwarp();
       rb.next(2);
     }
@@ -530,30 +510,6 @@ __global__ void __launch_bounds__(kMostThreads, 1)
 }
 
 int smem_bytes(int E) { return 1024 + kStages * kStage + kOutBytes + (int)((sizeof(Bars) + 127) & ~127) + tables_bytes(E); }
-
-// Clusters of two pairs that a device holds at once (asked for once).
-template <int DT>
-cudaError_t rooms(int* n) {
-  static std::atomic<int> known[PerDevice::kDevices];
-  int device = 0;
-  cudaError_t e = cudaGetDevice(&device);
-  if (e != cudaSuccess) return e;
-  const bool keep = device >= 0 && device < PerDevice::kDevices;
-  if (keep && (*n = known[device].load(std::memory_order_relaxed)) > 0) return cudaSuccess;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(4);
-  cfg.blockDim = dim3(kMostThreads);
-  cfg.dynamicSmemBytes = (size_t)smem_bytes(kGroupedMaxExperts);
-  cudaLaunchAttribute at;
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = 4;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  e = cudaOccupancyMaxActiveClusters(n, k_grouped_tc<DT>, &cfg);
-  if (e == cudaSuccess && keep) known[device].store(*n, std::memory_order_relaxed);
-  return e;
-}
 
 template <int DT>
 cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_count, cudaStream_t st) {
@@ -604,21 +560,10 @@ cudaError_t run(const GroupedArgs& a, Grouped what, const Waits& wt, int sm_coun
   g.status = wt.status;
   g.spin = wt.spin;
   g.stall = wt.stall;
-  // Two pairs where their features come out even, or nearly so: a pair past the
-  // last feature works for nothing.
-  const int ft = (g.F + 255) / 256;
-  int room = 0;
-  g.pairs = 1;
-  if (ft % 2 == 0 || ft >= 7) {
-    const cudaError_t r = rooms<DT>(&room);
-    if (r != cudaSuccess) return r;
-    if (room > 0) g.pairs = 2;
-  }
-  if (g.pairs == 1) room = sm_count / 2;
-  const long long most = rt * ((ft + g.pairs - 1) / g.pairs);
-  const int clusters = (int)(most < room ? most : room);
-  return launch_cluster(k_grouped_tc<DT>, dim3(2 * g.pairs * clusters), g.sets == 2 ? kMostThreads : kThreads, smem_bytes(a.E), 2 * g.pairs, st, mA, mB, mB64,
-                        mB32, g);
+  const long long most = rt * ((g.F + 255) / 256), slots = sm_count / 2;
+  const int pairs = (int)(most < slots ? most : slots);
+  return launch_cluster(k_grouped_tc<DT>, dim3(2 * pairs), g.sets == 2 ? kMostThreads : kThreads, smem_bytes(a.E), 2, st, mA, mB,
+                        mB64, mB32, g);
 }
 
 }  // namespace

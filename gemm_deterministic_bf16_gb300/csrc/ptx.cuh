@@ -401,15 +401,6 @@ __device__ __forceinline__ void pair_load_3d(void* dst, const void* tmap, int x,
       "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
       : "memory");
 }
-// The same into every CTA of `mask`, at the same place; the bytes are counted by
-// the barrier at bar's place in the first CTA (bar: of a first CTA) of each one's pair.
-__device__ __forceinline__ void pair_load_2d_multicast(void* dst, const void* tmap, int x, int y, uint32_t bar, uint16_t mask) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], "
-      "[%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(x), "r"(y), "r"(bar), "h"(mask)
-      : "memory");
-}
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* slot, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(slot)), "r"(ncols)
                : "memory");
@@ -430,12 +421,12 @@ __device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t a_desc, u
       "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// One arrival at the barrier of this place in each CTA of `mask` when this thread's MMAs so far are done.
-__device__ __forceinline__ void pair_commit(uint64_t* bar, uint16_t mask) {
+// One arrival at the barrier of this place in both CTAs when this thread's MMAs so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
           smem_u32(bar)),
-      "h"(mask)
+      "h"((uint16_t)3)
       : "memory");
 }
 
