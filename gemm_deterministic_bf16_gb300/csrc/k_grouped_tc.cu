@@ -75,6 +75,7 @@ struct Bars {
   uint64_t fin;
   uint32_t tmem;
   int abort, cap, total;
+  int stopped;               // a timeout was recorded before this launch
 };
 
 struct Args {
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kMostThreads, 1)
       mbar_init(&bars->acce[b], 8 * g.sets);   // the warps of both CTAs that write out
     }
     mbar_init(&bars->fin, 1);
-    bars->abort = 0;
+    bars->abort = bars->stopped = 0;
     fence_mbar_init();
     prefetch_tmap(&mA);
     prefetch_tmap(&mB);
@@ -297,11 +298,13 @@ __global__ void __launch_bounds__(kMostThreads, 1)
     }
     // A timeout recorded earlier stops this launch: one reading for both CTAs.
     if (lane == 0 && rank == 0 && g.status && *(volatile int*)g.status)
-      for (int c = 0; c < 2; ++c) cluster_st(cluster_addr(ab.mine, c), 1);
+      for (int c = 0; c < 2; ++c) cluster_st(cluster_addr(&bars->stopped, c), 1);
   }
   cluster_sync_all();
+  // (The same for all threads, as barriers of several warps follow: nothing writes `stopped` from
+  // here on.  `abort` may be set by a wait of this launch before a thread comes to read it.)
   const uint32_t tmem = bars->tmem;
-  const int cap = bars->cap, total = *(volatile int*)ab.mine ? 0 : bars->total;
+  const int cap = bars->cap, total = bars->stopped ? 0 : bars->total;
 
   if (warp == 0) {
     // ---------------- loads ----------------
