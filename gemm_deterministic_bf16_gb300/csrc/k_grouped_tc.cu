@@ -356,6 +356,8 @@ __global__ void __launch_bounds__(kMostThreads, 1)
         __syncwarp();
       }
     }
+    // The arrivals under way at both CTAs' `empty` barriers land before either CTA ends.
+    for (int i = 0; i < kStages && ok; ++i, rs.next(kStages)) ok = wait_pair(&bars->empty[rs.slot], rs.phase ^ 1u, ab);
   } else if (warp == 1 && rank == 0) {
     // ---------------- MMA issue, for both CTAs ----------------
     Ring rs, rb;
