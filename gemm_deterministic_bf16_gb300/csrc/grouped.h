@@ -7,7 +7,7 @@ namespace detffn {
 
 constexpr int kGroupedMaxExperts = 1024;
 constexpr long long kGroupedMaxWidth = 65536;        // of K and N
-constexpr long long kGroupedMaxRows = (1ll << 31) - 1;
+constexpr long long kGroupedMaxRows = (1ll << 31) - 256;   // (a count of rows and a tile of 256 add up in an int)
 
 // Expert e has rows [off[e], off[e + 1]) of x [R, K] and of out, dOut [R, N],
 // and the matrix W[e] [N, K].

@@ -148,7 +148,7 @@ struct Walk {
       first = t.pre[e];
       n = g.what == 2 ? g.N : t.cnt[e];
       const int rt = (n + cap - 1) / cap, c = g.what == 2 ? t.cnt[e] : g.C;
-      wide = up32((n + rt - 1) / rt);   // (at most cap, so the last tile has rows)
+      wide = up32(n / rt + (n % rt != 0));   // (at most cap, so the last tile has rows)
       steps = (c + kStep - 1) / kStep;
       last = c - (steps - 1) * kStep;
       area = rt * kSuper;

@@ -494,7 +494,8 @@ DETFFN_API detffn_status detffn_moe_forward(detffn_handle h, const void* x, cons
  * a sum follows from the sizes and from which rows lie on 16-byte boundaries).  `offsets` are E + 1 ascending ints on the device, read
  * there: no host waits for them.  They may begin after row 0 and end before row
  * R; rows of no expert are left as they were in out and dX.  Ends beyond R are
- * taken as R, and an end before its beginning as no rows.  R < 2^31, K, N <= 65536.
+ * taken as R, and an end before its beginning as no rows.  R <= 2^31 - 256, K, N <=
+ * 65536.
  * options->path: EXACT takes the CUDA-core kernels (any sizes and types), TENSOR
  * the tensor cores (FP16 and BF16, any widths; where K and N are multiples of 8, rows
  * on 16-byte boundaries; else DETFFN_ERR_UNSUPPORTED), AUTO these where they can.

@@ -29,3 +29,38 @@ def test_waits_of_few_tries(G, sizes, K, N, what):
         assert status == 7 or torch.equal(got, want)
         assert torch.equal(go(), want)
     assert G.detffn_get_status() == 0
+
+
+@pytest.mark.parametrize("ends", [lambda R: [0, R], lambda R: [3, R - 5000, R]], ids=["one", "two"])
+def test_as_many_rows_as_there_may_be(G, ends):
+    """2^31 - 256 rows, 34 GB of x: rows at both ends of it, and their sums, in whole numbers."""
+    R, K, N = (1 << 31) - 256, 8, 8
+    ends = ends(R)
+    E = len(ends) - 1
+    off = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    g = torch.Generator(device="cuda").manual_seed(4)
+    r = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").bfloat16()  # noqa: E731
+    W = r(E, N, K)
+    x, d = (torch.zeros((R, K), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    places = [slice(ends[0], 700), slice(R // 2, R // 2 + 513), slice(R - 6000, R)]
+    for s in places:
+        x[s], d[s] = r(s.stop - s.start, K), r(s.stop - s.start, N)
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    G.detffn_grouped_forward(x, W, off, out=out)
+    assert bool((out[:ends[0]] == 7.0).all())
+    for s in places:
+        row = torch.arange(s.start, s.stop, device="cuda")
+        of = torch.bucketize(row, off.long()[1:-1], right=True) if E > 1 else torch.zeros_like(row)
+        assert torch.equal(out[s], torch.einsum("rk,rnk->rn", x[s].double(), W[of].double()).bfloat16())
+    assert not bool(out[1000:R // 2].any())
+    del out
+    torch.cuda.empty_cache()
+    _, dW = G.detffn_grouped_backward(x, W, off, d, need_dX=False)
+    want = torch.zeros((E, N, K), dtype=torch.float64, device="cuda")
+    for s in places:
+        for e in range(E):
+            a, b = max(s.start, ends[e]), min(s.stop, ends[e + 1])
+            if a < b:
+                want[e] += d[a:b].double().T @ x[a:b].double()
+    assert torch.equal(dW, want.bfloat16())
+    assert G.detffn_get_status() == 0
