@@ -1,9 +1,14 @@
 """The products grouped by expert at the ends of what they accept: waits that run
-out at any point."""
+out at any point, as many rows as there may be, and sums whose every product
+counts.
+
+Sums of whole numbers are exact in FP32 in any order where the magnitudes of all
+products add up to less than 2^24, so a result has to be the 64-bit one rounded
+once: a product that is left out or taken twice shows at any length."""
 import pytest
 import torch
 
-from tests.test_gpu_grouped import G, TENSOR, make  # noqa: F401
+from tests.test_gpu_grouped import AUTO, EXACT, G, TENSOR, make  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +69,22 @@ def test_as_many_rows_as_there_may_be(G, ends):
                 want[e] += d[a:b].double().T @ x[a:b].double()
     assert torch.equal(dW, want.bfloat16())
     assert G.detffn_get_status() == 0
+
+
+@pytest.mark.parametrize("dtype,path", [(torch.bfloat16, AUTO), (torch.float16, AUTO), (torch.float32, AUTO), (torch.bfloat16, EXACT)],
+                         ids=["bf16", "f16", "f32", "bf16-exact"])
+@pytest.mark.parametrize("sizes,K,N", [
+    ([700, 0, 1033, 12, 255], 4096, 1536), ([64, 1, 100], 8192, 520), ([3, 17, 0, 1], 8189, 77), ([5] * 30, 2056, 1028),
+    ([9000, 8191], 64, 72), ([40000], 40, 9), ([300], 1100, 2048), ([20], 9, 65536), ([20], 65536, 9)], ids=str)
+def test_sums_of_whole_numbers(G, sizes, K, N, dtype, path):
+    """9 times the longest sum, 65536 products, stays below 2^24."""
+    x, W, d, off, ends = make(sizes, K, N, torch.float32, seed=K + N)
+    x, W, d = (t.round().clamp(-3, 3).to(dtype) for t in (x, W, d))
+    out = G.detffn_grouped_forward(x, W, off, path=path)
+    dX, dW = G.detffn_grouped_backward(x, W, off, d, path=path)
+    for e in range(len(sizes)):
+        a, b = ends[e], ends[e + 1]
+        x64, w64, d64 = x[a:b].double(), W[e].double(), d[a:b].double()
+        assert torch.equal(out[a:b], (x64 @ w64.T).to(dtype))
+        assert torch.equal(dX[a:b], (d64 @ w64).to(dtype))
+        assert torch.equal(dW[e], (d64.T @ x64).to(dtype))
