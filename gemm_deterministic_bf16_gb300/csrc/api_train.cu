@@ -100,11 +100,11 @@ detffn_status run_grouped(detffn_handle h, const GroupedArgs& a, std::initialize
     if (lay_x) t.x = Rows{s.x, grouped_pad(a.K)};
     if (lay_W) t.W = s.W, t.ldw = grouped_pad(a.K);
     if (lay_d) t.dout = Rows{s.dout, grouped_pad(a.N)};
-    const double rows = (lay_x ? (double)a.R * a.K : 0.0) + (lay_W ? (double)a.E * a.N * a.K : 0.0) + (lay_d ? (double)a.R * a.N : 0.0);
+    const double rows = (lay_x ? (double)a.R * a.K : 0.0) + (lay_W ? most * a.N * a.K : 0.0) + (lay_d ? (double)a.R * a.N : 0.0);
     if (rows > 0.0)
       TRY(timed(h, st, "grouped_rows", 2.0 * es * rows, 0.0, [&]() -> detffn_status {
         if (lay_x) TRYCU(launch_grouped_rows(a.x, a.R, a.K, s.x, h->sm_count, st));
-        if (lay_W) TRYCU(launch_grouped_rows(W, a.E * a.N, a.K, s.W, h->sm_count, st));
+        if (lay_W) TRYCU(launch_grouped_matrices(a, s.W, h->sm_count, st));
         if (lay_d) TRYCU(launch_grouped_rows(a.dout, a.R, a.N, s.dout, h->sm_count, st));
         return DETFFN_OK;
       }, (lay_x ? 1 : 0) + (lay_W ? 1 : 0) + (lay_d ? 1 : 0)));

@@ -32,6 +32,8 @@ inline bool grouped_boundary(const Rows& r, long long rows) {
 constexpr long long grouped_pad(long long n) { return (n + 7) / 8 * 8; }
 // to[r * grouped_pad(width) + c] = from's element (r, c), 16-bit types.
 cudaError_t launch_grouped_rows(const Rows& from, long long rows, long long width, uint16_t* to, int sm_count, cudaStream_t st);
+// The same of a.W; matrices of experts without rows may be left out.
+cudaError_t launch_grouped_matrices(const GroupedArgs& a, uint16_t* to, int sm_count, cudaStream_t st);
 
 // Tensor-core kernel: BF16 and FP16, rows of x, W and dout (those it reads) on
 // 16-byte boundaries.

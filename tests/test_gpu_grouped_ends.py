@@ -88,3 +88,37 @@ def test_sums_of_whole_numbers(G, sizes, K, N, dtype, path):
         assert torch.equal(out[a:b], (x64 @ w64.T).to(dtype))
         assert torch.equal(dX[a:b], (d64 @ w64).to(dtype))
         assert torch.equal(dW[e], (d64.T @ x64).to(dtype))
+
+
+@pytest.mark.parametrize("what", ["forward", "dX"])
+@pytest.mark.parametrize("sizes", [[2, 0, 0, 1, 0], [0] * 70 + [9] + [0] * 40, [0, 0, 1], [0] * 31 + [5, 2] + [0] * 3], ids=lambda s: str(len(s)))
+def test_matrices_of_no_row_are_not_laid_out(G, sizes, what):
+    """Odd widths and fewer rows than experts: the scratch of those without rows stays as it was."""
+    K, N, mark = 65, 33, -23131
+    x, W, d, off, ends = make(sizes, K, N, torch.bfloat16)
+    R, E = x.shape[0], len(sizes)
+    W[[e for e in range(E) if not sizes[e]]] = float("nan")
+    ws = torch.full((G.detffn_grouped_workspace_size(R, E, K, N) // 2,), mark, dtype=torch.int16, device="cuda")
+    buf = ws.view(torch.uint8)
+    if what == "forward":
+        got, want = G.detffn_grouped_forward(x, W, off, ws=buf), torch.cat([x[ends[e]:ends[e + 1]].double() @ W[e].double().T for e in range(E)])
+    else:
+        got, _ = G.detffn_grouped_backward(None, W, off, d, need_dW=False, ws=buf)
+        want = torch.cat([d[ends[e]:ends[e + 1]].double() @ W[e].double() for e in range(E)])
+    assert float((got.double() - want).norm() / want.norm()) < 2.0 ** -8
+    assert int((ws == mark).sum()) >= sizes.count(0) * N * 72
+
+
+def test_matrices_where_ends_are_out_of_order(G):
+    """More experts that have rows than there are rows: the last of them, which no other's rows meet, is laid out too."""
+    K, N = 65, 33
+    x, W, d, _, _ = make([4], K, N, torch.bfloat16)
+    W = torch.randn((40, N, K), device="cuda").bfloat16()
+    off = torch.tensor([0, 1] * 18 + [0, 0, 1, 2, 4], dtype=torch.int32, device="cuda")   # expert 38 has row 1, 39 rows 2 and 3
+    ws = torch.full((G.detffn_grouped_workspace_size(4, 40, K, N),), 0xFF, dtype=torch.uint8, device="cuda")
+    out = G.detffn_grouped_forward(x, W, off, ws=ws)
+    want = torch.cat([x[1:2].double() @ W[38].double().T, x[2:].double() @ W[39].double().T])
+    assert float((out[1:].double() - want).norm() / want.norm()) < 2.0 ** -8
+    dX, _ = G.detffn_grouped_backward(None, W, off, d, need_dW=False, ws=ws.fill_(0xFF))
+    want = torch.cat([d[1:2].double() @ W[38].double(), d[2:].double() @ W[39].double()])
+    assert float((dX[1:].double() - want).norm() / want.norm()) < 2.0 ** -8
