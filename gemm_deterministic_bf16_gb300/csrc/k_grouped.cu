@@ -623,14 +623,16 @@ cudaError_t launch_grouped_matrices(const GroupedArgs& a, uint16_t* to, int sm_c
 }
 
 cudaError_t launch_grouped_general(const GroupedArgs& a, Grouped what, int sm_count, cudaStream_t st) {
-  // Tiles of 64 x 64 take what K's rounds of loads do however few rows there are: 64
-  // experts, K = 2048, N = 768, 1, 8, 16 and 32 rows of each: 411, 413, 413 and 414 us,
-  // and 79, 121, 216 and 413 by rows of eight; one expert of 32, 64 and 128 rows, K = 1024,
-  // N = 512: 47, 34 and 34 us, and 6.4, 9.9 and 16.
-  if (a.dtype == DETFFN_F32 && what == Grouped::kForward && (a.R <= 16ll * a.E || a.R * a.N <= 1 << 17))
+  // Tiles of 64 x 64 take what K's rounds of loads do however few rows there are, rows by
+  // eights as long as there are eights.  64 experts of 8, 16, 24, 32 and 40 rows, K = 2048, N = 768:
+  // 418 us by tiles, 119, 212, 314, 408 and 508 by eights; 16 of 24, 32 and 48, K = N = 1024: 77, and 56,
+  // 72 and 110; one of 64, 256 and 384, K = 1024, N = 512: 14, 21 and 22, and 9, 16 and 23.  (The rows are
+  // taken as the experts' alike.  1024 that are all one's of 64, K = 2048, N = 768: 124 and 133.)
+  if (a.dtype == DETFFN_F32 && what == Grouped::kForward && (a.R <= 32ll * a.E || a.R * a.N <= 1 << 17))
     return run_few(a, sm_count, st);
-  // (dx of the same: 360, 361, 362 and 366 us, and 82, 138, 241 and 447; 25 to 18 us, and 9 to 16.)
-  if (a.dtype == DETFFN_F32 && what == Grouped::kInput && (a.R <= 16ll * a.E || a.R * a.K <= 1 << 17))
+  // dx of the same: 345, and 134, 243, 353, 456 and 582; 68, and 65, 74 and 131; 12, 17 and 18, and 9, 15
+  // and 28; 91 and 134.
+  if (a.dtype == DETFFN_F32 && what == Grouped::kInput && (a.R <= 24ll * a.E || a.R * a.K <= 1 << 16))
     return run_few_inputs(a, sm_count, st);
   if (a.dtype == DETFFN_F32) return run<DETFFN_F32>(a, what, sm_count, st);
   if (a.dtype == DETFFN_F16) return run<DETFFN_F16>(a, what, sm_count, st);

@@ -8,7 +8,7 @@ once: a product that is left out or taken twice shows at any length."""
 import pytest
 import torch
 
-from tests.test_gpu_grouped import AUTO, EXACT, G, TENSOR, make  # noqa: F401
+from tests.test_gpu_grouped import AUTO, EXACT, G, TENSOR, make, run  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -122,3 +122,11 @@ def test_matrices_where_ends_are_out_of_order(G):
     dX, _ = G.detffn_grouped_backward(None, W, off, d, need_dW=False, ws=ws.fill_(0xFF))
     want = torch.cat([d[1:2].double() @ W[38].double(), d[2:].double() @ W[39].double()])
     assert float((dX[1:].double() - want).norm() / want.norm()) < 2.0 ** -8
+
+
+@pytest.mark.parametrize("per", [23, 24, 25, 31, 32, 33])
+@pytest.mark.parametrize("K,N", [(264, 1040), (1031, 130), (96, 4096)])
+def test_where_rows_by_eights_end(G, per, K, N):
+    """On both sides of the sizes where FP32 changes kernels, alike and uneven experts."""
+    for sizes in ([per] * 9, [3 * per, 0, 0], [per - 3, per + 3, per], [64 * per]):
+        run(G, sizes, K, N, torch.float32, seed=per)
