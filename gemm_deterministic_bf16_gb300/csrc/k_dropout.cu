@@ -13,10 +13,12 @@
 // A word is 32 bits, so p is met to 2^-32.  The product x * scale and the sum
 // are FP32, rounded once to the stored type.
 //
-// The ten rounds bind it where bytes are few: 20 wide multiplications and 20 logic
-// operations for four elements keep the pipes that issue one in two cycles at 40 and 64 %
-// (16384 x 4096 BF16: 62 us without a residual, 65 % of the copy rate; 70 with one, 86 %;
-// FP32 89 us, 90 %; rows of 4095 94 us, element by element).
+// HBM bounds it with a residual or in FP32 (16384 x 4096: BF16 70 us with a residual, 86 %
+// of the copy rate; FP32 89 us without, 90 %).  Where bytes are fewer it is the latency
+// of the ten rounds, each of which waits for the last: 20 wide multiplications and 20
+// logic operations for four elements keep their pipes at 40 and 64 %, issue is at 55 and
+// HBM at 43, and none is full (BF16 without a residual 62 us, 65 %; rows of 4095 94 us,
+// element by element).
 #include "dropout.h"
 #include "elt.cuh"
 

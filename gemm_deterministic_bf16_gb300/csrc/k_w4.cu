@@ -3,12 +3,13 @@
 //
 //   y[t, n] = sum over groups g of  s[n, g] * ( sum over k in g of (code[n, k] - 8) * x[t, k] )
 //
-// What bounds it is the weights' bytes (half a byte a weight and the scales).
-// At the card's copy rate an SM has to take in some 46 weights a cycle, so
+// What has to be moved is the weights' bytes (half a byte a weight and the scales).
+// At the copy rate (6.68 TB/s to 152 SMs of 2070 MHz) an SM takes in some 41 weights a
+// cycle, so
 // the arithmetic goes to the tensor cores by mma.sync m16n8k16, straight from
-// registers: the weights are the 16-row operand, up to eight columns (tokens,
+// registers: the weights are the 16-row operand, eight columns (tokens,
 // or the terms of their activations) the other, and a weight is read and
-// converted once for all of them.  A code becomes BF16 or FP16 by putting its
+// converted once for all columns of a pass (8, 16 or 32).  A code becomes BF16 or FP16 by putting its
 // bits into the mantissa of 128 or 1024 and subtracting 136 or 1032: exact, as
 // are all products with a 16-bit x.  A group's sum is one accumulation in FP32,
 // scaled and added to the row's FP32 sum.
@@ -16,7 +17,10 @@
 // An FP32 activation is three BF16 terms (together all 24 bits), in columns of
 // their own; a small kernel lays them out first, and rows that are not on
 // 16-byte boundaries.  The hidden activation of the gated FFN goes from one
-// launch to the next as two terms (16 bits), three for FP32.
+// launch to the next as two terms (16 bits), three for FP32: two are off by at most
+// 2^-16 of a value, which a result of 8 or 11 bits does not show (the FFN of one token, H
+// = 4096, I = 12288, BF16, is 1.67666e-3 of its norm from the 64-bit one, with h in FP32
+// 1.67665e-3), and a third would be half as many columns again.
 //
 // The order of the codes makes this a matter of plain vectors: lane 4 r + t of
 // a warp holds row r (and r + 8) of the 16-row operand and columns 2 t, 2 t + 1,
@@ -34,7 +38,9 @@
 // groups of 64, 78 us (floor 43); the FFN of one token, H = 4096, I = 12288, BF16, groups of
 // 128, 26.6 us (floor 11.6); one token through 4096 x 4096 4.7 us (floor 1.3).  A run of
 // 128 codes of 16 rows takes 190 to 210 instructions, of which the integer pipe, which
-// issues one in two cycles, has 72 to 83.  With more columns it is latency: in the
+// issues one in two cycles, has 72 to 83; but issue is at 47 to 61 % and HBM at 26 to 45, so
+// nothing is full: the up to 24 warps an SM that registers and rings leave room for do
+// not cover the latency.  With more columns it is latency too: in the
 // FFN of 32 tokens (70 us; 22 of them the matrix instructions', one in two cycles for an
 // SM) eight warps an SM, all that the sums leave registers for, issue in 31 % of the
 // cycles and wait for results of a fixed latency most, then for x from L2; 2.5 tiles
@@ -457,7 +463,8 @@ cudaError_t run_group(const W4Args& a, int sm_count, cudaStream_t st) {
   if (a.w.group == 64) return run_one<BF, MT, NT, GATED, 64>(a, sm_count, st);
   return run_one<BF, MT, NT, GATED, 128>(a, sm_count, st);
 }
-// Columns in passes of 8, 16 or 32, weights read again (from L2) for each.  Four
+// Columns in passes of 8, 16 or 32, weights read again for each: the CTAs of a pass
+// follow those of the last, so from L2 where the matrix fits it, else from HBM.  Four
 // row and column tiles read x from L1 half as often as two, and leave an SM eight
 // warps instead of sixteen: they pay for gate and up from 17 columns on (FFN of 8
 // tokens in FP32, H = 4096, I = 12288: 59 and 55 us), else from 33 (16 tokens in BF16: 52 and

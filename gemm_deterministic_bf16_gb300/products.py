@@ -35,7 +35,9 @@ def detffn_grouped_forward(x, W, offsets, out=None, ws=None, path=PATH_AUTO, str
     expert e: x [R, K] sorted by expert (any row stride), W [E, N, K], offsets
     int32 [E + 1] on the device, which no host waits for.  Returns out [R, N].
     Rows of no expert stay as they were in ``out`` (without it they hold
-    whatever the memory held)."""
+    whatever the memory held).  16-bit rows of a width that is a multiple of 8 run
+    on the tensor cores only from 16-byte boundaries: a slice as wide[:, 1:] takes
+    some thirty times as long where rows are many, a copy of it does not."""
     f = (_b._LIB or _native()).grouped_forward
     args = (_handle(x), x, W, offsets, out, ws, path, spin_limit, flags)
     return (f(*args) if stream is None else _on(stream, f, *args))[0]
@@ -45,7 +47,9 @@ def detffn_grouped_backward(x, W, offsets, dOut, dX=None, dW=None, need_dX=True,
                             stream=None, spin_limit=0, flags=0):
     """Gradients of detffn_grouped_forward from dOut [R, N]: (dX [R, K], dW [E, N,
     K]), None for one that is not needed (x may be None without dW).  An expert
-    without rows has a dW of zeros; rows of no expert stay as they were in dX."""
+    without rows has a dW of zeros; rows of no expert stay as they were in dX.  One
+    operand off the boundaries that detffn_grouped_forward names takes both gradients
+    from the tensor cores."""
     f = (_b._LIB or _native()).grouped_backward
     args = (_handle(dOut), x, W, offsets, dOut, dX, dW, need_dX, need_dW, ws, path, spin_limit, flags)
     return f(*args) if stream is None else _on(stream, f, *args)
@@ -73,7 +77,7 @@ def detffn_w4_pack(w, group=128, scale_dtype=None, w4=None, stream=None):
 
 
 def detffn_w4_unpack(w4, out=None, dtype=torch.bfloat16, stream=None):
-    """The values [N, K] of a 4-bit matrix, in ``dtype`` (out's where it is given)."""
+    """The values [N, K] of a 4-bit matrix, FP32 products rounded to ``dtype`` (out's where it is given)."""
     f = (_b._LIB or _native()).w4_unpack
     args = (*w4, _CODE.get(dtype if out is None else out.dtype, -1), out)
     return (f(*args) if stream is None else _on(stream, f, *args))[0]

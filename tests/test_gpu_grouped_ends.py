@@ -8,7 +8,7 @@ once: a product that is left out or taken twice shows at any length."""
 import pytest
 import torch
 
-from tests.test_gpu_grouped import AUTO, EXACT, G, TENSOR, make, run  # noqa: F401
+from tests.test_gpu_grouped import AUTO, EXACT, G, TENSOR, check_backward, check_forward, make, run  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -130,3 +130,26 @@ def test_where_rows_by_eights_end(G, per, K, N):
     """On both sides of the sizes where FP32 changes kernels, alike and uneven experts."""
     for sizes in ([per] * 9, [3 * per, 0, 0], [per - 3, per + 3, per], [64 * per]):
         run(G, sizes, K, N, torch.float32, seed=per)
+
+
+@pytest.mark.parametrize("K,N,operand", [(64, 33, "x"), (33, 64, "dOut"), (64, 64, "x"), (64, 64, "dOut")])
+def test_rows_off_16_byte_boundaries(G, K, N, operand):
+    """An operand whose width is a multiple of 8: refused by the tensor path where a product reads it, right by default."""
+    x, W, d, off, ends = make([20, 0, 130], K, N, torch.bfloat16, first=1, behind=2)
+    place = lambda t: torch.cat((t[:, :1], t), 1)[:, 1:]  # noqa: E731
+    x, d = (place(x), d) if operand == "x" else (x, place(d))
+    before = torch.randn((x.shape[0], N), device="cuda").bfloat16()
+    check_forward(G, x, W, off, ends, G.detffn_grouped_forward(x, W, off, out=before.clone()), before)
+    before = torch.randn((x.shape[0], K), device="cuda").bfloat16()
+    dX, dW = G.detffn_grouped_backward(x, W, off, d, dX=before.clone())
+    check_backward(G, x, W, d, ends, dX, dW, before)
+    for read, call in ((operand == "x", lambda: G.detffn_grouped_forward(x, W, off, path=TENSOR)),
+                       (operand == "dOut", lambda: G.detffn_grouped_backward(x, W, off, d, need_dW=False, path=TENSOR)),
+                       (True, lambda: G.detffn_grouped_backward(x, W, off, d, need_dX=False, path=TENSOR)),
+                       (True, lambda: G.detffn_grouped_backward(x, W, off, d, path=TENSOR))):
+        if read:
+            with pytest.raises(G.DetFFNError) as e:
+                call()
+            assert e.value.status == 4
+        else:
+            call()
