@@ -40,11 +40,12 @@
 // 16384 x 4096 x 4096, 298 as it is.)
 //
 // BF16, 16384 x 4096 x 4096: 298 us forward, 300 dx, 347 dW (97, 97 and 83 % of the
-// measured matrix rate); 16384 uneven rows of 16 experts, K = 4096, N = 1536: 151 us forward, 312 both
-// gradients (72 and 70 %: six rounds of tiles on 76 pairs, the last in part
-// empty); 99 rows of 64 experts, K = 2048, N = 768: 38 us (60 % of the copy rate); 1499
-// rows of 16 experts, K = 1416, N = 4096, FP16: 123 us (both gradients; 48 % of the copy
-// rate: two rounds for dx, the results' way out for dW).
+// measured matrix rate); 16384 uneven rows of 16 experts, K = 4096, N = 1536: 151 to 155 us
+// forward, 312 to 352 both gradients, by the power there is (70 to 72 and 62 to 70 %: six
+// rounds of tiles on 76 pairs, the last in part empty); 99 rows of 64 experts, K = 2048, N
+// = 768: 34.5 to 38.7 us (66 to 59 % of the copy rate); 1499 rows of 16 experts, K = 1416, N
+// = 4096, FP16: 123 us (both gradients; 48 % of the copy rate: two rounds for dx, the
+// results' way out for dW).
 #include "elt.cuh"
 #include "grouped.h"
 #include "ptx.cuh"
